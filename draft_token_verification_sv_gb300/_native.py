@@ -30,11 +30,16 @@ SV_ROW_DEPTH_EXCEEDED = 4
 SV_ROW_BAD_TOKEN = 8
 SV_ROW_EMPTY = 16
 SV_ROW_RESAMPLE_FALLBACK = 32
+SV_ROW_BAD_PAGE = 64
+SV_ROW_BAD_LENGTH = 128
+SV_ROW_NOT_FINITE = 256
+SV_ROW_BAD_PATH = 512
 
 SV_MAX_GAMMA = 64
 SV_MAX_VOCAB = 16777216
 SV_MAX_TREE_NODES = 1024
 SV_MAX_TREE_DEPTH = 64
+SV_MAX_HEAD_DIM = 256
 
 SV_DEBUG_INDEX = 1
 
@@ -71,6 +76,27 @@ class TopkDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("row_stride", ctypes.c_int64)]
 
 
+class KvDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("table_stride", ctypes.c_int64)]
+
+
+class KvRowsDesc(ctypes.Structure):
+    _fields_ = [("max_new", ctypes.c_int32), ("total_new", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("k_row_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64)]
+
+
+class KvAttentionDesc(ctypes.Structure):
+    _fields_ = [("kv", KvDesc), ("heads", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("total_new", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -97,6 +123,11 @@ SIGNATURES = {
     "sv_sample_workspace_size": (_SZ, [ctypes.POINTER(SampleDesc)]),
     "sv_sample": (_I32, [ctypes.POINTER(SampleDesc), _P, _P, _P, _P, _P, _SZ, _P]),
     "sv_softmax_topp": (_I32, [ctypes.POINTER(SampleDesc), _P, _P, _I64, _P, _SZ, _P]),
+    "sv_kv_append": (_I32, [_P] * 12 + [_P]),
+    "sv_kv_read": (_I32, [_P] * 12 + [_P]),
+    "sv_kv_commit": (_I32, [_P, _I32, _I32] + [_P] * 10 + [_P]),
+    "sv_kv_attention_workspace_size": (_SZ, [_P]),
+    "sv_kv_attention": (_I32, [_P] * 13 + [_P, _SZ, _P]),
     "sv_status_string": (ctypes.c_char_p, [_I32]),
     "sv_version": (_I32, []),
     "sv_set_phase_events": (None, [_P, _I32]),

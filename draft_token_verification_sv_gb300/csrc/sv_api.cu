@@ -83,6 +83,53 @@ bool sample_desc_ok(const sv_sample_desc* d) {
   return true;
 }
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+constexpr int64_t kMaxStride = int64_t{1} << 40;
+
+bool kv_desc_ok(const sv_kv_desc* d) {
+  if (!d) return false;
+  if (d->batch < 0 || d->batch > 65535 || d->kv_heads < 1 || d->kv_heads > 1024) return false;
+  if (d->head_dim < 16 || d->head_dim > SV_MAX_HEAD_DIM || d->head_dim % 16) return false;
+  if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128) return false;
+  if (d->num_pages < 1 || d->max_pages < 1) return false;
+  if (static_cast<int64_t>(d->max_pages) * d->page_size > INT32_MAX) return false;
+  const int64_t strides[3] = {d->page_stride, d->head_stride, d->token_stride};
+  for (int64_t s : strides)
+    if (s < d->head_dim || s > kMaxStride || s % 16) return false;
+  return d->table_stride >= d->max_pages && d->table_stride <= kMaxStride;
+}
+
+// Rows of new tokens: how many there may be, and that the uniform layout
+// (no new_start) has batch * max_new of them.
+bool kv_rows_ok(const sv_kv_desc& d, int32_t max_new, int32_t total_new, bool ragged) {
+  if (max_new < 0 || total_new < 0) return false;
+  return ragged || static_cast<int64_t>(d.batch) * max_new == total_new;
+}
+
+bool kv_stride_ok(int64_t s, int head_dim) { return s >= head_dim && s <= kMaxStride; }
+
+bool kv_rows_desc_ok(const sv_kv_desc& d, const sv_kv_rows_desc* r, bool ragged) {
+  if (!r || !valid_dtype(r->dtype) || r->reserved != 0) return false;
+  if (!kv_rows_ok(d, r->max_new, r->total_new, ragged)) return false;
+  return kv_stride_ok(r->k_row_stride, d.head_dim) && kv_stride_ok(r->k_head_stride, d.head_dim) &&
+         kv_stride_ok(r->v_row_stride, d.head_dim) && kv_stride_ok(r->v_head_stride, d.head_dim);
+}
+
+bool kv_cache_ok(const void* k, const void* v, const float* ks, const float* vs, const int32_t* table) {
+  return k && v && ks && vs && table && aligned16(k) && aligned16(v) && aligned4(ks) && aligned4(vs) && aligned4(table);
+}
+
+bool kv_attention_desc_ok(const sv_kv_attention_desc* d, bool ragged) {
+  if (!d || !kv_desc_ok(&d->kv) || !valid_dtype(d->dtype) || d->reserved != 0) return false;
+  if (d->heads < 1 || d->heads % d->kv.kv_heads || d->heads / d->kv.kv_heads > 128) return false;
+  if (!kv_rows_ok(d->kv, d->max_new, d->total_new, ragged)) return false;
+  if (static_cast<int64_t>(d->max_new) * (d->heads / d->kv.kv_heads) > INT32_MAX) return false;
+  if (!std::isfinite(d->scale) || d->window < 0 || d->sinks < 0) return false;
+  return kv_stride_ok(d->q_row_stride, d->kv.head_dim) && kv_stride_ok(d->q_head_stride, d->kv.head_dim) &&
+         kv_stride_ok(d->out_row_stride, d->kv.head_dim) && kv_stride_ok(d->out_head_stride, d->kv.head_dim);
+}
+
 }  // namespace
 
 extern "C" {
@@ -280,6 +327,74 @@ sv_status sv_softmax_topp(const sv_sample_desc* desc, const void* logits, float*
     return SV_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < sv_sample_workspace_size(desc)) return SV_ERR_WORKSPACE_TOO_SMALL;
   return probs_rows(*desc, logits, out_probs, out_row_stride, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sv_status sv_kv_append(const sv_kv_desc* desc, const sv_kv_rows_desc* rows, const void* k, const void* v,
+                       const int32_t* page_table, const int32_t* ctx_lens, const int32_t* new_start,
+                       uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale,
+                       int32_t* row_status, sv_stream_t stream) {
+  CallScope scope;
+  if (!kv_desc_ok(desc) || !kv_rows_desc_ok(*desc, rows, new_start != nullptr)) return SV_ERR_INVALID_ARGUMENT;
+  if (desc->batch == 0) return SV_OK;
+  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens) return SV_ERR_INVALID_ARGUMENT;
+  if (rows->total_new > 0 && (!k || !v || !aligned_elem(k, rows->dtype) || !aligned_elem(v, rows->dtype)))
+    return SV_ERR_INVALID_ARGUMENT;
+  return kv_append(*desc, *rows, k, v, KvCache{k_cache, v_cache, k_scale, v_scale, page_table}, ctx_lens, new_start,
+                   row_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sv_status sv_kv_read(const sv_kv_desc* desc, const sv_kv_rows_desc* rows, const uint8_t* k_cache,
+                     const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                     const int32_t* page_table, const int32_t* first, const int32_t* new_start,
+                     void* k, void* v, int32_t* row_status, sv_stream_t stream) {
+  CallScope scope;
+  if (!kv_desc_ok(desc) || !kv_rows_desc_ok(*desc, rows, new_start != nullptr)) return SV_ERR_INVALID_ARGUMENT;
+  if (desc->batch == 0) return SV_OK;
+  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !first) return SV_ERR_INVALID_ARGUMENT;
+  if (rows->total_new > 0 && (!k || !v || !aligned_elem(k, rows->dtype) || !aligned_elem(v, rows->dtype)))
+    return SV_ERR_INVALID_ARGUMENT;
+  const KvCache c{const_cast<uint8_t*>(k_cache), const_cast<uint8_t*>(v_cache), const_cast<float*>(k_scale),
+                  const_cast<float*>(v_scale), page_table};
+  return kv_read(*desc, *rows, k, v, c, first, new_start, row_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sv_status sv_kv_commit(const sv_kv_desc* desc, int32_t nodes, int32_t path_len, const int32_t* page_table,
+                       const int32_t* ctx_lens, const int32_t* path, const int32_t* accept_len,
+                       uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale, int32_t* new_lens,
+                       int32_t* row_status, sv_stream_t stream) {
+  CallScope scope;
+  if (!kv_desc_ok(desc) || nodes < 1 || nodes > SV_MAX_TREE_NODES) return SV_ERR_INVALID_ARGUMENT;
+  if (path_len < 1 || path_len > SV_MAX_TREE_DEPTH + 1) return SV_ERR_INVALID_ARGUMENT;
+  if (desc->batch == 0) return SV_OK;
+  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens || !path || !accept_len || !new_lens ||
+      new_lens == ctx_lens)
+    return SV_ERR_INVALID_ARGUMENT;
+  return kv_commit(*desc, nodes, path_len, KvCache{k_cache, v_cache, k_scale, v_scale, page_table}, ctx_lens, path,
+                   accept_len, new_lens, row_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t sv_kv_attention_workspace_size(const sv_kv_attention_desc* desc) {
+  if (!kv_attention_desc_ok(desc, true)) return 0;
+  return kv_attention_workspace_bytes(*desc);
+}
+
+sv_status sv_kv_attention(const sv_kv_attention_desc* desc, const void* q, const uint8_t* k_cache,
+                          const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                          const int32_t* page_table, const int32_t* ctx_lens, const int32_t* new_start,
+                          const int32_t* parents, void* out, float* lse, int32_t* row_status,
+                          void* workspace, size_t workspace_bytes, sv_stream_t stream) {
+  CallScope scope;
+  if (!kv_attention_desc_ok(desc, new_start != nullptr)) return SV_ERR_INVALID_ARGUMENT;
+  if (desc->kv.batch == 0) return SV_OK;
+  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens || !workspace || !aligned16(workspace))
+    return SV_ERR_INVALID_ARGUMENT;
+  if (desc->total_new > 0 && (!q || !out || !aligned_elem(q, desc->dtype) || !aligned_elem(out, desc->dtype)))
+    return SV_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < sv_kv_attention_workspace_size(desc)) return SV_ERR_WORKSPACE_TOO_SMALL;
+  const KvCache c{const_cast<uint8_t*>(k_cache), const_cast<uint8_t*>(v_cache), const_cast<float*>(k_scale),
+                  const_cast<float*>(v_scale), page_table};
+  return kv_attention(*desc, q, c, ctx_lens, new_start, parents, out, lse, row_status, workspace,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -158,6 +158,26 @@ sv_status d2t_scatter(const void* in, int64_t in_stride, const int32_t* d2t, con
 sv_status build_t2d(const int32_t* d2t, int vd, int v, int32_t* t2d, int32_t* status,
                     cudaStream_t stream);
 
+// The target's cache (sv_kv.cu) and the attention over it (sv_kv_attention.cu).
+struct KvCache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+};
+sv_status kv_append(const sv_kv_desc& d, const sv_kv_rows_desc& r, const void* k, const void* v, const KvCache& c,
+                    const int32_t* ctx_lens, const int32_t* new_start, int32_t* row_status, cudaStream_t stream);
+sv_status kv_read(const sv_kv_desc& d, const sv_kv_rows_desc& r, void* k, void* v, const KvCache& c,
+                  const int32_t* first, const int32_t* new_start, int32_t* row_status, cudaStream_t stream);
+sv_status kv_commit(const sv_kv_desc& d, int nodes, int path_len, const KvCache& c, const int32_t* ctx_lens,
+                    const int32_t* path, const int32_t* accept_len, int32_t* new_lens, int32_t* row_status,
+                    cudaStream_t stream);
+size_t kv_attention_workspace_bytes(const sv_kv_attention_desc& d);
+sv_status kv_attention(const sv_kv_attention_desc& d, const void* q, const KvCache& c, const int32_t* ctx_lens,
+                       const int32_t* new_start, const int32_t* parents, void* out, float* lse, int32_t* row_status,
+                       void* workspace, cudaStream_t stream);
+
 #ifdef SV_DEBUG
 // This translation unit's debug word reader, registered at load time.
 static unsigned read_this_debug_word(bool reset) {

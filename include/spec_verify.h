@@ -66,6 +66,10 @@ typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_ROW_BAD_TOKEN 8           /* tree: a node token (n >= 1) outside [0, vocab) */
 #define SV_ROW_EMPTY 16              /* a logit row with no finite value */
 #define SV_ROW_RESAMPLE_FALLBACK 32  /* informational: residual mass was 0, drew from p_k */
+#define SV_ROW_BAD_PAGE 64           /* cache: a page_table entry in use outside [0, num_pages) */
+#define SV_ROW_BAD_LENGTH 128        /* cache: lengths that are negative or beyond the page table's row */
+#define SV_ROW_NOT_FINITE 256        /* cache: a NaN (stored as 0) or infinity (stored as +-448 * scale) was appended */
+#define SV_ROW_BAD_PATH 512          /* cache: a path that does not start at 0 and rise within [0, nodes) */
 
 /* Limits checked on the host. */
 #define SV_MAX_GAMMA 64
@@ -73,6 +77,7 @@ typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_MAX_TOPK 16
 #define SV_MAX_TREE_NODES 1024
 #define SV_MAX_TREE_DEPTH 64
+#define SV_MAX_HEAD_DIM 256
 
 typedef struct sv_chain_desc {
   int32_t batch;              /* B >= 0 (0: nothing to do) */
@@ -378,6 +383,176 @@ sv_status sv_sample(const sv_sample_desc* desc, const void* logits, const float*
 sv_status sv_softmax_topp(const sv_sample_desc* desc, const void* logits, float* out_probs,
                           int64_t out_row_stride, void* workspace, size_t workspace_bytes,
                           sv_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------
+ * The target model's cache and the attention of its scoring pass.
+ *
+ * Before a verify call the target scores the drafted tokens: their keys and
+ * values are appended to the cache of their sequence (sv_kv_append), every
+ * attention layer runs the new tokens' queries over it (sv_kv_attention),
+ * and after the verify call the accepted path stays (sv_kv_commit; for a
+ * chain the caller only keeps a shorter length).  sv_kv_read takes a range
+ * of tokens back out.
+ *
+ * The cache of one layer: pages of page_size tokens of 8-bit codes (e4m3:
+ * sign, 4 exponent bits, 3 mantissa bits, largest 448, no infinity) for keys
+ * and, with the same layout, for values, and one float scale for each
+ * (page, kv head) of either.  The stored value is code * scale; scales are
+ * powers of two, 2^-100 or larger, so a stored value is the input rounded to
+ * 4 significant bits whatever its page's scale, unless it lies below
+ * 2^-6 * scale.
+ *   code of (page g, head h, slot t, dim d):
+ *     cache[g * page_stride + h * head_stride + t * token_stride + d]
+ *   scale of (g, h): scale[g * kv_heads + h]
+ * Token j of sequence b lies in page page_table[b * table_stride +
+ * j / page_size], slot j % page_size.  Pages of different sequences, and the
+ * pages that one sequence's new tokens touch, must be different pages
+ * (sv_kv_read and sv_kv_attention may share pages between sequences).
+ *
+ * New tokens: sequence b has ctx_lens[b] cached tokens and n_b new ones after
+ * them.  With new_start == NULL every n_b is max_new and the new tokens'
+ * rows are b * max_new ..; else rows new_start[b] .. new_start[b + 1] - 1 of
+ * total_new rows, each n_b in [0, max_new].
+ *
+ * Sequences with ctx_lens[b] < 0, n_b outside [0, max_new], rows outside
+ * [0, total_new) or ctx_lens[b] + n_b beyond max_pages * page_size are left
+ * out and flagged SV_ROW_BAD_LENGTH; tokens on a page id outside
+ * [0, num_pages) are left out (neither written nor seen; read as 0) and
+ * their sequence is flagged SV_ROW_BAD_PAGE.
+ */
+typedef struct sv_kv_desc {
+  int32_t batch;         /* B in [0, 65535] */
+  int32_t kv_heads;      /* in [1, 1024] */
+  int32_t head_dim;      /* D: a multiple of 16 in [16, SV_MAX_HEAD_DIM] */
+  int32_t page_size;     /* 16, 32, 64 or 128 tokens */
+  int32_t num_pages;     /* pages in the pool, >= 1 */
+  int32_t max_pages;     /* entries of a page_table row, >= 1; max_pages * page_size < 2^31 */
+  int64_t page_stride;   /* codes between pages, heads and tokens of a page: */
+  int64_t head_stride;   /*   multiples of 16 (the pointers are 16-byte      */
+  int64_t token_stride;  /*   aligned), token_stride and head_stride >= D    */
+  int64_t table_stride;  /* entries between page_table rows, >= max_pages */
+} sv_kv_desc;
+
+/* The new tokens' rows.  Strides in elements between rows and between heads
+ * of a row (>= D; the D values of a head are contiguous). */
+typedef struct sv_kv_rows_desc {
+  int32_t max_new;       /* >= 0 */
+  int32_t total_new;     /* rows in all; batch * max_new when new_start is NULL */
+  sv_dtype dtype;
+  int32_t reserved;      /* 0 */
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+} sv_kv_rows_desc;
+
+/*
+ * Quantise the new tokens' keys and values and write them behind the cached
+ * tokens.  For each touched (page, head), with A the largest finite |x| of
+ * the new tokens in it and need(A) the smallest allowed power of two s with
+ * A <= 448 s:
+ *   the page holds no token before ctx_lens[b]: scale = need(A);
+ *   else scale = max(old scale, need(A)), and when that is larger the
+ *   earlier tokens' codes become round(code * old / new);
+ *   new codes are round(x / scale) (nearest, ties to even), NaN -> 0 and
+ *   infinities -> +-448, both flagged SV_ROW_NOT_FINITE.
+ * Slots behind the last new token keep their bytes.
+ *
+ *   k, v        [total_new, kv_heads, D] rows (rows->dtype, strides in rows).
+ *   page_table  [B, max_pages] int32;  ctx_lens [B] int32;
+ *   new_start   [B + 1] int32 or NULL.
+ *   k_cache, v_cache, k_scale, v_scale  the cache (updated in place).
+ *   row_status  optional [B] int32 (SV_ROW_*).
+ */
+sv_status sv_kv_append(const sv_kv_desc* desc, const sv_kv_rows_desc* rows, const void* k, const void* v,
+                       const int32_t* page_table, const int32_t* ctx_lens, const int32_t* new_start,
+                       uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale,
+                       int32_t* row_status, sv_stream_t stream);
+
+/*
+ * Read tokens first[b] .. first[b] + n_b - 1 of every sequence back:
+ * code * scale, rounded to rows->dtype, into k and v (rows as above, first
+ * in the place of ctx_lens).
+ */
+sv_status sv_kv_read(const sv_kv_desc* desc, const sv_kv_rows_desc* rows, const uint8_t* k_cache,
+                     const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                     const int32_t* page_table, const int32_t* first, const int32_t* new_start,
+                     void* k, void* v, int32_t* row_status, sv_stream_t stream);
+
+/*
+ * Keep the accepted path of a scored token tree: the tree's `nodes` tokens
+ * were appended behind ctx_lens[b], and path / accept_len are the results of
+ * sv_verify_tree, sv_verify_tree_path or sv_verify_tree_sample.  Token
+ * ctx_lens[b] + i becomes a copy of token ctx_lens[b] + path[b, i] for
+ * i = 0 .. accept_len[b], with the scales and codes that sv_kv_append would
+ * give the copied values, and new_lens[b] = ctx_lens[b] + accept_len[b] + 1.
+ * The bonus token is not in the cache yet: it is the next tree's root.
+ * path[b, 0] == -1 (a tree that verify flagged) keeps nothing: new_lens[b] =
+ * ctx_lens[b].  A path that does not start at 0 and rise strictly within
+ * [0, nodes), or accept_len[b] outside [0, path_len), also keeps nothing and
+ * is flagged SV_ROW_BAD_PATH.  A path that crosses a bad page is kept, as
+ * far as it can be read and written.
+ *
+ *   nodes     N in [1, SV_MAX_TREE_NODES];  path_len = D + 1 in [1, SV_MAX_TREE_DEPTH + 1].
+ *   path      [B, path_len] int32;  accept_len [B] int32.
+ *   new_lens  [B] int32, not ctx_lens itself.
+ */
+sv_status sv_kv_commit(const sv_kv_desc* desc, int32_t nodes, int32_t path_len, const int32_t* page_table,
+                       const int32_t* ctx_lens, const int32_t* path, const int32_t* accept_len,
+                       uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale, int32_t* new_lens,
+                       int32_t* row_status, sv_stream_t stream);
+
+typedef struct sv_kv_attention_desc {
+  sv_kv_desc kv;
+  int32_t heads;         /* query heads: a multiple of kv_heads, heads / kv_heads <= 128 */
+  int32_t max_new;       /* >= 0 */
+  int32_t total_new;     /* rows of q and out */
+  sv_dtype dtype;        /* of q and out */
+  float scale;           /* of the scores, finite (normally 1 / sqrt(D)) */
+  int32_t window;        /* 0: every earlier token is visible; W > 0: the last W, the query's own among them */
+  int32_t sinks;         /* >= 0: the first `sinks` tokens of a sequence stay visible under a window */
+  int32_t reserved;      /* 0 */
+  int64_t q_row_stride, q_head_stride;      /* elements; the D values of a head are contiguous */
+  int64_t out_row_stride, out_head_stride;
+} sv_kv_attention_desc;
+
+/* Workspace bytes for sv_kv_attention (scratch, no initialisation); 0 for an
+ * invalid descriptor. */
+size_t sv_kv_attention_workspace_size(const sv_kv_attention_desc* desc);
+
+/*
+ * Attention of the new tokens over the cache, which already holds them
+ * (sv_kv_append first).  Query i of sequence b with head h reads kv head
+ * h / (heads / kv_heads):
+ *   s_j = scale * <q, k_j>,  out = sum_j softmax(s)_j v_j,
+ *   lse = ln(sum_j exp(s_j)),
+ * over the tokens j that it sees.  Its position is p = ctx_lens[b] + i in a
+ * chain (parents == NULL), ctx_lens[b] + depth of node i in a tree; a cached
+ * token's position is its index, a new token's is its own query's.  Seen
+ * are, of the cached tokens and the query's ancestors (in a chain every
+ * earlier new token) and itself, those with p - position < window, and those
+ * with position < sinks (all of them when window == 0).  A query that sees
+ * nothing gets out = 0 and lse = -inf, as does every query of a sequence
+ * flagged SV_ROW_BAD_LENGTH whose rows are known.
+ *
+ *   q           [total_new, heads, D] (desc->dtype).
+ *   parents     optional [total_new] int32: node i's parent within its
+ *               sequence's new tokens, -1 for node 0 and 0 <= parent < i for
+ *               the others (as for sv_verify_tree); an entry outside that is
+ *               taken as -1, and flagged SV_ROW_BAD_PARENT.
+ *   out         [total_new, heads, D] (desc->dtype);  lse optional
+ *               [total_new, heads] float, contiguous.
+ *   row_status  optional [B] int32 (SV_ROW_*).
+ *
+ * The cache's codes reach the tensor cores without loss and sums are held in
+ * fp32.  NaN codes (0x7f, 0xff; sv_kv_append writes none) at visible tokens
+ * are not supported; what lies behind a sequence's last token is not seen,
+ * whatever its bytes.
+ */
+sv_status sv_kv_attention(const sv_kv_attention_desc* desc, const void* q, const uint8_t* k_cache,
+                          const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                          const int32_t* page_table, const int32_t* ctx_lens, const int32_t* new_start,
+                          const int32_t* parents, void* out, float* lse, int32_t* row_status,
+                          void* workspace, size_t workspace_bytes, sv_stream_t stream);
 
 /*
  * Profiling hooks (host-side; they add no device work).
