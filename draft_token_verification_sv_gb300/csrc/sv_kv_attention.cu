@@ -1,143 +1,513 @@
-// Attention of the new tokens over the 8-bit cache.
-#include "sv_kv.cuh"
+// Attention of few query rows for each kv head over the 8-bit cache: decoding
+// steps and short chains.
+//
+// O = sum_j 2^(s_j - m) v_j, one pass over the visible tokens with a running
+// maximum m for each row.  Both products run on the tensor cores
+// (m16n8k16): the 16 rows are the query heads that share a kv head (times the
+// new tokens), the codes are widened to fp16, which holds every e4m3 value,
+// and queries and weights are fp16 (a power of two for each row keeps queries
+// in range; fp32 queries and weights are the sum of two fp16).  Scales of K
+// and V are one factor for each page, on scores and weights.
+#include "sv_kv_schedule.cuh"
+
+#include <algorithm>
 
 namespace sv {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+// ------------------------------------------------------------ primitives ----
 
-struct AttentionParams {
-  KvView w;
-  const void* q;
-  void* out;
-  float* lse;
-  const int32_t* parents;
-  int64_t q_row_stride, q_head_stride, out_row_stride, out_head_stride;
-  int heads, group, window, sinks;
-  float scale_log2;  // scale * log2(e)
-};
+__device__ __forceinline__ uint32_t smem_address(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-// Parent of node i of a sequence whose rows start at `parents`, -1 for a root.
-__device__ __forceinline__ int tree_parent(const int32_t* parents, int i) {
-  const int p = __ldg(parents + i);
-  return p >= 0 && p < i ? p : -1;
+// 16 bytes to shared memory, zeros where !live.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0));
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(live ? 4 : 0));
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N));
 }
 
-// One block per (query, head): a tile of THREADS tokens at a time, one score
-// a thread, then the tile's values with one or two dims a thread.
-template <typename E, int THREADS>
-__global__ void __launch_bounds__(THREADS) kv_attention_simple_kernel(AttentionParams a) {
-  __shared__ float s_q[SV_MAX_HEAD_DIM];
-  __shared__ float s_p[THREADS], scratch[32];
-  __shared__ int s_page[THREADS];
+// c += a b, 16 x 16 times 16 x 8.
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t floats_to_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// The rest of two floats behind their fp16 values.
+__device__ __forceinline__ uint32_t rest_f16x2(float a, float b, uint32_t hi) {
+  const float2 h = f16x2_to_float2(hi);
+  return floats_to_f16x2(a - h.x, b - h.y);
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// 16 consecutive query values, 0 behind the row's end (dim is a multiple of 16).
+template <typename E>
+__device__ __forceinline__ void load_query16(const E* p, bool live, bool vec, float (&x)[16]) {
+  constexpr int kV = sizeof(E) == 2 ? 8 : 4;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+  if (!live) return;
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 16 / kV; ++i) unpack<E>(*reinterpret_cast<const uint4*>(p + i * kV), x + i * kV);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = Elem<E>::load(p + i);
+  }
+}
+
+// ----------------------------------------------------------------- shape ----
+
+constexpr int kRows = 16;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+
+// DP: head_dim rounded up to 64, 128 or 256 (the rest is zeros).
+template <int DP> struct Shape {
+  static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 4 : 3;
+  static constexpr int kBlocksPerSm = DP == 64 ? 4 : DP == 128 ? 3 : 2;
+  static constexpr int kStageBytes = 2 * kStep * DP;          // keys, values
+  static constexpr int kRing = kStages * (kStageBytes + 16);  // and their two scales
+  static constexpr int kMerge = kRows * DP * 4;               // a warp's values in the join of a block's warps
+  static constexpr int kPerWarp = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kShared = kWarps * kPerWarp;
+  static constexpr int kBlocks = kSMs * kBlocksPerSm;
+  static constexpr int kPart = kRows * (DP + 2);  // floats of a part in the workspace
+};
+
+// Where 16-byte chunk c of a token's row lies in a stage: the order makes
+// both reads below free of bank conflicts (two lanes' share of a value row
+// at DP = 64 excepted).  Keys: 8 lanes read 4 chunks of 2 rows.  Values: 8 or
+// 16 lanes read 32 bytes of each of 4 rows that lie two apart.
+template <int DP>
+__device__ __forceinline__ int key_chunk(int t, int c) {
+  if (DP == 64) return t * 4 + c;
+  return t * (DP / 16) + (c ^ ((t & 1) << 2));
+}
+template <int DP>
+__device__ __forceinline__ int value_chunk(int t, int c) {
+  if (DP == 64) return ((t & ~1) | ((t ^ (t >> 1)) & 1)) * 4 + (c ^ (((t >> 2) & 1) << 1));
+  return t * (DP / 16) + (c ^ (((t >> 1) & 3) << 1));
+}
+
+// ---------------------------------------------------------------- kernel ----
+
+// SPLIT: queries and weights as two fp16 each (fp32 inputs).
+template <typename E, int DP>
+__global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocksPerSm) kv_attention_kernel(AttentionParams a) {
+  using S = Shape<DP>;
+  constexpr bool SPLIT = sizeof(E) == 4;
+  constexpr int NQ = DP / 64;          // 16-byte chunks of a row that a lane reads
+  constexpr int NT = DP / 8;           // value tiles of 8 dims
+  constexpr int NV = DP == 64 ? 8 : 16;  // value tiles that one of a lane's pieces of a token feeds
+  extern __shared__ __align__(128) uint8_t shared[];
+  __shared__ CursorScratch s_cursor;
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   const KvView& w = a.w;
-  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const KvSpan s = kv_span(w, b);
-  const bool first = i == 0 && h == 0 && threadIdx.x == 0;
-  if (!s.ok && first) kv_flag(w, b, SV_ROW_BAD_LENGTH);
-  if (i >= s.n) return;
-  const int64_t row = s.row0 + i;
-  const int32_t* parents = a.parents ? a.parents + s.row0 : nullptr;
-  if (parents && s.ok && first)
-    for (int t = 0; t < s.n; ++t)
-      if (__ldg(parents + t) != (t == 0 ? -1 : tree_parent(parents, t)) || (t > 0 && tree_parent(parents, t) < 0))
-        kv_flag(w, b, SV_ROW_BAD_PARENT);
-  int depth = i;
-  if (parents) {
-    depth = 0;
-    for (int t = tree_parent(parents, i); t >= 0; t = tree_parent(parents, t)) ++depth;
-  }
-  const int pos = s.ok ? s.ctx + depth : 0;
-  const E* q = static_cast<const E*>(a.q) + row * a.q_row_stride + h * a.q_head_stride;
-  for (int d = threadIdx.x; d < w.dim; d += THREADS) s_q[d] = Elem<E>::load(q + d);
-  const int kvh = h / a.group;
-  float m = -CUDART_INF_F, l = 0.0f, o[2] = {0.0f, 0.0f};
-  const int end = s.ok ? s.ctx + i + 1 : 0;
-  for (int t0 = 0; t0 < end; t0 += THREADS) {
-    __syncthreads();
-    const int j = t0 + threadIdx.x;
-    bool seen = j < end;
-    int at = j;
-    if (seen && parents && j >= s.ctx) {
-      int t = i, back = 0;
-      while (t > j - s.ctx) t = tree_parent(parents, t), ++back;
-      seen = t == j - s.ctx;
-      at = pos - back;
-    }
-    seen = seen && (a.window == 0 || pos - at < a.window || at < a.sinks);
-    const int page = seen ? kv_page(w, b, j >> w.page_shift) : -1;
-    float x = -CUDART_INF_F;
-    if (page >= 0) {
-      const uint8_t* k = w.c.k + kv_offset(w, page, kvh, j & ((1 << w.page_shift) - 1));
-      float dot = 0.0f;
-      for (int d = 0; d < w.dim; d += 4) {
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(k + d);
-        const float2 u = f16x2_to_float2(e4m3x2_to_f16x2(c & 0xffffu)), v = f16x2_to_float2(e4m3x2_to_f16x2(c >> 16));
-        dot = fmaf(s_q[d], u.x, fmaf(s_q[d + 1], u.y, fmaf(s_q[d + 2], v.x, fmaf(s_q[d + 3], v.y, dot))));
-      }
-      x = dot * __ldg(w.c.k_scale + static_cast<int64_t>(page) * w.kv_heads + kvh) * a.scale_log2;
-    }
-    const float top = fmaxf(m, block_max<THREADS>(x, scratch));
-    const float base = top == -CUDART_INF_F ? 0.0f : top;
-    const float p = page >= 0 ? exp2f(x - base) : 0.0f;
-    const float fix = exp2f(m - base);
-    l = l * fix + block_sum<THREADS>(p, scratch);
-    m = top;
-    s_p[threadIdx.x] = page >= 0 ? p * __ldg(w.c.v_scale + static_cast<int64_t>(page) * w.kv_heads + kvh) : 0.0f;
-    s_page[threadIdx.x] = page;
-    __syncthreads();
-    o[0] *= fix;
-    o[1] *= fix;
-    const int n = min(THREADS, end - t0);
-    for (int t = 0; t < n; ++t) {
-      if (s_page[t] < 0) continue;
-      const uint8_t* v = w.c.v + kv_offset(w, s_page[t], kvh, (t0 + t) & ((1 << w.page_shift) - 1));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = lane >> 2, col = lane & 3;  // of the fragments
+  const int g = blockIdx.x, blocks = gridDim.x;
+  uint8_t* ring = shared + warp * S::kPerWarp;
+  const uint32_t ring_at = smem_address(ring);
+  const int page_mask = (1 << w.page_shift) - 1;
+
+  flag_sequences(a, g, blocks, kThreads);
+  Cursor c = find_cursor<kThreads, kRows, kWarps>(a, g, blocks, s_cursor);
+  if (threadIdx.x == 0 && a.joins) a.joins[g].rows = 0;
+
+  while (c.at < c.end) {
+    const KvSpan s = c.span;
+    const int32_t* parents = a.parents ? a.parents + s.row0 : nullptr;
+    const int r0 = c.rt * kRows, rows = min(kRows, s.n * a.group - r0);
+    const int i0 = r0 / a.group, i1 = (r0 + rows - 1) / a.group;
+    const ItemSteps steps = item_steps(a, s, i0, i1);
+    const int tiles = max(1, (steps.steps + kWarps - 1) / kWarps);
+    const int done = static_cast<int>(min(static_cast<long long>(tiles - c.tile), c.end - c.at));
+    const int step0 = c.tile * kWarps + warp;                       // this warp's steps:
+    const int step1 = min(steps.steps, (c.tile + done) * kWarps);   // step0, step0 + kWarps ..
+
+    // The stages in flight.  Bit of a stage in `bad`: its page is not there.
+    unsigned bad = 0;
+    int fill = 0;  // the next stage to fill
+    const auto fetch = [&](int step) {
+      if (step < step1) {
+        const int t0 = steps.token(step);
+        const int page = kv_page(w, c.b, t0 >> w.page_shift);
+        bad = (bad & ~(1u << fill)) | (page < 0 ? 1u << fill : 0u);
+        const int64_t o = kv_offset(w, max(page, 0), c.h, t0 & page_mask);
+        const uint32_t to = ring_at + fill * S::kStageBytes;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int d = threadIdx.x + k * THREADS;
-        if (d < w.dim) o[k] = fmaf(s_p[t], f16x2_to_float2(e4m3x2_to_f16x2(v[d])).x, o[k]);
+        for (int i = 0; i < kStep * DP / 16 / 32; ++i) {
+          const int t = (lane + 32 * i) / (DP / 16), ch = (lane + 32 * i) % (DP / 16);
+          const bool live = page >= 0 && t0 + t < steps.end && ch * 16 < w.dim;
+          const int64_t at = live ? o + t * w.token_stride + ch * 16 : 0;
+          copy16(to + key_chunk<DP>(t, ch) * 16, w.c.k + at, live);
+          copy16(to + kStep * DP + value_chunk<DP>(t, ch) * 16, w.c.v + at, live);
+        }
+        if (lane < 2)
+          copy4(ring_at + S::kStages * S::kStageBytes + fill * 16 + lane * 4,
+                (lane ? w.c.v_scale : w.c.k_scale) + static_cast<int64_t>(max(page, 0)) * w.kv_heads + c.h, page >= 0);
+      }
+      copy_commit();
+      fill = fill + 1 == S::kStages ? 0 : fill + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) fetch(step0 + i * kWarps);
+
+    // Queries: row's and row + 8's, as the first product's left side.
+    uint32_t q[NQ][4][4], q_rest[SPLIT ? NQ : 1][4][4];
+    float factor[2];  // scores in base 2 = factor * key scale * product
+    int token[2], pos[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = row + 8 * k;
+      const bool live = r < rows;
+      token[k] = (r0 + min(r, rows - 1)) / a.group;
+      const int head = c.h * a.group + (r0 + min(r, rows - 1)) % a.group;
+      const E* p = static_cast<const E*>(a.q) + (static_cast<int64_t>(s.row0) + token[k]) * a.q_row_stride + head * a.q_head_stride;
+      float x[NQ][16];
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        load_query16<E>(p + 64 * i + 16 * col, live && 64 * i + 16 * col < w.dim, a.q_vec, x[i]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[i][j]));
+      }
+      top = quad_max(top);
+      // the largest becomes 2^14 .. 2^15: fp16 keeps what is 2^-28 of it without loss for bf16 queries
+      const int e = top > 0.0f && top < CUDART_INF_F ? min(120, 141 - static_cast<int>(__float_as_uint(top) >> 23)) : 0;
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      factor[k] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float u = x[i][4 * j + 2 * h] * up, v = x[i][4 * j + 2 * h + 1] * up;
+            q[i][j][2 * h + k] = floats_to_f16x2(u, v);
+            if (SPLIT) q_rest[i][j][2 * h + k] = rest_f16x2(u, v, q[i][j][2 * h + k]);
+          }
+      pos[k] = s.ctx + token[k];
+      if (parents) {
+        int depth = 0;
+        for (int u = tree_parent(parents, token[k]); u >= 0; u = tree_parent(parents, u)) ++depth;
+        pos[k] = s.ctx + depth;
       }
     }
-  }
-  E* out = static_cast<E*>(a.out) + row * a.out_row_stride + h * a.out_head_stride;
-  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    // tokens before `all` are in every row's past; `far` is the furthest position of a row
+    const int all = parents ? s.ctx : s.ctx + i0 + 1, far = s.ctx + i1;
+
+    float o[NT][4] = {};
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.0f, 0.0f};
+    float v_ref = 0.0f, v_unit = 0.0f;  // weights are multiplied by v_scale * v_unit, v_unit = 2^12 / v_ref
+    int stage = 0;
+    for (int step = step0; step < step1; step += kWarps) {
+      copy_wait<S::kStages - 2>();
+      __syncwarp();
+      const uint8_t* k_at = ring + stage * S::kStageBytes;
+      const uint8_t* v_at = k_at + kStep * DP;
+      const float* sc = reinterpret_cast<const float*>(ring + S::kStages * S::kStageBytes + stage * 16);
+      const float k_scale = sc[0], v_scale = sc[1];
+      // scores of 16 tokens: x[n][0..1] row's, [2..3] row + 8's, tokens 8 n + 2 col + {0, 1}
+      float x[2][4] = {};
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int d = threadIdx.x + k * THREADS;
-    if (d >= w.dim) continue;
-    if (sizeof(E) == 2)
-      reinterpret_cast<uint16_t*>(out)[d] = static_cast<uint16_t>(floats_to_bf16x2(o[k] * inv, 0.0f));
-    else
-      reinterpret_cast<float*>(out)[d] = o[k] * inv;
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          const uint4 b = *reinterpret_cast<const uint4*>(k_at + 16 * key_chunk<DP>(8 * n + row, 4 * i + col));
+          const uint32_t word[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t b0 = e4m3x2_to_f16x2(word[j] & 0xffffu), b1 = e4m3x2_to_f16x2(word[j] >> 16);
+            mma(x[n], q[i][j][0], q[i][j][1], q[i][j][2], q[i][j][3], b0, b1);
+            if (SPLIT) mma(x[n], q_rest[i][j][0], q_rest[i][j][1], q_rest[i][j][2], q_rest[i][j][3], b0, b1);
+          }
+        }
+      const int t0 = steps.token(step);
+      const float f0 = factor[0] * k_scale, f1 = factor[1] * k_scale;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        x[n][0] *= f0;
+        x[n][1] *= f0;
+        x[n][2] *= f1;
+        x[n][3] *= f1;
+      }
+      const bool lost = (bad >> stage) & 1u;
+      const bool whole = !lost && t0 + kStep <= all && (a.window == 0 || far - t0 < a.window || t0 + kStep <= a.sinks);
+      if (!whole) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = t0 + 8 * n + 2 * col + (k & 1);
+            if (lost || j >= steps.end || !sees(a, parents, s.ctx, token[k >> 1], pos[k >> 1], j)) x[n][k] = -CUDART_INF_F;
+          }
+      }
+      if (v_scale > v_ref) {  // uniform: a page with larger values than any before
+        const float fix = v_ref / v_scale;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[t][k] *= fix;
+        v_ref = v_scale;
+        v_unit = 4096.0f / v_scale;
+      }
+      float top[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) top[k] = quad_max(fmaxf(fmaxf(x[0][2 * k], x[0][2 * k + 1]), fmaxf(x[1][2 * k], x[1][2 * k + 1])));
+      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float up = fmaxf(m[k], top[k]);
+          const float fix = up == -CUDART_INF_F ? 1.0f : ex2(m[k] - up);
+          m[k] = up;
+          l[k] *= fix;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            o[t][2 * k] *= fix;
+            o[t][2 * k + 1] *= fix;
+          }
+        }
+      }
+      const float unit = v_scale * v_unit;
+      uint32_t p[4], p_rest[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float base = m[k] == -CUDART_INF_F ? 0.0f : m[k];
+          const float u = ex2(x[n][2 * k] - base), v = ex2(x[n][2 * k + 1] - base);
+          l[k] += u + v;
+          p[2 * n + k] = floats_to_f16x2(u * unit, v * unit);
+          if (SPLIT) p_rest[2 * n + k] = rest_f16x2(u * unit, v * unit, p[2 * n + k]);
+        }
+      // values: a lane reads NV / 16 of the row of its four tokens, whose bytes i are dims of tile i
+#pragma unroll
+      for (int h = 0; h < NT / NV; ++h) {
+        uint32_t word[4][NV / 4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int token_at = 2 * col + (t & 1) + 8 * (t >> 1);
+          if constexpr (DP == 64) {
+            const uint2 b = *reinterpret_cast<const uint2*>(v_at + 16 * value_chunk<DP>(token_at, row >> 1) + 8 * (row & 1));
+            word[t][0] = b.x;
+            word[t][1] = b.y;
+          } else {
+            const uint4 b = *reinterpret_cast<const uint4*>(v_at + 16 * value_chunk<DP>(token_at, 8 * h + row));
+            word[t][0] = b.x;
+            word[t][1] = b.y;
+            word[t][2] = b.z;
+            word[t][3] = b.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NV / 4; ++i)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t u = __byte_perm(word[0][i], word[1][i], half ? 0x7362 : 0x5140);
+            const uint32_t v = __byte_perm(word[2][i], word[3][i], half ? 0x7362 : 0x5140);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t b0 = e4m3x2_to_f16x2(k ? u >> 16 : u & 0xffffu), b1 = e4m3x2_to_f16x2(k ? v >> 16 : v & 0xffffu);
+              const int t = h * NV + 4 * i + 2 * half + k;
+              mma(o[t], p[0], p[1], p[2], p[3], b0, b1);
+              if (SPLIT) mma(o[t], p_rest[0], p_rest[1], p_rest[2], p_rest[3], b0, b1);
+            }
+          }
+      }
+      __syncwarp();
+      fetch(step + (S::kStages - 1) * kWarps);
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+
+    // The block's warps joined: maxima and sums, then values, in shared memory.
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      l[k] = quad_sum(l[k]);
+      if (col == 0) {
+        s_m[warp][row + 8 * k] = m[k];
+        s_l[warp][row + 8 * k] = l[k];
+      }
+    }
+    __syncthreads();  // and every warp has read its ring
+    float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = row + 8 * k;
+      float top = s_m[0][r];
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_m[i][r]);
+      const float fix = (m[k] == -CUDART_INF_F ? 0.0f : ex2(m[k] - top)) * v_ref * (1.0f / 4096.0f);
+      // a lane's dims of tiles h NV ..: 2 NV in a row, from h (8 NV) + 2 NV col
+#pragma unroll
+      for (int h = 0; h < NT / NV; ++h)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int i = 0; i < NV / 4; ++i) {
+            const int d4 = h * (2 * NV) + col * (NV / 2) + half * (NV / 4) + i;  // in fours
+            const int t = h * NV + 4 * i, e = 2 * k + half;
+            *reinterpret_cast<float4*>(mine + r * DP + 4 * (d4 ^ ((row & 1) << 2 | col))) =
+                make_float4(o[t][e] * fix, o[t + 1][e] * fix, o[t + 2][e] * fix, o[t + 3][e] * fix);
+          }
+    }
+    __syncthreads();
+    const bool complete = done == tiles;
+    float* part = complete ? nullptr : a.parts + (2 * static_cast<int64_t>(g) + (c.tile == 0 ? 1 : 0)) * S::kPart;
+    for (int i = threadIdx.x; i < rows * (DP / 4); i += kThreads) {
+      const int r = i / (DP / 4), d4 = i % (DP / 4);
+      const int piece = d4 / (NV / 2) % 4;  // the lane column that wrote it
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float top = -CUDART_INF_F, total = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(shared + k * S::kPerWarp) + r * DP +
+                                                          4 * (d4 ^ ((r & 1) << 2 | piece)));
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+        top = fmaxf(top, s_m[k][r]);
+      }
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) total += s_m[k][r] == -CUDART_INF_F ? s_l[k][r] : s_l[k][r] * ex2(s_m[k][r] - top);
+      if (!complete) {
+        *reinterpret_cast<float4*>(part + r * DP + 4 * d4) = sum;
+        if (d4 == 0) *reinterpret_cast<float2*>(part + kRows * DP + 2 * r) = make_float2(top, total);
+      } else {
+        store_result<E>(a, s.row0, r0 + r, c.h, 4 * d4, sum, top, total);
+      }
+    }
+    if (!complete && c.tile == 0 && threadIdx.x == 0)
+      a.joins[g] = JoinRecord{s.row0, r0, rows, c.h, tile_owner(c.at + tiles - 1, c.total, c.blocks)};
+    __syncthreads();  // the ring and the maxima are free again
+    next_item<kRows>(a, c, done);
   }
-  if (a.lse && threadIdx.x == 0) a.lse[row * a.heads + h] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+}
+
+// One block for each part that began an item: its rows from all parts, in order.
+template <typename E, int DP, int ROWS>
+__global__ void __launch_bounds__(128) kv_attention_join_kernel(AttentionParams a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  const int g = blockIdx.x;
+  const JoinRecord j = a.joins[g];
+  constexpr int kPart = ROWS * (DP + 2);
+  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < j.rows * (DP / 4); i += blockDim.x * gridDim.y) {
+    const int r = i / (DP / 4), d4 = i % (DP / 4);
+    const auto part = [&](int k) { return a.parts + (2 * static_cast<int64_t>(k) + (k == g ? 1 : 0)) * kPart; };
+    float top = -CUDART_INF_F;
+    for (int k = g; k <= j.last; ++k) top = fmaxf(top, part(k)[ROWS * DP + 2 * r]);
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float total = 0.0f;
+#pragma unroll 4
+    for (int k = g; k <= j.last; ++k) {
+      const float2 ml = *reinterpret_cast<const float2*>(part(k) + ROWS * DP + 2 * r);
+      const float4 v = *reinterpret_cast<const float4*>(part(k) + r * DP + 4 * d4);
+      // a part that saw nothing has sums of 0 (or NaN, which stays)
+      const float fix = ml.x == -CUDART_INF_F ? 1.0f : ex2(ml.x - top);
+      total += ml.y * fix;
+      sum.x += v.x * fix;
+      sum.y += v.y * fix;
+      sum.z += v.z * fix;
+      sum.w += v.w * fix;
+    }
+    store_result<E>(a, j.row0, j.r0 + r, j.kv_head, 4 * d4, sum, top, total);
+  }
+}
+
+int round_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+
+template <typename E, int DP>
+sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspace, cudaStream_t stream) {
+  using S = Shape<DP>;
+  static FuncAttrCache attr;
+  const auto kernel = kv_attention_kernel<E, DP>;
+  if (!attr.ensure(reinterpret_cast<const void*>(kernel), S::kShared, false)) return SV_ERR_CUDA;
+  // no more blocks than there can be tiles
+  const int64_t row_tiles = (static_cast<int64_t>(d.max_new) * a.group + kRows - 1) / kRows;
+  const int64_t tiles = (static_cast<int64_t>(d.kv.max_pages) * d.kv.page_size + kStep * kWarps - 1) / (kStep * kWarps);
+  const int64_t items = row_tiles * d.kv.batch * d.kv.kv_heads;
+  const int blocks = items >= S::kBlocks || tiles >= S::kBlocks ? S::kBlocks
+                                                                : static_cast<int>(std::min<int64_t>(S::kBlocks, items * tiles));
+  a.parts = static_cast<float*>(workspace);
+  a.joins = reinterpret_cast<JoinRecord*>(a.parts + 2 * static_cast<int64_t>(S::kBlocks) * S::kPart);
+  kernel<<<blocks, kThreads, S::kShared, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  note_launch(stream);
+  if (blocks == 1 || tiles == 1) return SV_OK;  // no item has parts
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<E, DP, kRows>, a) != cudaSuccess) return SV_ERR_CUDA;
+  note_launch(stream);
+  return SV_OK;
+}
+
+template <int DP>
+size_t workspace_for() {
+  using S = Shape<DP>;
+  return S::kBlocks * (2 * S::kPart * sizeof(float) + sizeof(JoinRecord));
 }
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(const sv_kv_attention_desc&) { return 256; }
+size_t kv_attention_workspace_bytes(const sv_kv_attention_desc& d) {
+  const int dp = round_dim(d.kv.head_dim);
+  return align_up(dp == 64 ? workspace_for<64>() : dp == 128 ? workspace_for<128>() : workspace_for<256>(), 256);
+}
 
 sv_status kv_attention(const sv_kv_attention_desc& d, const void* q, const KvCache& c, const int32_t* ctx_lens,
                        const int32_t* new_start, const int32_t* parents, void* out, float* lse, int32_t* row_status,
                        void* workspace, cudaStream_t stream) {
-  (void)workspace;
   start_phases(stream);
-  if (row_status && cudaMemsetAsync(row_status, 0, static_cast<size_t>(d.kv.batch) * 4, stream) != cudaSuccess)
+  if (row_status && cudaMemsetAsync(row_status, 0, static_cast<size_t>(d.kv.batch) * sizeof(int32_t), stream) != cudaSuccess)
     return SV_ERR_CUDA;
   if (d.max_new == 0 || d.total_new == 0) return SV_OK;
-  const AttentionParams a{kv_view(d.kv, c, ctx_lens, new_start, d.max_new, d.total_new, row_status), q, out, lse, parents,
-                          d.q_row_stride, d.q_head_stride, d.out_row_stride, d.out_head_stride, d.heads,
-                          d.heads / d.kv.kv_heads, d.window, d.sinks, d.scale * kLog2e};
-  const dim3 grid(d.max_new, d.heads, d.kv.batch);
+  const int64_t e = d.dtype == SV_BF16 ? 2 : 4;
+  const auto aligned = [&](const void* p, int64_t row, int64_t head) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ((row | head) * e) % 16 == 0;
+  };
+  AttentionParams a{kv_view(d.kv, c, ctx_lens, new_start, d.max_new, d.total_new, row_status),
+                    q, out, lse, parents,
+                    d.q_row_stride, d.q_head_stride, d.out_row_stride, d.out_head_stride,
+                    d.heads, d.heads / d.kv.kv_heads, d.window, d.sinks, d.scale * kLog2e,
+                    aligned(q, d.q_row_stride, d.q_head_stride), aligned(out, d.out_row_stride, d.out_head_stride),
+                    nullptr, nullptr};
+  const int dp = round_dim(d.kv.head_dim);
   if (d.dtype == SV_BF16)
-    kv_attention_simple_kernel<uint16_t, 128><<<grid, 128, 0, stream>>>(a);
-  else
-    kv_attention_simple_kernel<float, 128><<<grid, 128, 0, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
-  note_launch(stream);
-  return SV_OK;
+    return dp == 64 ? launch<uint16_t, 64>(a, d, workspace, stream)
+                    : dp == 128 ? launch<uint16_t, 128>(a, d, workspace, stream) : launch<uint16_t, 256>(a, d, workspace, stream);
+  return dp == 64 ? launch<float, 64>(a, d, workspace, stream)
+                  : dp == 128 ? launch<float, 128>(a, d, workspace, stream) : launch<float, 256>(a, d, workspace, stream);
 }
 
 }  // namespace sv
