@@ -10,8 +10,6 @@
 // and V are one factor for each page, on scores and weights.
 #include "sv_kv_schedule.cuh"
 
-#include <algorithm>
-
 namespace sv {
 
 namespace {
@@ -408,36 +406,6 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocksPerSm) kv_attentio
   }
 }
 
-// One block for each part that began an item: its rows from all parts, in order.
-template <typename E, int DP, int ROWS>
-__global__ void __launch_bounds__(128) kv_attention_join_kernel(AttentionParams a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
-  const int g = blockIdx.x;
-  const JoinRecord j = a.joins[g];
-  constexpr int kPart = ROWS * (DP + 2);
-  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < j.rows * (DP / 4); i += blockDim.x * gridDim.y) {
-    const int r = i / (DP / 4), d4 = i % (DP / 4);
-    const auto part = [&](int k) { return a.parts + (2 * static_cast<int64_t>(k) + (k == g ? 1 : 0)) * kPart; };
-    float top = -CUDART_INF_F;
-    for (int k = g; k <= j.last; ++k) top = fmaxf(top, part(k)[ROWS * DP + 2 * r]);
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float total = 0.0f;
-#pragma unroll 4
-    for (int k = g; k <= j.last; ++k) {
-      const float2 ml = *reinterpret_cast<const float2*>(part(k) + ROWS * DP + 2 * r);
-      const float4 v = *reinterpret_cast<const float4*>(part(k) + r * DP + 4 * d4);
-      // a part that saw nothing has sums of 0 (or NaN, which stays)
-      const float fix = ml.x == -CUDART_INF_F ? 1.0f : ex2(ml.x - top);
-      total += ml.y * fix;
-      sum.x += v.x * fix;
-      sum.y += v.y * fix;
-      sum.z += v.z * fix;
-      sum.w += v.w * fix;
-    }
-    store_result<E>(a, j.row0, j.r0 + r, j.kv_head, 4 * d4, sum, top, total);
-  }
-}
-
 int round_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 template <typename E, int DP>
@@ -446,28 +414,16 @@ sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspa
   static FuncAttrCache attr;
   const auto kernel = kv_attention_kernel<E, DP>;
   if (!attr.ensure(reinterpret_cast<const void*>(kernel), S::kShared, false)) return SV_ERR_CUDA;
-  // no more blocks than there can be tiles
   const int64_t row_tiles = (static_cast<int64_t>(d.max_new) * a.group + kRows - 1) / kRows;
   const int64_t tiles = (static_cast<int64_t>(d.kv.max_pages) * d.kv.page_size + kStep * kWarps - 1) / (kStep * kWarps);
-  const int64_t items = row_tiles * d.kv.batch * d.kv.kv_heads;
-  const int blocks = items >= S::kBlocks || tiles >= S::kBlocks ? S::kBlocks
-                                                                : static_cast<int>(std::min<int64_t>(S::kBlocks, items * tiles));
+  const int blocks = schedule_blocks(row_tiles * d.kv.batch * d.kv.kv_heads, tiles, S::kBlocks);
   a.parts = static_cast<float*>(workspace);
   a.joins = reinterpret_cast<JoinRecord*>(a.parts + 2 * static_cast<int64_t>(S::kBlocks) * S::kPart);
   kernel<<<blocks, kThreads, S::kShared, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   if (blocks == 1 || tiles == 1) return SV_OK;  // no item has parts
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute early[1];
-  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = early;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<E, DP, kRows>, a) != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_join<E, DP, kRows>(a, blocks, stream) != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   return SV_OK;
 }
@@ -481,6 +437,7 @@ size_t workspace_for() {
 }  // namespace
 
 size_t kv_attention_workspace_bytes(const sv_kv_attention_desc& d) {
+  if (kv_attention_takes_tiles(d)) return kv_attention_tiles_workspace(d);
   const int dp = round_dim(d.kv.head_dim);
   return align_up(dp == 64 ? workspace_for<64>() : dp == 128 ? workspace_for<128>() : workspace_for<256>(), 256);
 }
@@ -493,15 +450,17 @@ sv_status kv_attention(const sv_kv_attention_desc& d, const void* q, const KvCac
     return SV_ERR_CUDA;
   if (d.max_new == 0 || d.total_new == 0) return SV_OK;
   const int64_t e = d.dtype == SV_BF16 ? 2 : 4;
-  const auto aligned = [&](const void* p, int64_t row, int64_t head) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ((row | head) * e) % 16 == 0;
+  const auto aligned = [&](const void* p, int64_t row, int64_t head, int to) {
+    return reinterpret_cast<uintptr_t>(p) % to == 0 && (row * e) % to == 0 && (head * e) % to == 0;
   };
   AttentionParams a{kv_view(d.kv, c, ctx_lens, new_start, d.max_new, d.total_new, row_status),
                     q, out, lse, parents,
                     d.q_row_stride, d.q_head_stride, d.out_row_stride, d.out_head_stride,
                     d.heads, d.heads / d.kv.kv_heads, d.window, d.sinks, d.scale * kLog2e,
-                    aligned(q, d.q_row_stride, d.q_head_stride), aligned(out, d.out_row_stride, d.out_head_stride),
+                    aligned(q, d.q_row_stride, d.q_head_stride, 16), aligned(out, d.out_row_stride, d.out_head_stride, 16),
+                    aligned(out, d.out_row_stride, d.out_head_stride, 32),
                     nullptr, nullptr};
+  if (kv_attention_takes_tiles(d)) return kv_attention_tiles(a, d, workspace, stream);
   const int dp = round_dim(d.kv.head_dim);
   if (d.dtype == SV_BF16)
     return dp == 64 ? launch<uint16_t, 64>(a, d, workspace, stream)

@@ -1,0 +1,664 @@
+// Attention of many query rows for each kv head over the 8-bit cache: token
+// trees, long chains, stretches of a prompt.
+//
+// 128 query rows at a time against tiles of 128 tokens on the 5th-generation
+// tensor cores: S = Q K^T and O += P V, accumulators in tensor memory.  The
+// left sides (Q, and the weights P, which take the place of the scores they
+// come from) are in tensor memory too, so that only K and V are read from
+// shared memory.  One block per SM, three roles:
+//   8 warps load codes, widen them to fp16 (which holds every e4m3 value) and
+//     lay them out for the products, a tile ahead in registers and two in
+//     shared memory;
+//   1 thread issues the products: S of tile t before P V of tile t - 1;
+//   4 warps turn scores into weights, a row a thread, with a running maximum
+//     that moves only when it is exceeded by 2^7 (then O is scaled anew).
+// Work is shared out as in sv_kv_schedule.cuh.
+#include "sv_kv_schedule.cuh"
+#include "sv_tcgen05.cuh"
+
+#include <type_traits>
+
+namespace sv {
+
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kTileSteps = 8;
+constexpr int kTokens = kStep * kTileSteps;
+// warps 0-3, 4-11 and 12 (13-15 idle: registers move in fours of warps)
+constexpr int kSoftmaxWarps = 4, kLoadWarps = 8;
+constexpr int kLoadThreads = 32 * kLoadWarps;
+constexpr int kThreads = 32 * (kSoftmaxWarps + kLoadWarps + 4);
+constexpr int kSoftmaxRegisters = 248, kLoadRegisters = 112, kProductRegisters = 32;
+static_assert(4 * kSoftmaxRegisters + 8 * kLoadRegisters + 4 * kProductRegisters <= 16 * 128, "registers of a block");
+constexpr float kLift = 8.0f;  // weights are 2^8 times what they stand for: fp16 then keeps 2^-22 of the largest
+
+template <int DP> struct Tiles {
+  static constexpr int kTileBytes = kTokens * DP * 2;      // fp16 keys or values of a tile
+  static constexpr int kBlockBytes = kTokens * 128;        // 64 dims of it
+  static constexpr int kStages = 2;
+  static constexpr int kOperands = 2 * kStages * kTileBytes;
+  // 1 KB to find a 1024-byte boundary; more than half of an SM's shared memory keeps it to one block
+  static constexpr int kShared = (kOperands > 118 * 1024 ? kOperands : 118 * 1024) + 1024;
+  // tensor memory, in columns: O, Q, two tiles of scores
+  static constexpr int kO = 0, kQ = DP, kS = DP + DP / 2;
+  static constexpr int kColumns = 512;
+  static constexpr int kPart = kRows * (DP + 2);
+};
+
+struct TileInfo {  // of a tile's eight steps
+  float k_scale[kTileSteps];
+  float v_log2[kTileSteps];  // log2 of the values' scale, kNoScale for none
+  int lost;                  // bits of steps whose page is not there
+};
+
+constexpr float kNoScale = -1000.0f;
+
+struct Shared {
+  CursorScratch cursor;
+  uint64_t k_full[2], v_full[2], s_full[2], p_ready[2], pv_done[2], info_full[4], q_ready, last;
+  TileInfo info[4];
+  uint32_t tmem;
+  int gave_up;
+};
+
+// 16 codes as fp16: 32 bytes.
+__device__ __forceinline__ void widen(const uint4& c, uint4& lo, uint4& hi) {
+  lo = make_uint4(e4m3x2_to_f16x2(c.x & 0xffffu), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y & 0xffffu), e4m3x2_to_f16x2(c.y >> 16));
+  hi = make_uint4(e4m3x2_to_f16x2(c.z & 0xffffu), e4m3x2_to_f16x2(c.z >> 16), e4m3x2_to_f16x2(c.w & 0xffffu), e4m3x2_to_f16x2(c.w >> 16));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Bits j of [from, to) for the 16 tokens from `base` on.
+__device__ __forceinline__ uint32_t bits16(int base, int from, int to) {
+  const int a = min(max(from - base, 0), 16), b = min(max(to - base, 0), 16);
+  return ((1u << b) - 1u) & ~((1u << a) - 1u);
+}
+
+// The part of an item that a block works on.
+struct Part {
+  ItemSteps steps;
+  int r0, rows, i0, i1;
+  int tiles, tile0, count;  // the item's tiles; first and number of the block's
+};
+
+__device__ __forceinline__ Part part_of(const AttentionParams& a, const Cursor& c) {
+  Part p;
+  p.r0 = c.rt * kRows;
+  p.rows = min(kRows, c.span.n * a.group - p.r0);
+  p.i0 = p.r0 / a.group;
+  p.i1 = (p.r0 + p.rows - 1) / a.group;
+  p.steps = item_steps(a, c.span, p.i0, p.i1);
+  p.tiles = max(1, (p.steps.steps + kTileSteps - 1) / kTileSteps);
+  p.tile0 = c.tile;
+  p.count = static_cast<int>(min(static_cast<long long>(p.tiles - c.tile), c.end - c.at));
+  return p;
+}
+
+// ---- loading ----
+
+// A step of a tile that is yet to be loaded (lanes 0-7 of every loading warp).
+struct StepAhead {
+  int page, slot, count;  // count: its tokens in sight, 0 for none
+  int b, h;
+};
+
+template <int DP>
+__device__ bool load_role(const AttentionParams& a, Cursor c, Shared& sh, uint8_t* k_tiles, uint8_t* v_tiles) {
+  using T = Tiles<DP>;
+  constexpr int kChunks = DP / 16;                        // of a token
+  constexpr int kPer = kLoadThreads / kChunks;            // tokens of a pass
+  constexpr int NI = kTokens / kPer;                      // passes
+  const KvView& w = a.w;
+  const int tid = threadIdx.x - 32 * kSoftmaxWarps, lane = tid & 31;
+  const int t0 = tid / kChunks, ch = tid % kChunks;
+  const bool in_dim = ch * 16 < w.dim;
+  const int page_mask = (1 << w.page_shift) - 1;
+  if (c.at >= c.end) return true;
+  const long long tiles = c.end - c.at;
+  Part p = part_of(a, c);
+  int next = 0;  // of the part's tiles, the one to look up
+
+  // Page ids are looked up a tile before the codes are asked for.
+  StepAhead ahead{0, 0, 0, 0, 0};
+  const auto look_up = [&]() {
+    const int s = (p.tile0 + next) * kTileSteps + (lane & 7);
+    ahead.count = 0;
+    if (s < p.steps.steps) {
+      const int j = p.steps.token(s);
+      ahead.count = min(kStep, p.steps.end - j);
+      ahead.slot = j & page_mask;
+      ahead.page = sv_in(j >> w.page_shift, w.max_pages) ? __ldg(w.c.page_table + c.b * w.table_stride + (j >> w.page_shift)) : -1;
+    }
+    ahead.b = c.b;
+    ahead.h = c.h;
+    if (++next == p.count) {
+      next_item<kRows>(a, c, p.count);
+      next = 0;
+      if (c.at < c.end) p = part_of(a, c);
+    }
+  };
+  int64_t chunk[NI];  // of the tile that is asked for next; -1: zeros
+  int64_t scale = -1;
+  bool lost = false;
+  const auto resolve = [&]() {
+    const bool there = ahead.count > 0 && ahead.page >= 0 && ahead.page < w.num_pages;
+    lost = ahead.count > 0 && !there;
+    if (lost) kv_flag(w, ahead.b, SV_ROW_BAD_PAGE);
+    const int64_t base = there ? kv_offset(w, ahead.page, ahead.h, ahead.slot) : -1;
+    scale = there ? static_cast<int64_t>(ahead.page) * w.kv_heads + ahead.h : -1;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int t = t0 + i * kPer;
+      const int64_t from = __shfl_sync(0xffffffffu, base, t / kStep);
+      const int count = __shfl_sync(0xffffffffu, ahead.count, t / kStep);
+      chunk[i] = from >= 0 && t % kStep < count && in_dim ? from + (t % kStep) * w.token_stride + ch * 16 : -1;
+    }
+  };
+  // two tiles in flight in registers
+  uint4 k[2][NI], v[2][NI];
+  float k_scale[2], v_scale[2];
+  unsigned gone[2];
+  const auto load = [&](uint4 (&x)[NI], const uint8_t* from) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (chunk[i] >= 0) x[i] = ldg_stream(from + chunk[i]);
+    }
+  };
+  const auto load_scales = [&](int buffer) {
+    k_scale[buffer] = v_scale[buffer] = 0.0f;
+    if (tid < kTileSteps && scale >= 0) {
+      k_scale[buffer] = __ldg(w.c.k_scale + scale);
+      v_scale[buffer] = __ldg(w.c.v_scale + scale);
+    }
+    gone[buffer] = __ballot_sync(0xffffffffu, lost) & 0xffu;
+  };
+  look_up();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (i < tiles) {
+      resolve();
+      load(k[i], w.c.k);
+      load_scales(i);
+      load(v[i], w.c.v);
+      if (i + 1 < tiles) look_up();
+    }
+  // both kinds lie alike: rows of 64 dims, swizzled
+  const auto put = [&](uint8_t* tile, const uint4 (&x)[NI]) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int t = t0 + i * kPer;
+      uint4 half[2];
+      widen(x[i], half[0], half[1]);
+      uint8_t* row = tile + (ch >> 2) * T::kBlockBytes + t * 128;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int turn = h ^ (ch >> 2 & 1);  // the two blocks' lanes write different banks
+        *reinterpret_cast<uint4*>(row + (((2 * (ch & 3) + turn) ^ (t & 7)) << 4)) = turn ? half[1] : half[0];
+      }
+    }
+    tc::publish_shared();
+  };
+  for (long long it0 = 0; it0 < tiles; it0 += 2) {
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const long long it = it0 + st;
+      if (it >= tiles) break;
+      const uint32_t before = static_cast<uint32_t>((it >> 1) & 1) ^ 1u;  // parity of the stage's last use
+      if (it >= 2 && !__all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&sh.s_full[st]), before, &sh.gave_up))) return false;
+      put(k_tiles + st * T::kTileBytes, k[st]);
+      // four slots: softmax has read tile it - 4 before S of tile it - 2 was issued
+      TileInfo& info = sh.info[it & 3];
+      if (tid < kTileSteps) {
+        const uint32_t bits = __float_as_uint(v_scale[st]);
+        info.k_scale[tid] = k_scale[st];
+        info.v_log2[tid] = v_scale[st] > 0.0f ? ((bits & 0x7fffffu) == 0 && bits >= 0x00800000u
+                                                     ? static_cast<float>(static_cast<int>(bits >> 23) - 127) : log2f(v_scale[st]))
+                                              : kNoScale;
+        if (tid == 0) info.lost = static_cast<int>(gone[st]);
+      }
+      __syncwarp();
+      if (lane == 0) tc::barrier_arrive(tc::smem_address(&sh.k_full[st]));
+      if (tid == 0) tc::barrier_arrive(tc::smem_address(&sh.info_full[it & 3]));
+      if (it + 2 < tiles) {
+        resolve();
+        load(k[st], w.c.k);
+        load_scales(st);
+      }
+      if (it >= 2 && !__all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&sh.pv_done[st]), before, &sh.gave_up))) return false;
+      put(v_tiles + st * T::kTileBytes, v[st]);
+      __syncwarp();
+      if (lane == 0) tc::barrier_arrive(tc::smem_address(&sh.v_full[st]));
+      if (it + 2 < tiles) {
+        load(v[st], w.c.v);
+        if (it + 3 < tiles) look_up();
+      }
+    }
+  }
+  return true;
+}
+
+// ---- products ----
+
+template <int DP>
+__device__ bool product_role(const AttentionParams& a, Cursor c, Shared& sh, uint32_t k_tiles, uint32_t v_tiles, uint32_t tmem) {
+  using T = Tiles<DP>;
+  constexpr uint32_t kScores = tc::product_f16(kTokens, false), kValues = tc::product_f16(DP, true);
+  const auto wait = [&](uint64_t& bar, long long n) {
+    const bool ok = tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up);
+    tc::fence_after();
+    return ok;
+  };
+  const auto weigh = [&](long long it, bool first) {  // O (+)= P V of tile it
+    const int st = it & 1;
+    if (!wait(sh.v_full[st], it >> 1) || !wait(sh.p_ready[st], it >> 1)) return false;
+#pragma unroll
+    for (int k = 0; k < kTokens / 16; ++k)
+      tc::product(tmem + T::kO, tmem + T::kS + st * kTokens + k * 8,
+                  tc::tile_descriptor(v_tiles + st * T::kTileBytes + k * 2048, T::kBlockBytes, 1024), kValues, !first || k > 0);
+    tc::products_arrive(tc::smem_address(&sh.pv_done[st]));
+    return true;
+  };
+  long long it = 0;
+  for (long long item = 0; c.at < c.end; ++item) {
+    const Part p = part_of(a, c);
+    if (!wait(sh.q_ready, item)) return false;
+    for (int t = 0; t < p.count; ++t, ++it) {
+      const int st = it & 1;
+      if (!wait(sh.k_full[st], it >> 1)) return false;
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k)
+        tc::product(tmem + T::kS + st * kTokens, tmem + T::kQ + k * 8,
+                    tc::tile_descriptor(k_tiles + st * T::kTileBytes + (k >> 2) * T::kBlockBytes + (k & 3) * 32, 16, 1024), kScores, k > 0);
+      tc::products_arrive(tc::smem_address(&sh.s_full[st]));
+      if (t > 0 && !weigh(it - 1, t == 1)) return false;
+    }
+    if (!weigh(it - 1, p.count == 1)) return false;
+    next_item<kRows>(a, c, p.count);
+  }
+  return true;
+}
+
+// ---- scores to weights, and results ----
+
+// Which of a tile's tokens the thread's row sees, 32 to a word.
+__device__ __forceinline__ void seen_tokens(const AttentionParams& a, const ItemSteps& steps, int s0, int lost, const int32_t* parents,
+                                            int ctx, int token, int pos, uint32_t (&seen)[4]) {
+  const int past = parents ? ctx : min(pos + 1, steps.end);
+  const int from = a.window ? max(0, pos - a.window + 1) : 0;
+#pragma unroll
+  for (int i = 0; i < kTileSteps; ++i) {
+    uint32_t b = 0;
+    if (s0 + i < steps.steps && !(lost >> i & 1)) {
+      const int base = steps.token(s0 + i);
+      b = bits16(base, from, past);
+      if (a.window) b |= bits16(base, 0, min(a.sinks, past));
+      if (parents && base + kStep > ctx)
+        for (int u = token, back = 0; u >= 0; u = tree_parent(parents, u), ++back) {
+          const int j = ctx + u - base;
+          if (j >= 0 && j < kStep && (a.window == 0 || back < a.window || pos - back < a.sinks)) b |= 1u << j;
+        }
+    }
+    if (i & 1)
+      seen[i >> 1] |= b << 16;
+    else
+      seen[i >> 1] = b;
+  }
+}
+
+// The largest of 16 scores (that are seen).
+template <bool MASKED>
+__device__ __forceinline__ float largest16(const uint32_t* x, uint32_t seen) {
+  float v[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = MASKED && !(seen >> k & 1u) ? -CUDART_INF_F : __uint_as_float(x[k]);
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+    for (int k = 0; k < n; ++k) v[k] = fmaxf(v[k], v[k + n]);
+  return v[0];
+}
+
+// 32 scores to weights 2^(x f + c): packed into w, and their sums by steps.
+template <bool MASKED>
+__device__ __forceinline__ float2 weights32(const uint32_t (&x)[32], uint32_t seen, float f0, float f1, float c0, float c1, uint32_t (&w)[16]) {
+  float2 sums;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint64_t f = tc::pair(h ? f1 : f0, h ? f1 : f0), c = tc::pair(h ? c1 : c0, h ? c1 : c0);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int n = 16 * h + 2 * k;
+      float2 e = tc::unpair(tc::fma2(tc::pair(__uint_as_float(x[n]), __uint_as_float(x[n + 1])), f, c));
+      e.x = ex2(e.x);
+      e.y = ex2(e.y);
+      if (MASKED) {
+        e.x = seen >> n & 1u ? e.x : 0.0f;
+        e.y = seen >> (n + 1) & 1u ? e.y : 0.0f;
+      }
+      sum = tc::add2(sum, tc::pair(e.x, e.y));
+      w[8 * h + k] = pack_f16x2(e.x, e.y);
+    }
+    const float2 s = tc::unpair(sum);
+    (h ? sums.y : sums.x) = s.x + s.y;
+  }
+  return sums;
+}
+
+template <int DP>
+__device__ bool softmax_role(const AttentionParams& a, Cursor c, Shared& sh, uint32_t tmem, int g) {
+  using T = Tiles<DP>;
+  const int lane = threadIdx.x & 31, r = threadIdx.x;
+  const uint32_t mine = tmem + ((threadIdx.x >> 5) << 21);  // the warp's 32 lanes
+  const auto wait = [&](uint64_t& bar, long long n) {
+    const bool ok = __all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up));
+    tc::fence_after();
+    return ok;
+  };
+  const auto arrive = [&](uint64_t& bar) {
+    tc::wait_stores();
+    tc::fence_before();
+    __syncwarp();
+    if (lane == 0) tc::barrier_arrive(tc::smem_address(&bar));
+  };
+  long long it = 0;
+  while (c.at < c.end) {
+    const Part p = part_of(a, c);
+    const KvSpan s = c.span;
+    const int32_t* parents = a.parents ? a.parents + s.row0 : nullptr;
+    const int row = p.r0 + min(r, p.rows - 1);
+    const int token = row / a.group, head = c.h * a.group + row % a.group;
+    const int64_t out_row = static_cast<int64_t>(s.row0) + token;
+
+    // the row's queries, scaled by a power of two into fp16's range (exact for bf16 down to 2^-28 of the largest)
+    float factor;
+    {
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + out_row * a.q_row_stride + head * a.q_head_stride;
+      uint4 raw[DP / 8];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < DP / 8; ++i) {
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (r < p.rows && i * 8 < a.w.dim) {
+          if (a.q_vec) {
+            raw[i] = *reinterpret_cast<const uint4*>(q + i * 8);
+          } else {
+            const uint16_t* e = q + i * 8;
+            raw[i] = make_uint4(__ldg(e) | __ldg(e + 1) << 16, __ldg(e + 2) | __ldg(e + 3) << 16,
+                                __ldg(e + 4) | __ldg(e + 5) << 16, __ldg(e + 6) | __ldg(e + 7) << 16);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < DP / 8; ++i) {
+        top = __vmaxu2(__vmaxu2(top, raw[i].x & 0x7fff7fffu), raw[i].y & 0x7fff7fffu);
+        top = __vmaxu2(__vmaxu2(top, raw[i].z & 0x7fff7fffu), raw[i].w & 0x7fff7fffu);
+      }
+      const int exponent = static_cast<int>(max(top >> 16, top & 0xffffu) >> 7);
+      const int e = exponent == 255 || top == 0 ? 0 : min(120, 141 - exponent);
+      __syncwarp();
+      // a negative factor goes into the queries, so that larger products are larger scores
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
+      factor = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      uint32_t x[32];
+#pragma unroll
+      for (int i = 0; i < DP / 8; ++i) {
+        float f[8];
+        unpack<uint16_t>(raw[i], f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[(i & 7) * 4 + k] = pack_f16x2(f[2 * k] * up, f[2 * k + 1] * up);
+        if ((i & 7) == 7) tc::tmem_store32(mine + T::kQ + (i >> 3) * 32, x);
+      }
+      arrive(sh.q_ready);
+    }
+    int pos = s.ctx + token;
+    if (parents) {
+      int depth = 0;
+      for (int u = tree_parent(parents, token); u >= 0; u = tree_parent(parents, u)) ++depth;
+      pos = s.ctx + depth;
+      __syncwarp();
+    }
+    // tokens before `all` are in every row's past; `far` is the furthest position of a row
+    const int all = parents ? s.ctx : s.ctx + p.i0 + 1, far = s.ctx + p.i1;
+
+    float m = -CUDART_INF_F, l = 0.0f, v_ref = kNoScale;  // v_ref: log2 of the values' unit
+    for (int t = 0; t < p.count; ++t, ++it) {
+      const int st = it & 1;
+      // (not k_full: the loaders may be a phase past it)
+      if (!wait(sh.info_full[it & 3], it >> 2) || !wait(sh.s_full[st], it >> 1)) return false;
+      const TileInfo& info = sh.info[it & 3];
+      const uint32_t scores = mine + T::kS + st * kTokens;
+      const int s0 = (p.tile0 + t) * kTileSteps, s1 = s0 + kTileSteps - 1;
+      const int first = p.steps.token(s0), last = p.steps.token(s1);
+      const int lost = info.lost;
+      float f[kTileSteps], unit[kTileSteps];
+      float v_top = kNoScale;
+#pragma unroll
+      for (int i = 0; i < kTileSteps; ++i) {
+        f[i] = factor * info.k_scale[i];
+        unit[i] = info.v_log2[i];
+        v_top = fmaxf(v_top, unit[i]);
+      }
+      const auto tile = [&](auto masked) {
+        constexpr bool M = decltype(masked)::value;
+        uint32_t seen[4] = {};
+        if (M) {
+          seen_tokens(a, p.steps, s0, lost, parents, s.ctx, token, pos, seen);
+          __syncwarp();
+        }
+        // the tile's largest score in base 2
+        float top = -CUDART_INF_F;
+        uint32_t x[2][32];
+        tc::tmem_load32(scores, x[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          tc::wait_loads();
+          if (i < 3) tc::tmem_load32(scores + 32 * (i + 1), x[(i + 1) & 1]);
+          top = fmaxf(top, largest16<M>(&x[i & 1][0], seen[i]) * f[2 * i]);
+          top = fmaxf(top, largest16<M>(&x[i & 1][16], seen[i] >> 16) * f[2 * i + 1]);
+        }
+        tc::tmem_load32(scores, x[0]);  // the first again, for the weights
+        if (t == 0) {
+          m = top;
+          v_ref = v_top;
+        } else if (__any_sync(0xffffffffu, top > m + 7.0f || v_top > v_ref)) {
+          const float up = fmaxf(m, top);
+          float fix = up == -CUDART_INF_F ? 1.0f : ex2(m - up);
+          l *= fix;
+          m = up;
+          if (v_top > v_ref) {
+            fix *= ex2(v_ref - v_top);
+            v_ref = v_top;
+          }
+          if (!wait(sh.pv_done[(it - 1) & 1], (it - 1) >> 1)) return false;
+#pragma unroll 1
+          for (int i = 0; i < DP / 32; ++i) {
+            uint32_t o[32];
+            tc::tmem_load32(mine + T::kO + 32 * i, o);
+            tc::wait_loads();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
+            tc::tmem_store32(mine + T::kO + 32 * i, o);
+          }
+        }
+        // weights, in the first half of the scores' columns, in units of their values' scales
+        const float base = kLift - (m == -CUDART_INF_F ? 0.0f : m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          tc::wait_loads();
+          if (i < 3) tc::tmem_load32(scores + 32 * (i + 1), x[(i + 1) & 1]);
+          const float u0 = fmaxf(unit[2 * i] - v_ref, -100.0f), u1 = fmaxf(unit[2 * i + 1] - v_ref, -100.0f);
+          uint32_t w[16];
+          const float2 sums = weights32<M>(x[i & 1], seen[i], f[2 * i], f[2 * i + 1], base + u0, base + u1, w);
+          l += sums.x * ex2(-u0) + sums.y * ex2(-u1);
+          tc::tmem_store16(scores + 16 * i, w);
+        }
+        return true;
+      };
+      const bool whole = !lost && s1 < p.steps.steps && last - first == kTokens - kStep && last + kStep <= all &&
+                         (a.window == 0 || far - first < a.window || last + kStep <= a.sinks);
+      if (!(whole ? tile(std::false_type{}) : tile(std::true_type{}))) return false;
+      arrive(sh.p_ready[st]);
+    }
+
+    // the part's result
+    if (!wait(sh.pv_done[(it - 1) & 1], (it - 1) >> 1)) return false;
+    const bool complete = p.count == p.tiles;
+    const float lift = 1.0f / 256.0f;
+    l *= lift;
+    const float scale = ex2(v_ref) * lift;
+    if (complete) {
+      uint16_t* out = static_cast<uint16_t*>(a.out) + out_row * a.out_row_stride + head * a.out_head_stride;
+      const float inv = l == 0.0f ? 0.0f : scale / l;
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) {
+        uint32_t x[32];
+        tc::tmem_load32(mine + T::kO + 32 * i, x);
+        tc::wait_loads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t o[8];
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+            o[n] = floats_to_bf16x2(__uint_as_float(x[16 * k + 2 * n]) * inv, __uint_as_float(x[16 * k + 2 * n + 1]) * inv);
+          const int d = 32 * i + 16 * k;
+          if (r < p.rows && d < a.w.dim) {
+            if (a.out_vec32) {
+              tc::store_32(out + d, o);
+            } else {
+#pragma unroll
+              for (int n = 0; n < 8; ++n) {
+                out[d + 2 * n] = static_cast<uint16_t>(o[n]);
+                out[d + 2 * n + 1] = static_cast<uint16_t>(o[n] >> 16);
+              }
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (r < p.rows && a.lse) a.lse[out_row * a.heads + head] = row_lse(m, l);
+    } else {
+      float* part = a.parts + (2 * static_cast<int64_t>(g) + (p.tile0 == 0 ? 1 : 0)) * T::kPart;
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) {
+        uint32_t x[32];
+        tc::tmem_load32(mine + T::kO + 32 * i, x);
+        tc::wait_loads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[8];
+#pragma unroll
+          for (int n = 0; n < 8; ++n) o[n] = __float_as_uint(__uint_as_float(x[8 * k + n]) * scale);
+          if (r < p.rows) tc::store_32(part + r * DP + 32 * i + 8 * k, o);
+        }
+        __syncwarp();
+      }
+      if (r < p.rows) *reinterpret_cast<float2*>(part + kRows * DP + 2 * r) = make_float2(m, l);
+      if (p.tile0 == 0 && r == 0)
+        a.joins[g] = JoinRecord{s.row0, p.r0, p.rows, c.h, tile_owner(c.at + p.tiles - 1, c.total, c.blocks)};
+    }
+    __syncwarp();
+    next_item<kRows>(a, c, p.count);
+  }
+  return true;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(AttentionParams a) {
+  using T = Tiles<DP>;
+  extern __shared__ uint8_t raw[];
+  __shared__ Shared sh;
+  const uint32_t at = tc::smem_address(raw);
+  uint8_t* tiles = raw + ((at + 1023u & ~1023u) - at);
+  uint8_t* v_tiles = tiles;
+  uint8_t* k_tiles = tiles + T::kStages * T::kTileBytes;
+  const int warp = threadIdx.x >> 5, g = blockIdx.x;
+  flag_sequences(a, g, gridDim.x, kThreads);
+  if (threadIdx.x == 0) {
+    a.joins[g].rows = 0;
+    sh.gave_up = 0;
+    for (int i = 0; i < 2; ++i) {
+      tc::barrier_init(tc::smem_address(&sh.k_full[i]), kLoadWarps);
+      tc::barrier_init(tc::smem_address(&sh.v_full[i]), kLoadWarps);
+      tc::barrier_init(tc::smem_address(&sh.s_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.p_ready[i]), kSoftmaxWarps);
+      tc::barrier_init(tc::smem_address(&sh.pv_done[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) tc::barrier_init(tc::smem_address(&sh.info_full[i]), 1);
+    tc::barrier_init(tc::smem_address(&sh.q_ready), kSoftmaxWarps);
+    tc::barrier_init(tc::smem_address(&sh.last), 1);
+    tc::publish_shared();
+  }
+  if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), T::kColumns);
+  const Cursor c = find_cursor<kThreads, kRows, kTileSteps>(a, g, gridDim.x, sh.cursor);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sh.tmem;
+  bool ok = true;
+  if (warp < kSoftmaxWarps) {
+    tc::registers_up<kSoftmaxRegisters>();
+    ok = softmax_role<DP>(a, c, sh, tmem, g);
+  } else if (warp < kSoftmaxWarps + kLoadWarps) {
+    tc::registers_down<kLoadRegisters>();
+    ok = load_role<DP>(a, c, sh, k_tiles, v_tiles);
+  } else {
+    tc::registers_down<kProductRegisters>();
+    if (threadIdx.x == 32 * (kSoftmaxWarps + kLoadWarps)) {
+    ok = product_role<DP>(a, c, sh, tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
+    // products in flight end before the memory that they use is given up
+    int unused = 0;
+    tc::products_arrive(tc::smem_address(&sh.last));
+    ok = tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused) && ok;
+    }
+  }
+  if (!ok && (threadIdx.x & 31) == 0) kv_flag(a.w, min(c.b, a.w.batch - 1), SV_ROW_TIMEOUT);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 0) tc::tmem_free(tmem, T::kColumns);
+}
+
+template <int DP>
+sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspace, cudaStream_t stream) {
+  using T = Tiles<DP>;
+  static FuncAttrCache attr;
+  const auto kernel = kv_attention_tiles_kernel<DP>;
+  if (!attr.ensure(reinterpret_cast<const void*>(kernel), T::kShared, false)) return SV_ERR_CUDA;
+  const int64_t row_tiles = (static_cast<int64_t>(d.max_new) * a.group + kRows - 1) / kRows;
+  const int64_t tiles = (static_cast<int64_t>(d.kv.max_pages) * d.kv.page_size + kTokens - 1) / kTokens;
+  const int blocks = schedule_blocks(row_tiles * d.kv.batch * d.kv.kv_heads, tiles, kSMs);
+  a.parts = static_cast<float*>(workspace);
+  a.joins = reinterpret_cast<JoinRecord*>(a.parts + 2 * static_cast<int64_t>(kSMs) * T::kPart);
+  kernel<<<blocks, kThreads, T::kShared, stream>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  note_launch(stream);
+  if (blocks == 1 || tiles == 1) return SV_OK;  // no item has parts
+  if (launch_join<uint16_t, DP, kRows>(a, blocks, stream) != cudaSuccess) return SV_ERR_CUDA;
+  note_launch(stream);
+  return SV_OK;
+}
+
+}  // namespace
+
+bool kv_attention_takes_tiles(const sv_kv_attention_desc& d) {
+  return d.dtype == SV_BF16 && d.kv.head_dim <= 128 &&
+         static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 16;
+}
+
+size_t kv_attention_tiles_workspace(const sv_kv_attention_desc& d) {
+  const size_t part = d.kv.head_dim <= 64 ? Tiles<64>::kPart : Tiles<128>::kPart;
+  return align_up(kSMs * (2 * part * sizeof(float) + sizeof(JoinRecord)), 256);
+}
+
+sv_status kv_attention_tiles(AttentionParams a, const sv_kv_attention_desc& d, void* workspace, cudaStream_t stream) {
+  return d.kv.head_dim <= 64 ? launch<64>(a, d, workspace, stream) : launch<128>(a, d, workspace, stream);
+}
+
+}  // namespace sv

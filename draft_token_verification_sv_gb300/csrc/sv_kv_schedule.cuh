@@ -33,6 +33,7 @@ struct AttentionParams {
   int heads, group, window, sinks;
   float scale_log2;  // scale * log2(e)
   bool q_vec, out_vec;  // rows on 16-byte boundaries
+  bool out_vec32;       // and on 32-byte ones
   float* parts;         // [2 G][rows][DP + 2] fp32: values, then (maximum, sum) pairs of all rows
   struct JoinRecord* joins;  // [G]
 };
@@ -233,6 +234,37 @@ __device__ __forceinline__ bool sees(const AttentionParams& a, const int32_t* pa
   return a.window == 0 || pos - at < a.window || at < a.sinks;
 }
 
+template <typename E>
+__device__ __forceinline__ void store4(E* out, float4 v, bool vec) {
+  if constexpr (sizeof(E) == 2) {
+    const uint32_t lo = floats_to_bf16x2(v.x, v.y), hi = floats_to_bf16x2(v.z, v.w);
+    if (vec) {
+      *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+    } else {
+      uint16_t* p = reinterpret_cast<uint16_t*>(out);
+      p[0] = static_cast<uint16_t>(lo);
+      p[1] = static_cast<uint16_t>(lo >> 16);
+      p[2] = static_cast<uint16_t>(hi);
+      p[3] = static_cast<uint16_t>(hi >> 16);
+    }
+  } else {
+    float* p = reinterpret_cast<float*>(out);
+    if (vec) {
+      *reinterpret_cast<float4*>(p) = v;
+    } else {
+      p[0] = v.x;
+      p[1] = v.y;
+      p[2] = v.z;
+      p[3] = v.w;
+    }
+  }
+}
+
+// log-sum-exp of a row from its maximum (base 2) and sum of weights
+__device__ __forceinline__ float row_lse(float top, float total) {
+  return total == 0.0f ? -CUDART_INF_F : (top + log2f(total)) * kLn2;
+}
+
 // Four values of a row's result from its weighted sum, maximum (base 2) and
 // sum of weights, and with the first of them the log-sum-exp.
 template <typename E>
@@ -243,33 +275,63 @@ __device__ __forceinline__ void store_result(const AttentionParams& a, int row0,
   const int head = kv_head * a.group + r % a.group;
   E* out = static_cast<E*>(a.out) + row * a.out_row_stride + head * a.out_head_stride + d;
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  sum.x *= inv;
-  sum.y *= inv;
-  sum.z *= inv;
-  sum.w *= inv;
-  if constexpr (sizeof(E) == 2) {
-    const uint32_t u = floats_to_bf16x2(sum.x, sum.y), v = floats_to_bf16x2(sum.z, sum.w);
-    if (a.out_vec) {
-      *reinterpret_cast<uint2*>(out) = make_uint2(u, v);
-    } else {
-      uint16_t* p = reinterpret_cast<uint16_t*>(out);
-      p[0] = static_cast<uint16_t>(u);
-      p[1] = static_cast<uint16_t>(u >> 16);
-      p[2] = static_cast<uint16_t>(v);
-      p[3] = static_cast<uint16_t>(v >> 16);
-    }
-  } else {
-    float* p = reinterpret_cast<float*>(out);
-    if (a.out_vec) {
-      *reinterpret_cast<float4*>(p) = sum;
-    } else {
-      p[0] = sum.x;
-      p[1] = sum.y;
-      p[2] = sum.z;
-      p[3] = sum.w;
-    }
-  }
-  if (d == 0 && a.lse) a.lse[row * a.heads + head] = total == 0.0f ? -CUDART_INF_F : (top + log2f(total)) * kLn2;
+  store4<E>(out, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv), a.out_vec);
+  if (d == 0 && a.lse) a.lse[row * a.heads + head] = row_lse(top, total);
 }
+
+// One block for each part that began an item: its rows from all parts, in order.
+template <typename E, int DP, int ROWS>
+__global__ void __launch_bounds__(128) kv_attention_join_kernel(AttentionParams a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  const int g = blockIdx.x;
+  const JoinRecord j = a.joins[g];
+  constexpr int kPart = ROWS * (DP + 2);
+  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < j.rows * (DP / 4); i += blockDim.x * gridDim.y) {
+    const int r = i / (DP / 4), d4 = i % (DP / 4);
+    const auto part = [&](int k) { return a.parts + (2 * static_cast<int64_t>(k) + (k == g ? 1 : 0)) * kPart; };
+    float top = -CUDART_INF_F;
+    for (int k = g; k <= j.last; ++k) top = fmaxf(top, part(k)[ROWS * DP + 2 * r]);
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float total = 0.0f;
+#pragma unroll 4
+    for (int k = g; k <= j.last; ++k) {
+      const float2 ml = *reinterpret_cast<const float2*>(part(k) + ROWS * DP + 2 * r);
+      const float4 v = *reinterpret_cast<const float4*>(part(k) + r * DP + 4 * d4);
+      // a part that saw nothing has sums of 0 (or NaN, which stays)
+      const float fix = ml.x == -CUDART_INF_F ? 1.0f : ex2(ml.x - top);
+      total += ml.y * fix;
+      sum.x += v.x * fix;
+      sum.y += v.y * fix;
+      sum.z += v.z * fix;
+      sum.w += v.w * fix;
+    }
+    store_result<E>(a, j.row0, j.r0 + r, j.kv_head, 4 * d4, sum, top, total);
+  }
+}
+
+// The second launch, which may begin its own start before the first ends.
+template <typename E, int DP, int ROWS>
+cudaError_t launch_join(const AttentionParams& a, int blocks, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, ROWS / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<E, DP, ROWS>, a);
+}
+
+// Blocks for a call that can have at most so many items of so many tiles.
+inline int schedule_blocks(int64_t items, int64_t tiles, int most) {
+  return items >= most || tiles >= most || items * tiles >= most ? most : static_cast<int>(items * tiles);
+}
+
+// Attention for many rows of a kv head (sv_kv_attention_tiles.cu).
+bool kv_attention_takes_tiles(const sv_kv_attention_desc& d);
+size_t kv_attention_tiles_workspace(const sv_kv_attention_desc& d);
+sv_status kv_attention_tiles(AttentionParams a, const sv_kv_attention_desc& d, void* workspace, cudaStream_t stream);
 
 }  // namespace sv
