@@ -5,9 +5,10 @@
 // tensor cores: S = Q K^T and O += P V, accumulators in tensor memory.  The
 // left sides (Q, and the weights P, which take the place of the scores they
 // come from) are in tensor memory too, so that only K and V are read from
-// shared memory.  One block per SM, three roles:
+// shared memory.  One block per SM, four roles:
+//   1 warp plans: it walks the block's tiles and looks pages and scales up;
 //   8 warps load codes, widen them to fp16 (which holds every e4m3 value) and
-//     lay them out for the products, a tile ahead in registers and two in
+//     lay them out for the products, two tiles ahead in registers and two in
 //     shared memory;
 //   1 thread issues the products: S of tile t before P V of tile t - 1;
 //   4 warps turn scores into weights, a row a thread, with a running maximum
@@ -25,11 +26,11 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kTileSteps = 8;
 constexpr int kTokens = kStep * kTileSteps;
-// warps 0-3, 4-11 and 12 (13-15 idle: registers move in fours of warps)
+// weights: warps 0-3; loads: 4-11; products: 12; plan: 13 (14, 15 idle: registers move in fours of warps)
 constexpr int kSoftmaxWarps = 4, kLoadWarps = 8;
 constexpr int kLoadThreads = 32 * kLoadWarps;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kLoadWarps + 4);
-constexpr int kSoftmaxRegisters = 248, kLoadRegisters = 112, kProductRegisters = 32;
+constexpr int kSoftmaxRegisters = 216, kLoadRegisters = 112, kProductRegisters = 72;
 static_assert(4 * kSoftmaxRegisters + 8 * kLoadRegisters + 4 * kProductRegisters <= 16 * 128, "registers of a block");
 constexpr float kLift = 8.0f;  // weights are 2^8 times what they stand for: fp16 then keeps 2^-22 of the largest
 
@@ -46,18 +47,35 @@ template <int DP> struct Tiles {
   static constexpr int kPart = kRows * (DP + 2);
 };
 
-struct TileInfo {  // of a tile's eight steps
+constexpr int kPlans = 8;  // tiles that may be planned ahead
+constexpr int kParts = 4;  // parts of items that may be
+constexpr float kNoScale = -1000.0f;
+
+// What the roles need of a tile.
+struct TilePlan {
+  int64_t base[kTileSteps];   // of each step's codes, or -1
+  int token[kTileSteps];      // its first token
+  int count[kTileSteps];      // tokens in sight
   float k_scale[kTileSteps];
-  float v_log2[kTileSteps];  // log2 of the values' scale, kNoScale for none
-  int lost;                  // bits of steps whose page is not there
+  float v_log2[kTileSteps];   // log2 of the values' scale, kNoScale for none
+  int whole;                  // every row sees every token
+  int first, last;            // of its part
 };
 
-constexpr float kNoScale = -1000.0f;
+// And of an item's part that the block works on.
+struct Part {
+  int b, h, ctx, row0;
+  int r0, rows, i0, i1;       // rows of the item, their new tokens
+  int tile0, count, tiles;    // first and number of the block's tiles, all of the item
+  int join_last;              // the last block with a part of the item
+};
 
 struct Shared {
   CursorScratch cursor;
-  uint64_t k_full[2], v_full[2], s_full[2], p_ready[2], pv_done[2], info_full[4], q_ready, last;
-  TileInfo info[4];
+  uint64_t plan_full[kPlans], plan_free[kPlans], part_full[kParts], part_free[kParts];
+  uint64_t k_full[2], v_full[2], s_full[2], p_ready[2], pv_done[2], q_ready, last;
+  TilePlan plan[kPlans];
+  Part part[kParts];
   uint32_t tmem;
   int gave_up;
 };
@@ -79,90 +97,111 @@ __device__ __forceinline__ uint32_t bits16(int base, int from, int to) {
   return ((1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
-// The part of an item that a block works on.
-struct Part {
-  ItemSteps steps;
-  int r0, rows, i0, i1;
-  int tiles, tile0, count;  // the item's tiles; first and number of the block's
-};
+// Every lane waits (for the n-th phase of a barrier); the answer is the warp's.
+__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, long long n) {
+  return __all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t& bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::barrier_arrive(tc::smem_address(&bar));
+}
 
-__device__ __forceinline__ Part part_of(const AttentionParams& a, const Cursor& c) {
-  Part p;
-  p.r0 = c.rt * kRows;
-  p.rows = min(kRows, c.span.n * a.group - p.r0);
-  p.i0 = p.r0 / a.group;
-  p.i1 = (p.r0 + p.rows - 1) / a.group;
-  p.steps = item_steps(a, c.span, p.i0, p.i1);
-  p.tiles = max(1, (p.steps.steps + kTileSteps - 1) / kTileSteps);
-  p.tile0 = c.tile;
-  p.count = static_cast<int>(min(static_cast<long long>(p.tiles - c.tile), c.end - c.at));
-  return p;
+// ---- plans ----
+
+// Four tiles at a time, a lane to a step: page ids, then scales.
+__device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
+  const KvView& w = a.w;
+  const int lane = threadIdx.x & 31, mine = lane / kTileSteps, step = lane % kTileSteps;
+  const int page_mask = (1 << w.page_shift) - 1;
+  long long it = 0;
+  for (long long item = 0; c.at < c.end; ++item) {
+    Part p;
+    p.b = c.b;
+    p.h = c.h;
+    p.ctx = c.span.ctx;
+    p.row0 = c.span.row0;
+    p.r0 = c.rt * kRows;
+    p.rows = min(kRows, c.span.n * a.group - p.r0);
+    p.i0 = p.r0 / a.group;
+    p.i1 = (p.r0 + p.rows - 1) / a.group;
+    const ItemSteps steps = item_steps(a, c.span, p.i0, p.i1);
+    p.tiles = max(1, (steps.steps + kTileSteps - 1) / kTileSteps);
+    p.tile0 = c.tile;
+    p.count = static_cast<int>(min(static_cast<long long>(p.tiles - c.tile), c.end - c.at));
+    p.join_last = p.tile0 == 0 && p.count < p.tiles ? tile_owner(c.at + p.tiles - 1, c.total, c.blocks) : 0;
+    if (item >= kParts && !warp_wait(sh, sh.part_free[item % kParts], item / kParts - 1)) return false;
+    if (lane == 0) sh.part[item % kParts] = p;
+    warp_arrive(sh.part_full[item % kParts]);
+    // tokens before `all` are in every row's past; `far` is the furthest position of a row
+    const int all = a.parents ? p.ctx : p.ctx + p.i0 + 1, far = p.ctx + p.i1;
+    for (int t0 = 0; t0 < p.count; t0 += 32 / kTileSteps) {
+      const int s = (p.tile0 + t0 + mine) * kTileSteps + step;
+      const bool live = t0 + mine < p.count && s < steps.steps;
+      const int token = steps.token(s);
+      int page = -1;
+      if (live && sv_in(token >> w.page_shift, w.max_pages)) page = __ldg(w.c.page_table + p.b * w.table_stride + (token >> w.page_shift));
+      const bool there = live && page >= 0 && page < w.num_pages;
+      if (live && !there) kv_flag(w, p.b, SV_ROW_BAD_PAGE);
+      float k_scale = 0.0f, v_scale = 0.0f;
+      if (there) {
+        k_scale = __ldg(w.c.k_scale + static_cast<int64_t>(page) * w.kv_heads + p.h);
+        v_scale = __ldg(w.c.v_scale + static_cast<int64_t>(page) * w.kv_heads + p.h);
+      }
+      const bool full = there && token + kStep <= all &&
+                        (a.window == 0 || far - token < a.window || token + kStep <= a.sinks);
+      const unsigned fulls = __ballot_sync(0xffffffffu, full) >> (mine * kTileSteps) & 0xffu;
+      const uint32_t bits = __float_as_uint(v_scale);
+      const float v_log2 = !(v_scale > 0.0f) ? kNoScale
+                           : (bits & 0x7fffffu) == 0 && bits >= 0x00800000u ? static_cast<float>(static_cast<int>(bits >> 23) - 127)
+                                                                            : log2f(v_scale);
+      for (int i = 0; i < 32 / kTileSteps && t0 + i < p.count; ++i, ++it) {
+        TilePlan& plan = sh.plan[it % kPlans];
+        if (it >= kPlans && !warp_wait(sh, sh.plan_free[it % kPlans], it / kPlans - 1)) return false;
+        if (mine == i) {
+          plan.base[step] = there ? kv_offset(w, page, p.h, token & page_mask) : -1;
+          plan.token[step] = token;
+          plan.count[step] = there ? min(kStep, steps.end - token) : 0;
+          plan.k_scale[step] = k_scale;
+          plan.v_log2[step] = v_log2;
+          if (step == 0) {
+            plan.whole = fulls == 0xffu;
+            plan.first = t0 + i == 0;
+            plan.last = t0 + i + 1 == p.count;
+          }
+        }
+        warp_arrive(sh.plan_full[it % kPlans]);
+      }
+    }
+    next_item<kRows>(a, c, p.count);
+  }
+  return true;
 }
 
 // ---- loading ----
 
-// A step of a tile that is yet to be loaded (lanes 0-7 of every loading warp).
-struct StepAhead {
-  int page, slot, count;  // count: its tokens in sight, 0 for none
-  int b, h;
-};
-
 template <int DP>
-__device__ bool load_role(const AttentionParams& a, Cursor c, Shared& sh, uint8_t* k_tiles, uint8_t* v_tiles) {
+__device__ bool load_role(const AttentionParams& a, const long long tiles, Shared& sh, uint8_t* k_tiles, uint8_t* v_tiles) {
   using T = Tiles<DP>;
   constexpr int kChunks = DP / 16;                        // of a token
   constexpr int kPer = kLoadThreads / kChunks;            // tokens of a pass
   constexpr int NI = kTokens / kPer;                      // passes
   const KvView& w = a.w;
-  const int tid = threadIdx.x - 32 * kSoftmaxWarps, lane = tid & 31;
+  const int tid = threadIdx.x - 32 * kSoftmaxWarps;
   const int t0 = tid / kChunks, ch = tid % kChunks;
   const bool in_dim = ch * 16 < w.dim;
-  const int page_mask = (1 << w.page_shift) - 1;
-  if (c.at >= c.end) return true;
-  const long long tiles = c.end - c.at;
-  Part p = part_of(a, c);
-  int next = 0;  // of the part's tiles, the one to look up
-
-  // Page ids are looked up a tile before the codes are asked for.
-  StepAhead ahead{0, 0, 0, 0, 0};
-  const auto look_up = [&]() {
-    const int s = (p.tile0 + next) * kTileSteps + (lane & 7);
-    ahead.count = 0;
-    if (s < p.steps.steps) {
-      const int j = p.steps.token(s);
-      ahead.count = min(kStep, p.steps.end - j);
-      ahead.slot = j & page_mask;
-      ahead.page = sv_in(j >> w.page_shift, w.max_pages) ? __ldg(w.c.page_table + c.b * w.table_stride + (j >> w.page_shift)) : -1;
-    }
-    ahead.b = c.b;
-    ahead.h = c.h;
-    if (++next == p.count) {
-      next_item<kRows>(a, c, p.count);
-      next = 0;
-      if (c.at < c.end) p = part_of(a, c);
-    }
-  };
-  int64_t chunk[NI];  // of the tile that is asked for next; -1: zeros
-  int64_t scale = -1;
-  bool lost = false;
-  const auto resolve = [&]() {
-    const bool there = ahead.count > 0 && ahead.page >= 0 && ahead.page < w.num_pages;
-    lost = ahead.count > 0 && !there;
-    if (lost) kv_flag(w, ahead.b, SV_ROW_BAD_PAGE);
-    const int64_t base = there ? kv_offset(w, ahead.page, ahead.h, ahead.slot) : -1;
-    scale = there ? static_cast<int64_t>(ahead.page) * w.kv_heads + ahead.h : -1;
+  const int64_t within = (t0 % kStep) * w.token_stride + ch * 16;  // kPer is a multiple of a step
+  int64_t chunk[NI];  // offsets of the tile that is asked for; -1: zeros
+  const auto look = [&](long long it) {
+    const TilePlan& plan = sh.plan[it % kPlans];
+    if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans)) return false;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int t = t0 + i * kPer;
-      const int64_t from = __shfl_sync(0xffffffffu, base, t / kStep);
-      const int count = __shfl_sync(0xffffffffu, ahead.count, t / kStep);
-      chunk[i] = from >= 0 && t % kStep < count && in_dim ? from + (t % kStep) * w.token_stride + ch * 16 : -1;
+      const int s = (t0 + i * kPer) / kStep;
+      chunk[i] = t0 % kStep < plan.count[s] && in_dim ? plan.base[s] + within : -1;
     }
+    warp_arrive(sh.plan_free[it % kPlans]);
+    return true;
   };
-  // two tiles in flight in registers
-  uint4 k[2][NI], v[2][NI];
-  float k_scale[2], v_scale[2];
-  unsigned gone[2];
   const auto load = [&](uint4 (&x)[NI], const uint8_t* from) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -170,74 +209,46 @@ __device__ bool load_role(const AttentionParams& a, Cursor c, Shared& sh, uint8_
       if (chunk[i] >= 0) x[i] = ldg_stream(from + chunk[i]);
     }
   };
-  const auto load_scales = [&](int buffer) {
-    k_scale[buffer] = v_scale[buffer] = 0.0f;
-    if (tid < kTileSteps && scale >= 0) {
-      k_scale[buffer] = __ldg(w.c.k_scale + scale);
-      v_scale[buffer] = __ldg(w.c.v_scale + scale);
-    }
-    gone[buffer] = __ballot_sync(0xffffffffu, lost) & 0xffu;
-  };
-  look_up();
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (i < tiles) {
-      resolve();
-      load(k[i], w.c.k);
-      load_scales(i);
-      load(v[i], w.c.v);
-      if (i + 1 < tiles) look_up();
-    }
-  // both kinds lie alike: rows of 64 dims, swizzled
+  // where a chunk's two halves go: both kinds lie alike, rows of 64 dims, swizzled; lanes of the
+  // second block of dims write their halves the other way round (other banks)
+  const int turn = ch >> 2 & 1;
+  const int to = (ch >> 2) * T::kBlockBytes + t0 * 128;
+  const int half0 = (2 * (ch & 3) + turn) ^ (t0 & 7), half1 = (2 * (ch & 3) + 1 - turn) ^ (t0 & 7);  // kPer is a multiple of 8
   const auto put = [&](uint8_t* tile, const uint4 (&x)[NI]) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int t = t0 + i * kPer;
-      uint4 half[2];
-      widen(x[i], half[0], half[1]);
-      uint8_t* row = tile + (ch >> 2) * T::kBlockBytes + t * 128;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int turn = h ^ (ch >> 2 & 1);  // the two blocks' lanes write different banks
-        *reinterpret_cast<uint4*>(row + (((2 * (ch & 3) + turn) ^ (t & 7)) << 4)) = turn ? half[1] : half[0];
-      }
+      uint4 lo, hi;
+      widen(x[i], lo, hi);
+      uint8_t* row = tile + to + i * kPer * 128;
+      *reinterpret_cast<uint4*>(row + (half0 << 4)) = turn ? hi : lo;
+      *reinterpret_cast<uint4*>(row + (half1 << 4)) = turn ? lo : hi;
     }
     tc::publish_shared();
   };
+  uint4 k[2][NI], v[2][NI];  // two tiles in flight
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (i < tiles) {
+      if (!look(i)) return false;
+      load(k[i], w.c.k);
+      load(v[i], w.c.v);
+    }
   for (long long it0 = 0; it0 < tiles; it0 += 2) {
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       const long long it = it0 + st;
       if (it >= tiles) break;
-      const uint32_t before = static_cast<uint32_t>((it >> 1) & 1) ^ 1u;  // parity of the stage's last use
-      if (it >= 2 && !__all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&sh.s_full[st]), before, &sh.gave_up))) return false;
+      if (it >= 2 && !warp_wait(sh, sh.s_full[st], (it >> 1) - 1)) return false;
       put(k_tiles + st * T::kTileBytes, k[st]);
-      // four slots: softmax has read tile it - 4 before S of tile it - 2 was issued
-      TileInfo& info = sh.info[it & 3];
-      if (tid < kTileSteps) {
-        const uint32_t bits = __float_as_uint(v_scale[st]);
-        info.k_scale[tid] = k_scale[st];
-        info.v_log2[tid] = v_scale[st] > 0.0f ? ((bits & 0x7fffffu) == 0 && bits >= 0x00800000u
-                                                     ? static_cast<float>(static_cast<int>(bits >> 23) - 127) : log2f(v_scale[st]))
-                                              : kNoScale;
-        if (tid == 0) info.lost = static_cast<int>(gone[st]);
-      }
-      __syncwarp();
-      if (lane == 0) tc::barrier_arrive(tc::smem_address(&sh.k_full[st]));
-      if (tid == 0) tc::barrier_arrive(tc::smem_address(&sh.info_full[it & 3]));
+      warp_arrive(sh.k_full[st]);
       if (it + 2 < tiles) {
-        resolve();
+        if (!look(it + 2)) return false;
         load(k[st], w.c.k);
-        load_scales(st);
       }
-      if (it >= 2 && !__all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&sh.pv_done[st]), before, &sh.gave_up))) return false;
+      if (it >= 2 && !warp_wait(sh, sh.pv_done[st], (it >> 1) - 1)) return false;
       put(v_tiles + st * T::kTileBytes, v[st]);
-      __syncwarp();
-      if (lane == 0) tc::barrier_arrive(tc::smem_address(&sh.v_full[st]));
-      if (it + 2 < tiles) {
-        load(v[st], w.c.v);
-        if (it + 3 < tiles) look_up();
-      }
+      warp_arrive(sh.v_full[st]);
+      if (it + 2 < tiles) load(v[st], w.c.v);
     }
   }
   return true;
@@ -246,7 +257,7 @@ __device__ bool load_role(const AttentionParams& a, Cursor c, Shared& sh, uint8_
 // ---- products ----
 
 template <int DP>
-__device__ bool product_role(const AttentionParams& a, Cursor c, Shared& sh, uint32_t k_tiles, uint32_t v_tiles, uint32_t tmem) {
+__device__ bool product_role(const long long tiles, Shared& sh, uint32_t k_tiles, uint32_t v_tiles, uint32_t tmem) {
   using T = Tiles<DP>;
   constexpr uint32_t kScores = tc::product_f16(kTokens, false), kValues = tc::product_f16(DP, true);
   const auto wait = [&](uint64_t& bar, long long n) {
@@ -264,22 +275,23 @@ __device__ bool product_role(const AttentionParams& a, Cursor c, Shared& sh, uin
     tc::products_arrive(tc::smem_address(&sh.pv_done[st]));
     return true;
   };
-  long long it = 0;
-  for (long long item = 0; c.at < c.end; ++item) {
-    const Part p = part_of(a, c);
-    if (!wait(sh.q_ready, item)) return false;
-    for (int t = 0; t < p.count; ++t, ++it) {
-      const int st = it & 1;
-      if (!wait(sh.k_full[st], it >> 1)) return false;
+  bool first_before = false;  // the last tile was its part's first
+  long long item = 0;
+  for (long long it = 0; it < tiles; ++it) {
+    const int st = it & 1;
+    if (!wait(sh.plan_full[it % kPlans], it / kPlans)) return false;
+    const bool first = sh.plan[it % kPlans].first, last = sh.plan[it % kPlans].last;
+    tc::barrier_arrive(tc::smem_address(&sh.plan_free[it % kPlans]));
+    if (first && !wait(sh.q_ready, item++)) return false;
+    if (!wait(sh.k_full[st], it >> 1)) return false;
 #pragma unroll
-      for (int k = 0; k < DP / 16; ++k)
-        tc::product(tmem + T::kS + st * kTokens, tmem + T::kQ + k * 8,
-                    tc::tile_descriptor(k_tiles + st * T::kTileBytes + (k >> 2) * T::kBlockBytes + (k & 3) * 32, 16, 1024), kScores, k > 0);
-      tc::products_arrive(tc::smem_address(&sh.s_full[st]));
-      if (t > 0 && !weigh(it - 1, t == 1)) return false;
-    }
-    if (!weigh(it - 1, p.count == 1)) return false;
-    next_item<kRows>(a, c, p.count);
+    for (int k = 0; k < DP / 16; ++k)
+      tc::product(tmem + T::kS + st * kTokens, tmem + T::kQ + k * 8,
+                  tc::tile_descriptor(k_tiles + st * T::kTileBytes + (k >> 2) * T::kBlockBytes + (k & 3) * 32, 16, 1024), kScores, k > 0);
+    tc::products_arrive(tc::smem_address(&sh.s_full[st]));
+    if (!first && !weigh(it - 1, first_before)) return false;
+    if (last && !weigh(it, first)) return false;
+    first_before = first;
   }
   return true;
 }
@@ -287,15 +299,15 @@ __device__ bool product_role(const AttentionParams& a, Cursor c, Shared& sh, uin
 // ---- scores to weights, and results ----
 
 // Which of a tile's tokens the thread's row sees, 32 to a word.
-__device__ __forceinline__ void seen_tokens(const AttentionParams& a, const ItemSteps& steps, int s0, int lost, const int32_t* parents,
-                                            int ctx, int token, int pos, uint32_t (&seen)[4]) {
-  const int past = parents ? ctx : min(pos + 1, steps.end);
+__device__ __forceinline__ void seen_tokens(const AttentionParams& a, const TilePlan& plan, const int32_t* parents, int ctx, int token,
+                                            int pos, uint32_t (&seen)[4]) {
+  const int past = parents ? ctx : pos + 1;
   const int from = a.window ? max(0, pos - a.window + 1) : 0;
 #pragma unroll
   for (int i = 0; i < kTileSteps; ++i) {
     uint32_t b = 0;
-    if (s0 + i < steps.steps && !(lost >> i & 1)) {
-      const int base = steps.token(s0 + i);
+    if (plan.count[i] > 0) {
+      const int base = plan.token[i];
       b = bits16(base, from, past);
       if (a.window) b |= bits16(base, 0, min(a.sinks, past));
       if (parents && base + kStep > ctx)
@@ -352,29 +364,29 @@ __device__ __forceinline__ float2 weights32(const uint32_t (&x)[32], uint32_t se
 }
 
 template <int DP>
-__device__ bool softmax_role(const AttentionParams& a, Cursor c, Shared& sh, uint32_t tmem, int g) {
+__device__ bool softmax_role(const AttentionParams& a, const long long tiles, Shared& sh, uint32_t tmem, int g) {
   using T = Tiles<DP>;
-  const int lane = threadIdx.x & 31, r = threadIdx.x;
+  const int r = threadIdx.x;
   const uint32_t mine = tmem + ((threadIdx.x >> 5) << 21);  // the warp's 32 lanes
   const auto wait = [&](uint64_t& bar, long long n) {
-    const bool ok = __all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up));
+    const bool ok = warp_wait(sh, bar, n);
     tc::fence_after();
     return ok;
   };
   const auto arrive = [&](uint64_t& bar) {
     tc::wait_stores();
     tc::fence_before();
-    __syncwarp();
-    if (lane == 0) tc::barrier_arrive(tc::smem_address(&bar));
+    warp_arrive(bar);
   };
   long long it = 0;
-  while (c.at < c.end) {
-    const Part p = part_of(a, c);
-    const KvSpan s = c.span;
-    const int32_t* parents = a.parents ? a.parents + s.row0 : nullptr;
+  for (long long item = 0; it < tiles; ++item) {
+    if (!wait(sh.part_full[item % kParts], item / kParts)) return false;
+    const Part p = sh.part[item % kParts];
+    warp_arrive(sh.part_free[item % kParts]);
+    const int32_t* parents = a.parents ? a.parents + p.row0 : nullptr;
     const int row = p.r0 + min(r, p.rows - 1);
-    const int token = row / a.group, head = c.h * a.group + row % a.group;
-    const int64_t out_row = static_cast<int64_t>(s.row0) + token;
+    const int token = row / a.group, head = p.h * a.group + row % a.group;
+    const int64_t out_row = static_cast<int64_t>(p.row0) + token;
 
     // the row's queries, scaled by a power of two into fp16's range (exact for bf16 down to 2^-28 of the largest)
     float factor;
@@ -417,39 +429,33 @@ __device__ bool softmax_role(const AttentionParams& a, Cursor c, Shared& sh, uin
       }
       arrive(sh.q_ready);
     }
-    int pos = s.ctx + token;
+    int pos = p.ctx + token;
     if (parents) {
       int depth = 0;
       for (int u = tree_parent(parents, token); u >= 0; u = tree_parent(parents, u)) ++depth;
-      pos = s.ctx + depth;
+      pos = p.ctx + depth;
       __syncwarp();
     }
-    // tokens before `all` are in every row's past; `far` is the furthest position of a row
-    const int all = parents ? s.ctx : s.ctx + p.i0 + 1, far = s.ctx + p.i1;
 
     float m = -CUDART_INF_F, l = 0.0f, v_ref = kNoScale;  // v_ref: log2 of the values' unit
     for (int t = 0; t < p.count; ++t, ++it) {
       const int st = it & 1;
-      // (not k_full: the loaders may be a phase past it)
-      if (!wait(sh.info_full[it & 3], it >> 2) || !wait(sh.s_full[st], it >> 1)) return false;
-      const TileInfo& info = sh.info[it & 3];
+      const TilePlan& plan = sh.plan[it % kPlans];
+      if (!wait(sh.plan_full[it % kPlans], it / kPlans) || !wait(sh.s_full[st], it >> 1)) return false;
       const uint32_t scores = mine + T::kS + st * kTokens;
-      const int s0 = (p.tile0 + t) * kTileSteps, s1 = s0 + kTileSteps - 1;
-      const int first = p.steps.token(s0), last = p.steps.token(s1);
-      const int lost = info.lost;
       float f[kTileSteps], unit[kTileSteps];
       float v_top = kNoScale;
 #pragma unroll
       for (int i = 0; i < kTileSteps; ++i) {
-        f[i] = factor * info.k_scale[i];
-        unit[i] = info.v_log2[i];
+        f[i] = factor * plan.k_scale[i];
+        unit[i] = plan.v_log2[i];
         v_top = fmaxf(v_top, unit[i]);
       }
       const auto tile = [&](auto masked) {
         constexpr bool M = decltype(masked)::value;
         uint32_t seen[4] = {};
         if (M) {
-          seen_tokens(a, p.steps, s0, lost, parents, s.ctx, token, pos, seen);
+          seen_tokens(a, plan, parents, p.ctx, token, pos, seen);
           __syncwarp();
         }
         // the tile's largest score in base 2
@@ -501,10 +507,9 @@ __device__ bool softmax_role(const AttentionParams& a, Cursor c, Shared& sh, uin
         }
         return true;
       };
-      const bool whole = !lost && s1 < p.steps.steps && last - first == kTokens - kStep && last + kStep <= all &&
-                         (a.window == 0 || far - first < a.window || last + kStep <= a.sinks);
-      if (!(whole ? tile(std::false_type{}) : tile(std::true_type{}))) return false;
+      if (!(plan.whole ? tile(std::false_type{}) : tile(std::true_type{}))) return false;
       arrive(sh.p_ready[st]);
+      warp_arrive(sh.plan_free[it % kPlans]);
     }
 
     // the part's result
@@ -561,10 +566,9 @@ __device__ bool softmax_role(const AttentionParams& a, Cursor c, Shared& sh, uin
       }
       if (r < p.rows) *reinterpret_cast<float2*>(part + kRows * DP + 2 * r) = make_float2(m, l);
       if (p.tile0 == 0 && r == 0)
-        a.joins[g] = JoinRecord{s.row0, p.r0, p.rows, c.h, tile_owner(c.at + p.tiles - 1, c.total, c.blocks)};
+        a.joins[g] = JoinRecord{p.row0, p.r0, p.rows, p.h, p.join_last};
     }
     __syncwarp();
-    next_item<kRows>(a, c, p.count);
   }
   return true;
 }
@@ -590,7 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
       tc::barrier_init(tc::smem_address(&sh.p_ready[i]), kSoftmaxWarps);
       tc::barrier_init(tc::smem_address(&sh.pv_done[i]), 1);
     }
-    for (int i = 0; i < 4; ++i) tc::barrier_init(tc::smem_address(&sh.info_full[i]), 1);
+    for (int i = 0; i < kPlans; ++i) {
+      tc::barrier_init(tc::smem_address(&sh.plan_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.plan_free[i]), kLoadWarps + kSoftmaxWarps + 1);
+    }
+    for (int i = 0; i < kParts; ++i) {
+      tc::barrier_init(tc::smem_address(&sh.part_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.part_free[i]), kSoftmaxWarps);
+    }
     tc::barrier_init(tc::smem_address(&sh.q_ready), kSoftmaxWarps);
     tc::barrier_init(tc::smem_address(&sh.last), 1);
     tc::publish_shared();
@@ -601,21 +612,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
+  const long long tiles_here = c.end - c.at;
   bool ok = true;
   if (warp < kSoftmaxWarps) {
     tc::registers_up<kSoftmaxRegisters>();
-    ok = softmax_role<DP>(a, c, sh, tmem, g);
+    ok = softmax_role<DP>(a, tiles_here, sh, tmem, g);
   } else if (warp < kSoftmaxWarps + kLoadWarps) {
     tc::registers_down<kLoadRegisters>();
-    ok = load_role<DP>(a, c, sh, k_tiles, v_tiles);
+    ok = load_role<DP>(a, tiles_here, sh, k_tiles, v_tiles);
   } else {
     tc::registers_down<kProductRegisters>();
     if (threadIdx.x == 32 * (kSoftmaxWarps + kLoadWarps)) {
-    ok = product_role<DP>(a, c, sh, tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
-    // products in flight end before the memory that they use is given up
-    int unused = 0;
-    tc::products_arrive(tc::smem_address(&sh.last));
-    ok = tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused) && ok;
+      ok = product_role<DP>(tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
+      // products in flight end before the memory that they use is given up
+      int unused = 0;
+      tc::products_arrive(tc::smem_address(&sh.last));
+      ok = tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused) && ok;
+    } else if (warp == kSoftmaxWarps + kLoadWarps + 1) {
+      ok = plan_role(a, c, sh);
     }
   }
   if (!ok && (threadIdx.x & 31) == 0) kv_flag(a.w, min(c.b, a.w.batch - 1), SV_ROW_TIMEOUT);
