@@ -96,10 +96,9 @@ __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {  // t
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 columns of the warp's 32 lanes, a lane to a thread (wait_loads before use).
+// 32 columns of the warp's 32 lanes, a lane to a thread; wait_loads before use.
 __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -110,6 +109,17 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
+}
+// Loads so far have arrived: these registers may be read (all loads are
+// waited for; naming the registers keeps their readers behind the wait).
+__device__ __forceinline__ void wait_loads(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
@@ -122,16 +132,15 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 // ---- products ----
+
+// One lane of a whole warp, chosen by the hardware: products issued under
+// this (and not under a comparison of thread indices) go out at full rate.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
 
 // A tile in shared memory whose rows of 128 bytes are swizzled in groups of
 // eight (16-byte chunk c of row r at c ^ (r & 7)), on a 1024-byte boundary.
@@ -142,16 +151,23 @@ __device__ __forceinline__ uint64_t tile_descriptor(uint32_t at, uint32_t block,
          static_cast<uint64_t>(group >> 4) << 32 | uint64_t{1} << 46 | uint64_t{2} << 61;
 }
 
-// fp16 x fp16 -> fp32, 128 x n; b_rows_inner: B's rows in memory are the inner dimension.
-__host__ __device__ constexpr uint32_t product_f16(int n, bool b_rows_inner) {
+// fp16 x fp16 -> fp32 and e4m3 x e4m3 -> fp32, 128 x n; b_rows_inner: B's rows in memory are the inner dimension.
+__host__ __device__ constexpr uint32_t product_kind(int n, bool b_rows_inner) {
   return 1u << 4 | (b_rows_inner ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (128u / 16) << 24;
 }
 
-// d += (or =, unless `add`) a b, with A (128 x 16) in tensor memory; one thread.
-__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+// d += (or =, unless `add`) a b, with A (128 x 16 fp16, 128 x 32 e4m3) in tensor memory; one thread.
+__device__ __forceinline__ void product_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+__device__ __forceinline__ void product_e4m3(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p; }" ::"r"(d),
       "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
