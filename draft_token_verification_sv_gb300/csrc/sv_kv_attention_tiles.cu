@@ -2,16 +2,18 @@
 // trees, long chains, stretches of a prompt.
 //
 // 128 query rows at a time against tiles of 128 tokens on the 5th-generation
-// tensor cores: S = Q K^T and O += P V, accumulators in tensor memory.  The
-// left sides (Q, and the weights P, which take the place of the scores they
-// come from) are in tensor memory too, so that only K and V are read from
-// shared memory.  One block per SM, four roles:
+// tensor cores: S = Q K^T and O += P V, accumulators in tensor memory, where
+// the weights P take the place of the scores they come from.  One block per
+// SM, four roles:
 //   1 warp plans: it walks the block's tiles and looks pages and scales up;
-//   8 warps load codes three tiles ahead and lay them out for the products:
+//   4 warps load codes two tiles ahead and lay them out for the products:
 //     keys as they are, values widened to fp16 (which holds them all);
 //   1 warp issues the products: S of tile t before P V of tile t - 1;
-//   4 warps turn scores into weights, a row a thread, with a running maximum
-//     that moves only when it is exceeded by 2^7 (then O is scaled anew).
+//   2 groups of 4 warps turn scores into weights, a row a thread, one group
+//     the even tiles and the other the odd ones, each with its own running
+//     maximum and its own O, which are joined where an item's part ends.
+//     The maximum moves only when weights reach 2^7 times it (then O is
+//     scaled anew), so that scores are read once and no maximum is taken.
 // S is formed in 8 bits without loss: a bf16 query is the sum of two e4m3
 // values (4 significant bits each, of 8; what lies below 2^-17 of the row's
 // largest is rounded), so S is two products of queries with the codes
@@ -30,26 +32,28 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kTileSteps = 8;
 constexpr int kTokens = kStep * kTileSteps;
-// weights: warps 0-3; loads: 4-11; products: 12; plan: 13 (14, 15 idle: registers move in fours of warps)
-constexpr int kSoftmaxWarps = 4, kLoadWarps = 8;
+// weights: warps 0-7; loads: 8-11; products: 12; plan: 13 (14, 15 idle: registers move in fours of warps)
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
 constexpr int kLoadThreads = 32 * kLoadWarps;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kLoadWarps + 4);
-constexpr int kSoftmaxRegisters = 216, kLoadRegisters = 96, kProductRegisters = 96;
-static_assert(4 * kSoftmaxRegisters + 8 * kLoadRegisters + 4 * kProductRegisters <= 16 * 128, "registers of a block");
+constexpr int kSoftmaxRegisters = 176, kLoadRegisters = 96, kProductRegisters = 64;
+static_assert(kSoftmaxWarps * kSoftmaxRegisters + kLoadWarps * kLoadRegisters + 4 * kProductRegisters <= 16 * 128,
+              "registers of a block");
 constexpr float kLift = 8.0f;  // weights are 2^8 times what they stand for: fp16 then keeps 2^-22 of the largest
 
-constexpr int kCodeStages = 4;
+constexpr int kCodeStages = 3;
 
 template <int DP> struct Tiles {
   static constexpr int kKeyBytes = kTokens * 128;          // a tile's keys: rows of 128 bytes (DP = 64 leaves half)
   static constexpr int kCodeBytes = kTokens * DP;          // its values' codes as they come,
   static constexpr int kValueBytes = kTokens * DP * 2;     // and in fp16,
   static constexpr int kBlockBytes = kTokens * 128;        // in blocks of 64 dims
-  static constexpr int kOperands = 2 * kValueBytes + kCodeStages * (kKeyBytes + kCodeBytes);
+  static constexpr int kQueryBytes = kRows * 128;          // one of the two parts of the queries
+  static constexpr int kOperands = 2 * kValueBytes + 2 * kQueryBytes + kCodeStages * (kKeyBytes + kCodeBytes);
   // 1 KB to find a 1024-byte boundary; more than half of an SM's shared memory keeps it to one block
   static constexpr int kShared = (kOperands > 118 * 1024 ? kOperands : 118 * 1024) + 1024;
-  // tensor memory, in columns: O, Q, two tiles of scores
-  static constexpr int kO = 0, kQ = DP, kS = DP + DP / 2;
+  // tensor memory, in columns: two O, two tiles of scores
+  static constexpr int kO = 0, kS = 2 * DP;
   static constexpr int kColumns = 512;
   static constexpr int kPart = kRows * (DP + 2);
 };
@@ -80,17 +84,17 @@ struct Part {
 struct Shared {
   CursorScratch cursor;
   uint64_t plan_full[kPlans], plan_free[kPlans], part_full[kParts], part_free[kParts];
-  uint64_t k_full[kCodeStages], v_full[2], s_full[2], p_ready[2], pv_done[2], q_ready, last;
+  uint64_t k_full[kCodeStages], v_full[2], s_full[2], p_ready[2], pv_done[2], q_ready, last, both[4];
+  float exchange[2][kRows][3];  // between the two threads of a row
   TilePlan plan[kPlans];
   Part part[kParts];
   uint32_t tmem;
   int gave_up;
 };
 
-// 16 codes as fp16: 32 bytes.
-__device__ __forceinline__ void widen(const uint4& c, uint4& lo, uint4& hi) {
-  lo = make_uint4(e4m3x2_to_f16x2(c.x & 0xffffu), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y & 0xffffu), e4m3x2_to_f16x2(c.y >> 16));
-  hi = make_uint4(e4m3x2_to_f16x2(c.z & 0xffffu), e4m3x2_to_f16x2(c.z >> 16), e4m3x2_to_f16x2(c.w & 0xffffu), e4m3x2_to_f16x2(c.w >> 16));
+// Eight codes as fp16.
+__device__ __forceinline__ uint4 widen(const uint2& c) {
+  return make_uint4(e4m3x2_to_f16x2(c.x & 0xffffu), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y & 0xffffu), e4m3x2_to_f16x2(c.y >> 16));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
@@ -105,7 +109,7 @@ __device__ __forceinline__ uint32_t bits16(int base, int from, int to) {
 }
 
 // Every lane waits (for the n-th phase of a barrier); the answer is the warp's.
-__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, long long n) {
+__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, int n) {
   return __all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up));
 }
 __device__ __forceinline__ void warp_arrive(uint64_t& bar) {
@@ -120,8 +124,8 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
   const KvView& w = a.w;
   const int lane = threadIdx.x & 31, mine = lane / kTileSteps, step = lane % kTileSteps;
   const int page_mask = (1 << w.page_shift) - 1;
-  long long it = 0;
-  for (long long item = 0; c.at < c.end; ++item) {
+  int it = 0;
+  for (int item = 0; c.at < c.end; ++item) {
     Part p;
     p.b = c.b;
     p.h = c.h;
@@ -187,7 +191,7 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
 // ---- loading ----
 
 template <int DP>
-__device__ bool load_role(const AttentionParams& a, const long long tiles, Shared& sh, uint8_t* k_tiles, uint8_t* v_tiles,
+__device__ bool load_role(const AttentionParams& a, const int tiles, Shared& sh, uint8_t* k_tiles, uint8_t* v_tiles,
                           uint8_t* codes) {
   using T = Tiles<DP>;
   constexpr int kChunks = DP / 16;                        // of a token
@@ -203,7 +207,7 @@ __device__ bool load_role(const AttentionParams& a, const long long tiles, Share
   const uint32_t key_at = tc::smem_address(k_tiles) + t0 * 128 + ((ch ^ (t0 & 7)) << 4);
   uint8_t* const mine = codes + tid * 16;
   const uint32_t code_at = tc::smem_address(mine);
-  const auto ask = [&](long long it) {
+  const auto ask = [&](int it) {
     const TilePlan& plan = sh.plan[it % kPlans];
     if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans)) return false;
     const uint32_t stage = static_cast<uint32_t>(it % kCodeStages);
@@ -221,30 +225,35 @@ __device__ bool load_role(const AttentionParams& a, const long long tiles, Share
     warp_arrive(sh.plan_free[it % kPlans]);
     return true;
   };
-  // A chunk of values becomes two of fp16, in rows of 64 dims, swizzled; lanes of the second block of dims write theirs
-  // the other way round (other banks).
+  // A chunk of values becomes two of fp16, in rows of 64 dims, swizzled; lanes of the second block of dims do its
+  // halves the other way round (they write other banks then).
   const int turn = ch >> 2 & 1;
   const int to = (ch >> 2) * T::kBlockBytes + t0 * 128;
-  const int half0 = (2 * (ch & 3) + turn) ^ (t0 & 7), half1 = (2 * (ch & 3) + 1 - turn) ^ (t0 & 7);
+  const int half0 = to + (((2 * (ch & 3) + turn) ^ (t0 & 7)) << 4), half1 = to + (((2 * (ch & 3) + 1 - turn) ^ (t0 & 7)) << 4);
   for (int i = 0; i < kCodeStages - 1; ++i) {
     if (i < tiles && !ask(i)) return false;
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   bool ok = true;
 #pragma unroll 1
-  for (long long it = 0; ok && it < tiles; ++it) {
+  for (int it = 0; ok && it < tiles; ++it) {
     const int st = it & 1;
     asm volatile("cp.async.wait_group %0;" ::"n"(kCodeStages - 2) : "memory");
     tc::publish_shared();
     warp_arrive(sh.k_full[it % kCodeStages]);
     ok = it < 2 || warp_wait(sh, sh.pv_done[st], (it >> 1) - 1);
+    uint2 c[NI][2];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      uint4 lo, hi;
-      widen(*reinterpret_cast<const uint4*>(mine + (it % kCodeStages) * T::kCodeBytes + i * kLoadThreads * 16), lo, hi);
-      uint8_t* row = v_tiles + st * T::kValueBytes + to + i * kPer * 128;
-      *reinterpret_cast<uint4*>(row + (half0 << 4)) = turn ? hi : lo;
-      *reinterpret_cast<uint4*>(row + (half1 << 4)) = turn ? lo : hi;
+      const uint8_t* from = mine + (it % kCodeStages) * T::kCodeBytes + i * kLoadThreads * 16;
+      c[i][0] = *reinterpret_cast<const uint2*>(from + 8 * turn);
+      c[i][1] = *reinterpret_cast<const uint2*>(from + 8 - 8 * turn);
+    }
+    uint8_t* row = v_tiles + st * T::kValueBytes;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      *reinterpret_cast<uint4*>(row + half0 + i * kPer * 128) = widen(c[i][0]);
+      *reinterpret_cast<uint4*>(row + half1 + i * kPer * 128) = widen(c[i][1]);
     }
     tc::publish_shared();
     warp_arrive(sh.v_full[st]);
@@ -260,77 +269,78 @@ __device__ bool load_role(const AttentionParams& a, const long long tiles, Share
 // ---- products ----
 
 template <int DP>
-__device__ bool product_role(const long long tiles, Shared& sh, uint32_t k_tiles, uint32_t v_tiles, uint32_t tmem) {
+__device__ bool product_role(const int tiles, Shared& sh, uint32_t q_tiles, uint32_t k_tiles, uint32_t v_tiles, uint32_t tmem) {
   using T = Tiles<DP>;
   constexpr uint32_t kScores = tc::product_kind(kTokens, false), kValues = tc::product_kind(DP, true);
-  const auto wait = [&](uint64_t& bar, long long n) {
+  const auto wait = [&](uint64_t& bar, int n) {
     const bool ok = warp_wait(sh, bar, n);
     tc::fence_after();
     return ok;
   };
-  const auto weigh = [&](long long it, bool first) {  // O (+)= P V of tile it
+  const auto weigh = [&](int it, bool first) {  // O (+)= P V of tile it, its group's first of the part
     const int st = it & 1;
     if (!wait(sh.v_full[st], it >> 1) || !wait(sh.p_ready[st], it >> 1)) return false;
     if (tc::elected()) {
 #pragma unroll
       for (int k = 0; k < kTokens / 16; ++k)
-        tc::product_f16(tmem + T::kO, tmem + T::kS + st * kTokens + k * 8,
+        tc::product_f16(tmem + T::kO + st * DP, tmem + T::kS + st * kTokens + k * 8,
                         tc::tile_descriptor(v_tiles + st * T::kValueBytes + k * 2048, T::kBlockBytes, 1024), kValues, !first || k > 0);
       tc::products_arrive(tc::smem_address(&sh.pv_done[st]));
     }
     __syncwarp();
     return true;
   };
-  bool first_before = false;  // the last tile was its part's first
-  long long item = 0;
-  for (long long it = 0; it < tiles; ++it) {
+  int in_part = 0;  // tiles of the part before this one
+  int item = 0;
+  for (int it = 0; it < tiles; ++it) {
     const int st = it & 1;
     if (!wait(sh.plan_full[it % kPlans], it / kPlans)) return false;
     const bool first = sh.plan[it % kPlans].first, last = sh.plan[it % kPlans].last;
     warp_arrive(sh.plan_free[it % kPlans]);
-    if (first && !wait(sh.q_ready, item++)) return false;
+    if (first) {
+      in_part = 0;
+      if (!wait(sh.q_ready, item++)) return false;
+    }
     if (!wait(sh.k_full[it % kCodeStages], it / kCodeStages)) return false;
     if (tc::elected()) {
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k)  // both parts of the queries with the same keys
-        tc::product_e4m3(tmem + T::kS + st * kTokens, tmem + T::kQ + (k & 1) * (DP / 4) + (k >> 1) * 8,
+        tc::product_e4m3(tmem + T::kS + st * kTokens, tc::tile_descriptor(q_tiles + (k & 1) * T::kQueryBytes + (k >> 1) * 32, 16, 1024),
                          tc::tile_descriptor(k_tiles + static_cast<uint32_t>(it % kCodeStages) * T::kKeyBytes + (k >> 1) * 32, 16, 1024),
                          kScores, k > 0);
       tc::products_arrive(tc::smem_address(&sh.s_full[st]));
     }
     __syncwarp();
-    if (!first && !weigh(it - 1, first_before)) return false;
-    if (last && !weigh(it, first)) return false;
-    first_before = first;
+    if (!first && !weigh(it - 1, in_part <= 2)) return false;
+    if (last && !weigh(it, in_part < 2)) return false;
+    ++in_part;
   }
   return true;
 }
 
 // ---- scores to weights, and results ----
 
-// Which of a tile's tokens the thread's row sees, 32 to a word.
-__device__ __forceinline__ void seen_tokens(const AttentionParams& a, const TilePlan& plan, const int32_t* parents, int ctx, int token,
-                                            int pos, uint32_t (&seen)[4]) {
+// Which tokens of two of a tile's steps the thread's row sees.
+__device__ __forceinline__ uint32_t seen_tokens(const AttentionParams& a, const TilePlan& plan, int step0, const int32_t* parents, int ctx,
+                                                int token, int pos) {
   const int past = parents ? ctx : pos + 1;
   const int from = a.window ? max(0, pos - a.window + 1) : 0;
-#pragma unroll
-  for (int i = 0; i < kTileSteps; ++i) {
-    uint32_t b = 0;
-    if (plan.count[i] > 0) {
-      const int base = plan.token[i];
-      b = bits16(base, from, past);
-      if (a.window) b |= bits16(base, 0, min(a.sinks, past));
-      if (parents && base + kStep > ctx)
-        for (int u = token, back = 0; u >= 0; u = tree_parent(parents, u), ++back) {
-          const int j = ctx + u - base;
-          if (j >= 0 && j < kStep && (a.window == 0 || back < a.window || pos - back < a.sinks)) b |= 1u << j;
-        }
-    }
-    if (i & 1)
-      seen[i >> 1] |= b << 16;
-    else
-      seen[i >> 1] = b;
+  uint32_t seen = 0;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (plan.count[step0 + i] <= 0) continue;
+    const int base = plan.token[step0 + i];
+    uint32_t b = bits16(base, from, past);
+    if (a.window) b |= bits16(base, 0, min(a.sinks, past));
+    if (parents && base + kStep > ctx)
+      for (int u = token, back = 0; u >= 0; u = tree_parent(parents, u), ++back) {
+        const int j = ctx + u - base;
+        if (j >= 0 && j < kStep && (a.window == 0 || back < a.window || pos - back < a.sinks)) b |= 1u << j;
+      }
+    seen |= b << (16 * i);
   }
+  __syncwarp();
+  return seen;
 }
 
 // The largest of 16 scores (that are seen).
@@ -374,11 +384,13 @@ __device__ __forceinline__ float2 weights32(const uint32_t (&x)[32], uint32_t se
 }
 
 template <int DP>
-__device__ bool softmax_role(const AttentionParams& a, const long long tiles, Shared& sh, uint32_t tmem, int g) {
+__device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& sh, uint8_t* q_tiles, uint32_t tmem, int g) {
   using T = Tiles<DP>;
-  const int r = threadIdx.x;
-  const uint32_t mine = tmem + ((threadIdx.x >> 5) << 21);  // the warp's 32 lanes
-  const auto wait = [&](uint64_t& bar, long long n) {
+  constexpr int kDims = DP / 2;  // a thread's share of a row of queries and results
+  const int r = threadIdx.x & (kRows - 1), group = threadIdx.x / kRows, quarter = (threadIdx.x >> 5) & 3;
+  const uint32_t mine = tmem + (quarter << 21);  // the warp's 32 lanes
+  const uint32_t scores = mine + T::kS + group * kTokens, own_o = mine + T::kO + group * DP;
+  const auto wait = [&](uint64_t& bar, int n) {
     const bool ok = warp_wait(sh, bar, n);
     tc::fence_after();
     return ok;
@@ -388,26 +400,31 @@ __device__ bool softmax_role(const AttentionParams& a, const long long tiles, Sh
     tc::fence_before();
     warp_arrive(bar);
   };
-  long long it = 0;
-  for (long long item = 0; it < tiles; ++item) {
+  // The row's two threads meet.
+  int meetings = 0;
+  const auto meet = [&]() {
+    warp_arrive(sh.both[quarter]);
+    return warp_wait(sh, sh.both[quarter], meetings++);
+  };
+  int it0 = 0;  // the part's first tile
+  for (int item = 0; it0 < tiles; ++item) {
     if (!wait(sh.part_full[item % kParts], item / kParts)) return false;
-    const Part p = sh.part[item % kParts];
-    warp_arrive(sh.part_free[item % kParts]);
+    const Part& p = sh.part[item % kParts];
     const int32_t* parents = a.parents ? a.parents + p.row0 : nullptr;
-    const int row = p.r0 + min(r, p.rows - 1);
-    const int token = row / a.group, head = p.h * a.group + row % a.group;
-    const int64_t out_row = static_cast<int64_t>(p.row0) + token;
+    const int ctx = p.ctx, token = (p.r0 + min(r, p.rows - 1)) / a.group;
 
     // the row's queries, scaled by a power of two, in two parts
     float factor;
     {
-      const uint16_t* q = static_cast<const uint16_t*>(a.q) + out_row * a.q_row_stride + head * a.q_head_stride;
-      uint4 raw[DP / 8];
+      const int head = p.h * a.group + (p.r0 + min(r, p.rows - 1)) % a.group;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + (static_cast<int64_t>(p.row0) + token) * a.q_row_stride +
+                          head * a.q_head_stride + group * kDims;
+      uint4 raw[kDims / 8];
       uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < DP / 8; ++i) {
+      for (int i = 0; i < kDims / 8; ++i) {
         raw[i] = make_uint4(0, 0, 0, 0);
-        if (r < p.rows && i * 8 < a.w.dim) {
+        if (r < p.rows && group * kDims + i * 8 < a.w.dim) {
           if (a.q_vec) {
             raw[i] = *reinterpret_cast<const uint4*>(q + i * 8);
           } else {
@@ -418,95 +435,88 @@ __device__ bool softmax_role(const AttentionParams& a, const long long tiles, Sh
         }
       }
 #pragma unroll
-      for (int i = 0; i < DP / 8; ++i) {
+      for (int i = 0; i < kDims / 8; ++i) {
         top = __vmaxu2(__vmaxu2(top, raw[i].x & 0x7fff7fffu), raw[i].y & 0x7fff7fffu);
         top = __vmaxu2(__vmaxu2(top, raw[i].z & 0x7fff7fffu), raw[i].w & 0x7fff7fffu);
       }
-      const int exponent = static_cast<int>(max(top >> 16, top & 0xffffu) >> 7);
+      top = max(top >> 16, top & 0xffffu);
+      // (the last part's exchange has been read by both: each came here from its second meeting)
+      sh.exchange[group][r][0] = __uint_as_float(top);
+      if (!meet()) return false;
+      top = max(top, __float_as_uint(sh.exchange[group ^ 1][r][0]));
+      const int exponent = static_cast<int>(top >> 7);
       const int e = exponent == 255 || top == 0 ? 0 : min(120, 134 - exponent);
-      __syncwarp();
       // the largest becomes 2^7 .. 2^8; a negative factor goes into the queries, so that larger products are larger scores
       const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
       factor = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       if (exponent == 255) factor = CUDART_NAN_F;  // the row's scores are not numbers
-      uint32_t hi[DP / 4], lo[DP / 4];
+      uint8_t* to = q_tiles + r * 128;
 #pragma unroll
-      for (int i = 0; i < DP / 8; ++i) {
-        float f[8];
-        unpack<uint16_t>(raw[i], f);
+      for (int i = 0; i < kDims / 16; ++i) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t h[2], r[2];
+        for (int k = 0; k < 4; ++k) {
+          const uint4 c = raw[2 * i + (k >> 1)];
+          const uint32_t words[2] = {k & 1 ? c.z : c.x, k & 1 ? c.w : c.y};
+          uint32_t h[2], rest[2];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const float u = f[4 * k + 2 * n] * up, v = f[4 * k + 2 * n + 1] * up;
+            const float u = __uint_as_float(words[n] << 16) * up, v = __uint_as_float(words[n] & 0xffff0000u) * up;
             h[n] = floats_to_e4m3x2(u, v);
             const float2 held = f16x2_to_float2(e4m3x2_to_f16x2(h[n]));
-            r[n] = floats_to_e4m3x2(u - held.x, v - held.y);
+            rest[n] = floats_to_e4m3x2(u - held.x, v - held.y);
           }
-          hi[2 * i + k] = h[0] | h[1] << 16;
-          lo[2 * i + k] = r[0] | r[1] << 16;
+          hi[k] = h[0] | h[1] << 16;
+          lo[k] = rest[0] | rest[1] << 16;
         }
+        const int at = ((group * (kDims / 16) + i) ^ (r & 7)) << 4;
+        *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(to + T::kQueryBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
-      if constexpr (DP == 128) {
-        tc::tmem_store32(mine + T::kQ, hi);
-        tc::tmem_store32(mine + T::kQ + 32, lo);
-      } else {
-        uint32_t both[32];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          both[i] = hi[i];
-          both[16 + i] = lo[i];
-        }
-        tc::tmem_store32(mine + T::kQ, both);
-      }
+      tc::publish_shared();
       arrive(sh.q_ready);
     }
-    int pos = p.ctx + token;
+    int pos = ctx + token;
     if (parents) {
       int depth = 0;
       for (int u = tree_parent(parents, token); u >= 0; u = tree_parent(parents, u)) ++depth;
-      pos = p.ctx + depth;
+      pos = ctx + depth;
       __syncwarp();
     }
 
-    float m = -CUDART_INF_F, l = 0.0f, v_ref = kNoScale;  // v_ref: log2 of the values' unit
-    for (int t = 0; t < p.count; ++t, ++it) {
-      const int st = it & 1;
+    // m: the maximum so far (base 2), l: sum of weights, v_ref: log2 of the values' unit
+    float m = -CUDART_INF_F, l = 0.0f, v_ref = kNoScale;
+    const int end = it0 + p.count;
+    int it = it0 + ((it0 & 1) != group);
+    const int begin = it;
+    for (; it < end; it += 2) {
       const TilePlan& plan = sh.plan[it % kPlans];
-      if (!wait(sh.plan_full[it % kPlans], it / kPlans) || !wait(sh.s_full[st], it >> 1)) return false;
-      const uint32_t scores = mine + T::kS + st * kTokens;
+      if (!wait(sh.plan_full[it % kPlans], it / kPlans) || !wait(sh.s_full[group], it >> 1)) return false;
       float v_top = kNoScale;
 #pragma unroll
       for (int i = 0; i < kTileSteps; ++i) v_top = fmaxf(v_top, plan.v_log2[i]);
-      // Twice over the scores, 64 at a time.  The loops stay rolled: the roles share the instruction cache, and this one
-      // in a straight line took 2100 cycles a tile instead of 800.
+      // Twice over the scores, 64 at a time.  The loops stay rolled: the roles share the instruction cache.
       const auto tile = [&](auto masked) {
         constexpr bool M = decltype(masked)::value;
-        uint32_t seen[4] = {};
-        if (M) {
-          seen_tokens(a, plan, parents, p.ctx, token, pos, seen);
-          __syncwarp();
-        }
         float top = -CUDART_INF_F;  // the tile's largest score in base 2
-        uint32_t x0[32], x1[32];
-        tc::tmem_load32(scores, x0);
 #pragma unroll 1
-        for (int i = 0; i < kTokens; i += 64) {
-          const uint32_t b0 = i ? seen[2] : seen[0], b1 = i ? seen[3] : seen[1];
-          const float* k = plan.k_scale + i / kStep;
+        for (int c = 0; c < kTileSteps; c += 4) {
+          uint32_t x0[32], x1[32];
+          tc::tmem_load32(scores + 16 * c, x0);
+          tc::tmem_load32(scores + 16 * c + 32, x1);
+          const uint32_t seen0 = M ? seen_tokens(a, plan, c, parents, ctx, token, pos) : 0;
+          const uint32_t seen1 = M ? seen_tokens(a, plan, c + 2, parents, ctx, token, pos) : 0;
+          const float* k = plan.k_scale + c;
           tc::wait_loads(x0);
-          tc::tmem_load32(scores + i + 32, x1);
-          top = fmaxf(top, fmaxf(largest16<M>(&x0[0], b0) * (factor * k[0]), largest16<M>(&x0[16], b0 >> 16) * (factor * k[1])));
+          top = fmaxf(top, fmaxf(largest16<M>(&x0[0], seen0) * (factor * k[0]), largest16<M>(&x0[16], seen0 >> 16) * (factor * k[1])));
           tc::wait_loads(x1);
-          tc::tmem_load32(scores + (i + 64) % kTokens, x0);  // at the end the first again
-          top = fmaxf(top, fmaxf(largest16<M>(&x1[0], b1) * (factor * k[2]), largest16<M>(&x1[16], b1 >> 16) * (factor * k[3])));
+          top = fmaxf(top, fmaxf(largest16<M>(&x1[0], seen1) * (factor * k[2]), largest16<M>(&x1[16], seen1 >> 16) * (factor * k[3])));
         }
-        if (t == 0) {
-          m = top;
+        if (it == begin) {
+          m = ceilf(top);
           v_ref = v_top;
         } else if (__any_sync(0xffffffffu, top > m + 7.0f || v_top > v_ref)) {
-          const float up = fmaxf(m, top);
+          const float up = fmaxf(m, ceilf(top));
           float fix = up == -CUDART_INF_F ? 1.0f : ex2(m - up);
           l *= fix;
           m = up;
@@ -514,101 +524,120 @@ __device__ bool softmax_role(const AttentionParams& a, const long long tiles, Sh
             fix *= ex2(v_ref - v_top);
             v_ref = v_top;
           }
-          if (!wait(sh.pv_done[(it - 1) & 1], (it - 1) >> 1)) return false;
+          if (!wait(sh.pv_done[group], (it >> 1) - 1)) return false;
 #pragma unroll 1
-          for (int i = 0; i < DP; i += 32) {
-            tc::tmem_load32(mine + T::kO + i, x1);
-            tc::wait_loads(x1);
+          for (int i = 0; i < DP; i += 16) {
+            uint32_t o[16];
+            tc::tmem_load16(own_o + i, o);
+            tc::wait_loads(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x1[k] = __float_as_uint(__uint_as_float(x1[k]) * fix);
-            tc::tmem_store32(mine + T::kO + i, x1);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
+            tc::tmem_store(own_o + i, o);
           }
         }
         // weights, in the place of the scores' first half, in units of their values' scales
         const float base = kLift - (m == -CUDART_INF_F ? 0.0f : m);
 #pragma unroll 1
-        for (int i = 0; i < kTokens; i += 64) {
-          const uint32_t b0 = i ? seen[2] : seen[0], b1 = i ? seen[3] : seen[1];
-          const float* k = plan.k_scale + i / kStep;
-          const float* v = plan.v_log2 + i / kStep;
-          uint32_t w[32];
-          float u[4];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) u[n] = fmaxf(v[n] - v_ref, -100.0f);
+        for (int c = 0; c < kTileSteps; c += 4) {
+          uint32_t x0[32], x1[32], w[16];
+          tc::tmem_load32(scores + 16 * c, x0);
+          tc::tmem_load32(scores + 16 * c + 32, x1);
+          const uint32_t seen0 = M ? seen_tokens(a, plan, c, parents, ctx, token, pos) : 0;
+          const uint32_t seen1 = M ? seen_tokens(a, plan, c + 2, parents, ctx, token, pos) : 0;
+          const float* k = plan.k_scale + c;
+          const float* v = plan.v_log2 + c;
+          float u0 = fmaxf(v[0] - v_ref, -100.0f), u1 = fmaxf(v[1] - v_ref, -100.0f);
           tc::wait_loads(x0);
-          tc::tmem_load32(scores + i + 32, x1);
-          float2 sums = weights32<M>(x0, b0, factor * k[0], factor * k[1], base + u[0], base + u[1], w);
-          l += sums.x * ex2(-u[0]) + sums.y * ex2(-u[1]);
+          float2 sums = weights32<M>(x0, seen0, factor * k[0], factor * k[1], base + u0, base + u1, w);
+          l += sums.x * ex2(-u0) + sums.y * ex2(-u1);
           tc::wait_loads(x1);
-          if (i == 0) tc::tmem_load32(scores + 64, x0);
-          sums = weights32<M>(x1, b1, factor * k[2], factor * k[3], base + u[2], base + u[3], w + 16);
-          l += sums.x * ex2(-u[2]) + sums.y * ex2(-u[3]);
-          tc::tmem_store32(scores + i / 2, w);
+          tc::tmem_store(scores + 8 * c, w);
+          u0 = fmaxf(v[2] - v_ref, -100.0f);
+          u1 = fmaxf(v[3] - v_ref, -100.0f);
+          sums = weights32<M>(x1, seen1, factor * k[2], factor * k[3], base + u0, base + u1, w);
+          l += sums.x * ex2(-u0) + sums.y * ex2(-u1);
+          tc::tmem_store(scores + 8 * c + 16, w);
         }
         return true;
       };
       if (!(plan.whole ? tile(std::false_type{}) : tile(std::true_type{}))) return false;
-      arrive(sh.p_ready[st]);
+      arrive(sh.p_ready[group]);
       warp_arrive(sh.plan_free[it % kPlans]);
     }
 
-    // the part's result
-    if (!wait(sh.pv_done[(it - 1) & 1], (it - 1) >> 1)) return false;
-    const bool complete = p.count == p.tiles;
+    // The part's result: both threads of a row know both halves' sums, and each joins half of the dims.
+    float* given = sh.exchange[group][r];
+    given[0] = m;
+    given[1] = l;
+    given[2] = v_ref;
+    if (!meet()) return false;
+    const float* theirs = sh.exchange[group ^ 1][r];
+    const float their_m = theirs[0], their_l = theirs[1], their_v = theirs[2];
+    const bool own = begin < end, other = p.count > 1 || !own;
+    if ((own && !wait(sh.pv_done[group], (it >> 1) - 1)) ||
+        (other && !wait(sh.pv_done[group ^ 1], (end - 1 - (((end - 1) & 1) == group)) >> 1)))
+      return false;
+    if (!meet()) return false;  // (the exchange is free again)
+    const float top = fmaxf(m, their_m);
     const float lift = 1.0f / 256.0f;
-    l *= lift;
-    const float scale = ex2(v_ref) * lift;
-    if (complete) {
-      uint16_t* out = static_cast<uint16_t*>(a.out) + out_row * a.out_row_stride + head * a.out_head_stride;
-      const float inv = l == 0.0f ? 0.0f : scale / l;
+    // (a group that saw nothing has sums of 0, or sums that are not numbers, which stay)
+    const float fix = m == -CUDART_INF_F ? 1.0f : ex2(m - top), their_fix = their_m == -CUDART_INF_F ? 1.0f : ex2(their_m - top);
+    const float total = (l * fix + their_l * their_fix) * lift;
+    const bool complete = p.count == p.tiles;
+    const float inv = !complete ? lift : total == 0.0f ? 0.0f : lift / total;
+    const float scale = fix * ex2(v_ref) * inv, their_scale = their_fix * ex2(their_v) * inv;
+    const int head = p.h * a.group + (p.r0 + min(r, p.rows - 1)) % a.group;
+    const int64_t out_row = static_cast<int64_t>(p.row0) + token;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + out_row * a.out_row_stride + head * a.out_head_stride;
+    float* part = a.parts + (2 * static_cast<int64_t>(g) + (p.tile0 == 0 ? 1 : 0)) * T::kPart;
+#pragma unroll 1
+    for (int d = group * kDims; d < (group + 1) * kDims; d += 32) {
+      uint32_t x[32], y[32];
+      if (own) tc::tmem_load32(own_o + d, x);
+      if (other) tc::tmem_load32(mine + T::kO + (group ^ 1) * DP + d, y);
+      tc::wait_loads(x);
+      tc::wait_loads(y);
 #pragma unroll
-      for (int i = 0; i < DP / 32; ++i) {
-        uint32_t x[32];
-        tc::tmem_load32(mine + T::kO + 32 * i, x);
-        tc::wait_loads(x);
+      for (int k = 0; k < 32; ++k)
+        x[k] = __float_as_uint((own ? __uint_as_float(x[k]) * scale : 0.0f) + (other ? __uint_as_float(y[k]) * their_scale : 0.0f));
+      if (complete) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t o[8];
 #pragma unroll
-          for (int n = 0; n < 8; ++n)
-            o[n] = floats_to_bf16x2(__uint_as_float(x[16 * k + 2 * n]) * inv, __uint_as_float(x[16 * k + 2 * n + 1]) * inv);
-          const int d = 32 * i + 16 * k;
-          if (r < p.rows && d < a.w.dim) {
+          for (int n = 0; n < 8; ++n) o[n] = floats_to_bf16x2(__uint_as_float(x[16 * k + 2 * n]), __uint_as_float(x[16 * k + 2 * n + 1]));
+          if (r < p.rows && d + 16 * k < a.w.dim) {
             if (a.out_vec32) {
-              tc::store_32(out + d, o);
+              tc::store_32(out + d + 16 * k, o);
             } else {
 #pragma unroll
               for (int n = 0; n < 8; ++n) {
-                out[d + 2 * n] = static_cast<uint16_t>(o[n]);
-                out[d + 2 * n + 1] = static_cast<uint16_t>(o[n] >> 16);
+                out[d + 16 * k + 2 * n] = static_cast<uint16_t>(o[n]);
+                out[d + 16 * k + 2 * n + 1] = static_cast<uint16_t>(o[n] >> 16);
               }
             }
           }
         }
-        __syncwarp();
-      }
-      if (r < p.rows && a.lse) a.lse[out_row * a.heads + head] = row_lse(m, l);
-    } else {
-      float* part = a.parts + (2 * static_cast<int64_t>(g) + (p.tile0 == 0 ? 1 : 0)) * T::kPart;
-#pragma unroll
-      for (int i = 0; i < DP / 32; ++i) {
-        uint32_t x[32];
-        tc::tmem_load32(mine + T::kO + 32 * i, x);
-        tc::wait_loads(x);
+      } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t o[8];
 #pragma unroll
-          for (int n = 0; n < 8; ++n) o[n] = __float_as_uint(__uint_as_float(x[8 * k + n]) * scale);
-          if (r < p.rows) tc::store_32(part + r * DP + 32 * i + 8 * k, o);
+          for (int n = 0; n < 8; ++n) o[n] = x[8 * k + n];
+          if (r < p.rows) tc::store_32(part + r * DP + d + 8 * k, o);
         }
-        __syncwarp();
       }
-      if (r < p.rows) *reinterpret_cast<float2*>(part + kRows * DP + 2 * r) = make_float2(m, l);
-      if (p.tile0 == 0 && r == 0)
-        a.joins[g] = JoinRecord{p.row0, p.r0, p.rows, p.h, p.join_last};
+      __syncwarp();
     }
-    __syncwarp();
+    if (group == 0 && r < p.rows) {
+      if (!complete)
+        *reinterpret_cast<float2*>(part + kRows * DP + 2 * r) = make_float2(top, total);
+      else if (a.lse)
+        a.lse[out_row * a.heads + head] = row_lse(top, total);
+    }
+    if (!complete && p.tile0 == 0 && threadIdx.x == 0) a.joins[g] = JoinRecord{p.row0, p.r0, p.rows, p.h, p.join_last};
+    warp_arrive(sh.part_free[item % kParts]);
+    it0 = end;
   }
   return true;
 }
@@ -621,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   const uint32_t at = tc::smem_address(raw);
   uint8_t* tiles = raw + ((at + 1023u & ~1023u) - at);
   uint8_t* v_tiles = tiles;
-  uint8_t* k_tiles = tiles + 2 * T::kValueBytes;
+  uint8_t* q_tiles = tiles + 2 * T::kValueBytes;
+  uint8_t* k_tiles = q_tiles + 2 * T::kQueryBytes;
   const int warp = threadIdx.x >> 5, g = blockIdx.x;
   flag_sequences(a, g, gridDim.x, kThreads);
   if (threadIdx.x == 0) {
@@ -631,17 +661,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
     for (int i = 0; i < 2; ++i) {
       tc::barrier_init(tc::smem_address(&sh.v_full[i]), kLoadWarps);
       tc::barrier_init(tc::smem_address(&sh.s_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.p_ready[i]), kSoftmaxWarps);
+      tc::barrier_init(tc::smem_address(&sh.p_ready[i]), kSoftmaxWarps / 2);
       tc::barrier_init(tc::smem_address(&sh.pv_done[i]), 1);
     }
     for (int i = 0; i < kPlans; ++i) {
       tc::barrier_init(tc::smem_address(&sh.plan_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.plan_free[i]), kLoadWarps + kSoftmaxWarps + 1);
+      tc::barrier_init(tc::smem_address(&sh.plan_free[i]), kLoadWarps + kSoftmaxWarps / 2 + 1);
     }
     for (int i = 0; i < kParts; ++i) {
       tc::barrier_init(tc::smem_address(&sh.part_full[i]), 1);
       tc::barrier_init(tc::smem_address(&sh.part_free[i]), kSoftmaxWarps);
     }
+    for (int i = 0; i < 4; ++i) tc::barrier_init(tc::smem_address(&sh.both[i]), 2);
     tc::barrier_init(tc::smem_address(&sh.q_ready), kSoftmaxWarps);
     tc::barrier_init(tc::smem_address(&sh.last), 1);
     tc::publish_shared();
@@ -652,18 +683,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
-  const long long tiles_here = c.end - c.at;
+  const int tiles_here = static_cast<int>(c.end - c.at);  // 2^31 tiles would take half an hour
   bool ok = true;
   if (warp < kSoftmaxWarps) {
     tc::registers_up<kSoftmaxRegisters>();
-    ok = softmax_role<DP>(a, tiles_here, sh, tmem, g);
+    ok = softmax_role<DP>(a, tiles_here, sh, q_tiles, tmem, g);
   } else if (warp < kSoftmaxWarps + kLoadWarps) {
     tc::registers_down<kLoadRegisters>();
     ok = load_role<DP>(a, tiles_here, sh, k_tiles, v_tiles, k_tiles + kCodeStages * T::kKeyBytes);
   } else {
     tc::registers_down<kProductRegisters>();
     if (warp == kSoftmaxWarps + kLoadWarps) {
-      ok = product_role<DP>(tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
+      ok = product_role<DP>(tiles_here, sh, tc::smem_address(q_tiles), tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
       // products in flight end before the memory that they use is given up
       int unused = 0;
       if (tc::elected()) tc::products_arrive(tc::smem_address(&sh.last));

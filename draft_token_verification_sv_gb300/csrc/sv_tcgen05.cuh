@@ -110,6 +110,14 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
 }
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
 // Loads so far have arrived: these registers may be read (all loads are
 // waited for; naming the registers keeps their readers behind the wait).
 __device__ __forceinline__ void wait_loads(uint32_t (&r)[32]) {
@@ -121,17 +129,22 @@ __device__ __forceinline__ void wait_loads(uint32_t (&r)[32]) {
                :
                : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void wait_loads(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+
 // ---- products ----
 
 // One lane of a whole warp, chosen by the hardware: products issued under
@@ -156,7 +169,7 @@ __host__ __device__ constexpr uint32_t product_kind(int n, bool b_rows_inner) {
   return 1u << 4 | (b_rows_inner ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (128u / 16) << 24;
 }
 
-// d += (or =, unless `add`) a b, with A (128 x 16 fp16, 128 x 32 e4m3) in tensor memory; one thread.
+// d += (or =, unless `add`) a b, 128 x 16 fp16 and 128 x 32 e4m3; one thread.  A in tensor memory:
 __device__ __forceinline__ void product_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
@@ -164,11 +177,12 @@ __device__ __forceinline__ void product_f16(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
-__device__ __forceinline__ void product_e4m3(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+// The same with A in shared memory.
+__device__ __forceinline__ void product_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
 // The barrier gets an arrival when this thread's products so far are done.
