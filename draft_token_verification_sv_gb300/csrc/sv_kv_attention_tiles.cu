@@ -4,10 +4,11 @@
 // 128 query rows at a time against tiles of 128 tokens on the 5th-generation
 // tensor cores: S = Q K^T and O += P V, accumulators in tensor memory, where
 // the weights P take the place of the scores they come from.  One block per
-// SM, four roles:
+// SM, five roles:
 //   1 warp plans: it walks the block's tiles and looks pages and scales up;
-//   4 warps load codes two tiles ahead and lay them out for the products:
-//     keys as they are, values widened to fp16 (which holds them all);
+//   1 warp fetches codes, a box of 16 tokens of a page to a copy, two tiles
+//     ahead: keys to where the products read them, swizzled;
+//   4 warps widen the values to fp16 (which holds them all);
 //   1 warp issues the products: S of tile t before P V of tile t - 1;
 //   2 groups of 4 warps turn scores into weights, a row a thread, one group
 //     the even tiles and the other the odd ones, each with its own running
@@ -32,16 +33,16 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kTileSteps = 8;
 constexpr int kTokens = kStep * kTileSteps;
-// weights: warps 0-7; loads: 8-11; products: 12; plan: 13 (14, 15 idle: registers move in fours of warps)
-constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
-constexpr int kLoadThreads = 32 * kLoadWarps;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kLoadWarps + 4);
-constexpr int kSoftmaxRegisters = 176, kLoadRegisters = 96, kProductRegisters = 64;
-static_assert(kSoftmaxWarps * kSoftmaxRegisters + kLoadWarps * kLoadRegisters + 4 * kProductRegisters <= 16 * 128,
+// weights: warps 0-7; values: 8-11; products: 12; plan: 13; fetch: 14 (15 idle: registers move in fours of warps)
+constexpr int kSoftmaxWarps = 8, kValueWarps = 4;
+constexpr int kValueThreads = 32 * kValueWarps;
+constexpr int kThreads = 32 * (kSoftmaxWarps + kValueWarps + 4);
+constexpr int kSoftmaxRegisters = 176, kValueRegisters = 96, kOtherRegisters = 64;
+static_assert(kSoftmaxWarps * kSoftmaxRegisters + kValueWarps * kValueRegisters + 4 * kOtherRegisters <= 16 * 128,
               "registers of a block");
 constexpr float kLift = 8.0f;  // weights are 2^8 times what they stand for: fp16 then keeps 2^-22 of the largest
 
-constexpr int kCodeStages = 3;
+constexpr int kCodeStages = 3;  // tiles of codes in shared memory
 
 template <int DP> struct Tiles {
   static constexpr int kKeyBytes = kTokens * 128;          // a tile's keys: rows of 128 bytes (DP = 64 leaves half)
@@ -64,9 +65,10 @@ constexpr float kNoScale = -1000.0f;
 
 // What the roles need of a tile.
 struct TilePlan {
-  int64_t base[kTileSteps];   // of each step's codes, or -1
+  int page[kTileSteps], slot[kTileSteps];  // where each step's codes lie
+  int head;
   int token[kTileSteps];      // its first token
-  int count[kTileSteps];      // tokens in sight
+  int count[kTileSteps];      // tokens in sight, 0: nothing to fetch
   float k_scale[kTileSteps];
   float v_log2[kTileSteps];   // log2 of the values' scale, kNoScale for none
   int whole;                  // every row sees every token
@@ -84,12 +86,14 @@ struct Part {
 struct Shared {
   CursorScratch cursor;
   uint64_t plan_full[kPlans], plan_free[kPlans], part_full[kParts], part_free[kParts];
-  uint64_t k_full[kCodeStages], v_full[2], s_full[2], p_ready[2], pv_done[2], q_ready, last, both[4];
+  uint64_t k_full[kCodeStages], k_free[kCodeStages], c_full[kCodeStages], c_free[kCodeStages];  // keys, codes of values
+  uint64_t v_full[2], s_full[2], p_ready[2], pv_done[2], q_ready, last, both[4];
   float exchange[2][kRows][3];  // between the two threads of a row
   TilePlan plan[kPlans];
   Part part[kParts];
   uint32_t tmem;
   int gave_up;
+  int fetched;  // tiles that copies were issued for
 };
 
 // Eight codes as fp16.
@@ -169,12 +173,14 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
         TilePlan& plan = sh.plan[it % kPlans];
         if (it >= kPlans && !warp_wait(sh, sh.plan_free[it % kPlans], it / kPlans - 1)) return false;
         if (mine == i) {
-          plan.base[step] = there ? kv_offset(w, page, p.h, token & page_mask) : -1;
+          plan.page[step] = page;
+          plan.slot[step] = token & page_mask;
           plan.token[step] = token;
           plan.count[step] = there ? min(kStep, steps.end - token) : 0;
           plan.k_scale[step] = k_scale;
           plan.v_log2[step] = v_log2;
           if (step == 0) {
+            plan.head = p.h;
             plan.whole = fulls == 0xffu;
             plan.first = t0 + i == 0;
             plan.last = t0 + i + 1 == p.count;
@@ -188,67 +194,70 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
   return true;
 }
 
-// ---- loading ----
+// ---- codes ----
 
+// Two copies for each step that has tokens, a lane to a step.
 template <int DP>
-__device__ bool load_role(const AttentionParams& a, const int tiles, Shared& sh, uint8_t* k_tiles, uint8_t* v_tiles,
-                          uint8_t* codes) {
+__device__ bool fetch_role(const CUtensorMap* keys, const CUtensorMap* values, const int tiles, Shared& sh, uint32_t k_tiles, uint32_t codes) {
   using T = Tiles<DP>;
-  constexpr int kChunks = DP / 16;                        // of a token
-  constexpr int kPer = kLoadThreads / kChunks;            // tokens of a pass
-  constexpr int NI = kTokens / kPer;                      // passes
-  const KvView& w = a.w;
-  const int tid = threadIdx.x - 32 * kSoftmaxWarps;
-  const int t0 = tid / kChunks, ch = tid % kChunks;
-  const bool in_dim = ch * 16 < w.dim;
-  const int64_t within = (t0 % kStep) * w.token_stride + ch * 16;  // kPer is a multiple of a step
-  // Asks for a tile's codes.  Keys go straight to where the product reads them (kPer is a multiple of 8: a thread's
-  // rows are swizzled alike); a thread's value codes lie side by side, only it reads them again.
-  const uint32_t key_at = tc::smem_address(k_tiles) + t0 * 128 + ((ch ^ (t0 & 7)) << 4);
-  uint8_t* const mine = codes + tid * 16;
-  const uint32_t code_at = tc::smem_address(mine);
-  const auto ask = [&](int it) {
+  const int lane = threadIdx.x & 31;
+  for (int it = 0; it < tiles; ++it) {
     const TilePlan& plan = sh.plan[it % kPlans];
+    const int stage = it % kCodeStages;
     if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans)) return false;
-    const uint32_t stage = static_cast<uint32_t>(it % kCodeStages);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int s = (t0 + i * kPer) / kStep;
-      const bool live = t0 % kStep < plan.count[s] && in_dim;
-      const int64_t from = live ? plan.base[s] + within : 0;
-      const int size = live ? 16 : 0;  // zeros for the rest
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(key_at + stage * T::kKeyBytes + i * kPer * 128),
-                   "l"(w.c.k + from), "r"(size) : "memory");
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(code_at + stage * T::kCodeBytes + i * kLoadThreads * 16),
-                   "l"(w.c.v + from), "r"(size) : "memory");
+    if (it >= kCodeStages && (!warp_wait(sh, sh.k_free[stage], it / kCodeStages - 1) || !warp_wait(sh, sh.c_free[stage], it / kCodeStages - 1)))
+      return false;
+    const bool live = lane < kTileSteps && plan.count[lane] > 0;
+    const int steps = __popc(__ballot_sync(0xffffffffu, live));
+    const uint32_t k_bar = tc::smem_address(&sh.k_full[stage]), c_bar = tc::smem_address(&sh.c_full[stage]);
+    if (lane == 0) {
+      tc::barrier_expect(k_bar, steps * (kStep * 128));
+      tc::barrier_expect(c_bar, steps * (kStep * DP));
+    }
+    if (lane == 0) sh.fetched = it + 1;
+    __syncwarp();
+    if (live) {
+      tc::copy_box(k_tiles + stage * T::kKeyBytes + lane * (kStep * 128), keys, 0, plan.slot[lane], plan.head, plan.page[lane], k_bar);
+      tc::copy_box(codes + stage * T::kCodeBytes + lane * (kStep * DP), values, 0, plan.slot[lane], plan.head, plan.page[lane], c_bar);
     }
     warp_arrive(sh.plan_free[it % kPlans]);
-    return true;
-  };
-  // A chunk of values becomes two of fp16, in rows of 64 dims, swizzled; lanes of the second block of dims do its
-  // halves the other way round (they write other banks then).
+  }
+  return true;
+}
+
+// A chunk of 16 codes becomes two of fp16, in rows of 64 dims, swizzled; lanes of the second block of dims do its halves
+// the other way round (they write other banks then).  What is not a token in sight becomes 0, whatever its bytes.
+template <int DP>
+__device__ bool value_role(const int tiles, Shared& sh, uint8_t* v_tiles, const uint8_t* codes) {
+  using T = Tiles<DP>;
+  constexpr int kChunks = DP / 16;                        // of a token
+  constexpr int kPer = kValueThreads / kChunks;           // tokens of a pass, 16 or 32
+  constexpr int NI = kTokens / kPer;                      // passes
+  const int tid = threadIdx.x - 32 * kSoftmaxWarps;
+  const int t0 = tid / kChunks, ch = tid % kChunks;
   const int turn = ch >> 2 & 1;
   const int to = (ch >> 2) * T::kBlockBytes + t0 * 128;
   const int half0 = to + (((2 * (ch & 3) + turn) ^ (t0 & 7)) << 4), half1 = to + (((2 * (ch & 3) + 1 - turn) ^ (t0 & 7)) << 4);
-  for (int i = 0; i < kCodeStages - 1; ++i) {
-    if (i < tiles && !ask(i)) return false;
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  bool ok = true;
 #pragma unroll 1
-  for (int it = 0; ok && it < tiles; ++it) {
-    const int st = it & 1;
-    asm volatile("cp.async.wait_group %0;" ::"n"(kCodeStages - 2) : "memory");
-    tc::publish_shared();
-    warp_arrive(sh.k_full[it % kCodeStages]);
-    ok = it < 2 || warp_wait(sh, sh.pv_done[st], (it >> 1) - 1);
+  for (int it = 0; it < tiles; ++it) {
+    const int st = it & 1, stage = it % kCodeStages;
+    const TilePlan& plan = sh.plan[it % kPlans];
+    if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans) || !warp_wait(sh, sh.c_full[stage], it / kCodeStages)) return false;
+    const uint8_t* from = codes + stage * T::kCodeBytes + t0 * DP + ch * 16;
     uint2 c[NI][2];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const uint8_t* from = mine + (it % kCodeStages) * T::kCodeBytes + i * kLoadThreads * 16;
-      c[i][0] = *reinterpret_cast<const uint2*>(from + 8 * turn);
-      c[i][1] = *reinterpret_cast<const uint2*>(from + 8 - 8 * turn);
+      c[i][0] = *reinterpret_cast<const uint2*>(from + i * kPer * DP + 8 * turn);
+      c[i][1] = *reinterpret_cast<const uint2*>(from + i * kPer * DP + 8 - 8 * turn);
     }
+    if (!plan.whole) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (t0 % kStep >= plan.count[(t0 + i * kPer) / kStep]) c[i][0] = c[i][1] = make_uint2(0, 0);
+    }
+    warp_arrive(sh.plan_free[it % kPlans]);
+    warp_arrive(sh.c_free[stage]);
+    if (it >= 2 && !warp_wait(sh, sh.pv_done[st], (it >> 1) - 1)) return false;
     uint8_t* row = v_tiles + st * T::kValueBytes;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -257,13 +266,8 @@ __device__ bool load_role(const AttentionParams& a, const int tiles, Shared& sh,
     }
     tc::publish_shared();
     warp_arrive(sh.v_full[st]);
-    // the next tile to ask for takes the stage of tile it - 1, whose keys the product must have read
-    if (ok && it + kCodeStages - 1 < tiles)
-      ok = (it == 0 || warp_wait(sh, sh.s_full[st ^ 1], (it - 1) >> 1)) && ask(it + kCodeStages - 1);
-    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  return ok;
+  return true;
 }
 
 // ---- products ----
@@ -309,6 +313,7 @@ __device__ bool product_role(const int tiles, Shared& sh, uint32_t q_tiles, uint
                          tc::tile_descriptor(k_tiles + static_cast<uint32_t>(it % kCodeStages) * T::kKeyBytes + (k >> 1) * 32, 16, 1024),
                          kScores, k > 0);
       tc::products_arrive(tc::smem_address(&sh.s_full[st]));
+      tc::products_arrive(tc::smem_address(&sh.k_free[it % kCodeStages]));
     }
     __syncwarp();
     if (!first && !weigh(it - 1, in_part <= 2)) return false;
@@ -643,7 +648,8 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(AttentionParams a) {
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(AttentionParams a, const __grid_constant__ CUtensorMap keys,
+                                                                              const __grid_constant__ CUtensorMap values) {
   using T = Tiles<DP>;
   extern __shared__ uint8_t raw[];
   __shared__ Shared sh;
@@ -652,21 +658,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   uint8_t* v_tiles = tiles;
   uint8_t* q_tiles = tiles + 2 * T::kValueBytes;
   uint8_t* k_tiles = q_tiles + 2 * T::kQueryBytes;
+  uint8_t* codes = k_tiles + kCodeStages * T::kKeyBytes;
   const int warp = threadIdx.x >> 5, g = blockIdx.x;
   flag_sequences(a, g, gridDim.x, kThreads);
   if (threadIdx.x == 0) {
     a.joins[g].rows = 0;
     sh.gave_up = 0;
-    for (int i = 0; i < kCodeStages; ++i) tc::barrier_init(tc::smem_address(&sh.k_full[i]), kLoadWarps);
+    sh.fetched = 0;
+    tc::prefetch_map(&keys);
+    tc::prefetch_map(&values);
+    for (int i = 0; i < kCodeStages; ++i) {
+      tc::barrier_init(tc::smem_address(&sh.k_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.k_free[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.c_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.c_free[i]), kValueWarps);
+    }
     for (int i = 0; i < 2; ++i) {
-      tc::barrier_init(tc::smem_address(&sh.v_full[i]), kLoadWarps);
+      tc::barrier_init(tc::smem_address(&sh.v_full[i]), kValueWarps);
       tc::barrier_init(tc::smem_address(&sh.s_full[i]), 1);
       tc::barrier_init(tc::smem_address(&sh.p_ready[i]), kSoftmaxWarps / 2);
       tc::barrier_init(tc::smem_address(&sh.pv_done[i]), 1);
     }
     for (int i = 0; i < kPlans; ++i) {
       tc::barrier_init(tc::smem_address(&sh.plan_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.plan_free[i]), kLoadWarps + kSoftmaxWarps / 2 + 1);
+      tc::barrier_init(tc::smem_address(&sh.plan_free[i]), kValueWarps + kSoftmaxWarps / 2 + 2);
     }
     for (int i = 0; i < kParts; ++i) {
       tc::barrier_init(tc::smem_address(&sh.part_full[i]), 1);
@@ -688,20 +703,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   if (warp < kSoftmaxWarps) {
     tc::registers_up<kSoftmaxRegisters>();
     ok = softmax_role<DP>(a, tiles_here, sh, q_tiles, tmem, g);
-  } else if (warp < kSoftmaxWarps + kLoadWarps) {
-    tc::registers_down<kLoadRegisters>();
-    ok = load_role<DP>(a, tiles_here, sh, k_tiles, v_tiles, k_tiles + kCodeStages * T::kKeyBytes);
+  } else if (warp < kSoftmaxWarps + kValueWarps) {
+    tc::registers_down<kValueRegisters>();
+    ok = value_role<DP>(tiles_here, sh, v_tiles, codes);
   } else {
-    tc::registers_down<kProductRegisters>();
-    if (warp == kSoftmaxWarps + kLoadWarps) {
+    tc::registers_down<kOtherRegisters>();
+    if (warp == kSoftmaxWarps + kValueWarps) {
       ok = product_role<DP>(tiles_here, sh, tc::smem_address(q_tiles), tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
       // products in flight end before the memory that they use is given up
       int unused = 0;
       if (tc::elected()) tc::products_arrive(tc::smem_address(&sh.last));
       ok = tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused) && ok;
       __syncwarp();
-    } else if (warp == kSoftmaxWarps + kLoadWarps + 1) {
+    } else if (warp == kSoftmaxWarps + kValueWarps + 1) {
       ok = plan_role(a, c, sh);
+    } else if (warp == kSoftmaxWarps + kValueWarps + 2) {
+      ok = fetch_role<DP>(&keys, &values, tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(codes));
+      // and copies in flight: the last of each stage, which no other role may have waited for
+      int unused = 0;
+      for (int it = max(0, sh.fetched - kCodeStages); !ok && it < sh.fetched; ++it)
+        tc::barrier_wait(tc::smem_address(&sh.k_full[it % kCodeStages]), it / kCodeStages & 1, &unused),
+            tc::barrier_wait(tc::smem_address(&sh.c_full[it % kCodeStages]), it / kCodeStages & 1, &unused);
+      __syncwarp();
     }
   }
   if (!ok && (threadIdx.x & 31) == 0) kv_flag(a.w, min(c.b, a.w.batch - 1), SV_ROW_TIMEOUT);
@@ -709,6 +732,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   __syncthreads();
   tc::fence_after();
   if (warp == 0) tc::tmem_free(tmem, T::kColumns);
+}
+
+// The driver's encoder of tensor maps, looked up through the runtime (the library does not link the driver).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encoder() {
+  static const EncodeTiled found = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+        how != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return found;
+}
+
+// Boxes of `width` dims (zeros behind the last) of 16 tokens of one head and page.
+bool cache_map(CUtensorMap* map, const sv_kv_desc& d, const uint8_t* cache, int width, CUtensorMapSwizzle swizzle) {
+  const EncodeTiled encode = encoder();
+  if (!encode) return false;
+  const cuuint64_t size[4] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.page_size),
+                              static_cast<cuuint64_t>(d.kv_heads), static_cast<cuuint64_t>(d.num_pages)};
+  const cuuint64_t stride[3] = {static_cast<cuuint64_t>(d.token_stride), static_cast<cuuint64_t>(d.head_stride),
+                                static_cast<cuuint64_t>(d.page_stride)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(width), kStep, 1, 1}, step[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(cache), size, stride, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DP>
@@ -722,7 +775,11 @@ sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspa
   const int blocks = schedule_blocks(row_tiles * d.kv.batch * d.kv.kv_heads, tiles, kSMs);
   a.parts = static_cast<float*>(workspace);
   a.joins = reinterpret_cast<JoinRecord*>(a.parts + 2 * static_cast<int64_t>(kSMs) * T::kPart);
-  kernel<<<blocks, kThreads, T::kShared, stream>>>(a);
+  CUtensorMap keys, values;
+  if (!cache_map(&keys, d.kv, a.w.c.k, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !cache_map(&values, d.kv, a.w.c.v, DP, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return SV_ERR_UNSUPPORTED;
+  kernel<<<blocks, kThreads, T::kShared, stream>>>(a, keys, values);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   if (blocks == 1 || tiles == 1) return SV_OK;  // no item has parts

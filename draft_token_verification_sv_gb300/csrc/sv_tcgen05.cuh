@@ -2,6 +2,7 @@
 // barriers in shared memory with bounded waits.
 #pragma once
 
+#include <cuda.h>
 #include <stdint.h>
 
 namespace sv {
@@ -40,6 +41,21 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, vola
     }
   }
   return true;
+}
+
+// An arrival that also announces bytes which copies will bring.
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// A box of a tensor of four dimensions to shared memory; its bytes count at the barrier.
+__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // Writes of this thread to shared memory become visible to the tensor core.
