@@ -112,6 +112,10 @@ __device__ __forceinline__ uint32_t bits16(int base, int from, int to) {
   return ((1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
+// Weights of step k of a tile (8 columns) within its scores' 128: those of the first half take the place of that half's
+// first quarter, those of the second of the last, so that neither half's scores are lost with the other's weights.
+__device__ __forceinline__ constexpr int weight_column(int k) { return k < 4 ? 8 * k : 96 + 8 * (k - 4); }
+
 // Every lane waits (for the n-th phase of a barrier); the answer is the warp's.
 __device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, int n) {
   return __all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up));
@@ -287,7 +291,7 @@ __device__ bool product_role(const int tiles, Shared& sh, uint32_t q_tiles, uint
     if (tc::elected()) {
 #pragma unroll
       for (int k = 0; k < kTokens / 16; ++k)
-        tc::product_f16(tmem + T::kO + st * DP, tmem + T::kS + st * kTokens + k * 8,
+        tc::product_f16(tmem + T::kO + st * DP, tmem + T::kS + st * kTokens + weight_column(k),
                         tc::tile_descriptor(v_tiles + st * T::kValueBytes + k * 2048, T::kBlockBytes, 1024), kValues, !first || k > 0);
       tc::products_arrive(tc::smem_address(&sh.pv_done[st]));
     }
@@ -497,42 +501,13 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
     for (; it < end; it += 2) {
       const TilePlan& plan = sh.plan[it % kPlans];
       if (!wait(sh.plan_full[it % kPlans], it / kPlans) || !wait(sh.s_full[group], it >> 1)) return false;
-      float v_top = kNoScale;
-#pragma unroll
-      for (int i = 0; i < kTileSteps; ++i) v_top = fmaxf(v_top, plan.v_log2[i]);
-      // Twice over the scores, 64 at a time.  The loops stay rolled: the roles share the instruction cache.
-      const auto tile = [&](auto masked) {
-        constexpr bool M = decltype(masked)::value;
-        float top = -CUDART_INF_F;  // the tile's largest score in base 2
-#pragma unroll 1
-        for (int c = 0; c < kTileSteps; c += 4) {
-          uint32_t x0[32], x1[32];
-          tc::tmem_load32(scores + 16 * c, x0);
-          tc::tmem_load32(scores + 16 * c + 32, x1);
-          const uint32_t seen0 = M ? seen_tokens(a, plan, c, parents, ctx, token, pos) : 0;
-          const uint32_t seen1 = M ? seen_tokens(a, plan, c + 2, parents, ctx, token, pos) : 0;
-          const float* k = plan.k_scale + c;
-          tc::wait_loads(x0);
-          top = fmaxf(top, fmaxf(largest16<M>(&x0[0], seen0) * (factor * k[0]), largest16<M>(&x0[16], seen0 >> 16) * (factor * k[1])));
-          tc::wait_loads(x1);
-          top = fmaxf(top, fmaxf(largest16<M>(&x1[0], seen1) * (factor * k[2]), largest16<M>(&x1[16], seen1 >> 16) * (factor * k[3])));
-        }
-        if (it == begin) {
-          m = ceilf(top);
-          v_ref = v_top;
-        } else if (__any_sync(0xffffffffu, top > m + 7.0f || v_top > v_ref)) {
-          const float up = fmaxf(m, ceilf(top));
-          float fix = up == -CUDART_INF_F ? 1.0f : ex2(m - up);
-          l *= fix;
-          m = up;
-          if (v_top > v_ref) {
-            fix *= ex2(v_ref - v_top);
-            v_ref = v_top;
-          }
+      // O and, in a tile's second half, the weights of its first are multiplied by `fix`, a power of two
+      const auto rescale = [&](float fix, bool weights) {
+        uint32_t o[16];
+        if (it > begin) {
           if (!wait(sh.pv_done[group], (it >> 1) - 1)) return false;
 #pragma unroll 1
           for (int i = 0; i < DP; i += 16) {
-            uint32_t o[16];
             tc::tmem_load16(own_o + i, o);
             tc::wait_loads(o);
 #pragma unroll
@@ -540,28 +515,80 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
             tc::tmem_store(own_o + i, o);
           }
         }
-        // weights, in the place of the scores' first half, in units of their values' scales
-        const float base = kLift - (m == -CUDART_INF_F ? 0.0f : m);
+        if (weights) {
+          const uint32_t fix2 = pack_f16x2(fix, fix);
+          tc::wait_stores();
 #pragma unroll 1
-        for (int c = 0; c < kTileSteps; c += 4) {
-          uint32_t x0[32], x1[32], w[16];
-          tc::tmem_load32(scores + 16 * c, x0);
-          tc::tmem_load32(scores + 16 * c + 32, x1);
-          const uint32_t seen0 = M ? seen_tokens(a, plan, c, parents, ctx, token, pos) : 0;
-          const uint32_t seen1 = M ? seen_tokens(a, plan, c + 2, parents, ctx, token, pos) : 0;
-          const float* k = plan.k_scale + c;
-          const float* v = plan.v_log2 + c;
-          float u0 = fmaxf(v[0] - v_ref, -100.0f), u1 = fmaxf(v[1] - v_ref, -100.0f);
-          tc::wait_loads(x0);
-          float2 sums = weights32<M>(x0, seen0, factor * k[0], factor * k[1], base + u0, base + u1, w);
-          l += sums.x * ex2(-u0) + sums.y * ex2(-u1);
-          tc::wait_loads(x1);
-          tc::tmem_store(scores + 8 * c, w);
-          u0 = fmaxf(v[2] - v_ref, -100.0f);
-          u1 = fmaxf(v[3] - v_ref, -100.0f);
-          sums = weights32<M>(x1, seen1, factor * k[2], factor * k[3], base + u0, base + u1, w);
-          l += sums.x * ex2(-u0) + sums.y * ex2(-u1);
-          tc::tmem_store(scores + 8 * c + 16, w);
+          for (int i = 0; i < 32; i += 16) {
+            tc::tmem_load16(scores + i, o);
+            tc::wait_loads(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(fix2));
+            tc::tmem_store(scores + i, o);
+          }
+        }
+        return true;
+      };
+      float v_top = kNoScale;
+#pragma unroll
+      for (int i = 0; i < kTileSteps; ++i) v_top = fmaxf(v_top, plan.v_log2[i]);
+      if (v_top > v_ref) {  // the same for all threads
+        if (!rescale(v_ref == kNoScale ? 0.0f : ex2(v_ref - v_top), false)) return false;
+        v_ref = v_top;
+      }
+      // 64 scores at a time, once.  The loops stay rolled: the roles share the instruction cache.
+      const auto tile = [&](auto masked) {
+        constexpr bool M = decltype(masked)::value;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t seen0 = 0, seen1 = 0;
+          if (M) {
+            seen0 = seen_tokens(a, plan, 4 * h, parents, ctx, token, pos);
+            seen1 = seen_tokens(a, plan, 4 * h + 2, parents, ctx, token, pos);
+          }
+          const float* k = plan.k_scale + 4 * h;
+          const float* v = plan.v_log2 + 4 * h;
+          // against the maximum so far, unless there is none; raised, and gone over again, where weights get too large
+          bool raise = __any_sync(0xffffffffu, m == -CUDART_INF_F);
+#pragma unroll 1
+          for (bool sure = raise;; sure = true) {
+            uint32_t x0[32], x1[32];
+            if (raise) {
+              tc::tmem_load32(scores + 64 * h, x0);
+              tc::tmem_load32(scores + 64 * h + 32, x1);
+              tc::wait_loads(x0);
+              tc::wait_loads(x1);
+              float top = fmaxf(fmaxf(largest16<M>(&x0[0], seen0) * (factor * k[0]), largest16<M>(&x0[16], seen0 >> 16) * (factor * k[1])),
+                                fmaxf(largest16<M>(&x1[0], seen1) * (factor * k[2]), largest16<M>(&x1[16], seen1 >> 16) * (factor * k[3])));
+              top = fmaxf(m, ceilf(top));  // whole: what is scaled anew is scaled exactly (m where scores are not numbers)
+              const float fix = top == -CUDART_INF_F ? 1.0f : ex2(m - top);
+              m = top;
+              l *= fix;
+              if (!rescale(fix, h == 1)) return false;
+            }
+            tc::tmem_load32(scores + 64 * h, x0);
+            tc::tmem_load32(scores + 64 * h + 32, x1);
+            // in units of their values' scales
+            const float base = kLift - (m == -CUDART_INF_F ? 0.0f : m);
+            float u0 = fmaxf(v[0] - v_ref, -100.0f), u1 = fmaxf(v[1] - v_ref, -100.0f);
+            uint32_t w0[16], w1[16];
+            tc::wait_loads(x0);
+            float2 sums = weights32<M>(x0, seen0, factor * k[0], factor * k[1], base + u0, base + u1, w0);
+            float most = fmaxf(sums.x, sums.y), sum = sums.x * ex2(-u0) + sums.y * ex2(-u1);
+            u0 = fmaxf(v[2] - v_ref, -100.0f);
+            u1 = fmaxf(v[3] - v_ref, -100.0f);
+            tc::wait_loads(x1);
+            sums = weights32<M>(x1, seen1, factor * k[2], factor * k[3], base + u0, base + u1, w1);
+            most = fmaxf(most, fmaxf(sums.x, sums.y));
+            sum += sums.x * ex2(-u0) + sums.y * ex2(-u1);
+            raise = !sure && __any_sync(0xffffffffu, most > 32768.0f);
+            if (!raise) {
+              l += sum;
+              tc::tmem_store(scores + weight_column(4 * h), w0);
+              tc::tmem_store(scores + weight_column(4 * h) + 16, w1);
+              break;
+            }
+          }
         }
         return true;
       };
