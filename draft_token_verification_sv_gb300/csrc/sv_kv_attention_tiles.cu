@@ -1,15 +1,15 @@
 // Attention of many query rows for each kv head over the 8-bit cache: token
 // trees, long chains, stretches of a prompt.
 //
-// 128 query rows at a time against tiles of 128 tokens on the 5th-generation
-// tensor cores: S = Q K^T and O += P V, accumulators in tensor memory, where
-// the weights P take the place of the scores they come from.  One block per
-// SM, five roles:
+// 128 query rows at a time against tiles of 64 tokens on the 5th-generation
+// tensor cores: S = Q K^T and O += P V.  Accumulators and the left sides are
+// in tensor memory, where the weights P take the place of the scores they
+// come from.  One block per SM, five roles:
 //   1 warp plans: it walks the block's tiles and looks pages and scales up;
-//   1 warp fetches codes, a box of 16 tokens of a page to a copy, two tiles
-//     ahead: keys to where the products read them, swizzled;
+//   1 warp fetches codes, a box of 16 tokens of a page to a copy, up to
+//     eight tiles ahead: keys to where the products read them, swizzled;
 //   4 warps widen the values to fp16 (which holds them all);
-//   1 warp issues the products: S of tile t before P V of tile t - 1;
+//   1 warp issues the products: S of tile t before P V of tile t - 2;
 //   2 groups of 4 warps turn scores into weights, a row a thread, one group
 //     the even tiles and the other the odd ones, each with its own running
 //     maximum and its own O, which are joined where an item's part ends.
@@ -31,7 +31,7 @@ namespace sv {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kTileSteps = 8;
+constexpr int kTileSteps = 4;
 constexpr int kTokens = kStep * kTileSteps;
 // weights: warps 0-7; values: 8-11; products: 12; plan: 13; fetch: 14 (15 idle: registers move in fours of warps)
 constexpr int kSoftmaxWarps = 8, kValueWarps = 4;
@@ -42,24 +42,26 @@ static_assert(kSoftmaxWarps * kSoftmaxRegisters + kValueWarps * kValueRegisters 
               "registers of a block");
 constexpr float kLift = 8.0f;  // weights are 2^8 times what they stand for: fp16 then keeps 2^-22 of the largest
 
-constexpr int kCodeStages = 3;  // tiles of codes in shared memory
+constexpr int kCodeStages = 8;   // tiles of codes in shared memory,
+constexpr int kValueStages = 4;  // of widened values,
+constexpr int kScoreStages = 3;  // and of scores in tensor memory
+constexpr int kLag = 2;          // tiles that scores are formed ahead of the sums over values
 
 template <int DP> struct Tiles {
   static constexpr int kKeyBytes = kTokens * 128;          // a tile's keys: rows of 128 bytes (DP = 64 leaves half)
   static constexpr int kCodeBytes = kTokens * DP;          // its values' codes as they come,
   static constexpr int kValueBytes = kTokens * DP * 2;     // and in fp16,
   static constexpr int kBlockBytes = kTokens * 128;        // in blocks of 64 dims
-  static constexpr int kQueryBytes = kRows * 128;          // one of the two parts of the queries
-  static constexpr int kOperands = 2 * kValueBytes + 2 * kQueryBytes + kCodeStages * (kKeyBytes + kCodeBytes);
+  static constexpr int kOperands = kValueStages * kValueBytes + kCodeStages * (kKeyBytes + kCodeBytes);
   // 1 KB to find a 1024-byte boundary; more than half of an SM's shared memory keeps it to one block
   static constexpr int kShared = (kOperands > 118 * 1024 ? kOperands : 118 * 1024) + 1024;
-  // tensor memory, in columns: two O, two tiles of scores
-  static constexpr int kO = 0, kS = 2 * DP;
+  // tensor memory, in columns: two O, both parts of Q, three tiles of scores
+  static constexpr int kO = 0, kQ = 2 * DP, kS = kQ + DP / 2;
   static constexpr int kColumns = 512;
   static constexpr int kPart = kRows * (DP + 2);
 };
 
-constexpr int kPlans = 8;  // tiles that may be planned ahead
+constexpr int kPlans = 16;  // tiles that may be planned ahead
 constexpr int kParts = 4;  // parts of items that may be
 constexpr float kNoScale = -1000.0f;
 
@@ -72,7 +74,6 @@ struct TilePlan {
   float k_scale[kTileSteps];
   float v_log2[kTileSteps];   // log2 of the values' scale, kNoScale for none
   int whole;                  // every row sees every token
-  int first, last;            // of its part
 };
 
 // And of an item's part that the block works on.
@@ -86,8 +87,8 @@ struct Part {
 struct Shared {
   CursorScratch cursor;
   uint64_t plan_full[kPlans], plan_free[kPlans], part_full[kParts], part_free[kParts];
-  uint64_t k_full[kCodeStages], k_free[kCodeStages], c_full[kCodeStages], c_free[kCodeStages];  // keys, codes of values
-  uint64_t v_full[2], s_full[2], p_ready[2], pv_done[2], q_ready, last, both[4];
+  uint64_t codes_full[kCodeStages], codes_free[kCodeStages];
+  uint64_t pv_ready[kValueStages], pv_done[kValueStages], s_full[kScoreStages], q_ready, last, both[4];
   float exchange[2][kRows][3];  // between the two threads of a row
   TilePlan plan[kPlans];
   Part part[kParts];
@@ -112,10 +113,6 @@ __device__ __forceinline__ uint32_t bits16(int base, int from, int to) {
   return ((1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
-// Weights of step k of a tile (8 columns) within its scores' 128: those of the first half take the place of that half's
-// first quarter, those of the second of the last, so that neither half's scores are lost with the other's weights.
-__device__ __forceinline__ constexpr int weight_column(int k) { return k < 4 ? 8 * k : 96 + 8 * (k - 4); }
-
 // Every lane waits (for the n-th phase of a barrier); the answer is the warp's.
 __device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, int n) {
   return __all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up));
@@ -127,7 +124,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar) {
 
 // ---- plans ----
 
-// Four tiles at a time, a lane to a step: page ids, then scales.
+// Eight tiles at a time, a lane to a step: page ids, then scales.
 __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
   const KvView& w = a.w;
   const int lane = threadIdx.x & 31, mine = lane / kTileSteps, step = lane % kTileSteps;
@@ -168,7 +165,7 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
       }
       const bool full = there && token + kStep <= all &&
                         (a.window == 0 || far - token < a.window || token + kStep <= a.sinks);
-      const unsigned fulls = __ballot_sync(0xffffffffu, full) >> (mine * kTileSteps) & 0xffu;
+      const unsigned fulls = __ballot_sync(0xffffffffu, full) >> (mine * kTileSteps) & ((1u << kTileSteps) - 1u);
       const uint32_t bits = __float_as_uint(v_scale);
       const float v_log2 = !(v_scale > 0.0f) ? kNoScale
                            : (bits & 0x7fffffu) == 0 && bits >= 0x00800000u ? static_cast<float>(static_cast<int>(bits >> 23) - 127)
@@ -185,9 +182,7 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
           plan.v_log2[step] = v_log2;
           if (step == 0) {
             plan.head = p.h;
-            plan.whole = fulls == 0xffu;
-            plan.first = t0 + i == 0;
-            plan.last = t0 + i + 1 == p.count;
+            plan.whole = fulls == (1u << kTileSteps) - 1u;
           }
         }
         warp_arrive(sh.plan_full[it % kPlans]);
@@ -200,31 +195,31 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
 
 // ---- codes ----
 
-// Two copies for each step that has tokens, a lane to a step.
+// Two copies for each step that has tokens, a lane to a copy.
 template <int DP>
 __device__ bool fetch_role(const CUtensorMap* keys, const CUtensorMap* values, const int tiles, Shared& sh, uint32_t k_tiles, uint32_t codes) {
   using T = Tiles<DP>;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, step = lane % kTileSteps;
+  const bool key = lane < kTileSteps;
+  const CUtensorMap* map = key ? keys : values;
+  const uint32_t to = key ? k_tiles + step * (kStep * 128) : codes + step * (kStep * DP);
+  const int stride = key ? T::kKeyBytes : T::kCodeBytes;
   for (int it = 0; it < tiles; ++it) {
     const TilePlan& plan = sh.plan[it % kPlans];
     const int stage = it % kCodeStages;
     if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans)) return false;
-    if (it >= kCodeStages && (!warp_wait(sh, sh.k_free[stage], it / kCodeStages - 1) || !warp_wait(sh, sh.c_free[stage], it / kCodeStages - 1)))
-      return false;
-    const bool live = lane < kTileSteps && plan.count[lane] > 0;
-    const int steps = __popc(__ballot_sync(0xffffffffu, live));
-    const uint32_t k_bar = tc::smem_address(&sh.k_full[stage]), c_bar = tc::smem_address(&sh.c_full[stage]);
-    if (lane == 0) {
-      tc::barrier_expect(k_bar, steps * (kStep * 128));
-      tc::barrier_expect(c_bar, steps * (kStep * DP));
-    }
-    if (lane == 0) sh.fetched = it + 1;
-    __syncwarp();
-    if (live) {
-      tc::copy_box(k_tiles + stage * T::kKeyBytes + lane * (kStep * 128), keys, 0, plan.slot[lane], plan.head, plan.page[lane], k_bar);
-      tc::copy_box(codes + stage * T::kCodeBytes + lane * (kStep * DP), values, 0, plan.slot[lane], plan.head, plan.page[lane], c_bar);
-    }
+    const bool live = lane < 2 * kTileSteps && plan.count[step] > 0;
+    const int slot = plan.slot[step], page = plan.page[step], head = plan.head;
+    const int copies = __popc(__ballot_sync(0xffffffffu, live));
     warp_arrive(sh.plan_free[it % kPlans]);
+    if (it >= kCodeStages && !warp_wait(sh, sh.codes_free[stage], it / kCodeStages - 1)) return false;
+    const uint32_t bar = tc::smem_address(&sh.codes_full[stage]);
+    if (lane == 0) {
+      tc::barrier_expect(bar, copies / 2 * (kStep * (128 + DP)));
+      sh.fetched = it + 1;
+    }
+    __syncwarp();
+    if (live) tc::copy_box(to + stage * stride, map, 0, slot, head, page, bar);
   }
   return true;
 }
@@ -244,9 +239,9 @@ __device__ bool value_role(const int tiles, Shared& sh, uint8_t* v_tiles, const 
   const int half0 = to + (((2 * (ch & 3) + turn) ^ (t0 & 7)) << 4), half1 = to + (((2 * (ch & 3) + 1 - turn) ^ (t0 & 7)) << 4);
 #pragma unroll 1
   for (int it = 0; it < tiles; ++it) {
-    const int st = it & 1, stage = it % kCodeStages;
+    const int st = it % kValueStages, stage = it % kCodeStages;
     const TilePlan& plan = sh.plan[it % kPlans];
-    if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans) || !warp_wait(sh, sh.c_full[stage], it / kCodeStages)) return false;
+    if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans) || !warp_wait(sh, sh.codes_full[stage], it / kCodeStages)) return false;
     const uint8_t* from = codes + stage * T::kCodeBytes + t0 * DP + ch * 16;
     uint2 c[NI][2];
 #pragma unroll
@@ -260,8 +255,11 @@ __device__ bool value_role(const int tiles, Shared& sh, uint8_t* v_tiles, const 
         if (t0 % kStep >= plan.count[(t0 + i * kPer) / kStep]) c[i][0] = c[i][1] = make_uint2(0, 0);
     }
     warp_arrive(sh.plan_free[it % kPlans]);
-    warp_arrive(sh.c_free[stage]);
-    if (it >= 2 && !warp_wait(sh, sh.pv_done[st], (it >> 1) - 1)) return false;
+    // the products of tile it - 4, after which its keys' and codes' place is free too
+    if (it >= kValueStages) {
+      if (!warp_wait(sh, sh.pv_done[st], it / kValueStages - 1)) return false;
+      warp_arrive(sh.codes_free[(it - kValueStages) % kCodeStages]);
+    }
     uint8_t* row = v_tiles + st * T::kValueBytes;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -269,60 +267,51 @@ __device__ bool value_role(const int tiles, Shared& sh, uint8_t* v_tiles, const 
       *reinterpret_cast<uint4*>(row + half1 + i * kPer * 128) = widen(c[i][1]);
     }
     tc::publish_shared();
-    warp_arrive(sh.v_full[st]);
+    warp_arrive(sh.pv_ready[st]);
   }
   return true;
 }
 
 // ---- products ----
 
+// One thread (elected of its warp): what it waits for delays the products, so it waits as little as it can.
 template <int DP>
-__device__ bool product_role(const int tiles, Shared& sh, uint32_t q_tiles, uint32_t k_tiles, uint32_t v_tiles, uint32_t tmem) {
+__device__ bool product_role(const int tiles, Shared& sh, uint32_t k_tiles, uint32_t v_tiles, uint32_t tmem) {
   using T = Tiles<DP>;
   constexpr uint32_t kScores = tc::product_kind(kTokens, false), kValues = tc::product_kind(DP, true);
   const auto wait = [&](uint64_t& bar, int n) {
-    const bool ok = warp_wait(sh, bar, n);
+    const bool ok = tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up);
     tc::fence_after();
     return ok;
   };
   const auto weigh = [&](int it, bool first) {  // O (+)= P V of tile it, its group's first of the part
-    const int st = it & 1;
-    if (!wait(sh.v_full[st], it >> 1) || !wait(sh.p_ready[st], it >> 1)) return false;
-    if (tc::elected()) {
+    const int v = it % kValueStages;
+    if (!wait(sh.pv_ready[v], it / kValueStages)) return false;
 #pragma unroll
-      for (int k = 0; k < kTokens / 16; ++k)
-        tc::product_f16(tmem + T::kO + st * DP, tmem + T::kS + st * kTokens + weight_column(k),
-                        tc::tile_descriptor(v_tiles + st * T::kValueBytes + k * 2048, T::kBlockBytes, 1024), kValues, !first || k > 0);
-      tc::products_arrive(tc::smem_address(&sh.pv_done[st]));
-    }
-    __syncwarp();
+    for (int k = 0; k < kTokens / 16; ++k)
+      tc::product_f16(tmem + T::kO + (it & 1) * DP, tmem + T::kS + it % kScoreStages * kTokens + k * 8,
+                      tc::tile_descriptor(v_tiles + v * T::kValueBytes + k * 2048, T::kBlockBytes, 1024), kValues, !first || k > 0);
+    tc::products_arrive(tc::smem_address(&sh.pv_done[v]));
     return true;
   };
-  int in_part = 0;  // tiles of the part before this one
-  int item = 0;
-  for (int it = 0; it < tiles; ++it) {
-    const int st = it & 1;
-    if (!wait(sh.plan_full[it % kPlans], it / kPlans)) return false;
-    const bool first = sh.plan[it % kPlans].first, last = sh.plan[it % kPlans].last;
-    warp_arrive(sh.plan_free[it % kPlans]);
-    if (first) {
-      in_part = 0;
-      if (!wait(sh.q_ready, item++)) return false;
-    }
-    if (!wait(sh.k_full[it % kCodeStages], it / kCodeStages)) return false;
-    if (tc::elected()) {
+  for (int it = 0, item = 0; it < tiles; ++item) {
+    if (!wait(sh.part_full[item % kParts], item / kParts)) return false;
+    const int count = sh.part[item % kParts].count;
+    tc::barrier_arrive(tc::smem_address(&sh.part_free[item % kParts]));
+    if (!wait(sh.q_ready, item)) return false;
+    for (int t = 0; t < count; ++t, ++it) {
+      const int s = it % kScoreStages, stage = it % kCodeStages;
+      if (!wait(sh.codes_full[stage], it / kCodeStages)) return false;
+      // (these scores' place was tile it - 3's weights', whose products were issued before)
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k)  // both parts of the queries with the same keys
-        tc::product_e4m3(tmem + T::kS + st * kTokens, tc::tile_descriptor(q_tiles + (k & 1) * T::kQueryBytes + (k >> 1) * 32, 16, 1024),
-                         tc::tile_descriptor(k_tiles + static_cast<uint32_t>(it % kCodeStages) * T::kKeyBytes + (k >> 1) * 32, 16, 1024),
-                         kScores, k > 0);
-      tc::products_arrive(tc::smem_address(&sh.s_full[st]));
-      tc::products_arrive(tc::smem_address(&sh.k_free[it % kCodeStages]));
+        tc::product_e4m3(tmem + T::kS + s * kTokens, tmem + T::kQ + (k & 1) * (DP / 4) + (k >> 1) * 8,
+                         tc::tile_descriptor(k_tiles + stage * T::kKeyBytes + (k >> 1) * 32, 16, 1024), kScores, k > 0);
+      tc::products_arrive(tc::smem_address(&sh.s_full[s]));
+      if (t >= kLag && !weigh(it - kLag, t - kLag < 2)) return false;
     }
-    __syncwarp();
-    if (!first && !weigh(it - 1, in_part <= 2)) return false;
-    if (last && !weigh(it, in_part < 2)) return false;
-    ++in_part;
+    for (int n = min(count, kLag); n > 0; --n)
+      if (!weigh(it - n, count - n < 2)) return false;
   }
   return true;
 }
@@ -393,12 +382,12 @@ __device__ __forceinline__ float2 weights32(const uint32_t (&x)[32], uint32_t se
 }
 
 template <int DP>
-__device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& sh, uint8_t* q_tiles, uint32_t tmem, int g) {
+__device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& sh, uint32_t tmem, int g) {
   using T = Tiles<DP>;
   constexpr int kDims = DP / 2;  // a thread's share of a row of queries and results
   const int r = threadIdx.x & (kRows - 1), group = threadIdx.x / kRows, quarter = (threadIdx.x >> 5) & 3;
   const uint32_t mine = tmem + (quarter << 21);  // the warp's 32 lanes
-  const uint32_t scores = mine + T::kS + group * kTokens, own_o = mine + T::kO + group * DP;
+  const uint32_t own_o = mine + T::kO + group * DP;
   const auto wait = [&](uint64_t& bar, int n) {
     const bool ok = warp_wait(sh, bar, n);
     tc::fence_after();
@@ -459,30 +448,24 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
       const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
       factor = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       if (exponent == 255) factor = CUDART_NAN_F;  // the row's scores are not numbers
-      uint8_t* to = q_tiles + r * 128;
+      uint32_t hi[kDims / 4], lo[kDims / 4];
 #pragma unroll
-      for (int i = 0; i < kDims / 16; ++i) {
-        uint32_t hi[4], lo[4];
+      for (int i = 0; i < kDims / 4; ++i) {
+        const uint4 c = raw[i >> 1];
+        const uint32_t words[2] = {i & 1 ? c.z : c.x, i & 1 ? c.w : c.y};
+        uint32_t h[2], rest[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 c = raw[2 * i + (k >> 1)];
-          const uint32_t words[2] = {k & 1 ? c.z : c.x, k & 1 ? c.w : c.y};
-          uint32_t h[2], rest[2];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float u = __uint_as_float(words[n] << 16) * up, v = __uint_as_float(words[n] & 0xffff0000u) * up;
-            h[n] = floats_to_e4m3x2(u, v);
-            const float2 held = f16x2_to_float2(e4m3x2_to_f16x2(h[n]));
-            rest[n] = floats_to_e4m3x2(u - held.x, v - held.y);
-          }
-          hi[k] = h[0] | h[1] << 16;
-          lo[k] = rest[0] | rest[1] << 16;
+        for (int n = 0; n < 2; ++n) {
+          const float u = __uint_as_float(words[n] << 16) * up, v = __uint_as_float(words[n] & 0xffff0000u) * up;
+          h[n] = floats_to_e4m3x2(u, v);
+          const float2 held = f16x2_to_float2(e4m3x2_to_f16x2(h[n]));
+          rest[n] = floats_to_e4m3x2(u - held.x, v - held.y);
         }
-        const int at = ((group * (kDims / 16) + i) ^ (r & 7)) << 4;
-        *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(to + T::kQueryBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        hi[i] = h[0] | h[1] << 16;
+        lo[i] = rest[0] | rest[1] << 16;
       }
-      tc::publish_shared();
+      tc::tmem_store(mine + T::kQ + group * (kDims / 4), hi);
+      tc::tmem_store(mine + T::kQ + DP / 4 + group * (kDims / 4), lo);
       arrive(sh.q_ready);
     }
     int pos = ctx + token;
@@ -500,32 +483,21 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
     const int begin = it;
     for (; it < end; it += 2) {
       const TilePlan& plan = sh.plan[it % kPlans];
-      if (!wait(sh.plan_full[it % kPlans], it / kPlans) || !wait(sh.s_full[group], it >> 1)) return false;
-      // O and, in a tile's second half, the weights of its first are multiplied by `fix`, a power of two
-      const auto rescale = [&](float fix, bool weights) {
+      const int stage = it % kScoreStages;
+      const uint32_t scores = mine + T::kS + stage * kTokens;
+      if (!wait(sh.plan_full[it % kPlans], it / kPlans) || !wait(sh.s_full[stage], it / kScoreStages)) return false;
+      // O is multiplied by `fix`, a power of two
+      const auto rescale = [&](float fix) {
+        if (it == begin) return true;
+        if (!wait(sh.pv_done[(it - 2) % kValueStages], (it - 2) / kValueStages)) return false;
         uint32_t o[16];
-        if (it > begin) {
-          if (!wait(sh.pv_done[group], (it >> 1) - 1)) return false;
 #pragma unroll 1
-          for (int i = 0; i < DP; i += 16) {
-            tc::tmem_load16(own_o + i, o);
-            tc::wait_loads(o);
+        for (int i = 0; i < DP; i += 16) {
+          tc::tmem_load16(own_o + i, o);
+          tc::wait_loads(o);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
-            tc::tmem_store(own_o + i, o);
-          }
-        }
-        if (weights) {
-          const uint32_t fix2 = pack_f16x2(fix, fix);
-          tc::wait_stores();
-#pragma unroll 1
-          for (int i = 0; i < 32; i += 16) {
-            tc::tmem_load16(scores + i, o);
-            tc::wait_loads(o);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(o[k]) : "r"(fix2));
-            tc::tmem_store(scores + i, o);
-          }
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
+          tc::tmem_store(own_o + i, o);
         }
         return true;
       };
@@ -533,67 +505,62 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
 #pragma unroll
       for (int i = 0; i < kTileSteps; ++i) v_top = fmaxf(v_top, plan.v_log2[i]);
       if (v_top > v_ref) {  // the same for all threads
-        if (!rescale(v_ref == kNoScale ? 0.0f : ex2(v_ref - v_top), false)) return false;
+        if (!rescale(v_ref == kNoScale ? 0.0f : ex2(v_ref - v_top))) return false;
         v_ref = v_top;
       }
-      // 64 scores at a time, once.  The loops stay rolled: the roles share the instruction cache.
       const auto tile = [&](auto masked) {
         constexpr bool M = decltype(masked)::value;
+        uint32_t seen0 = 0, seen1 = 0;
+        if (M) {
+          seen0 = seen_tokens(a, plan, 0, parents, ctx, token, pos);
+          seen1 = seen_tokens(a, plan, 2, parents, ctx, token, pos);
+        }
+        const float* k = plan.k_scale;
+        const float* v = plan.v_log2;
+        // against the maximum so far, unless there is none; raised, and gone over again, where weights get too large
+        bool raise = __any_sync(0xffffffffu, m == -CUDART_INF_F);
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t seen0 = 0, seen1 = 0;
-          if (M) {
-            seen0 = seen_tokens(a, plan, 4 * h, parents, ctx, token, pos);
-            seen1 = seen_tokens(a, plan, 4 * h + 2, parents, ctx, token, pos);
-          }
-          const float* k = plan.k_scale + 4 * h;
-          const float* v = plan.v_log2 + 4 * h;
-          // against the maximum so far, unless there is none; raised, and gone over again, where weights get too large
-          bool raise = __any_sync(0xffffffffu, m == -CUDART_INF_F);
-#pragma unroll 1
-          for (bool sure = raise;; sure = true) {
-            uint32_t x0[32], x1[32];
-            if (raise) {
-              tc::tmem_load32(scores + 64 * h, x0);
-              tc::tmem_load32(scores + 64 * h + 32, x1);
-              tc::wait_loads(x0);
-              tc::wait_loads(x1);
-              float top = fmaxf(fmaxf(largest16<M>(&x0[0], seen0) * (factor * k[0]), largest16<M>(&x0[16], seen0 >> 16) * (factor * k[1])),
-                                fmaxf(largest16<M>(&x1[0], seen1) * (factor * k[2]), largest16<M>(&x1[16], seen1 >> 16) * (factor * k[3])));
-              top = fmaxf(m, ceilf(top));  // whole: what is scaled anew is scaled exactly (m where scores are not numbers)
-              const float fix = top == -CUDART_INF_F ? 1.0f : ex2(m - top);
-              m = top;
-              l *= fix;
-              if (!rescale(fix, h == 1)) return false;
-            }
-            tc::tmem_load32(scores + 64 * h, x0);
-            tc::tmem_load32(scores + 64 * h + 32, x1);
-            // in units of their values' scales
-            const float base = kLift - (m == -CUDART_INF_F ? 0.0f : m);
-            float u0 = fmaxf(v[0] - v_ref, -100.0f), u1 = fmaxf(v[1] - v_ref, -100.0f);
-            uint32_t w0[16], w1[16];
+        for (bool sure = raise;; sure = true) {
+          uint32_t x0[32], x1[32];
+          if (raise) {
+            tc::tmem_load32(scores, x0);
+            tc::tmem_load32(scores + 32, x1);
             tc::wait_loads(x0);
-            float2 sums = weights32<M>(x0, seen0, factor * k[0], factor * k[1], base + u0, base + u1, w0);
-            float most = fmaxf(sums.x, sums.y), sum = sums.x * ex2(-u0) + sums.y * ex2(-u1);
-            u0 = fmaxf(v[2] - v_ref, -100.0f);
-            u1 = fmaxf(v[3] - v_ref, -100.0f);
             tc::wait_loads(x1);
-            sums = weights32<M>(x1, seen1, factor * k[2], factor * k[3], base + u0, base + u1, w1);
-            most = fmaxf(most, fmaxf(sums.x, sums.y));
-            sum += sums.x * ex2(-u0) + sums.y * ex2(-u1);
-            raise = !sure && __any_sync(0xffffffffu, most > 32768.0f);
-            if (!raise) {
-              l += sum;
-              tc::tmem_store(scores + weight_column(4 * h), w0);
-              tc::tmem_store(scores + weight_column(4 * h) + 16, w1);
-              break;
-            }
+            float top = fmaxf(fmaxf(largest16<M>(&x0[0], seen0) * (factor * k[0]), largest16<M>(&x0[16], seen0 >> 16) * (factor * k[1])),
+                              fmaxf(largest16<M>(&x1[0], seen1) * (factor * k[2]), largest16<M>(&x1[16], seen1 >> 16) * (factor * k[3])));
+            top = fmaxf(m, ceilf(top));  // whole: what is scaled anew is scaled exactly (m where scores are not numbers)
+            const float fix = top == -CUDART_INF_F ? 1.0f : ex2(m - top);
+            m = top;
+            l *= fix;
+            if (!rescale(fix)) return false;
+          }
+          tc::tmem_load32(scores, x0);
+          tc::tmem_load32(scores + 32, x1);
+          // in units of their values' scales
+          const float base = kLift - (m == -CUDART_INF_F ? 0.0f : m);
+          float u0 = fmaxf(v[0] - v_ref, -100.0f), u1 = fmaxf(v[1] - v_ref, -100.0f);
+          uint32_t w0[16], w1[16];
+          tc::wait_loads(x0);
+          float2 sums = weights32<M>(x0, seen0, factor * k[0], factor * k[1], base + u0, base + u1, w0);
+          float most = fmaxf(sums.x, sums.y), sum = sums.x * ex2(-u0) + sums.y * ex2(-u1);
+          u0 = fmaxf(v[2] - v_ref, -100.0f);
+          u1 = fmaxf(v[3] - v_ref, -100.0f);
+          tc::wait_loads(x1);
+          sums = weights32<M>(x1, seen1, factor * k[2], factor * k[3], base + u0, base + u1, w1);
+          most = fmaxf(most, fmaxf(sums.x, sums.y));
+          sum += sums.x * ex2(-u0) + sums.y * ex2(-u1);
+          raise = !sure && __any_sync(0xffffffffu, most > 32768.0f);
+          if (!raise) {
+            l += sum;
+            tc::tmem_store(scores, w0);
+            tc::tmem_store(scores + 16, w1);
+            return true;
           }
         }
-        return true;
       };
       if (!(plan.whole ? tile(std::false_type{}) : tile(std::true_type{}))) return false;
-      arrive(sh.p_ready[group]);
+      arrive(sh.pv_ready[it % kValueStages]);
       warp_arrive(sh.plan_free[it % kPlans]);
     }
 
@@ -606,9 +573,8 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
     const float* theirs = sh.exchange[group ^ 1][r];
     const float their_m = theirs[0], their_l = theirs[1], their_v = theirs[2];
     const bool own = begin < end, other = p.count > 1 || !own;
-    if ((own && !wait(sh.pv_done[group], (it >> 1) - 1)) ||
-        (other && !wait(sh.pv_done[group ^ 1], (end - 1 - (((end - 1) & 1) == group)) >> 1)))
-      return false;
+    // the last tiles' products: all before them are done then
+    if (!wait(sh.pv_done[(end - 1) % kValueStages], (end - 1) / kValueStages)) return false;
     if (!meet()) return false;  // (the exchange is free again)
     const float top = fmaxf(m, their_m);
     const float lift = 1.0f / 256.0f;
@@ -683,8 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   const uint32_t at = tc::smem_address(raw);
   uint8_t* tiles = raw + ((at + 1023u & ~1023u) - at);
   uint8_t* v_tiles = tiles;
-  uint8_t* q_tiles = tiles + 2 * T::kValueBytes;
-  uint8_t* k_tiles = q_tiles + 2 * T::kQueryBytes;
+  uint8_t* k_tiles = tiles + kValueStages * T::kValueBytes;
   uint8_t* codes = k_tiles + kCodeStages * T::kKeyBytes;
   const int warp = threadIdx.x >> 5, g = blockIdx.x;
   flag_sequences(a, g, gridDim.x, kThreads);
@@ -695,24 +660,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
     tc::prefetch_map(&keys);
     tc::prefetch_map(&values);
     for (int i = 0; i < kCodeStages; ++i) {
-      tc::barrier_init(tc::smem_address(&sh.k_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.k_free[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.c_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.c_free[i]), kValueWarps);
+      tc::barrier_init(tc::smem_address(&sh.codes_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.codes_free[i]), kValueWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::barrier_init(tc::smem_address(&sh.v_full[i]), kValueWarps);
-      tc::barrier_init(tc::smem_address(&sh.s_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.p_ready[i]), kSoftmaxWarps / 2);
+    for (int i = 0; i < kValueStages; ++i) {
+      tc::barrier_init(tc::smem_address(&sh.pv_ready[i]), kValueWarps + kSoftmaxWarps / 2);
       tc::barrier_init(tc::smem_address(&sh.pv_done[i]), 1);
     }
+    for (int i = 0; i < kScoreStages; ++i) tc::barrier_init(tc::smem_address(&sh.s_full[i]), 1);
     for (int i = 0; i < kPlans; ++i) {
       tc::barrier_init(tc::smem_address(&sh.plan_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.plan_free[i]), kValueWarps + kSoftmaxWarps / 2 + 2);
+      tc::barrier_init(tc::smem_address(&sh.plan_free[i]), kValueWarps + kSoftmaxWarps / 2 + 1);
     }
     for (int i = 0; i < kParts; ++i) {
       tc::barrier_init(tc::smem_address(&sh.part_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.part_free[i]), kSoftmaxWarps);
+      tc::barrier_init(tc::smem_address(&sh.part_free[i]), kSoftmaxWarps + 1);
     }
     for (int i = 0; i < 4; ++i) tc::barrier_init(tc::smem_address(&sh.both[i]), 2);
     tc::barrier_init(tc::smem_address(&sh.q_ready), kSoftmaxWarps);
@@ -729,19 +691,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   bool ok = true;
   if (warp < kSoftmaxWarps) {
     tc::registers_up<kSoftmaxRegisters>();
-    ok = softmax_role<DP>(a, tiles_here, sh, q_tiles, tmem, g);
+    ok = softmax_role<DP>(a, tiles_here, sh, tmem, g);
   } else if (warp < kSoftmaxWarps + kValueWarps) {
     tc::registers_down<kValueRegisters>();
     ok = value_role<DP>(tiles_here, sh, v_tiles, codes);
   } else {
     tc::registers_down<kOtherRegisters>();
     if (warp == kSoftmaxWarps + kValueWarps) {
-      ok = product_role<DP>(tiles_here, sh, tc::smem_address(q_tiles), tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
-      // products in flight end before the memory that they use is given up
-      int unused = 0;
-      if (tc::elected()) tc::products_arrive(tc::smem_address(&sh.last));
-      ok = tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused) && ok;
-      __syncwarp();
+      if (tc::elected()) {
+        ok = product_role<DP>(tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
+        // products in flight end before the memory that they use is given up
+        int unused = 0;
+        tc::products_arrive(tc::smem_address(&sh.last));
+        ok = tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused) && ok;
+      }
+      ok = __all_sync(0xffffffffu, ok);
     } else if (warp == kSoftmaxWarps + kValueWarps + 1) {
       ok = plan_role(a, c, sh);
     } else if (warp == kSoftmaxWarps + kValueWarps + 2) {
@@ -749,8 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
       // and copies in flight: the last of each stage, which no other role may have waited for
       int unused = 0;
       for (int it = max(0, sh.fetched - kCodeStages); !ok && it < sh.fetched; ++it)
-        tc::barrier_wait(tc::smem_address(&sh.k_full[it % kCodeStages]), it / kCodeStages & 1, &unused),
-            tc::barrier_wait(tc::smem_address(&sh.c_full[it % kCodeStages]), it / kCodeStages & 1, &unused);
+        tc::barrier_wait(tc::smem_address(&sh.codes_full[it % kCodeStages]), it / kCodeStages & 1, &unused);
       __syncwarp();
     }
   }

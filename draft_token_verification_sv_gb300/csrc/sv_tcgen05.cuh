@@ -161,6 +161,12 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16])
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // ---- products ----
 
 // One lane of a whole warp, chosen by the hardware: products issued under
@@ -185,7 +191,7 @@ __host__ __device__ constexpr uint32_t product_kind(int n, bool b_rows_inner) {
   return 1u << 4 | (b_rows_inner ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (128u / 16) << 24;
 }
 
-// d += (or =, unless `add`) a b, 128 x 16 fp16 and 128 x 32 e4m3; one thread.  A in tensor memory:
+// d += (or =, unless `add`) a b, with A (128 x 16 fp16, 128 x 32 e4m3) in tensor memory; one thread.
 __device__ __forceinline__ void product_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
@@ -193,12 +199,11 @@ __device__ __forceinline__ void product_f16(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
-// The same with A in shared memory.
-__device__ __forceinline__ void product_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void product_e4m3(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
 // The barrier gets an arrival when this thread's products so far are done.
