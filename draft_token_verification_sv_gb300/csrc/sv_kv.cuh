@@ -4,6 +4,8 @@
 
 #include "sv_internal.h"
 
+#include <type_traits>
+
 namespace sv {
 
 struct KvView {
@@ -99,5 +101,25 @@ __device__ __forceinline__ float kv_scale_for(float a) {
   const int e = static_cast<int>(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // biased exponent of s
   return __uint_as_float(static_cast<uint32_t>(max(e, 27)) << 23);
 }
+
+// Launches a kernel whose blocks may take their places while the launch
+// before it in the stream ends; wait_for_stream() comes before anything in
+// it that reads or writes memory.
+template <typename... Args>
+cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                         const std::remove_cv_t<Args>&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace sv

@@ -3,12 +3,14 @@
 //
 // O = sum_j 2^(s_j - m) v_j, one pass over the visible tokens with a running
 // maximum m for each row.  Both products run on the tensor cores
-// (m16n8k16): the 16 rows are the query heads that share a kv head (times the
-// new tokens), the codes are widened to fp16, which holds every e4m3 value,
+// (m16n8k16): the 16 rows (or two times 16) are the query heads that share a
+// kv head (times the new tokens), the codes are widened to fp16, which holds every e4m3 value,
 // and queries and weights are fp16 (a power of two for each row keeps queries
 // in range; fp32 queries and weights are the sum of two fp16).  Scales of K
 // and V are one factor for each page, on scores and weights.
 #include "sv_kv_schedule.cuh"
+
+#include <type_traits>
 
 namespace sv {
 
@@ -77,14 +79,17 @@ __device__ __forceinline__ void load_query16(const E* p, bool live, bool vec, fl
 
 // ----------------------------------------------------------------- shape ----
 
-constexpr int kRows = 16;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 
-// DP: head_dim rounded up to 64, 128 or 256 (the rest is zeros).
-template <int DP> struct Shape {
+// DP: head_dim rounded up to 64, 128 or 256 (the rest is zeros).  MT: tiles of
+// 16 rows.  What the rows take in registers (values' sums 16 DP, queries 8 DP,
+// for fp32 16 DP, floats of a warp) sets how many blocks an SM holds.
+template <typename E, int DP, int MT> struct Shape {
+  static constexpr bool kSplit = sizeof(E) == 4;  // queries and weights as two fp16 each
+  static constexpr int kRows = 16 * MT;
   static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 4 : 3;
-  static constexpr int kBlocksPerSm = DP == 64 ? 4 : DP == 128 ? 3 : 2;
+  static constexpr int kBlocksPerSm = MT == 1 && !kSplit ? (DP == 64 ? 4 : DP == 128 ? 3 : 2) : DP == 64 && !(kSplit && MT == 2) ? 3 : 2;
   static constexpr int kStageBytes = 2 * kStep * DP;          // keys, values
   static constexpr int kRing = kStages * (kStageBytes + 16);  // and their two scales
   static constexpr int kMerge = kRows * DP * 4;               // a warp's values in the join of a block's warps
@@ -111,14 +116,15 @@ __device__ __forceinline__ int value_chunk(int t, int c) {
 
 // ---------------------------------------------------------------- kernel ----
 
-// SPLIT: queries and weights as two fp16 each (fp32 inputs).
-template <typename E, int DP>
-__global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocksPerSm) kv_attention_kernel(AttentionParams a) {
-  using S = Shape<DP>;
-  constexpr bool SPLIT = sizeof(E) == 4;
+template <typename E, int DP, int MT>
+__global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_attention_kernel(AttentionParams a) {
+  using S = Shape<E, DP, MT>;
+  constexpr bool SPLIT = S::kSplit;
+  constexpr int kRows = S::kRows;
   constexpr int NQ = DP / 64;          // 16-byte chunks of a row that a lane reads
   constexpr int NT = DP / 8;           // value tiles of 8 dims
   constexpr int NV = DP == 64 ? 8 : 16;  // value tiles that one of a lane's pieces of a token feeds
+  constexpr int NC = kStep * DP / 16 / 32;  // chunks of keys (and of values) that a lane copies for a step
   extern __shared__ __align__(128) uint8_t shared[];
   __shared__ CursorScratch s_cursor;
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
@@ -129,7 +135,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocksPerSm) kv_attentio
   uint8_t* ring = shared + warp * S::kPerWarp;
   const uint32_t ring_at = smem_address(ring);
   const int page_mask = (1 << w.page_shift) - 1;
+  // what a lane copies of every step: chunk c0 of tokens tk0, tk0 + 512 / DP ..
+  const int tk0 = lane / (DP / 16), c0 = lane % (DP / 16);
+  const int64_t lane_at = tk0 * w.token_stride + c0 * 16, lane_step = (512 / DP) * w.token_stride;
 
+  wait_for_stream();
   flag_sequences(a, g, blocks, kThreads);
   Cursor c = find_cursor<kThreads, kRows, kWarps>(a, g, blocks, s_cursor);
   if (threadIdx.x == 0 && a.joins) a.joins[g].rows = 0;
@@ -144,83 +154,110 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocksPerSm) kv_attentio
     const int done = static_cast<int>(min(static_cast<long long>(tiles - c.tile), c.end - c.at));
     const int step0 = c.tile * kWarps + warp;                       // this warp's steps:
     const int step1 = min(steps.steps, (c.tile + done) * kWarps);   // step0, step0 + kWarps ..
+    const int64_t head_at = c.h * w.head_stride + lane_at;
 
-    // The stages in flight.  Bit of a stage in `bad`: its page is not there.
+    // The stages in flight.  Bit of a stage in `bad`: its page is not there.  Page ids are looked up ahead of their use.
     unsigned bad = 0;
     int fill = 0;  // the next stage to fill
-    const auto fetch = [&](int step) {
+    const auto look_up = [&](int step) {
+      if (step >= step1) return -1;
+      const int column = steps.token(step) >> w.page_shift;
+      return sv_in(column, w.max_pages) ? __ldg(w.c.page_table + c.b * w.table_stride + column) : -1;
+    };
+    const auto fetch = [&](int step, int page) {
       if (step < step1) {
         const int t0 = steps.token(step);
-        const int page = kv_page(w, c.b, t0 >> w.page_shift);
-        bad = (bad & ~(1u << fill)) | (page < 0 ? 1u << fill : 0u);
-        const int64_t o = kv_offset(w, max(page, 0), c.h, t0 & page_mask);
+        const bool there = page >= 0 && page < w.num_pages;
+        if (!there) {
+          kv_flag(w, c.b, SV_ROW_BAD_PAGE);
+          page = 0;
+        }
+        bad = (bad & ~(1u << fill)) | (there ? 0u : 1u << fill);
+        int64_t o = page * w.page_stride + (t0 & page_mask) * w.token_stride + head_at;
+        const int count = !there || c0 * 16 >= w.dim ? 0 : steps.end - t0;
         const uint32_t to = ring_at + fill * S::kStageBytes;
 #pragma unroll
-        for (int i = 0; i < kStep * DP / 16 / 32; ++i) {
-          const int t = (lane + 32 * i) / (DP / 16), ch = (lane + 32 * i) % (DP / 16);
-          const bool live = page >= 0 && t0 + t < steps.end && ch * 16 < w.dim;
-          const int64_t at = live ? o + t * w.token_stride + ch * 16 : 0;
-          copy16(to + key_chunk<DP>(t, ch) * 16, w.c.k + at, live);
-          copy16(to + kStep * DP + value_chunk<DP>(t, ch) * 16, w.c.v + at, live);
+        for (int i = 0; i < NC; ++i, o += lane_step) {
+          const int t = tk0 + i * (512 / DP);
+          copy16(to + key_chunk<DP>(t, c0) * 16, w.c.k + o, t < count);
+          copy16(to + kStep * DP + value_chunk<DP>(t, c0) * 16, w.c.v + o, t < count);
         }
         if (lane < 2)
           copy4(ring_at + S::kStages * S::kStageBytes + fill * 16 + lane * 4,
-                (lane ? w.c.v_scale : w.c.k_scale) + static_cast<int64_t>(max(page, 0)) * w.kv_heads + c.h, page >= 0);
+                (lane ? w.c.v_scale : w.c.k_scale) + static_cast<int64_t>(page) * w.kv_heads + c.h, there);
       }
       copy_commit();
       fill = fill + 1 == S::kStages ? 0 : fill + 1;
     };
+    int ahead;  // page id of the step to fetch next
+    {
+      int page[S::kStages - 1];
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) fetch(step0 + i * kWarps);
-
-    // Queries: row's and row + 8's, as the first product's left side.
-    uint32_t q[NQ][4][4], q_rest[SPLIT ? NQ : 1][4][4];
-    float factor[2];  // scores in base 2 = factor * key scale * product
-    int token[2], pos[2];
+      for (int i = 0; i < S::kStages - 1; ++i) page[i] = look_up(step0 + i * kWarps);
+      ahead = look_up(step0 + (S::kStages - 1) * kWarps);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = row + 8 * k;
-      const bool live = r < rows;
-      token[k] = (r0 + min(r, rows - 1)) / a.group;
-      const int head = c.h * a.group + (r0 + min(r, rows - 1)) % a.group;
-      const E* p = static_cast<const E*>(a.q) + (static_cast<int64_t>(s.row0) + token[k]) * a.q_row_stride + head * a.q_head_stride;
-      float x[NQ][16];
-      float top = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        load_query16<E>(p + 64 * i + 16 * col, live && 64 * i + 16 * col < w.dim, a.q_vec, x[i]);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[i][j]));
-      }
-      top = quad_max(top);
-      // the largest becomes 2^14 .. 2^15: fp16 keeps what is 2^-28 of it without loss for bf16 queries
-      const int e = top > 0.0f && top < CUDART_INF_F ? min(120, 141 - static_cast<int>(__float_as_uint(top) >> 23)) : 0;
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      factor[k] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-      for (int i = 0; i < NQ; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float u = x[i][4 * j + 2 * h] * up, v = x[i][4 * j + 2 * h + 1] * up;
-            q[i][j][2 * h + k] = floats_to_f16x2(u, v);
-            if (SPLIT) q_rest[i][j][2 * h + k] = rest_f16x2(u, v, q[i][j][2 * h + k]);
-          }
-      pos[k] = s.ctx + token[k];
-      if (parents) {
-        int depth = 0;
-        for (int u = tree_parent(parents, token[k]); u >= 0; u = tree_parent(parents, u)) ++depth;
-        pos[k] = s.ctx + depth;
-      }
+      for (int i = 0; i < S::kStages - 1; ++i) fetch(step0 + i * kWarps, page[i]);
     }
+
+    // Queries: of each 16 rows row's and row + 8's, as the first product's left side.
+    uint32_t q[MT][NQ][4][4], q_rest[SPLIT ? MT : 1][SPLIT ? NQ : 1][4][4];
+    float factor[MT][2];  // scores in base 2 = factor * key scale * product, factor >= 0
+    int token[MT][2], pos[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = 16 * mt + row + 8 * k;
+        const bool live = r < rows;
+        token[mt][k] = (r0 + min(r, rows - 1)) / a.group;
+        const int head = c.h * a.group + (r0 + min(r, rows - 1)) % a.group;
+        const E* p = static_cast<const E*>(a.q) + (static_cast<int64_t>(s.row0) + token[mt][k]) * a.q_row_stride + head * a.q_head_stride;
+        float x[NQ][16];
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          load_query16<E>(p + 64 * i + 16 * col, live && 64 * i + 16 * col < w.dim, a.q_vec, x[i]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[i][j]));
+        }
+        top = quad_max(top);
+        // the largest becomes 2^14 .. 2^15: fp16 keeps what is 2^-28 of it without loss for bf16 queries;
+        // a negative factor goes into the queries, so that larger products are larger scores
+        const int e = top > 0.0f && top < CUDART_INF_F ? min(120, 141 - static_cast<int>(__float_as_uint(top) >> 23)) : 0;
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
+        factor[mt][k] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float u = x[i][4 * j + 2 * h] * up, v = x[i][4 * j + 2 * h + 1] * up;
+              q[mt][i][j][2 * h + k] = floats_to_f16x2(u, v);
+              if constexpr (SPLIT) q_rest[mt][i][j][2 * h + k] = rest_f16x2(u, v, q[mt][i][j][2 * h + k]);
+            }
+        pos[mt][k] = s.ctx + token[mt][k];
+        if (parents) {
+          int depth = 0;
+          for (int u = tree_parent(parents, token[mt][k]); u >= 0; u = tree_parent(parents, u)) ++depth;
+          pos[mt][k] = s.ctx + depth;
+        }
+      }
     // tokens before `all` are in every row's past; `far` is the furthest position of a row
     const int all = parents ? s.ctx : s.ctx + i0 + 1, far = s.ctx + i1;
 
-    float o[NT][4] = {};
-    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.0f, 0.0f};
-    float v_ref = 0.0f, v_unit = 0.0f;  // weights are multiplied by v_scale * v_unit, v_unit = 2^12 / v_ref
+    float o[MT][NT][4] = {};
+    float m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        m[mt][k] = -CUDART_INF_F;
+        l[mt][k] = 0.0f;
+      }
+    float v_ref = 0.0f, v_unit = 0.0f;  // weights are multiplied by v_scale * v_unit, v_unit = 2^6 / v_ref
     int stage = 0;
+#pragma unroll 1
     for (int step = step0; step < step1; step += kWarps) {
       copy_wait<S::kStages - 2>();
       __syncwarp();
@@ -228,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocksPerSm) kv_attentio
       const uint8_t* v_at = k_at + kStep * DP;
       const float* sc = reinterpret_cast<const float*>(ring + S::kStages * S::kStageBytes + stage * 16);
       const float k_scale = sc[0], v_scale = sc[1];
-      // scores of 16 tokens: x[n][0..1] row's, [2..3] row + 8's, tokens 8 n + 2 col + {0, 1}
-      float x[2][4] = {};
+      // products of 16 tokens: x[n][0..1] row's, [2..3] row + 8's, tokens 8 n + 2 col + {0, 1}
+      float x[MT][2][4] = {};
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -239,68 +276,93 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocksPerSm) kv_attentio
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t b0 = e4m3x2_to_f16x2(word[j] & 0xffffu), b1 = e4m3x2_to_f16x2(word[j] >> 16);
-            mma(x[n], q[i][j][0], q[i][j][1], q[i][j][2], q[i][j][3], b0, b1);
-            if (SPLIT) mma(x[n], q_rest[i][j][0], q_rest[i][j][1], q_rest[i][j][2], q_rest[i][j][3], b0, b1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma(x[mt][n], q[mt][i][j][0], q[mt][i][j][1], q[mt][i][j][2], q[mt][i][j][3], b0, b1);
+              if constexpr (SPLIT)
+                mma(x[mt][n], q_rest[mt][i][j][0], q_rest[mt][i][j][1], q_rest[mt][i][j][2], q_rest[mt][i][j][3], b0, b1);
+            }
           }
         }
       const int t0 = steps.token(step);
-      const float f0 = factor[0] * k_scale, f1 = factor[1] * k_scale;
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        x[n][0] *= f0;
-        x[n][1] *= f0;
-        x[n][2] *= f1;
-        x[n][3] *= f1;
-      }
       const bool lost = (bad >> stage) & 1u;
       const bool whole = !lost && t0 + kStep <= all && (a.window == 0 || far - t0 < a.window || t0 + kStep <= a.sinks);
-      if (!whole) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int j = t0 + 8 * n + 2 * col + (k & 1);
-            if (lost || j >= steps.end || !sees(a, parents, s.ctx, token[k >> 1], pos[k >> 1], j)) x[n][k] = -CUDART_INF_F;
-          }
-      }
       if (v_scale > v_ref) {  // uniform: a page with larger values than any before
         const float fix = v_ref / v_scale;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[t][k] *= fix;
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[mt][t][k] *= fix;
         v_ref = v_scale;
-        v_unit = 4096.0f / v_scale;
-      }
-      float top[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) top[k] = quad_max(fmaxf(fmaxf(x[0][2 * k], x[0][2 * k + 1]), fmaxf(x[1][2 * k], x[1][2 * k + 1])));
-      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float up = fmaxf(m[k], top[k]);
-          const float fix = up == -CUDART_INF_F ? 1.0f : ex2(m[k] - up);
-          m[k] = up;
-          l[k] *= fix;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            o[t][2 * k] *= fix;
-            o[t][2 * k + 1] *= fix;
-          }
-        }
+        v_unit = 64.0f / v_scale;
       }
       const float unit = v_scale * v_unit;
-      uint32_t p[4], p_rest[4];
+      uint32_t p[MT][4], p_rest[SPLIT ? MT : 1][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int mt = 0; mt < MT; ++mt) {
+        unsigned seen = 0xffu;  // bit 4 n + k: x[n][k]
+        if (!whole) {
+          seen = 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float base = m[k] == -CUDART_INF_F ? 0.0f : m[k];
-          const float u = ex2(x[n][2 * k] - base), v = ex2(x[n][2 * k + 1] - base);
-          l[k] += u + v;
-          p[2 * n + k] = floats_to_f16x2(u * unit, v * unit);
-          if (SPLIT) p_rest[2 * n + k] = rest_f16x2(u * unit, v * unit, p[2 * n + k]);
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int j = t0 + 8 * n + 2 * col + (k & 1);
+              if (!lost && j < steps.end && sees(a, parents, s.ctx, token[mt][k >> 1], pos[mt][k >> 1], j)) seen |= 1u << (4 * n + k);
+            }
         }
+        // Weights against the maximum so far; where they sum to 2^7 and more (infinity where there is no maximum yet) it is
+        // raised and they are taken again.
+        const float f[2] = {factor[mt][0] * k_scale, factor[mt][1] * k_scale};
+        float e[2][4], sum[2];
+        const auto weigh = [&]() {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e[n][k] = ex2(fmaf(x[mt][n][k], f[k >> 1], -m[mt][k >> 1]));
+          if (!whole)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) e[n][k] = seen >> (4 * n + k) & 1u ? e[n][k] : 0.0f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) sum[k] = (e[0][2 * k] + e[0][2 * k + 1]) + (e[1][2 * k] + e[1][2 * k + 1]);
+        };
+        weigh();
+        if (__any_sync(0xffffffffu, sum[0] > 128.0f || sum[1] > 128.0f)) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (seen >> (4 * n + 2 * k + i) & 1u) top = fmaxf(top, x[mt][n][2 * k + i] * f[k]);
+            const float up = fmaxf(m[mt][k], quad_max(top));
+            const float fix = up == -CUDART_INF_F ? 1.0f : ex2(m[mt][k] - up);
+            m[mt][k] = up;
+            l[mt][k] *= fix;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              o[mt][t][2 * k] *= fix;
+              o[mt][t][2 * k + 1] *= fix;
+            }
+          }
+          weigh();
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) l[mt][k] += sum[k];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float u = e[n][2 * k] * unit, v = e[n][2 * k + 1] * unit;
+            p[mt][2 * n + k] = floats_to_f16x2(u, v);
+            if constexpr (SPLIT) p_rest[mt][2 * n + k] = rest_f16x2(u, v, p[mt][2 * n + k]);
+          }
+      }
       // values: a lane reads NV / 16 of the row of its four tokens, whose bytes i are dims of tile i
 #pragma unroll
       for (int h = 0; h < NT / NV; ++h) {
@@ -330,48 +392,56 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocksPerSm) kv_attentio
             for (int k = 0; k < 2; ++k) {
               const uint32_t b0 = e4m3x2_to_f16x2(k ? u >> 16 : u & 0xffffu), b1 = e4m3x2_to_f16x2(k ? v >> 16 : v & 0xffffu);
               const int t = h * NV + 4 * i + 2 * half + k;
-              mma(o[t], p[0], p[1], p[2], p[3], b0, b1);
-              if (SPLIT) mma(o[t], p_rest[0], p_rest[1], p_rest[2], p_rest[3], b0, b1);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma(o[mt][t], p[mt][0], p[mt][1], p[mt][2], p[mt][3], b0, b1);
+                if constexpr (SPLIT) mma(o[mt][t], p_rest[mt][0], p_rest[mt][1], p_rest[mt][2], p_rest[mt][3], b0, b1);
+              }
             }
           }
       }
       __syncwarp();
-      fetch(step + (S::kStages - 1) * kWarps);
+      fetch(step + (S::kStages - 1) * kWarps, ahead);
+      ahead = look_up(step + S::kStages * kWarps);
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
     copy_wait<0>();
 
     // The block's warps joined: maxima and sums, then values, in shared memory.
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      l[k] = quad_sum(l[k]);
-      if (col == 0) {
-        s_m[warp][row + 8 * k] = m[k];
-        s_l[warp][row + 8 * k] = l[k];
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l[mt][k] = quad_sum(l[mt][k]);
+        if (col == 0) {
+          s_m[warp][16 * mt + row + 8 * k] = m[mt][k];
+          s_l[warp][16 * mt + row + 8 * k] = l[mt][k];
+        }
       }
-    }
     __syncthreads();  // and every warp has read its ring
     float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = row + 8 * k;
-      float top = s_m[0][r];
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_m[i][r]);
-      const float fix = (m[k] == -CUDART_INF_F ? 0.0f : ex2(m[k] - top)) * v_ref * (1.0f / 4096.0f);
-      // a lane's dims of tiles h NV ..: 2 NV in a row, from h (8 NV) + 2 NV col
+      for (int k = 0; k < 2; ++k) {
+        const int r = 16 * mt + row + 8 * k;
+        float top = s_m[0][r];
 #pragma unroll
-      for (int h = 0; h < NT / NV; ++h)
+        for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_m[i][r]);
+        const float fix = (m[mt][k] == -CUDART_INF_F ? (l[mt][k] == 0.0f ? 0.0f : 1.0f) : ex2(m[mt][k] - top)) * v_ref * (1.0f / 64.0f);
+        // a lane's dims of tiles h NV ..: 2 NV in a row, from h (8 NV) + 2 NV col
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int h = 0; h < NT / NV; ++h)
 #pragma unroll
-          for (int i = 0; i < NV / 4; ++i) {
-            const int d4 = h * (2 * NV) + col * (NV / 2) + half * (NV / 4) + i;  // in fours
-            const int t = h * NV + 4 * i, e = 2 * k + half;
-            *reinterpret_cast<float4*>(mine + r * DP + 4 * (d4 ^ ((row & 1) << 2 | col))) =
-                make_float4(o[t][e] * fix, o[t + 1][e] * fix, o[t + 2][e] * fix, o[t + 3][e] * fix);
-          }
-    }
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = 0; i < NV / 4; ++i) {
+              const int d4 = h * (2 * NV) + col * (NV / 2) + half * (NV / 4) + i;  // in fours
+              const int t = h * NV + 4 * i, e = 2 * k + half;
+              *reinterpret_cast<float4*>(mine + r * DP + 4 * (d4 ^ ((row & 1) << 2 | col))) =
+                  make_float4(o[mt][t][e] * fix, o[mt][t + 1][e] * fix, o[mt][t + 2][e] * fix, o[mt][t + 3][e] * fix);
+            }
+      }
     __syncthreads();
     const bool complete = done == tiles;
     float* part = complete ? nullptr : a.parts + (2 * static_cast<int64_t>(g) + (c.tile == 0 ? 1 : 0)) * S::kPart;
@@ -406,40 +476,57 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kBlocksPerSm) kv_attentio
   }
 }
 
+template <int N> using Int = std::integral_constant<int, N>;
+
 int round_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-template <typename E, int DP>
+template <typename E, int DP, int MT>
 sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspace, cudaStream_t stream) {
-  using S = Shape<DP>;
+  using S = Shape<E, DP, MT>;
   static FuncAttrCache attr;
-  const auto kernel = kv_attention_kernel<E, DP>;
+  const auto kernel = kv_attention_kernel<E, DP, MT>;
   if (!attr.ensure(reinterpret_cast<const void*>(kernel), S::kShared, false)) return SV_ERR_CUDA;
-  const int64_t row_tiles = (static_cast<int64_t>(d.max_new) * a.group + kRows - 1) / kRows;
+  const int64_t row_tiles = (static_cast<int64_t>(d.max_new) * a.group + S::kRows - 1) / S::kRows;
   const int64_t tiles = (static_cast<int64_t>(d.kv.max_pages) * d.kv.page_size + kStep * kWarps - 1) / (kStep * kWarps);
   const int blocks = schedule_blocks(row_tiles * d.kv.batch * d.kv.kv_heads, tiles, S::kBlocks);
   a.parts = static_cast<float*>(workspace);
   a.joins = reinterpret_cast<JoinRecord*>(a.parts + 2 * static_cast<int64_t>(S::kBlocks) * S::kPart);
-  kernel<<<blocks, kThreads, S::kShared, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_early(kernel, dim3(blocks), dim3(kThreads), S::kShared, stream, a) != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   if (blocks == 1 || tiles == 1) return SV_OK;  // no item has parts
-  if (launch_join<E, DP, kRows>(a, blocks, stream) != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_join<E, DP, S::kRows>(a, blocks, stream) != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   return SV_OK;
 }
 
-template <int DP>
+template <typename E, int DP, int MT>
 size_t workspace_for() {
-  using S = Shape<DP>;
+  using S = Shape<E, DP, MT>;
   return S::kBlocks * (2 * S::kPart * sizeof(float) + sizeof(JoinRecord));
+}
+
+// Calls f with the kernel's template arguments as types: one tile of 16 rows
+// where a kv head has no more, two where it has (but not for fp32 queries of
+// more than 64 dims nor for more than 128 dims: their rows' registers would
+// spill).
+template <typename F>
+auto with_shape(const sv_kv_attention_desc& d, F f) {
+  const bool two = static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 16;
+  const int dp = round_dim(d.kv.head_dim);
+  if (d.dtype == SV_BF16) {
+    if (dp == 64) return two ? f(uint16_t{}, Int<64>{}, Int<2>{}) : f(uint16_t{}, Int<64>{}, Int<1>{});
+    if (dp == 128) return two ? f(uint16_t{}, Int<128>{}, Int<2>{}) : f(uint16_t{}, Int<128>{}, Int<1>{});
+    return f(uint16_t{}, Int<256>{}, Int<1>{});
+  }
+  if (dp == 64) return two ? f(float{}, Int<64>{}, Int<2>{}) : f(float{}, Int<64>{}, Int<1>{});
+  return dp == 128 ? f(float{}, Int<128>{}, Int<1>{}) : f(float{}, Int<256>{}, Int<1>{});
 }
 
 }  // namespace
 
 size_t kv_attention_workspace_bytes(const sv_kv_attention_desc& d) {
   if (kv_attention_takes_tiles(d)) return kv_attention_tiles_workspace(d);
-  const int dp = round_dim(d.kv.head_dim);
-  return align_up(dp == 64 ? workspace_for<64>() : dp == 128 ? workspace_for<128>() : workspace_for<256>(), 256);
+  return align_up(with_shape(d, [](auto e, auto dp, auto mt) { return workspace_for<decltype(e), dp.value, mt.value>(); }), 256);
 }
 
 sv_status kv_attention(const sv_kv_attention_desc& d, const void* q, const KvCache& c, const int32_t* ctx_lens,
@@ -461,12 +548,7 @@ sv_status kv_attention(const sv_kv_attention_desc& d, const void* q, const KvCac
                     aligned(out, d.out_row_stride, d.out_head_stride, 32),
                     nullptr, nullptr};
   if (kv_attention_takes_tiles(d)) return kv_attention_tiles(a, d, workspace, stream);
-  const int dp = round_dim(d.kv.head_dim);
-  if (d.dtype == SV_BF16)
-    return dp == 64 ? launch<uint16_t, 64>(a, d, workspace, stream)
-                    : dp == 128 ? launch<uint16_t, 128>(a, d, workspace, stream) : launch<uint16_t, 256>(a, d, workspace, stream);
-  return dp == 64 ? launch<float, 64>(a, d, workspace, stream)
-                  : dp == 128 ? launch<float, 128>(a, d, workspace, stream) : launch<float, 256>(a, d, workspace, stream);
+  return with_shape(d, [&](auto e, auto dp, auto mt) { return launch<decltype(e), dp.value, mt.value>(a, d, workspace, stream); });
 }
 
 }  // namespace sv

@@ -652,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   uint8_t* k_tiles = tiles + kValueStages * T::kValueBytes;
   uint8_t* codes = k_tiles + kCodeStages * T::kKeyBytes;
   const int warp = threadIdx.x >> 5, g = blockIdx.x;
+  wait_for_stream();
   flag_sequences(a, g, gridDim.x, kThreads);
   if (threadIdx.x == 0) {
     a.joins[g].rows = 0;
@@ -769,8 +770,7 @@ sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspa
   if (!cache_map(&keys, d.kv, a.w.c.k, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !cache_map(&values, d.kv, a.w.c.v, DP, CU_TENSOR_MAP_SWIZZLE_NONE))
     return SV_ERR_UNSUPPORTED;
-  kernel<<<blocks, kThreads, T::kShared, stream>>>(a, keys, values);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_early(kernel, dim3(blocks), dim3(kThreads), T::kShared, stream, a, keys, values) != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   if (blocks == 1 || tiles == 1) return SV_OK;  // no item has parts
   if (launch_join<uint16_t, DP, kRows>(a, blocks, stream) != cudaSuccess) return SV_ERR_CUDA;

@@ -282,7 +282,7 @@ __device__ __forceinline__ void store_result(const AttentionParams& a, int row0,
 // One block for each part that began an item: its rows from all parts, in order.
 template <typename E, int DP, int ROWS>
 __global__ void __launch_bounds__(128) kv_attention_join_kernel(AttentionParams a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  wait_for_stream();  // the parts are written
   const int g = blockIdx.x;
   const JoinRecord j = a.joins[g];
   constexpr int kPart = ROWS * (DP + 2);
@@ -309,19 +309,9 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(AttentionParams 
   }
 }
 
-// The second launch, which may begin its own start before the first ends.
 template <typename E, int DP, int ROWS>
 cudaError_t launch_join(const AttentionParams& a, int blocks, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, ROWS / 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute early[1];
-  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<E, DP, ROWS>, a);
+  return launch_early(kv_attention_join_kernel<E, DP, ROWS>, dim3(blocks, ROWS / 4), dim3(128), 0, stream, a);
 }
 
 // Blocks for a call that can have at most so many items of so many tiles.
