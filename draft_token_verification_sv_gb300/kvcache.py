@@ -10,6 +10,10 @@ kv_heads, head_dim] array transposed is as good) and ``k_scale``, ``v_scale``
 
 New tokens come as [B, n, ...] tensors (every sequence has n) or, with
 ``new_start`` [B + 1] int32 and ``max_new``, as [total, ...] rows.
+
+A call's checks and descriptors depend on the tensors' shapes, strides and
+types alone, so they are made once for each combination and kept (what a call
+costs on the host is most of a decoding step's small launches).
 """
 from __future__ import annotations
 
@@ -19,9 +23,13 @@ import functools
 import torch
 
 from . import _native as N
-from .verify import _code, _cuda, _i32, _p, _stream, workspace
+from .verify import _WORKSPACES, _code, workspace
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_KEPT = 4096  # combinations of shapes kept for each entry point
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda") -> dict:
@@ -35,75 +43,180 @@ def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, 
     return dict(k=codes(), v=codes(), k_scale=scales(), v_scale=scales())
 
 
-@functools.lru_cache(maxsize=1024)
-def _kv_desc(shape, stride, batch, columns, table_stride) -> N.KvDesc:
-    pages, heads, page, dim = shape
-    # a dimension of one entry is never stepped over: its stride may be anything
-    step = [s if n > 1 else -(-max(s, dim) // 16) * 16 for n, s in zip(shape[:3], stride)]
-    return N.KvDesc(batch, heads, dim, page, pages, columns, step[0], step[1], step[2], max(table_stride, columns))
+class _Meta(tuple):
+    """What the checks see of a tensor: (shape, strides, dtype, on a GPU)."""
+    __slots__ = ()
+    shape = property(lambda m: m[0])
+    strides = property(lambda m: m[1])
+    dtype = property(lambda m: m[2])
+    is_cuda = property(lambda m: m[3])
 
 
-def _cache(cache, page_table, lens, name) -> N.KvDesc:
-    k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
-    for t, n in ((k, "cache['k']"), (v, "cache['v']"), (ks, "cache['k_scale']"), (vs, "cache['v_scale']"),
-                 (page_table, "page_table"), (lens, name)):
-        _cuda(t, n)
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.is_cuda)
+
+
+def _see(meta, name) -> _Meta:
+    if meta is None:
+        return None
+    m = _Meta(meta)
+    if not m.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return m
+
+
+def _numel(shape) -> int:
+    n = 1
+    for x in shape:
+        n *= x
+    return n
+
+
+def _contiguous(m: _Meta) -> bool:
+    want = 1
+    for n, s in zip(reversed(m.shape), reversed(m.strides)):
+        if n != 1 and s != want and _numel(m.shape) > 0:
+            return False
+        want *= n
+    return True
+
+
+def _int32(meta, name, numel, what):
+    m = _see(meta, name)
+    if m is None:
+        return
+    if m.dtype != torch.int32 or not _contiguous(m):
+        raise ValueError(f"{name} must be a contiguous int32 tensor")
+    if _numel(m.shape) != numel:
+        raise ValueError(f"{name} must have {what}")
+
+
+def _kv_desc(k, v, ks, vs, table, lens, name) -> N.KvDesc:
+    k, v, ks, vs = _see(k, "cache['k']"), _see(v, "cache['v']"), _see(ks, "cache['k_scale']"), _see(vs, "cache['v_scale']")
+    table = _see(table, "page_table")
     if k.dtype not in _CODES or v.dtype not in _CODES:
         raise TypeError("cache codes must be float8_e4m3fn or uint8")
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+    if len(k.shape) != 4 or k.shape != v.shape or k.strides != v.strides or k.strides[3] != 1:
         raise ValueError("cache['k'] and cache['v'] must be [pages, kv_heads, page_size, head_dim] with the same "
                          "strides and a contiguous last dimension")
-    for t, n in ((ks, "cache['k_scale']"), (vs, "cache['v_scale']")):
-        if t.dtype != torch.float32 or t.shape != k.shape[:2] or not t.is_contiguous():
+    for m, n in ((ks, "cache['k_scale']"), (vs, "cache['v_scale']")):
+        if m.dtype != torch.float32 or m.shape != k.shape[:2] or not _contiguous(m):
             raise ValueError(f"{n} must be a contiguous float32 [pages, kv_heads] tensor")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 and page_table.shape[1] > 1:
+    if table.dtype != torch.int32 or len(table.shape) != 2 or table.strides[1] != 1 and table.shape[1] > 1:
         raise ValueError("page_table must be an int32 [B, pages] tensor with contiguous rows")
-    _i32(lens, name)
-    B, columns = page_table.shape
-    if lens.numel() != B:
-        raise ValueError(f"{name} must have one entry for each row of page_table")
-    return _kv_desc(k.shape, k.stride(), B, columns, page_table.stride(0) if B > 1 else columns)
+    B, columns = table.shape
+    _int32(lens, name, B, "one entry for each row of page_table")
+    pages, heads, page, dim = k.shape
+    # a dimension of one entry is never stepped over: its stride may be anything
+    step = [s if n > 1 else -(-max(s, dim) // 16) * 16 for n, s in zip(k.shape[:3], k.strides)]
+    return N.KvDesc(B, heads, dim, page, pages, columns, step[0], step[1], step[2],
+                    max(table.strides[0], columns) if B > 1 else columns)
 
 
-def _status(row_status, B):
-    _cuda(row_status, "row_status")
-    if row_status is not None and _i32(row_status, "row_status").numel() != B:
-        raise ValueError("row_status must have one entry for each sequence")
-    return _p(row_status)
-
-
-def _rows(t: torch.Tensor, name: str, B: int, ragged: bool):
+def _rows(m: _Meta, name: str, B: int, ragged: bool):
     """(rows, heads, dim, row stride, head stride) of [B, n, heads, dim] or [total, heads, dim]."""
-    if t.dim() != (3 if ragged else 4):
+    shape, strides = m.shape, m.strides
+    if len(shape) != (3 if ragged else 4):
         raise ValueError(f"{name} must be [total, heads, dim] with new_start, else [B, n, heads, dim]")
-    shape, stride = t.shape, t.stride()
     heads, dim = shape[-2:]
-    if stride[-1] != 1:
+    if strides[-1] != 1:
         raise ValueError(f"{name}: last dimension must be contiguous")
-    head_stride = stride[-2] if heads > 1 else dim
+    head_stride = strides[-2] if heads > 1 else dim
     if ragged:
-        return shape[0], heads, dim, stride[0] if shape[0] > 1 else max(dim, stride[0]), head_stride
+        return shape[0], heads, dim, strides[0] if shape[0] > 1 else max(dim, strides[0]), head_stride
     if shape[0] != B:
         raise ValueError(f"{name} must have one entry for each row of page_table")
     n = shape[1]
-    row_stride = stride[1] if n > 1 else stride[0]
-    if B > 1 and n > 1 and stride[0] != n * stride[1]:
+    row_stride = strides[1] if n > 1 else strides[0]
+    if B > 1 and n > 1 and strides[0] != n * strides[1]:
         raise ValueError(f"{name}: rows are not evenly spaced")
     return B * n, heads, dim, row_stride if B * n > 1 else max(dim, row_stride), head_stride
 
 
-def _new(new_start, max_new, t, name, B):
-    """max_new of a call whose new tokens are ``t``."""
+def _new(new_start, max_new, m: _Meta, B):
+    """max_new of a call whose new tokens have the shape of ``m``."""
     if new_start is None:
-        if max_new is not None and t.dim() == 4 and max_new != t.shape[1]:
+        if max_new is not None and len(m.shape) == 4 and max_new != m.shape[1]:
             raise ValueError("max_new differs from the tokens given")
-        return t.shape[1] if t.dim() == 4 else 0
-    _cuda(new_start, "new_start")
-    if _i32(new_start, "new_start").numel() != B + 1:
-        raise ValueError("new_start must have one entry more than page_table has rows")
+        return m.shape[1] if len(m.shape) == 4 else 0
+    _int32(new_start, "new_start", B + 1, "one entry more than page_table has rows")
     if max_new is None:
         raise ValueError("new_start needs max_new, the largest number of new tokens of a sequence")
     return int(max_new)
+
+
+_PER_SEQUENCE = "one entry for each sequence"
+
+
+@functools.lru_cache(maxsize=_KEPT)
+def _append_plan(kc, vc, ks, vs, table, lens, k, v, start, max_new, status):
+    d = _kv_desc(kc, vc, ks, vs, table, lens, "ctx_lens")
+    k, v = _see(k, "k"), _see(v, "v")
+    B, ragged = d.batch, start is not None
+    n, hk, dk, k_row, k_head = _rows(k, "k", B, ragged)
+    nv, hv, dv, v_row, v_head = _rows(v, "v", B, ragged)
+    if (n, hk, dk) != (nv, hv, dv) or k.dtype != v.dtype:
+        raise ValueError("k and v must match in shape and dtype")
+    if hk != d.kv_heads or dk != d.head_dim:
+        raise ValueError("k and v must have the cache's heads and head_dim")
+    r = N.KvRowsDesc(_new(start, max_new, k, B), n, _code(k), 0, k_row, k_head, v_row, v_head)
+    _int32(status, "row_status", B, _PER_SEQUENCE)
+    return ctypes.byref(d), ctypes.byref(r)
+
+
+@functools.lru_cache(maxsize=_KEPT)
+def _read_plan(kc, vc, ks, vs, table, first, k, v, start, tokens, status):
+    d = _kv_desc(kc, vc, ks, vs, table, first, "first")
+    k, v = _see(k, "out[0]"), _see(v, "out[1]")
+    B, ragged = d.batch, start is not None
+    for m, name in ((k, "out[0]"), (v, "out[1]")):
+        if m.shape != k.shape or m.dtype != k.dtype or tuple(m.shape[-2:]) != (d.kv_heads, d.head_dim):
+            raise ValueError(f"{name} must be [..., {d.kv_heads}, {d.head_dim}], both of one shape and dtype")
+    n, _, _, k_row, k_head = _rows(k, "out[0]", B, ragged)
+    _, _, _, v_row, v_head = _rows(v, "out[1]", B, ragged)
+    r = N.KvRowsDesc(_new(start, tokens, k, B), n, _code(k), 0, k_row, k_head, v_row, v_head)
+    _int32(status, "row_status", B, _PER_SEQUENCE)
+    return ctypes.byref(d), ctypes.byref(r)
+
+
+@functools.lru_cache(maxsize=_KEPT)
+def _commit_plan(kc, vc, ks, vs, table, lens, path, accept, new_lens, status):
+    d = _kv_desc(kc, vc, ks, vs, table, lens, "ctx_lens")
+    B, p = d.batch, _see(path, "path")
+    if len(p.shape) != 2:
+        raise ValueError("path must be [B, D+1]")
+    _int32(path, "path", B * p.shape[1], "one row for each sequence")
+    _int32(accept, "accept_len", B, _PER_SEQUENCE)
+    _int32(new_lens, "new_lens", B, _PER_SEQUENCE)
+    _int32(status, "row_status", B, _PER_SEQUENCE)
+    return ctypes.byref(d), p.shape[1]
+
+
+@functools.lru_cache(maxsize=_KEPT)
+def _attention_plan(q, kc, vc, ks, vs, table, lens, start, max_new, parents, scale, window, sinks, out, status):
+    d = _kv_desc(kc, vc, ks, vs, table, lens, "ctx_lens")
+    q, out = _see(q, "q"), _see(out, "out")
+    B, ragged = d.batch, start is not None
+    n, heads, dim, q_row, q_head = _rows(q, "q", B, ragged)
+    if dim != d.head_dim:
+        raise ValueError("q must have the cache's head_dim")
+    _int32(parents, "parents", n, "one entry for each new token")
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must match q in shape and dtype")
+    _, _, _, o_row, o_head = _rows(out, "out", B, ragged)
+    a = N.KvAttentionDesc(d, heads, _new(start, max_new, q, B), n, _code(q),
+                          float(scale) if scale is not None else dim ** -0.5, int(window), int(sinks), 0, q_row, q_head,
+                          o_row, o_head)
+    _int32(status, "row_status", B, _PER_SEQUENCE)
+    return ctypes.byref(a), N.lib().sv_kv_attention_workspace_size(ctypes.byref(a))
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(stream, t) -> int:
+    return stream.cuda_stream if stream is not None else _raw_stream(t.device.index)
 
 
 def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, ctx_lens: torch.Tensor, *,
@@ -113,21 +226,12 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, page_table: torch.T
     sv_kv_append.  k, v [B, n, kv_heads, dim] (or [total, kv_heads, dim] with
     ``new_start``), float32 or bfloat16, any row and head strides.  Updates
     and returns ``cache``; ``row_status`` [B] int32 receives the flags."""
-    d = _cache(cache, page_table, ctx_lens, "ctx_lens")
-    _cuda(k, "k")
-    _cuda(v, "v")
-    B = d.batch
-    ragged = new_start is not None
-    n, hk, dk, k_row, k_head = _rows(k, "k", B, ragged)
-    nv, hv, dv, v_row, v_head = _rows(v, "v", B, ragged)
-    if (n, hk, dk) != (nv, hv, dv) or k.dtype != v.dtype:
-        raise ValueError("k and v must match in shape and dtype")
-    if hk != d.kv_heads or dk != d.head_dim:
-        raise ValueError("k and v must have the cache's heads and head_dim")
-    r = N.KvRowsDesc(_new(new_start, max_new, k, "k", B), n, _code(k), 0, k_row, k_head, v_row, v_head)
-    st = N.lib().sv_kv_append(
-        ctypes.byref(d), ctypes.byref(r), _p(k), _p(v), _p(page_table), _p(ctx_lens), _p(new_start), _p(cache["k"]),
-        _p(cache["v"]), _p(cache["k_scale"]), _p(cache["v_scale"]), _status(row_status, B), _stream(stream))
+    kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
+    d, r = _append_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(k), _meta(v),
+                        _meta(new_start), max_new, _meta(row_status))
+    st = N.lib().sv_kv_append(d, r, k.data_ptr(), v.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start),
+                              kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), _at(row_status),
+                              _stream_of(stream, kc))
     N.check(st, "sv_kv_append")
     return cache
 
@@ -139,28 +243,23 @@ def kv_read(cache: dict, page_table: torch.Tensor, first: torch.Tensor, tokens: 
 
     Returns (k, v): [B, tokens, kv_heads, dim], or with ``new_start`` [B + 1]
     [total, kv_heads, dim] rows, ``tokens`` being the most of one sequence."""
-    d = _cache(cache, page_table, first, "first")
-    B = d.batch
-    if new_start is None:
-        shape = (B, int(tokens), d.kv_heads, d.head_dim)
-    else:
-        if total is None:
-            raise ValueError("new_start needs total, the number of rows")
-        shape = (int(total), d.kv_heads, d.head_dim)
+    kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     if out is None:
-        out = tuple(torch.empty(shape, dtype=dtype, device=cache["k"].device) for _ in range(2))
-    k, v = out
-    for t, n in ((k, "out[0]"), (v, "out[1]")):
-        _cuda(t, n)
-        if tuple(t.shape) != shape or t.dtype != k.dtype:
-            raise ValueError(f"{n} must be {list(shape)}, both of one dtype")
-    ragged = new_start is not None
-    n, _, _, k_row, k_head = _rows(k, "out[0]", B, ragged)
-    _, _, _, v_row, v_head = _rows(v, "out[1]", B, ragged)
-    r = N.KvRowsDesc(_new(new_start, int(tokens), k, "out[0]", B), n, _code(k), 0, k_row, k_head, v_row, v_head)
-    st = N.lib().sv_kv_read(
-        ctypes.byref(d), ctypes.byref(r), _p(cache["k"]), _p(cache["v"]), _p(cache["k_scale"]), _p(cache["v_scale"]),
-        _p(page_table), _p(first), _p(new_start), _p(k), _p(v), _status(row_status, B), _stream(stream))
+        _, heads, _, dim = kc.shape
+        if new_start is None:
+            shape = (page_table.shape[0], int(tokens), heads, dim)
+        elif total is None:
+            raise ValueError("new_start needs total, the number of rows")
+        else:
+            shape = (int(total), heads, dim)
+        k, v = kc.new_empty(shape, dtype=dtype), kc.new_empty(shape, dtype=dtype)
+    else:
+        k, v = out
+    d, r = _read_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(first), _meta(k), _meta(v),
+                      _meta(new_start), int(tokens), _meta(row_status))
+    st = N.lib().sv_kv_read(d, r, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), page_table.data_ptr(),
+                            first.data_ptr(), _at(new_start), k.data_ptr(), v.data_ptr(), _at(row_status),
+                            _stream_of(stream, kc))
     N.check(st, "sv_kv_read")
     return k, v
 
@@ -172,21 +271,14 @@ def kv_commit(cache: dict, page_table: torch.Tensor, ctx_lens: torch.Tensor, pat
     sv_kv_commit.  path [B, D+1] and accept_len [B] int32 are the results of
     verify_tree or verify_tree_sample.  Returns the sequences' new lengths
     [B] int32 and updates ``cache``."""
-    d = _cache(cache, page_table, ctx_lens, "ctx_lens")
-    _cuda(path, "path")
-    _cuda(accept_len, "accept_len")
-    B = d.batch
-    if _i32(path, "path").dim() != 2 or path.shape[0] != B or _i32(accept_len, "accept_len").numel() != B:
-        raise ValueError("path must be [B, D+1] and accept_len [B]")
+    kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     if new_lens is None:
-        new_lens = torch.empty(B, dtype=torch.int32, device=path.device)
-    _cuda(new_lens, "new_lens")
-    if _i32(new_lens, "new_lens").numel() != B:
-        raise ValueError("new_lens must have one entry for each sequence")
-    st = N.lib().sv_kv_commit(
-        ctypes.byref(d), int(nodes), path.shape[1], _p(page_table), _p(ctx_lens), _p(path), _p(accept_len),
-        _p(cache["k"]), _p(cache["v"]), _p(cache["k_scale"]), _p(cache["v_scale"]), _p(new_lens),
-        _status(row_status, B), _stream(stream))
+        new_lens = torch.empty_like(ctx_lens)
+    d, length = _commit_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(path),
+                             _meta(accept_len), _meta(new_lens), _meta(row_status))
+    st = N.lib().sv_kv_commit(d, int(nodes), length, page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
+                              accept_len.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                              new_lens.data_ptr(), _at(row_status), _stream_of(stream, kc))
     N.check(st, "sv_kv_commit")
     return new_lens
 
@@ -203,33 +295,19 @@ def kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, ctx_len
     or bfloat16; ``parents`` ([B, n] or [total] int32) makes the new tokens a
     tree; ``scale`` defaults to 1 / sqrt(dim).  Returns out like q, and with
     ``lse`` the log-sum-exp [..., heads] float32 as well."""
-    d = _cache(cache, page_table, ctx_lens, "ctx_lens")
-    _cuda(q, "q")
-    _cuda(parents, "parents")
-    B = d.batch
-    ragged = new_start is not None
-    n, heads, dim, q_row, q_head = _rows(q, "q", B, ragged)
-    if dim != d.head_dim:
-        raise ValueError("q must have the cache's head_dim")
-    if parents is not None and _i32(parents, "parents").numel() != n:
-        raise ValueError("parents must have one entry for each new token")
+    kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _cuda(out, "out")
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must match q in shape and dtype")
-    _, _, _, o_row, o_head = _rows(out, "out", B, ragged)
-    sums = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if lse else None
-    a = N.KvAttentionDesc(d, heads, _new(new_start, max_new, q, "q", B), n, _code(q),
-                          float(scale) if scale is not None else dim ** -0.5, int(window), int(sinks), 0, q_row, q_head,
-                          o_row, o_head)
-    lib = N.lib()
-    need = lib.sv_kv_attention_workspace_size(ctypes.byref(a))
+        out = q.new_empty(q.shape)
+    a, need = _attention_plan(_meta(q), _meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens),
+                              _meta(new_start), max_new, _meta(parents), scale, window, sinks, _meta(out), _meta(row_status))
+    sums = q.new_empty(q.shape[:-1], dtype=torch.float32) if lse else None
+    raw = _stream_of(stream, q)
     if ws is None:
-        ws = workspace(need, q.device, stream)
-    st = lib.sv_kv_attention(
-        ctypes.byref(a), _p(q), _p(cache["k"]), _p(cache["v"]), _p(cache["k_scale"]), _p(cache["v_scale"]),
-        _p(page_table), _p(ctx_lens), _p(new_start), _p(parents), _p(out), _p(sums), _status(row_status, B), _p(ws),
-        ctypes.c_size_t(ws.numel()), _stream(stream))
+        ws = _WORKSPACES.get((q.device.index, raw))
+        if ws is None or ws.numel() < need:
+            ws = workspace(need, q.device, stream)
+    st = N.lib().sv_kv_attention(a, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                                 page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start), _at(parents), out.data_ptr(),
+                                 _at(sums), _at(row_status), ws.data_ptr(), ws.numel(), raw)
     N.check(st, "sv_kv_attention")
     return (out, sums) if lse else out
