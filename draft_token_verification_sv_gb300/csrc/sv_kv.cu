@@ -109,9 +109,10 @@ struct AppendRows {
 // other way round 24,000 prompt tokens took 82 us).  The new tokens of the page
 // are read once: up to kHeld vectors a thread stay in registers between the
 // maximum and the rounding, what is beyond them is read again (from L2).
+constexpr int kHeld = 16;
+
 template <typename E, int THREADS, bool VEC>
 __global__ void __launch_bounds__(THREADS) kv_append_kernel(KvView w, AppendRows rows) {
-  constexpr int kHeld = 8;
   constexpr int kN = Packed<E>::kN;
   __shared__ uint32_t scratch[THREADS / 32];
   const int b = blockIdx.z, span = blockIdx.x / (2 * w.kv_heads), part = blockIdx.x - span * (2 * w.kv_heads);
@@ -336,11 +337,29 @@ __global__ void __launch_bounds__(THREADS) kv_commit_kernel(KvView w, int nodes,
 }
 
 template <typename E, int THREADS>
-void launch_append(const KvView& w, const AppendRows& rows, bool vec, dim3 grid, cudaStream_t stream) {
+void launch_append(const KvView& w, const AppendRows& rows, bool vec, const dim3& grid, cudaStream_t stream) {
   if (vec)
     kv_append_kernel<E, THREADS, true><<<grid, THREADS, 0, stream>>>(w, rows);
   else
     kv_append_kernel<E, THREADS, false><<<grid, THREADS, 0, stream>>>(w, rows);
+}
+
+// What a block takes stays in registers, so the fewest threads that hold it,
+// each with much in flight: 24,000 prompt tokens in pages of 128 take 58 us
+// with 128 threads of 16 vectors, 72 us with 256 of 8 and 93 us with 512 of 4;
+// in pages of 64, 64 us with the fewest threads and 77 us with twice as many.
+// A token's vectors are spread over threads of their own, so no fewer than those.
+template <typename E>
+void launch_append(const KvView& w, const AppendRows& rows, bool vec, int tokens, dim3 grid, cudaStream_t stream) {
+  const int vectors = w.dim / Packed<E>::kN, all = tokens * vectors;
+  if (all <= 32 * kHeld && vectors <= 32)
+    launch_append<E, 32>(w, rows, vec, grid, stream);
+  else if (all <= 64 * kHeld)
+    launch_append<E, 64>(w, rows, vec, grid, stream);
+  else if (all <= 128 * kHeld)
+    launch_append<E, 128>(w, rows, vec, grid, stream);
+  else
+    launch_append<E, 256>(w, rows, vec, grid, stream);
 }
 
 bool rows_aligned16(const void* k, const void* v, const sv_kv_rows_desc& r) {
@@ -369,12 +388,10 @@ sv_status kv_append(const sv_kv_desc& d, const sv_kv_rows_desc& r, const void* k
   const dim3 grid(static_cast<unsigned>(spans * 2 * d.kv_heads), 1, d.batch);
   const bool vec = rows_aligned16(k, v, r);
   const int tokens = r.max_new < d.page_size ? r.max_new : d.page_size;
-  // a block of 64 threads holds 512 vectors in registers, one of 256 four times that
-  const bool few = tokens * d.head_dim <= (r.dtype == SV_BF16 ? 4096 : 2048);
   if (r.dtype == SV_BF16)
-    few ? launch_append<uint16_t, 64>(w, rows, vec, grid, stream) : launch_append<uint16_t, 256>(w, rows, vec, grid, stream);
+    launch_append<uint16_t>(w, rows, vec, tokens, grid, stream);
   else
-    few ? launch_append<float, 64>(w, rows, vec, grid, stream) : launch_append<float, 256>(w, rows, vec, grid, stream);
+    launch_append<float>(w, rows, vec, tokens, grid, stream);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   return SV_OK;
