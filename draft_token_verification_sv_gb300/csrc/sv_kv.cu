@@ -260,7 +260,8 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS) kv_commit_kernel(KvView w, int nodes, int path_len, const int32_t* path,
                                                             const int32_t* accept_len, int32_t* new_lens) {
   extern __shared__ uint4 codes4[];  // [path_len][dim / 16]
-  __shared__ float s_scale[kMaxPath], s_top[kMaxPath];
+  __shared__ float s_scale[kMaxPath];
+  __shared__ uint32_t s_top[kMaxPath];  // largest magnitude code
   const int b = blockIdx.y, head = blockIdx.x >> 1, which = blockIdx.x & 1;
   const bool first = blockIdx.x == 0 && threadIdx.x == 0;
   const int ctx = __ldg(w.ctx_lens + b);
@@ -286,12 +287,15 @@ __global__ void __launch_bounds__(THREADS) kv_commit_kernel(KvView w, int nodes,
   float* scales = which ? w.c.v_scale : w.c.k_scale;
   const int mask = (1 << w.page_shift) - 1;
   const int cpr = w.dim >> 4;
-  const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i <= a; i += THREADS / 32) {  // a warp per token
+  for (int i = threadIdx.x; i <= a; i += THREADS) s_top[i] = 0;
+  __syncthreads();
+  for (int n = threadIdx.x; n < (a + 1) * cpr; n += THREADS) {  // a thread per 16 codes
+    const int i = n / cpr, ch = n - i * cpr;
     const int pos = ctx + __ldg(p + i);
     const int page = kv_page(w, b, pos >> w.page_shift);
     uint4 c = make_uint4(0, 0, 0, 0);
-    if (lane < cpr && page >= 0) c = *reinterpret_cast<const uint4*>(cache + kv_offset(w, page, head, pos & mask) + lane * 16);
+    if (page >= 0) c = *reinterpret_cast<const uint4*>(cache + kv_offset(w, page, head, pos & mask) + ch * 16);
+    if (ch == 0) s_scale[i] = page >= 0 ? scales[static_cast<int64_t>(page) * w.kv_heads + head] : 0.0f;
     uint32_t m = 0;
     const uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
@@ -301,13 +305,8 @@ __global__ void __launch_bounds__(THREADS) kv_commit_kernel(KvView w, int nodes,
         const uint32_t u = (word[k] >> (8 * j)) & 0x7fu;
         m = u == 0x7fu ? m : max(m, u);
       }
-    if (lane < cpr) codes4[i * cpr + lane] = c;
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) {
-      const float s = page >= 0 ? scales[static_cast<int64_t>(page) * w.kv_heads + head] : 0.0f;
-      s_scale[i] = s;
-      s_top[i] = f16x2_to_float2(e4m3x2_to_f16x2(m)).x * s;
-    }
+    codes4[n] = c;
+    atomicMax(&s_top[i], m);
   }
   __syncthreads();
   const uint32_t* words = reinterpret_cast<const uint32_t*>(codes4);
@@ -321,7 +320,7 @@ __global__ void __launch_bounds__(THREADS) kv_commit_kernel(KvView w, int nodes,
     const int held = lo - page0;
     const float old = held > 0 ? *scale : 0.0f;
     float top = 0.0f;
-    for (int i = lo; i < hi; ++i) top = fmaxf(top, s_top[i - ctx]);
+    for (int i = lo - ctx; i < hi - ctx; ++i) top = fmaxf(top, f16x2_to_float2(e4m3x2_to_f16x2(s_top[i])).x * s_scale[i]);
     const float grown = fmaxf(old, kv_scale_for(top));
     const float inv = 1.0f / grown;
     if (held > 0 && grown > old) regrow<THREADS>(w, cache, page, head, held, old * inv);
@@ -427,7 +426,7 @@ sv_status kv_commit(const sv_kv_desc& d, int nodes, int path_len, const KvCache&
   start_phases(stream);
   if (!clear_status(row_status, d.batch, stream)) return SV_ERR_CUDA;
   const KvView w = kv_view(d, c, ctx_lens, nullptr, nodes, d.batch * nodes, row_status);
-  constexpr int kThreads = 128;
+  constexpr int kThreads = 64;
   // 65 tokens of 256 dims: 16,640 bytes, within the default limit
   const size_t smem = static_cast<size_t>(path_len) * d.head_dim;
   kv_commit_kernel<kThreads><<<dim3(2 * d.kv_heads, d.batch), kThreads, smem, stream>>>(w, nodes, path_len, path,
