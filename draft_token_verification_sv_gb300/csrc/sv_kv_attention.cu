@@ -61,19 +61,24 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// 16 consecutive query values, 0 behind the row's end (dim is a multiple of 16).
+// 16 consecutive query values (zeros unless `live`).
 template <typename E>
 __device__ __forceinline__ void load_query16(const E* p, bool live, bool vec, float (&x)[16]) {
   constexpr int kV = sizeof(E) == 2 ? 8 : 4;
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = 0.0f;
   if (!live) return;
-  if (vec) {
 #pragma unroll
-    for (int i = 0; i < 16 / kV; ++i) unpack<E>(*reinterpret_cast<const uint4*>(p + i * kV), x + i * kV);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = Elem<E>::load(p + i);
+  for (int i = 0; i < 16 / kV; ++i) {
+    uint4 v;
+    if (vec) {
+      v = *reinterpret_cast<const uint4*>(p + i * kV);
+    } else {
+      E* e = reinterpret_cast<E*>(&v);
+#pragma unroll 1
+      for (int j = 0; j < kV; ++j) e[j] = __ldg(p + i * kV + j);
+    }
+    unpack<E>(v, x + i * kV);
   }
 }
 
@@ -88,13 +93,14 @@ constexpr int kThreads = 32 * kWarps;
 template <typename E, int DP, int MT> struct Shape {
   static constexpr bool kSplit = sizeof(E) == 4;  // queries and weights as two fp16 each
   static constexpr int kRows = 16 * MT;
-  static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 4 : 3;
+  static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 4 : kSplit ? 2 : 3;
   static constexpr int kBlocksPerSm = MT == 1 && !kSplit ? (DP == 64 ? 4 : DP == 128 ? 3 : 2) : DP == 64 && !(kSplit && MT == 2) ? 3 : 2;
   static constexpr int kStageBytes = 2 * kStep * DP;          // keys, values
   static constexpr int kRing = kStages * (kStageBytes + 16);  // and their two scales
   static constexpr int kMerge = kRows * DP * 4;               // a warp's values in the join of a block's warps
   static constexpr int kPerWarp = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kShared = kWarps * kPerWarp;
+  static constexpr int kQueryBytes = kRows * DP * 2;          // queries as fp16 (for fp32 twice)
+  static constexpr int kShared = kWarps * kPerWarp + (kSplit ? 2 : 1) * kQueryBytes;
   static constexpr int kBlocks = kSMs * kBlocksPerSm;
   static constexpr int kPart = kRows * (DP + 2);  // floats of a part in the workspace
 };
@@ -127,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
   constexpr int NC = kStep * DP / 16 / 32;  // chunks of keys (and of values) that a lane copies for a step
   extern __shared__ __align__(128) uint8_t shared[];
   __shared__ CursorScratch s_cursor;
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_factor[kRows];
+  __shared__ int s_token[kRows], s_pos[kRows];
   const KvView& w = a.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = lane >> 2, col = lane & 3;  // of the fragments
@@ -199,49 +206,79 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
       for (int i = 0; i < S::kStages - 1; ++i) fetch(step0 + i * kWarps, page[i]);
     }
 
-    // Queries: of each 16 rows row's and row + 8's, as the first product's left side.
+    // Queries, by all threads into shared memory: a thread takes 16 dims of a row, the threads of a row lie together in a
+    // warp.  Times a power of two that puts the row's largest at 2^14 .. 2^15: fp16 then keeps what is 2^-28 of it without
+    // loss for bf16; a negative factor goes into the queries, so that larger products are larger scores.
+    uint8_t* const queries = shared + kWarps * S::kPerWarp;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < kRows * (DP / 16); i += kThreads) {
+      const int r = i / (DP / 16), chunk = i % (DP / 16);
+      const bool live = r < rows;
+      const int at = r0 + min(r, rows - 1), token = at / a.group, head = c.h * a.group + at - token * a.group;
+      const E* p = static_cast<const E*>(a.q) + (static_cast<int64_t>(s.row0) + token) * a.q_row_stride + head * a.q_head_stride + chunk * 16;
+      float x[16];
+      load_query16<E>(p, live && chunk * 16 < w.dim, a.q_vec, x);
+      float top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+      for (int n = 1; n < DP / 16; n <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, n));
+      const int e = top > 0.0f && top < CUDART_INF_F ? min(120, 141 - static_cast<int>(__float_as_uint(top) >> 23)) : 0;
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = x[2 * j] * up, v = x[2 * j + 1] * up;
+        hi[j] = floats_to_f16x2(u, v);
+        lo[j] = SPLIT ? rest_f16x2(u, v, hi[j]) : 0;
+      }
+      uint4* to = reinterpret_cast<uint4*>(queries + i * 32);
+      to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      to[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+      if constexpr (SPLIT) {
+        to = reinterpret_cast<uint4*>(queries + S::kQueryBytes + i * 32);
+        to[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        to[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+      }
+      if (chunk == 0) {
+        s_factor[r] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        int depth = token;
+        if (parents) {
+          depth = 0;
+          for (int u = tree_parent(parents, token); u >= 0; u = tree_parent(parents, u)) ++depth;
+        }
+        s_token[r] = token;
+        s_pos[r] = s.ctx + depth;
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    // of each 16 rows row's and row + 8's, as the first product's left side
     uint32_t q[MT][NQ][4][4], q_rest[SPLIT ? MT : 1][SPLIT ? NQ : 1][4][4];
     float factor[MT][2];  // scores in base 2 = factor * key scale * product, factor >= 0
-    int token[MT][2], pos[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = 16 * mt + row + 8 * k;
-        const bool live = r < rows;
-        token[mt][k] = (r0 + min(r, rows - 1)) / a.group;
-        const int head = c.h * a.group + (r0 + min(r, rows - 1)) % a.group;
-        const E* p = static_cast<const E*>(a.q) + (static_cast<int64_t>(s.row0) + token[mt][k]) * a.q_row_stride + head * a.q_head_stride;
-        float x[NQ][16];
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          load_query16<E>(p + 64 * i + 16 * col, live && 64 * i + 16 * col < w.dim, a.q_vec, x[i]);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[i][j]));
-        }
-        top = quad_max(top);
-        // the largest becomes 2^14 .. 2^15: fp16 keeps what is 2^-28 of it without loss for bf16 queries;
-        // a negative factor goes into the queries, so that larger products are larger scores
-        const int e = top > 0.0f && top < CUDART_INF_F ? min(120, 141 - static_cast<int>(__float_as_uint(top) >> 23)) : 0;
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
-        factor[mt][k] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        factor[mt][k] = s_factor[r];
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
+            const uint4* from = reinterpret_cast<const uint4*>(queries + part * S::kQueryBytes + (r * (DP / 16) + 4 * i + col) * 32);
+            const uint4 u = from[0], v = from[1];
+            const uint32_t word[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float u = x[i][4 * j + 2 * h] * up, v = x[i][4 * j + 2 * h + 1] * up;
-              q[mt][i][j][2 * h + k] = floats_to_f16x2(u, v);
-              if constexpr (SPLIT) q_rest[mt][i][j][2 * h + k] = rest_f16x2(u, v, q[mt][i][j][2 * h + k]);
-            }
-        pos[mt][k] = s.ctx + token[mt][k];
-        if (parents) {
-          int depth = 0;
-          for (int u = tree_parent(parents, token[mt][k]); u >= 0; u = tree_parent(parents, u)) ++depth;
-          pos[mt][k] = s.ctx + depth;
-        }
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (part == 0)
+                  q[mt][i][j][2 * h + k] = word[2 * j + h];
+                else
+                  q_rest[SPLIT ? mt : 0][SPLIT ? i : 0][j][2 * h + k] = word[2 * j + h];
+              }
+          }
       }
     // tokens before `all` are in every row's past; `far` is the furthest position of a row
     const int all = parents ? s.ctx : s.ctx + i0 + 1, far = s.ctx + i1;
@@ -305,13 +342,11 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
         unsigned seen = 0xffu;  // bit 4 n + k: x[n][k]
         if (!whole) {
           seen = 0;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int j = t0 + 8 * n + 2 * col + (k & 1);
-              if (!lost && j < steps.end && sees(a, parents, s.ctx, token[mt][k >> 1], pos[mt][k >> 1], j)) seen |= 1u << (4 * n + k);
-            }
+#pragma unroll 1
+          for (int n = 0; n < 8; ++n) {  // (rolled: seldom run, and code is fetched anew by every launch)
+            const int j = t0 + 8 * (n >> 2) + 2 * col + (n & 1), r = 16 * mt + row + 4 * (n & 2);
+            if (!lost && j < steps.end && sees(a, parents, s.ctx, s_token[r], s_pos[r], j)) seen |= 1u << n;
+          }
         }
         // Weights against the maximum so far; where they sum to 2^7 and more (infinity where there is no maximum yet) it is
         // raised and they are taken again.
@@ -505,18 +540,17 @@ size_t workspace_for() {
   return S::kBlocks * (2 * S::kPart * sizeof(float) + sizeof(JoinRecord));
 }
 
-// Calls f with the kernel's template arguments as types: one tile of 16 rows
-// where a kv head has no more, two where it has (but not for fp32 queries of
-// more than 64 dims nor for more than 128 dims: their rows' registers would
-// spill).
+// Calls f with the kernel's template arguments as types: one tile of 16 rows,
+// or two for up to 64 dims where a kv head has more rows (the second tile costs
+// registers that longer rows do not have; bf16 rows of up to 128 dims take the
+// tile kernel then).
 template <typename F>
 auto with_shape(const sv_kv_attention_desc& d, F f) {
   const bool two = static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 16;
   const int dp = round_dim(d.kv.head_dim);
   if (d.dtype == SV_BF16) {
     if (dp == 64) return two ? f(uint16_t{}, Int<64>{}, Int<2>{}) : f(uint16_t{}, Int<64>{}, Int<1>{});
-    if (dp == 128) return two ? f(uint16_t{}, Int<128>{}, Int<2>{}) : f(uint16_t{}, Int<128>{}, Int<1>{});
-    return f(uint16_t{}, Int<256>{}, Int<1>{});
+    return dp == 128 ? f(uint16_t{}, Int<128>{}, Int<1>{}) : f(uint16_t{}, Int<256>{}, Int<1>{});
   }
   if (dp == 64) return two ? f(float{}, Int<64>{}, Int<2>{}) : f(float{}, Int<64>{}, Int<1>{});
   return dp == 128 ? f(float{}, Int<128>{}, Int<1>{}) : f(float{}, Int<256>{}, Int<1>{});
