@@ -252,7 +252,8 @@ def kv_read(cache: dict, page_table: torch.Tensor, first: torch.Tensor, tokens: 
             raise ValueError("new_start needs total, the number of rows")
         else:
             shape = (int(total), heads, dim)
-        k, v = kc.new_empty(shape, dtype=dtype), kc.new_empty(shape, dtype=dtype)
+        device = kc.device
+        k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
     else:
         k, v = out
     d, r = _read_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(first), _meta(k), _meta(v),
@@ -296,16 +297,17 @@ def kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, ctx_len
     tree; ``scale`` defaults to 1 / sqrt(dim).  Returns out like q, and with
     ``lse`` the log-sum-exp [..., heads] float32 as well."""
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
+    device = q.device
     if out is None:
-        out = q.new_empty(q.shape)
+        out = torch.empty(q.shape, dtype=q.dtype, device=device)
     a, need = _attention_plan(_meta(q), _meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens),
                               _meta(new_start), max_new, _meta(parents), scale, window, sinks, _meta(out), _meta(row_status))
-    sums = q.new_empty(q.shape[:-1], dtype=torch.float32) if lse else None
+    sums = torch.empty(q.shape[:-1], dtype=torch.float32, device=device) if lse else None
     raw = _stream_of(stream, q)
     if ws is None:
-        ws = _WORKSPACES.get((q.device.index, raw))
+        ws = _WORKSPACES.get((device.index, raw))
         if ws is None or ws.numel() < need:
-            ws = workspace(need, q.device, stream)
+            ws = workspace(need, device, stream)
     st = N.lib().sv_kv_attention(a, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
                                  page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start), _at(parents), out.data_ptr(),
                                  _at(sums), _at(row_status), ws.data_ptr(), ws.numel(), raw)
