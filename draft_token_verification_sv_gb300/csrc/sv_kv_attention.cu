@@ -92,6 +92,7 @@ constexpr int kThreads = 32 * kWarps;
 // for fp32 16 DP, floats of a warp) sets how many blocks an SM holds.
 template <typename E, int DP, int MT> struct Shape {
   static constexpr bool kSplit = sizeof(E) == 4;  // queries and weights as two fp16 each
+  static constexpr bool kQueriesStay = MT == 1 || DP == 64;  // in registers; else read from shared memory for every step
   static constexpr int kRows = 16 * MT;
   static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 4 : kSplit ? 2 : 3;
   static constexpr int kBlocksPerSm = MT == 1 && !kSplit ? (DP == 64 ? 4 : DP == 128 ? 3 : 2) : DP == 64 && !(kSplit && MT == 2) ? 3 : 2;
@@ -232,13 +233,12 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
         hi[j] = floats_to_f16x2(u, v);
         lo[j] = SPLIT ? rest_f16x2(u, v, hi[j]) : 0;
       }
-      uint4* to = reinterpret_cast<uint4*>(queries + i * 32);
-      to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      to[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-      if constexpr (SPLIT) {
-        to = reinterpret_cast<uint4*>(queries + S::kQueryBytes + i * 32);
-        to[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        to[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+      // in the order of the products' left side: of (16 rows, 64 dims, 16 of them, lane) four words
+      uint32_t* to = reinterpret_cast<uint32_t*>(queries) + (((r >> 4) * NQ + (chunk >> 2)) * 4 * 32 + (r & 7) * 4 + (chunk & 3)) * 4 + ((r >> 3) & 1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        to[(j >> 1) * 128 + 2 * (j & 1)] = hi[j];
+        if constexpr (SPLIT) to[(j >> 1) * 128 + 2 * (j & 1) + S::kQueryBytes / 4] = lo[j];
       }
       if (chunk == 0) {
         s_factor[r] = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
@@ -254,32 +254,28 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
     }
     __syncthreads();
     // of each 16 rows row's and row + 8's, as the first product's left side
-    uint32_t q[MT][NQ][4][4], q_rest[SPLIT ? MT : 1][SPLIT ? NQ : 1][4][4];
+    const auto load_queries = [&](int mt, int i, int j, int part, uint32_t (&f)[4]) {
+      const uint4 u = reinterpret_cast<const uint4*>(queries + part * S::kQueryBytes)[((mt * NQ + i) * 4 + j) * 32 + lane];
+      f[0] = u.x;
+      f[1] = u.y;
+      f[2] = u.z;
+      f[3] = u.w;
+    };
+    uint32_t q[S::kQueriesStay ? MT : 1][S::kQueriesStay ? NQ : 1][4][4], q_rest[SPLIT ? MT : 1][SPLIT ? NQ : 1][4][4];
     float factor[MT][2];  // scores in base 2 = factor * key scale * product, factor >= 0
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = 16 * mt + row + 8 * k;
-        factor[mt][k] = s_factor[r];
+      for (int k = 0; k < 2; ++k) factor[mt][k] = s_factor[16 * mt + row + 8 * k];
+      if constexpr (S::kQueriesStay)
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
 #pragma unroll
-          for (int part = 0; part < (SPLIT ? 2 : 1); ++part) {
-            const uint4* from = reinterpret_cast<const uint4*>(queries + part * S::kQueryBytes + (r * (DP / 16) + 4 * i + col) * 32);
-            const uint4 u = from[0], v = from[1];
-            const uint32_t word[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (part == 0)
-                  q[mt][i][j][2 * h + k] = word[2 * j + h];
-                else
-                  q_rest[SPLIT ? mt : 0][SPLIT ? i : 0][j][2 * h + k] = word[2 * j + h];
-              }
+          for (int j = 0; j < 4; ++j) {
+            load_queries(mt, i, j, 0, q[mt][i][j]);
+            if constexpr (SPLIT) load_queries(mt, i, j, 1, q_rest[mt][i][j]);
           }
-      }
+    }
     // tokens before `all` are in every row's past; `far` is the furthest position of a row
     const int all = parents ? s.ctx : s.ctx + i0 + 1, far = s.ctx + i1;
 
@@ -305,22 +301,46 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
       // products of 16 tokens: x[n][0..1] row's, [2..3] row + 8's, tokens 8 n + 2 col + {0, 1}
       float x[MT][2][4] = {};
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int i = 0; i < NQ; ++i) {
+        if constexpr (!S::kQueriesStay) {
+          uint32_t keys[2][4][2];
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          const uint4 b = *reinterpret_cast<const uint4*>(k_at + 16 * key_chunk<DP>(8 * n + row, 4 * i + col));
-          const uint32_t word[4] = {b.x, b.y, b.z, b.w};
+          for (int n = 0; n < 2; ++n) {
+            const uint4 b = *reinterpret_cast<const uint4*>(k_at + 16 * key_chunk<DP>(8 * n + row, 4 * i + col));
+            const uint32_t word[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t b0 = e4m3x2_to_f16x2(word[j] & 0xffffu), b1 = e4m3x2_to_f16x2(word[j] >> 16);
+            for (int j = 0; j < 4; ++j) {
+              keys[n][j][0] = e4m3x2_to_f16x2(word[j] & 0xffffu);
+              keys[n][j][1] = e4m3x2_to_f16x2(word[j] >> 16);
+            }
+          }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma(x[mt][n], q[mt][i][j][0], q[mt][i][j][1], q[mt][i][j][2], q[mt][i][j][3], b0, b1);
-              if constexpr (SPLIT)
-                mma(x[mt][n], q_rest[mt][i][j][0], q_rest[mt][i][j][1], q_rest[mt][i][j][2], q_rest[mt][i][j][3], b0, b1);
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t f[4];
+              load_queries(mt, i, j, 0, f);
+#pragma unroll
+              for (int n = 0; n < 2; ++n) mma(x[mt][n], f[0], f[1], f[2], f[3], keys[n][j][0], keys[n][j][1]);
+            }
+        } else {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint4 b = *reinterpret_cast<const uint4*>(k_at + 16 * key_chunk<DP>(8 * n + row, 4 * i + col));
+            const uint32_t word[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t b0 = e4m3x2_to_f16x2(word[j] & 0xffffu), b1 = e4m3x2_to_f16x2(word[j] >> 16);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma(x[mt][n], q[mt][i][j][0], q[mt][i][j][1], q[mt][i][j][2], q[mt][i][j][3], b0, b1);
+                if constexpr (SPLIT)
+                  mma(x[mt][n], q_rest[mt][i][j][0], q_rest[mt][i][j][1], q_rest[mt][i][j][2], q_rest[mt][i][j][3], b0, b1);
+              }
             }
           }
         }
+      }
       const int t0 = steps.token(step);
       const bool lost = (bad >> stage) & 1u;
       const bool whole = !lost && t0 + kStep <= all && (a.window == 0 || far - t0 < a.window || t0 + kStep <= a.sinks);
@@ -550,7 +570,8 @@ auto with_shape(const sv_kv_attention_desc& d, F f) {
   const int dp = round_dim(d.kv.head_dim);
   if (d.dtype == SV_BF16) {
     if (dp == 64) return two ? f(uint16_t{}, Int<64>{}, Int<2>{}) : f(uint16_t{}, Int<64>{}, Int<1>{});
-    return dp == 128 ? f(uint16_t{}, Int<128>{}, Int<1>{}) : f(uint16_t{}, Int<256>{}, Int<1>{});
+    if (dp == 128) return two ? f(uint16_t{}, Int<128>{}, Int<2>{}) : f(uint16_t{}, Int<128>{}, Int<1>{});
+    return f(uint16_t{}, Int<256>{}, Int<1>{});
   }
   if (dp == 64) return two ? f(float{}, Int<64>{}, Int<2>{}) : f(float{}, Int<64>{}, Int<1>{});
   return dp == 128 ? f(float{}, Int<128>{}, Int<1>{}) : f(float{}, Int<256>{}, Int<1>{});

@@ -785,7 +785,7 @@ sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspa
 // for two tiles of 16, which spill), at 64 dims 32 (170 us against 117).
 bool kv_attention_takes_tiles(const sv_kv_attention_desc& d) {
   return d.dtype == SV_BF16 && d.kv.head_dim <= 128 &&
-         static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > (d.kv.head_dim <= 64 ? 32 : 16);
+         static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 32;
 }
 
 size_t kv_attention_tiles_workspace(const sv_kv_attention_desc& d) {
