@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
       if (step < step1) {
         const int t0 = steps.token(step);
         const bool there = page >= 0 && page < w.num_pages;
-        if (!there) {
+        if (__builtin_expect(!there, 0)) {
           kv_flag(w, c.b, SV_ROW_BAD_PAGE);
           page = 0;
         }
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
       const int t0 = steps.token(step);
       const bool lost = (bad >> stage) & 1u;
       const bool whole = !lost && t0 + kStep <= all && (a.window == 0 || far - t0 < a.window || t0 + kStep <= a.sinks);
-      if (v_scale > v_ref) {  // uniform: a page with larger values than any before
+      if (__builtin_expect(v_scale > v_ref, 0)) {  // uniform: a page with larger values than any before
         const float fix = v_ref / v_scale;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         unsigned seen = 0xffu;  // bit 4 n + k: x[n][k]
-        if (!whole) {
+        if (__builtin_expect(!whole, 0)) {
           seen = 0;
 #pragma unroll 1
           for (int n = 0; n < 8; ++n) {  // (rolled: seldom run, and code is fetched anew by every launch)
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int k = 0; k < 4; ++k) e[n][k] = ex2(fmaf(x[mt][n][k], f[k >> 1], -m[mt][k >> 1]));
-          if (!whole)
+          if (__builtin_expect(!whole, 0))
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
           for (int k = 0; k < 2; ++k) sum[k] = (e[0][2 * k] + e[0][2 * k + 1]) + (e[1][2 * k] + e[1][2 * k + 1]);
         };
         weigh();
-        if (__any_sync(0xffffffffu, sum[0] > 128.0f || sum[1] > 128.0f)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, sum[0] > 128.0f || sum[1] > 128.0f), 0)) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float top = -CUDART_INF_F;
@@ -561,9 +561,10 @@ size_t workspace_for() {
 }
 
 // Calls f with the kernel's template arguments as types: one tile of 16 rows,
-// or two for up to 64 dims where a kv head has more rows (the second tile costs
-// registers that longer rows do not have; bf16 rows of up to 128 dims take the
-// tile kernel then).
+// or two where a kv head has more rows (32 rows of 128 dims on contexts of up to
+// 32768 tokens: 165 us against 235 for one tile, which reads the cache twice).
+// Longer rows, and fp32 ones of more than 64 dims, have one tile: their sums
+// alone fill the registers.
 template <typename F>
 auto with_shape(const sv_kv_attention_desc& d, F f) {
   const bool two = static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 16;

@@ -224,8 +224,8 @@ __device__ bool fetch_role(const CUtensorMap* keys, const CUtensorMap* values, c
   return true;
 }
 
-// A chunk of 16 codes becomes two of fp16, in rows of 64 dims, swizzled; lanes of the second block of dims do its halves
-// the other way round (they write other banks then).  What is not a token in sight becomes 0, whatever its bytes.
+// A chunk of 16 codes becomes two of fp16, in rows of 64 dims, swizzled; lanes of the second block of dims, and those of odd
+// tokens, do its halves the other way round (they use other banks then).  What is not a token in sight becomes 0, whatever its bytes.
 template <int DP>
 __device__ bool value_role(const int tiles, Shared& sh, uint8_t* v_tiles, const uint8_t* codes) {
   using T = Tiles<DP>;
@@ -234,7 +234,7 @@ __device__ bool value_role(const int tiles, Shared& sh, uint8_t* v_tiles, const 
   constexpr int NI = kTokens / kPer;                      // passes
   const int tid = threadIdx.x - 32 * kSoftmaxWarps;
   const int t0 = tid / kChunks, ch = tid % kChunks;
-  const int turn = ch >> 2 & 1;
+  const int turn = ((ch >> 2) ^ t0) & 1;
   const int to = (ch >> 2) * T::kBlockBytes + t0 * 128;
   const int half0 = to + (((2 * (ch & 3) + turn) ^ (t0 & 7)) << 4), half1 = to + (((2 * (ch & 3) + 1 - turn) ^ (t0 & 7)) << 4);
 #pragma unroll 1
@@ -504,7 +504,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
       float v_top = kNoScale;
 #pragma unroll
       for (int i = 0; i < kTileSteps; ++i) v_top = fmaxf(v_top, plan.v_log2[i]);
-      if (v_top > v_ref) {  // the same for all threads
+      if (__builtin_expect(v_top > v_ref, 0)) {  // the same for all threads
         if (!rescale(v_ref == kNoScale ? 0.0f : ex2(v_ref - v_top))) return false;
         v_ref = v_top;
       }
@@ -522,7 +522,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
 #pragma unroll 1
         for (bool sure = raise;; sure = true) {
           uint32_t x0[32], x1[32];
-          if (raise) {
+          if (__builtin_expect(raise, 0)) {
             tc::tmem_load32(scores, x0);
             tc::tmem_load32(scores + 32, x1);
             tc::wait_loads(x0);
@@ -559,7 +559,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
           }
         }
       };
-      if (!(plan.whole ? tile(std::false_type{}) : tile(std::true_type{}))) return false;
+      if (!(__builtin_expect(plan.whole, 1) ? tile(std::false_type{}) : tile(std::true_type{}))) return false;
       arrive(sh.pv_ready[it % kValueStages]);
       warp_arrive(sh.plan_free[it % kPlans]);
     }
@@ -780,9 +780,10 @@ sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspa
 
 }  // namespace
 
-// More rows of a kv head than the other kernel's one or two tiles of 16.  At
-// 128 dims that is 16 (32 rows on contexts of up to 32768: 188 us against 203
-// for two tiles of 16, which spill), at 64 dims 32 (170 us against 117).
+// More rows of a kv head than the other kernel's two tiles of 16.  Rows are
+// padded to 128 here, which costs more than it gives up to 32 of them: on
+// contexts of up to 32768 tokens 188 us against 165 at 128 dims, 170 against 117
+// at 64.  From 33 on the other kernel would read the cache twice.
 bool kv_attention_takes_tiles(const sv_kv_attention_desc& d) {
   return d.dtype == SV_BF16 && d.kv.head_dim <= 128 &&
          static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 32;
