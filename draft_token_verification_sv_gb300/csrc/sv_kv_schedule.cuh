@@ -12,6 +12,10 @@
 // two at most: the end of an item that began before it, and the beginning of
 // one that ends after it) and a second launch joins them, in order, so that
 // the result does not depend on timing.
+//
+// Taking up an item and handing over its result cost a block as much as some
+// tiles do.  So each item has that many empty tiles (OPEN, below 0) ahead of its
+// own in the list, and blocks that take more items take fewer tiles.
 #pragma once
 
 #include "sv_kv.cuh"
@@ -78,6 +82,7 @@ __device__ __forceinline__ ItemSteps item_steps(const AttentionParams& a, const 
   return x;
 }
 
+// Without the empty ones.
 template <int ROWS, int TILE>
 __device__ __forceinline__ int item_tiles(const AttentionParams& a, const KvSpan& s, int rt) {
   const int i0 = rt * ROWS / a.group;
@@ -90,13 +95,13 @@ __device__ __forceinline__ int row_tiles(const AttentionParams& a, const KvSpan&
   return s.n > 0 ? (s.n * a.group + ROWS - 1) / ROWS : 0;
 }
 
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, int OPEN>
 __device__ __forceinline__ long long sequence_tiles(const AttentionParams& a, int b) {
   if (b >= a.w.batch) return 0;
   const KvSpan s = kv_span(a.w, b);
   const int rts = row_tiles<ROWS>(a, s);
   long long t = 0;
-  for (int rt = 0; rt < rts; ++rt) t += item_tiles<ROWS, TILE>(a, s, rt);
+  for (int rt = 0; rt < rts; ++rt) t += OPEN + item_tiles<ROWS, TILE>(a, s, rt);
   return t * a.w.kv_heads;
 }
 
@@ -104,9 +109,9 @@ __device__ __forceinline__ long long sequence_tiles(const AttentionParams& a, in
 struct Cursor {
   long long at, end;   // its tiles
   long long total;
-  int blocks;          // that take part: each has a tile at least
+  int blocks;          // that take part: each has a tile at least, if an empty one
   int b, rt, h;        // the item of tile `at`
-  int tile;            // and the tile within it
+  int tile;            // and the tile within it, below 0 for the empty ones
   KvSpan span;
 };
 
@@ -117,13 +122,13 @@ struct CursorScratch {
 };
 
 // Sums every sequence's tiles and finds the block's first one.
-template <int THREADS, int ROWS, int TILE>
+template <int THREADS, int ROWS, int TILE, int OPEN>
 __device__ __forceinline__ Cursor find_cursor(const AttentionParams& a, int g, int blocks, CursorScratch& scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Cursor c;
-  const long long mine = sequence_tiles<ROWS, TILE>(a, threadIdx.x);
+  const long long mine = sequence_tiles<ROWS, TILE, OPEN>(a, threadIdx.x);
   long long sum = mine;
-  for (int b = threadIdx.x + THREADS; b < a.w.batch; b += THREADS) sum += sequence_tiles<ROWS, TILE>(a, b);
+  for (int b = threadIdx.x + THREADS; b < a.w.batch; b += THREADS) sum += sequence_tiles<ROWS, TILE, OPEN>(a, b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) scratch.warp[warp] = sum;
@@ -141,7 +146,7 @@ __device__ __forceinline__ Cursor find_cursor(const AttentionParams& a, int g, i
   if (c.at >= c.end) return c;
   long long base = 0;
   for (int b0 = 0; b0 < a.w.batch; b0 += THREADS) {
-    const long long n = b0 == 0 ? mine : sequence_tiles<ROWS, TILE>(a, b0 + threadIdx.x);
+    const long long n = b0 == 0 ? mine : sequence_tiles<ROWS, TILE, OPEN>(a, b0 + threadIdx.x);
     long long x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -170,11 +175,11 @@ __device__ __forceinline__ Cursor find_cursor(const AttentionParams& a, int g, i
   long long left = c.at - scratch.before;
   c.span = kv_span(a.w, c.b);
   for (c.rt = 0;; ++c.rt) {
-    const int n = item_tiles<ROWS, TILE>(a, c.span, c.rt);
+    const int n = OPEN + item_tiles<ROWS, TILE>(a, c.span, c.rt);
     const long long all = static_cast<long long>(n) * a.w.kv_heads;
     if (left < all) {
       c.h = static_cast<int>(left / n);
-      c.tile = static_cast<int>(left - static_cast<long long>(c.h) * n);
+      c.tile = static_cast<int>(left - static_cast<long long>(c.h) * n) - OPEN;
       break;
     }
     left -= all;
@@ -183,10 +188,10 @@ __device__ __forceinline__ Cursor find_cursor(const AttentionParams& a, int g, i
 }
 
 // The next item, `done` tiles on (which end an item).
-template <int ROWS>
+template <int ROWS, int OPEN>
 __device__ __forceinline__ void next_item(const AttentionParams& a, Cursor& c, int done) {
   c.at += done;
-  c.tile = 0;
+  c.tile = -OPEN;
   if (c.at >= c.end) return;
   if (++c.h < a.w.kv_heads) return;
   c.h = 0;
@@ -195,6 +200,18 @@ __device__ __forceinline__ void next_item(const AttentionParams& a, Cursor& c, i
   do {
     c.span = kv_span(a.w, ++c.b);
   } while (row_tiles<ROWS>(a, c.span) == 0);  // ends: at < total, so a sequence with tiles follows
+}
+
+// Tiles of the block's range that are not empty.
+template <int ROWS, int TILE, int OPEN>
+__device__ __forceinline__ long long full_tiles(const AttentionParams& a, Cursor c) {
+  long long t = 0;
+  while (c.at < c.end) {
+    const int done = static_cast<int>(min(static_cast<long long>(item_tiles<ROWS, TILE>(a, c.span, c.rt) - c.tile), c.end - c.at));
+    t += max(c.tile + done, 0) - max(c.tile, 0);
+    next_item<ROWS, OPEN>(a, c, done);
+  }
+  return t;
 }
 
 // The block that takes tile t: the largest g with g T / G <= t.
