@@ -34,6 +34,7 @@ SV_ROW_BAD_PAGE = 64
 SV_ROW_BAD_LENGTH = 128
 SV_ROW_NOT_FINITE = 256
 SV_ROW_BAD_PATH = 512
+SV_ROW_TIMEOUT = 1024
 
 SV_MAX_GAMMA = 64
 SV_MAX_VOCAB = 16777216

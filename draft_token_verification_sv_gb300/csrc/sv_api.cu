@@ -85,7 +85,7 @@ bool sample_desc_ok(const sv_sample_desc* d) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int64_t kMaxStride = int64_t{1} << 40;
+constexpr int64_t kMaxStride = (int64_t{1} << 40) - 1;  // what a tensor map can hold
 
 bool kv_desc_ok(const sv_kv_desc* d) {
   if (!d) return false;

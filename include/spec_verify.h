@@ -432,7 +432,7 @@ typedef struct sv_kv_desc {
   int64_t page_stride;   /* codes between pages, heads and tokens of a page: */
   int64_t head_stride;   /*   multiples of 16 (the pointers are 16-byte      */
   int64_t token_stride;  /*   aligned), token_stride and head_stride >= D    */
-  int64_t table_stride;  /* entries between page_table rows, >= max_pages */
+  int64_t table_stride;  /* entries between page_table rows, >= max_pages; all strides < 2^40 */
 } sv_kv_desc;
 
 /* The new tokens' rows.  Strides in elements between rows and between heads
@@ -472,7 +472,8 @@ sv_status sv_kv_append(const sv_kv_desc* desc, const sv_kv_rows_desc* rows, cons
 /*
  * Read tokens first[b] .. first[b] + n_b - 1 of every sequence back:
  * code * scale, rounded to rows->dtype, into k and v (rows as above, first
- * in the place of ctx_lens).
+ * in the place of ctx_lens).  Tokens on a bad page, and the rows of a
+ * sequence flagged SV_ROW_BAD_LENGTH where they are known, are read as 0.
  */
 sv_status sv_kv_read(const sv_kv_desc* desc, const sv_kv_rows_desc* rows, const uint8_t* k_cache,
                      const uint8_t* v_cache, const float* k_scale, const float* v_scale,
