@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
       f[2] = u.z;
       f[3] = u.w;
     };
-    uint32_t q[S::kQueriesStay ? MT : 1][S::kQueriesStay ? NQ : 1][4][4], q_rest[SPLIT ? MT : 1][SPLIT ? NQ : 1][4][4];
+    uint32_t q[S::kQueriesStay ? MT : 1][S::kQueriesStay ? NQ : 1][4][4], q_rest[SPLIT && S::kQueriesStay ? MT : 1][SPLIT && S::kQueriesStay ? NQ : 1][4][4];
     float factor[MT][2];  // scores in base 2 = factor * key scale * product, factor >= 0
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -327,6 +327,11 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
               load_queries(mt, i, j, 0, f);
 #pragma unroll
               for (int n = 0; n < 2; ++n) mma(x[mt][n], f[0], f[1], f[2], f[3], keys[n][j][0], keys[n][j][1]);
+              if constexpr (SPLIT) {
+                load_queries(mt, i, j, 1, f);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) mma(x[mt][n], f[0], f[1], f[2], f[3], keys[n][j][0], keys[n][j][1]);
+              }
             }
         } else {
 #pragma unroll
@@ -566,10 +571,9 @@ size_t workspace_for() {
 }
 
 // Calls f with the kernel's template arguments as types: one tile of 16 rows,
-// or two where a kv head has more rows (32 rows of 128 dims on contexts of up to
-// 32768 tokens: 165 us against 235 for one tile, which reads the cache twice).
-// Longer rows, and fp32 ones of more than 64 dims, have one tile: their sums
-// alone fill the registers.
+// or two where a kv head has more rows and the sums fit the registers (32 rows
+// of 128 dims on contexts of up to 32768 tokens: 165 us against 235 for one tile,
+// which reads the cache twice; 2000 tokens of a prompt in fp32 1496 against 1891).
 template <typename F>
 auto with_shape(const sv_kv_attention_desc& d, F f) {
   const bool two = static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 16;
@@ -580,7 +584,8 @@ auto with_shape(const sv_kv_attention_desc& d, F f) {
     return f(uint16_t{}, Int<256>{}, Int<1>{});
   }
   if (dp == 64) return two ? f(float{}, Int<64>{}, Int<2>{}) : f(float{}, Int<64>{}, Int<1>{});
-  return dp == 128 ? f(float{}, Int<128>{}, Int<1>{}) : f(float{}, Int<256>{}, Int<1>{});
+  if (dp == 128) return two ? f(float{}, Int<128>{}, Int<2>{}) : f(float{}, Int<128>{}, Int<1>{});
+  return f(float{}, Int<256>{}, Int<1>{});
 }
 
 }  // namespace
