@@ -142,7 +142,7 @@ def _new(new_start, max_new, m: _Meta, B):
     _int32(new_start, "new_start", B + 1, "one entry more than page_table has rows")
     if max_new is None:
         raise ValueError("new_start needs max_new, the largest number of new tokens of a sequence")
-    return int(max_new)
+    return max_new
 
 
 _PER_SEQUENCE = "one entry for each sequence"
@@ -205,7 +205,7 @@ def _attention_plan(q, kc, vc, ks, vs, table, lens, start, max_new, parents, sca
         raise ValueError("out must match q in shape and dtype")
     _, _, _, o_row, o_head = _rows(out, "out", B, ragged)
     a = N.KvAttentionDesc(d, heads, _new(start, max_new, q, B), n, _code(q),
-                          float(scale) if scale is not None else dim ** -0.5, int(window), int(sinks), 0, q_row, q_head,
+                          dim ** -0.5 if scale is None else scale, window, sinks, 0, q_row, q_head,
                           o_row, o_head)
     _int32(status, "row_status", B, _PER_SEQUENCE)
     return ctypes.byref(a), N.lib().sv_kv_attention_workspace_size(ctypes.byref(a))
@@ -228,7 +228,7 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, page_table: torch.T
     and returns ``cache``; ``row_status`` [B] int32 receives the flags."""
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     d, r = _append_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(k), _meta(v),
-                        _meta(new_start), max_new, _meta(row_status))
+                        _meta(new_start), None if max_new is None else int(max_new), _meta(row_status))
     st = N.lib().sv_kv_append(d, r, k.data_ptr(), v.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start),
                               kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), _at(row_status),
                               _stream_of(stream, kc))
@@ -301,7 +301,8 @@ def kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, ctx_len
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=device)
     a, need = _attention_plan(_meta(q), _meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens),
-                              _meta(new_start), max_new, _meta(parents), scale, window, sinks, _meta(out), _meta(row_status))
+                              _meta(new_start), None if max_new is None else int(max_new), _meta(parents),
+                              None if scale is None else float(scale), int(window), int(sinks), _meta(out), _meta(row_status))
     sums = torch.empty(q.shape[:-1], dtype=torch.float32, device=device) if lse else None
     raw = _stream_of(stream, q)
     if ws is None:
