@@ -594,40 +594,35 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
     uint16_t* out = static_cast<uint16_t*>(a.out) + out_row * a.out_row_stride + head * a.out_head_stride;
     float* part = a.parts + (2 * static_cast<int64_t>(g) + (p.tile0 == 0 ? 1 : 0)) * T::kPart;
 #pragma unroll 1
-    for (int d = group * kDims; d < (group + 1) * kDims; d += 32) {
-      uint32_t x[32], y[32];
-      if (own) tc::tmem_load32(own_o + d, x);
-      if (other) tc::tmem_load32(mine + T::kO + (group ^ 1) * DP + d, y);
+    for (int d = group * kDims; d < (group + 1) * kDims; d += 16) {  // (short: code that runs once a part is fetched anew)
+      uint32_t x[16], y[16];
+      if (own) tc::tmem_load16(own_o + d, x);
+      if (other) tc::tmem_load16(mine + T::kO + (group ^ 1) * DP + d, y);
       tc::wait_loads(x);
       tc::wait_loads(y);
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
+      for (int k = 0; k < 16; ++k)
         x[k] = __float_as_uint((own ? __uint_as_float(x[k]) * scale : 0.0f) + (other ? __uint_as_float(y[k]) * their_scale : 0.0f));
-      if (complete) {
+      if (r < p.rows && !complete) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t o[8];
 #pragma unroll
-          for (int n = 0; n < 8; ++n) o[n] = floats_to_bf16x2(__uint_as_float(x[16 * k + 2 * n]), __uint_as_float(x[16 * k + 2 * n + 1]));
-          if (r < p.rows && d + 16 * k < a.w.dim) {
-            if (a.out_vec32) {
-              tc::store_32(out + d + 16 * k, o);
-            } else {
-#pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                out[d + 16 * k + 2 * n] = static_cast<uint16_t>(o[n]);
-                out[d + 16 * k + 2 * n + 1] = static_cast<uint16_t>(o[n] >> 16);
-              }
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[8];
-#pragma unroll
           for (int n = 0; n < 8; ++n) o[n] = x[8 * k + n];
-          if (r < p.rows) tc::store_32(part + r * DP + d + 8 * k, o);
+          tc::store_32(part + r * DP + d + 8 * k, o);
+        }
+      } else if (r < p.rows && d < a.w.dim) {
+        uint32_t o[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) o[n] = floats_to_bf16x2(__uint_as_float(x[2 * n]), __uint_as_float(x[2 * n + 1]));
+        if (a.out_vec32) {
+          tc::store_32(out + d, o);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            out[d + 2 * n] = static_cast<uint16_t>(o[n]);
+            out[d + 2 * n + 1] = static_cast<uint16_t>(o[n] >> 16);
+          }
         }
       }
       __syncwarp();

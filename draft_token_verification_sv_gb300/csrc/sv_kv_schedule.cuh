@@ -101,6 +101,7 @@ __device__ __forceinline__ long long sequence_tiles(const AttentionParams& a, in
   const KvSpan s = kv_span(a.w, b);
   const int rts = row_tiles<ROWS>(a, s);
   long long t = 0;
+#pragma unroll 1
   for (int rt = 0; rt < rts; ++rt) t += OPEN + item_tiles<ROWS, TILE>(a, s, rt);
   return t * a.w.kv_heads;
 }
@@ -128,6 +129,7 @@ __device__ __forceinline__ Cursor find_cursor(const AttentionParams& a, int g, i
   Cursor c;
   const long long mine = sequence_tiles<ROWS, TILE, OPEN>(a, threadIdx.x);
   long long sum = mine;
+#pragma unroll 1
   for (int b = threadIdx.x + THREADS; b < a.w.batch; b += THREADS) sum += sequence_tiles<ROWS, TILE, OPEN>(a, b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -145,6 +147,7 @@ __device__ __forceinline__ Cursor find_cursor(const AttentionParams& a, int g, i
   c.b = c.rt = c.h = c.tile = 0;
   if (c.at >= c.end) return c;
   long long base = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.w.batch; b0 += THREADS) {
     const long long n = b0 == 0 ? mine : sequence_tiles<ROWS, TILE, OPEN>(a, b0 + threadIdx.x);
     long long x = n;
@@ -174,6 +177,7 @@ __device__ __forceinline__ Cursor find_cursor(const AttentionParams& a, int g, i
   c.b = scratch.b;
   long long left = c.at - scratch.before;
   c.span = kv_span(a.w, c.b);
+#pragma unroll 1
   for (c.rt = 0;; ++c.rt) {
     const int n = OPEN + item_tiles<ROWS, TILE>(a, c.span, c.rt);
     const long long all = static_cast<long long>(n) * a.w.kv_heads;
@@ -197,6 +201,7 @@ __device__ __forceinline__ void next_item(const AttentionParams& a, Cursor& c, i
   c.h = 0;
   if (++c.rt < row_tiles<ROWS>(a, c.span)) return;
   c.rt = 0;
+#pragma unroll 1
   do {
     c.span = kv_span(a.w, ++c.b);
   } while (row_tiles<ROWS>(a, c.span) == 0);  // ends: at < total, so a sequence with tiles follows
@@ -206,6 +211,7 @@ __device__ __forceinline__ void next_item(const AttentionParams& a, Cursor& c, i
 template <int ROWS, int TILE, int OPEN>
 __device__ __forceinline__ long long full_tiles(const AttentionParams& a, Cursor c) {
   long long t = 0;
+#pragma unroll 1
   while (c.at < c.end) {
     const int done = static_cast<int>(min(static_cast<long long>(item_tiles<ROWS, TILE>(a, c.span, c.rt) - c.tile), c.end - c.at));
     t += max(c.tile + done, 0) - max(c.tile, 0);
@@ -222,11 +228,13 @@ __device__ __forceinline__ int tile_owner(long long t, long long total, int bloc
 // Status bits of the sequences that this block looks after.
 __device__ __forceinline__ void flag_sequences(const AttentionParams& a, int g, int blocks, int threads) {
   if (!a.w.status) return;
+#pragma unroll 1
   for (int b = g; b < a.w.batch; b += blocks) {
     const KvSpan s = kv_span(a.w, b);
     if (!s.ok && threadIdx.x == 0) kv_flag(a.w, b, SV_ROW_BAD_LENGTH);
     if (!a.parents || !s.ok) continue;
     const int32_t* p = a.parents + s.row0;
+#pragma unroll 1
     for (int i = threadIdx.x; i < s.n; i += threads) {
       const int t = __ldg(p + i);
       if (i == 0 ? t != -1 : (t < 0 || t >= i)) kv_flag(a.w, b, SV_ROW_BAD_PARENT);
@@ -243,6 +251,7 @@ __device__ __forceinline__ bool sees(const AttentionParams& a, const int32_t* pa
       if (t > i) return false;
     } else {
       int u = i, back = 0;
+#pragma unroll 1
       while (u > t) u = tree_parent(parents, u), ++back;
       if (u != t) return false;
       at = pos - back;
@@ -303,6 +312,7 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(AttentionParams 
   const int g = blockIdx.x;
   const JoinRecord j = a.joins[g];
   constexpr int kPart = ROWS * (DP + 2);
+#pragma unroll 1
   for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < j.rows * (DP / 4); i += blockDim.x * gridDim.y) {
     const int r = i / (DP / 4), d4 = i % (DP / 4);
     const auto part = [&](int k) { return a.parts + (2 * static_cast<int64_t>(k) + (k == g ? 1 : 0)) * kPart; };
