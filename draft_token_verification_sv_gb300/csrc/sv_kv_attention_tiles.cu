@@ -577,7 +577,8 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
     if (!meet()) return false;
     const float* theirs = sh.exchange[group ^ 1][r];
     const float their_m = theirs[0], their_l = theirs[1], their_v = theirs[2];
-    const bool own = begin < end, other = p.count > 1 || !own;
+    // masks: what a group without a tile of the part has in O is of another
+    const uint32_t own = begin < end ? ~0u : 0u, other = p.count > 1 || !own ? ~0u : 0u;
     // the last tiles' products: all before them are done then
     if (!wait(sh.pv_done[(end - 1) % kValueStages], (end - 1) / kValueStages)) return false;
     if (!meet()) return false;  // (the exchange is free again)
@@ -588,7 +589,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
     const float total = (l * fix + their_l * their_fix) * lift;
     const bool complete = p.count == p.tiles;
     const float inv = !complete ? lift : total == 0.0f ? 0.0f : lift / total;
-    const float scale = fix * ex2(v_ref) * inv, their_scale = their_fix * ex2(their_v) * inv;
+    const float scale = own ? fix * ex2(v_ref) * inv : 0.0f, their_scale = other ? their_fix * ex2(their_v) * inv : 0.0f;
     const int head = p.h * a.group + (p.r0 + min(r, p.rows - 1)) % a.group;
     const int64_t out_row = static_cast<int64_t>(p.row0) + token;
     uint16_t* out = static_cast<uint16_t*>(a.out) + out_row * a.out_row_stride + head * a.out_head_stride;
@@ -596,13 +597,13 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
 #pragma unroll 1
     for (int d = group * kDims; d < (group + 1) * kDims; d += 16) {  // (short: code that runs once a part is fetched anew)
       uint32_t x[16], y[16];
-      if (own) tc::tmem_load16(own_o + d, x);
-      if (other) tc::tmem_load16(mine + T::kO + (group ^ 1) * DP + d, y);
+      tc::tmem_load16(own_o + d, x);
+      tc::tmem_load16(mine + T::kO + (group ^ 1) * DP + d, y);
       tc::wait_loads(x);
       tc::wait_loads(y);
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        x[k] = __float_as_uint((own ? __uint_as_float(x[k]) * scale : 0.0f) + (other ? __uint_as_float(y[k]) * their_scale : 0.0f));
+        x[k] = __float_as_uint(fmaf(__uint_as_float(x[k] & own), scale, __uint_as_float(y[k] & other) * their_scale));
       if (r < p.rows && !complete) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
