@@ -50,12 +50,14 @@ constexpr int kValueStages = 4;  // of widened values,
 constexpr int kScoreStages = 3;  // and of scores in tensor memory
 constexpr int kLag = 2;          // tiles that scores are formed ahead of the sums over values
 
+constexpr int kPiece = 80;       // 64 bytes of a row of queries, at a pitch free of bank conflicts
+
 template <int DP> struct Tiles {
   static constexpr int kKeyBytes = kTokens * 128;          // a tile's keys: rows of 128 bytes (DP = 64 leaves half)
   static constexpr int kCodeBytes = kTokens * DP;          // its values' codes as they come,
   static constexpr int kValueBytes = kTokens * DP * 2;     // and in fp16,
   static constexpr int kBlockBytes = kTokens * 128;        // in blocks of 64 dims
-  static constexpr int kOperands = kValueStages * kValueBytes + kCodeStages * (kKeyBytes + kCodeBytes);
+  static constexpr int kOperands = kValueStages * kValueBytes + kCodeStages * (kKeyBytes + kCodeBytes) + kSoftmaxWarps * 32 * kPiece;
   // 1 KB to find a 1024-byte boundary; more than half of an SM's shared memory keeps it to one block
   static constexpr int kShared = (kOperands > 118 * 1024 ? kOperands : 118 * 1024) + 1024;
   // tensor memory, in columns: two O, both parts of Q, three tiles of scores
@@ -387,12 +389,13 @@ __device__ __forceinline__ float2 weights32(const uint32_t (&x)[32], uint32_t se
 }
 
 template <int DP>
-__device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& sh, uint32_t tmem, int g) {
+__device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& sh, uint8_t* staging, uint32_t tmem, int g) {
   using T = Tiles<DP>;
   constexpr int kDims = DP / 2;  // a thread's share of a row of queries and results
-  const int r = threadIdx.x & (kRows - 1), group = threadIdx.x / kRows, quarter = (threadIdx.x >> 5) & 3;
+  const int r = threadIdx.x & (kRows - 1), group = threadIdx.x / kRows, quarter = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t mine = tmem + (quarter << 21);  // the warp's 32 lanes
   const uint32_t own_o = mine + T::kO + group * DP;
+  staging += (threadIdx.x >> 5) * 32 * kPiece;
   const auto wait = [&](uint64_t& bar, int n) {
     const bool ok = warp_wait(sh, bar, n);
     tc::fence_after();
@@ -424,18 +427,35 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
                           head * a.q_head_stride + group * kDims;
       uint4 raw[kDims / 8];
       uint32_t top = 0;
+      if (a.q_vec) {  // 8 rows' pieces of 64 bytes at a time: a lane that loads its own row alone touches a line for each 16 bytes
+        uint64_t from[4];
 #pragma unroll
-      for (int i = 0; i < kDims / 8; ++i) {
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (r < p.rows && group * kDims + i * 8 < a.w.dim) {
-          if (a.q_vec) {
-            raw[i] = *reinterpret_cast<const uint4*>(q + i * 8);
-          } else {
+        for (int i = 0; i < 4; ++i) from[i] = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(q), 8 * i + (lane >> 2)) + 16 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < kDims / 8; ++i) {
+          const bool live = 32 * quarter + 8 * (i & 3) + (lane >> 2) < p.rows && group * kDims + 32 * (i >> 2) + 8 * (lane & 3) < a.w.dim;
+          raw[i] = live ? *reinterpret_cast<const uint4*>(from[i & 3] + 64 * (i >> 2)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < kDims / 32; ++n) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(staging + (8 * i + (lane >> 2)) * kPiece + 16 * (lane & 3)) = raw[4 * n + i];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) raw[4 * n + i] = *reinterpret_cast<const uint4*>(staging + lane * kPiece + 16 * i);
+          __syncwarp();
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kDims / 8; ++i) {
+          raw[i] = make_uint4(0, 0, 0, 0);
+          if (r < p.rows && group * kDims + i * 8 < a.w.dim) {
             const uint16_t* e = q + i * 8;
             raw[i] = make_uint4(__ldg(e) | __ldg(e + 1) << 16, __ldg(e + 2) | __ldg(e + 3) << 16,
                                 __ldg(e + 4) | __ldg(e + 5) << 16, __ldg(e + 6) | __ldg(e + 7) << 16);
           }
         }
+        __syncwarp();
       }
 #pragma unroll
       for (int i = 0; i < kDims / 8; ++i) {
@@ -693,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   bool ok = true;
   if (warp < kSoftmaxWarps) {
     tc::registers_up<kSoftmaxRegisters>();
-    ok = softmax_role<DP>(a, tiles_here, sh, tmem, g);
+    ok = softmax_role<DP>(a, tiles_here, sh, codes + kCodeStages * T::kCodeBytes, tmem, g);
   } else if (warp < kSoftmaxWarps + kValueWarps) {
     tc::registers_down<kValueRegisters>();
     ok = value_role<DP>(tiles_here, sh, v_tiles, codes);
