@@ -33,9 +33,9 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kTileSteps = 4;
 constexpr int kTokens = kStep * kTileSteps;
-// Empty tiles ahead of an item: 64 trees of 32 nodes on contexts of up to 4096 tokens take 169 us without, 140 with 6, 135 with 12
-// and 137 with 20, prompt chunks 385, 376, 374 and 382.
-constexpr int kOpen = 12;
+// Empty tiles ahead of an item: none, 5, 8 and 12 take 153, 135, 124 and 124 us for 64 trees of 32 nodes on contexts of up to
+// 4096 tokens, 370, 364, 367 and 370 for 2000 tokens of two prompts behind 4096, 367, 220, 197 and 201 for 16 prompts of 836.
+constexpr int kOpen = 8;
 // weights: warps 0-7; values: 8-11; products: 12; plan: 13; fetch: 14 (15 idle: registers move in fours of warps)
 constexpr int kSoftmaxWarps = 8, kValueWarps = 4;
 constexpr int kValueThreads = 32 * kValueWarps;
