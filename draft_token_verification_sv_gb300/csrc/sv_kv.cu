@@ -104,6 +104,10 @@ struct AppendRows {
   int64_t row_stride[2], head_stride[2];
 };
 
+// Bound by HBM where there is much: 24,000 prompt tokens of 8 heads of 128 dims
+// take 58 us, 5.4 TB/s read and written, 80% of a copy's rate (the largest value
+// of a page is known before its first code is written, so a block's loads and
+// stores do not overlap); one token for each of 64 sequences 4.6 us of latency.
 // One block per (touched page, head, K or V), heads first: blocks that run
 // together read and write what lies together in the rows of new tokens (the
 // other way round 24,000 prompt tokens took 82 us).  The new tokens of the page
@@ -219,6 +223,8 @@ __device__ __forceinline__ void store_codes16(const uint4& c, float s, E* to) {
   }
 }
 
+// Bound by HBM: 2 x 65537 tokens of 8 heads of 128 dims take 108 us, 6.0 TB/s
+// read and written, 89% of a copy's rate; one short stretch 8 us of latency.
 // One block per (tile of kTile tokens, head, sequence); a thread takes the
 // same 16 codes of every rows_per_pass-th token, keys and values.
 template <typename E, int THREADS, bool VEC>
@@ -254,6 +260,8 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(KvView w, ReadRows row
 
 constexpr int kMaxPath = SV_MAX_TREE_DEPTH + 1;
 
+// Bound by its chain of dependent loads (length, path, page, codes, scale): 64
+// trees of depth 5 take 6.2 us, 256 of depth 16 8.3.
 // One block per (head and K or V, sequence): the path's codes go to shared
 // memory, then each page they land in is written by append's rule.
 template <int THREADS>

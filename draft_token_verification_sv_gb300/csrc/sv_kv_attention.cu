@@ -4,10 +4,22 @@
 // O = sum_j 2^(s_j - m) v_j, one pass over the visible tokens with a running
 // maximum m for each row.  Both products run on the tensor cores
 // (m16n8k16): the 16 rows (or two times 16) are the query heads that share a
-// kv head (times the new tokens), the codes are widened to fp16, which holds every e4m3 value,
-// and queries and weights are fp16 (a power of two for each row keeps queries
-// in range; fp32 queries and weights are the sum of two fp16).  Scales of K
-// and V are one factor for each page, on scores and weights.
+// kv head (times the new tokens), the codes are widened to fp16, which holds
+// every e4m3 value, and queries and weights are fp16 (a power of two for each
+// row keeps queries in range; fp32 queries and weights are the sum of two fp16,
+// bf16 queries fit one, and their weights are rounded to 2^-11, an eighth of
+// what the result's type keeps).  Scales of K and V are one factor for each
+// page, on scores and weights.  Sums and statistics are fp32.
+//
+// A warp streams its own steps of 16 tokens through its own ring of
+// asynchronous copies, so that no barrier stands between a block's four warps;
+// they are joined where an item ends.  A 16-row tile that reads the whole cache
+// is bound by HBM (a step of 64 sequences of up to 8192 tokens, 8 kv heads of
+// 128 dims: 112 us, 5.5 TB/s, 81% of a copy's rate); two tiles by the
+// instructions that widen codes and weigh scores (chains of 8 on up to 32768
+// tokens: 157 us, 3.7 TB/s); short calls by latency (500 tokens of one
+// sequence: 9.7 us with the join, of which about 8 pass before the first
+// product when nothing is in the caches).
 #include "sv_kv_schedule.cuh"
 
 #include <type_traits>
@@ -571,9 +583,10 @@ size_t workspace_for() {
 }
 
 // Calls f with the kernel's template arguments as types: one tile of 16 rows,
-// or two where a kv head has more rows and the sums fit the registers (32 rows
-// of 128 dims on contexts of up to 32768 tokens: 165 us against 235 for one tile,
-// which reads the cache twice; 2000 tokens of a prompt in fp32 1496 against 1891).
+// or two where a kv head has more rows and the sums fit the registers.  Chains
+// of 8 (32 rows) on contexts of up to 32768 tokens take 157 us with two tiles
+// and 193 with one, which reads the cache twice, at 64 dims 102 and 126; 2000
+// tokens of a prompt in fp32 1496 and 1891.
 template <typename F>
 auto with_shape(const sv_kv_attention_desc& d, F f) {
   const bool two = static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 16;

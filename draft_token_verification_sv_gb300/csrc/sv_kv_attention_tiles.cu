@@ -21,6 +21,12 @@
 // themselves.  Weights would need more: a long even tail of a softmax lies
 // below e4m3's range, so P V is fp16.
 // Work is shared out as in sv_kv_schedule.cuh.
+//
+// 2000 tokens of two prompts behind 4096 cached ones, 32 heads of 128 dims: 364
+// us, 805 TFLOP/s of useful work, bound by the step from scores to weights (two
+// tiles of it under way at a time, 1.4 thousand cycles each) and what each step
+// of a tile waits for the other.  64 trees of 32 nodes on up to 4096 tokens: 124
+// us, 2.7 TB/s, a fifth of it spent at the ends of items.
 #include "sv_kv_schedule.cuh"
 #include "sv_tcgen05.cuh"
 
@@ -802,9 +808,10 @@ sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspa
 }  // namespace
 
 // More rows of a kv head than the other kernel's two tiles of 16.  Rows are
-// padded to 128 here, which costs more than it gives up to 32 of them: on
-// contexts of up to 32768 tokens 188 us against 165 at 128 dims, 170 against 117
-// at 64.  From 33 on the other kernel would read the cache twice.
+// padded to 128 here, which costs more than it gives up to 32 of them: chains of
+// 8 (32 rows) on contexts of up to 32768 tokens take 171 us here and 157 there at
+// 128 dims, 169 and 102 at 64.  From 33 on the other kernel reads the cache
+// twice: chains of 12 (48 rows) take 173 us here and 283 there.
 bool kv_attention_takes_tiles(const sv_kv_attention_desc& d) {
   return d.dtype == SV_BF16 && d.kv.head_dim <= 128 &&
          static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 32;
