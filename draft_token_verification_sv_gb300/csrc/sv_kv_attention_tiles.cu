@@ -100,7 +100,7 @@ struct Shared {
   uint64_t plan_full[kPlans], plan_free[kPlans], part_full[kParts], part_free[kParts];
   uint64_t codes_full[kCodeStages], codes_free[kCodeStages];
   uint64_t pv_ready[kValueStages], pv_done[kValueStages], s_full[kScoreStages], q_ready, last, both[4];
-  float exchange[2][kRows][3];  // between the two threads of a row
+  float exchange[2][kRows][4];  // between the two threads of a row: maximum, sum, values' unit; the queries' largest
   TilePlan plan[kPlans];
   Part part[kParts];
   uint32_t tmem;
@@ -469,10 +469,10 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
         top = __vmaxu2(__vmaxu2(top, raw[i].z & 0x7fff7fffu), raw[i].w & 0x7fff7fffu);
       }
       top = max(top >> 16, top & 0xffffu);
-      // (the last part's exchange has been read by both: each came here from its second meeting)
-      sh.exchange[group][r][0] = __uint_as_float(top);
+      // (read before the row's second meeting, so free for the next part; the other three before its next first one)
+      sh.exchange[group][r][3] = __uint_as_float(top);
       if (!meet()) return false;
-      top = max(top, __float_as_uint(sh.exchange[group ^ 1][r][0]));
+      top = max(top, __float_as_uint(sh.exchange[group ^ 1][r][3]));
       const int exponent = static_cast<int>(top >> 7);
       const int e = exponent == 255 || top == 0 ? 0 : min(120, 134 - exponent);
       // the largest becomes 2^7 .. 2^8; a negative factor goes into the queries, so that larger products are larger scores
@@ -607,7 +607,6 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
     const uint32_t own = begin < end ? ~0u : 0u, other = p.count > 1 || !own ? ~0u : 0u;
     // the last tiles' products: all before them are done then
     if (!wait(sh.pv_done[(end - 1) % kValueStages], (end - 1) / kValueStages)) return false;
-    if (!meet()) return false;  // (the exchange is free again)
     const float top = fmaxf(m, their_m);
     const float lift = 1.0f / 256.0f;
     // (a group that saw nothing has sums of 0, or sums that are not numbers, which stay)
