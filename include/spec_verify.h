@@ -546,7 +546,10 @@ size_t sv_kv_attention_workspace_size(const sv_kv_attention_desc* desc);
  *   row_status  optional [B] int32 (SV_ROW_*).
  *
  * The cache's codes reach the tensor cores without loss and sums are held in
- * fp32.  NaN codes (0x7f, 0xff; sv_kv_append writes none) at visible tokens
+ * fp32.  Weights are fp16 (for float32 calls the sum of two): each is rounded
+ * to 2^-11 (2^-21) of itself, or to 2^-31 of its row's largest (both counted
+ * with the scales of V) where that is
+ * more.  NaN codes (0x7f, 0xff; sv_kv_append writes none) at visible tokens
  * are not supported; what lies behind a sequence's last token is not seen,
  * whatever its bytes.
  */

@@ -120,6 +120,67 @@ def test_long_contexts(sv, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,dim", [(2, 64), (6, 128), (16, 64), (12, 128)])
+def test_long_contexts_of_more_rows(sv, dtype, heads, dim):
+    """Items of up to 16, 32, 128 and more rows in parts of several blocks."""
+    g = np.random.default_rng(heads + dim)
+    _check(sv, g, dtype, dim, 64, heads, 1, [5003, 17, 0, 1203, 2600], [5, 4, 2, 5, 1] if heads < 8 else [11, 2, 4, 5, 3])
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 3), (100, 17), (7, 1000), (700, 4)])
+def test_window_and_sinks_of_many_rows(sv, tree, dim, window, sinks):
+    g = np.random.default_rng(window + sinks + dim)
+    _check(sv, g, "bf16", dim, 16, 8, 1, [0, 3, 50, 129, 1260], [9, 40, 7, 0, 12], tree=tree, window=window, sinks=sinks, layout="nhd")
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", 2), ("f32", 6), ("bf16", 12)])
+def test_more_sequences_than_threads(sv, dtype, heads):
+    """Empty sequences among them, and lengths from nothing on: the results of
+    calls of 50 sequences each, bit for bit (no sequence is in parts here)."""
+    import torch
+    g = np.random.default_rng(heads)
+    ctx, new = g.integers(0, 40, 700).astype(np.int32), g.integers(0, 4, 700).astype(np.int32)
+    new[:3] = new[300:420] = 0
+    table, pages = make_table(g, [int(n) for n in ctx + new], 16)
+    cache = cache_gpu(make_cache(g, pages, 1, 16, 64))
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = to_gpu(g.normal(0, 1.5, (int(start[-1]), heads, 64)).astype(np.float32), dtype)
+    out, lse = sv.kv_attention(q, cache, to_gpu(table), to_gpu(ctx), new_start=to_gpu(start), max_new=3, lse=True)
+    for b in range(0, 700, 50):
+        lo, hi = int(start[b]), int(start[b + 50])
+        some, sums = sv.kv_attention(q[lo:hi], cache, to_gpu(table[b:b + 50]), to_gpu(ctx[b:b + 50]),
+                                     new_start=to_gpu(start[b:b + 51] - lo), max_new=3, lse=True)
+        assert torch.equal(out[lo:hi], some) and torch.equal(lse[lo:hi], sums), b
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", 2), ("f32", 2), ("bf16", 6), ("f32", 6), ("bf16", 12)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_small_weights(sv, dtype, heads, dim):
+    """Scores that differ by more than fp16 weights can hold.  Weights are
+    multiplied by 2^6 at least against a row's largest and their steps end at
+    2^-24, so each is off by at most 2^-25 2^-6 of the largest, with the value's
+    code and the largest scale of V behind it.  (The weight of a token whose
+    rivals all hold exactly 0 in a dim is all that is left there.)"""
+    g = np.random.default_rng(heads + dim)
+    ctx, n, page = [1, 28, 300], 3, 16
+    table, pages = make_table(g, [c + n for c in ctx], page)
+    cache = make_cache(g, pages, 1, page, dim)
+    cache["v"][g.random(cache["v"].shape) < 0.3] = 0
+    q = round_to(g.normal(0, 4, (len(ctx), n, heads, dim)), dtype)
+    out = sv.kv_attention(to_gpu(q, dtype), cache_gpu(cache), to_gpu(table), to_gpu(np.array(ctx, np.int32))).double().cpu().numpy()
+    for b, c in enumerate(ctx):
+        want, _, absolute, largest = KO.attention(q[b].astype(np.float64), cache, table[b], page, c, None, dim ** -0.5, 0, 0)
+        tol, _ = attention_tolerance(want, absolute, largest, c + n, dim, dtype)
+        used = table[b, :-(-(c + n) // page)]
+        codes = np.abs(KO.read(dict(cache, v_scale=np.ones_like(cache["v_scale"])), "v", table[b], page, 0, c + n)).sum(0)[0]
+        tol += 2.0 ** -31 * cache["v_scale"][used].max() * codes
+        off = np.abs(out[b] - want)
+        assert (off <= tol).all(), (b, float((off / tol).max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("peak,spread,scale", [(0.0, 2, None), (40.0, 2, None), (1.5, 12, None), (1.5, 2, -0.3), (1.5, 2, 0.0), (1e-20, 2, 1e18), (3e4, 2, 1e-6)])
 def test_scores_and_scales(sv, dtype, peak, spread, scale):
     """Equal scores, scores that leave one token, page scales that differ by
