@@ -547,11 +547,10 @@ size_t sv_kv_attention_workspace_size(const sv_kv_attention_desc* desc);
  *
  * The cache's codes reach the tensor cores without loss and sums are held in
  * fp32.  Weights are fp16 (for float32 calls the sum of two): each is rounded
- * to 2^-11 (2^-21) of itself, or to 2^-31 of its row's largest (both counted
- * with the scales of V) where that is
- * more.  NaN codes (0x7f, 0xff; sv_kv_append writes none) at visible tokens
- * are not supported; what lies behind a sequence's last token is not seen,
- * whatever its bytes.
+ * to 2^-11 (2^-21) of itself, or to 2^-31 of its row's largest where that is
+ * more (both counted with the scales of V).  NaN codes (0x7f, 0xff;
+ * sv_kv_append writes none) at visible tokens are not supported; what lies
+ * behind a sequence's last token is not seen, whatever its bytes.
  */
 sv_status sv_kv_attention(const sv_kv_attention_desc* desc, const void* q, const uint8_t* k_cache,
                           const uint8_t* v_cache, const float* k_scale, const float* v_scale,
