@@ -105,12 +105,14 @@ def _kv_desc(k, v, ks, vs, table, lens, name) -> N.KvDesc:
     if table.dtype != torch.int32 or len(table.shape) != 2 or table.strides[1] != 1 and table.shape[1] > 1:
         raise ValueError("page_table must be an int32 [B, pages] tensor with contiguous rows")
     B, columns = table.shape
+    if B > 1 and table.strides[0] < columns:
+        raise ValueError("page_table rows overlap in memory (an expanded tensor? .contiguous() gives every sequence a row)")
     _int32(lens, name, B, "one entry for each row of page_table")
     pages, heads, page, dim = k.shape
     # a dimension of one entry is never stepped over: its stride may be anything
     step = [s if n > 1 else -(-max(s, dim) // 16) * 16 for n, s in zip(k.shape[:3], k.strides)]
     return N.KvDesc(B, heads, dim, page, pages, columns, step[0], step[1], step[2],
-                    max(table.strides[0], columns) if B > 1 else columns)
+                    table.strides[0] if B > 1 else columns)
 
 
 def _rows(m: _Meta, name: str, B: int, ragged: bool):
