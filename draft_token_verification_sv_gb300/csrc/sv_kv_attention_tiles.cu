@@ -69,8 +69,11 @@ template <int DP> struct Tiles {
   // tensor memory, in columns: two O, both parts of Q, three tiles of scores
   static constexpr int kO = 0, kQ = 2 * DP, kS = kQ + DP / 2;
   static constexpr int kColumns = 512;
-  static constexpr int kPart = kRows * (DP + 2);
+  static constexpr int kPart = kRows * (DP + 2);  // floats of a part in the workspace
+  static_assert(kPart * sizeof(float) % 32 == 0 && DP * sizeof(float) % 32 == 0, "parts are written 32 bytes at a time");
 };
+// Where the parts begin in the workspace, which callers align to 16 bytes: its size has room for rounding up.
+constexpr size_t kPartAlign = 32;
 
 constexpr int kPlans = 16;  // tiles that may be planned ahead
 constexpr int kParts = 4;  // parts of items that may be
@@ -790,7 +793,7 @@ sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspa
   const int64_t row_tiles = (static_cast<int64_t>(d.max_new) * a.group + kRows - 1) / kRows;
   const int64_t tiles = (static_cast<int64_t>(d.kv.max_pages) * d.kv.page_size + kTokens - 1) / kTokens;
   const int blocks = schedule_blocks(row_tiles * d.kv.batch * d.kv.kv_heads, tiles + kOpen, kSMs);
-  a.parts = static_cast<float*>(workspace);
+  a.parts = reinterpret_cast<float*>(align_up(reinterpret_cast<uintptr_t>(workspace), kPartAlign));
   a.joins = reinterpret_cast<JoinRecord*>(a.parts + 2 * static_cast<int64_t>(kSMs) * T::kPart);
   CUtensorMap keys, values;
   if (!cache_map(&keys, d.kv, a.w.c.k, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -818,7 +821,7 @@ bool kv_attention_takes_tiles(const sv_kv_attention_desc& d) {
 
 size_t kv_attention_tiles_workspace(const sv_kv_attention_desc& d) {
   const size_t part = d.kv.head_dim <= 64 ? Tiles<64>::kPart : Tiles<128>::kPart;
-  return align_up(kSMs * (2 * part * sizeof(float) + sizeof(JoinRecord)), 256);
+  return align_up(kPartAlign + kSMs * (2 * part * sizeof(float) + sizeof(JoinRecord)), 256);
 }
 
 sv_status kv_attention_tiles(AttentionParams a, const sv_kv_attention_desc& d, void* workspace, cudaStream_t stream) {

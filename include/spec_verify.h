@@ -517,8 +517,8 @@ typedef struct sv_kv_attention_desc {
   int64_t out_row_stride, out_head_stride;
 } sv_kv_attention_desc;
 
-/* Workspace bytes for sv_kv_attention (scratch, no initialisation); 0 for an
- * invalid descriptor. */
+/* Workspace bytes for sv_kv_attention (scratch on a 16-byte boundary, no
+ * initialisation); 0 for an invalid descriptor. */
 size_t sv_kv_attention_workspace_size(const sv_kv_attention_desc* desc);
 
 /*
