@@ -221,6 +221,18 @@ def _stream_of(stream, t) -> int:
     return stream.cuda_stream if stream is not None else _raw_stream(t.device.index)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A result that a call on ``stream`` writes and the current stream may
+    use: allocated on the one, so that no earlier use of its memory is still
+    under way there, and released behind the other."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, ctx_lens: torch.Tensor, *,
               new_start: torch.Tensor | None = None, max_new: int | None = None,
               row_status: torch.Tensor | None = None, stream=None) -> dict:
@@ -254,8 +266,7 @@ def kv_read(cache: dict, page_table: torch.Tensor, first: torch.Tensor, tokens: 
             raise ValueError("new_start needs total, the number of rows")
         else:
             shape = (int(total), heads, dim)
-        device = kc.device
-        k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
+        k, v = _empty(shape, dtype, kc.device, stream), _empty(shape, dtype, kc.device, stream)
     else:
         k, v = out
     d, r = _read_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(first), _meta(k), _meta(v),
@@ -276,7 +287,7 @@ def kv_commit(cache: dict, page_table: torch.Tensor, ctx_lens: torch.Tensor, pat
     [B] int32 and updates ``cache``."""
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     if new_lens is None:
-        new_lens = torch.empty_like(ctx_lens)
+        new_lens = _empty(ctx_lens.shape, ctx_lens.dtype, ctx_lens.device, stream)
     d, length = _commit_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(path),
                              _meta(accept_len), _meta(new_lens), _meta(row_status))
     st = N.lib().sv_kv_commit(d, int(nodes), length, page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
@@ -301,11 +312,11 @@ def kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, ctx_len
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     device = q.device
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        out = _empty(q.shape, q.dtype, device, stream)
     a, need = _attention_plan(_meta(q), _meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens),
                               _meta(new_start), None if max_new is None else int(max_new), _meta(parents),
                               None if scale is None else float(scale), int(window), int(sinks), _meta(out), _meta(row_status))
-    sums = torch.empty(q.shape[:-1], dtype=torch.float32, device=device) if lse else None
+    sums = _empty(q.shape[:-1], torch.float32, device, stream) if lse else None
     raw = _stream_of(stream, q)
     if ws is None:
         ws = _WORKSPACES.get((device.index, raw))

@@ -76,7 +76,9 @@ def workspace(nbytes: int, device: torch.device, stream=None) -> torch.Tensor:
     key = (device.index, s.cuda_stream)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        # on that stream: calls on it follow the fill, and what a workspace that grew gives back is used behind them
+        with torch.cuda.stream(s):
+            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
         _WORKSPACES[key] = ws
     return ws
 

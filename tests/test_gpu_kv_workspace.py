@@ -38,3 +38,29 @@ def test_any_workspace_on_a_16_byte_boundary(sv, dtype, heads, shift):
     got = sv.kv_attention(q, dev, to_gpu(table), lens, ws=whole[1024 + shift:1024 + shift + need])
     assert torch.equal(got, want)
     assert (whole[:1024 + shift] == 0xa5).all() and (whole[1024 + shift + need:] == 0xa5).all()
+
+
+@pytest.mark.parametrize("dtype,heads", [("bf16", 2), ("f32", 6), ("bf16", 12)])
+def test_stream_argument_beside_a_busy_current_stream(sv, dtype, heads):
+    """A first call on a stream, then one that needs a larger workspace, both
+    while the current stream is held up."""
+    import torch
+    g = np.random.default_rng(heads)
+    page, dim, n = 64, 128, 5
+    table, pages = make_table(g, [5003 + n], page)
+    dev = cache_gpu(make_cache(g, pages, 1, page, dim))
+    t, lens, zero, side = to_gpu(table), to_gpu(np.array([5003], np.int32)), to_gpu(np.zeros(1, np.int32)), torch.cuda.Stream()
+    for rows in (1, heads):
+        q = to_gpu(g.normal(0, 1, (1, n, rows, dim)).astype(np.float32), dtype)
+        want, sums = sv.kv_attention(q, dev, t, lens, lse=True)
+        back = sv.kv_read(dev, t, zero, 700)
+        spoilt = torch.empty(1 << 24, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+        spoilt.fill_(float("nan"))
+        del spoilt  # its memory is free for what the current stream allocates, and still to be written by it
+        got, lse = sv.kv_attention(q, dev, t, lens, lse=True, stream=side)
+        k, v = sv.kv_read(dev, t, zero, 700, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(lse, sums)
+        assert torch.equal(k, back[0]) and torch.equal(v, back[1])

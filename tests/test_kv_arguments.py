@@ -1,5 +1,7 @@
 """What the Python layer of the cache refuses and how it passes tensors on
 (no GPU: stand-ins that have a tensor's shape, strides, type and place)."""
+import math
+
 import pytest
 import torch
 
@@ -16,8 +18,8 @@ class Stand:
     """A CUDA tensor as the argument checks see it."""
 
     def __init__(self, shape, dtype=torch.float32, strides=None, device="cuda:0", address=1 << 20):
-        t = torch.empty(shape, dtype=dtype, device="meta")
-        self.shape, self.dtype, self._strides, self._address = t.shape, dtype, strides or t.stride(), address
+        self.shape, self.dtype, self._address = torch.Size(shape), dtype, address
+        self._strides = strides or tuple(math.prod(shape[i + 1:]) for i in range(len(shape)))
         self.device = torch.device(device)
         self.is_cuda = self.device.type == "cuda"
 
@@ -63,3 +65,65 @@ def test_rows_of_a_page_table_that_overlap_are_refused(call, strides):
     """An expanded row of page ids is not five rows of memory."""
     with pytest.raises(ValueError, match="page_table"):
         _calls(_ints(4, 5, strides=strides))[call]()
+
+
+@pytest.fixture
+def fake_streams(monkeypatch):
+    """torch's streams and allocations replaced by stand-ins: yields the list
+    of (stream that memory was allocated on, streams recorded on it)."""
+    import contextlib
+
+    from draft_token_verification_sv_gb300 import _native as N
+    current, made = ["main"], []
+
+    class Fake:
+        def __init__(self, name):
+            self.name, self.cuda_stream = name, hash(name) & 0xffff
+
+    class Made(Stand):
+        def record_stream(self, stream):
+            made[self.at][1].append(stream.name)
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(stream.name)
+        yield
+        current.pop()
+
+    def allocate(shape, dtype=torch.float32, device="cuda:0"):
+        t = Made((shape,) if isinstance(shape, int) else shape, dtype)
+        t.at = len(made)
+        made.append((current[-1], []))
+        return t
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: 1000 if name.endswith("size") else N.SV_OK
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Fake("main"))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch, "empty", allocate)
+    monkeypatch.setattr(torch, "zeros", allocate)
+    monkeypatch.setattr(N, "lib", Lib)
+    monkeypatch.setattr(sv.verify, "_WORKSPACES", {})
+    monkeypatch.setattr(sv.kvcache, "_WORKSPACES", sv.verify._WORKSPACES)
+    for plan in (sv.kvcache._append_plan, sv.kvcache._read_plan, sv.kvcache._commit_plan, sv.kvcache._attention_plan):
+        plan.cache_clear()
+    yield Fake, made
+    sv.kvcache._attention_plan.cache_clear()
+
+
+def test_results_and_workspaces_belong_to_the_calls_stream(fake_streams):
+    """With stream=, memory is allocated there (a fill of the workspace and
+    earlier users of the memory are then ordered with the call), and results
+    are kept until the current stream is done with them."""
+    Fake, made = fake_streams
+    side, cache, q = Fake("side"), _cache(), Stand((4, 3, 8, 64))
+    sv.kv_attention(q, cache, _ints(4, 5), _ints(4), lse=True, stream=side)
+    assert sorted(made) == [("side", []), ("side", ["main"]), ("side", ["main"])]  # workspace, out, lse
+    made.clear()
+    sv.kv_attention(q, cache, _ints(4, 5), _ints(4), lse=True, stream=side)
+    assert made == [("side", ["main"])] * 2
+    made.clear()
+    sv.kv_read(cache, _ints(4, 5), _ints(4), 3, stream=side)
+    sv.kv_commit(cache, _ints(4, 5), _ints(4), _ints(4, 5), _ints(4), 8, stream=side)
+    assert made == [("side", ["main"])] * 3
