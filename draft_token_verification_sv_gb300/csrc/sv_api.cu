@@ -120,6 +120,12 @@ bool kv_cache_ok(const void* k, const void* v, const float* ks, const float* vs,
   return k && v && ks && vs && table && aligned16(k) && aligned16(v) && aligned4(ks) && aligned4(vs) && aligned4(table);
 }
 
+// Do a's n ints share memory with b's m?
+bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + m * sizeof(int32_t) && y < x + n * sizeof(int32_t);
+}
+
 bool kv_attention_desc_ok(const sv_kv_attention_desc* d, bool ragged) {
   if (!d || !kv_desc_ok(&d->kv) || !valid_dtype(d->dtype) || d->reserved != 0) return false;
   if (d->heads < 1 || d->heads % d->kv.kv_heads || d->heads / d->kv.kv_heads > 128) return false;
@@ -366,8 +372,12 @@ sv_status sv_kv_commit(const sv_kv_desc* desc, int32_t nodes, int32_t path_len, 
   if (!kv_desc_ok(desc) || nodes < 1 || nodes > SV_MAX_TREE_NODES) return SV_ERR_INVALID_ARGUMENT;
   if (path_len < 1 || path_len > SV_MAX_TREE_DEPTH + 1) return SV_ERR_INVALID_ARGUMENT;
   if (desc->batch == 0) return SV_OK;
-  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens || !path || !accept_len || !new_lens ||
-      new_lens == ctx_lens)
+  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens || !path || !accept_len || !new_lens)
+    return SV_ERR_INVALID_ARGUMENT;
+  // one block of a sequence writes its new length while others still read these
+  const int64_t B = desc->batch;
+  if (overlap(new_lens, B, ctx_lens, B) || overlap(new_lens, B, accept_len, B) || overlap(new_lens, B, path, B * path_len) ||
+      overlap(new_lens, B, page_table, (B - 1) * desc->table_stride + desc->max_pages))
     return SV_ERR_INVALID_ARGUMENT;
   return kv_commit(*desc, nodes, path_len, KvCache{k_cache, v_cache, k_scale, v_scale, page_table}, ctx_lens, path,
                    accept_len, new_lens, row_status, reinterpret_cast<cudaStream_t>(stream));

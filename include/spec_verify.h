@@ -496,7 +496,7 @@ sv_status sv_kv_read(const sv_kv_desc* desc, const sv_kv_rows_desc* rows, const 
  *
  *   nodes     N in [1, SV_MAX_TREE_NODES];  path_len = D + 1 in [1, SV_MAX_TREE_DEPTH + 1].
  *   path      [B, path_len] int32;  accept_len [B] int32.
- *   new_lens  [B] int32, not ctx_lens itself.
+ *   new_lens  [B] int32, apart from the int32 inputs (refused where they overlap).
  */
 sv_status sv_kv_commit(const sv_kv_desc* desc, int32_t nodes, int32_t path_len, const int32_t* page_table,
                        const int32_t* ctx_lens, const int32_t* path, const int32_t* accept_len,

@@ -1,0 +1,29 @@
+"""Refusals of the cache's C entry points beyond those of single arguments (no GPU)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def N():
+    from draft_token_verification_sv_gb300 import build as b
+    b.build()
+    from draft_token_verification_sv_gb300 import _native
+    _native.lib()
+    return _native
+
+
+def _kv(N):
+    return N.KvDesc(4, 2, 64, 16, 100, 8, 2 * 16 * 64, 16 * 64, 64, 10)
+
+
+@pytest.mark.parametrize("place", [dict(ctx=0), dict(ctx=12), dict(ctx=-12), dict(accept=0), dict(accept=4), dict(path=0),
+                                   dict(path=-60), dict(path=12), dict(table=0), dict(table=-148), dict(table=12)],
+                         ids=lambda p: "".join(f"{k}{v}" for k, v in p.items()))
+def test_commit_refuses_new_lengths_over_its_inputs(N, place):
+    """4 sequences, paths of 4 nodes, page table rows of 8 entries 10 apart: `place` is how many bytes an input begins behind new_lens."""
+    new = 0x200000
+    at = {n: ctypes.c_void_p(new + place[n] if n in place else 0x100000) for n in ("table", "ctx", "path", "accept")}
+    A = ctypes.c_void_p(0x100000)
+    assert N.lib().sv_kv_commit(ctypes.byref(_kv(N)), 8, 4, at["table"], at["ctx"], at["path"], at["accept"], A, A, A, A,
+                                ctypes.c_void_p(new), None, None) == N.SV_ERR_INVALID_ARGUMENT
