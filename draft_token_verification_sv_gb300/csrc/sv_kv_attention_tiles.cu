@@ -533,6 +533,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
           for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
           tc::tmem_store(own_o + i, o);
         }
+        tc::wait_stores();  // a second change in the same tile loads them again
         return true;
       };
       float v_top = kNoScale;

@@ -1,0 +1,60 @@
+"""What the attention over the 8-bit cache keeps of weights and queries whose
+sizes differ widely, against the fp64 oracle within bounds derived from the
+operations (tests/_kv.py)."""
+import numpy as np
+import pytest
+
+from oracle import kv_oracle as KO
+
+from _kv import attention_tolerance, cache_gpu, make_cache, make_table, round_to, to_gpu
+
+pytestmark = pytest.mark.gpu
+
+# (type, heads of one kv head): up to 16 rows, up to 32, and more
+ROWS = [("bf16", 2), ("f32", 2), ("bf16", 24), ("f32", 24), ("bf16", 48)]
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import __graft_entry__
+    __graft_entry__.build()
+    import draft_token_verification_sv_gb300 as sv
+    return sv
+
+
+def _compare(sv, cache, table, page, ctx, q, dtype, scale):
+    """One sequence, one new token, one kv head."""
+    heads, dim = q.shape[1:]
+    lens = to_gpu(np.array([ctx], np.int32))
+    out, lse = sv.kv_attention(to_gpu(q, dtype)[None], cache_gpu(cache), to_gpu(table), lens, scale=scale, lse=True)
+    want, wlse, absolute, largest = KO.attention(q.astype(np.float64), cache, table[0], page, ctx, None, scale, 0, 0)
+    tol, ltol = attention_tolerance(want, absolute, largest, ctx + 1, dim, dtype)
+    # weights end at 2^-31 of the row's largest, counted with the scales of V
+    k = KO.read(cache, "k", table[0], page, 0, ctx + 1)[:, 0]
+    codes = np.abs(KO.read(dict(cache, v_scale=np.ones_like(cache["v_scale"])), "v", table[0], page, 0, ctx + 1))[:, 0]
+    unit = cache["v_scale"][table[0][np.arange(ctx + 1) // page], 0]
+    p = np.exp(q[0].astype(np.float64) @ k.T * scale - wlse[0][:, None])
+    tol[0] += 2.0 ** -31 * (p * unit).max(1)[:, None] * codes.sum(0)
+    off = np.abs(out[0].double().cpu().numpy() - want)
+    assert (off <= tol).all(), float((off / tol).max())
+    loff = np.abs(lse[0].double().cpu().numpy() - wlse)
+    assert (loff <= ltol).all(), float((loff / ltol).max())
+
+
+@pytest.mark.parametrize("dtype,heads", ROWS)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_weights_and_values_that_rise_together(sv, dtype, heads, dim):
+    """Every page has larger values and larger weights than the one before, so
+    that both units change within a tile, again and again."""
+    g = np.random.default_rng(dim + heads)
+    page, ctx = 16, 700
+    table, pages = make_table(g, [ctx + 1], page)
+    cache = make_cache(g, pages, 1, page, dim)
+    cache["k"][:] = 0
+    cache["k_scale"][:] = 1.0
+    for i, p in enumerate(table[0]):
+        cache["v_scale"][p] = 2.0 ** (i - 20)
+        cache["k"][p, 0, :, 0] = KO.encode(np.full(page, 10.0 * (i - 20)))
+    q = np.zeros((1, heads, dim), np.float32)
+    q[0, :, 0] = np.linspace(0.05, 0.7, heads)
+    _compare(sv, cache, table, page, ctx, round_to(q, dtype), dtype, 1.0)
