@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
       ok = fetch_role<DP>(&keys, &values, tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(codes));
       // and copies in flight: the last of each stage, which no other role may have waited for
       int unused = 0;
-      for (int it = max(0, sh.fetched - kCodeStages); !ok && it < sh.fetched; ++it)
+      for (int it = max(0, sh.fetched - kCodeStages); it < sh.fetched; ++it)
         tc::barrier_wait(tc::smem_address(&sh.codes_full[it % kCodeStages]), it / kCodeStages & 1, &unused);
       __syncwarp();
     }
