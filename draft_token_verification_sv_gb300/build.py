@@ -44,16 +44,21 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
+def build(force: bool = False, verbose: bool = False, debug: bool = False, variant: str | None = None,
+          defines: tuple = ()) -> str:
     """Compile and link the library (the bounds-checked debug build when
-    ``debug``); returns its path."""
+    ``debug``; with ``variant``, a build of that name with ``defines``, kept
+    apart under _build); returns its path."""
     lib, bdir = (DEBUG_LIB, DEBUG_BUILD) if debug else (LIB, BUILD)
+    if variant:
+        bdir = os.path.join(BUILD, variant)
+        lib = os.path.join(bdir, "libspec_verify.so")
     if not force and up_to_date(lib):
         return lib
     os.makedirs(bdir, exist_ok=True)
     procs = []
     objs = []
-    extra = ["-DSV_DEBUG"] if debug else []
+    extra = (["-DSV_DEBUG"] if debug else []) + [f"-D{d}" for d in defines]
     for src in _sources():
         obj = os.path.join(bdir, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)

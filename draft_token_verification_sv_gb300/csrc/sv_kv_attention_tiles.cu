@@ -109,6 +109,7 @@ struct Shared {
   uint32_t tmem;
   int gave_up;
   int fetched;  // tiles that copies were issued for
+  Cursor begin; // where the block's range begins
 };
 
 // Eight codes as fp16.
@@ -135,6 +136,11 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) tc::barrier_arrive(tc::smem_address(&bar));
 }
+
+// A block's tile that is never planned, in builds that test what happens when the other roles' waits run out.
+#ifndef SV_LOST_TILE
+#define SV_LOST_TILE -1
+#endif
 
 // ---- plans ----
 
@@ -187,6 +193,7 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
                            : (bits & 0x7fffffu) == 0 && bits >= 0x00800000u ? static_cast<float>(static_cast<int>(bits >> 23) - 127)
                                                                             : log2f(v_scale);
       for (int i = 0; i < 32 / kTileSteps && t0 + i < p.count; ++i, ++it) {
+        if (it == SV_LOST_TILE) return true;
         TilePlan& plan = sh.plan[it % kPlans];
         if (it >= kPlans && !warp_wait(sh, sh.plan_free[it % kPlans], it / kPlans - 1)) return false;
         if (mine == i) {
@@ -670,6 +677,37 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
   return true;
 }
 
+// A wait ran out, so the block's results are not valid: every sequence that it had a part of is flagged, and its rows become
+// NaN, those of whole items here, those of items in parts where the parts are joined.  By the warps that hand results over.
+template <int DP>
+__device__ __noinline__ void spoil(const AttentionParams& a, Cursor c, int g) {
+  using T = Tiles<DP>;
+  constexpr int kMine = 32 * kSoftmaxWarps;
+  while (c.at < c.end) {
+    const int r0 = c.rt * kRows, rows = min(kRows, c.span.n * a.group - r0);
+    const int tiles = item_tiles<kRows, kTileSteps>(a, c.span, c.rt);
+    const int done = static_cast<int>(min(static_cast<long long>(tiles - c.tile), c.end - c.at));
+    if (c.tile + done <= 0) return;  // the range ends in the item's empty tiles
+    const bool begins = c.tile <= 0, complete = begins && c.tile + done == tiles;
+    if (threadIdx.x == 0) kv_flag(a.w, c.b, SV_ROW_TIMEOUT);
+    float* part = a.parts + (2 * static_cast<int64_t>(g) + (begins ? 1 : 0)) * T::kPart;
+    for (int r = threadIdx.x; r < rows; r += kMine) {
+      if (!complete) {
+        *reinterpret_cast<float2*>(part + kRows * DP + 2 * r) = make_float2(0.0f, CUDART_NAN_F);
+        continue;
+      }
+      const int64_t row = static_cast<int64_t>(c.span.row0) + (r0 + r) / a.group;
+      const int head = c.h * a.group + (r0 + r) % a.group;
+      uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.out_row_stride + head * a.out_head_stride;
+      for (int d = 0; d < a.w.dim; ++d) out[d] = 0x7fff;
+      if (a.lse) a.lse[row * a.heads + head] = CUDART_NAN_F;
+    }
+    if (!complete && begins && threadIdx.x == 0)
+      a.joins[g] = JoinRecord{c.span.row0, r0, rows, c.h, tile_owner(c.at - c.tile + tiles - 1, c.total, c.blocks)};
+    next_item<kRows, kOpen>(a, c, done);
+  }
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(AttentionParams a, const __grid_constant__ CUtensorMap keys,
                                                                               const __grid_constant__ CUtensorMap values) {
@@ -714,41 +752,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   }
   if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), T::kColumns);
   const Cursor c = find_cursor<kThreads, kRows, kTileSteps, kOpen>(a, g, gridDim.x, sh.cursor);
+  if (threadIdx.x == 0) sh.begin = c;
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
   const int tiles_here = static_cast<int>(full_tiles<kRows, kTileSteps, kOpen>(a, c));  // 2^31 tiles would take half an hour
-  bool ok = true;
   if (warp < kSoftmaxWarps) {
     tc::registers_up<kSoftmaxRegisters>();
-    ok = softmax_role<DP>(a, tiles_here, sh, codes + kCodeStages * T::kCodeBytes, tmem, g);
+    if (!tc::all_of<1, 32 * kSoftmaxWarps>(softmax_role<DP>(a, tiles_here, sh, codes + kCodeStages * T::kCodeBytes, tmem, g)))
+      spoil<DP>(a, sh.begin, g);
   } else if (warp < kSoftmaxWarps + kValueWarps) {
     tc::registers_down<kValueRegisters>();
-    ok = value_role<DP>(tiles_here, sh, v_tiles, codes);
+    value_role<DP>(tiles_here, sh, v_tiles, codes);
   } else {
     tc::registers_down<kOtherRegisters>();
     if (warp == kSoftmaxWarps + kValueWarps) {
       if (tc::elected()) {
-        ok = product_role<DP>(tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
+        product_role<DP>(tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
         // products in flight end before the memory that they use is given up
         int unused = 0;
         tc::products_arrive(tc::smem_address(&sh.last));
-        ok = tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused) && ok;
+        tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused, tc::kEndCycles);
       }
-      ok = __all_sync(0xffffffffu, ok);
+      __syncwarp();
     } else if (warp == kSoftmaxWarps + kValueWarps + 1) {
-      ok = plan_role(a, c, sh);
+      plan_role(a, c, sh);
     } else if (warp == kSoftmaxWarps + kValueWarps + 2) {
-      ok = fetch_role<DP>(&keys, &values, tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(codes));
+      fetch_role<DP>(&keys, &values, tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(codes));
       // and copies in flight: the last of each stage, which no other role may have waited for
       int unused = 0;
       for (int it = max(0, sh.fetched - kCodeStages); it < sh.fetched; ++it)
-        tc::barrier_wait(tc::smem_address(&sh.codes_full[it % kCodeStages]), it / kCodeStages & 1, &unused);
+        tc::barrier_wait(tc::smem_address(&sh.codes_full[it % kCodeStages]), it / kCodeStages & 1, &unused, tc::kEndCycles);
       __syncwarp();
     }
   }
-  if (!ok && (threadIdx.x & 31) == 0) kv_flag(a.w, min(c.b, a.w.batch - 1), SV_ROW_TIMEOUT);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();

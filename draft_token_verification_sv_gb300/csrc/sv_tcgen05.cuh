@@ -28,19 +28,38 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
-// Waits for the phase of `parity` to end; false if it did not within 2^32
-// cycles (about two seconds), or if another role of the block has given up.
-__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+// How long a role waits for another: about two seconds.  (Builds for tests set less.)
+#ifndef SV_WAIT_CYCLES
+#define SV_WAIT_CYCLES (1ll << 32)
+#endif
+// And for the hardware to end what was begun, whatever the build.
+constexpr long long kEndCycles = 1ll << 32;
+
+// Waits for the phase of `parity` to end; false if it did not within `limit`
+// cycles, or if another role of the block has given up.
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int* gave_up, long long limit = SV_WAIT_CYCLES) {
   if (barrier_try(bar, parity)) return true;
   const long long begin = clock64();
   while (!barrier_try(bar, parity)) {
     if (*gave_up) return false;
-    if (clock64() - begin > (1ll << 32)) {
+    if (clock64() - begin > limit) {
       *gave_up = 1;
       return false;
     }
   }
   return true;
+}
+
+// THREADS threads of the block (whole warps) meet at its barrier ID: is `mine` true for all of them?
+template <int ID, int THREADS>
+__device__ __forceinline__ bool all_of(bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.and.pred q, %2, %3, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(mine)), "n"(ID), "n"(THREADS)
+      : "memory");
+  return r != 0;
 }
 
 // An arrival that also announces bytes which copies will bring.

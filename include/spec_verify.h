@@ -70,7 +70,7 @@ typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_ROW_BAD_LENGTH 128        /* cache: lengths that are negative or beyond the page table's row */
 #define SV_ROW_NOT_FINITE 256        /* cache: a NaN (stored as 0) or infinity (stored as +-448 * scale) was appended */
 #define SV_ROW_BAD_PATH 512          /* cache: a path that does not start at 0 and rise within [0, nodes) */
-#define SV_ROW_TIMEOUT 1024          /* an internal wait ran out: the results are not valid */
+#define SV_ROW_TIMEOUT 1024          /* an internal wait ran out: results of the row are not valid (NaN where they are floats) */
 
 /* Limits checked on the host. */
 #define SV_MAX_GAMMA 64
