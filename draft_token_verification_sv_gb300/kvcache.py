@@ -72,6 +72,14 @@ def _numel(shape) -> int:
     return n
 
 
+def _count(value, name: str) -> int:
+    """``value`` as an int that the descriptors' 32 bits hold."""
+    n = int(value)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {n}")
+    return n
+
+
 def _contiguous(m: _Meta) -> bool:
     want = 1
     for n, s in zip(reversed(m.shape), reversed(m.strides)):
@@ -121,6 +129,7 @@ def _rows(m: _Meta, name: str, B: int, ragged: bool):
     if len(shape) != (3 if ragged else 4):
         raise ValueError(f"{name} must be [total, heads, dim] with new_start, else [B, n, heads, dim]")
     heads, dim = shape[-2:]
+    _count(_numel(shape[:-2]), f"the number of {name}'s rows")
     if strides[-1] != 1:
         raise ValueError(f"{name}: last dimension must be contiguous")
     head_stride = strides[-2] if heads > 1 else dim
@@ -242,7 +251,7 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, page_table: torch.T
     and returns ``cache``; ``row_status`` [B] int32 receives the flags."""
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     d, r = _append_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(k), _meta(v),
-                        _meta(new_start), None if max_new is None else int(max_new), _meta(row_status))
+                        _meta(new_start), None if max_new is None else _count(max_new, "max_new"), _meta(row_status))
     st = N.lib().sv_kv_append(d, r, k.data_ptr(), v.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start),
                               kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), _at(row_status),
                               _stream_of(stream, kc))
@@ -258,10 +267,11 @@ def kv_read(cache: dict, page_table: torch.Tensor, first: torch.Tensor, tokens: 
     Returns (k, v): [B, tokens, kv_heads, dim], or with ``new_start`` [B + 1]
     [total, kv_heads, dim] rows, ``tokens`` being the most of one sequence."""
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
+    tokens = _count(tokens, "tokens")
     if out is None:
         _, heads, _, dim = kc.shape
         if new_start is None:
-            shape = (page_table.shape[0], int(tokens), heads, dim)
+            shape = (page_table.shape[0], tokens, heads, dim)
         elif total is None:
             raise ValueError("new_start needs total, the number of rows")
         else:
@@ -270,7 +280,7 @@ def kv_read(cache: dict, page_table: torch.Tensor, first: torch.Tensor, tokens: 
     else:
         k, v = out
     d, r = _read_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(first), _meta(k), _meta(v),
-                      _meta(new_start), int(tokens), _meta(row_status))
+                      _meta(new_start), tokens, _meta(row_status))
     st = N.lib().sv_kv_read(d, r, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), page_table.data_ptr(),
                             first.data_ptr(), _at(new_start), k.data_ptr(), v.data_ptr(), _at(row_status),
                             _stream_of(stream, kc))
@@ -290,7 +300,7 @@ def kv_commit(cache: dict, page_table: torch.Tensor, ctx_lens: torch.Tensor, pat
         new_lens = _empty(ctx_lens.shape, ctx_lens.dtype, ctx_lens.device, stream)
     d, length = _commit_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(path),
                              _meta(accept_len), _meta(new_lens), _meta(row_status))
-    st = N.lib().sv_kv_commit(d, int(nodes), length, page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
+    st = N.lib().sv_kv_commit(d, _count(nodes, "nodes"), length, page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
                               accept_len.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
                               new_lens.data_ptr(), _at(row_status), _stream_of(stream, kc))
     N.check(st, "sv_kv_commit")
@@ -314,8 +324,9 @@ def kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, ctx_len
     if out is None:
         out = _empty(q.shape, q.dtype, device, stream)
     a, need = _attention_plan(_meta(q), _meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens),
-                              _meta(new_start), None if max_new is None else int(max_new), _meta(parents),
-                              None if scale is None else float(scale), int(window), int(sinks), _meta(out), _meta(row_status))
+                              _meta(new_start), None if max_new is None else _count(max_new, "max_new"), _meta(parents),
+                              None if scale is None else float(scale), _count(window, "window"), _count(sinks, "sinks"),
+                              _meta(out), _meta(row_status))
     sums = _empty(q.shape[:-1], torch.float32, device, stream) if lse else None
     raw = _stream_of(stream, q)
     if ws is None:

@@ -103,6 +103,7 @@ def fake_streams(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch, "empty", allocate)
     monkeypatch.setattr(torch, "zeros", allocate)
+    monkeypatch.setattr(sv.kvcache, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(N, "lib", Lib)
     monkeypatch.setattr(sv.verify, "_WORKSPACES", {})
     monkeypatch.setattr(sv.kvcache, "_WORKSPACES", sv.verify._WORKSPACES)
@@ -127,3 +128,17 @@ def test_results_and_workspaces_belong_to_the_calls_stream(fake_streams):
     sv.kv_read(cache, _ints(4, 5), _ints(4), 3, stream=side)
     sv.kv_commit(cache, _ints(4, 5), _ints(4), _ints(4, 5), _ints(4), 8, stream=side)
     assert made == [("side", ["main"])] * 3
+
+
+@pytest.mark.parametrize("what,call", [
+    ("window", lambda c, q, x: sv.kv_attention(q, c, _ints(4, 5), _ints(4), window=2 ** 32 + 1)),
+    ("sinks", lambda c, q, x: sv.kv_attention(q, c, _ints(4, 5), _ints(4), window=8, sinks=2 ** 32)),
+    ("max_new", lambda c, q, x: sv.kv_append(c, x, x, _ints(4, 5), _ints(4), new_start=_ints(5), max_new=2 ** 32 + 3)),
+    ("tokens", lambda c, q, x: sv.kv_read(c, _ints(4, 5), _ints(4), 2 ** 32 + 3, new_start=_ints(5), out=(x, x))),
+    ("nodes", lambda c, q, x: sv.kv_commit(c, _ints(4, 5), _ints(4), _ints(4, 5), _ints(4), 2 ** 32 + 8, new_lens=_ints(4))),
+    ("rows", lambda c, q, x: sv.kv_append(c, Stand((2 ** 32 + 1, 2, 64)), Stand((2 ** 32 + 1, 2, 64)), _ints(4, 5), _ints(4),
+                                          new_start=_ints(5), max_new=1))])
+def test_numbers_beyond_32_bits_are_refused(fake_streams, what, call):
+    """They lost their upper bits on the way into the descriptors (a window of 2^32 + 1 became one of 1)."""
+    with pytest.raises(ValueError, match="32 bits"):
+        call(_cache(), Stand((4, 3, 8, 64)), Stand((12, 2, 64)))
