@@ -44,25 +44,32 @@ def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, 
 
 
 class _Meta(tuple):
-    """What the checks see of a tensor: (shape, strides, dtype, on a GPU)."""
+    """What the checks see of a tensor: (shape, strides, dtype, GPU or -1)."""
     __slots__ = ()
     shape = property(lambda m: m[0])
     strides = property(lambda m: m[1])
     dtype = property(lambda m: m[2])
-    is_cuda = property(lambda m: m[3])
+    device = property(lambda m: m[3])
 
 
 def _meta(t):
-    return None if t is None else (t.shape, t.stride(), t.dtype, t.is_cuda)
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
 def _see(meta, name) -> _Meta:
     if meta is None:
         return None
     m = _Meta(meta)
-    if not m.is_cuda:
+    if m.device < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     return m
+
+
+def _one_device(*metas) -> int:
+    devices = {m[3] for m in metas if m is not None}
+    if len(devices) > 1:
+        raise ValueError("all tensors of a call must be on one GPU")
+    return devices.pop()
 
 
 def _numel(shape) -> int:
@@ -172,7 +179,7 @@ def _append_plan(kc, vc, ks, vs, table, lens, k, v, start, max_new, status):
         raise ValueError("k and v must have the cache's heads and head_dim")
     r = N.KvRowsDesc(_new(start, max_new, k, B), n, _code(k), 0, k_row, k_head, v_row, v_head)
     _int32(status, "row_status", B, _PER_SEQUENCE)
-    return ctypes.byref(d), ctypes.byref(r)
+    return ctypes.byref(d), ctypes.byref(r), _one_device(kc, vc, ks, vs, table, lens, k, v, start, status)
 
 
 @functools.lru_cache(maxsize=_KEPT)
@@ -187,7 +194,7 @@ def _read_plan(kc, vc, ks, vs, table, first, k, v, start, tokens, status):
     _, _, _, v_row, v_head = _rows(v, "out[1]", B, ragged)
     r = N.KvRowsDesc(_new(start, tokens, k, B), n, _code(k), 0, k_row, k_head, v_row, v_head)
     _int32(status, "row_status", B, _PER_SEQUENCE)
-    return ctypes.byref(d), ctypes.byref(r)
+    return ctypes.byref(d), ctypes.byref(r), _one_device(kc, vc, ks, vs, table, first, k, v, start, status)
 
 
 @functools.lru_cache(maxsize=_KEPT)
@@ -200,7 +207,7 @@ def _commit_plan(kc, vc, ks, vs, table, lens, path, accept, new_lens, status):
     _int32(accept, "accept_len", B, _PER_SEQUENCE)
     _int32(new_lens, "new_lens", B, _PER_SEQUENCE)
     _int32(status, "row_status", B, _PER_SEQUENCE)
-    return ctypes.byref(d), p.shape[1]
+    return ctypes.byref(d), p.shape[1], _one_device(kc, vc, ks, vs, table, lens, path, accept, new_lens, status)
 
 
 @functools.lru_cache(maxsize=_KEPT)
@@ -219,15 +226,30 @@ def _attention_plan(q, kc, vc, ks, vs, table, lens, start, max_new, parents, sca
                           dim ** -0.5 if scale is None else scale, window, sinks, 0, q_row, q_head,
                           o_row, o_head)
     _int32(status, "row_status", B, _PER_SEQUENCE)
-    return ctypes.byref(a), N.lib().sv_kv_attention_workspace_size(ctypes.byref(a))
+    return (ctypes.byref(a), N.lib().sv_kv_attention_workspace_size(ctypes.byref(a)),
+            _one_device(kc, vc, ks, vs, table, lens, q, start, parents, out, status))
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_of(stream, t) -> int:
-    return stream.cuda_stream if stream is not None else _raw_stream(t.device.index)
+def _stream_of(stream, device: int) -> int:
+    if stream is None:
+        return _raw_stream(device)
+    if stream.device_index != device:
+        raise ValueError("stream belongs to another GPU than the tensors")
+    return stream.cuda_stream
+
+
+def _call(device: int, entry: str, *args) -> None:
+    """A call of the library with its tensors' GPU as the current one."""
+    if torch.cuda.current_device() == device:
+        st = getattr(N.lib(), entry)(*args)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(N.lib(), entry)(*args)
+    N.check(st, entry)
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -250,12 +272,10 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, page_table: torch.T
     ``new_start``), float32 or bfloat16, any row and head strides.  Updates
     and returns ``cache``; ``row_status`` [B] int32 receives the flags."""
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
-    d, r = _append_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(k), _meta(v),
-                        _meta(new_start), None if max_new is None else _count(max_new, "max_new"), _meta(row_status))
-    st = N.lib().sv_kv_append(d, r, k.data_ptr(), v.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start),
-                              kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), _at(row_status),
-                              _stream_of(stream, kc))
-    N.check(st, "sv_kv_append")
+    d, r, gpu = _append_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(k), _meta(v),
+                             _meta(new_start), None if max_new is None else _count(max_new, "max_new"), _meta(row_status))
+    _call(gpu, "sv_kv_append", d, r, k.data_ptr(), v.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start),
+          kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), _at(row_status), _stream_of(stream, gpu))
     return cache
 
 
@@ -279,12 +299,10 @@ def kv_read(cache: dict, page_table: torch.Tensor, first: torch.Tensor, tokens: 
         k, v = _empty(shape, dtype, kc.device, stream), _empty(shape, dtype, kc.device, stream)
     else:
         k, v = out
-    d, r = _read_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(first), _meta(k), _meta(v),
-                      _meta(new_start), tokens, _meta(row_status))
-    st = N.lib().sv_kv_read(d, r, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), page_table.data_ptr(),
-                            first.data_ptr(), _at(new_start), k.data_ptr(), v.data_ptr(), _at(row_status),
-                            _stream_of(stream, kc))
-    N.check(st, "sv_kv_read")
+    d, r, gpu = _read_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(first), _meta(k), _meta(v),
+                           _meta(new_start), tokens, _meta(row_status))
+    _call(gpu, "sv_kv_read", d, r, kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), page_table.data_ptr(),
+          first.data_ptr(), _at(new_start), k.data_ptr(), v.data_ptr(), _at(row_status), _stream_of(stream, gpu))
     return k, v
 
 
@@ -298,12 +316,11 @@ def kv_commit(cache: dict, page_table: torch.Tensor, ctx_lens: torch.Tensor, pat
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     if new_lens is None:
         new_lens = _empty(ctx_lens.shape, ctx_lens.dtype, ctx_lens.device, stream)
-    d, length = _commit_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(path),
-                             _meta(accept_len), _meta(new_lens), _meta(row_status))
-    st = N.lib().sv_kv_commit(d, _count(nodes, "nodes"), length, page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
-                              accept_len.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-                              new_lens.data_ptr(), _at(row_status), _stream_of(stream, kc))
-    N.check(st, "sv_kv_commit")
+    d, length, gpu = _commit_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(path),
+                                  _meta(accept_len), _meta(new_lens), _meta(row_status))
+    _call(gpu, "sv_kv_commit", d, _count(nodes, "nodes"), length, page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
+          accept_len.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), new_lens.data_ptr(),
+          _at(row_status), _stream_of(stream, gpu))
     return new_lens
 
 
@@ -323,18 +340,19 @@ def kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, ctx_len
     device = q.device
     if out is None:
         out = _empty(q.shape, q.dtype, device, stream)
-    a, need = _attention_plan(_meta(q), _meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens),
-                              _meta(new_start), None if max_new is None else _count(max_new, "max_new"), _meta(parents),
-                              None if scale is None else float(scale), _count(window, "window"), _count(sinks, "sinks"),
-                              _meta(out), _meta(row_status))
+    a, need, gpu = _attention_plan(_meta(q), _meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens),
+                                   _meta(new_start), None if max_new is None else _count(max_new, "max_new"), _meta(parents),
+                                   None if scale is None else float(scale), _count(window, "window"), _count(sinks, "sinks"),
+                                   _meta(out), _meta(row_status))
     sums = _empty(q.shape[:-1], torch.float32, device, stream) if lse else None
-    raw = _stream_of(stream, q)
+    raw = _stream_of(stream, gpu)
     if ws is None:
-        ws = _WORKSPACES.get((device.index, raw))
+        ws = _WORKSPACES.get((gpu, raw))
         if ws is None or ws.numel() < need:
             ws = workspace(need, device, stream)
-    st = N.lib().sv_kv_attention(a, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-                                 page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start), _at(parents), out.data_ptr(),
-                                 _at(sums), _at(row_status), ws.data_ptr(), ws.numel(), raw)
-    N.check(st, "sv_kv_attention")
+    elif ws.get_device() != gpu or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the GPU of the other tensors")
+    _call(gpu, "sv_kv_attention", a, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+          page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start), _at(parents), out.data_ptr(), _at(sums),
+          _at(row_status), ws.data_ptr(), ws.numel(), raw)
     return (out, sums) if lse else out

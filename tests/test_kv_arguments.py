@@ -26,6 +26,12 @@ class Stand:
     def stride(self):
         return self._strides
 
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
+    def is_contiguous(self):
+        return self._strides == tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
+
     def data_ptr(self):
         return self._address
 
@@ -78,7 +84,7 @@ def fake_streams(monkeypatch):
 
     class Fake:
         def __init__(self, name):
-            self.name, self.cuda_stream = name, hash(name) & 0xffff
+            self.name, self.cuda_stream, self.device_index = name, hash(name) & 0xffff, 0
 
     class Made(Stand):
         def record_stream(self, stream):
@@ -142,3 +148,42 @@ def test_numbers_beyond_32_bits_are_refused(fake_streams, what, call):
     """They lost their upper bits on the way into the descriptors (a window of 2^32 + 1 became one of 1)."""
     with pytest.raises(ValueError, match="32 bits"):
         call(_cache(), Stand((4, 3, 8, 64)), Stand((12, 2, 64)))
+
+
+OTHER = dict(device="cuda:1")
+
+
+@pytest.mark.parametrize("what", ["table", "lens", "cache", "q", "parents", "status", "out"])
+def test_tensors_of_two_gpus_are_refused(what):
+    place = lambda name: OTHER if name == what else {}
+    with pytest.raises(ValueError, match="one GPU"):
+        sv.kv_attention(Stand((4, 3, 8, 64), **place("q")), _cache(**place("cache")), _ints(4, 5, **place("table")),
+                        _ints(4, **place("lens")), parents=_ints(4, 3, **place("parents")), out=Stand((4, 3, 8, 64), **place("out")),
+                        row_status=_ints(4, **place("status")), ws=Stand((1 << 30,), torch.uint8))
+
+
+@pytest.mark.parametrize("ws", [Stand((1 << 30,), torch.uint8, device="cpu"), Stand((1 << 30,), torch.uint8, **OTHER),
+                                Stand((1 << 30,), torch.uint8, strides=(0,))],
+                         ids=["host", "other GPU", "expanded"])
+def test_workspaces_the_call_cannot_write_are_refused(monkeypatch, ws):
+    monkeypatch.setattr(sv.kvcache, "_raw_stream", lambda index: 0)
+    with pytest.raises(ValueError, match="ws"):
+        sv.kv_attention(Stand((4, 3, 8, 64)), _cache(), _ints(4, 5), _ints(4), out=Stand((4, 3, 8, 64)), ws=ws)
+
+
+def test_the_tensors_gpu_is_made_current(fake_streams, monkeypatch):
+    import contextlib
+    entered = []
+
+    @contextlib.contextmanager
+    def device(index):
+        entered.append(index)
+        yield
+    monkeypatch.setattr(torch.cuda, "device", device)
+    x, one = Stand((4, 3, 2, 64), **OTHER), lambda *shape: _ints(*shape, **OTHER)
+    sv.kv_append(_cache(**OTHER), x, x, one(4, 5), one(4))
+    assert entered == [1]
+    sv.kv_append(_cache(), Stand((4, 3, 2, 64)), Stand((4, 3, 2, 64)), _ints(4, 5), _ints(4))
+    assert entered == [1]
+    with pytest.raises(ValueError, match="stream"):
+        sv.kv_append(_cache(**OTHER), x, x, one(4, 5), one(4), stream=fake_streams[0]("side"))
