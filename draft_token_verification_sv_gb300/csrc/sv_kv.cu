@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(THREADS) kv_commit_kernel(KvView w, int nodes,
     for (int i = threadIdx.x; i < (hi - lo) * wpr; i += THREADS) {
       const int t = i / wpr, k = i - t * wpr;
       const int src = lo - ctx + t;
-      reinterpret_cast<uint32_t*>(to + t * w.token_stride)[k] = rescale4(words[src * wpr + k], s_scale[src] * inv);
+      // (beyond float only where all of the path's codes here are zeros, which stay)
+      reinterpret_cast<uint32_t*>(to + t * w.token_stride)[k] = rescale4(words[src * wpr + k], fminf(s_scale[src] * inv, 0x1p127f));
     }
   }
 }
