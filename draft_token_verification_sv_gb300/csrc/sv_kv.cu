@@ -235,11 +235,11 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(KvView w, ReadRows row
   const int cpr = w.dim >> 4;
   const int per = THREADS / cpr;  // tokens of a pass
   const int t0 = threadIdx.x / cpr, chunk = threadIdx.x - t0 * cpr;
-  const int end = static_cast<int>(min(static_cast<int64_t>(tile) * (block + 1), static_cast<int64_t>(s.n)));
+  const int count = min(tile, s.n - tile * block);  // (counted from the tile's first: sums with t0 could pass 2^31)
   if (t0 >= per) return;
 #pragma unroll 4
-  for (int t = tile * block + t0; t < end; t += per) {
-    const int pos = s.ctx + t;
+  for (int i = t0; i < count; i += per) {
+    const int t = tile * block + i, pos = s.ctx + t;
     const int page = s.ok ? kv_page(w, b, pos >> w.page_shift) : -1;
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
     float ks = 0.0f, vs = 0.0f;
