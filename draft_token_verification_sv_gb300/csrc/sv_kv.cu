@@ -344,6 +344,11 @@ __global__ void __launch_bounds__(THREADS) kv_commit_kernel(KvView w, int nodes,
   }
 }
 
+__global__ void kv_lengths_kernel(KvView w) {
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b < w.batch && !kv_span(w, b).ok) kv_flag(w, b, SV_ROW_BAD_LENGTH);
+}
+
 template <typename E, int THREADS>
 void launch_append(const KvView& w, const AppendRows& rows, bool vec, const dim3& grid, cudaStream_t stream) {
   if (vec)
@@ -383,12 +388,20 @@ bool clear_status(int32_t* status, int batch, cudaStream_t stream) {
 
 }  // namespace
 
+sv_status kv_check_lengths(const KvView& w, cudaStream_t stream) {
+  if (!w.status) return SV_OK;
+  kv_lengths_kernel<<<(w.batch + 127) / 128, 128, 0, stream>>>(w);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  note_launch(stream);
+  return SV_OK;
+}
+
 sv_status kv_append(const sv_kv_desc& d, const sv_kv_rows_desc& r, const void* k, const void* v, const KvCache& c,
                     const int32_t* ctx_lens, const int32_t* new_start, int32_t* row_status, cudaStream_t stream) {
   start_phases(stream);
   if (!clear_status(row_status, d.batch, stream)) return SV_ERR_CUDA;
-  if (r.max_new == 0 || r.total_new == 0) return SV_OK;
   const KvView w = kv_view(d, c, ctx_lens, new_start, r.max_new, r.total_new, row_status);
+  if (r.max_new == 0 || r.total_new == 0) return kv_check_lengths(w, stream);
   const AppendRows rows{{k, v}, {r.k_row_stride, r.v_row_stride}, {r.k_head_stride, r.v_head_stride}};
   // pages that max_new tokens touch at most: the first may start at its last slot
   const int64_t spans = (static_cast<int64_t>(r.max_new) + 2 * d.page_size - 2) / d.page_size;
@@ -409,8 +422,8 @@ sv_status kv_read(const sv_kv_desc& d, const sv_kv_rows_desc& r, void* k, void* 
                   const int32_t* first, const int32_t* new_start, int32_t* row_status, cudaStream_t stream) {
   start_phases(stream);
   if (!clear_status(row_status, d.batch, stream)) return SV_ERR_CUDA;
-  if (r.max_new == 0 || r.total_new == 0) return SV_OK;
   const KvView w = kv_view(d, c, first, new_start, r.max_new, r.total_new, row_status);
+  if (r.max_new == 0 || r.total_new == 0) return kv_check_lengths(w, stream);
   const ReadRows rows{{k, v}, {r.k_row_stride, r.v_row_stride}, {r.k_head_stride, r.v_head_stride}};
   constexpr int kThreads = 256;
   const int tile = 4 * (kThreads / (d.head_dim / 16));  // four passes

@@ -54,6 +54,9 @@ __device__ __forceinline__ void kv_flag(const KvView& w, int b, int bit) {
   if (w.status) atomicOr(w.status + b, bit);
 }
 
+// Flags bad lengths, for calls without a new token.
+sv_status kv_check_lengths(const KvView& w, cudaStream_t stream);
+
 // Page id of column `col` of sequence b, or -1 (flagged) outside the pool.
 __device__ __forceinline__ int kv_page(const KvView& w, int b, int col) {
   if (!sv_in(col, w.max_pages)) return -1;

@@ -614,7 +614,8 @@ sv_status kv_attention(const sv_kv_attention_desc& d, const void* q, const KvCac
   start_phases(stream);
   if (row_status && cudaMemsetAsync(row_status, 0, static_cast<size_t>(d.kv.batch) * sizeof(int32_t), stream) != cudaSuccess)
     return SV_ERR_CUDA;
-  if (d.max_new == 0 || d.total_new == 0) return SV_OK;
+  if (d.max_new == 0 || d.total_new == 0)
+    return kv_check_lengths(kv_view(d.kv, c, ctx_lens, new_start, d.max_new, d.total_new, row_status), stream);
   const int64_t e = d.dtype == SV_BF16 ? 2 : 4;
   const auto aligned = [&](const void* p, int64_t row, int64_t head, int to) {
     return reinterpret_cast<uintptr_t>(p) % to == 0 && (row * e) % to == 0 && (head * e) % to == 0;
