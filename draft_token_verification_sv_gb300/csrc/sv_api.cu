@@ -120,6 +120,12 @@ bool kv_cache_ok(const void* k, const void* v, const float* ks, const float* vs,
   return k && v && ks && vs && table && aligned16(k) && aligned16(v) && aligned4(ks) && aligned4(vs) && aligned4(table);
 }
 
+// Ints and floats, some of them optional, on their boundaries.
+template <typename... P>
+bool kv_words_ok(P... p) {
+  return (aligned4(p) && ...);
+}
+
 // Do a's n ints share memory with b's m?
 bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -342,7 +348,8 @@ sv_status sv_kv_append(const sv_kv_desc* desc, const sv_kv_rows_desc* rows, cons
   CallScope scope;
   if (!kv_desc_ok(desc) || !kv_rows_desc_ok(*desc, rows, new_start != nullptr)) return SV_ERR_INVALID_ARGUMENT;
   if (desc->batch == 0) return SV_OK;
-  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens) return SV_ERR_INVALID_ARGUMENT;
+  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens || !kv_words_ok(ctx_lens, new_start, row_status))
+    return SV_ERR_INVALID_ARGUMENT;
   if (rows->total_new > 0 && (!k || !v || !aligned_elem(k, rows->dtype) || !aligned_elem(v, rows->dtype)))
     return SV_ERR_INVALID_ARGUMENT;
   return kv_append(*desc, *rows, k, v, KvCache{k_cache, v_cache, k_scale, v_scale, page_table}, ctx_lens, new_start,
@@ -356,7 +363,8 @@ sv_status sv_kv_read(const sv_kv_desc* desc, const sv_kv_rows_desc* rows, const 
   CallScope scope;
   if (!kv_desc_ok(desc) || !kv_rows_desc_ok(*desc, rows, new_start != nullptr)) return SV_ERR_INVALID_ARGUMENT;
   if (desc->batch == 0) return SV_OK;
-  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !first) return SV_ERR_INVALID_ARGUMENT;
+  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !first || !kv_words_ok(first, new_start, row_status))
+    return SV_ERR_INVALID_ARGUMENT;
   if (rows->total_new > 0 && (!k || !v || !aligned_elem(k, rows->dtype) || !aligned_elem(v, rows->dtype)))
     return SV_ERR_INVALID_ARGUMENT;
   const KvCache c{const_cast<uint8_t*>(k_cache), const_cast<uint8_t*>(v_cache), const_cast<float*>(k_scale),
@@ -372,7 +380,8 @@ sv_status sv_kv_commit(const sv_kv_desc* desc, int32_t nodes, int32_t path_len, 
   if (!kv_desc_ok(desc) || nodes < 1 || nodes > SV_MAX_TREE_NODES) return SV_ERR_INVALID_ARGUMENT;
   if (path_len < 1 || path_len > SV_MAX_TREE_DEPTH + 1) return SV_ERR_INVALID_ARGUMENT;
   if (desc->batch == 0) return SV_OK;
-  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens || !path || !accept_len || !new_lens)
+  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens || !path || !accept_len || !new_lens ||
+      !kv_words_ok(ctx_lens, path, accept_len, new_lens, row_status))
     return SV_ERR_INVALID_ARGUMENT;
   // one block of a sequence writes its new length while others still read these
   const int64_t B = desc->batch;
@@ -396,7 +405,8 @@ sv_status sv_kv_attention(const sv_kv_attention_desc* desc, const void* q, const
   CallScope scope;
   if (!kv_attention_desc_ok(desc, new_start != nullptr)) return SV_ERR_INVALID_ARGUMENT;
   if (desc->kv.batch == 0) return SV_OK;
-  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens || !workspace || !aligned16(workspace))
+  if (!kv_cache_ok(k_cache, v_cache, k_scale, v_scale, page_table) || !ctx_lens || !workspace || !aligned16(workspace) ||
+      !kv_words_ok(ctx_lens, new_start, parents, lse, row_status))
     return SV_ERR_INVALID_ARGUMENT;
   if (desc->total_new > 0 && (!q || !out || !aligned_elem(q, desc->dtype) || !aligned_elem(out, desc->dtype)))
     return SV_ERR_INVALID_ARGUMENT;

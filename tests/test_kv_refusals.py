@@ -27,3 +27,32 @@ def test_commit_refuses_new_lengths_over_its_inputs(N, place):
     A = ctypes.c_void_p(0x100000)
     assert N.lib().sv_kv_commit(ctypes.byref(_kv(N)), 8, 4, at["table"], at["ctx"], at["path"], at["accept"], A, A, A, A,
                                 ctypes.c_void_p(new), None, None) == N.SV_ERR_INVALID_ARGUMENT
+
+
+A, MIS = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x100002)
+
+
+@pytest.mark.parametrize("i", range(3))
+def test_append_and_read_refuse_words_off_their_boundary(N, i):
+    """ctx_lens (first), new_start, row_status."""
+    rows = N.KvRowsDesc(3, 12, N.SV_BF16, 0, 128, 64, 128, 64)
+    w = [MIS if j == i else (A if j == 0 else None) for j in range(3)]
+    assert N.lib().sv_kv_append(ctypes.byref(_kv(N)), ctypes.byref(rows), A, A, A, w[0], w[1], A, A, A, A, w[2], None) == N.SV_ERR_INVALID_ARGUMENT
+    assert N.lib().sv_kv_read(ctypes.byref(_kv(N)), ctypes.byref(rows), A, A, A, A, A, w[0], w[1], A, A, w[2], None) == N.SV_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("i", range(5))
+def test_commit_refuses_words_off_their_boundary(N, i):
+    """ctx_lens, path, accept_len, new_lens, row_status."""
+    w = [A, A, A, ctypes.c_void_p(0x200000), None]
+    w[i] = ctypes.c_void_p(0x300002)
+    assert N.lib().sv_kv_commit(ctypes.byref(_kv(N)), 8, 4, A, w[0], w[1], w[2], A, A, A, A, w[3], w[4], None) == N.SV_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("i", range(5))
+def test_attention_refuses_words_off_their_boundary(N, i):
+    """ctx_lens, new_start, parents, lse, row_status."""
+    a = N.KvAttentionDesc(_kv(N), 8, 3, 12, N.SV_BF16, 0.125, 0, 0, 0, 512, 64, 512, 64)
+    w = [MIS if j == i else (A if j == 0 else None) for j in range(5)]
+    assert N.lib().sv_kv_attention(ctypes.byref(a), A, A, A, A, A, A, w[0], w[1], w[2], A, w[3], w[4], A, ctypes.c_size_t(1 << 40),
+                                   None) == N.SV_ERR_INVALID_ARGUMENT
