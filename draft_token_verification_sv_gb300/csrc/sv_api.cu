@@ -136,7 +136,8 @@ bool kv_attention_desc_ok(const sv_kv_attention_desc* d, bool ragged) {
   if (!d || !kv_desc_ok(&d->kv) || !valid_dtype(d->dtype) || d->reserved != 0) return false;
   if (d->heads < 1 || d->heads % d->kv.kv_heads || d->heads / d->kv.kv_heads > 128) return false;
   if (!kv_rows_ok(d->kv, d->max_new, d->total_new, ragged)) return false;
-  if (static_cast<int64_t>(d->max_new) * (d->heads / d->kv.kv_heads) > INT32_MAX) return false;
+  // rows of a kv head, rounded up to the tallest tile, are counted in 32 bits
+  if (static_cast<int64_t>(d->max_new) * (d->heads / d->kv.kv_heads) > INT32_MAX - 128) return false;
   if (!std::isfinite(d->scale) || d->window < 0 || d->sinks < 0) return false;
   return kv_stride_ok(d->q_row_stride, d->kv.head_dim) && kv_stride_ok(d->q_head_stride, d->kv.head_dim) &&
          kv_stride_ok(d->out_row_stride, d->kv.head_dim) && kv_stride_ok(d->out_head_stride, d->kv.head_dim);

@@ -56,3 +56,12 @@ def test_attention_refuses_words_off_their_boundary(N, i):
     w = [MIS if j == i else (A if j == 0 else None) for j in range(5)]
     assert N.lib().sv_kv_attention(ctypes.byref(a), A, A, A, A, A, A, w[0], w[1], w[2], A, w[3], w[4], A, ctypes.c_size_t(1 << 40),
                                    None) == N.SV_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("max_new,group", [(2 ** 31 - 1, 1), (2 ** 31 - 128, 1), (2 ** 29, 4), (2 ** 24, 128)])
+def test_more_rows_than_32_bits_count_are_refused(N, max_new, group):
+    """Rounded up to whole tiles of up to 128 rows; one row less is taken."""
+    a = N.KvAttentionDesc(_kv(N), 2 * group, max_new, 12, N.SV_BF16, 0.125, 0, 0, 0, 512, 64, 512, 64)
+    assert N.lib().sv_kv_attention_workspace_size(ctypes.byref(a)) == 0
+    a.max_new = (2 ** 31 - 129) // group
+    assert N.lib().sv_kv_attention_workspace_size(ctypes.byref(a)) > 0
