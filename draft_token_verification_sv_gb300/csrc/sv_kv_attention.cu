@@ -9,7 +9,10 @@
 // row keeps queries in range; fp32 queries and weights are the sum of two fp16,
 // bf16 queries fit one, and their weights are rounded to 2^-11, an eighth of
 // what the result's type keeps).  Scales of K and V are one factor for each
-// page, on scores and weights.  Sums and statistics are fp32.
+// page, on scores and weights.  Weights become fp16 times their page's V scale
+// and a power of two of their row's own, which follows the row's largest such
+// product: pages of large values without weight cost the others no bits.
+// Sums and statistics are fp32.
 //
 // A warp streams its own steps of 16 tokens through its own ring of
 // asynchronous copies, so that no barrier stands between a block's four warps;
@@ -102,12 +105,31 @@ constexpr int kThreads = 32 * kWarps;
 // 119, 164 and 34.5 us without, 112, 161 and 32.4 with 3, 113, 155 and 32.8 with 8, 117, 157 and 33.5 with 12.
 constexpr int kOpen = 6;
 
+constexpr float kMost = 8192.0f;  // sum of a thread's four weights of a row as they become fp16
+// Scales are 2^-100 or larger.  Where the scale is part of the weights' exponent, pages 2^100 and more below what carries a row's
+// weight (zeros may be: they have the smallest scale) count as 2^-100 of it, so that their weights still count in the row's sum.
+constexpr float kMostLift = 106.0f, kLeastUnit = -100.0f, kLeastScale = 0x1p-110f;
+
+// The largest power of two that is no larger, of a positive normal number.
+__device__ __forceinline__ float power_of_two(float x) { return __uint_as_float(__float_as_uint(x) & 0x7f800000u); }
+
+// log2 of a positive normal number, exact for powers of two (lg2.approx is not below 1): of the exponent and of the rest.
+__device__ __forceinline__ float scale_log2(float x) {
+  const uint32_t u = __float_as_uint(x);
+  float rest;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(rest) : "f"(__uint_as_float((u & 0x7fffffu) | 0x3f800000u)));
+  return __uint_as_float(u >> 23 | 0x4b000000u) - 8388735.0f + rest;  // 2^23 + exponent + 127
+}
+
 // DP: head_dim rounded up to 64, 128 or 256 (the rest is zeros).  MT: tiles of
 // 16 rows.  What the rows take in registers (values' sums 16 DP, queries 8 DP,
 // for fp32 16 DP, floats of a warp) sets how many blocks an SM holds.
 template <typename E, int DP, int MT> struct Shape {
   static constexpr bool kSplit = sizeof(E) == 4;  // queries and weights as two fp16 each
   static constexpr bool kQueriesStay = MT == 1 || DP == 64;  // in registers; else read from shared memory for every step
+  // A step's V scale and its rows' lift: in the exponent of the weights, or multiplied to them.  Chains of 8 (two tiles) take 157 and
+  // 159.6 us, a step of 64 sequences (one tile, where what stands between two products counts for more) 115 and 112.7.
+  static constexpr bool kFold = MT == 2;
   static constexpr int kRows = 16 * MT;
   static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 4 : kSplit ? 2 : 3;
   static constexpr int kBlocksPerSm = MT == 1 && !kSplit ? (DP == 64 ? 4 : DP == 128 ? 3 : 2) : DP == 64 && !(kSplit && MT == 2) ? 3 : 2;
@@ -297,15 +319,18 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
     const int all = parents ? s.ctx : s.ctx + i0 + 1, far = s.ctx + i1;
 
     float o[MT][NT][4] = {};
-    float m[MT][2], l[MT][2];
+    // m: a row's maximum so far (whole, base 2), l: its sum of weights.  Weights are multiplied by their page's V scale and by
+    // the row's lift to become fp16: a power of two (its exponent, where folded) that put the largest such product at 2^6 and
+    // more when it was taken.
+    float m[MT][2], l[MT][2], lift[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         m[mt][k] = -CUDART_INF_F;
         l[mt][k] = 0.0f;
+        lift[mt][k] = S::kFold ? 0.0f : 1.0f;
       }
-    float v_ref = 0.0f, v_unit = 0.0f;  // weights are multiplied by v_scale * v_unit, v_unit = 2^6 / v_ref
     int stage = 0;
 #pragma unroll 1
     for (int step = step0; step < step1; step += kWarps) {
@@ -314,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
       const uint8_t* k_at = ring + stage * S::kStageBytes;
       const uint8_t* v_at = k_at + kStep * DP;
       const float* sc = reinterpret_cast<const float*>(ring + S::kStages * S::kStageBytes + stage * 16);
-      const float k_scale = sc[0], v_scale = sc[1];
+      const float k_scale = sc[0], v_scale = fmaxf(sc[1], kLeastScale), v_log2 = S::kFold ? scale_log2(v_scale) : 0.0f;
       // products of 16 tokens: x[n][0..1] row's, [2..3] row + 8's, tokens 8 n + 2 col + {0, 1}
       float x[MT][2][4] = {};
 #pragma unroll
@@ -366,18 +391,6 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
       const int t0 = steps.token(step);
       const bool lost = (bad >> stage) & 1u;
       const bool whole = !lost && t0 + kStep <= all && (a.window == 0 || far - t0 < a.window || t0 + kStep <= a.sinks);
-      if (__builtin_expect(v_scale > v_ref, 0)) {  // uniform: a page with larger values than any before
-        const float fix = v_ref / v_scale;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[mt][t][k] *= fix;
-        v_ref = v_scale;
-        v_unit = 64.0f / v_scale;
-      }
-      const float unit = v_scale * v_unit;
       uint32_t p[MT][4], p_rest[SPLIT ? MT : 1][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -390,15 +403,21 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
             if (!lost && j < steps.end && sees(a, parents, s.ctx, s_token[r], s_pos[r], j)) seen |= 1u << n;
           }
         }
-        // Weights against the maximum so far; where they sum to 2^7 and more (infinity where there is no maximum yet) it is
-        // raised and they are taken again.
+        // Weights against the maximum so far; where they sum to 2^13 and more (infinity where there is no maximum yet) the rows'
+        // maxima are raised, their lifts taken anew, and they are taken again.
         const float f[2] = {factor[mt][0] * k_scale, factor[mt][1] * k_scale};
-        float e[2][4], sum[2];
+        float e[2][4], sum[2], unit[2];
         const auto weigh = [&]() {
+          float c[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            unit[k] = S::kFold ? fmaxf(v_log2 + lift[mt][k], kLeastUnit) : fminf(v_scale * lift[mt][k], 0x1p126f);
+            c[k] = S::kFold ? unit[k] - m[mt][k] : -m[mt][k];
+          }
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) e[n][k] = ex2(fmaf(x[mt][n][k], f[k >> 1], -m[mt][k >> 1]));
+            for (int k = 0; k < 4; ++k) e[n][k] = ex2(fmaf(x[mt][n][k], f[k >> 1], c[k >> 1]));
           if (__builtin_expect(!whole, 0))
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -408,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
           for (int k = 0; k < 2; ++k) sum[k] = (e[0][2 * k] + e[0][2 * k + 1]) + (e[1][2 * k] + e[1][2 * k + 1]);
         };
         weigh();
-        if (__builtin_expect(__any_sync(0xffffffffu, sum[0] > 128.0f || sum[1] > 128.0f), 0)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, (S::kFold ? sum[0] : sum[0] * unit[0]) > kMost || (S::kFold ? sum[1] : sum[1] * unit[1]) > kMost), 0)) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float top = -CUDART_INF_F;
@@ -417,25 +436,37 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
 #pragma unroll
               for (int i = 0; i < 2; ++i)
                 if (seen >> (4 * n + 2 * k + i) & 1u) top = fmaxf(top, x[mt][n][2 * k + i] * f[k]);
-            const float up = fmaxf(m[mt][k], quad_max(top));
-            const float fix = up == -CUDART_INF_F ? 1.0f : ex2(m[mt][k] - up);
+            top = quad_max(top);
+            const float up = fmaxf(m[mt][k], ceilf(top));
+            const bool none = up == -CUDART_INF_F;  // the row sees nothing so far: no maximum, nothing to scale
+            const float down = none ? 0.0f : m[mt][k] - up, l_fix = ex2(down);
+            float to, o_fix;  // the lift that this step asks for, or what is left of the one so far
+            if constexpr (S::kFold) {
+              to = none ? lift[mt][k] : fminf(fminf(lift[mt][k] - down, 7.0f - ceilf(top - up + v_log2)), kMostLift);
+              o_fix = ex2(down + (to - lift[mt][k]));
+            } else {
+              to = none ? lift[mt][k]
+                        : power_of_two(fminf(fminf(__fdividef(lift[mt][k], l_fix), __fdividef(128.0f, ex2(top - up) * v_scale)), 0x1p106f));
+              o_fix = l_fix > 0.0f ? l_fix * __fdividef(to, lift[mt][k]) : 0.0f;
+            }
             m[mt][k] = up;
-            l[mt][k] *= fix;
+            lift[mt][k] = to;
+            l[mt][k] *= l_fix;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              o[mt][t][2 * k] *= fix;
-              o[mt][t][2 * k + 1] *= fix;
+              o[mt][t][2 * k] *= o_fix;
+              o[mt][t][2 * k + 1] *= o_fix;
             }
           }
           weigh();
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) l[mt][k] += sum[k];
+        for (int k = 0; k < 2; ++k) l[mt][k] = S::kFold ? fmaf(sum[k], ex2(-unit[k]), l[mt][k]) : l[mt][k] + sum[k];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float u = e[n][2 * k] * unit, v = e[n][2 * k + 1] * unit;
+            const float u = S::kFold ? e[n][2 * k] : e[n][2 * k] * unit[k], v = S::kFold ? e[n][2 * k + 1] : e[n][2 * k + 1] * unit[k];
             p[mt][2 * n + k] = floats_to_f16x2(u, v);
             if constexpr (SPLIT) p_rest[mt][2 * n + k] = rest_f16x2(u, v, p[mt][2 * n + k]);
           }
@@ -505,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
         float top = s_m[0][r];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) top = fmaxf(top, s_m[i][r]);
-        const float fix = (m[mt][k] == -CUDART_INF_F ? (l[mt][k] == 0.0f ? 0.0f : 1.0f) : ex2(m[mt][k] - top)) * v_ref * (1.0f / 64.0f);
+        const float fix = (m[mt][k] == -CUDART_INF_F ? (l[mt][k] == 0.0f ? 0.0f : 1.0f) : ex2(m[mt][k] - top)) * (S::kFold ? ex2(-lift[mt][k]) : 1.0f / lift[mt][k]);
         // a lane's dims of tiles h NV ..: 2 NV in a row, from h (8 NV) + 2 NV col
 #pragma unroll
         for (int h = 0; h < NT / NV; ++h)

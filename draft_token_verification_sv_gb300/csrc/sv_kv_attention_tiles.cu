@@ -49,7 +49,7 @@ constexpr int kThreads = 32 * (kSoftmaxWarps + kValueWarps + 4);
 constexpr int kSoftmaxRegisters = 176, kValueRegisters = 96, kOtherRegisters = 64;
 static_assert(kSoftmaxWarps * kSoftmaxRegisters + kValueWarps * kValueRegisters + 4 * kOtherRegisters <= 16 * 128,
               "registers of a block");
-constexpr float kLift = 8.0f;  // weights are 2^8 times what they stand for: fp16 then keeps 2^-22 of the largest
+constexpr float kLift = 8.0f;  // weights are 2^8 times what they stand for: fp16 then keeps 2^-22 of a row's largest
 
 constexpr int kCodeStages = 8;   // tiles of codes in shared memory,
 constexpr int kValueStages = 4;  // of widened values,
@@ -517,8 +517,9 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
       __syncwarp();
     }
 
-    // m: the maximum so far (base 2), l: sum of weights, v_ref: log2 of the values' unit
-    float m = -CUDART_INF_F, l = 0.0f, v_ref = kNoScale;
+    // m: the row's maximum so far (base 2), l: its sum of weights.  v_ref: m + v_ref is the largest sum so far of a score and
+    // the log2 of its page's V scale; weights are multiplied by 2^(that log2 - v_ref), whatever larger scales carry no weight.
+    float m = -CUDART_INF_F, l = 0.0f, v_ref = 0.0f;
     const int end = it0 + p.count;
     int it = it0 + ((it0 & 1) != group);
     const int begin = it;
@@ -527,7 +528,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
       const int stage = it % kScoreStages;
       const uint32_t scores = mine + T::kS + stage * kTokens;
       if (!wait(sh.plan_full[it % kPlans], it / kPlans) || !wait(sh.s_full[stage], it / kScoreStages)) return false;
-      // O is multiplied by `fix`, a power of two
+      // O is multiplied by `fix`, a power of two (where scales of V are)
       const auto rescale = [&](float fix) {
         if (it == begin) return true;
         if (!wait(sh.pv_done[(it - 2) % kValueStages], (it - 2) / kValueStages)) return false;
@@ -543,13 +544,6 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
         tc::wait_stores();  // a second change in the same tile loads them again
         return true;
       };
-      float v_top = kNoScale;
-#pragma unroll
-      for (int i = 0; i < kTileSteps; ++i) v_top = fmaxf(v_top, plan.v_log2[i]);
-      if (__builtin_expect(v_top > v_ref, 0)) {  // the same for all threads
-        if (!rescale(v_ref == kNoScale ? 0.0f : ex2(v_ref - v_top))) return false;
-        v_ref = v_top;
-      }
       const auto tile = [&](auto masked) {
         constexpr bool M = decltype(masked)::value;
         uint32_t seen0 = 0, seen1 = 0;
@@ -559,23 +553,34 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
         }
         const float* k = plan.k_scale;
         const float* v = plan.v_log2;
-        // against the maximum so far, unless there is none; raised, and gone over again, where weights get too large
-        bool raise = __any_sync(0xffffffffu, m == -CUDART_INF_F);
+        // against the maximum so far, unless there is none; raised, and gone over again, where weights get too large.  Rows do
+        // not depend on each other: one that needs nothing keeps its bits.
+        bool mine = m == -CUDART_INF_F;
+        bool raise = __any_sync(0xffffffffu, mine);
 #pragma unroll 1
-        for (bool sure = raise;; sure = true) {
+        for (int pass = 0;; ++pass) {
           uint32_t x0[32], x1[32];
           if (__builtin_expect(raise, 0)) {
             tc::tmem_load32(scores, x0);
             tc::tmem_load32(scores + 32, x1);
             tc::wait_loads(x0);
             tc::wait_loads(x1);
-            float top = fmaxf(fmaxf(largest16<M>(&x0[0], seen0) * (factor * k[0]), largest16<M>(&x0[16], seen0 >> 16) * (factor * k[1])),
-                              fmaxf(largest16<M>(&x1[0], seen1) * (factor * k[2]), largest16<M>(&x1[16], seen1 >> 16) * (factor * k[3])));
-            top = fmaxf(m, ceilf(top));  // whole: what is scaled anew is scaled exactly (m where scores are not numbers)
-            const float fix = top == -CUDART_INF_F ? 1.0f : ex2(m - top);
-            m = top;
-            l *= fix;
-            if (!rescale(fix)) return false;
+            float top = -CUDART_INF_F, most = m + v_ref;  // of scores, and with their V scales
+#pragma unroll
+            for (int i = 0; i < kTileSteps; ++i) {  // whole: what is scaled anew is scaled exactly (fmaxf leaves out what is not a number)
+              const float t = ceilf(largest16<M>(i < 2 ? &x0[16 * i] : &x1[16 * i - 32], (i < 2 ? seen0 : seen1) >> (16 * (i & 1))) * (factor * k[i]));
+              top = fmaxf(top, t);
+              most = fmaxf(most, t + v[i]);
+            }
+            top = fmaxf(m, top);
+            float o_fix = 1.0f;
+            if (mine && top > -CUDART_INF_F) {
+              o_fix = ex2(m + v_ref - most);
+              l *= ex2(m - top);
+              m = top;
+              v_ref = most - top;
+            }
+            if (!rescale(o_fix)) return false;
           }
           tc::tmem_load32(scores, x0);
           tc::tmem_load32(scores + 32, x1);
@@ -592,7 +597,8 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
           sums = weights32<M>(x1, seen1, factor * k[2], factor * k[3], base + u0, base + u1, w1);
           most = fmaxf(most, fmaxf(sums.x, sums.y));
           sum += sums.x * ex2(-u0) + sums.y * ex2(-u1);
-          raise = !sure && __any_sync(0xffffffffu, most > 32768.0f);
+          mine = most > 32768.0f;
+          raise = pass < 2 && __any_sync(0xffffffffu, mine);  // (the first pass may be for other rows; a raised row has sums below)
           if (!raise) {
             l += sum;
             tc::tmem_store(scores, w0);

@@ -22,11 +22,13 @@ def sv():
     return sv
 
 
-def _compare(sv, cache, table, page, ctx, q, dtype, scale):
-    """One sequence, one new token, one kv head."""
+def _compare(sv, cache, table, page, ctx, q, dtype, scale, copies=1):
+    """One sequence, one new token, one kv head (or so many sequences on the
+    same pages, each then the work of a block or two)."""
     heads, dim = q.shape[1:]
-    lens = to_gpu(np.array([ctx], np.int32))
-    out, lse = sv.kv_attention(to_gpu(q, dtype)[None], cache_gpu(cache), to_gpu(table), lens, scale=scale, lse=True)
+    lens = to_gpu(np.full(copies, ctx, np.int32))
+    outs, sums = sv.kv_attention(to_gpu(np.stack([q] * copies), dtype), cache_gpu(cache), to_gpu(np.repeat(table, copies, 0)), lens,
+                                 scale=scale, lse=True)
     want, wlse, absolute, largest = KO.attention(q.astype(np.float64), cache, table[0], page, ctx, None, scale, 0, 0)
     tol, ltol = attention_tolerance(want, absolute, largest, ctx + 1, dim, dtype)
     # weights end at 2^-31 of the row's largest, counted with the scales of V
@@ -35,9 +37,9 @@ def _compare(sv, cache, table, page, ctx, q, dtype, scale):
     unit = cache["v_scale"][table[0][np.arange(ctx + 1) // page], 0]
     p = np.exp(q[0].astype(np.float64) @ k.T * scale - wlse[0][:, None])
     tol[0] += 2.0 ** -31 * (p * unit).max(1)[:, None] * codes.sum(0)
-    off = np.abs(out[0].double().cpu().numpy() - want)
+    off = np.abs(outs.double().cpu().numpy() - want)
     assert (off <= tol).all(), float((off / tol).max())
-    loff = np.abs(lse[0].double().cpu().numpy() - wlse)
+    loff = np.abs(sums.double().cpu().numpy() - wlse)
     assert (loff <= ltol).all(), float((loff / ltol).max())
 
 
@@ -58,3 +60,45 @@ def test_weights_and_values_that_rise_together(sv, dtype, heads, dim):
     q = np.zeros((1, heads, dim), np.float32)
     q[0, :, 0] = np.linspace(0.05, 0.7, heads)
     _compare(sv, cache, table, page, ctx, round_to(q, dtype), dtype, 1.0)
+
+
+@pytest.mark.parametrize("dtype,heads", ROWS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("r", [0, 10, 16, 24, 60])
+def test_pages_of_large_values_without_weight(sv, dtype, heads, dim, where, r):
+    """One token of much weight and a long even tail 2^-12 below it, on pages
+    whose scale of V lies 2^-r below that of pages that weigh 2^-40 and less."""
+    g = np.random.default_rng(r + dim)
+    page, ctx = 16, 2999
+    table, pages = make_table(g, [ctx + 1], page)
+    cache = make_cache(g, pages, 1, page, dim)
+    cache["k"][:] = 0
+    cache["k_scale"][:] = 1.0
+    cache["k"][..., 0] = KO.encode(-12.0)
+    cache["v"] = np.maximum(cache["v"] & 0x7f, 0x20).astype(np.uint8) | (cache["v"] & 0x80)
+    cache["v_scale"][:] = 2.0 ** -6
+    at = {"first": 0, "middle": 101, "last": (ctx + 1) // page - 8}[where]
+    heavy = table[0, at:at + 8]  # enough for every warp to meet one
+    cache["v_scale"][heavy] *= 2.0 ** r
+    cache["k"][heavy, 0, :, 0] = KO.encode(-(40.0 + min(r, 40)))
+    peak = 1234
+    cache["k"][table[0, peak // page], 0, peak % page, 0] = 0
+    q = np.zeros((1, heads, dim), np.float32)
+    q[0, :, 0] = np.log(2.0) * (1 + np.arange(heads) / 200)
+    _compare(sv, cache, table, page, ctx, round_to(q, dtype), dtype, 1.0, copies=600)
+
+
+@pytest.mark.parametrize("dtype,heads", ROWS)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_pages_of_zeros_among_large_values(sv, dtype, heads, dim):
+    """Appended zeros have the smallest scale, 2^-100; their weights count all the same."""
+    g = np.random.default_rng(dim + heads)
+    page, ctx = 16, 400
+    table, pages = make_table(g, [ctx + 1], page)
+    cache = make_cache(g, pages, 1, page, dim)
+    zeros = table[0, ::3]
+    cache["v"][zeros] = 0
+    cache["v_scale"][zeros] = 2.0 ** -100
+    cache["v_scale"][table[0, 1::3]] = 2.0 ** 20
+    _compare(sv, cache, table, page, ctx, round_to(g.normal(0, 1.5, (1, heads, dim)), dtype), dtype, dim ** -0.5)
