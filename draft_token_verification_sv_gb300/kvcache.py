@@ -28,6 +28,7 @@ from .verify import _WORKSPACES, _code, workspace
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _KEPT = 4096  # combinations of shapes kept for each entry point
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -79,9 +80,8 @@ def _numel(shape) -> int:
     return n
 
 
-def _count(value, name: str) -> int:
-    """``value`` as an int that the descriptors' 32 bits hold."""
-    n = int(value)
+def _count(n: int, name: str) -> int:
+    """``n``, if the descriptors' 32 bits hold it."""
     if not -2 ** 31 <= n < 2 ** 31:
         raise ValueError(f"{name} must fit 32 bits, got {n}")
     return n
@@ -160,7 +160,7 @@ def _new(new_start, max_new, m: _Meta, B):
     _int32(new_start, "new_start", B + 1, "one entry more than page_table has rows")
     if max_new is None:
         raise ValueError("new_start needs max_new, the largest number of new tokens of a sequence")
-    return max_new
+    return _count(max_new, "the largest number of new tokens")
 
 
 _PER_SEQUENCE = "one entry for each sequence"
@@ -223,7 +223,7 @@ def _attention_plan(q, kc, vc, ks, vs, table, lens, start, max_new, parents, sca
         raise ValueError("out must match q in shape and dtype")
     _, _, _, o_row, o_head = _rows(out, "out", B, ragged)
     a = N.KvAttentionDesc(d, heads, _new(start, max_new, q, B), n, _code(q),
-                          dim ** -0.5 if scale is None else scale, window, sinks, 0, q_row, q_head,
+                          dim ** -0.5 if scale is None else scale, _count(window, "window"), _count(sinks, "sinks"), 0, q_row, q_head,
                           o_row, o_head)
     _int32(status, "row_status", B, _PER_SEQUENCE)
     return (ctypes.byref(a), N.lib().sv_kv_attention_workspace_size(ctypes.byref(a)),
@@ -244,7 +244,7 @@ def _stream_of(stream, device: int) -> int:
 
 def _call(device: int, entry: str, *args) -> None:
     """A call of the library with its tensors' GPU as the current one."""
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         st = getattr(N.lib(), entry)(*args)
     else:
         with torch.cuda.device(device):
@@ -273,7 +273,7 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, page_table: torch.T
     and returns ``cache``; ``row_status`` [B] int32 receives the flags."""
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     d, r, gpu = _append_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(k), _meta(v),
-                             _meta(new_start), None if max_new is None else _count(max_new, "max_new"), _meta(row_status))
+                             _meta(new_start), None if max_new is None else int(max_new), _meta(row_status))
     _call(gpu, "sv_kv_append", d, r, k.data_ptr(), v.data_ptr(), page_table.data_ptr(), ctx_lens.data_ptr(), _at(new_start),
           kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), _at(row_status), _stream_of(stream, gpu))
     return cache
@@ -287,7 +287,7 @@ def kv_read(cache: dict, page_table: torch.Tensor, first: torch.Tensor, tokens: 
     Returns (k, v): [B, tokens, kv_heads, dim], or with ``new_start`` [B + 1]
     [total, kv_heads, dim] rows, ``tokens`` being the most of one sequence."""
     kc, vc, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
-    tokens = _count(tokens, "tokens")
+    tokens = int(tokens)
     if out is None:
         _, heads, _, dim = kc.shape
         if new_start is None:
@@ -318,7 +318,7 @@ def kv_commit(cache: dict, page_table: torch.Tensor, ctx_lens: torch.Tensor, pat
         new_lens = _empty(ctx_lens.shape, ctx_lens.dtype, ctx_lens.device, stream)
     d, length, gpu = _commit_plan(_meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens), _meta(path),
                                   _meta(accept_len), _meta(new_lens), _meta(row_status))
-    _call(gpu, "sv_kv_commit", d, _count(nodes, "nodes"), length, page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
+    _call(gpu, "sv_kv_commit", d, _count(int(nodes), "nodes"), length, page_table.data_ptr(), ctx_lens.data_ptr(), path.data_ptr(),
           accept_len.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), new_lens.data_ptr(),
           _at(row_status), _stream_of(stream, gpu))
     return new_lens
@@ -341,8 +341,8 @@ def kv_attention(q: torch.Tensor, cache: dict, page_table: torch.Tensor, ctx_len
     if out is None:
         out = _empty(q.shape, q.dtype, device, stream)
     a, need, gpu = _attention_plan(_meta(q), _meta(kc), _meta(vc), _meta(ks), _meta(vs), _meta(page_table), _meta(ctx_lens),
-                                   _meta(new_start), None if max_new is None else _count(max_new, "max_new"), _meta(parents),
-                                   None if scale is None else float(scale), _count(window, "window"), _count(sinks, "sinks"),
+                                   _meta(new_start), None if max_new is None else int(max_new), _meta(parents),
+                                   None if scale is None else float(scale), int(window), int(sinks),
                                    _meta(out), _meta(row_status))
     sums = _empty(q.shape[:-1], torch.float32, device, stream) if lse else None
     raw = _stream_of(stream, gpu)

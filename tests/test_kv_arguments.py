@@ -106,7 +106,7 @@ def fake_streams(monkeypatch):
             return lambda *args: 1000 if name.endswith("size") else N.SV_OK
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Fake("main"))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(sv.kvcache, "_current_device", lambda: 0)
     monkeypatch.setattr(torch, "empty", allocate)
     monkeypatch.setattr(torch, "zeros", allocate)
     monkeypatch.setattr(sv.kvcache, "_raw_stream", lambda index: 0)
