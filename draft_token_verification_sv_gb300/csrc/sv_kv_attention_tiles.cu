@@ -6,27 +6,30 @@
 // in tensor memory, where the weights P take the place of the scores they
 // come from.  One block per SM, five roles:
 //   1 warp plans: it walks the block's tiles and looks pages and scales up;
-//   1 warp fetches codes, a box of 16 tokens of a page to a copy, up to
-//     eight tiles ahead: keys to where the products read them, swizzled;
-//   4 warps widen the values to fp16 (which holds them all);
+//   1 warp fetches codes, a box of 16 tokens of a page to a copy, three tiles
+//     ahead of the widening (eight of up to 64 dims);
+//   4 warps widen keys and values to fp16 (which holds them all), to where the
+//     products read them, swizzled;
 //   1 warp issues the products: S of tile t before P V of tile t - 2;
 //   2 groups of 4 warps turn scores into weights, a row a thread, one group
 //     the even tiles and the other the odd ones, each with its own running
 //     maximum and its own O, which are joined where an item's part ends.
 //     The maximum moves only when weights reach 2^7 times it (then O is
 //     scaled anew), so that scores are read once and no maximum is taken.
-// S is formed in 8 bits without loss: a bf16 query is the sum of two e4m3
-// values (4 significant bits each, of 8; what lies below 2^-17 of the row's
-// largest is rounded), so S is two products of queries with the codes
-// themselves.  Weights would need more: a long even tail of a softmax lies
-// below e4m3's range, so P V is fp16.
+// Both products are fp16.  A power of two for each row puts its largest query
+// at 2^14 and more, so that a bf16 query keeps all its bits down to 2^-31 of
+// the row's largest.  (8-bit scores, of queries as the sum of two e4m3 values
+// and keys as they come, were 2% to 3% faster, 124 and 364 us, but rounded what
+// lies below 2^-17 of it: one dim far above the others cost the others theirs.)
+// Weights would not fit 8 bits either: a long even tail of a softmax lies below
+// e4m3's range.
 // Work is shared out as in sv_kv_schedule.cuh.
 //
-// 2000 tokens of two prompts behind 4096 cached ones, 32 heads of 128 dims: 364
-// us, 805 TFLOP/s of useful work, bound by the step from scores to weights (two
+// 2000 tokens of two prompts behind 4096 cached ones, 32 heads of 128 dims: 375
+// us, 780 TFLOP/s of useful work, bound by the step from scores to weights (two
 // tiles of it under way at a time, 1.4 thousand cycles each) and what each step
-// of a tile waits for the other.  64 trees of 32 nodes on up to 4096 tokens: 124
-// us, 2.7 TB/s, a fifth of it spent at the ends of items.
+// of a tile waits for the other.  64 trees of 32 nodes on up to 4096 tokens: 127
+// us, 2.65 TB/s, a fifth of it spent at the ends of items.
 #include "sv_kv_schedule.cuh"
 #include "sv_tcgen05.cuh"
 
@@ -42,31 +45,33 @@ constexpr int kTokens = kStep * kTileSteps;
 // Empty tiles ahead of an item: none, 5, 8 and 12 take 153, 135, 124 and 124 us for 64 trees of 32 nodes on contexts of up to
 // 4096 tokens, 370, 364, 367 and 370 for 2000 tokens of two prompts behind 4096, 367, 220, 197 and 201 for 16 prompts of 836.
 constexpr int kOpen = 8;
-// weights: warps 0-7; values: 8-11; products: 12; plan: 13; fetch: 14 (15 idle: registers move in fours of warps)
-constexpr int kSoftmaxWarps = 8, kValueWarps = 4;
-constexpr int kValueThreads = 32 * kValueWarps;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kValueWarps + 4);
-constexpr int kSoftmaxRegisters = 176, kValueRegisters = 96, kOtherRegisters = 64;
-static_assert(kSoftmaxWarps * kSoftmaxRegisters + kValueWarps * kValueRegisters + 4 * kOtherRegisters <= 16 * 128,
+// weights: warps 0-7; widening: 8-11; products: 12; plan: 13; fetch: 14 (15 idle: registers move in fours of warps)
+constexpr int kSoftmaxWarps = 8, kWidenWarps = 4;
+constexpr int kWidenThreads = 32 * kWidenWarps;
+constexpr int kThreads = 32 * (kSoftmaxWarps + kWidenWarps + 4);
+constexpr int kSoftmaxRegisters = 176, kWidenRegisters = 96, kOtherRegisters = 64;
+static_assert(kSoftmaxWarps * kSoftmaxRegisters + kWidenWarps * kWidenRegisters + 4 * kOtherRegisters <= 16 * 128,
               "registers of a block");
 constexpr float kLift = 8.0f;  // weights are 2^8 times what they stand for: fp16 then keeps 2^-22 of a row's largest
 
-constexpr int kCodeStages = 8;   // tiles of codes in shared memory,
-constexpr int kValueStages = 4;  // of widened values,
-constexpr int kScoreStages = 3;  // and of scores in tensor memory
+constexpr int kMostCodeStages = 8;
+constexpr int kValueStages = 6;  // tiles of widened values in shared memory,
+constexpr int kScoreStages = 3;  // of widened keys, and of scores in tensor memory
 constexpr int kLag = 2;          // tiles that scores are formed ahead of the sums over values
 
 constexpr int kPiece = 80;       // 64 bytes of a row of queries, at a pitch free of bank conflicts
 
 template <int DP> struct Tiles {
-  static constexpr int kKeyBytes = kTokens * 128;          // a tile's keys: rows of 128 bytes (DP = 64 leaves half)
-  static constexpr int kCodeBytes = kTokens * DP;          // its values' codes as they come,
-  static constexpr int kValueBytes = kTokens * DP * 2;     // and in fp16,
+  // Tiles of codes in shared memory.  At 128 dims what it holds is better spent on widened values: 5 of codes and 4 of values, 4 and
+  // 5, 3 and 6 take 130, 128 and 127 us for 64 trees of 32 nodes, 378, 375 and 375 for 2000 tokens of two prompts.
+  static constexpr int kCodeStages = DP == 64 ? kMostCodeStages : 3;
+  static constexpr int kCodeBytes = kTokens * DP;          // a tile's codes of keys (and of values) as they come,
+  static constexpr int kTileBytes = kTokens * DP * 2;      // and in fp16,
   static constexpr int kBlockBytes = kTokens * 128;        // in blocks of 64 dims
-  static constexpr int kOperands = kValueStages * kValueBytes + kCodeStages * (kKeyBytes + kCodeBytes) + kSoftmaxWarps * 32 * kPiece;
+  static constexpr int kOperands = (kValueStages + kScoreStages) * kTileBytes + kCodeStages * 2 * kCodeBytes + kSoftmaxWarps * 32 * kPiece;
   // 1 KB to find a 1024-byte boundary; more than half of an SM's shared memory keeps it to one block
   static constexpr int kShared = (kOperands > 118 * 1024 ? kOperands : 118 * 1024) + 1024;
-  // tensor memory, in columns: two O, both parts of Q, three tiles of scores
+  // tensor memory, in columns: two O, Q, three tiles of scores
   static constexpr int kO = 0, kQ = 2 * DP, kS = kQ + DP / 2;
   static constexpr int kColumns = 512;
   static constexpr int kPart = kRows * (DP + 2);  // floats of a part in the workspace
@@ -101,8 +106,8 @@ struct Part {
 struct Shared {
   CursorScratch cursor;
   uint64_t plan_full[kPlans], plan_free[kPlans], part_full[kParts], part_free[kParts];
-  uint64_t codes_full[kCodeStages], codes_free[kCodeStages];
-  uint64_t pv_ready[kValueStages], pv_done[kValueStages], s_full[kScoreStages], q_ready, last, both[4];
+  uint64_t codes_full[kMostCodeStages], codes_free[kMostCodeStages];
+  uint64_t k_ready[kScoreStages], pv_ready[kValueStages], pv_done[kValueStages], s_full[kScoreStages], q_ready, last, both[4];
   float exchange[2][kRows][4];  // between the two threads of a row: maximum, sum, values' unit; the queries' largest
   TilePlan plan[kPlans];
   Part part[kParts];
@@ -220,13 +225,13 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
 
 // Two copies for each step that has tokens, a lane to a copy.
 template <int DP>
-__device__ bool fetch_role(const CUtensorMap* keys, const CUtensorMap* values, const int tiles, Shared& sh, uint32_t k_tiles, uint32_t codes) {
+__device__ bool fetch_role(const CUtensorMap* keys, const CUtensorMap* values, const int tiles, Shared& sh, uint32_t codes) {
   using T = Tiles<DP>;
+  constexpr int kCodeStages = T::kCodeStages;
   const int lane = threadIdx.x & 31, step = lane % kTileSteps;
   const bool key = lane < kTileSteps;
   const CUtensorMap* map = key ? keys : values;
-  const uint32_t to = key ? k_tiles + step * (kStep * 128) : codes + step * (kStep * DP);
-  const int stride = key ? T::kKeyBytes : T::kCodeBytes;
+  const uint32_t to = codes + (key ? 0 : T::kCodeBytes) + step * (kStep * DP);
   for (int it = 0; it < tiles; ++it) {
     const TilePlan& plan = sh.plan[it % kPlans];
     const int stage = it % kCodeStages;
@@ -238,11 +243,11 @@ __device__ bool fetch_role(const CUtensorMap* keys, const CUtensorMap* values, c
     if (it >= kCodeStages && !warp_wait(sh, sh.codes_free[stage], it / kCodeStages - 1)) return false;
     const uint32_t bar = tc::smem_address(&sh.codes_full[stage]);
     if (lane == 0) {
-      tc::barrier_expect(bar, copies / 2 * (kStep * (128 + DP)));
+      tc::barrier_expect(bar, copies * (kStep * DP));
       sh.fetched = it + 1;
     }
     __syncwarp();
-    if (live) tc::copy_box(to + stage * stride, map, 0, slot, head, page, bar);
+    if (live) tc::copy_box(to + stage * 2 * T::kCodeBytes, map, 0, slot, head, page, bar);
   }
   return true;
 }
@@ -250,47 +255,58 @@ __device__ bool fetch_role(const CUtensorMap* keys, const CUtensorMap* values, c
 // A chunk of 16 codes becomes two of fp16, in rows of 64 dims, swizzled; lanes of the second block of dims, and those of odd
 // tokens, do its halves the other way round (they use other banks then).  What is not a token in sight becomes 0, whatever its bytes.
 template <int DP>
-__device__ bool value_role(const int tiles, Shared& sh, uint8_t* v_tiles, const uint8_t* codes) {
+__device__ bool widen_role(const int tiles, Shared& sh, uint8_t* k_tiles, uint8_t* v_tiles, const uint8_t* codes) {
   using T = Tiles<DP>;
+  constexpr int kCodeStages = T::kCodeStages;
   constexpr int kChunks = DP / 16;                        // of a token
-  constexpr int kPer = kValueThreads / kChunks;           // tokens of a pass, 16 or 32
+  constexpr int kPer = kWidenThreads / kChunks;           // tokens of a pass, 16 or 32
   constexpr int NI = kTokens / kPer;                      // passes
   const int tid = threadIdx.x - 32 * kSoftmaxWarps;
   const int t0 = tid / kChunks, ch = tid % kChunks;
   const int turn = ((ch >> 2) ^ t0) & 1;
   const int to = (ch >> 2) * T::kBlockBytes + t0 * 128;
   const int half0 = to + (((2 * (ch & 3) + turn) ^ (t0 & 7)) << 4), half1 = to + (((2 * (ch & 3) + 1 - turn) ^ (t0 & 7)) << 4);
-#pragma unroll 1
-  for (int it = 0; it < tiles; ++it) {
-    const int st = it % kValueStages, stage = it % kCodeStages;
-    const TilePlan& plan = sh.plan[it % kPlans];
-    if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans) || !warp_wait(sh, sh.codes_full[stage], it / kCodeStages)) return false;
-    const uint8_t* from = codes + stage * T::kCodeBytes + t0 * DP + ch * 16;
-    uint2 c[NI][2];
+  uint2 c[NI][2];
+  const auto load = [&](const uint8_t* from, unsigned seen) {
+    from += t0 * DP + ch * 16;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      c[i][0] = *reinterpret_cast<const uint2*>(from + i * kPer * DP + 8 * turn);
-      c[i][1] = *reinterpret_cast<const uint2*>(from + i * kPer * DP + 8 - 8 * turn);
+      const bool live = seen >> i & 1u;
+      c[i][0] = live ? *reinterpret_cast<const uint2*>(from + i * kPer * DP + 8 * turn) : make_uint2(0, 0);
+      c[i][1] = live ? *reinterpret_cast<const uint2*>(from + i * kPer * DP + 8 - 8 * turn) : make_uint2(0, 0);
     }
-    if (!plan.whole) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (t0 % kStep >= plan.count[(t0 + i * kPer) / kStep]) c[i][0] = c[i][1] = make_uint2(0, 0);
-    }
-    warp_arrive(sh.plan_free[it % kPlans]);
-    // the products of tile it - 4, after which its keys' and codes' place is free too
-    if (it >= kValueStages) {
-      if (!warp_wait(sh, sh.pv_done[st], it / kValueStages - 1)) return false;
-      warp_arrive(sh.codes_free[(it - kValueStages) % kCodeStages]);
-    }
-    uint8_t* row = v_tiles + st * T::kValueBytes;
+  };
+  const auto store = [&](uint8_t* row) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       *reinterpret_cast<uint4*>(row + half0 + i * kPer * 128) = widen(c[i][0]);
       *reinterpret_cast<uint4*>(row + half1 + i * kPer * 128) = widen(c[i][1]);
     }
     tc::publish_shared();
-    warp_arrive(sh.pv_ready[st]);
+  };
+#pragma unroll 1
+  for (int it = 0; it < tiles; ++it) {
+    const int ks = it % kScoreStages, vs = it % kValueStages, stage = it % kCodeStages;
+    const TilePlan& plan = sh.plan[it % kPlans];
+    if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans) || !warp_wait(sh, sh.codes_full[stage], it / kCodeStages)) return false;
+    unsigned seen = ~0u;  // bit i: the thread's token of pass i is in sight
+    if (!plan.whole) {
+      seen = 0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) seen |= (t0 % kStep < plan.count[(t0 + i * kPer) / kStep] ? 1u : 0u) << i;
+    }
+    warp_arrive(sh.plan_free[it % kPlans]);
+    const uint8_t* from = codes + stage * 2 * T::kCodeBytes;
+    load(from, seen);
+    // (the scores of tile it - 3 have been formed, so its keys' place is free)
+    if (it >= kScoreStages && !warp_wait(sh, sh.s_full[ks], it / kScoreStages - 1)) return false;
+    store(k_tiles + ks * T::kTileBytes);
+    warp_arrive(sh.k_ready[ks]);
+    load(from + T::kCodeBytes, seen);
+    warp_arrive(sh.codes_free[stage]);
+    if (it >= kValueStages && !warp_wait(sh, sh.pv_done[vs], it / kValueStages - 1)) return false;
+    store(v_tiles + vs * T::kTileBytes);
+    warp_arrive(sh.pv_ready[vs]);
   }
   return true;
 }
@@ -313,7 +329,7 @@ __device__ bool product_role(const int tiles, Shared& sh, uint32_t k_tiles, uint
 #pragma unroll
     for (int k = 0; k < kTokens / 16; ++k)
       tc::product_f16(tmem + T::kO + (it & 1) * DP, tmem + T::kS + it % kScoreStages * kTokens + k * 8,
-                      tc::tile_descriptor(v_tiles + v * T::kValueBytes + k * 2048, T::kBlockBytes, 1024), kValues, !first || k > 0);
+                      tc::tile_descriptor(v_tiles + v * T::kTileBytes + k * 2048, T::kBlockBytes, 1024), kValues, !first || k > 0);
     tc::products_arrive(tc::smem_address(&sh.pv_done[v]));
     return true;
   };
@@ -323,13 +339,13 @@ __device__ bool product_role(const int tiles, Shared& sh, uint32_t k_tiles, uint
     tc::barrier_arrive(tc::smem_address(&sh.part_free[item % kParts]));
     if (!wait(sh.q_ready, item)) return false;
     for (int t = 0; t < count; ++t, ++it) {
-      const int s = it % kScoreStages, stage = it % kCodeStages;
-      if (!wait(sh.codes_full[stage], it / kCodeStages)) return false;
-      // (these scores' place was tile it - 3's weights', whose products were issued before)
+      const int s = it % kScoreStages;
+      if (!wait(sh.k_ready[s], it / kScoreStages)) return false;
+      // (these scores' place was tile it - 3's weights, whose products were issued before)
 #pragma unroll
-      for (int k = 0; k < DP / 16; ++k)  // both parts of the queries with the same keys
-        tc::product_e4m3(tmem + T::kS + s * kTokens, tmem + T::kQ + (k & 1) * (DP / 4) + (k >> 1) * 8,
-                         tc::tile_descriptor(k_tiles + stage * T::kKeyBytes + (k >> 1) * 32, 16, 1024), kScores, k > 0);
+      for (int k = 0; k < DP / 16; ++k)
+        tc::product_f16(tmem + T::kS + s * kTokens, tmem + T::kQ + k * 8,
+                        tc::tile_descriptor(k_tiles + s * T::kTileBytes + (k >> 2) * T::kBlockBytes + (k & 3) * 32, 16, 1024), kScores, k > 0);
       tc::products_arrive(tc::smem_address(&sh.s_full[s]));
       if (t >= kLag && !weigh(it - kLag, t - kLag < 2)) return false;
     }
@@ -435,7 +451,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
     const int32_t* parents = a.parents ? a.parents + p.row0 : nullptr;
     const int ctx = p.ctx, token = (p.r0 + min(r, p.rows - 1)) / a.group;
 
-    // the row's queries, scaled by a power of two, in two parts
+    // the row's queries, scaled by a power of two
     float factor;
     {
       const int head = p.h * a.group + (p.r0 + min(r, p.rows - 1)) % a.group;
@@ -484,29 +500,23 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
       if (!meet()) return false;
       top = max(top, __float_as_uint(sh.exchange[group ^ 1][r][3]));
       const int exponent = static_cast<int>(top >> 7);
-      const int e = exponent == 255 || top == 0 ? 0 : min(120, 134 - exponent);
-      // the largest becomes 2^7 .. 2^8; a negative factor goes into the queries, so that larger products are larger scores
+      const int e = exponent == 255 || top == 0 ? 0 : min(120, 141 - exponent);
+      // the largest becomes 2^14 .. 2^15, so that what is 2^-31 of it is kept whole; a negative factor goes into the queries, so
+      // that larger products are larger scores
       const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 < 0.0f ? -1.0f : 1.0f);
       factor = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       if (exponent == 255) factor = CUDART_NAN_F;  // the row's scores are not numbers
-      uint32_t hi[kDims / 4], lo[kDims / 4];
 #pragma unroll
-      for (int i = 0; i < kDims / 4; ++i) {
-        const uint4 c = raw[i >> 1];
-        const uint32_t words[2] = {i & 1 ? c.z : c.x, i & 1 ? c.w : c.y};
-        uint32_t h[2], rest[2];
+      for (int n = 0; n < kDims / 32; ++n) {
+        uint32_t h[16];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float u = __uint_as_float(words[n] << 16) * up, v = __uint_as_float(words[n] & 0xffff0000u) * up;
-          h[n] = floats_to_e4m3x2(u, v);
-          const float2 held = f16x2_to_float2(e4m3x2_to_f16x2(h[n]));
-          rest[n] = floats_to_e4m3x2(u - held.x, v - held.y);
+        for (int i = 0; i < 16; ++i) {
+          const uint4 c = raw[4 * n + (i >> 2)];
+          const uint32_t two = (i & 3) == 0 ? c.x : (i & 3) == 1 ? c.y : (i & 3) == 2 ? c.z : c.w;
+          h[i] = pack_f16x2(__uint_as_float(two << 16) * up, __uint_as_float(two & 0xffff0000u) * up);
         }
-        hi[i] = h[0] | h[1] << 16;
-        lo[i] = rest[0] | rest[1] << 16;
+        tc::tmem_store(mine + T::kQ + group * (kDims / 2) + 16 * n, h);
       }
-      tc::tmem_store(mine + T::kQ + group * (kDims / 4), hi);
-      tc::tmem_store(mine + T::kQ + DP / 4 + group * (kDims / 4), lo);
       arrive(sh.q_ready);
     }
     int pos = ctx + token;
@@ -723,8 +733,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   const uint32_t at = tc::smem_address(raw);
   uint8_t* tiles = raw + ((at + 1023u & ~1023u) - at);
   uint8_t* v_tiles = tiles;
-  uint8_t* k_tiles = tiles + kValueStages * T::kValueBytes;
-  uint8_t* codes = k_tiles + kCodeStages * T::kKeyBytes;
+  uint8_t* k_tiles = v_tiles + kValueStages * T::kTileBytes;
+  uint8_t* codes = k_tiles + kScoreStages * T::kTileBytes;
+  constexpr int kCodeStages = T::kCodeStages;
   const int warp = threadIdx.x >> 5, g = blockIdx.x;
   wait_for_stream();
   flag_sequences(a, g, gridDim.x, kThreads);
@@ -736,16 +747,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
     tc::prefetch_map(&values);
     for (int i = 0; i < kCodeStages; ++i) {
       tc::barrier_init(tc::smem_address(&sh.codes_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.codes_free[i]), kValueWarps);
+      tc::barrier_init(tc::smem_address(&sh.codes_free[i]), kWidenWarps);
     }
     for (int i = 0; i < kValueStages; ++i) {
-      tc::barrier_init(tc::smem_address(&sh.pv_ready[i]), kValueWarps + kSoftmaxWarps / 2);
+      tc::barrier_init(tc::smem_address(&sh.pv_ready[i]), kWidenWarps + kSoftmaxWarps / 2);
       tc::barrier_init(tc::smem_address(&sh.pv_done[i]), 1);
     }
-    for (int i = 0; i < kScoreStages; ++i) tc::barrier_init(tc::smem_address(&sh.s_full[i]), 1);
+    for (int i = 0; i < kScoreStages; ++i) {
+      tc::barrier_init(tc::smem_address(&sh.k_ready[i]), kWidenWarps);
+      tc::barrier_init(tc::smem_address(&sh.s_full[i]), 1);
+    }
     for (int i = 0; i < kPlans; ++i) {
       tc::barrier_init(tc::smem_address(&sh.plan_full[i]), 1);
-      tc::barrier_init(tc::smem_address(&sh.plan_free[i]), kValueWarps + kSoftmaxWarps / 2 + 1);
+      tc::barrier_init(tc::smem_address(&sh.plan_free[i]), kWidenWarps + kSoftmaxWarps / 2 + 1);
     }
     for (int i = 0; i < kParts; ++i) {
       tc::barrier_init(tc::smem_address(&sh.part_full[i]), 1);
@@ -766,14 +780,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   const int tiles_here = static_cast<int>(full_tiles<kRows, kTileSteps, kOpen>(a, c));  // 2^31 tiles would take half an hour
   if (warp < kSoftmaxWarps) {
     tc::registers_up<kSoftmaxRegisters>();
-    if (!tc::all_of<1, 32 * kSoftmaxWarps>(softmax_role<DP>(a, tiles_here, sh, codes + kCodeStages * T::kCodeBytes, tmem, g)))
+    if (!tc::all_of<1, 32 * kSoftmaxWarps>(softmax_role<DP>(a, tiles_here, sh, codes + kCodeStages * 2 * T::kCodeBytes, tmem, g)))
       spoil<DP>(a, sh.begin, g);
-  } else if (warp < kSoftmaxWarps + kValueWarps) {
-    tc::registers_down<kValueRegisters>();
-    value_role<DP>(tiles_here, sh, v_tiles, codes);
+  } else if (warp < kSoftmaxWarps + kWidenWarps) {
+    tc::registers_down<kWidenRegisters>();
+    widen_role<DP>(tiles_here, sh, k_tiles, v_tiles, codes);
   } else {
     tc::registers_down<kOtherRegisters>();
-    if (warp == kSoftmaxWarps + kValueWarps) {
+    if (warp == kSoftmaxWarps + kWidenWarps) {
       if (tc::elected()) {
         product_role<DP>(tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(v_tiles), tmem);
         // products in flight end before the memory that they use is given up
@@ -782,10 +796,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
         tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused, tc::kEndCycles);
       }
       __syncwarp();
-    } else if (warp == kSoftmaxWarps + kValueWarps + 1) {
+    } else if (warp == kSoftmaxWarps + kWidenWarps + 1) {
       plan_role(a, c, sh);
-    } else if (warp == kSoftmaxWarps + kValueWarps + 2) {
-      fetch_role<DP>(&keys, &values, tiles_here, sh, tc::smem_address(k_tiles), tc::smem_address(codes));
+    } else if (warp == kSoftmaxWarps + kWidenWarps + 2) {
+      fetch_role<DP>(&keys, &values, tiles_here, sh, tc::smem_address(codes));
       // and copies in flight: the last of each stage, which no other role may have waited for
       int unused = 0;
       for (int it = max(0, sh.fetched - kCodeStages); it < sh.fetched; ++it)
@@ -816,7 +830,7 @@ EncodeTiled encoder() {
 }
 
 // Boxes of `width` dims (zeros behind the last) of 16 tokens of one head and page.
-bool cache_map(CUtensorMap* map, const sv_kv_desc& d, const uint8_t* cache, int width, CUtensorMapSwizzle swizzle) {
+bool cache_map(CUtensorMap* map, const sv_kv_desc& d, const uint8_t* cache, int width) {
   const EncodeTiled encode = encoder();
   if (!encode) return false;
   const cuuint64_t size[4] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.page_size),
@@ -825,7 +839,7 @@ bool cache_map(CUtensorMap* map, const sv_kv_desc& d, const uint8_t* cache, int 
                                 static_cast<cuuint64_t>(d.page_stride)};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(width), kStep, 1, 1}, step[4] = {1, 1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(cache), size, stride, box, step,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -841,8 +855,7 @@ sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspa
   a.parts = reinterpret_cast<float*>(align_up(reinterpret_cast<uintptr_t>(workspace), kPartAlign));
   a.joins = reinterpret_cast<JoinRecord*>(a.parts + 2 * static_cast<int64_t>(kSMs) * T::kPart);
   CUtensorMap keys, values;
-  if (!cache_map(&keys, d.kv, a.w.c.k, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !cache_map(&values, d.kv, a.w.c.v, DP, CU_TENSOR_MAP_SWIZZLE_NONE))
+  if (!cache_map(&keys, d.kv, a.w.c.k, DP) || !cache_map(&values, d.kv, a.w.c.v, DP))
     return SV_ERR_UNSUPPORTED;
   if (launch_early(kernel, dim3(blocks), dim3(kThreads), T::kShared, stream, a, keys, values) != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);

@@ -205,23 +205,16 @@ __device__ __forceinline__ uint64_t tile_descriptor(uint32_t at, uint32_t block,
          static_cast<uint64_t>(group >> 4) << 32 | uint64_t{1} << 46 | uint64_t{2} << 61;
 }
 
-// fp16 x fp16 -> fp32 and e4m3 x e4m3 -> fp32, 128 x n; b_rows_inner: B's rows in memory are the inner dimension.
+// fp16 x fp16 -> fp32, 128 x n; b_rows_inner: B's rows in memory are the inner dimension.
 __host__ __device__ constexpr uint32_t product_kind(int n, bool b_rows_inner) {
   return 1u << 4 | (b_rows_inner ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (128u / 16) << 24;
 }
 
-// d += (or =, unless `add`) a b, with A (128 x 16 fp16, 128 x 32 e4m3) in tensor memory; one thread.
+// d += (or =, unless `add`) a b, with A (128 x 16) in tensor memory; one thread.
 __device__ __forceinline__ void product_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
-      : "memory");
-}
-__device__ __forceinline__ void product_e4m3(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p; }" ::"r"(d),
       "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
       : "memory");
 }

@@ -546,11 +546,14 @@ size_t sv_kv_attention_workspace_size(const sv_kv_attention_desc* desc);
  *   row_status  optional [B] int32 (SV_ROW_*).
  *
  * The cache's codes reach the tensor cores without loss and sums are held in
- * fp32.  Weights are fp16 (for float32 calls the sum of two): each is rounded
- * to 2^-11 (2^-21) of itself, or to 2^-31 of its row's largest where that is
- * more (both counted with the scales of V).  NaN codes (0x7f, 0xff;
- * sv_kv_append writes none) at visible tokens are not supported; what lies
- * behind a sequence's last token is not seen, whatever its bytes.
+ * fp32.  Queries are fp16 times a power of two for each row (for float32 calls
+ * the sum of two): bf16 ones keep all their bits down to 2^-31 of their row's
+ * largest value, float32 ones are rounded to 2^-22 of themselves, or to 2^-39
+ * of that where it is more.  Weights are fp16 (for float32 calls the sum of
+ * two): each is rounded to 2^-11 (2^-21) of itself, or to 2^-31 of its row's
+ * largest where that is more (both counted with the scales of V).  NaN codes
+ * (0x7f, 0xff; sv_kv_append writes none) at visible tokens are not supported;
+ * what lies behind a sequence's last token is not seen, whatever its bytes.
  */
 sv_status sv_kv_attention(const sv_kv_attention_desc* desc, const void* q, const uint8_t* k_cache,
                           const uint8_t* v_cache, const float* k_scale, const float* v_scale,

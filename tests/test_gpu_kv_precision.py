@@ -102,3 +102,19 @@ def test_pages_of_zeros_among_large_values(sv, dtype, heads, dim):
     cache["v_scale"][zeros] = 2.0 ** -100
     cache["v_scale"][table[0, 1::3]] = 2.0 ** 20
     _compare(sv, cache, table, page, ctx, round_to(g.normal(0, 1.5, (1, heads, dim)), dtype), dtype, dim ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,heads", ROWS)
+@pytest.mark.parametrize("dim", [64, 80, 128])
+@pytest.mark.parametrize("key", [0.0, 1.0])
+@pytest.mark.parametrize("factor", [100.0, 300.0, 3000.0, 3e6])
+def test_one_dim_of_the_queries_is_far_larger(sv, dtype, heads, dim, key, factor):
+    """The rest keeps its bits, whether the keys have anything in that dim or not."""
+    g = np.random.default_rng(dim + heads)
+    page, ctx, at = 32, 500, 17
+    table, pages = make_table(g, [ctx + 1], page)
+    cache = make_cache(g, pages, 1, page, dim)
+    cache["k"][..., at] = KO.encode(KO.VALUE[cache["k"][..., at]] * key)
+    q = g.normal(0, 1, (1, heads, dim))
+    q[..., at] = factor * np.sign(q[..., at])
+    _compare(sv, cache, table, page, ctx, round_to(q, dtype), dtype, dim ** -0.5)
