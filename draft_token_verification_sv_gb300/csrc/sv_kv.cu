@@ -35,6 +35,7 @@ __device__ __forceinline__ void regrow(const KvView& w, uint8_t* cache, int page
   const int words = w.dim / 4;
   for (int i = threadIdx.x; i < held * words; i += THREADS) {
     const int t = i / words;
+    if (!kv_slot_in(w, t)) return;
     uint32_t* p = reinterpret_cast<uint32_t*>(cache + kv_offset(w, page, head, t)) + (i - t * words);
     *p = rescale4(*p, ratio);
   }
@@ -140,11 +141,12 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(KvView w, AppendRows
   const E* x = static_cast<const E*>(rows.x[which]) + head * rows.head_stride[which] +
                static_cast<int64_t>(s.row0 + (lo - s.ctx) + t0) * rs + ch * kN;
   const int64_t step = per * rs;
+  const int row = s.row0 + (lo - s.ctx) + t0;
   uint4 held_v[kHeld];
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < kHeld; ++j)
-    held_v[j] = t0 + j * per < mine ? load_row16<E, VEC>(x + j * step) : make_uint4(0, 0, 0, 0);
+    held_v[j] = t0 + j * per < mine && kv_row_in(w, row + j * per) ? load_row16<E, VEC>(x + j * step) : make_uint4(0, 0, 0, 0);
   const int page = kv_page(w, b, col);
   if (page < 0) return;  // the same for the whole block
   uint8_t* cache = which ? w.c.v : w.c.k;
@@ -153,12 +155,12 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(KvView w, AppendRows
   const float old = held > 0 ? *scale : 0.0f;
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) m = Packed<E>::magnitude(held_v[j], m);
-  for (int t = t0 + kHeld * per, j = kHeld; t < mine; t += per, ++j) m = Packed<E>::magnitude(load_row16<E, VEC>(x + j * step), m);
+  for (int t = t0 + kHeld * per, j = kHeld; t < mine && kv_row_in(w, row + j * per); t += per, ++j) m = Packed<E>::magnitude(load_row16<E, VEC>(x + j * step), m);
   uint32_t top = block_max_u32<THREADS>(Packed<E>::bits(m), scratch);
   const bool finite = top < 0x7f800000u;
   if (!finite) {
     top = 0;
-    for (int t = t0, j = 0; t < mine; t += per, ++j) {
+    for (int t = t0, j = 0; t < mine && kv_row_in(w, row + j * per); t += per, ++j) {
       const uint4 v = load_row16<E, VEC>(x + j * step);
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
@@ -179,9 +181,9 @@ __global__ void __launch_bounds__(THREADS) kv_append_kernel(KvView w, AppendRows
   if (finite) {
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
-      if (t0 + j * per < mine) quantise_store<E, true>(held_v[j], inv, to + j * to_step);
+      if (t0 + j * per < mine && kv_slot_in(w, held + t0 + j * per)) quantise_store<E, true>(held_v[j], inv, to + j * to_step);
   }
-  for (int j = finite ? kHeld : 0, t = t0 + j * per; t < mine; t += per, ++j)
+  for (int j = finite ? kHeld : 0, t = t0 + j * per; t < mine && kv_row_in(w, row + j * per) && kv_slot_in(w, held + t); t += per, ++j)
     quantise_store<E, false>(load_row16<E, VEC>(x + j * step), inv, to + j * to_step);
 }
 
@@ -251,6 +253,7 @@ __global__ void __launch_bounds__(THREADS) kv_read_kernel(KvView w, ReadRows row
       vs = __ldg(w.c.v_scale + static_cast<int64_t>(page) * w.kv_heads + head);
     }
     const int64_t row = s.row0 + t;
+    if (!kv_row_in(w, row)) break;
     store_codes16<E, VEC>(k, ks, static_cast<E*>(rows.x[0]) + row * rows.row_stride[0] + head * rows.head_stride[0] + chunk * 16);
     store_codes16<E, VEC>(v, vs, static_cast<E*>(rows.x[1]) + row * rows.row_stride[1] + head * rows.head_stride[1] + chunk * 16);
   }
@@ -299,6 +302,7 @@ __global__ void __launch_bounds__(THREADS) kv_commit_kernel(KvView w, int nodes,
   __syncthreads();
   for (int n = threadIdx.x; n < (a + 1) * cpr; n += THREADS) {  // a thread per 16 codes
     const int i = n / cpr, ch = n - i * cpr;
+    if (!sv_in(i, path_len)) break;
     const int pos = ctx + __ldg(p + i);
     const int page = kv_page(w, b, pos >> w.page_shift);
     uint4 c = make_uint4(0, 0, 0, 0);
@@ -338,6 +342,7 @@ __global__ void __launch_bounds__(THREADS) kv_commit_kernel(KvView w, int nodes,
     for (int i = threadIdx.x; i < (hi - lo) * wpr; i += THREADS) {
       const int t = i / wpr, k = i - t * wpr;
       const int src = lo - ctx + t;
+      if (!sv_in(src, path_len) || !kv_slot_in(w, held + t)) break;
       // (beyond float only where all of the path's codes here are zeros, which stay)
       reinterpret_cast<uint32_t*>(to + t * w.token_stride)[k] = rescale4(words[src * wpr + k], fminf(s_scale[src] * inv, 0x1p127f));
     }

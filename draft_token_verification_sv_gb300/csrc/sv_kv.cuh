@@ -57,6 +57,10 @@ __device__ __forceinline__ void kv_flag(const KvView& w, int b, int bit) {
 // Flags bad lengths, for calls without a new token.
 sv_status kv_check_lengths(const KvView& w, cudaStream_t stream);
 
+// For the debug build's checks: is this a row of new tokens, a slot of a page (the first of `span`)?
+__device__ __forceinline__ bool kv_row_in(const KvView& w, long long row) { return sv_in(row, w.total_new); }
+__device__ __forceinline__ bool kv_slot_in(const KvView& w, int slot, int span = 1) { return sv_in(slot, (1 << w.page_shift) - span + 1); }
+
 // Page id of column `col` of sequence b, or -1 (flagged) outside the pool.
 __device__ __forceinline__ int kv_page(const KvView& w, int b, int col) {
   if (!sv_in(col, w.max_pages)) return -1;

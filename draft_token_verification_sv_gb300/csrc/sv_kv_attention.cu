@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
         }
         bad = (bad & ~(1u << fill)) | (there ? 0u : 1u << fill);
         int64_t o = page * w.page_stride + (t0 & page_mask) * w.token_stride + head_at;
-        const int count = !there || c0 * 16 >= w.dim ? 0 : steps.end - t0;
+        const int count = !there || c0 * 16 >= w.dim || !kv_slot_in(w, t0 & page_mask, kStep) ? 0 : steps.end - t0;
         const uint32_t to = ring_at + fill * S::kStageBytes;
 #pragma unroll
         for (int i = 0; i < NC; ++i, o += lane_step) {
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
       const int at = r0 + min(r, rows - 1), token = at / a.group, head = c.h * a.group + at - token * a.group;
       const E* p = static_cast<const E*>(a.q) + (static_cast<int64_t>(s.row0) + token) * a.q_row_stride + head * a.q_head_stride + chunk * 16;
       float x[16];
-      load_query16<E>(p, live && chunk * 16 < w.dim, a.q_vec, x);
+      load_query16<E>(p, live && chunk * 16 < w.dim && kv_row_in(w, static_cast<int64_t>(s.row0) + token) && sv_in(head, a.heads), a.q_vec, x);
       float top = 0.0f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
@@ -571,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, Shape<E, DP, MT>::kBlocksPerSm) kv_a
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) total += s_m[k][r] == -CUDART_INF_F ? s_l[k][r] : s_l[k][r] * ex2(s_m[k][r] - top);
       if (!complete) {
+        if (!sv_in(g, S::kBlocks)) break;  // the workspace's parts
         *reinterpret_cast<float4*>(part + r * DP + 4 * d4) = sum;
         if (d4 == 0) *reinterpret_cast<float2*>(part + kRows * DP + 2 * r) = make_float2(top, total);
       } else {

@@ -225,7 +225,7 @@ __device__ bool plan_role(const AttentionParams& a, Cursor c, Shared& sh) {
 
 // Two copies for each step that has tokens, a lane to a copy.
 template <int DP>
-__device__ bool fetch_role(const CUtensorMap* keys, const CUtensorMap* values, const int tiles, Shared& sh, uint32_t codes) {
+__device__ bool fetch_role(const AttentionParams& a, const CUtensorMap* keys, const CUtensorMap* values, const int tiles, Shared& sh, uint32_t codes) {
   using T = Tiles<DP>;
   constexpr int kCodeStages = T::kCodeStages;
   const int lane = threadIdx.x & 31, step = lane % kTileSteps;
@@ -236,8 +236,9 @@ __device__ bool fetch_role(const CUtensorMap* keys, const CUtensorMap* values, c
     const TilePlan& plan = sh.plan[it % kPlans];
     const int stage = it % kCodeStages;
     if (!warp_wait(sh, sh.plan_full[it % kPlans], it / kPlans)) return false;
-    const bool live = lane < 2 * kTileSteps && plan.count[step] > 0;
     const int slot = plan.slot[step], page = plan.page[step], head = plan.head;
+    const bool live = lane < 2 * kTileSteps && plan.count[step] > 0 && kv_slot_in(a.w, slot, kStep) && sv_in(page, a.w.num_pages) &&
+                      sv_in(head, a.w.kv_heads);
     const int copies = __popc(__ballot_sync(0xffffffffu, live));
     warp_arrive(sh.plan_free[it % kPlans]);
     if (it >= kCodeStages && !warp_wait(sh, sh.codes_free[stage], it / kCodeStages - 1)) return false;
@@ -450,6 +451,8 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
     const Part& p = sh.part[item % kParts];
     const int32_t* parents = a.parents ? a.parents + p.row0 : nullptr;
     const int ctx = p.ctx, token = (p.r0 + min(r, p.rows - 1)) / a.group;
+    // the row is the call's, and so is its place in q, out and lse
+    const bool held = r < p.rows && kv_row_in(a.w, static_cast<int64_t>(p.row0) + token) && sv_in(g, kSMs);
 
     // the row's queries, scaled by a power of two
     float factor;
@@ -460,12 +463,13 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
       uint4 raw[kDims / 8];
       uint32_t top = 0;
       if (a.q_vec) {  // 8 rows' pieces of 64 bytes at a time: a lane that loads its own row alone touches a line for each 16 bytes
+        const unsigned rows_held = __ballot_sync(0xffffffffu, held);
         uint64_t from[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) from[i] = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(q), 8 * i + (lane >> 2)) + 16 * (lane & 3);
 #pragma unroll
         for (int i = 0; i < kDims / 8; ++i) {
-          const bool live = 32 * quarter + 8 * (i & 3) + (lane >> 2) < p.rows && group * kDims + 32 * (i >> 2) + 8 * (lane & 3) < a.w.dim;
+          const bool live = rows_held >> (8 * (i & 3) + (lane >> 2)) & 1u && group * kDims + 32 * (i >> 2) + 8 * (lane & 3) < a.w.dim;
           raw[i] = live ? *reinterpret_cast<const uint4*>(from[i & 3] + 64 * (i >> 2)) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
@@ -481,7 +485,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
 #pragma unroll
         for (int i = 0; i < kDims / 8; ++i) {
           raw[i] = make_uint4(0, 0, 0, 0);
-          if (r < p.rows && group * kDims + i * 8 < a.w.dim) {
+          if (held && group * kDims + i * 8 < a.w.dim) {
             const uint16_t* e = q + i * 8;
             raw[i] = make_uint4(__ldg(e) | __ldg(e + 1) << 16, __ldg(e + 2) | __ldg(e + 3) << 16,
                                 __ldg(e + 4) | __ldg(e + 5) << 16, __ldg(e + 6) | __ldg(e + 7) << 16);
@@ -656,7 +660,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
 #pragma unroll
       for (int k = 0; k < 16; ++k)
         x[k] = __float_as_uint(fmaf(__uint_as_float(x[k] & own), scale, __uint_as_float(y[k] & other) * their_scale));
-      if (r < p.rows && !complete) {
+      if (held && !complete) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t o[8];
@@ -664,7 +668,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
           for (int n = 0; n < 8; ++n) o[n] = x[8 * k + n];
           tc::store_32(part + r * DP + d + 8 * k, o);
         }
-      } else if (r < p.rows && d < a.w.dim) {
+      } else if (held && d < a.w.dim) {
         uint32_t o[8];
 #pragma unroll
         for (int n = 0; n < 8; ++n) o[n] = floats_to_bf16x2(__uint_as_float(x[2 * n]), __uint_as_float(x[2 * n + 1]));
@@ -680,7 +684,7 @@ __device__ bool softmax_role(const AttentionParams& a, const int tiles, Shared& 
       }
       __syncwarp();
     }
-    if (group == 0 && r < p.rows) {
+    if (group == 0 && held) {
       if (!complete)
         *reinterpret_cast<float2*>(part + kRows * DP + 2 * r) = make_float2(top, total);
       else if (a.lse)
@@ -799,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
     } else if (warp == kSoftmaxWarps + kWidenWarps + 1) {
       plan_role(a, c, sh);
     } else if (warp == kSoftmaxWarps + kWidenWarps + 2) {
-      fetch_role<DP>(&keys, &values, tiles_here, sh, tc::smem_address(codes));
+      fetch_role<DP>(a, &keys, &values, tiles_here, sh, tc::smem_address(codes));
       // and copies in flight: the last of each stage, which no other role may have waited for
       int unused = 0;
       for (int it = max(0, sh.fetched - kCodeStages); it < sh.fetched; ++it)

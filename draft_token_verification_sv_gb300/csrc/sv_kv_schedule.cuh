@@ -235,7 +235,7 @@ __device__ __forceinline__ void flag_sequences(const AttentionParams& a, int g, 
     if (!a.parents || !s.ok) continue;
     const int32_t* p = a.parents + s.row0;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < s.n; i += threads) {
+    for (int i = threadIdx.x; i < s.n && kv_row_in(a.w, s.row0 + i); i += threads) {
       const int t = __ldg(p + i);
       if (i == 0 ? t != -1 : (t < 0 || t >= i)) kv_flag(a.w, b, SV_ROW_BAD_PARENT);
     }
@@ -299,6 +299,7 @@ __device__ __forceinline__ void store_result(const AttentionParams& a, int row0,
   if (d >= a.w.dim) return;
   const int64_t row = static_cast<int64_t>(row0) + r / a.group;
   const int head = kv_head * a.group + r % a.group;
+  if (!kv_row_in(a.w, row) || !sv_in(head, a.heads)) return;
   E* out = static_cast<E*>(a.out) + row * a.out_row_stride + head * a.out_head_stride + d;
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   store4<E>(out, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv), a.out_vec);
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(AttentionParams 
   wait_for_stream();  // the parts are written
   const int g = blockIdx.x;
   const JoinRecord j = a.joins[g];
+  if (j.rows > 0 && (!sv_in(j.last, gridDim.x) || !sv_in(j.rows - 1, ROWS))) return;
   constexpr int kPart = ROWS * (DP + 2);
 #pragma unroll 1
   for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < j.rows * (DP / 4); i += blockDim.x * gridDim.y) {
