@@ -15,7 +15,11 @@
  *     a malformed tree, a row with no finite logit) never trap: they are
  *     reported per batch row in `row_status` (bits SV_ROW_*); such rows emit
  *     num_accepted = 0 / accept_len = 0 and token -1.
- *   - No kernel spins on a flag or waits on another launch.
+ *   - No kernel waits on one that may run beside it, and no wait is endless.
+ *     The attention over the cache begins while the launch before it in the
+ *     stream ends, waits for that end and then works; inside its many-row
+ *     kernel the warps of a block wait for one another, two seconds at most
+ *     (then the call ends with SV_ROW_TIMEOUT).
  *
  * Layouts: logits are row-major; a "row" is one position's logits over the
  * vocabulary.  Row strides are in ELEMENTS and at least the row length; any
