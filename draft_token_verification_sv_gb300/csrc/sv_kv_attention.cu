@@ -126,7 +126,9 @@ __device__ __forceinline__ float scale_log2(float x) {
 // for fp32 16 DP, floats of a warp) sets how many blocks an SM holds.
 template <typename E, int DP, int MT> struct Shape {
   static constexpr bool kSplit = sizeof(E) == 4;  // queries and weights as two fp16 each
-  static constexpr bool kQueriesStay = MT == 1 || DP == 64;  // in registers; else read from shared memory for every step
+  // Queries in registers, or read from shared memory for every step, where sums and queries together do not fit them: a step of 64
+  // sequences at 256 dims takes 222 us reading and 231 holding them (fp32 283 and 467), chains of 8 at 64 dims 106.5 and 115.
+  static constexpr bool kQueriesStay = DP == 64 ? MT == 1 || kSplit : DP == 128 && MT == 1;
   // A step's V scale and its rows' lift: in the exponent of the weights, or multiplied to them.  Chains of 8 (two tiles) take 157 and
   // 159.6 us, a step of 64 sequences (one tile, where what stands between two products counts for more) 115 and 112.7.
   static constexpr bool kFold = MT == 2;
