@@ -18,9 +18,9 @@
 // asynchronous copies, so that no barrier stands between a block's four warps;
 // they are joined where an item ends.  A 16-row tile that reads the whole cache
 // is bound by HBM (a step of 64 sequences of up to 8192 tokens, 8 kv heads of
-// 128 dims: 112 us, 5.5 TB/s, 81% of a copy's rate); two tiles by the
+// 128 dims: 113 us, 5.5 TB/s, 80% of a copy's rate); two tiles by the
 // instructions that widen codes and weigh scores (chains of 8 on up to 32768
-// tokens: 157 us, 3.7 TB/s); short calls by latency (500 tokens of one
+// tokens: 155 us, 3.8 TB/s); short calls by latency (500 tokens of one
 // sequence: 9.7 us with the join, of which about 8 pass before the first
 // product when nothing is in the caches).
 #include "sv_kv_schedule.cuh"
@@ -102,7 +102,7 @@ __device__ __forceinline__ void load_query16(const E* p, bool live, bool vec, fl
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 // Empty tiles ahead of an item.  A step of 64 sequences of up to 8192 tokens, 16 chains of 8 on up to 32768 and a window in fp32 take
-// 119, 164 and 34.5 us without, 112, 161 and 32.4 with 3, 113, 155 and 32.8 with 8, 117, 157 and 33.5 with 12.
+// 120, 163 and 34.4 us without, 114, 159 and 31.8 with 3, 113, 155 and 31.4 with 6, 114, 153 and 32.6 with 8, 118, 155 and 33.4 with 12.
 constexpr int kOpen = 6;
 
 constexpr float kMost = 8192.0f;  // sum of a thread's four weights of a row as they become fp16
@@ -618,9 +618,9 @@ size_t workspace_for() {
 
 // Calls f with the kernel's template arguments as types: one tile of 16 rows,
 // or two where a kv head has more rows and the sums fit the registers.  Chains
-// of 8 (32 rows) on contexts of up to 32768 tokens take 157 us with two tiles
-// and 193 with one, which reads the cache twice, at 64 dims 102 and 126; 2000
-// tokens of a prompt in fp32 1496 and 1891.
+// of 8 (32 rows) on contexts of up to 32768 tokens take 155 us with two tiles
+// and 194 with one, which reads the cache twice, at 64 dims 101 and 129; 2000
+// tokens of a prompt in fp32 1483 and 1953.
 template <typename F>
 auto with_shape(const sv_kv_attention_desc& d, F f) {
   const bool two = static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 16;

@@ -42,8 +42,8 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kTileSteps = 4;
 constexpr int kTokens = kStep * kTileSteps;
-// Empty tiles ahead of an item: none, 5, 8 and 12 take 153, 135, 124 and 124 us for 64 trees of 32 nodes on contexts of up to
-// 4096 tokens, 370, 364, 367 and 370 for 2000 tokens of two prompts behind 4096, 367, 220, 197 and 201 for 16 prompts of 836.
+// Empty tiles ahead of an item: none, 5, 8 and 12 take 148, 131, 127 and 127 us for 64 trees of 32 nodes on contexts of up to
+// 4096 tokens, 379, 374, 374 and 378 for 2000 tokens of two prompts behind 4096, 335, 208, 189 and 193 for 16 prompts of 836.
 constexpr int kOpen = 8;
 // weights: warps 0-7; widening: 8-11; products: 12; plan: 13; fetch: 14 (15 idle: registers move in fours of warps)
 constexpr int kSoftmaxWarps = 8, kWidenWarps = 4;
@@ -873,9 +873,9 @@ sv_status launch(AttentionParams a, const sv_kv_attention_desc& d, void* workspa
 
 // More rows of a kv head than the other kernel's two tiles of 16.  Rows are
 // padded to 128 here, which costs more than it gives up to 32 of them: chains of
-// 8 (32 rows) on contexts of up to 32768 tokens take 171 us here and 157 there at
-// 128 dims, 169 and 102 at 64.  From 33 on the other kernel reads the cache
-// twice: chains of 12 (48 rows) take 173 us here and 283 there.
+// 8 (32 rows) on contexts of up to 32768 tokens take 171 us here and 155 there at
+// 128 dims, 163 and 101 at 64.  From 33 on the other kernel reads the cache
+// twice: chains of 12 (48 rows) take 173 us here and 279 there.
 bool kv_attention_takes_tiles(const sv_kv_attention_desc& d) {
   return d.dtype == SV_BF16 && d.kv.head_dim <= 128 &&
          static_cast<int64_t>(d.max_new) * (d.heads / d.kv.kv_heads) > 32;
