@@ -35,12 +35,14 @@ SV_ROW_BAD_LENGTH = 128
 SV_ROW_NOT_FINITE = 256
 SV_ROW_BAD_PATH = 512
 SV_ROW_TIMEOUT = 1024
+SV_ROW_NO_PAGE = 2048
 
 SV_MAX_GAMMA = 64
 SV_MAX_VOCAB = 16777216
 SV_MAX_TREE_NODES = 1024
 SV_MAX_TREE_DEPTH = 64
 SV_MAX_HEAD_DIM = 256
+SV_MAX_ROPE_AXES = 4
 
 SV_DEBUG_INDEX = 1
 
@@ -98,6 +100,33 @@ class KvAttentionDesc(ctypes.Structure):
                 ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
 
 
+class KvAssignDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("max_new", ctypes.c_int32), ("total_new", ctypes.c_int32),
+                ("table_stride", ctypes.c_int64)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("adjacent", ctypes.c_int32), ("dtype", ctypes.c_int32), ("position_stride", ctypes.c_int64),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_row_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("q_out_row_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+                ("k_out_row_stride", ctypes.c_int64), ("k_out_head_stride", ctypes.c_int64),
+                ("axis", ctypes.c_uint8 * (SV_MAX_HEAD_DIM // 2))]
+
+
+class PromptAttentionDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("max_new", ctypes.c_int32), ("total_new", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_row_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -129,6 +158,10 @@ SIGNATURES = {
     "sv_kv_commit": (_I32, [_P, _I32, _I32] + [_P] * 10 + [_P]),
     "sv_kv_attention_workspace_size": (_SZ, [_P]),
     "sv_kv_attention": (_I32, [_P] * 13 + [_P, _SZ, _P]),
+    "sv_kv_assign": (_I32, [_P] * 11 + [_P]),
+    "sv_rope": (_I32, [_P] * 7 + [_P]),
+    "sv_prompt_attention_workspace_size": (_SZ, [_P]),
+    "sv_prompt_attention": (_I32, [_P] * 8 + [_P, _SZ, _P]),
     "sv_status_string": (ctypes.c_char_p, [_I32]),
     "sv_version": (_I32, []),
     "sv_set_phase_events": (None, [_P, _I32]),

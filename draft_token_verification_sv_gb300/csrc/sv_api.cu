@@ -143,6 +143,66 @@ bool kv_attention_desc_ok(const sv_kv_attention_desc* d, bool ragged) {
          kv_stride_ok(d->out_row_stride, d->kv.head_dim) && kv_stride_ok(d->out_head_stride, d->kv.head_dim);
 }
 
+bool kv_assign_desc_ok(const sv_kv_assign_desc* d, bool ragged) {
+  if (!d || d->batch < 0 || d->batch > 65535) return false;
+  if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128) return false;
+  if (d->num_pages < 1 || d->max_pages < 1 || static_cast<int64_t>(d->max_pages) * d->page_size > INT32_MAX) return false;
+  if (d->max_new < 0 || d->total_new < 0) return false;
+  if (!ragged && static_cast<int64_t>(d->batch) * d->max_new != d->total_new) return false;
+  return d->table_stride >= d->max_pages && d->table_stride <= kMaxStride;
+}
+
+// Bytes that a call reads or writes.
+struct Span {
+  const void* at;
+  int64_t bytes;
+  bool written;
+};
+
+// Do two of them share memory, one of which is written?
+template <size_t N>
+bool shared_writes(const Span (&s)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = 0; j < i; ++j) {
+      if (!s[i].at || !s[j].at || !(s[i].written || s[j].written)) continue;
+      const uintptr_t x = reinterpret_cast<uintptr_t>(s[i].at), y = reinterpret_cast<uintptr_t>(s[j].at);
+      if (x < y + s[j].bytes && y < x + s[i].bytes) return true;
+    }
+  return false;
+}
+
+bool rope_desc_ok(const sv_rope_desc* d) {
+  if (!d || d->rows < 0 || d->heads < 1 || d->heads > 131072 || d->kv_heads < 0 || d->kv_heads > 131072) return false;
+  if (d->head_dim < 16 || d->head_dim > SV_MAX_HEAD_DIM || d->head_dim % 16) return false;
+  if (d->rotary_dim < 2 || d->rotary_dim > d->head_dim || d->rotary_dim % 2) return false;
+  if (d->axes < 1 || d->axes > SV_MAX_ROPE_AXES || (d->adjacent != 0 && d->adjacent != 1) || !valid_dtype(d->dtype)) return false;
+  if (d->axes > 1 && (d->position_stride < d->rows || d->position_stride > kMaxStride)) return false;
+  for (int i = 0; i < d->rotary_dim / 2; ++i)
+    if (d->axis[i] >= d->axes) return false;
+  const int64_t q[4] = {d->q_row_stride, d->q_head_stride, d->q_out_row_stride, d->q_out_head_stride};
+  const int64_t k[4] = {d->k_row_stride, d->k_head_stride, d->k_out_row_stride, d->k_out_head_stride};
+  for (int64_t s : q)
+    if (!kv_stride_ok(s, d->head_dim)) return false;
+  for (int64_t s : k)
+    if (d->kv_heads > 0 && !kv_stride_ok(s, d->head_dim)) return false;
+  return true;
+}
+
+bool prompt_desc_ok(const sv_prompt_attention_desc* d, bool ragged) {
+  if (!d || d->batch < 0 || d->batch > 65535 || d->kv_heads < 1 || d->kv_heads > 1024) return false;
+  if (d->heads < 1 || d->heads % d->kv_heads || d->heads / d->kv_heads > 128) return false;
+  if (d->head_dim < 16 || d->head_dim > SV_MAX_HEAD_DIM || d->head_dim % 16) return false;
+  if (d->max_new < 0 || d->total_new < 0) return false;
+  if (!ragged && static_cast<int64_t>(d->batch) * d->max_new != d->total_new) return false;
+  if (static_cast<int64_t>(d->max_new) * (d->heads / d->kv_heads) > INT32_MAX - 256) return false;
+  if (!valid_dtype(d->dtype) || !std::isfinite(d->scale) || d->window < 0 || d->sinks < 0) return false;
+  const int64_t strides[8] = {d->q_row_stride, d->q_head_stride, d->k_row_stride, d->k_head_stride,
+                              d->v_row_stride, d->v_head_stride, d->out_row_stride, d->out_head_stride};
+  for (int64_t s : strides)
+    if (!kv_stride_ok(s, d->head_dim)) return false;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -416,6 +476,60 @@ sv_status sv_kv_attention(const sv_kv_attention_desc* desc, const void* q, const
                   const_cast<float*>(v_scale), page_table};
   return kv_attention(*desc, q, c, ctx_lens, new_start, parents, out, lse, row_status, workspace,
                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+sv_status sv_kv_assign(const sv_kv_assign_desc* desc, int32_t* free_pages, int32_t* free_count, int32_t* page_table,
+                       int32_t* held, const int32_t* ctx_lens, const int32_t* new_start, const int32_t* parents,
+                       int64_t* slots, int32_t* positions, int32_t* row_status, sv_stream_t stream) {
+  CallScope scope;
+  if (!kv_assign_desc_ok(desc, new_start != nullptr)) return SV_ERR_INVALID_ARGUMENT;
+  if (desc->batch == 0) return SV_OK;
+  if (!free_pages || !free_count || !page_table || !held || !ctx_lens ||
+      !kv_words_ok(free_pages, free_count, page_table, held, ctx_lens, new_start, parents, positions, row_status) ||
+      (reinterpret_cast<uintptr_t>(slots) & 7u))
+    return SV_ERR_INVALID_ARGUMENT;
+  const int64_t B = desc->batch, total = desc->total_new;
+  const Span spans[] = {{free_pages, int64_t{4} * desc->num_pages, true}, {free_count, 4, true},
+                        {page_table, 4 * ((B - 1) * desc->table_stride + desc->max_pages), true}, {held, 4 * B, true},
+                        {slots, 8 * total, true}, {positions, 4 * total, true}, {row_status, 4 * B, true},
+                        {ctx_lens, 4 * B, false}, {new_start, 4 * (B + 1), false}, {parents, 4 * total, false}};
+  if (shared_writes(spans)) return SV_ERR_INVALID_ARGUMENT;
+  return kv_assign(*desc, free_pages, free_count, page_table, held, ctx_lens, new_start, parents, slots, positions,
+                   row_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+sv_status sv_rope(const sv_rope_desc* desc, const void* q, const void* k, const int32_t* positions,
+                  const float* inv_freq, void* q_out, void* k_out, sv_stream_t stream) {
+  CallScope scope;
+  if (!rope_desc_ok(desc)) return SV_ERR_INVALID_ARGUMENT;
+  if (desc->rows == 0) return SV_OK;
+  if (!q || !q_out || !positions || !inv_freq || !kv_words_ok(positions, inv_freq) || !aligned_elem(q, desc->dtype) ||
+      !aligned_elem(q_out, desc->dtype))
+    return SV_ERR_INVALID_ARGUMENT;
+  if (desc->kv_heads > 0 && (!k || !k_out || !aligned_elem(k, desc->dtype) || !aligned_elem(k_out, desc->dtype)))
+    return SV_ERR_INVALID_ARGUMENT;
+  return rope(*desc, q, k, positions, inv_freq, q_out, k_out, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t sv_prompt_attention_workspace_size(const sv_prompt_attention_desc* desc) {
+  if (!prompt_desc_ok(desc, true)) return 0;
+  return prompt_attention_workspace_bytes(*desc);
+}
+
+sv_status sv_prompt_attention(const sv_prompt_attention_desc* desc, const void* q, const void* k, const void* v,
+                              const int32_t* new_start, void* out, float* lse, int32_t* row_status,
+                              void* workspace, size_t workspace_bytes, sv_stream_t stream) {
+  CallScope scope;
+  if (!prompt_desc_ok(desc, new_start != nullptr)) return SV_ERR_INVALID_ARGUMENT;
+  if (desc->batch == 0) return SV_OK;
+  if (!workspace || !aligned16(workspace) || !kv_words_ok(new_start, lse, row_status)) return SV_ERR_INVALID_ARGUMENT;
+  if (desc->total_new > 0) {
+    const void* rows[4] = {q, k, v, out};
+    for (const void* p : rows)
+      if (!p || !aligned_elem(p, desc->dtype)) return SV_ERR_INVALID_ARGUMENT;
+  }
+  if (workspace_bytes < sv_prompt_attention_workspace_size(desc)) return SV_ERR_WORKSPACE_TOO_SMALL;
+  return prompt_attention(*desc, q, k, v, new_start, out, lse, row_status, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -178,6 +178,18 @@ sv_status kv_attention(const sv_kv_attention_desc& d, const void* q, const KvCac
                        const int32_t* new_start, const int32_t* parents, void* out, float* lse, int32_t* row_status,
                        void* workspace, cudaStream_t stream);
 
+// Pages and places (sv_kv_assign.cu), rotary positions (sv_rope.cu), the
+// attention of prompts (sv_prompt_attention.cu).
+sv_status kv_assign(const sv_kv_assign_desc& d, int32_t* free_pages, int32_t* free_count, int32_t* page_table, int32_t* held,
+                    const int32_t* ctx_lens, const int32_t* new_start, const int32_t* parents, int64_t* slots,
+                    int32_t* positions, int32_t* row_status, cudaStream_t stream);
+sv_status rope(const sv_rope_desc& d, const void* q, const void* k, const int32_t* positions, const float* inv_freq,
+               void* q_out, void* k_out, cudaStream_t stream);
+size_t prompt_attention_workspace_bytes(const sv_prompt_attention_desc& d);
+sv_status prompt_attention(const sv_prompt_attention_desc& d, const void* q, const void* k, const void* v,
+                           const int32_t* new_start, void* out, float* lse, int32_t* row_status, void* workspace,
+                           cudaStream_t stream);
+
 #ifdef SV_DEBUG
 // This translation unit's debug word reader, registered at load time.
 static unsigned read_this_debug_word(bool reset) {

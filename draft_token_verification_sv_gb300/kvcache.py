@@ -44,6 +44,13 @@ def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, 
     return dict(k=codes(), v=codes(), k_scale=scales(), v_scale=scales())
 
 
+def kv_pool(num_pages: int, device="cuda") -> dict:
+    """The free pages of a cache, all of them: ``free``, a stack of page ids
+    (page 0 on top), and ``count``, how many are on it."""
+    return dict(free=torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                count=torch.full((1,), num_pages, dtype=torch.int32, device=device))
+
+
 class _Meta(tuple):
     """What the checks see of a tensor: (shape, strides, dtype, GPU or -1)."""
     __slots__ = ()
@@ -106,6 +113,16 @@ def _int32(meta, name, numel, what):
         raise ValueError(f"{name} must have {what}")
 
 
+def _table(table: _Meta):
+    """(sequences, columns, row stride) of a page table."""
+    if table.dtype != torch.int32 or len(table.shape) != 2 or table.strides[1] != 1 and table.shape[1] > 1:
+        raise ValueError("page_table must be an int32 [B, pages] tensor with contiguous rows")
+    B, columns = table.shape
+    if B > 1 and table.strides[0] < columns:
+        raise ValueError("page_table rows overlap in memory (an expanded tensor? .contiguous() gives every sequence a row)")
+    return B, columns, table.strides[0] if B > 1 else columns
+
+
 def _kv_desc(k, v, ks, vs, table, lens, name) -> N.KvDesc:
     k, v, ks, vs = _see(k, "cache['k']"), _see(v, "cache['v']"), _see(ks, "cache['k_scale']"), _see(vs, "cache['v_scale']")
     table = _see(table, "page_table")
@@ -117,17 +134,13 @@ def _kv_desc(k, v, ks, vs, table, lens, name) -> N.KvDesc:
     for m, n in ((ks, "cache['k_scale']"), (vs, "cache['v_scale']")):
         if m.dtype != torch.float32 or m.shape != k.shape[:2] or not _contiguous(m):
             raise ValueError(f"{n} must be a contiguous float32 [pages, kv_heads] tensor")
-    if table.dtype != torch.int32 or len(table.shape) != 2 or table.strides[1] != 1 and table.shape[1] > 1:
-        raise ValueError("page_table must be an int32 [B, pages] tensor with contiguous rows")
-    B, columns = table.shape
-    if B > 1 and table.strides[0] < columns:
-        raise ValueError("page_table rows overlap in memory (an expanded tensor? .contiguous() gives every sequence a row)")
+    B, columns, table_stride = _table(table)
     _int32(lens, name, B, "one entry for each row of page_table")
     pages, heads, page, dim = k.shape
     # a dimension of one entry is never stepped over: its stride may be anything
     step = [s if n > 1 else -(-max(s, dim) // 16) * 16 for n, s in zip(k.shape[:3], k.strides)]
     return N.KvDesc(B, heads, dim, page, pages, columns, step[0], step[1], step[2],
-                    table.strides[0] if B > 1 else columns)
+                    table_stride)
 
 
 def _rows(m: _Meta, name: str, B: int, ragged: bool):
@@ -230,6 +243,30 @@ def _attention_plan(q, kc, vc, ks, vs, table, lens, start, max_new, parents, sca
             _one_device(kc, vc, ks, vs, table, lens, q, start, parents, out, status))
 
 
+@functools.lru_cache(maxsize=_KEPT)
+def _assign_plan(free, count, table, held, lens, page, start, max_new, parents, slots, positions, status):
+    free, count, table = _see(free, "pool['free']"), _see(count, "pool['count']"), _see(table, "page_table")
+    if free.dtype != torch.int32 or len(free.shape) != 1 or not _contiguous(free):
+        raise ValueError("pool['free'] must be a contiguous int32 [num_pages] tensor")
+    _int32(count, "pool['count']", 1, "one entry")
+    B, columns, stride = _table(table)
+    _int32(held, "held", B, "one entry for each row of page_table")
+    _int32(lens, "ctx_lens", B, "one entry for each row of page_table")
+    _int32(status, "row_status", B, _PER_SEQUENCE)
+    if start is not None:
+        _int32(start, "new_start", B + 1, "one entry more than page_table has rows")
+    s, p = _see(slots, "slots"), _see(positions, "positions")
+    total = _numel(s.shape)
+    if s.dtype != torch.int64 or not _contiguous(s) or p.dtype != torch.int32 or not _contiguous(p) or p.shape != s.shape:
+        raise ValueError("slots must be a contiguous int64 tensor and positions a contiguous int32 tensor of its shape")
+    if start is None and total != B * max_new:
+        raise ValueError("slots and positions must have one entry for each new token")
+    _int32(parents, "parents", total, "one entry for each new token")
+    d = N.KvAssignDesc(B, _count(page, "page_size"), _count(free.shape[0], "the number of pages"), columns,
+                       _count(max_new, "the largest number of new tokens"), _count(total, "the number of new tokens"), stride)
+    return ctypes.byref(d), _one_device(free, count, table, held, lens, start, parents, slots, positions, status)
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -262,6 +299,39 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(device))
     return t
+
+
+def kv_assign(pool: dict, page_table: torch.Tensor, held: torch.Tensor, ctx_lens: torch.Tensor, page_size: int, *,
+              new_start: torch.Tensor | None = None, max_new: int = 0, total: int | None = None,
+              parents: torch.Tensor | None = None, out: tuple | None = None, row_status: torch.Tensor | None = None,
+              stream=None) -> dict:
+    """Make every sequence hold the pages that its cached and ``max_new`` new
+    tokens need, from and to ``pool`` (see kv_pool), and say where the new ones
+    go; see sv_kv_assign.  ``held`` [B] int32 counts the entries of each
+    page_table row that the sequence holds.  With ``new_start`` [B + 1] each
+    sequence has its own number of new tokens, ``max_new`` at most and
+    ``total`` in all; ``parents`` makes them trees.  Without new tokens, pages
+    beyond ctx_lens go back.
+
+    Updates pool, page_table and held, and returns dict(slots=int64,
+    positions=int32), each [B, max_new] or [total] (or ``out``, the two)."""
+    max_new = int(max_new)
+    if out is None:
+        if new_start is None:
+            shape = (page_table.shape[0], max_new)
+        elif total is None:
+            raise ValueError("new_start needs total, the number of rows")
+        else:
+            shape = (int(total),)
+        out = tuple(_empty(shape, t, page_table.device, stream) for t in (torch.int64, torch.int32))
+    slots, positions = out
+    free, count = pool["free"], pool["count"]
+    d, gpu = _assign_plan(_meta(free), _meta(count), _meta(page_table), _meta(held), _meta(ctx_lens), int(page_size),
+                          _meta(new_start), max_new, _meta(parents), _meta(slots), _meta(positions), _meta(row_status))
+    _call(gpu, "sv_kv_assign", d, free.data_ptr(), count.data_ptr(), page_table.data_ptr(), held.data_ptr(), ctx_lens.data_ptr(),
+          _at(new_start), _at(parents), slots.data_ptr() or None, positions.data_ptr() or None, _at(row_status),
+          _stream_of(stream, gpu))
+    return dict(slots=slots, positions=positions)
 
 
 def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, ctx_lens: torch.Tensor, *,

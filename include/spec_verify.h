@@ -75,6 +75,7 @@ typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_ROW_NOT_FINITE 256        /* cache: a NaN (stored as 0) or infinity (stored as +-448 * scale) was appended */
 #define SV_ROW_BAD_PATH 512          /* cache: a path that does not start at 0 and rise within [0, nodes) */
 #define SV_ROW_TIMEOUT 1024          /* an internal wait ran out: results of the row are not valid (NaN where they are floats) */
+#define SV_ROW_NO_PAGE 2048          /* cache: too few free pages for the sequence, which got none */
 
 /* Limits checked on the host. */
 #define SV_MAX_GAMMA 64
@@ -83,6 +84,7 @@ typedef enum sv_dtype { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
 #define SV_MAX_TREE_NODES 1024
 #define SV_MAX_TREE_DEPTH 64
 #define SV_MAX_HEAD_DIM 256
+#define SV_MAX_ROPE_AXES 4
 
 typedef struct sv_chain_desc {
   int32_t batch;              /* B >= 0 (0: nothing to do) */
@@ -564,6 +566,148 @@ sv_status sv_kv_attention(const sv_kv_attention_desc* desc, const void* q, const
                           const int32_t* page_table, const int32_t* ctx_lens, const int32_t* new_start,
                           const int32_t* parents, void* out, float* lse, int32_t* row_status,
                           void* workspace, size_t workspace_bytes, sv_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------
+ * A request's way into the cache: pages for its length and a place for
+ * every new token (sv_kv_assign), rotary positions (sv_rope), and the
+ * attention of its prompt in the inputs' own precision
+ * (sv_prompt_attention; sv_kv_append then puts the keys and values away
+ * for the tokens that follow).
+ */
+typedef struct sv_kv_assign_desc {
+  int32_t batch;         /* B in [0, 65535] */
+  int32_t page_size;     /* 16, 32, 64 or 128 tokens */
+  int32_t num_pages;     /* pages in the pool = entries of free_pages, >= 1 */
+  int32_t max_pages;     /* entries of a page_table row, >= 1; max_pages * page_size < 2^31 */
+  int32_t max_new;       /* as for sv_kv_append */
+  int32_t total_new;
+  int64_t table_stride;  /* entries between page_table rows, >= max_pages, < 2^40 */
+} sv_kv_assign_desc;
+
+/*
+ * Make every sequence hold the pages that its tokens need, and say where the
+ * new ones go.  Sequence b holds the pages page_table[b, 0 .. held[b] - 1];
+ * free_pages is a stack of the pages that none holds, free_count[0] of them,
+ * the last one on top.  With n_b new tokens (new_start, max_new and
+ * total_new as for sv_kv_append) it shall hold
+ *   want_b = ceil((ctx_lens[b] + n_b) / page_size)  pages.
+ * First what sequences hold beyond that goes onto the stack, from the last
+ * page of the last sequence to the first page of the first.  Then sequences
+ * take what they lack from its top, in their order, page by page.  So a call
+ * that gives back what the call before took leaves the pool as it was.  A
+ * sequence that lacks pages when those before it and its own need are more
+ * than there are gets none and is flagged SV_ROW_NO_PAGE, and so is every
+ * later one that lacks any; all others are served.  held becomes want_b for
+ * those.  Entries of a page_table row beyond held, and of the stack beyond
+ * its count, keep what they had.
+ *
+ * With ctx_lens the lengths that stay and no new tokens, this is how pages
+ * go back after a verify (a length of 0: all of them).  One table serves the
+ * caches of all layers; pages that sequences share are not counted here.
+ *
+ * Of the token in row r, new token i of sequence b:
+ *   slots[r]      page * page_size + j % page_size with j = ctx_lens[b] + i
+ *                 and its page; -1 if b was not served or the page's id lies
+ *                 outside [0, num_pages) (flagged SV_ROW_BAD_PAGE).
+ *   positions[r]  ctx_lens[b] + i in a chain (parents == NULL), ctx_lens[b] +
+ *                 depth of node i in a tree (parents as for sv_kv_attention).
+ * Sequences whose lengths sv_kv_append would leave out, or with held[b]
+ * outside [0, max_pages], keep their pages and are flagged SV_ROW_BAD_LENGTH;
+ * where their rows are known these get slot -1 and position 0.  Rows that
+ * belong to no sequence are not touched, those of several are any one's.  free_count[0] outside [0,
+ * num_pages] is taken as the nearer of the two; what would go beyond the end
+ * of the stack is lost.
+ *
+ *   free_pages [num_pages] int32, free_count [1] int32, page_table
+ *   [B, max_pages] int32, held [B] int32: updated in place.
+ *   ctx_lens [B], new_start [B + 1] or NULL, parents [total_new] or NULL.
+ *   slots      optional [total_new] int64;  positions optional [total_new] int32.
+ *   row_status optional [B] int32 (SV_ROW_*).
+ * No two of these may share memory (refused where one of them is written).
+ */
+sv_status sv_kv_assign(const sv_kv_assign_desc* desc, int32_t* free_pages, int32_t* free_count, int32_t* page_table,
+                       int32_t* held, const int32_t* ctx_lens, const int32_t* new_start, const int32_t* parents,
+                       int64_t* slots, int32_t* positions, int32_t* row_status, sv_stream_t stream);
+
+typedef struct sv_rope_desc {
+  int32_t rows;          /* tokens, >= 0 */
+  int32_t heads;         /* heads of q, >= 1 */
+  int32_t kv_heads;      /* heads of k, >= 0 (0: no k) */
+  int32_t head_dim;      /* D: a multiple of 16 in [16, SV_MAX_HEAD_DIM] */
+  int32_t rotary_dim;    /* R: even, in [2, D]: the first R dims turn, the others stay */
+  int32_t axes;          /* positions of a token, in [1, SV_MAX_ROPE_AXES] */
+  int32_t adjacent;      /* 0: dims i and i + R/2 are pair i; 1: dims 2i and 2i + 1 */
+  sv_dtype dtype;        /* of q, k and their results */
+  int64_t position_stride;                  /* entries between the axes' positions, >= rows where axes > 1 */
+  int64_t q_row_stride, q_head_stride;      /* elements, >= D; the D values of a head are contiguous */
+  int64_t k_row_stride, k_head_stride;
+  int64_t q_out_row_stride, q_out_head_stride;
+  int64_t k_out_row_stride, k_out_head_stride;
+  uint8_t axis[SV_MAX_HEAD_DIM / 2];        /* axis[i] < axes: whose position turns pair i, for i < R / 2 */
+} sv_rope_desc;
+
+/*
+ * Rotary position embedding of the queries and keys of `rows` tokens.  Pair i
+ * (a, b) of every head of token r becomes
+ *   (a cos t - b sin t, a sin t + b cos t),  t = positions[axis[i], r] * inv_freq[i].
+ * Text has one axis; images and video have one for the time, the height and
+ * the width each, which share the pairs.  t is taken modulo a whole turn in
+ * 64 bits, so that far positions are as exact as near ones; sine and cosine
+ * are within 2^-23 of their values, and the result is rounded once.
+ *
+ *   q [rows, heads, D], k [rows, kv_heads, D];  positions [axes, rows] int32
+ *   (any value);  inv_freq [R / 2] float, finite: radians a position.
+ *   q_out, k_out: like q and k.  Either may be its input (the same pointer
+ *   and strides); otherwise they share no memory with q or k.
+ */
+sv_status sv_rope(const sv_rope_desc* desc, const void* q, const void* k, const int32_t* positions,
+                  const float* inv_freq, void* q_out, void* k_out, sv_stream_t stream);
+
+typedef struct sv_prompt_attention_desc {
+  int32_t batch;         /* B in [0, 65535] */
+  int32_t heads;         /* query heads: a multiple of kv_heads, heads / kv_heads <= 128 */
+  int32_t kv_heads;      /* in [1, 1024] */
+  int32_t head_dim;      /* D: a multiple of 16 in [16, SV_MAX_HEAD_DIM] */
+  int32_t max_new;       /* >= 0: the most tokens of a sequence */
+  int32_t total_new;     /* rows of q, k, v and out; batch * max_new when new_start is NULL */
+  sv_dtype dtype;        /* of q, k, v and out */
+  float scale;           /* of the scores, finite (normally 1 / sqrt(D)) */
+  int32_t window;        /* 0: every earlier token is visible; W > 0: the last W, the query's own among them */
+  int32_t sinks;         /* >= 0: the first `sinks` tokens of a sequence stay visible under a window */
+  int64_t q_row_stride, q_head_stride;      /* elements, >= D; the D values of a head are contiguous */
+  int64_t k_row_stride, k_head_stride;
+  int64_t v_row_stride, v_head_stride;
+  int64_t out_row_stride, out_head_stride;
+} sv_prompt_attention_desc;
+
+/* Workspace bytes for sv_prompt_attention (scratch on a 16-byte boundary, no
+ * initialisation); 0 for an invalid descriptor. */
+size_t sv_prompt_attention_workspace_size(const sv_prompt_attention_desc* desc);
+
+/*
+ * Causal attention of whole prompts over their own keys and values, before
+ * these are rounded to 8 bits.  Sequences are packed: token i of sequence b
+ * is row new_start[b] + i (b * max_new + i when new_start is NULL).  Query i
+ * with head h sees token j <= i of its own sequence and kv head
+ * h / (heads / kv_heads) where window == 0, i - j < window or j < sinks:
+ *   s_j = scale * <q_i, k_j>,  out = sum_j softmax(s)_j v_j,
+ *   lse = ln(sum_j exp(s_j)).
+ * What a query does not see has no influence on its result, whatever it
+ * holds (infinities and NaN too).  Rows that belong to no sequence are not
+ * touched.  A sequence with a negative length, more than max_new tokens or
+ * rows outside [0, total_new) is left out and flagged SV_ROW_BAD_LENGTH.
+ *
+ *   q [total_new, heads, D];  k, v [total_new, kv_heads, D];
+ *   out [total_new, heads, D], shares no memory with q, k or v;
+ *   lse optional [total_new, heads] float, contiguous;
+ *   new_start [B + 1] int32 or NULL;  row_status optional [B] int32.
+ *
+ * Scores and sums are held in fp32.
+ */
+sv_status sv_prompt_attention(const sv_prompt_attention_desc* desc, const void* q, const void* k, const void* v,
+                              const int32_t* new_start, void* out, float* lse, int32_t* row_status,
+                              void* workspace, size_t workspace_bytes, sv_stream_t stream);
 
 /*
  * Profiling hooks (host-side; they add no device work).
