@@ -817,25 +817,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_tiles_kernel(Attenti
   if (warp == 0) tc::tmem_free(tmem, T::kColumns);
 }
 
-// The driver's encoder of tensor maps, looked up through the runtime (the library does not link the driver).
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encoder() {
-  static const EncodeTiled found = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult how;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
-        how != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return found;
-}
-
 // Boxes of `width` dims (zeros behind the last) of 16 tokens of one head and page.
 bool cache_map(CUtensorMap* map, const sv_kv_desc& d, const uint8_t* cache, int width) {
-  const EncodeTiled encode = encoder();
+  const tc::EncodeTiled encode = tc::encoder();
   if (!encode) return false;
   const cuuint64_t size[4] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.page_size),
                               static_cast<cuuint64_t>(d.kv_heads), static_cast<cuuint64_t>(d.num_pages)};

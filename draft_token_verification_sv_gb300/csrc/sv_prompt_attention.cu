@@ -1,42 +1,11 @@
 // Causal attention of whole prompts over their own keys and values.
-#include "sv_kv.cuh"
+#include "sv_prompt.cuh"
 
 namespace sv {
 
 namespace {
 
 constexpr int kWarps = 8;
-
-struct PromptView {
-  const void* q;
-  const void* k;
-  const void* v;
-  void* out;
-  float* lse;
-  int64_t q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head;
-  const int32_t* new_start;
-  int32_t* status;  // [batch], cleared before the launch, or NULL
-  int batch, max_new, total_new, heads, kv_heads, group, dim, window, sinks;
-  float scale;
-};
-
-// Sequence b's rows; false: they are not rows of the call.
-struct PromptSpan {
-  int row0, n;
-  bool ok;
-};
-
-__device__ __forceinline__ PromptSpan prompt_span(const PromptView& a, int b) {
-  if (!a.new_start) return PromptSpan{b * a.max_new, a.max_new, true};
-  const int row0 = __ldg(a.new_start + b);
-  const int64_t n = static_cast<int64_t>(__ldg(a.new_start + b + 1)) - row0;
-  const bool ok = row0 >= 0 && n >= 0 && n <= a.max_new && row0 + n <= a.total_new;
-  return PromptSpan{row0, ok ? static_cast<int>(n) : 0, ok};
-}
-
-__device__ __forceinline__ void prompt_flag(const PromptView& a, int b, int bit) {
-  if (a.status) atomicOr(a.status + b, bit);
-}
 
 __device__ __forceinline__ float value_of(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float value_of(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16); }
@@ -99,6 +68,7 @@ sv_status prompt_attention(const sv_prompt_attention_desc& d, const void* q, con
   const PromptView a{q, k, v, out, lse, d.q_row_stride, d.q_head_stride, d.k_row_stride, d.k_head_stride, d.v_row_stride, d.v_head_stride,
                d.out_row_stride, d.out_head_stride, new_start, row_status, d.batch, d.max_new, d.total_new, d.heads, d.kv_heads,
                d.heads / d.kv_heads, d.head_dim, d.window, d.sinks, d.scale};
+  if (prompt_takes_tiles(a, d.dtype)) return prompt_tiles(a, stream);
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(d.max_new) + kWarps - 1) / kWarps + (d.max_new == 0)), d.heads, d.batch);
   if (d.dtype == SV_BF16)
     prompt_rows_kernel<uint16_t><<<grid, 32 * kWarps, 0, stream>>>(a);

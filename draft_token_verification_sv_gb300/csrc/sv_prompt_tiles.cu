@@ -1,0 +1,793 @@
+// Causal attention of bf16 prompts on the 5th-generation tensor cores.
+//
+// A block's item is one kv head and 128 rows, or two times 128, of queries:
+// row r of a tile is token r / group and head r % group of those that share
+// the kv head, so that short prompts and odd groups fill tiles, too, and a
+// tile's keys end close behind its tokens.  S = Q K^T and O += P V run against
+// tiles of 128 keys: Q, K and V come by tensor copies to shared memory, S and
+// O are in tensor memory, where the weights P take the place of their scores.
+// Roles of a block's warps:
+//   one loads: it finds the items and copies queries, keys and values;
+//   one issues the products;
+//   two look at the values of tiles that some rows do not see whole (below);
+//   four for each 128 rows turn scores into weights, a row a thread.
+// Weights are exp2(s - m) with m the row's largest score of the first tile
+// that it sees: bf16 weights have float's range, so m moves (and O is scaled
+// anew) only when a later tile's weights sum to 2^13 and more, and what a
+// weight loses by a small m is nothing.  Weights are rounded to bf16 (2^-8),
+// the type that the products ask for beside bf16 values; their sum is taken
+// before that, in fp32.
+// What a row does not see has weight 0, but 0 times what is not finite is not
+// 0: values of partly seen tiles that are not finite become 0 in shared memory
+// before their product, and rows that do see them get them where results are
+// written.
+#include "sv_prompt.cuh"
+#include "sv_tcgen05.cuh"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace sv {
+
+namespace {
+
+constexpr int kRows = 128;   // of a tile of queries
+constexpr int kKeys = 128;   // of a tile of keys
+constexpr int kItems = 4;    // items that may be known ahead
+constexpr int kSorted = 128; // sequences that are put in order of their lengths
+constexpr float kLargeSum = 8192.0f;
+
+template <int DP> struct Config {
+  static constexpr int NQ = DP == 256 ? 1 : 2;           // tiles of queries
+  static constexpr int kHalves = DP == 256 ? 2 : 1;      // copies of a tile of keys or values, of 128 dims at most
+  static constexpr int kUnitDims = DP / kHalves;
+  static constexpr int kUnitBytes = kKeys * kUnitDims * 2;
+  static constexpr int kBlockBytes = kKeys * 128;        // 64 dims of a tile
+  static constexpr int kQueryBytes = kRows * DP * 2;
+  static constexpr int kStages = DP == 64 ? 10 : 5;
+  static constexpr int kShared = NQ * kQueryBytes + kStages * kUnitBytes + 1024;
+  static constexpr int kSoftmaxWarps = 4 * NQ, kCheckWarps = 2;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+  // tensor memory, in columns: two places for scores, then O
+  static constexpr int kS = 0, kO = 2 * kKeys;
+  static constexpr int kSoftmaxRegisters = 208, kOtherRegisters = 88;  // (of 168 at launch, where there are three groups of four warps)
+};
+
+struct Item {
+  int row0, n, h;        // the sequence's rows, the kv head
+  int tok0;              // first token
+  int tiles;             // of keys, -1: no more items
+  int count[2];          // of them for each tile of queries
+  int first, window;     // tiles of the first tokens (sinks), then from this tile on
+  int dirty;             // values that are not finite were taken out
+};
+
+struct Shared {
+  uint64_t item_full[kItems], item_free[kItems];
+  uint64_t q_full[2], q_free[2];
+  uint64_t kv_full[10], kv_free[10], checked[10];
+  uint64_t s_full[2], p_ready[2], pv_done[2], o_free[2], last, answer;
+  uint4 block;           // what ask_for_block brings
+  Item item[kItems];
+  int n[kSorted], row0[kSorted];
+  uint8_t order[kSorted];
+  uint32_t tmem;
+  int gave_up;
+  int claimed, finished[8];  // items known, and done with by each warp that writes results
+};
+
+__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, int n) {
+  return __all_sync(0xffffffffu, tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t& bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::barrier_arrive(tc::smem_address(&bar));
+}
+
+// First key of the item's tile t.
+__device__ __forceinline__ int key_of(const Item& it, int t) { return kKeys * (t < it.first ? t : it.window + t - it.first); }
+
+// Does every row of tile i of queries see all of the tile at key kb?
+__device__ __forceinline__ bool whole(const PromptView& a, const Item& it, int tpt, int i, int kb) {
+  const int first = it.tok0 + i * tpt, last = min(first + tpt, it.n) - 1;
+  return kb + kKeys - 1 <= first && (a.window == 0 || last - kb < a.window || kb + kKeys - 1 < a.sinks);
+}
+
+// Are there rows that do not see all of tile t?
+template <int NQ>
+__device__ __forceinline__ bool partly_seen(const PromptView& a, const Item& it, int tpt, int t) {
+  bool all = true;
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) all = all && (t >= it.count[i] || whole(a, it, tpt, i, key_of(it, t)));
+  return !all;
+}
+
+// Bits c of [from, to) for the 32 from `base` on.
+__device__ __forceinline__ uint32_t bits32(int base, int from, int to) {
+  const int lo = min(max(from - base, 0), 32), hi = min(max(to - base, 0), 32);
+  return static_cast<uint32_t>(((1ull << hi) - 1ull) & ~((1ull << lo) - 1ull));
+}
+
+// ---- items ----
+
+// Finds items by their numbers: sequences in order (longest first where they are few), in each the last tokens first, kv heads
+// innermost.  One warp.
+struct Finder {
+  int at;            // sequences passed
+  long long before;  // items of those
+
+  template <int NQ>
+  __device__ __forceinline__ bool find(const PromptView& a, const Shared& sh, int tpt, long long index, Item& it) {
+    const int lane = threadIdx.x & 31, per = NQ * tpt;
+    if (index < before) at = 0, before = 0;
+    for (; at < a.batch;) {
+      int n = 0, row0 = 0;
+      if (at + lane < a.batch) {
+        if (a.batch <= kSorted) {
+          const int b = sh.order[at + lane];
+          n = sh.n[b];
+          row0 = sh.row0[b];
+        } else {
+          const PromptSpan s = prompt_span(a, at + lane);
+          n = s.n;
+          row0 = s.row0;
+        }
+      }
+      const int groups = (n + per - 1) / per;
+      long long upto = static_cast<long long>(groups) * a.kv_heads;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + upto > index);
+      if (past == 0) {
+        before += __shfl_sync(0xffffffffu, upto, 31);
+        at += 32;
+        continue;
+      }
+      const int who = __ffs(past) - 1;
+      const long long begin = before + __shfl_sync(0xffffffffu, upto, who) - static_cast<long long>(__shfl_sync(0xffffffffu, groups, who)) * a.kv_heads;
+      it.n = __shfl_sync(0xffffffffu, n, who);
+      it.row0 = __shfl_sync(0xffffffffu, row0, who);
+      const int local = static_cast<int>(index - begin);
+      it.h = local % a.kv_heads;
+      it.tok0 = (__shfl_sync(0xffffffffu, groups, who) - 1 - local / a.kv_heads) * per;
+      const int from = a.window ? max(0, it.tok0 - a.window + 1) : 0;
+      it.window = from / kKeys;
+      it.first = a.window ? min(it.window, a.sinks / kKeys + (a.sinks % kKeys != 0)) : 0;
+      it.tiles = 0;
+      it.dirty = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int first = it.tok0 + i * tpt, last = min(it.n, first + tpt) - 1;
+        it.count[i] = i < NQ && first < it.n ? it.first + last / kKeys - it.window + 1 : 0;
+        it.tiles = max(it.tiles, it.count[i]);
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+// A row of the call's results for row r of tile i, or -1.
+struct Place {
+  int64_t row;
+  int token, head;
+};
+__device__ __forceinline__ Place place_of(const PromptView& a, const Item& it, int tpt, int i, int r) {
+  Place p;
+  const int t = r / a.group;
+  p.token = it.tok0 + i * tpt + t;
+  p.head = it.h * a.group + r - t * a.group;
+  p.row = t < tpt && p.token < it.n && sv_in(it.row0 + static_cast<int64_t>(p.token), a.total_new) ? it.row0 + static_cast<int64_t>(p.token) : -1;
+  return p;
+}
+
+// ---- loading ----
+
+// A block's tile that is never copied, in builds that test what happens when waits run out.
+#ifndef SV_PROMPT_LOST_TILE
+#define SV_PROMPT_LOST_TILE -1
+#endif
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+// What the loading warp has under way.
+struct Loads {
+  int units, queries[2];  // copies of keys and values, of queries
+  int answers;            // questions for a block that were answered
+  bool asked;             // and one that was not
+  long long next;         // the number of the item that is published next
+};
+
+template <int DP>
+__device__ bool load_role(const PromptView& a, const Maps& maps, int tpt, Shared& sh, uint32_t q_at, uint32_t kv_at, Finder& finder, Loads& under) {
+  using C = Config<DP>;
+  const int lane = threadIdx.x & 31;
+  int items = 0, tile = 0;
+  const auto publish = [&](const Item& it) {
+    if (items >= kItems && !warp_wait(sh, sh.item_free[items % kItems], items / kItems - 1)) return false;
+    if (lane == 0) {
+      sh.item[items % kItems] = it;
+      if (it.tiles >= 0) sh.claimed = items + 1;
+    }
+    warp_arrive(sh.item_full[items % kItems]);
+    ++items;
+    return true;
+  };
+  const auto copy = [&](const CUtensorMap& map, const Item& it, int t) {  // a tile of keys or values
+    if (tile++ == SV_PROMPT_LOST_TILE) return false;
+    const int kb = key_of(it, t);
+#pragma unroll
+    for (int half = 0; half < C::kHalves; ++half) {
+      const int unit = under.units, stage = unit % C::kStages;
+      if (unit >= C::kStages && !warp_wait(sh, sh.kv_free[stage], unit / C::kStages - 1)) return false;
+      const uint32_t bar = tc::smem_address(&sh.kv_full[stage]);
+      if (lane == 0) {
+        tc::barrier_expect(bar, C::kUnitBytes);
+#pragma unroll
+        for (int x = 0; x < C::kUnitDims; x += 64)
+          tc::copy_box(kv_at + stage * C::kUnitBytes + x / 64 * C::kBlockBytes, &map, half * C::kUnitDims + x, it.h, it.row0 + kb, bar);
+      }
+      ++under.units;
+    }
+    return true;
+  };
+  Item it;
+  for (int x = blockIdx.x; x >= 0;) {
+    if (lane == 0) {
+      const uint32_t bar = tc::smem_address(&sh.answer);
+      tc::barrier_expect(bar, sizeof(sh.block));
+      tc::ask_for_block(tc::smem_address(&sh.block), bar);
+    }
+    under.asked = true;
+    for (under.next = x; finder.find<C::NQ>(a, sh, tpt, under.next, it);) {
+      if (!publish(it)) return false;
+      under.next += gridDim.x;
+#pragma unroll
+      for (int i = 0; i < C::NQ; ++i) {
+        if (it.count[i] == 0) continue;
+        if (under.queries[i] > 0 && !warp_wait(sh, sh.q_free[i], under.queries[i] - 1)) return false;
+        const uint32_t bar = tc::smem_address(&sh.q_full[i]);
+        if (lane == 0) {
+          tc::barrier_expect(bar, tpt * a.group * DP * 2);
+#pragma unroll
+          for (int d = 0; d < DP; d += 64)
+            tc::copy_box(q_at + i * C::kQueryBytes + d / 64 * (kRows * 128), &maps.q, d, it.h * a.group, it.row0 + it.tok0 + i * tpt, bar);
+        }
+        ++under.queries[i];
+        if (i == 0 && !copy(maps.k, it, 0)) return false;  // (the first keys behind the first queries)
+      }
+      for (int t = 0; t < it.tiles; ++t) {
+        if (C::NQ == 2) {
+          if (t > 0 && !copy(maps.k, it, t)) return false;
+        } else {
+          if (t + 1 < it.tiles && !copy(maps.k, it, t + 1)) return false;
+        }
+        if (!copy(maps.v, it, t)) return false;
+      }
+    }
+    if (!warp_wait(sh, sh.answer, under.answers)) return false;
+    ++under.answers;
+    under.asked = false;
+    x = tc::taken_block(tc::smem_address(&sh.block));
+    __syncwarp();
+    tc::publish_shared();  // (read before the next answer is written)
+  }
+  it.tiles = -1;
+  return publish(it);
+}
+
+// ---- values that are not finite ----
+
+// It takes part in every copy's way, so that it is never a round of the stages behind.
+template <int DP>
+__device__ bool check_role(const PromptView& a, int tpt, Shared& sh, uint8_t* kv) {
+  using C = Config<DP>;
+  const int tid = threadIdx.x - 32 * (C::kSoftmaxWarps + 2);
+  int unit = 0;
+  for (int items = 0;; ++items) {
+    if (!warp_wait(sh, sh.item_full[items % kItems], items / kItems)) return false;
+    Item& it = sh.item[items % kItems];
+    const int tiles = it.tiles;
+    if (tiles < 0) return true;
+    const auto pass = [&](bool look) {
+      for (int half = 0; half < C::kHalves; ++half, ++unit) {
+        const int stage = unit % C::kStages;
+        if (!warp_wait(sh, sh.kv_full[stage], unit / C::kStages)) return false;
+        if (look) {
+          uint4* at = reinterpret_cast<uint4*>(kv + stage * C::kUnitBytes);
+          bool found = false;
+#pragma unroll 8
+          for (int c = tid; c < C::kUnitBytes / 16; c += 32 * C::kCheckWarps) {
+            uint4 v = at[c];
+            // the largest magnitude of each half word: 0x7f80 and more is not finite
+            const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+            if (__vcmpgeu2(m, 0x7f807f80u)) {
+              found = true;
+              v.x &= ~__vcmpgeu2(v.x & 0x7fff7fffu, 0x7f807f80u);
+              v.y &= ~__vcmpgeu2(v.y & 0x7fff7fffu, 0x7f807f80u);
+              v.z &= ~__vcmpgeu2(v.z & 0x7fff7fffu, 0x7f807f80u);
+              v.w &= ~__vcmpgeu2(v.w & 0x7fff7fffu, 0x7f807f80u);
+              at[c] = v;
+            }
+          }
+          if (found) it.dirty = 1;
+          tc::publish_shared();
+          warp_arrive(sh.checked[stage]);
+        }
+        warp_arrive(sh.kv_free[stage]);
+      }
+      return true;
+    };
+    if (C::NQ == 1 && !pass(false)) return false;  // the first keys
+    for (int t = 0; t < tiles; ++t) {
+      if ((C::NQ == 2 || t + 1 < tiles) && !pass(false)) return false;  // keys
+      if (!pass(partly_seen<C::NQ>(a, it, tpt, t))) return false;
+    }
+    warp_arrive(sh.item_free[items % kItems]);
+  }
+}
+
+// ---- products ----
+
+template <int DP>
+__device__ bool product_role(const PromptView& a, int tpt, Shared& sh, uint32_t q_at, uint32_t kv_at, uint32_t tmem) {
+  using C = Config<DP>;
+  constexpr uint32_t kScores = tc::product_kind_bf16(kKeys, false), kValues = tc::product_kind_bf16(C::kUnitDims, true);
+  const auto wait = [&](uint64_t& bar, int n) {
+    const bool ok = tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up);
+    tc::fence_after();
+    return ok;
+  };
+  const auto arrive = [&](uint64_t& bar) { tc::products_arrive(tc::smem_address(&bar)); };
+  uint32_t checks = 0;  // parity of `checked` for each stage
+  int unit = 0, loads[2] = {0, 0}, done[2] = {0, 0}, weighed[2] = {0, 0}, tile = 0;
+  for (int items = 0;; ++items) {
+    if (!wait(sh.item_full[items % kItems], items / kItems)) return false;
+    const Item it = sh.item[items % kItems];
+    tc::barrier_arrive(tc::smem_address(&sh.item_free[items % kItems]));
+    if (it.tiles < 0) return true;
+    // S of tile i of queries with the keys of unit u, to place s
+    const auto score = [&](int i, int u, int s, bool last_use) {
+#pragma unroll
+      for (int half = 0; half < C::kHalves; ++half) {
+        const int stage = (u + half) % C::kStages;
+        if (!wait(sh.kv_full[stage], (u + half) / C::kStages)) return false;
+        const uint32_t k = kv_at + stage * C::kUnitBytes, q = q_at + i * C::kQueryBytes + half * (kRows * 256);
+#pragma unroll
+        for (int d = 0; d < C::kUnitDims / 16; ++d)
+          tc::product_f16(tmem + C::kS + s * kKeys, tc::tile_descriptor(q + (d >> 2) * (kRows * 128) + (d & 3) * 32, 16, 1024),
+                          tc::tile_descriptor(k + (d >> 2) * C::kBlockBytes + (d & 3) * 32, 16, 1024), kScores, half > 0 || d > 0);
+        if (last_use) arrive(sh.kv_free[stage]);
+      }
+      arrive(sh.s_full[s]);
+      return true;
+    };
+    // O of tile i (+)= P in place s times the values of unit u
+    const auto weigh = [&](int i, int u, int s, int uses, bool first, bool check, bool last_use) {
+      if (!wait(sh.p_ready[s], uses)) return false;
+#pragma unroll
+      for (int half = 0; half < C::kHalves; ++half) {
+        const int stage = (u + half) % C::kStages;
+        if (!wait(sh.kv_full[stage], (u + half) / C::kStages)) return false;
+        if (check && !wait(sh.checked[stage], checks >> stage)) return false;
+        const uint32_t v = kv_at + stage * C::kUnitBytes;
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          tc::product_f16(tmem + C::kO + i * DP + half * C::kUnitDims, tmem + C::kS + s * kKeys + k * 8,
+                          tc::tile_descriptor(v + k * 2048, C::kBlockBytes, 1024), kValues, !first || k > 0);
+        if (last_use) {
+          if (check) checks ^= 1u << stage;
+          arrive(sh.kv_free[stage]);
+        }
+      }
+      arrive(sh.pv_done[i]);
+      return true;
+    };
+    if (C::NQ == 2) {
+      // the last of the tiles of queries that need tile t
+      const auto last_of = [&](int t) { return t < it.count[1] ? 1 : 0; };
+#pragma unroll
+      for (int i = 0; i < C::NQ; ++i) {
+        if (it.count[i] == 0) continue;
+        if (!wait(sh.q_full[i], loads[i]++)) return false;
+        if (!score(i, unit, i, i == last_of(0))) return false;
+        if (it.count[i] == 1) arrive(sh.q_free[i]);
+      }
+      for (int t = 0; t < it.tiles; ++t, unit += 2) {
+        const bool check = partly_seen<C::NQ>(a, it, tpt, t);
+#pragma unroll
+        for (int i = 0; i < C::NQ; ++i) {
+          if (t >= it.count[i]) continue;
+          if (t == 0 && done[i] > 0 && !wait(sh.o_free[i], done[i] - 1)) return false;
+          if (!weigh(i, unit + 1, i, weighed[i]++, t == 0, check, i == last_of(t))) return false;
+          if (t + 1 >= it.count[i]) continue;
+          if (!score(i, unit + 2, i, i == last_of(t + 1))) return false;
+          if (t + 2 == it.count[i]) arrive(sh.q_free[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < C::NQ; ++i) done[i] += it.count[i] > 0;
+    } else {
+      if (!wait(sh.q_full[0], loads[0]++)) return false;
+      if (!score(0, unit, tile & 1, true)) return false;
+      unit += C::kHalves;
+      if (it.tiles == 1) arrive(sh.q_free[0]);
+      for (int t = 0; t < it.tiles; ++t, ++tile) {
+        if (t + 1 < it.tiles) {
+          if (!score(0, unit, tile + 1 & 1, true)) return false;
+          unit += C::kHalves;
+          if (t + 2 == it.tiles) arrive(sh.q_free[0]);
+        }
+        if (t == 0 && done[0] > 0 && !wait(sh.o_free[0], done[0] - 1)) return false;
+        if (!weigh(0, unit, tile & 1, tile >> 1, t == 0, partly_seen<C::NQ>(a, it, tpt, t), true)) return false;
+        unit += C::kHalves;
+      }
+      ++done[0];
+    }
+  }
+}
+
+// ---- scores to weights, and results ----
+
+// 32 scores to weights 2^(x f + c), packed into w; their sum.
+template <bool MASKED>
+__device__ __forceinline__ float weights32(const uint32_t (&x)[32], uint32_t seen, float f, float c, uint32_t (&w)[16]) {
+  const uint64_t ff = tc::pair(f, f), cc = tc::pair(c, c);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float2 e = tc::unpair(tc::fma2(tc::pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), ff, cc));
+    e.x = ex2(e.x);
+    e.y = ex2(e.y);
+    if (MASKED) {
+      e.x = seen >> (2 * k) & 1u ? e.x : 0.0f;
+      e.y = seen >> (2 * k + 1) & 1u ? e.y : 0.0f;
+    }
+    sum[k & 1] = tc::add2(sum[k & 1], tc::pair(e.x, e.y));
+    w[k] = floats_to_bf16x2(e.x, e.y);
+  }
+  const float2 s = tc::unpair(tc::add2(sum[0], sum[1]));
+  return s.x + s.y;
+}
+
+template <bool MASKED>
+__device__ __forceinline__ float largest32(const uint32_t (&x)[32], uint32_t seen, float f) {
+  float v[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k & 3] = fmaxf(v[k & 3], MASKED && !(seen >> k & 1u) ? -CUDART_INF_F : __uint_as_float(x[k]) * f);
+  return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+}
+
+// What the row sees of values that are not finite and were left out.
+__device__ __noinline__ void add_rest(const PromptView& a, const Item& it, int tpt, int token, int d, float (&x)[16]) {
+  const uint16_t* v = static_cast<const uint16_t*>(a.v) + static_cast<int64_t>(it.row0) * a.v_row + it.h * a.v_head;
+  for (int t = 0; t < it.tiles; ++t) {
+    const int kb = key_of(it, t);
+    if (!partly_seen<2>(a, it, tpt, t)) continue;
+    for (int j = kb; j < kb + kKeys && j <= token; ++j) {
+      if (a.window != 0 && token - j >= a.window && j >= a.sinks) continue;
+      if (!sv_in(it.row0 + static_cast<int64_t>(j), a.total_new)) break;
+      for (int k = 0; k < 16 && d + k < a.dim; ++k) {
+        const float y = __uint_as_float(static_cast<uint32_t>(__ldg(v + j * a.v_row + d + k)) << 16);
+        if (!(fabsf(y) < CUDART_INF_F)) x[k] += y;
+      }
+    }
+  }
+}
+
+template <int DP>
+__device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, uint32_t tmem, bool out_vec32) {
+  using C = Config<DP>;
+  const int i = threadIdx.x / kRows, r = threadIdx.x & (kRows - 1), quarter = (threadIdx.x >> 5) & 3;
+  const uint32_t mine = tmem + (quarter << 21);  // the warp's 32 lanes
+  const uint32_t own_o = mine + C::kO + i * DP;
+  const auto wait = [&](uint64_t& bar, int n) {
+    const bool ok = warp_wait(sh, bar, n);
+    tc::fence_after();
+    return ok;
+  };
+  int tile = 0;
+  for (int items = 0;; ++items) {
+    if (!wait(sh.item_full[items % kItems], items / kItems)) return false;
+    const Item& it = sh.item[items % kItems];
+    if (it.tiles < 0) return true;
+    const int count = it.count[i];
+    if (count > 0) {
+      const Place at = place_of(a, it, tpt, i, r);
+      const int token = at.token;
+      const bool held = at.row >= 0;
+      float m = held ? -CUDART_INF_F : 0.0f, l = 0.0f;  // the largest score of the first tile seen (base 2), the sum of weights
+      for (int t = 0; t < count; ++t, ++tile) {
+        const int s = C::NQ == 2 ? i : tile & 1, uses = C::NQ == 2 ? tile : tile >> 1;
+        const int kb = key_of(it, t);
+        const uint32_t scores = mine + C::kS + s * kKeys;
+        if (!wait(sh.s_full[s], uses)) return false;
+        const auto turn = [&](auto masked) {
+          constexpr bool M = decltype(masked)::value;
+          uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+          if (M) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              seen[c] = bits32(kb + 32 * c, a.window ? max(0, token - a.window + 1) : 0, token + 1);
+              if (a.window) seen[c] |= bits32(kb + 32 * c, 0, min(a.sinks, token + 1));
+            }
+          }
+          uint32_t x[4][32], w[16];
+          bool raise = held && m == -CUDART_INF_F;
+          bool any = __any_sync(0xffffffffu, raise);
+          tc::tmem_load32(scores, x[0]);
+          if (any) {
+#pragma unroll
+            for (int c = 1; c < 4; ++c) tc::tmem_load32(scores + 32 * c, x[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::wait_loads(x[c]);
+          } else {
+            float sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              tc::wait_loads(x[c]);
+              if (c < 3) tc::tmem_load32(scores + 32 * (c + 1), x[c + 1]);
+              sum += weights32<M>(x[c], seen[c], f, -m, w);
+              tc::tmem_store(scores + 16 * c, w);
+            }
+            raise = held && sum > kLargeSum;
+            any = __any_sync(0xffffffffu, raise);
+            if (!any) l += sum;
+          }
+          if (__builtin_expect(any, 0)) {
+            float top = m;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) top = fmaxf(top, largest32<M>(x[c], seen[c], f));
+            float fix = 1.0f;
+            if (raise && top > -CUDART_INF_F) {
+              fix = m == -CUDART_INF_F ? 1.0f : ex2(m - top);
+              m = top;
+              l *= fix;
+            }
+            if (t > 0 && __any_sync(0xffffffffu, fix != 1.0f)) {
+              if (!wait(sh.pv_done[i], tile - 1)) return false;
+              uint32_t o[16];
+#pragma unroll 1
+              for (int d = 0; d < DP; d += 16) {
+                tc::tmem_load16(own_o + d, o);
+                tc::wait_loads(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
+                tc::tmem_store(own_o + d, o);
+              }
+            }
+            const float base = m == -CUDART_INF_F ? 0.0f : m;
+            float sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              sum += weights32<M>(x[c], seen[c], f, -base, w);
+              tc::tmem_store(scores + 16 * c, w);
+            }
+            l += sum;
+          }
+          return true;
+        };
+        if (!(whole(a, it, tpt, i, kb) ? turn(std::false_type{}) : turn(std::true_type{}))) return false;
+        tc::wait_stores();
+        // (with one tile of queries the scores do not say that the sums before them are done, and a barrier is never two phases ahead)
+        if (C::NQ == 1 && t > 0 && !wait(sh.pv_done[i], tile - 1)) return false;
+        tc::fence_before();
+        warp_arrive(sh.p_ready[s]);
+      }
+      if (!wait(sh.pv_done[i], tile - 1)) return false;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      uint16_t* out = static_cast<uint16_t*>(a.out) + at.row * a.out_row + at.head * a.out_head;
+      const bool dirty = *const_cast<const volatile int*>(&it.dirty) != 0;
+#pragma unroll 1
+      for (int d = 0; d < DP; d += 16) {
+        uint32_t o[16];
+        tc::tmem_load16(own_o + d, o);
+        tc::wait_loads(o);
+        if (held && d < a.dim) {
+          float x[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]) * inv;
+          if (dirty) add_rest(a, it, tpt, token, d, x);
+          uint32_t y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = floats_to_bf16x2(x[2 * k], x[2 * k + 1]);
+          if (out_vec32) {
+            tc::store_32(out + d, y);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              out[d + 2 * k] = static_cast<uint16_t>(y[k]);
+              out[d + 2 * k + 1] = static_cast<uint16_t>(y[k] >> 16);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      tc::fence_before();
+      warp_arrive(sh.o_free[i]);
+      if (held && a.lse) a.lse[at.row * a.heads + at.head] = (m + log2f(l)) * 0.69314718055994530942f;
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) sh.finished[threadIdx.x >> 5] = items + 1;
+    warp_arrive(sh.item_free[items % kItems]);
+  }
+}
+
+// A wait ran out: results of the item are not valid.
+__device__ __noinline__ void spoil(const PromptView& a, const Item& it, int tpt, int nq, int thread, int threads) {
+  for (int b = thread; b < a.batch; b += threads) {
+    const PromptSpan s = prompt_span(a, b);
+    if (s.ok && s.row0 == it.row0 && s.n == it.n) prompt_flag(a, b, SV_ROW_TIMEOUT);
+  }
+  for (int r = thread; r < nq * kRows; r += threads) {
+    const Place p = place_of(a, it, tpt, r / kRows, r % kRows);
+    if (p.row < 0) continue;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + p.row * a.out_row + p.head * a.out_head;
+    for (int d = 0; d < a.dim; ++d) out[d] = 0x7fff;
+    if (a.lse) a.lse[p.row * a.heads + p.head] = CUDART_NAN_F;
+  }
+}
+
+static_assert(Config<128>::kShared + sizeof(Shared) <= 227 * 1024, "shared memory of a block");
+
+template <int DP>
+__global__ void __launch_bounds__(Config<DP>::kThreads, 1)
+    prompt_tiles_kernel(const __grid_constant__ PromptView a, const __grid_constant__ Maps maps, int tpt, float f, int out_vec32) {
+  using C = Config<DP>;
+  extern __shared__ uint8_t raw[];
+  __shared__ Shared sh;
+  const uint32_t at = tc::smem_address(raw);
+  uint8_t* tiles = raw + ((at + 1023u & ~1023u) - at);
+  const uint32_t q_at = tc::smem_address(tiles), kv_at = q_at + C::NQ * C::kQueryBytes;
+  const int warp = threadIdx.x >> 5, tid = threadIdx.x;
+  if (tid == 0) {
+    sh.gave_up = 0;
+    sh.claimed = 0;
+    for (int i = 0; i < 8; ++i) sh.finished[i] = 0;
+    tc::prefetch_map(&maps.q);
+    tc::prefetch_map(&maps.k);
+    tc::prefetch_map(&maps.v);
+    for (int i = 0; i < kItems; ++i) {
+      tc::barrier_init(tc::smem_address(&sh.item_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.item_free[i]), C::kSoftmaxWarps + C::kCheckWarps + 1);
+    }
+    for (int i = 0; i < C::kStages; ++i) {
+      tc::barrier_init(tc::smem_address(&sh.kv_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.kv_free[i]), 1 + C::kCheckWarps);
+      tc::barrier_init(tc::smem_address(&sh.checked[i]), C::kCheckWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::barrier_init(tc::smem_address(&sh.q_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.q_free[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.s_full[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.p_ready[i]), 4);
+      tc::barrier_init(tc::smem_address(&sh.pv_done[i]), 1);
+      tc::barrier_init(tc::smem_address(&sh.o_free[i]), 4);
+    }
+    tc::barrier_init(tc::smem_address(&sh.last), 1);
+    tc::barrier_init(tc::smem_address(&sh.answer), 1);
+    tc::publish_shared();
+  }
+  if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), 512);
+  if (a.batch <= kSorted) {
+    for (int b = tid; b < a.batch; b += C::kThreads) {
+      const PromptSpan s = prompt_span(a, b);
+      sh.n[b] = s.n;
+      sh.row0[b] = s.row0;
+    }
+    __syncthreads();
+    for (int b = tid; b < a.batch; b += C::kThreads) {
+      const int n = sh.n[b];
+      int rank = 0;
+      for (int o = 0; o < a.batch; ++o) rank += sh.n[o] > n || (sh.n[o] == n && o < b);
+      sh.order[rank] = static_cast<uint8_t>(b);
+    }
+  }
+  if (blockIdx.x == 0 && a.status)
+    for (int b = tid; b < a.batch; b += C::kThreads)
+      if (!prompt_span(a, b).ok) prompt_flag(a, b, SV_ROW_BAD_LENGTH);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sh.tmem;
+  if (warp < C::kSoftmaxWarps) {
+    if constexpr (C::NQ == 2) tc::registers_up<C::kSoftmaxRegisters>();
+    softmax_role<DP>(a, tpt, f, sh, tmem, out_vec32);
+  } else {
+    if constexpr (C::NQ == 2) tc::registers_down<C::kOtherRegisters>();
+    if (warp == C::kSoftmaxWarps) {
+      Finder finder{0, 0};
+      Loads under{};
+      if (!load_role<DP>(a, maps, tpt, sh, q_at, kv_at, finder, under)) {
+        // What is under way ends before its memory is given up: the last copies to each place, which no other role may have
+        // waited for, and the answer.  Items that no other role knows of are spoilt here.
+        int unused = 0;
+        for (int u = max(0, under.units - C::kStages); u < under.units; ++u)
+          tc::barrier_wait(tc::smem_address(&sh.kv_full[u % C::kStages]), u / C::kStages & 1, &unused, tc::kEndCycles);
+        for (int i = 0; i < C::NQ; ++i)
+          if (under.queries[i] > 0) tc::barrier_wait(tc::smem_address(&sh.q_full[i]), under.queries[i] - 1 & 1, &unused, tc::kEndCycles);
+        Item it;
+        for (; finder.find<C::NQ>(a, sh, tpt, under.next, it); under.next += gridDim.x) spoil(a, it, tpt, C::NQ, tid & 31, 32);
+        if (under.asked) {
+          const bool answered = tc::barrier_wait(tc::smem_address(&sh.answer), under.answers & 1, &unused, tc::kEndCycles);
+          const int x = __all_sync(0xffffffffu, answered) ? tc::taken_block(tc::smem_address(&sh.block)) : -1;
+          if (x >= 0)
+            for (long long index = x; finder.find<C::NQ>(a, sh, tpt, index, it); index += gridDim.x) spoil(a, it, tpt, C::NQ, tid & 31, 32);
+        }
+      }
+    } else if (warp == C::kSoftmaxWarps + 1) {
+      if (tc::elected()) {
+        product_role<DP>(a, tpt, sh, q_at, kv_at, tmem);
+        int unused = 0;
+        tc::products_arrive(tc::smem_address(&sh.last));
+        tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused, tc::kEndCycles);
+      }
+      __syncwarp();
+    } else {
+      check_role<DP>(a, tpt, sh, tiles + C::NQ * C::kQueryBytes);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (sh.gave_up) {
+    int done = sh.finished[0];
+    for (int i = 1; i < C::kSoftmaxWarps; ++i) done = min(done, sh.finished[i]);
+    for (int k = done; k < sh.claimed; ++k) spoil(a, sh.item[k % kItems], tpt, C::NQ, tid, C::kThreads);
+  }
+  if (warp == 0) tc::tmem_free(tmem, 512);
+}
+
+// Boxes of 64 dims (zeros behind the last) of `heads` heads of `rows` rows.
+bool rows_map(CUtensorMap* map, const void* at, int dim, int heads, int rows, int64_t head_stride, int64_t row_stride, int box_heads, int box_rows) {
+  const tc::EncodeTiled encode = tc::encoder();
+  if (!encode) return false;
+  const cuuint64_t size[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t stride[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(row_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)}, step[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(at), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP>
+sv_status launch(const PromptView& a, cudaStream_t stream) {
+  using C = Config<DP>;
+  static FuncAttrCache attr;
+  const auto kernel = prompt_tiles_kernel<DP>;
+  if (!attr.ensure(reinterpret_cast<const void*>(kernel), C::kShared, false)) return SV_ERR_CUDA;
+  const int tpt = kRows / a.group, per = C::NQ * tpt;
+  Maps maps;
+  if (!rows_map(&maps.q, a.q, a.dim, a.heads, a.total_new, a.q_head, a.q_row, a.group, tpt) ||
+      !rows_map(&maps.k, a.k, a.dim, a.kv_heads, a.total_new, a.k_head, a.k_row, 1, kKeys) ||
+      !rows_map(&maps.v, a.v, a.dim, a.kv_heads, a.total_new, a.v_head, a.v_row, 1, kKeys))
+    return SV_ERR_UNSUPPORTED;
+  // A block for each item: of packed sequences it is not known here how many there are, at most one more a sequence and head
+  // than their tokens fill.  Blocks take items beyond the grid, too.
+  int64_t blocks = a.new_start ? (static_cast<int64_t>(a.total_new) / per + std::min<int64_t>(a.batch, 4096 / a.kv_heads + 1)) * a.kv_heads
+                               : static_cast<int64_t>(a.batch) * ((a.max_new + per - 1) / per) * a.kv_heads;
+  blocks = std::min<int64_t>(std::max<int64_t>(blocks, 1), 1 << 30);
+  const bool vec32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_row % 16 == 0 && a.out_head % 16 == 0;
+  kernel<<<static_cast<unsigned>(blocks), C::kThreads, C::kShared, stream>>>(a, maps, tpt, a.scale * 1.44269504088896340736f, vec32);
+  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  note_launch(stream);
+  return SV_OK;
+}
+
+}  // namespace
+
+bool prompt_takes_tiles(const PromptView& a, sv_dtype dtype) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+  const int64_t strides = a.q_row | a.q_head | a.k_row | a.k_head | a.v_row | a.v_head;
+  return dtype == SV_BF16 && at % 16 == 0 && strides % 8 == 0 && a.total_new > 0;
+}
+
+sv_status prompt_tiles(const PromptView& a, cudaStream_t stream) {
+  return a.dim <= 64 ? launch<64>(a, stream) : a.dim <= 128 ? launch<128>(a, stream) : launch<256>(a, stream);
+}
+
+}  // namespace sv

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace sv {
@@ -71,6 +72,13 @@ __device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, in
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+// The same of three dimensions.
+__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
@@ -205,9 +213,34 @@ __device__ __forceinline__ uint64_t tile_descriptor(uint32_t at, uint32_t block,
          static_cast<uint64_t>(group >> 4) << 32 | uint64_t{1} << 46 | uint64_t{2} << 61;
 }
 
+// A piece of the launch that no block has taken yet is taken from it (its
+// block will not start), by one thread: 16 bytes of answer come to shared
+// memory and count at the barrier.
+__device__ __forceinline__ void ask_for_block(uint32_t to, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to), "r"(bar)
+               : "memory");
+}
+// The answer: an x index of the grid, or -1 where none was left (then no more may be asked for).
+__device__ __forceinline__ int taken_block(uint32_t at) {
+  int x;
+  asm volatile(
+      "{ .reg .b128 r; .reg .pred p; .reg .b32 i; ld.shared.b128 r, [%1]; "
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r; mov.b32 i, -1; "
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 i, r; mov.b32 %0, i; }"
+      : "=r"(x)
+      : "r"(at)
+      : "memory");
+  return x;
+}
+
 // fp16 x fp16 -> fp32, 128 x n; b_rows_inner: B's rows in memory are the inner dimension.
 __host__ __device__ constexpr uint32_t product_kind(int n, bool b_rows_inner) {
   return 1u << 4 | (b_rows_inner ? 1u << 16 : 0u) | static_cast<uint32_t>(n / 8) << 17 | (128u / 16) << 24;
+}
+
+// The same of bf16.
+__host__ __device__ constexpr uint32_t product_kind_bf16(int n, bool b_rows_inner) {
+  return product_kind(n, b_rows_inner) | 1u << 7 | 1u << 10;
 }
 
 // d += (or =, unless `add`) a b, with A (128 x 16) in tensor memory; one thread.
@@ -218,9 +251,33 @@ __device__ __forceinline__ void product_f16(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
+// The same with A in shared memory.
+__device__ __forceinline__ void product_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
 // The barrier gets an arrival when this thread's products so far are done.
 __device__ __forceinline__ void products_arrive(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The driver's encoder of tensor maps, looked up through the runtime (the library does not link the driver).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeTiled encoder() {
+  static const EncodeTiled found = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+        how != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return found;
 }
 
 }  // namespace tc
