@@ -160,8 +160,7 @@ SIGNATURES = {
     "sv_kv_attention": (_I32, [_P] * 13 + [_P, _SZ, _P]),
     "sv_kv_assign": (_I32, [_P] * 11 + [_P]),
     "sv_rope": (_I32, [_P] * 7 + [_P]),
-    "sv_prompt_attention_workspace_size": (_SZ, [_P]),
-    "sv_prompt_attention": (_I32, [_P] * 8 + [_P, _SZ, _P]),
+    "sv_prompt_attention": (_I32, [_P] * 8 + [_P]),
     "sv_status_string": (ctypes.c_char_p, [_I32]),
     "sv_version": (_I32, []),
     "sv_set_phase_events": (None, [_P, _I32]),

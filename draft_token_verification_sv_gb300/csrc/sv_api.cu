@@ -511,25 +511,18 @@ sv_status sv_rope(const sv_rope_desc* desc, const void* q, const void* k, const 
   return rope(*desc, q, k, positions, inv_freq, q_out, k_out, reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t sv_prompt_attention_workspace_size(const sv_prompt_attention_desc* desc) {
-  if (!prompt_desc_ok(desc, true)) return 0;
-  return prompt_attention_workspace_bytes(*desc);
-}
-
 sv_status sv_prompt_attention(const sv_prompt_attention_desc* desc, const void* q, const void* k, const void* v,
-                              const int32_t* new_start, void* out, float* lse, int32_t* row_status,
-                              void* workspace, size_t workspace_bytes, sv_stream_t stream) {
+                              const int32_t* new_start, void* out, float* lse, int32_t* row_status, sv_stream_t stream) {
   CallScope scope;
   if (!prompt_desc_ok(desc, new_start != nullptr)) return SV_ERR_INVALID_ARGUMENT;
   if (desc->batch == 0) return SV_OK;
-  if (!workspace || !aligned16(workspace) || !kv_words_ok(new_start, lse, row_status)) return SV_ERR_INVALID_ARGUMENT;
+  if (!kv_words_ok(new_start, lse, row_status)) return SV_ERR_INVALID_ARGUMENT;
   if (desc->total_new > 0) {
     const void* rows[4] = {q, k, v, out};
     for (const void* p : rows)
       if (!p || !aligned_elem(p, desc->dtype)) return SV_ERR_INVALID_ARGUMENT;
   }
-  if (workspace_bytes < sv_prompt_attention_workspace_size(desc)) return SV_ERR_WORKSPACE_TOO_SMALL;
-  return prompt_attention(*desc, q, k, v, new_start, out, lse, row_status, workspace, reinterpret_cast<cudaStream_t>(stream));
+  return prompt_attention(*desc, q, k, v, new_start, out, lse, row_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

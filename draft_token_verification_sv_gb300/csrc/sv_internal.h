@@ -185,10 +185,8 @@ sv_status kv_assign(const sv_kv_assign_desc& d, int32_t* free_pages, int32_t* fr
                     int32_t* positions, int32_t* row_status, cudaStream_t stream);
 sv_status rope(const sv_rope_desc& d, const void* q, const void* k, const int32_t* positions, const float* inv_freq,
                void* q_out, void* k_out, cudaStream_t stream);
-size_t prompt_attention_workspace_bytes(const sv_prompt_attention_desc& d);
 sv_status prompt_attention(const sv_prompt_attention_desc& d, const void* q, const void* k, const void* v,
-                           const int32_t* new_start, void* out, float* lse, int32_t* row_status, void* workspace,
-                           cudaStream_t stream);
+                           const int32_t* new_start, void* out, float* lse, int32_t* row_status, cudaStream_t stream);
 
 #ifdef SV_DEBUG
 // This translation unit's debug word reader, registered at load time.

@@ -39,5 +39,7 @@ __device__ __forceinline__ void prompt_flag(const PromptView& a, int b, int bit)
 // bf16 rows that tensor copies can read, on the tensor cores (sv_prompt_tiles.cu).
 bool prompt_takes_tiles(const PromptView& a, sv_dtype dtype);
 sv_status prompt_tiles(const PromptView& a, cudaStream_t stream);
+// Any others, on the tensor cores, too (sv_prompt_split.cu).
+sv_status prompt_split(const PromptView& a, sv_dtype dtype, cudaStream_t stream);
 
 }  // namespace sv

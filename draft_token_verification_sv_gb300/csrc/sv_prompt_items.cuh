@@ -1,0 +1,189 @@
+// How the tensor core kernels of prompt attention share their work out.
+//
+// An item is one kv head and 128 rows of queries, or NQ times 128: row r of a
+// tile is token r / group and head r % group of those that share the kv head,
+// so that short prompts and odd groups fill tiles, too, and a tile's keys end
+// close behind its tokens.
+#pragma once
+
+#include "sv_prompt.cuh"
+#include "sv_tcgen05.cuh"
+
+#include <algorithm>
+
+namespace sv {
+
+constexpr int kRows = 128;  // of a tile of queries
+
+struct Item {
+  int row0, n, h;        // the sequence's rows, the kv head
+  int tok0;              // first token
+  int tiles;             // of keys, -1: no more items
+  int count[2];          // of them for each tile of queries
+  int first, window;     // tiles of the first tokens (sinks), then from this tile on
+  int dirty;             // values that are not finite were taken out
+};
+
+// Sequences where they are few: their rows, and the longest first.
+constexpr int kSorted = 128;
+struct Sequences {
+  int n[kSorted], row0[kSorted];
+  uint8_t order[kSorted];
+};
+
+// By all threads of the block; the order is complete behind its next barrier.
+__device__ __forceinline__ void sort_sequences(const PromptView& a, Sequences& sq, int threads) {
+  if (a.batch > kSorted) return;
+  for (int b = threadIdx.x; b < a.batch; b += threads) {
+    const PromptSpan s = prompt_span(a, b);
+    sq.n[b] = s.n;
+    sq.row0[b] = s.row0;
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.batch; b += threads) {
+    const int n = sq.n[b];
+    int rank = 0;
+    for (int o = 0; o < a.batch; ++o) rank += sq.n[o] > n || (sq.n[o] == n && o < b);
+    sq.order[rank] = static_cast<uint8_t>(b);
+  }
+}
+
+// Flags of sequences that are left out, by one block's threads.
+__device__ __forceinline__ void flag_lengths(const PromptView& a, int threads) {
+  if (a.status)
+    for (int b = threadIdx.x; b < a.batch; b += threads)
+      if (!prompt_span(a, b).ok) prompt_flag(a, b, SV_ROW_BAD_LENGTH);
+}
+
+// First key of the item's tile t.
+template <int KEYS>
+__device__ __forceinline__ int key_of(const Item& it, int t) {
+  return KEYS * (t < it.first ? t : it.window + t - it.first);
+}
+
+// Does every row of tile i of queries see all of the tile at key kb?
+template <int KEYS>
+__device__ __forceinline__ bool whole(const PromptView& a, const Item& it, int tpt, int i, int kb) {
+  const int first = it.tok0 + i * tpt, last = min(first + tpt, it.n) - 1;
+  return kb + KEYS - 1 <= first && (a.window == 0 || last - kb < a.window || kb + KEYS - 1 < a.sinks);
+}
+
+// Are there rows that do not see all of tile t?
+template <int KEYS, int NQ>
+__device__ __forceinline__ bool partly_seen(const PromptView& a, const Item& it, int tpt, int t) {
+  bool all = true;
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) all = all && (t >= it.count[i] || whole<KEYS>(a, it, tpt, i, key_of<KEYS>(it, t)));
+  return !all;
+}
+
+// Bits c of [from, to) for the 32 from `base` on.
+__device__ __forceinline__ uint32_t bits32(int base, int from, int to) {
+  const int lo = min(max(from - base, 0), 32), hi = min(max(to - base, 0), 32);
+  return static_cast<uint32_t>(((1ull << hi) - 1ull) & ~((1ull << lo) - 1ull));
+}
+
+// Finds items by their numbers: sequences in order (longest first where they are few), in each the last tokens first, kv heads
+// innermost.  One warp.
+struct Finder {
+  int at;            // sequences passed
+  long long before;  // items of those
+
+  template <int KEYS, int NQ>
+  __device__ __forceinline__ bool find(const PromptView& a, const Sequences& sq, int tpt, long long index, Item& it) {
+    const int lane = threadIdx.x & 31, per = NQ * tpt;
+    if (index < before) at = 0, before = 0;
+    for (; at < a.batch;) {
+      int n = 0, row0 = 0;
+      if (at + lane < a.batch) {
+        if (a.batch <= kSorted) {
+          const int b = sq.order[at + lane];
+          n = sq.n[b];
+          row0 = sq.row0[b];
+        } else {
+          const PromptSpan s = prompt_span(a, at + lane);
+          n = s.n;
+          row0 = s.row0;
+        }
+      }
+      const int groups = (n + per - 1) / per;
+      long long upto = static_cast<long long>(groups) * a.kv_heads;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + upto > index);
+      if (past == 0) {
+        before += __shfl_sync(0xffffffffu, upto, 31);
+        at += 32;
+        continue;
+      }
+      const int who = __ffs(past) - 1;
+      const long long begin = before + __shfl_sync(0xffffffffu, upto, who) - static_cast<long long>(__shfl_sync(0xffffffffu, groups, who)) * a.kv_heads;
+      it.n = __shfl_sync(0xffffffffu, n, who);
+      it.row0 = __shfl_sync(0xffffffffu, row0, who);
+      const int local = static_cast<int>(index - begin);
+      it.h = local % a.kv_heads;
+      it.tok0 = (__shfl_sync(0xffffffffu, groups, who) - 1 - local / a.kv_heads) * per;
+      const int from = a.window ? max(0, it.tok0 - a.window + 1) : 0;
+      it.window = from / KEYS;
+      it.first = a.window ? min(it.window, a.sinks / KEYS + (a.sinks % KEYS != 0)) : 0;
+      it.tiles = 0;
+      it.dirty = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int first = it.tok0 + i * tpt, last = min(it.n, first + tpt) - 1;
+        it.count[i] = i < NQ && first < it.n ? it.first + last / KEYS - it.window + 1 : 0;
+        it.tiles = max(it.tiles, it.count[i]);
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+// A row of the call's results for row r of tile i, or -1.
+struct Place {
+  int64_t row;
+  int token, head;
+};
+__device__ __forceinline__ Place place_of(const PromptView& a, const Item& it, int tpt, int i, int r) {
+  Place p;
+  const int t = r / a.group;
+  p.token = it.tok0 + i * tpt + t;
+  p.head = it.h * a.group + r - t * a.group;
+  p.row = t < tpt && p.token < it.n && sv_in(it.row0 + static_cast<int64_t>(p.token), a.total_new) ? it.row0 + static_cast<int64_t>(p.token) : -1;
+  return p;
+}
+
+// A block for each item (of `per` tokens): of packed sequences it is not known on the host how many there are, at most one more a
+// sequence and head than their tokens fill.  Blocks take items beyond the grid, too.
+inline unsigned prompt_blocks(const PromptView& a, int per) {
+  const int64_t blocks = a.new_start ? (static_cast<int64_t>(a.total_new) / per + std::min<int64_t>(a.batch, 4096 / a.kv_heads + 1)) * a.kv_heads
+                                     : static_cast<int64_t>(a.batch) * ((a.max_new + per - 1) / per) * a.kv_heads;
+  return static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(blocks, 1), 1 << 30));
+}
+
+__device__ __forceinline__ float value_of(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float value_of(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16); }
+__device__ __forceinline__ void put_value(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put_value(uint16_t* p, float v) { *p = static_cast<uint16_t>(floats_to_bf16x2(v, 0.0f)); }
+
+// A wait ran out: results of the item are not valid.
+template <typename E>
+__device__ __noinline__ void spoil(const PromptView& a, const Item& it, int tpt, int nq, int thread, int threads) {
+  for (int b = thread; b < a.batch; b += threads) {
+    const PromptSpan s = prompt_span(a, b);
+    if (s.ok && s.row0 == it.row0 && s.n == it.n) prompt_flag(a, b, SV_ROW_TIMEOUT);
+  }
+  for (int r = thread; r < nq * kRows; r += threads) {
+    const Place p = place_of(a, it, tpt, r / kRows, r % kRows);
+    if (p.row < 0) continue;
+    E* out = static_cast<E*>(a.out) + p.row * a.out_row + p.head * a.out_head;
+    for (int d = 0; d < a.dim; ++d) put_value(out + d, CUDART_NAN_F);
+    if (a.lse) a.lse[p.row * a.heads + p.head] = CUDART_NAN_F;
+  }
+}
+
+}  // namespace sv

@@ -1,11 +1,9 @@
 // Causal attention of bf16 prompts on the 5th-generation tensor cores.
 //
-// A block's item is one kv head and 128 rows, or two times 128, of queries:
-// row r of a tile is token r / group and head r % group of those that share
-// the kv head, so that short prompts and odd groups fill tiles, too, and a
-// tile's keys end close behind its tokens.  S = Q K^T and O += P V run against
-// tiles of 128 keys: Q, K and V come by tensor copies to shared memory, S and
-// O are in tensor memory, where the weights P take the place of their scores.
+// A block takes 128 rows, or two times 128, of one kv head's queries at a time
+// (sv_prompt_items.cuh).  S = Q K^T and O += P V run against tiles of 128 keys:
+// Q, K and V come by tensor copies to shared memory, S and O are in tensor
+// memory, where the weights P take the place of their scores.
 // Roles of a block's warps:
 //   one loads: it finds the items and copies queries, keys and values;
 //   one issues the products;
@@ -21,20 +19,16 @@
 // 0: values of partly seen tiles that are not finite become 0 in shared memory
 // before their product, and rows that do see them get them where results are
 // written.
-#include "sv_prompt.cuh"
-#include "sv_tcgen05.cuh"
+#include "sv_prompt_items.cuh"
 
-#include <algorithm>
 #include <type_traits>
 
 namespace sv {
 
 namespace {
 
-constexpr int kRows = 128;   // of a tile of queries
 constexpr int kKeys = 128;   // of a tile of keys
 constexpr int kItems = 4;    // items that may be known ahead
-constexpr int kSorted = 128; // sequences that are put in order of their lengths
 constexpr float kLargeSum = 8192.0f;
 
 template <int DP> struct Config {
@@ -53,15 +47,6 @@ template <int DP> struct Config {
   static constexpr int kSoftmaxRegisters = 208, kOtherRegisters = 88;  // (of 168 at launch, where there are three groups of four warps)
 };
 
-struct Item {
-  int row0, n, h;        // the sequence's rows, the kv head
-  int tok0;              // first token
-  int tiles;             // of keys, -1: no more items
-  int count[2];          // of them for each tile of queries
-  int first, window;     // tiles of the first tokens (sinks), then from this tile on
-  int dirty;             // values that are not finite were taken out
-};
-
 struct Shared {
   uint64_t item_full[kItems], item_free[kItems];
   uint64_t q_full[2], q_free[2];
@@ -69,8 +54,7 @@ struct Shared {
   uint64_t s_full[2], p_ready[2], pv_done[2], o_free[2], last, answer;
   uint4 block;           // what ask_for_block brings
   Item item[kItems];
-  int n[kSorted], row0[kSorted];
-  uint8_t order[kSorted];
+  Sequences sequences;
   uint32_t tmem;
   int gave_up;
   int claimed, finished[8];  // items known, and done with by each warp that writes results
@@ -82,106 +66,6 @@ __device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t& bar, int n) {
 __device__ __forceinline__ void warp_arrive(uint64_t& bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) tc::barrier_arrive(tc::smem_address(&bar));
-}
-
-// First key of the item's tile t.
-__device__ __forceinline__ int key_of(const Item& it, int t) { return kKeys * (t < it.first ? t : it.window + t - it.first); }
-
-// Does every row of tile i of queries see all of the tile at key kb?
-__device__ __forceinline__ bool whole(const PromptView& a, const Item& it, int tpt, int i, int kb) {
-  const int first = it.tok0 + i * tpt, last = min(first + tpt, it.n) - 1;
-  return kb + kKeys - 1 <= first && (a.window == 0 || last - kb < a.window || kb + kKeys - 1 < a.sinks);
-}
-
-// Are there rows that do not see all of tile t?
-template <int NQ>
-__device__ __forceinline__ bool partly_seen(const PromptView& a, const Item& it, int tpt, int t) {
-  bool all = true;
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) all = all && (t >= it.count[i] || whole(a, it, tpt, i, key_of(it, t)));
-  return !all;
-}
-
-// Bits c of [from, to) for the 32 from `base` on.
-__device__ __forceinline__ uint32_t bits32(int base, int from, int to) {
-  const int lo = min(max(from - base, 0), 32), hi = min(max(to - base, 0), 32);
-  return static_cast<uint32_t>(((1ull << hi) - 1ull) & ~((1ull << lo) - 1ull));
-}
-
-// ---- items ----
-
-// Finds items by their numbers: sequences in order (longest first where they are few), in each the last tokens first, kv heads
-// innermost.  One warp.
-struct Finder {
-  int at;            // sequences passed
-  long long before;  // items of those
-
-  template <int NQ>
-  __device__ __forceinline__ bool find(const PromptView& a, const Shared& sh, int tpt, long long index, Item& it) {
-    const int lane = threadIdx.x & 31, per = NQ * tpt;
-    if (index < before) at = 0, before = 0;
-    for (; at < a.batch;) {
-      int n = 0, row0 = 0;
-      if (at + lane < a.batch) {
-        if (a.batch <= kSorted) {
-          const int b = sh.order[at + lane];
-          n = sh.n[b];
-          row0 = sh.row0[b];
-        } else {
-          const PromptSpan s = prompt_span(a, at + lane);
-          n = s.n;
-          row0 = s.row0;
-        }
-      }
-      const int groups = (n + per - 1) / per;
-      long long upto = static_cast<long long>(groups) * a.kv_heads;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += up;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, before + upto > index);
-      if (past == 0) {
-        before += __shfl_sync(0xffffffffu, upto, 31);
-        at += 32;
-        continue;
-      }
-      const int who = __ffs(past) - 1;
-      const long long begin = before + __shfl_sync(0xffffffffu, upto, who) - static_cast<long long>(__shfl_sync(0xffffffffu, groups, who)) * a.kv_heads;
-      it.n = __shfl_sync(0xffffffffu, n, who);
-      it.row0 = __shfl_sync(0xffffffffu, row0, who);
-      const int local = static_cast<int>(index - begin);
-      it.h = local % a.kv_heads;
-      it.tok0 = (__shfl_sync(0xffffffffu, groups, who) - 1 - local / a.kv_heads) * per;
-      const int from = a.window ? max(0, it.tok0 - a.window + 1) : 0;
-      it.window = from / kKeys;
-      it.first = a.window ? min(it.window, a.sinks / kKeys + (a.sinks % kKeys != 0)) : 0;
-      it.tiles = 0;
-      it.dirty = 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int first = it.tok0 + i * tpt, last = min(it.n, first + tpt) - 1;
-        it.count[i] = i < NQ && first < it.n ? it.first + last / kKeys - it.window + 1 : 0;
-        it.tiles = max(it.tiles, it.count[i]);
-      }
-      return true;
-    }
-    return false;
-  }
-};
-
-// A row of the call's results for row r of tile i, or -1.
-struct Place {
-  int64_t row;
-  int token, head;
-};
-__device__ __forceinline__ Place place_of(const PromptView& a, const Item& it, int tpt, int i, int r) {
-  Place p;
-  const int t = r / a.group;
-  p.token = it.tok0 + i * tpt + t;
-  p.head = it.h * a.group + r - t * a.group;
-  p.row = t < tpt && p.token < it.n && sv_in(it.row0 + static_cast<int64_t>(p.token), a.total_new) ? it.row0 + static_cast<int64_t>(p.token) : -1;
-  return p;
 }
 
 // ---- loading ----
@@ -220,7 +104,7 @@ __device__ bool load_role(const PromptView& a, const Maps& maps, int tpt, Shared
   };
   const auto copy = [&](const CUtensorMap& map, const Item& it, int t) {  // a tile of keys or values
     if (tile++ == SV_PROMPT_LOST_TILE) return false;
-    const int kb = key_of(it, t);
+    const int kb = key_of<kKeys>(it, t);
 #pragma unroll
     for (int half = 0; half < C::kHalves; ++half) {
       const int unit = under.units, stage = unit % C::kStages;
@@ -244,7 +128,7 @@ __device__ bool load_role(const PromptView& a, const Maps& maps, int tpt, Shared
       tc::ask_for_block(tc::smem_address(&sh.block), bar);
     }
     under.asked = true;
-    for (under.next = x; finder.find<C::NQ>(a, sh, tpt, under.next, it);) {
+    for (under.next = x; finder.find<kKeys, C::NQ>(a, sh.sequences, tpt, under.next, it);) {
       if (!publish(it)) return false;
       under.next += gridDim.x;
 #pragma unroll
@@ -326,7 +210,7 @@ __device__ bool check_role(const PromptView& a, int tpt, Shared& sh, uint8_t* kv
     if (C::NQ == 1 && !pass(false)) return false;  // the first keys
     for (int t = 0; t < tiles; ++t) {
       if ((C::NQ == 2 || t + 1 < tiles) && !pass(false)) return false;  // keys
-      if (!pass(partly_seen<C::NQ>(a, it, tpt, t))) return false;
+      if (!pass(partly_seen<kKeys, C::NQ>(a, it, tpt, t))) return false;
     }
     warp_arrive(sh.item_free[items % kItems]);
   }
@@ -399,7 +283,7 @@ __device__ bool product_role(const PromptView& a, int tpt, Shared& sh, uint32_t 
         if (it.count[i] == 1) arrive(sh.q_free[i]);
       }
       for (int t = 0; t < it.tiles; ++t, unit += 2) {
-        const bool check = partly_seen<C::NQ>(a, it, tpt, t);
+        const bool check = partly_seen<kKeys, C::NQ>(a, it, tpt, t);
 #pragma unroll
         for (int i = 0; i < C::NQ; ++i) {
           if (t >= it.count[i]) continue;
@@ -424,7 +308,7 @@ __device__ bool product_role(const PromptView& a, int tpt, Shared& sh, uint32_t 
           if (t + 2 == it.tiles) arrive(sh.q_free[0]);
         }
         if (t == 0 && done[0] > 0 && !wait(sh.o_free[0], done[0] - 1)) return false;
-        if (!weigh(0, unit, tile & 1, tile >> 1, t == 0, partly_seen<C::NQ>(a, it, tpt, t), true)) return false;
+        if (!weigh(0, unit, tile & 1, tile >> 1, t == 0, partly_seen<kKeys, C::NQ>(a, it, tpt, t), true)) return false;
         unit += C::kHalves;
       }
       ++done[0];
@@ -467,8 +351,8 @@ __device__ __forceinline__ float largest32(const uint32_t (&x)[32], uint32_t see
 __device__ __noinline__ void add_rest(const PromptView& a, const Item& it, int tpt, int token, int d, float (&x)[16]) {
   const uint16_t* v = static_cast<const uint16_t*>(a.v) + static_cast<int64_t>(it.row0) * a.v_row + it.h * a.v_head;
   for (int t = 0; t < it.tiles; ++t) {
-    const int kb = key_of(it, t);
-    if (!partly_seen<2>(a, it, tpt, t)) continue;
+    const int kb = key_of<kKeys>(it, t);
+    if (!partly_seen<kKeys, 2>(a, it, tpt, t)) continue;
     for (int j = kb; j < kb + kKeys && j <= token; ++j) {
       if (a.window != 0 && token - j >= a.window && j >= a.sinks) continue;
       if (!sv_in(it.row0 + static_cast<int64_t>(j), a.total_new)) break;
@@ -504,7 +388,7 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
       float m = held ? -CUDART_INF_F : 0.0f, l = 0.0f;  // the largest score of the first tile seen (base 2), the sum of weights
       for (int t = 0; t < count; ++t, ++tile) {
         const int s = C::NQ == 2 ? i : tile & 1, uses = C::NQ == 2 ? tile : tile >> 1;
-        const int kb = key_of(it, t);
+        const int kb = key_of<kKeys>(it, t);
         const uint32_t scores = mine + C::kS + s * kKeys;
         if (!wait(sh.s_full[s], uses)) return false;
         const auto turn = [&](auto masked) {
@@ -572,7 +456,7 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
           }
           return true;
         };
-        if (!(whole(a, it, tpt, i, kb) ? turn(std::false_type{}) : turn(std::true_type{}))) return false;
+        if (!(whole<kKeys>(a, it, tpt, i, kb) ? turn(std::false_type{}) : turn(std::true_type{}))) return false;
         tc::wait_stores();
         // (with one tile of queries the scores do not say that the sums before them are done, and a barrier is never two phases ahead)
         if (C::NQ == 1 && t > 0 && !wait(sh.pv_done[i], tile - 1)) return false;
@@ -618,21 +502,6 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
   }
 }
 
-// A wait ran out: results of the item are not valid.
-__device__ __noinline__ void spoil(const PromptView& a, const Item& it, int tpt, int nq, int thread, int threads) {
-  for (int b = thread; b < a.batch; b += threads) {
-    const PromptSpan s = prompt_span(a, b);
-    if (s.ok && s.row0 == it.row0 && s.n == it.n) prompt_flag(a, b, SV_ROW_TIMEOUT);
-  }
-  for (int r = thread; r < nq * kRows; r += threads) {
-    const Place p = place_of(a, it, tpt, r / kRows, r % kRows);
-    if (p.row < 0) continue;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + p.row * a.out_row + p.head * a.out_head;
-    for (int d = 0; d < a.dim; ++d) out[d] = 0x7fff;
-    if (a.lse) a.lse[p.row * a.heads + p.head] = CUDART_NAN_F;
-  }
-}
-
 static_assert(Config<128>::kShared + sizeof(Shared) <= 227 * 1024, "shared memory of a block");
 
 template <int DP>
@@ -674,23 +543,8 @@ __global__ void __launch_bounds__(Config<DP>::kThreads, 1)
     tc::publish_shared();
   }
   if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), 512);
-  if (a.batch <= kSorted) {
-    for (int b = tid; b < a.batch; b += C::kThreads) {
-      const PromptSpan s = prompt_span(a, b);
-      sh.n[b] = s.n;
-      sh.row0[b] = s.row0;
-    }
-    __syncthreads();
-    for (int b = tid; b < a.batch; b += C::kThreads) {
-      const int n = sh.n[b];
-      int rank = 0;
-      for (int o = 0; o < a.batch; ++o) rank += sh.n[o] > n || (sh.n[o] == n && o < b);
-      sh.order[rank] = static_cast<uint8_t>(b);
-    }
-  }
-  if (blockIdx.x == 0 && a.status)
-    for (int b = tid; b < a.batch; b += C::kThreads)
-      if (!prompt_span(a, b).ok) prompt_flag(a, b, SV_ROW_BAD_LENGTH);
+  sort_sequences(a, sh.sequences, C::kThreads);
+  if (blockIdx.x == 0) flag_lengths(a, C::kThreads);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -712,12 +566,12 @@ __global__ void __launch_bounds__(Config<DP>::kThreads, 1)
         for (int i = 0; i < C::NQ; ++i)
           if (under.queries[i] > 0) tc::barrier_wait(tc::smem_address(&sh.q_full[i]), under.queries[i] - 1 & 1, &unused, tc::kEndCycles);
         Item it;
-        for (; finder.find<C::NQ>(a, sh, tpt, under.next, it); under.next += gridDim.x) spoil(a, it, tpt, C::NQ, tid & 31, 32);
+        for (; finder.find<kKeys, C::NQ>(a, sh.sequences, tpt, under.next, it); under.next += gridDim.x) spoil<uint16_t>(a, it, tpt, C::NQ, tid & 31, 32);
         if (under.asked) {
           const bool answered = tc::barrier_wait(tc::smem_address(&sh.answer), under.answers & 1, &unused, tc::kEndCycles);
           const int x = __all_sync(0xffffffffu, answered) ? tc::taken_block(tc::smem_address(&sh.block)) : -1;
           if (x >= 0)
-            for (long long index = x; finder.find<C::NQ>(a, sh, tpt, index, it); index += gridDim.x) spoil(a, it, tpt, C::NQ, tid & 31, 32);
+            for (long long index = x; finder.find<kKeys, C::NQ>(a, sh.sequences, tpt, index, it); index += gridDim.x) spoil<uint16_t>(a, it, tpt, C::NQ, tid & 31, 32);
         }
       }
     } else if (warp == C::kSoftmaxWarps + 1) {
@@ -738,7 +592,7 @@ __global__ void __launch_bounds__(Config<DP>::kThreads, 1)
   if (sh.gave_up) {
     int done = sh.finished[0];
     for (int i = 1; i < C::kSoftmaxWarps; ++i) done = min(done, sh.finished[i]);
-    for (int k = done; k < sh.claimed; ++k) spoil(a, sh.item[k % kItems], tpt, C::NQ, tid, C::kThreads);
+    for (int k = done; k < sh.claimed; ++k) spoil<uint16_t>(a, sh.item[k % kItems], tpt, C::NQ, tid, C::kThreads);
   }
   if (warp == 0) tc::tmem_free(tmem, 512);
 }
@@ -760,19 +614,14 @@ sv_status launch(const PromptView& a, cudaStream_t stream) {
   static FuncAttrCache attr;
   const auto kernel = prompt_tiles_kernel<DP>;
   if (!attr.ensure(reinterpret_cast<const void*>(kernel), C::kShared, false)) return SV_ERR_CUDA;
-  const int tpt = kRows / a.group, per = C::NQ * tpt;
+  const int tpt = kRows / a.group;
   Maps maps;
   if (!rows_map(&maps.q, a.q, a.dim, a.heads, a.total_new, a.q_head, a.q_row, a.group, tpt) ||
       !rows_map(&maps.k, a.k, a.dim, a.kv_heads, a.total_new, a.k_head, a.k_row, 1, kKeys) ||
       !rows_map(&maps.v, a.v, a.dim, a.kv_heads, a.total_new, a.v_head, a.v_row, 1, kKeys))
     return SV_ERR_UNSUPPORTED;
-  // A block for each item: of packed sequences it is not known here how many there are, at most one more a sequence and head
-  // than their tokens fill.  Blocks take items beyond the grid, too.
-  int64_t blocks = a.new_start ? (static_cast<int64_t>(a.total_new) / per + std::min<int64_t>(a.batch, 4096 / a.kv_heads + 1)) * a.kv_heads
-                               : static_cast<int64_t>(a.batch) * ((a.max_new + per - 1) / per) * a.kv_heads;
-  blocks = std::min<int64_t>(std::max<int64_t>(blocks, 1), 1 << 30);
   const bool vec32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_row % 16 == 0 && a.out_head % 16 == 0;
-  kernel<<<static_cast<unsigned>(blocks), C::kThreads, C::kShared, stream>>>(a, maps, tpt, a.scale * 1.44269504088896340736f, vec32);
+  kernel<<<prompt_blocks(a, C::NQ * tpt), C::kThreads, C::kShared, stream>>>(a, maps, tpt, a.scale * 1.44269504088896340736f, vec32);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   return SV_OK;

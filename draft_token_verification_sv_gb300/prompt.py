@@ -16,7 +16,7 @@ import torch
 from . import _native as N
 from .kvcache import (_KEPT, _PER_SEQUENCE, _at, _call, _contiguous, _count, _empty, _int32, _meta, _new, _numel, _one_device,
                       _rows, _see, _stream_of)
-from .verify import _WORKSPACES, _code, workspace
+from .verify import _code
 
 
 def _token_rows(m, name):
@@ -100,14 +100,12 @@ def _prompt_plan(q, k, v, start, max_new, scale, window, sinks, out, status):
     _int32(status, "row_status", B, _PER_SEQUENCE)
     a = N.PromptAttentionDesc(B, heads, kv_heads, dim, _new(start, max_new, q, B), n, _code(q), dim ** -0.5 if scale is None else scale,
                               _count(window, "window"), _count(sinks, "sinks"), *q_strides, *k_strides, *v_strides, *out_strides)
-    return (ctypes.byref(a), N.lib().sv_prompt_attention_workspace_size(ctypes.byref(a)),
-            _one_device(q, k, v, start, out, status))
+    return ctypes.byref(a), _one_device(q, k, v, start, out, status)
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, new_start: torch.Tensor | None = None,
                      max_new: int | None = None, scale: float | None = None, window: int = 0, sinks: int = 0, lse: bool = False,
-                     out: torch.Tensor | None = None, row_status: torch.Tensor | None = None,
-                     ws: torch.Tensor | None = None, stream=None):
+                     out: torch.Tensor | None = None, row_status: torch.Tensor | None = None, stream=None):
     """Causal attention of whole prompts over their own keys and values; see
     sv_prompt_attention.
 
@@ -117,16 +115,9 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, new_s
     q, and with ``lse`` the log-sum-exp [..., heads] float32 as well."""
     if out is None:
         out = _empty(q.shape, q.dtype, q.device, stream)
-    a, need, gpu = _prompt_plan(_meta(q), _meta(k), _meta(v), _meta(new_start), None if max_new is None else int(max_new),
-                                None if scale is None else float(scale), int(window), int(sinks), _meta(out), _meta(row_status))
+    a, gpu = _prompt_plan(_meta(q), _meta(k), _meta(v), _meta(new_start), None if max_new is None else int(max_new),
+                          None if scale is None else float(scale), int(window), int(sinks), _meta(out), _meta(row_status))
     sums = _empty(q.shape[:-1], torch.float32, q.device, stream) if lse else None
-    raw = _stream_of(stream, gpu)
-    if ws is None:
-        ws = _WORKSPACES.get((gpu, raw))
-        if ws is None or ws.numel() < need:
-            ws = workspace(need, q.device, stream)
-    elif ws.get_device() != gpu or not ws.is_contiguous():
-        raise ValueError("ws must be a contiguous tensor on the GPU of the other tensors")
     _call(gpu, "sv_prompt_attention", a, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(new_start), out.data_ptr(), _at(sums),
-          _at(row_status), ws.data_ptr(), ws.numel(), raw)
+          _at(row_status), _stream_of(stream, gpu))
     return (out, sums) if lse else out

@@ -681,10 +681,6 @@ typedef struct sv_prompt_attention_desc {
   int64_t out_row_stride, out_head_stride;
 } sv_prompt_attention_desc;
 
-/* Workspace bytes for sv_prompt_attention (scratch on a 16-byte boundary, no
- * initialisation); 0 for an invalid descriptor. */
-size_t sv_prompt_attention_workspace_size(const sv_prompt_attention_desc* desc);
-
 /*
  * Causal attention of whole prompts over their own keys and values, before
  * these are rounded to 8 bits.  Sequences are packed: token i of sequence b
@@ -707,7 +703,7 @@ size_t sv_prompt_attention_workspace_size(const sv_prompt_attention_desc* desc);
  */
 sv_status sv_prompt_attention(const sv_prompt_attention_desc* desc, const void* q, const void* k, const void* v,
                               const int32_t* new_start, void* out, float* lse, int32_t* row_status,
-                              void* workspace, size_t workspace_bytes, sv_stream_t stream);
+                              sv_stream_t stream);
 
 /*
  * Profiling hooks (host-side; they add no device work).

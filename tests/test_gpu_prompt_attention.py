@@ -291,39 +291,20 @@ def test_the_same_call_gives_the_same_bits(sv, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("shift", [0, 16, 48])
-def test_any_workspace_on_a_16_byte_boundary(sv, dtype, shift):
-    import ctypes
-    import torch
-    from draft_token_verification_sv_gb300 import _native as N
-    g = np.random.default_rng(0)
-    q, k, v = (to_gpu(x, dtype)[None] for x in _inputs(g, dtype, 300, 4, 2, 80))
-    want = sv.prompt_attention(q, k, v)
-    a = N.PromptAttentionDesc(1, 4, 2, 80, 300, 300, N.SV_BF16 if dtype == "bf16" else N.SV_F32, 80 ** -0.5, 0, 0,
-                              320, 80, 160, 80, 160, 80, 320, 80)
-    need = N.lib().sv_prompt_attention_workspace_size(ctypes.byref(a))
-    whole = torch.full((need + 4096,), 0xa5, dtype=torch.uint8, device="cuda")
-    assert torch.equal(sv.prompt_attention(q, k, v, ws=whole[1024 + shift:1024 + shift + need]), want)
-    assert (whole[:1024 + shift] == 0xa5).all() and (whole[1024 + shift + need:] == 0xa5).all()
-    with pytest.raises(sv.SVError, match="workspace"):
-        sv.prompt_attention(q, k, v, ws=whole[1024:1024 + need - 1])
-
-
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_captured_and_replayed_beside_another_stream(sv, dtype):
     import torch
     g = np.random.default_rng(0)
     q, k, v = (to_gpu(x, dtype) for x in _inputs(g, dtype, 500, 8, 2, 64))
     start = to_gpu(np.array([0, 200, 500], np.int32))
     out = torch.empty_like(q)
-    side, ws = torch.cuda.Stream(), torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        sv.prompt_attention(q, k, v, new_start=start, max_new=500, out=out, ws=ws)
+        sv.prompt_attention(q, k, v, new_start=start, max_new=500, out=out)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
-            sv.prompt_attention(q, k, v, new_start=start, max_new=500, out=out, ws=ws)
+            sv.prompt_attention(q, k, v, new_start=start, max_new=500, out=out)
     for at in (1, 250, 499):
         start[1] = at
         q.mul_(-1.25)

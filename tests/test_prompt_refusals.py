@@ -189,10 +189,10 @@ def _prompt_desc(N, **kw):
     return d
 
 
-def _prompt(N, ptr=None, ws_bytes=1 << 30, **kw):
-    at = dict(q=A, k=A, v=A, start=None, out=A, lse=None, status=None, ws=A)
+def _prompt(N, ptr=None, **kw):
+    at = dict(q=A, k=A, v=A, start=None, out=A, lse=None, status=None)
     at.update(ptr or {})
-    return N.lib().sv_prompt_attention(ctypes.byref(_prompt_desc(N, **kw)), *(at[n] for n in at), ctypes.c_size_t(ws_bytes), None)
+    return N.lib().sv_prompt_attention(ctypes.byref(_prompt_desc(N, **kw)), *(at[n] for n in at), None)
 
 
 @pytest.mark.parametrize("field,value", [("batch", -1), ("batch", 65536), ("kv_heads", 0), ("kv_heads", 1025), ("kv_heads", 3), ("heads", 0),
@@ -202,11 +202,9 @@ def _prompt(N, ptr=None, ws_bytes=1 << 30, **kw):
                                          ("v_row_stride", 63), ("v_head_stride", 63), ("out_row_stride", 63), ("out_head_stride", 0)])
 def test_prompt_attention_refuses_descriptors(N, field, value):
     assert _prompt(N, **{field: value}) == N.SV_ERR_INVALID_ARGUMENT
-    if field != "total_new" or value < 0:
-        assert N.lib().sv_prompt_attention_workspace_size(ctypes.byref(_prompt_desc(N, **{field: value}))) == 0
 
 
-@pytest.mark.parametrize("name", ["q", "k", "v", "out", "ws"])
+@pytest.mark.parametrize("name", ["q", "k", "v", "out"])
 def test_prompt_attention_refuses_pointers(N, name):
     assert _prompt(N, {name: None}) == N.SV_ERR_INVALID_ARGUMENT
     assert _prompt(N, {name: ODD}) == N.SV_ERR_INVALID_ARGUMENT
@@ -217,11 +215,7 @@ def test_prompt_attention_refuses_words_off_their_boundary(N, name):
     assert _prompt(N, {name: ctypes.c_void_p(0x10000002)}) == N.SV_ERR_INVALID_ARGUMENT
 
 
-def test_prompt_attention_wants_its_workspace(N):
-    need = N.lib().sv_prompt_attention_workspace_size(ctypes.byref(_prompt_desc(N)))
-    assert need > 0
-    assert _prompt(N, ws_bytes=need - 1) == N.SV_ERR_WORKSPACE_TOO_SMALL
-    assert _prompt(N, {"ws": ctypes.c_void_p(0x10000008)}) == N.SV_ERR_INVALID_ARGUMENT
+def test_prompt_attention_without_sequences_and_with_too_many_rows(N):
     assert _prompt(N, batch=0, total_new=0) == N.SV_OK
     # rows times heads of a kv head pass 32 bits
     assert _prompt(N, {"start": A}, max_new=1 << 30, total_new=12) == N.SV_ERR_INVALID_ARGUMENT
@@ -229,7 +223,7 @@ def test_prompt_attention_wants_its_workspace(N):
 
 def _prompt_py(**kw):
     rows = lambda h, t=torch.float32: Stand((12, h, 64), t)
-    args = dict(q=rows(8), k=rows(2), v=rows(2), new_start=_ints(5), max_new=3, out=rows(8), ws=Stand((1 << 30,), torch.uint8))
+    args = dict(q=rows(8), k=rows(2), v=rows(2), new_start=_ints(5), max_new=3, out=rows(8))
     args.update(kw)
     return lambda: sv.prompt_attention(**args)
 
@@ -241,15 +235,13 @@ def _prompt_py(**kw):
     (dict(out=Stand((12, 8, 64), torch.bfloat16)), ValueError), (dict(window=2 ** 31), ValueError), (dict(sinks=-2 ** 31 - 1), ValueError),
     (dict(row_status=_ints(5)), ValueError), (dict(q=Stand((12, 8, 64), strides=(512, 1, 8))), ValueError),
     (dict(q=Stand((12, 8, 64), device="cuda:1"), out=Stand((12, 8, 64), device="cuda:1")), ValueError),
-    (dict(new_start=_ints(5, device="cpu")), ValueError), (dict(ws=Stand((1 << 30,), torch.uint8, device="cuda:1")), ValueError),
+    (dict(new_start=_ints(5, device="cpu")), ValueError),
     (dict(q=Stand((12, 8, 64), torch.float16), k=Stand((12, 2, 64), torch.float16), v=Stand((12, 2, 64), torch.float16),
           out=Stand((12, 8, 64), torch.float16)), TypeError),
     (dict(q=Stand((4, 3, 8, 64)), out=Stand((4, 3, 8, 64)), new_start=None, max_new=None), ValueError),
     (dict(q=Stand((4, 3, 8, 64)), k=Stand((4, 3, 2, 64)), v=Stand((4, 3, 2, 64)), out=Stand((4, 3, 8, 64)), new_start=None, max_new=4), ValueError),
 ], ids=lambda d: "-".join(d) if isinstance(d, dict) else "")
-def test_prompt_attention_refuses_tensors(N, bad, error, monkeypatch):
-    monkeypatch.setattr(sv.kvcache, "_raw_stream", lambda index: 0)
-    monkeypatch.setattr(sv.prompt, "_stream_of", lambda stream, device: 0)
+def test_prompt_attention_refuses_tensors(N, bad, error):
     with pytest.raises(error):
         _prompt_py(**bad)()
 
@@ -259,8 +251,7 @@ def test_prompt_attention_refuses_tensors(N, bad, error, monkeypatch):
 CALLS = {
     "assign": lambda **kw: sv.kv_assign(_pool(), _ints(4, 5), _ints(4), _ints(4), 16, max_new=3, **kw),
     "rope": lambda **kw: sv.rope(Stand((7, 4, 64)), Stand((7, 2, 64)), _ints(7), Stand((32,)), **kw),
-    "prompt": lambda **kw: sv.prompt_attention(Stand((4, 3, 8, 64)), Stand((4, 3, 2, 64)), Stand((4, 3, 2, 64)), lse=True,
-                                               ws=Stand((1 << 30,), torch.uint8), **kw),
+    "prompt": lambda **kw: sv.prompt_attention(Stand((4, 3, 8, 64)), Stand((4, 3, 2, 64)), Stand((4, 3, 2, 64)), lse=True, **kw),
 }
 
 
@@ -268,10 +259,8 @@ CALLS = {
 def test_results_belong_to_the_stream_they_are_made_on(N, call, fake_streams):  # noqa: F811
     Fake, made = fake_streams
     CALLS[call](stream=Fake("side"))
-    sv.prompt._prompt_plan.cache_clear()  # (it kept a size that the stand-in of the library gave)
     assert made == [("side", ["main"])] * 2
     other = Fake("other")
     other.device_index = 1
     with pytest.raises(ValueError, match="another GPU"):
         CALLS[call](stream=other)
-    sv.prompt._prompt_plan.cache_clear()
