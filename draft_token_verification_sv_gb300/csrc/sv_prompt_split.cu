@@ -37,7 +37,7 @@ template <int DP, typename E> struct Config {
   static constexpr int kParts = sizeof(E) == 4 ? 3 : 1;           // bf16 values that make a value
   static constexpr bool kStream = DP == 256 && kParts == 3;       // queries come with each tile of keys
   static constexpr int kScoreDims = kStream ? 64 : DP < 128 ? DP : 128, kScoreUnits = DP / kScoreDims;  // dims of a unit of a tile of keys
-  static constexpr int kValueDims = DP < 128 ? DP : 128, kValueUnits = DP / kValueDims;                 // and of values
+  static constexpr int kValueDims = kStream || DP < 128 ? 64 : 128, kValueUnits = DP / kValueDims;      // and of values
   static constexpr int kQueryPart = kRows * (kStream ? kScoreDims : DP) * 2;  // bytes of one part of a tile of queries (of a unit's)
   static constexpr int kKeyPart = kKeys * kScoreDims * 2, kValuePart = kKeys * kValueDims * 2;
   static constexpr int kKeyAt = kStream ? kParts * kQueryPart : 0;  // of the keys in a stage
@@ -48,14 +48,15 @@ template <int DP, typename E> struct Config {
   static constexpr int kBytes = kQueryBytes + kStages * kStageBytes;
   // more than half of an SM's shared memory keeps it to one block
   static constexpr int kShared = (kBytes > 118 * 1024 ? kBytes : 118 * 1024) + 1024;
-  // tensor memory, in columns: two places for scores and the weights they become, then O
-  static constexpr int kPlace = 128, kO = 2 * kPlace;
+  // tensor memory, in columns: two places for scores and the weights they become, O, and the sums of a unit of values
+  static constexpr int kPlace = kParts == 1 ? 64 : DP == 256 ? 96 : 128, kO = 2 * kPlace, kSums = kO + DP;
+  static_assert(kPlace >= kParts * (kKeys / 2) && kPlace >= kKeys && kSums + kValueDims <= 512, "tensor memory");
 };
 
 struct Shared {
   uint64_t item_full[kItems], item_free[kItems];
   uint64_t q_full, q_free, full[6], free[6];
-  uint64_t s_full[2], p_ready[2], pv_done, o_free, last, answer;
+  uint64_t s_full[2], p_ready[2], sums_full, sums_free, last, answer;
   uint4 block;
   Item item[kItems];
   Sequences sequences;
@@ -320,7 +321,7 @@ __device__ bool product_role(Shared& sh, uint32_t q_at, uint32_t stages, uint32_
     return ok;
   };
   const auto arrive = [&](uint64_t& bar) { tc::products_arrive(tc::smem_address(&bar)); };
-  int unit = 0, tile = 0;
+  int unit = 0, tile = 0, sums = 0;
   for (int items = 0;; ++items) {
     if (!wait(sh.item_full[items % kItems], items / kItems)) return false;
     const int tiles = sh.item[items % kItems].tiles;
@@ -353,22 +354,22 @@ __device__ bool product_role(Shared& sh, uint32_t q_at, uint32_t stages, uint32_
         if (!score(tile + 1 & 1)) return false;
         if (!C::kStream && t + 2 == tiles) arrive(sh.q_free);
       }
-      if (t == 0 && items > 0 && !wait(sh.o_free, items - 1)) return false;
       if (!wait(sh.p_ready[tile & 1], tile >> 1)) return false;
-      for (int u = 0; u < C::kValueUnits; ++u, ++unit) {
+      for (int u = 0; u < C::kValueUnits; ++u, ++unit, ++sums) {
         const int stage = unit % C::kStages;
         if (!wait(sh.full[stage], unit / C::kStages)) return false;
+        if (sums > 0 && !wait(sh.sums_free, sums - 1)) return false;
         const uint32_t v = stages + stage * C::kStageBytes;
 #pragma unroll
         for (int n = 0; n < kProducts; ++n)
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            tc::product_f16(tmem + C::kO + u * C::kValueDims, tmem + (tile & 1) * C::kPlace + left_part<C::kParts>(n) * (kKeys / 2) + k * 8,
+            tc::product_f16(tmem + C::kSums, tmem + (tile & 1) * C::kPlace + left_part<C::kParts>(n) * (kKeys / 2) + k * 8,
                             tc::tile_descriptor(v + right_part<C::kParts>(n) * C::kValuePart + k * 2048, kKeys * 128, 1024), kValues,
-                            t > 0 || n > 0 || k > 0);
+                            n > 0 || k > 0);
         arrive(sh.free[stage]);
+        arrive(sh.sums_full);
       }
-      arrive(sh.pv_done);
     }
   }
 }
@@ -418,7 +419,35 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
     tc::fence_after();
     return ok;
   };
-  int tile = 0;
+  int tile = 0, sums = 0;
+  // O = O fix + the sums of the next tile: these are formed by themselves, since what the products add to is cut off, not rounded,
+  // each time (over 2048 tokens that came to 6e-6 of the result; here it is 2e-7).
+  const auto gather = [&](bool first, float fix) {
+    for (int u = 0; u < C::kValueUnits; ++u, ++sums) {
+      if (!wait(sh.sums_full, sums)) return false;
+#pragma unroll 1
+      for (int d = 0; d < C::kValueDims; d += 32) {
+        uint32_t y[32], o[2][16];
+        tc::tmem_load32(mine + C::kSums + d, y);
+        if (!first) {
+          tc::tmem_load16(own_o + u * C::kValueDims + d, o[0]);
+          tc::tmem_load16(own_o + u * C::kValueDims + d + 16, o[1]);
+          tc::wait_loads(o[0]);
+          tc::wait_loads(o[1]);
+        }
+        tc::wait_loads(y);
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          o[k >> 4][k & 15] = first ? y[k] : __float_as_uint(fmaf(__uint_as_float(o[k >> 4][k & 15]), fix, __uint_as_float(y[k])));
+        tc::tmem_store(own_o + u * C::kValueDims + d, o[0]);
+        tc::tmem_store(own_o + u * C::kValueDims + d + 16, o[1]);
+      }
+      tc::wait_stores();
+      tc::fence_before();
+      warp_arrive(sh.sums_free);
+    }
+    return true;
+  };
   for (int items = 0;; ++items) {
     if (!wait(sh.item_full[items % kItems], items / kItems)) return false;
     const Item& it = sh.item[items % kItems];
@@ -427,7 +456,7 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
     const Place at = place_of(a, it, tpt, 0, r);
     const int token = at.token;
     const bool held = at.row >= 0;
-    float m = held ? -CUDART_INF_F : 0.0f, l = 0.0f;
+    float m = held ? -CUDART_INF_F : 0.0f, l = 0.0f, fix = 1.0f, fix_before = 1.0f;  // fix: of what was summed before this tile
     for (int t = 0; t < tiles; ++t, ++tile) {
       const int s = tile & 1, kb = key_of<kKeys>(it, t);
       const uint32_t scores = mine + s * C::kPlace;
@@ -451,23 +480,11 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int k = 0; k < 32; ++k) top = fmaxf(top, seen[c] >> k & 1u ? __uint_as_float(x[c][k]) * f : -CUDART_INF_F);
-          float fix = 1.0f;
           if (raise && top > -CUDART_INF_F) {
-            fix = m == -CUDART_INF_F ? 1.0f : ex2(m - top);
+            const float down = m == -CUDART_INF_F ? 1.0f : ex2(m - top);
             m = top;
-            l *= fix;
-          }
-          if (t > 0 && __any_sync(0xffffffffu, fix != 1.0f)) {
-            if (!wait(sh.pv_done, tile - 1)) return false;
-            uint32_t o[16];
-#pragma unroll 1
-            for (int d = 0; d < DP; d += 16) {
-              tc::tmem_load16(own_o + d, o);
-              tc::wait_loads(o);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
-              tc::tmem_store(own_o + d, o);
-            }
+            l *= down;
+            fix *= down;
           }
         }
         const float base = m == -CUDART_INF_F ? 0.0f : m;
@@ -485,12 +502,13 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
         }
       }
       tc::wait_stores();
-      // (a barrier is never two phases ahead)
-      if (t > 0 && !wait(sh.pv_done, tile - 1)) return false;
       tc::fence_before();
       warp_arrive(sh.p_ready[s]);
+      if (t > 0 && !gather(t == 1, fix_before)) return false;
+      fix_before = fix;
+      fix = 1.0f;
     }
-    if (!wait(sh.pv_done, tile - 1)) return false;
+    if (!gather(tiles == 1, fix_before)) return false;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     E* out = static_cast<E*>(a.out) + at.row * a.out_row + at.head * a.out_head;
     const bool dirty = *const_cast<const volatile int*>(&it.dirty) != 0;
@@ -519,8 +537,6 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
       }
       __syncwarp();
     }
-    tc::fence_before();
-    warp_arrive(sh.o_free);
     if (held && a.lse) a.lse[at.row * a.heads + at.head] = (m + log2f(l)) * 0.69314718055994530942f;
     __syncwarp();
     if ((threadIdx.x & 31) == 0) sh.finished[quarter] = items + 1;
@@ -557,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_split_kernel(const __grid_
     }
     tc::barrier_init(tc::smem_address(&sh.q_full), kLoadWarps);
     tc::barrier_init(tc::smem_address(&sh.q_free), 1);
-    tc::barrier_init(tc::smem_address(&sh.pv_done), 1);
-    tc::barrier_init(tc::smem_address(&sh.o_free), kSoftmaxWarps);
+    tc::barrier_init(tc::smem_address(&sh.sums_full), 1);
+    tc::barrier_init(tc::smem_address(&sh.sums_free), kSoftmaxWarps);
     tc::barrier_init(tc::smem_address(&sh.last), 1);
     tc::barrier_init(tc::smem_address(&sh.answer), 1);
     tc::publish_shared();
