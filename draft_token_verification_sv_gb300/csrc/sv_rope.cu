@@ -24,12 +24,23 @@ struct RopeView {
 
 // Radians a position as turns in units of 2^-64, modulo whole turns: a
 // position's multiple of it wraps around where the angle does, so the angle
-// of a far position loses nothing to its size.  1 / (2 pi) is the sum of two
-// doubles and the products are exact to 2^-64 turns, 2^-33 after 2^31 positions.
+// of a far position loses nothing to its size.  A float is m 2^e, so this is
+// m times the bits of 1 / (2 pi), moved by e: off by 2^-64 turns, 2^-33 after
+// 2^31 positions.  (Doubles would do, but eight of them for each thread took
+// longer than the rest of 12,000 tokens of 32 heads: 72 us, now XX.)
 __device__ __forceinline__ unsigned long long turns(float inv_freq) {
-  const double f = inv_freq, high = f * 0.15915494309189535;
-  const double low = fma(f, -9.839338337591243e-18, fma(f, 0.15915494309189535, -high));
-  return static_cast<unsigned long long>(__double2ll_rn((high - rint(high)) * 0x1p64)) + static_cast<unsigned long long>(__double2ll_rn(low * 0x1p64));
+  constexpr unsigned long long kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f47d4d3770ull;  // 2^128 / (2 pi)
+  const uint32_t u = __float_as_uint(inv_freq), raised = u >> 23 & 0xffu;
+  const uint32_t m = (u & 0x7fffffu) | (raised ? 0x800000u : 0u);
+  const int down = 64 + 150 - static_cast<int>(raised ? raised : 1u);  // bits that the product moves down by
+  const unsigned __int128 low = static_cast<unsigned __int128>(m) * kLow;
+  const unsigned __int128 high = static_cast<unsigned __int128>(m) * kHigh + static_cast<unsigned long long>(low >> 64);
+  unsigned long long t = 0;
+  if (down >= 64)
+    t = down < 192 ? static_cast<unsigned long long>(high >> (down - 64)) : 0ull;
+  else if (down > 0)
+    t = static_cast<unsigned long long>(high) << (64 - down) | static_cast<unsigned long long>(low) >> down;
+  return u >> 31 ? 0ull - t : t;
 }
 
 // Cosine and sine of an angle in units of 2^-64 turns: the nearest quarter
@@ -51,21 +62,23 @@ __device__ __forceinline__ float value_of(const uint16_t* p) { return __uint_as_
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = static_cast<uint16_t>(floats_to_bf16x2(v, 0.0f)); }
 
-// A block a token, a thread a pair (or one of the dims that stay).
-constexpr int kThreads = 128;
+__device__ __forceinline__ int64_t angle_position(const RopeView& w, int pair, int row) {
+  return __ldg(w.positions + w.axis[pair] * w.position_stride + row);
+}
+
+// Rows on any boundary, and parts of a head that are no multiple of 16 dims: a block a token, a thread a pair (or one of the
+// dims that stay).
+constexpr int kPairThreads = 128;
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeView w) {
+__global__ void __launch_bounds__(kPairThreads) rope_pairs_kernel(const __grid_constant__ RopeView w) {
   const int row = blockIdx.x;
   if (!sv_in(row, w.rows)) return;
-  for (int u = threadIdx.x; u < w.dim - w.half; u += kThreads) {
+  for (int u = threadIdx.x; u < w.dim - w.half; u += kPairThreads) {
     const bool pair = u < w.half;
     const int i = !pair ? u + w.half : w.adjacent ? 2 * u : u, j = w.adjacent ? 2 * u + 1 : u + w.half;
     float2 t = make_float2(1.0f, 0.0f);
-    if (pair) {
-      const long long position = __ldg(w.positions + w.axis[u] * w.position_stride + row);
-      t = cos_sin(static_cast<unsigned long long>(position) * turns(__ldg(w.inv_freq + u)));
-    }
+    if (pair) t = cos_sin(static_cast<unsigned long long>(angle_position(w, u, row)) * turns(__ldg(w.inv_freq + u)));
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const E* x = static_cast<const E*>(w.side[s].x) + row * w.side[s].x_row;
@@ -81,6 +94,135 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeView w) {
       }
     }
   }
+}
+
+// ---- rows on 16-byte boundaries ----
+
+// (not by the read-only path: a call may work in place)
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
+template <typename E> __device__ __forceinline__ uint4 pack(const float* x);
+template <> __device__ __forceinline__ uint4 pack<float>(const float* x) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+template <> __device__ __forceinline__ uint4 pack<uint16_t>(const float* x) {
+  return make_uint4(floats_to_bf16x2(x[0], x[1]), floats_to_bf16x2(x[2], x[3]), floats_to_bf16x2(x[4], x[5]), floats_to_bf16x2(x[6], x[7]));
+}
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+// A thread has eight pairs of a head, whose sines and cosines it uses for every head that it takes of a token: the units of 16
+// values of a head lie side by side in a warp, and as many heads as fit.  `split` warps share a token.
+template <typename E, bool ADJACENT>
+__global__ void __launch_bounds__(kThreads) rope_units_kernel(const __grid_constant__ RopeView w, int split) {
+  constexpr int kVec = Elem<E>::kPerVec, kVecs = 16 / kVec, kHeads = sizeof(E) == 2 ? 4 : 2;  // heads under way
+  const int units = w.dim >> 4, per = 32 / units;
+  const int lane = threadIdx.x & 31, unit = lane % units, sub = lane / units;
+  const int warp = threadIdx.x >> 5, part = warp % split, first = warp / split;
+  const bool turned = unit < w.half >> 3, busy = sub < per;
+  unsigned long long by[8];
+  uint32_t axes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    by[i] = 0;
+    if (turned) {
+      by[i] = turns(__ldg(w.inv_freq + 8 * unit + i));
+      axes |= static_cast<uint32_t>(w.axis[8 * unit + i]) << (2 * i);
+    }
+  }
+  // where the thread's vectors lie in a head
+  int at[kVecs];
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v)
+    at[v] = ADJACENT || !turned ? 16 * unit + v * kVec : 8 * unit + (v % (kVecs / 2)) * kVec + (v >= kVecs / 2 ? w.half : 0);
+  const int all = w.heads[0] + w.heads[1], step = split * per;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kWarps / split) + first; row < w.rows; row += static_cast<int64_t>(gridDim.x) * (kWarps / split)) {
+    if (!sv_in(row, w.rows)) break;
+    float2 t[8];
+    const int32_t* p = w.positions + row;
+    if (w.axes == 1) {
+      const long long position = __ldg(p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = cos_sin(static_cast<unsigned long long>(position) * by[i]);
+    } else {
+      int position[SV_MAX_ROPE_AXES];
+#pragma unroll
+      for (int n = 0; n < SV_MAX_ROPE_AXES; ++n) position[n] = n < w.axes ? __ldg(p + n * w.position_stride) : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t n = axes >> (2 * i) & 3u;
+        const long long mine = n & 2 ? (n & 1 ? position[3] : position[2]) : (n & 1 ? position[1] : position[0]);
+        t[i] = cos_sin(static_cast<unsigned long long>(mine) * by[i]);
+      }
+    }
+    if (!busy) continue;
+    for (int h0 = part * per + sub; h0 < all; h0 += kHeads * step) {
+      uint4 raw[kHeads][kVecs];
+#pragma unroll
+      for (int n = 0; n < kHeads; ++n) {
+        const int h = h0 + n * step;
+        if (h >= all) break;
+        const int s = h >= w.heads[0];
+        const E* x = static_cast<const E*>(w.side[s].x) + row * w.side[s].x_row + (h - (s ? w.heads[0] : 0)) * w.side[s].x_head;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) raw[n][v] = load16(x + at[v]);
+      }
+#pragma unroll
+      for (int n = 0; n < kHeads; ++n) {
+        const int h = h0 + n * step;
+        if (h >= all) break;
+        const int s = h >= w.heads[0];
+        E* y = static_cast<E*>(w.side[s].y) + row * w.side[s].y_row + (h - (s ? w.heads[0] : 0)) * w.side[s].y_head;
+        if (turned) {
+          float x[16];
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v) unpack<E>(raw[n][v], x + v * kVec);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float& a = x[ADJACENT ? 2 * i : i];
+            float& b = x[ADJACENT ? 2 * i + 1 : i + 8];
+            const float u = a * t[i].x - b * t[i].y, z = a * t[i].y + b * t[i].x;
+            a = u;
+            b = z;
+          }
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v) raw[n][v] = pack<E>(x + v * kVec);
+        }
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) *reinterpret_cast<uint4*>(y + at[v]) = raw[n][v];
+      }
+    }
+  }
+}
+
+template <typename E>
+bool whole_vectors(const RopeView& w) {
+  if (w.half % 8) return false;
+  uintptr_t all = 0;
+  for (int s = 0; s < (w.heads[1] ? 2 : 1); ++s) {
+    const RopeSide& r = w.side[s];
+    all |= reinterpret_cast<uintptr_t>(r.x) | reinterpret_cast<uintptr_t>(r.y) | static_cast<uintptr_t>(r.x_row | r.x_head | r.y_row | r.y_head) * sizeof(E);
+  }
+  return all % 16 == 0;
+}
+
+template <typename E>
+void launch(const RopeView& w, cudaStream_t stream) {
+  if (!whole_vectors<E>(w)) {
+    rope_pairs_kernel<E><<<w.rows, kPairThreads, 0, stream>>>(w);
+    return;
+  }
+  const int split = w.rows >= 152 * 16 ? 1 : w.rows >= 152 * 4 ? 2 : 8;
+  const int64_t blocks = (static_cast<int64_t>(w.rows) * split + kWarps - 1) / kWarps;
+  const unsigned grid = static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8);
+  if (w.adjacent)
+    rope_units_kernel<E, true><<<grid, kThreads, 0, stream>>>(w, split);
+  else
+    rope_units_kernel<E, false><<<grid, kThreads, 0, stream>>>(w, split);
 }
 
 }  // namespace
@@ -103,9 +245,9 @@ sv_status rope(const sv_rope_desc& d, const void* q, const void* k, const int32_
   w.inv_freq = inv_freq;
   for (int i = 0; i < w.half; ++i) w.axis[i] = d.axis[i];
   if (d.dtype == SV_BF16)
-    rope_kernel<uint16_t><<<d.rows, kThreads, 0, stream>>>(w);
+    launch<uint16_t>(w, stream);
   else
-    rope_kernel<float><<<d.rows, kThreads, 0, stream>>>(w);
+    launch<float>(w, stream);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   return SV_OK;
