@@ -24,27 +24,35 @@ struct Item {
   int dirty;             // values that are not finite were taken out
 };
 
-// Sequences where they are few: their rows, and the longest first.
-constexpr int kSorted = 128;
+// Sequences where they are few: the longest first, their rows, and the items up to and with each.
+constexpr int kSorted = 96;
 struct Sequences {
-  int n[kSorted], row0[kSorted];
-  uint8_t order[kSorted];
+  int n[kSorted], row0[kSorted], items[kSorted];
 };
 
-// By all threads of the block; the order is complete behind its next barrier.
-__device__ __forceinline__ void sort_sequences(const PromptView& a, Sequences& sq, int threads) {
+// By all threads of the block, of `per` tokens to an item; complete behind its next barrier.
+__device__ __forceinline__ void sort_sequences(const PromptView& a, Sequences& sq, int per, int threads) {
   if (a.batch > kSorted) return;
-  for (int b = threadIdx.x; b < a.batch; b += threads) {
-    const PromptSpan s = prompt_span(a, b);
-    sq.n[b] = s.n;
-    sq.row0[b] = s.row0;
+  for (int b = threadIdx.x; b < a.batch; b += threads) sq.items[b] = prompt_span(a, b).n;
+  __syncthreads();
+  int rank = -1, before = 0;
+  PromptSpan s{};
+  for (int b = threadIdx.x; b < a.batch; b += threads) {  // (a thread has one at most: no block is smaller than kSorted)
+    s = prompt_span(a, b);
+    rank = 0;
+    for (int o = 0; o < a.batch; ++o) {
+      const int n = sq.items[o];
+      if (n > s.n || (n == s.n && o <= b)) {
+        rank += o != b;
+        before += (n + per - 1) / per * a.kv_heads;
+      }
+    }
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < a.batch; b += threads) {
-    const int n = sq.n[b];
-    int rank = 0;
-    for (int o = 0; o < a.batch; ++o) rank += sq.n[o] > n || (sq.n[o] == n && o < b);
-    sq.order[rank] = static_cast<uint8_t>(b);
+  if (rank >= 0) {
+    sq.n[rank] = s.n;
+    sq.row0[rank] = s.row0;
+    sq.items[rank] = before;
   }
 }
 
@@ -91,23 +99,51 @@ struct Finder {
 
   template <int KEYS, int NQ>
   __device__ __forceinline__ bool find(const PromptView& a, const Sequences& sq, int tpt, long long index, Item& it) {
-    const int lane = threadIdx.x & 31, per = NQ * tpt;
+    const int per = NQ * tpt;
+    int local;  // the item's number among its sequence's
+    if (a.batch <= kSorted) {
+      if (!find_sorted(a, sq, index, it, local)) return false;
+    } else if (!find_any(a, per, index, it, local)) {
+      return false;
+    }
+    const int group = local / a.kv_heads;
+    it.h = local - group * a.kv_heads;
+    it.tok0 = ((it.n - 1) / per - group) * per;
+    const int from = a.window ? max(0, it.tok0 - a.window + 1) : 0;
+    it.window = from / KEYS;
+    it.first = a.window ? min(it.window, a.sinks / KEYS + (a.sinks % KEYS != 0)) : 0;
+    it.tiles = 0;
+    it.dirty = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int first = it.tok0 + i * tpt, last = min(it.n, first + tpt) - 1;
+      it.count[i] = i < NQ && first < it.n ? it.first + last / KEYS - it.window + 1 : 0;
+      it.tiles = max(it.tiles, it.count[i]);
+    }
+    return true;
+  }
+
+  __device__ __forceinline__ bool find_sorted(const PromptView& a, const Sequences& sq, long long index, Item& it, int& local) {
+    for (int base = 0; base < a.batch; base += 32) {
+      const int o = base + (threadIdx.x & 31);
+      const unsigned past = __ballot_sync(0xffffffffu, o < a.batch && sq.items[o] > index);
+      if (past == 0) continue;
+      const int who = base + __ffs(past) - 1;
+      it.n = sq.n[who];
+      it.row0 = sq.row0[who];
+      local = static_cast<int>(index) - (who > 0 ? sq.items[who - 1] : 0);
+      return true;
+    }
+    return false;
+  }
+
+  __device__ __forceinline__ bool find_any(const PromptView& a, int per, long long index, Item& it, int& local) {
+    const int lane = threadIdx.x & 31;
     if (index < before) at = 0, before = 0;
     for (; at < a.batch;) {
-      int n = 0, row0 = 0;
-      if (at + lane < a.batch) {
-        if (a.batch <= kSorted) {
-          const int b = sq.order[at + lane];
-          n = sq.n[b];
-          row0 = sq.row0[b];
-        } else {
-          const PromptSpan s = prompt_span(a, at + lane);
-          n = s.n;
-          row0 = s.row0;
-        }
-      }
-      const int groups = (n + per - 1) / per;
-      long long upto = static_cast<long long>(groups) * a.kv_heads;
+      const PromptSpan s = at + lane < a.batch ? prompt_span(a, at + lane) : PromptSpan{0, 0, false};
+      const long long own = static_cast<long long>((s.n + per - 1) / per) * a.kv_heads;
+      long long upto = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long up = __shfl_up_sync(0xffffffffu, upto, o);
@@ -120,23 +156,9 @@ struct Finder {
         continue;
       }
       const int who = __ffs(past) - 1;
-      const long long begin = before + __shfl_sync(0xffffffffu, upto, who) - static_cast<long long>(__shfl_sync(0xffffffffu, groups, who)) * a.kv_heads;
-      it.n = __shfl_sync(0xffffffffu, n, who);
-      it.row0 = __shfl_sync(0xffffffffu, row0, who);
-      const int local = static_cast<int>(index - begin);
-      it.h = local % a.kv_heads;
-      it.tok0 = (__shfl_sync(0xffffffffu, groups, who) - 1 - local / a.kv_heads) * per;
-      const int from = a.window ? max(0, it.tok0 - a.window + 1) : 0;
-      it.window = from / KEYS;
-      it.first = a.window ? min(it.window, a.sinks / KEYS + (a.sinks % KEYS != 0)) : 0;
-      it.tiles = 0;
-      it.dirty = 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int first = it.tok0 + i * tpt, last = min(it.n, first + tpt) - 1;
-        it.count[i] = i < NQ && first < it.n ? it.first + last / KEYS - it.window + 1 : 0;
-        it.tiles = max(it.tiles, it.count[i]);
-      }
+      it.n = __shfl_sync(0xffffffffu, s.n, who);
+      it.row0 = __shfl_sync(0xffffffffu, s.row0, who);
+      local = static_cast<int>(index - before - __shfl_sync(0xffffffffu, upto - own, who));
       return true;
     }
     return false;

@@ -397,15 +397,15 @@ __device__ __forceinline__ float weights32(const uint32_t (&x)[32], uint32_t see
 
 // What the row sees of values that are not finite and were left out.
 template <typename E>
-__device__ __noinline__ void add_rest(const PromptView& a, const Item& it, int token, int d, float (&x)[16]) {
+__device__ __noinline__ float rest_of(const PromptView& a, const Item& it, int token, int d) {
   const E* v = static_cast<const E*>(a.v) + static_cast<int64_t>(it.row0) * a.v_row + it.h * a.v_head;
+  float sum = 0.0f;
   for (int j = 0; j <= token && sv_in(it.row0 + static_cast<int64_t>(j), a.total_new); ++j) {
     if (a.window != 0 && token - j >= a.window && j >= a.sinks) continue;
-    for (int k = 0; k < 16 && d + k < a.dim; ++k) {
-      const float y = value_of(v + j * a.v_row + d + k);
-      if (!(fabsf(y) < CUDART_INF_F)) x[k] += y;
-    }
+    const float y = value_of(v + j * a.v_row + d);
+    if (!(fabsf(y) < CUDART_INF_F)) sum += y;
   }
+  return sum;
 }
 
 template <int DP, typename E>
@@ -521,7 +521,9 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
         float x[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]) * inv;
-        if (dirty) add_rest<E>(a, it, token, d, x);
+        if (__builtin_expect(dirty, 0))
+#pragma unroll
+          for (int k = 0; k < 16; ++k) x[k] += rest_of<E>(a, it, token, d + k);
         if (out_vec32) {
 #pragma unroll
           for (int h = 0; h < static_cast<int>(sizeof(E)) / 2; ++h) {
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_split_kernel(const __grid_
     tc::publish_shared();
   }
   if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), 512);
-  sort_sequences(a, sh.sequences, kThreads);
+  sort_sequences(a, sh.sequences, tpt, kThreads);
   if (blockIdx.x == 0) flag_lengths(a, kThreads);
   tc::fence_before();
   __syncthreads();

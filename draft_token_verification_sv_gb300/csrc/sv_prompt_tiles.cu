@@ -11,7 +11,7 @@
 //   four for each 128 rows turn scores into weights, a row a thread.
 // Weights are exp2(s - m) with m the row's largest score of the first tile
 // that it sees: bf16 weights have float's range, so m moves (and O is scaled
-// anew) only when a later tile's weights sum to 2^13 and more, and what a
+// anew) only where a later tile's weights sum to more than 2^13, and what a
 // weight loses by a small m is nothing.  Weights are rounded to bf16 (2^-8),
 // the type that the products ask for beside bf16 values; their sum is taken
 // before that, in fp32.
@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kKeys = 128;   // of a tile of keys
 constexpr int kItems = 4;    // items that may be known ahead
-constexpr float kLargeSum = 8192.0f;
+constexpr float kLargeSum = 8192.0f, kLargeLog = 13.0f;
 
 template <int DP> struct Config {
   static constexpr int NQ = DP == 256 ? 1 : 2;           // tiles of queries
@@ -339,31 +339,33 @@ __device__ __forceinline__ float weights32(const uint32_t (&x)[32], uint32_t see
   return s.x + s.y;
 }
 
-template <bool MASKED>
 __device__ __forceinline__ float largest32(const uint32_t (&x)[32], uint32_t seen, float f) {
   float v[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-  for (int k = 0; k < 32; ++k) v[k & 3] = fmaxf(v[k & 3], MASKED && !(seen >> k & 1u) ? -CUDART_INF_F : __uint_as_float(x[k]) * f);
+  for (int k = 0; k < 32; ++k) v[k & 3] = fmaxf(v[k & 3], seen >> k & 1u ? __uint_as_float(x[k]) * f : -CUDART_INF_F);
   return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
 }
 
-// What the row sees of values that are not finite and were left out.
-__device__ __noinline__ void add_rest(const PromptView& a, const Item& it, int tpt, int token, int d, float (&x)[16]) {
+// Adds to a row's results what it sees of values that are not finite and were left out.
+__device__ __noinline__ void add_rest(const PromptView& a, const Item& it, int tpt, int token, uint16_t* out) {
   const uint16_t* v = static_cast<const uint16_t*>(a.v) + static_cast<int64_t>(it.row0) * a.v_row + it.h * a.v_head;
-  for (int t = 0; t < it.tiles; ++t) {
-    const int kb = key_of<kKeys>(it, t);
-    if (!partly_seen<kKeys, 2>(a, it, tpt, t)) continue;
-    for (int j = kb; j < kb + kKeys && j <= token; ++j) {
-      if (a.window != 0 && token - j >= a.window && j >= a.sinks) continue;
-      if (!sv_in(it.row0 + static_cast<int64_t>(j), a.total_new)) break;
-      for (int k = 0; k < 16 && d + k < a.dim; ++k) {
-        const float y = __uint_as_float(static_cast<uint32_t>(__ldg(v + j * a.v_row + d + k)) << 16);
-        if (!(fabsf(y) < CUDART_INF_F)) x[k] += y;
+  for (int d = 0; d < a.dim; ++d) {
+    float sum = 0.0f;
+    for (int t = 0; t < it.tiles; ++t) {
+      const int kb = key_of<kKeys>(it, t);
+      if (!partly_seen<kKeys, 2>(a, it, tpt, t)) continue;
+      for (int j = kb; j < kb + kKeys && j <= token; ++j) {
+        if (a.window != 0 && token - j >= a.window && j >= a.sinks) continue;
+        if (!sv_in(it.row0 + static_cast<int64_t>(j), a.total_new)) break;
+        const float y = value_of(v + j * a.v_row + d);
+        if (!(fabsf(y) < CUDART_INF_F)) sum += y;
       }
     }
+    if (sum != 0.0f) put_value(out + d, __uint_as_float(static_cast<uint32_t>(out[d]) << 16) + sum);
   }
 }
 
+// (What runs once an item, or for a few of its tiles, is kept short: its instructions are fetched anew each time.)
 template <int DP>
 __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, uint32_t tmem, bool out_vec32) {
   using C = Config<DP>;
@@ -385,116 +387,110 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
       const Place at = place_of(a, it, tpt, i, r);
       const int token = at.token;
       const bool held = at.row >= 0;
-      float m = held ? -CUDART_INF_F : 0.0f, l = 0.0f;  // the largest score of the first tile seen (base 2), the sum of weights
+      const int from = a.window ? max(0, token - a.window + 1) : 0, sinks = a.window ? min(a.sinks, token + 1) : 0;
+      float m = held ? -CUDART_INF_F : 0.0f, l = 0.0f;  // what scores are taken from (base 2), the sum of weights
+#pragma unroll 1
       for (int t = 0; t < count; ++t, ++tile) {
         const int s = C::NQ == 2 ? i : tile & 1, uses = C::NQ == 2 ? tile : tile >> 1;
         const int kb = key_of<kKeys>(it, t);
         const uint32_t scores = mine + C::kS + s * kKeys;
+        bool slow = !whole<kKeys>(a, it, tpt, i, kb) || __any_sync(0xffffffffu, m == -CUDART_INF_F);
         if (!wait(sh.s_full[s], uses)) return false;
-        const auto turn = [&](auto masked) {
-          constexpr bool M = decltype(masked)::value;
-          uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-          if (M) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              seen[c] = bits32(kb + 32 * c, a.window ? max(0, token - a.window + 1) : 0, token + 1);
-              if (a.window) seen[c] |= bits32(kb + 32 * c, 0, min(a.sinks, token + 1));
-            }
-          }
-          uint32_t x[4][32], w[16];
-          bool raise = held && m == -CUDART_INF_F;
-          bool any = __any_sync(0xffffffffu, raise);
+        if (!slow) {
+          uint32_t x[2][32], w[4][16];
+          float sum = 0.0f;
           tc::tmem_load32(scores, x[0]);
-          if (any) {
 #pragma unroll
-            for (int c = 1; c < 4; ++c) tc::tmem_load32(scores + 32 * c, x[c]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tc::wait_loads(x[c]);
-          } else {
-            float sum = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tc::wait_loads(x[c]);
-              if (c < 3) tc::tmem_load32(scores + 32 * (c + 1), x[c + 1]);
-              sum += weights32<M>(x[c], seen[c], f, -m, w);
-              tc::tmem_store(scores + 16 * c, w);
-            }
-            raise = held && sum > kLargeSum;
-            any = __any_sync(0xffffffffu, raise);
-            if (!any) l += sum;
+          for (int c = 0; c < 4; ++c) {
+            tc::wait_loads(x[c & 1]);
+            if (c < 3) tc::tmem_load32(scores + 32 * (c + 1), x[c + 1 & 1]);
+            sum += weights32<false>(x[c & 1], 0, f, -m, w[c]);
           }
-          if (__builtin_expect(any, 0)) {
-            float top = m;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) top = fmaxf(top, largest32<M>(x[c], seen[c], f));
-            float fix = 1.0f;
-            if (raise && top > -CUDART_INF_F) {
-              fix = m == -CUDART_INF_F ? 1.0f : ex2(m - top);
-              m = top;
-              l *= fix;
-            }
-            if (t > 0 && __any_sync(0xffffffffu, fix != 1.0f)) {
-              if (!wait(sh.pv_done[i], tile - 1)) return false;
-              uint32_t o[16];
-#pragma unroll 1
-              for (int d = 0; d < DP; d += 16) {
-                tc::tmem_load16(own_o + d, o);
-                tc::wait_loads(o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fix);
-                tc::tmem_store(own_o + d, o);
-              }
-            }
-            const float base = m == -CUDART_INF_F ? 0.0f : m;
-            float sum = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              sum += weights32<M>(x[c], seen[c], f, -base, w);
-              tc::tmem_store(scores + 16 * c, w);
-            }
+          slow = __any_sync(0xffffffffu, held && sum > kLargeSum);
+          if (!slow) {
             l += sum;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::tmem_store(scores + 16 * c, w[c]);
           }
-          return true;
-        };
-        if (!(whole<kKeys>(a, it, tpt, i, kb) ? turn(std::false_type{}) : turn(std::true_type{}))) return false;
+        }
+        if (slow) {
+          uint32_t x[32], w[16];
+          const auto seen = [&](int c) { return bits32(kb + 32 * c, from, token + 1) | bits32(kb + 32 * c, 0, sinks); };
+          float top = m;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            tc::tmem_load32(scores + 32 * c, x);
+            tc::wait_loads(x);
+            top = fmaxf(top, largest32(x, seen(c), f));
+          }
+          // rows that need nothing keep what they have, to the bit
+          float fix = 1.0f;
+          if (held && top > m + kLargeLog) {
+            fix = m == -CUDART_INF_F ? 1.0f : ex2(m - top);
+            m = top;
+            l *= fix;
+          }
+          if (t > 0 && __any_sync(0xffffffffu, fix != 1.0f)) {
+            if (!wait(sh.pv_done[i], tile - 1)) return false;
+#pragma unroll 1
+            for (int d = 0; d < DP; d += 16) {
+              tc::tmem_load16(own_o + d, w);
+              tc::wait_loads(w);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * fix);
+              tc::tmem_store(own_o + d, w);
+            }
+          }
+          const float base = m == -CUDART_INF_F ? 0.0f : m;
+          float sum = 0.0f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            tc::tmem_load32(scores + 32 * c, x);
+            tc::wait_loads(x);
+            sum += weights32<true>(x, seen(c), f, -base, w);
+            tc::tmem_store(scores + 16 * c, w);
+          }
+          l += sum;
+        }
         tc::wait_stores();
         // (with one tile of queries the scores do not say that the sums before them are done, and a barrier is never two phases ahead)
         if (C::NQ == 1 && t > 0 && !wait(sh.pv_done[i], tile - 1)) return false;
         tc::fence_before();
         warp_arrive(sh.p_ready[s]);
       }
-      if (!wait(sh.pv_done[i], tile - 1)) return false;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       uint16_t* out = static_cast<uint16_t*>(a.out) + at.row * a.out_row + at.head * a.out_head;
-      const bool dirty = *const_cast<const volatile int*>(&it.dirty) != 0;
+      if (held && a.lse) a.lse[at.row * a.heads + at.head] = (m + log2f(l)) * 0.69314718055994530942f;
+      if (!wait(sh.pv_done[i], tile - 1)) return false;
 #pragma unroll 1
-      for (int d = 0; d < DP; d += 16) {
-        uint32_t o[16];
-        tc::tmem_load16(own_o + d, o);
+      for (int d = 0; d < DP; d += 32) {
+        uint32_t o[32];
+        tc::tmem_load32(own_o + d, o);
         tc::wait_loads(o);
-        if (held && d < a.dim) {
-          float x[16];
+        if (d + 32 >= DP) {
+          tc::fence_before();
+          warp_arrive(sh.o_free[i]);
+        }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]) * inv;
-          if (dirty) add_rest(a, it, tpt, token, d, x);
+        for (int h = 0; h < 2; ++h) {
           uint32_t y[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = floats_to_bf16x2(x[2 * k], x[2 * k + 1]);
+          for (int k = 0; k < 8; ++k) y[k] = floats_to_bf16x2(__uint_as_float(o[16 * h + 2 * k]) * inv, __uint_as_float(o[16 * h + 2 * k + 1]) * inv);
+          uint16_t* to = out + d + 16 * h;
+          if (!held || d + 16 * h >= a.dim) continue;
           if (out_vec32) {
-            tc::store_32(out + d, y);
+            tc::store_32(to, y);
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              out[d + 2 * k] = static_cast<uint16_t>(y[k]);
-              out[d + 2 * k + 1] = static_cast<uint16_t>(y[k] >> 16);
+              to[2 * k] = static_cast<uint16_t>(y[k]);
+              to[2 * k + 1] = static_cast<uint16_t>(y[k] >> 16);
             }
           }
         }
         __syncwarp();
       }
-      tc::fence_before();
-      warp_arrive(sh.o_free[i]);
-      if (held && a.lse) a.lse[at.row * a.heads + at.head] = (m + log2f(l)) * 0.69314718055994530942f;
+      if (*const_cast<const volatile int*>(&it.dirty) != 0 && held) add_rest(a, it, tpt, token, out);
     }
     __syncwarp();
     if ((threadIdx.x & 31) == 0) sh.finished[threadIdx.x >> 5] = items + 1;
@@ -543,7 +539,7 @@ __global__ void __launch_bounds__(Config<DP>::kThreads, 1)
     tc::publish_shared();
   }
   if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), 512);
-  sort_sequences(a, sh.sequences, C::kThreads);
+  sort_sequences(a, sh.sequences, C::NQ * tpt, C::kThreads);
   if (blockIdx.x == 0) flag_lengths(a, C::kThreads);
   tc::fence_before();
   __syncthreads();
