@@ -9,10 +9,10 @@
 //   one issues the products;
 //   two look at the values of tiles that some rows do not see whole (below);
 //   four for each 128 rows turn scores into weights, a row a thread.
-// Weights are exp2(s - m) with m the row's largest score of the first tile
-// that it sees: bf16 weights have float's range, so m moves (and O is scaled
-// anew) only where a later tile's weights sum to more than 2^13, and what a
-// weight loses by a small m is nothing.  Weights are rounded to bf16 (2^-8),
+// Weights are exp2(s - m) with m the largest of the first scores that the row
+// sees: bf16 weights have float's range, so m moves (and O is scaled anew) only
+// where a tile's weights get large against it (a sum of more than 2^13), and
+// what a weight loses by a small m is nothing.  Weights are rounded to bf16 (2^-8),
 // the type that the products ask for beside bf16 values; their sum is taken
 // before that, in fp32.
 // What a row does not see has weight 0, but 0 times what is not finite is not
@@ -339,10 +339,11 @@ __device__ __forceinline__ float weights32(const uint32_t (&x)[32], uint32_t see
   return s.x + s.y;
 }
 
+template <bool MASKED>
 __device__ __forceinline__ float largest32(const uint32_t (&x)[32], uint32_t seen, float f) {
   float v[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-  for (int k = 0; k < 32; ++k) v[k & 3] = fmaxf(v[k & 3], seen >> k & 1u ? __uint_as_float(x[k]) * f : -CUDART_INF_F);
+  for (int k = 0; k < 32; ++k) v[k & 3] = fmaxf(v[k & 3], MASKED && !(seen >> k & 1u) ? -CUDART_INF_F : __uint_as_float(x[k]) * f);
   return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
 }
 
@@ -377,6 +378,7 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
     tc::fence_after();
     return ok;
   };
+  const int row_token = r / a.group, row_head = r - row_token * a.group;
   int tile = 0;
   for (int items = 0;; ++items) {
     if (!wait(sh.item_full[items % kItems], items / kItems)) return false;
@@ -384,9 +386,8 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
     if (it.tiles < 0) return true;
     const int count = it.count[i];
     if (count > 0) {
-      const Place at = place_of(a, it, tpt, i, r);
-      const int token = at.token;
-      const bool held = at.row >= 0;
+      const int token = it.tok0 + i * tpt + row_token;
+      const bool held = row_token < tpt && token < it.n && sv_in(it.row0 + static_cast<int64_t>(token), a.total_new);
       const int from = a.window ? max(0, token - a.window + 1) : 0, sinks = a.window ? min(a.sinks, token + 1) : 0;
       float m = held ? -CUDART_INF_F : 0.0f, l = 0.0f;  // what scores are taken from (base 2), the sum of weights
 #pragma unroll 1
@@ -394,8 +395,16 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
         const int s = C::NQ == 2 ? i : tile & 1, uses = C::NQ == 2 ? tile : tile >> 1;
         const int kb = key_of<kKeys>(it, t);
         const uint32_t scores = mine + C::kS + s * kKeys;
-        bool slow = !whole<kKeys>(a, it, tpt, i, kb) || __any_sync(0xffffffffu, m == -CUDART_INF_F);
+        bool slow = !whole<kKeys>(a, it, tpt, i, kb);
         if (!wait(sh.s_full[s], uses)) return false;
+        if (!slow && __any_sync(0xffffffffu, m == -CUDART_INF_F)) {  // the first tile: a few of its scores will do for m
+          uint32_t x[32];
+          tc::tmem_load32(scores, x);
+          tc::wait_loads(x);
+          const float top = largest32<false>(x, 0, f);
+          m = m == -CUDART_INF_F ? top : m;
+          slow = __any_sync(0xffffffffu, m == -CUDART_INF_F);
+        }
         if (!slow) {
           uint32_t x[2][32], w[4][16];
           float sum = 0.0f;
@@ -419,9 +428,11 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
           float top = m;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            const uint32_t mask = seen(c);
+            if (!__any_sync(0xffffffffu, mask != 0)) continue;
             tc::tmem_load32(scores + 32 * c, x);
             tc::wait_loads(x);
-            top = fmaxf(top, largest32(x, seen(c), f));
+            top = fmaxf(top, largest32<true>(x, mask, f));
           }
           // rows that need nothing keep what they have, to the bit
           float fix = 1.0f;
@@ -445,9 +456,15 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
           float sum = 0.0f;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            tc::tmem_load32(scores + 32 * c, x);
-            tc::wait_loads(x);
-            sum += weights32<true>(x, seen(c), f, -base, w);
+            const uint32_t mask = seen(c);
+            if (__any_sync(0xffffffffu, mask != 0)) {
+              tc::tmem_load32(scores + 32 * c, x);
+              tc::wait_loads(x);
+              sum += weights32<true>(x, mask, f, -base, w);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) w[k] = 0;
+            }
             tc::tmem_store(scores + 16 * c, w);
           }
           l += sum;
@@ -459,8 +476,10 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
         warp_arrive(sh.p_ready[s]);
       }
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      uint16_t* out = static_cast<uint16_t*>(a.out) + at.row * a.out_row + at.head * a.out_head;
-      if (held && a.lse) a.lse[at.row * a.heads + at.head] = (m + log2f(l)) * 0.69314718055994530942f;
+      const int64_t row = it.row0 + static_cast<int64_t>(token);
+      const int head = it.h * a.group + row_head;
+      uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.out_row + head * a.out_head;
+      if (held && a.lse) a.lse[row * a.heads + head] = (m + log2f(l)) * 0.69314718055994530942f;
       if (!wait(sh.pv_done[i], tile - 1)) return false;
 #pragma unroll 1
       for (int d = 0; d < DP; d += 32) {
