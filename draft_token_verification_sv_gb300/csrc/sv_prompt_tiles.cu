@@ -87,39 +87,30 @@ struct Loads {
   long long next;         // the number of the item that is published next
 };
 
+// The u-th of an item's tiles of keys and values in the order in which they are loaded and used: with two tiles of queries each
+// tile's keys and then its values; with one the next tile's keys, whose scores are formed meanwhile, come before the values.
+struct Turn {
+  bool keys;
+  int t;
+};
+template <int NQ>
+__device__ __forceinline__ Turn turn_of(int u, int tiles) {
+  if (NQ == 2) return Turn{(u & 1) == 0, u >> 1};
+  const bool last = u == 2 * tiles - 1;
+  const bool keys = !last && (u == 0 || (u & 1));
+  return Turn{keys, keys ? (u + 1) >> 1 : last ? tiles - 1 : (u >> 1) - 1};
+}
+
+template <int DP>
+__device__ __forceinline__ bool find_item(const PromptView& a, const Sequences& sq, int tpt, Finder& finder, long long index, Item& it) {
+  return finder.find<kKeys, Config<DP>::NQ>(a, sq, tpt, index, it);
+}
+
 template <int DP>
 __device__ bool load_role(const PromptView& a, const Maps& maps, int tpt, Shared& sh, uint32_t q_at, uint32_t kv_at, Finder& finder, Loads& under) {
   using C = Config<DP>;
   const int lane = threadIdx.x & 31;
   int items = 0, tile = 0;
-  const auto publish = [&](const Item& it) {
-    if (items >= kItems && !warp_wait(sh, sh.item_free[items % kItems], items / kItems - 1)) return false;
-    if (lane == 0) {
-      sh.item[items % kItems] = it;
-      if (it.tiles >= 0) sh.claimed = items + 1;
-    }
-    warp_arrive(sh.item_full[items % kItems]);
-    ++items;
-    return true;
-  };
-  const auto copy = [&](const CUtensorMap& map, const Item& it, int t) {  // a tile of keys or values
-    if (tile++ == SV_PROMPT_LOST_TILE) return false;
-    const int kb = key_of<kKeys>(it, t);
-#pragma unroll
-    for (int half = 0; half < C::kHalves; ++half) {
-      const int unit = under.units, stage = unit % C::kStages;
-      if (unit >= C::kStages && !warp_wait(sh, sh.kv_free[stage], unit / C::kStages - 1)) return false;
-      const uint32_t bar = tc::smem_address(&sh.kv_full[stage]);
-      if (lane == 0) {
-        tc::barrier_expect(bar, C::kUnitBytes);
-#pragma unroll
-        for (int x = 0; x < C::kUnitDims; x += 64)
-          tc::copy_box(kv_at + stage * C::kUnitBytes + x / 64 * C::kBlockBytes, &map, half * C::kUnitDims + x, it.h, it.row0 + kb, bar);
-      }
-      ++under.units;
-    }
-    return true;
-  };
   Item it;
   for (int x = blockIdx.x; x >= 0;) {
     if (lane == 0) {
@@ -128,13 +119,21 @@ __device__ bool load_role(const PromptView& a, const Maps& maps, int tpt, Shared
       tc::ask_for_block(tc::smem_address(&sh.block), bar);
     }
     under.asked = true;
-    for (under.next = x; finder.find<kKeys, C::NQ>(a, sh.sequences, tpt, under.next, it);) {
-      if (!publish(it)) return false;
+    under.next = x;
+    while (find_item<DP>(a, sh.sequences, tpt, finder, under.next, it)) {
+      if (items >= kItems && !warp_wait(sh, sh.item_free[items % kItems], items / kItems - 1)) return false;
+      if (lane == 0) {
+        sh.item[items % kItems] = it;
+        sh.claimed = items + 1;
+      }
+      warp_arrive(sh.item_full[items % kItems]);
+      ++items;
       under.next += gridDim.x;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < C::NQ; ++i) {
-        if (it.count[i] == 0) continue;
-        if (under.queries[i] > 0 && !warp_wait(sh, sh.q_free[i], under.queries[i] - 1)) return false;
+        if ((i ? it.count[1] : it.count[0]) == 0) continue;
+        const int before = i ? under.queries[1] : under.queries[0];
+        if (before > 0 && !warp_wait(sh, sh.q_free[i], before - 1)) return false;
         const uint32_t bar = tc::smem_address(&sh.q_full[i]);
         if (lane == 0) {
           tc::barrier_expect(bar, tpt * a.group * DP * 2);
@@ -142,16 +141,27 @@ __device__ bool load_role(const PromptView& a, const Maps& maps, int tpt, Shared
           for (int d = 0; d < DP; d += 64)
             tc::copy_box(q_at + i * C::kQueryBytes + d / 64 * (kRows * 128), &maps.q, d, it.h * a.group, it.row0 + it.tok0 + i * tpt, bar);
         }
-        ++under.queries[i];
-        if (i == 0 && !copy(maps.k, it, 0)) return false;  // (the first keys behind the first queries)
+        (i ? under.queries[1] : under.queries[0]) = before + 1;
       }
-      for (int t = 0; t < it.tiles; ++t) {
-        if (C::NQ == 2) {
-          if (t > 0 && !copy(maps.k, it, t)) return false;
-        } else {
-          if (t + 1 < it.tiles && !copy(maps.k, it, t + 1)) return false;
+#pragma unroll 1
+      for (int u = 0; u < 2 * it.tiles; ++u) {
+        if (tile++ == SV_PROMPT_LOST_TILE) return false;
+        const Turn turn = turn_of<C::NQ>(u, it.tiles);
+        const int kb = key_of<kKeys>(it, turn.t);
+        const CUtensorMap* map = turn.keys ? &maps.k : &maps.v;
+#pragma unroll 1
+        for (int half = 0; half < C::kHalves; ++half) {
+          const int unit = under.units, stage = unit % C::kStages;
+          if (unit >= C::kStages && !warp_wait(sh, sh.kv_free[stage], unit / C::kStages - 1)) return false;
+          const uint32_t bar = tc::smem_address(&sh.kv_full[stage]);
+          if (lane == 0) {
+            tc::barrier_expect(bar, C::kUnitBytes);
+#pragma unroll
+            for (int d = 0; d < C::kUnitDims; d += 64)
+              tc::copy_box(kv_at + stage * C::kUnitBytes + d / 64 * C::kBlockBytes, map, half * C::kUnitDims + d, it.h, it.row0 + kb, bar);
+          }
+          ++under.units;
         }
-        if (!copy(maps.v, it, t)) return false;
       }
     }
     if (!warp_wait(sh, sh.answer, under.answers)) return false;
@@ -161,11 +171,37 @@ __device__ bool load_role(const PromptView& a, const Maps& maps, int tpt, Shared
     __syncwarp();
     tc::publish_shared();  // (read before the next answer is written)
   }
-  it.tiles = -1;
-  return publish(it);
+  if (items >= kItems && !warp_wait(sh, sh.item_free[items % kItems], items / kItems - 1)) return false;
+  if (lane == 0) sh.item[items % kItems].tiles = -1;
+  warp_arrive(sh.item_full[items % kItems]);
+  return true;
+}
+
+// What is under way when the loading warp gives up ends before its memory does: the last copies to each place, which no other
+// role may have waited for, and the answer.  Items that no other role knows of are spoilt here.
+template <int DP>
+__device__ __noinline__ void end_loads(const PromptView& a, int tpt, Shared& sh, Finder& finder, Loads& under) {
+  using C = Config<DP>;
+  int unused = 0;
+  for (int u = max(0, under.units - C::kStages); u < under.units; ++u)
+    tc::barrier_wait(tc::smem_address(&sh.kv_full[u % C::kStages]), u / C::kStages & 1, &unused, tc::kEndCycles);
+  for (int i = 0; i < C::NQ; ++i)
+    if (under.queries[i] > 0) tc::barrier_wait(tc::smem_address(&sh.q_full[i]), under.queries[i] - 1 & 1, &unused, tc::kEndCycles);
+  Item it;
+  for (;;) {
+    for (; find_item<DP>(a, sh.sequences, tpt, finder, under.next, it); under.next += gridDim.x) spoil<uint16_t>(a, it, tpt, C::NQ, threadIdx.x & 31, 32);
+    if (!under.asked) return;
+    under.asked = false;
+    const bool answered = tc::barrier_wait(tc::smem_address(&sh.answer), under.answers & 1, &unused, tc::kEndCycles);
+    under.next = __all_sync(0xffffffffu, answered) ? tc::taken_block(tc::smem_address(&sh.block)) : -1;
+    if (under.next < 0) return;
+  }
 }
 
 // ---- values that are not finite ----
+
+// Both values of a word, 0 where they are not finite.
+__device__ __forceinline__ uint32_t finite_of(uint32_t w) { return w & ~__vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u); }
 
 // It takes part in every copy's way, so that it is never a round of the stages behind.
 template <int DP>
@@ -178,25 +214,25 @@ __device__ bool check_role(const PromptView& a, int tpt, Shared& sh, uint8_t* kv
     Item& it = sh.item[items % kItems];
     const int tiles = it.tiles;
     if (tiles < 0) return true;
-    const auto pass = [&](bool look) {
+#pragma unroll 1
+    for (int u = 0; u < 2 * tiles; ++u) {
+      const Turn turn = turn_of<C::NQ>(u, tiles);
+      const bool look = !turn.keys && partly_seen<kKeys, C::NQ>(a, it, tpt, turn.t);
+#pragma unroll 1
       for (int half = 0; half < C::kHalves; ++half, ++unit) {
         const int stage = unit % C::kStages;
         if (!warp_wait(sh, sh.kv_full[stage], unit / C::kStages)) return false;
         if (look) {
           uint4* at = reinterpret_cast<uint4*>(kv + stage * C::kUnitBytes);
           bool found = false;
-#pragma unroll 8
+#pragma unroll 4
           for (int c = tid; c < C::kUnitBytes / 16; c += 32 * C::kCheckWarps) {
             uint4 v = at[c];
             // the largest magnitude of each half word: 0x7f80 and more is not finite
             const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
             if (__vcmpgeu2(m, 0x7f807f80u)) {
               found = true;
-              v.x &= ~__vcmpgeu2(v.x & 0x7fff7fffu, 0x7f807f80u);
-              v.y &= ~__vcmpgeu2(v.y & 0x7fff7fffu, 0x7f807f80u);
-              v.z &= ~__vcmpgeu2(v.z & 0x7fff7fffu, 0x7f807f80u);
-              v.w &= ~__vcmpgeu2(v.w & 0x7fff7fffu, 0x7f807f80u);
-              at[c] = v;
+              at[c] = make_uint4(finite_of(v.x), finite_of(v.y), finite_of(v.z), finite_of(v.w));
             }
           }
           if (found) it.dirty = 1;
@@ -205,12 +241,6 @@ __device__ bool check_role(const PromptView& a, int tpt, Shared& sh, uint8_t* kv
         }
         warp_arrive(sh.kv_free[stage]);
       }
-      return true;
-    };
-    if (C::NQ == 1 && !pass(false)) return false;  // the first keys
-    for (int t = 0; t < tiles; ++t) {
-      if ((C::NQ == 2 || t + 1 < tiles) && !pass(false)) return false;  // keys
-      if (!pass(partly_seen<kKeys, C::NQ>(a, it, tpt, t))) return false;
     }
     warp_arrive(sh.item_free[items % kItems]);
   }
@@ -229,41 +259,47 @@ __device__ bool product_role(const PromptView& a, int tpt, Shared& sh, uint32_t 
   };
   const auto arrive = [&](uint64_t& bar) { tc::products_arrive(tc::smem_address(&bar)); };
   uint32_t checks = 0;  // parity of `checked` for each stage
-  int unit = 0, loads[2] = {0, 0}, done[2] = {0, 0}, weighed[2] = {0, 0}, tile = 0;
+  int unit = 0, done[2] = {0, 0}, weighed[2] = {0, 0}, tile = 0;
   for (int items = 0;; ++items) {
     if (!wait(sh.item_full[items % kItems], items / kItems)) return false;
     const Item it = sh.item[items % kItems];
     tc::barrier_arrive(tc::smem_address(&sh.item_free[items % kItems]));
     if (it.tiles < 0) return true;
     // S of tile i of queries with the keys of unit u, to place s
-    const auto score = [&](int i, int u, int s, bool last_use) {
-#pragma unroll
+    const auto score = [&](int i, int t, int u, int s, bool last_use) {
+      if (t == 0 && !wait(sh.q_full[i], i ? done[1] : done[0])) return false;
+#pragma unroll 1
       for (int half = 0; half < C::kHalves; ++half) {
         const int stage = (u + half) % C::kStages;
         if (!wait(sh.kv_full[stage], (u + half) / C::kStages)) return false;
-        const uint32_t k = kv_at + stage * C::kUnitBytes, q = q_at + i * C::kQueryBytes + half * (kRows * 256);
+        const uint64_t k = tc::tile_descriptor(kv_at + stage * C::kUnitBytes, 16, 1024);
+        const uint64_t q = tc::tile_descriptor(q_at + i * C::kQueryBytes + half * (kRows * 256), 16, 1024);
 #pragma unroll
-        for (int d = 0; d < C::kUnitDims / 16; ++d)
-          tc::product_f16(tmem + C::kS + s * kKeys, tc::tile_descriptor(q + (d >> 2) * (kRows * 128) + (d & 3) * 32, 16, 1024),
-                          tc::tile_descriptor(k + (d >> 2) * C::kBlockBytes + (d & 3) * 32, 16, 1024), kScores, half > 0 || d > 0);
+        for (int d = 0; d < C::kUnitDims / 16; ++d) {
+          constexpr int kStep = 32 >> 4;
+          const int off = (d >> 2) * (kRows * 128 >> 4) + (d & 3) * kStep;  // (tiles of queries and keys are of one height)
+          tc::product_f16(tmem + C::kS + s * kKeys, q + off, k + off, kScores, d > 0 || half > 0);
+        }
         if (last_use) arrive(sh.kv_free[stage]);
       }
       arrive(sh.s_full[s]);
+      if (t + 1 == (i ? it.count[1] : it.count[0])) arrive(sh.q_free[i]);
       return true;
     };
     // O of tile i (+)= P in place s times the values of unit u
-    const auto weigh = [&](int i, int u, int s, int uses, bool first, bool check, bool last_use) {
+    const auto weigh = [&](int i, int t, int u, int s, int uses, bool check, bool last_use) {
+      const int before = i ? done[1] : done[0];
+      if (t == 0 && before > 0 && !wait(sh.o_free[i], before - 1)) return false;
       if (!wait(sh.p_ready[s], uses)) return false;
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < C::kHalves; ++half) {
         const int stage = (u + half) % C::kStages;
         if (!wait(sh.kv_full[stage], (u + half) / C::kStages)) return false;
         if (check && !wait(sh.checked[stage], checks >> stage)) return false;
-        const uint32_t v = kv_at + stage * C::kUnitBytes;
+        const uint64_t v = tc::tile_descriptor(kv_at + stage * C::kUnitBytes, C::kBlockBytes, 1024);
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          tc::product_f16(tmem + C::kO + i * DP + half * C::kUnitDims, tmem + C::kS + s * kKeys + k * 8,
-                          tc::tile_descriptor(v + k * 2048, C::kBlockBytes, 1024), kValues, !first || k > 0);
+          tc::product_f16(tmem + C::kO + i * DP + half * C::kUnitDims, tmem + C::kS + s * kKeys + k * 8, v + k * (2048 >> 4), kValues, k > 0 || t > 0);
         if (last_use) {
           if (check) checks ^= 1u << stage;
           arrive(sh.kv_free[stage]);
@@ -273,44 +309,36 @@ __device__ bool product_role(const PromptView& a, int tpt, Shared& sh, uint32_t 
       return true;
     };
     if (C::NQ == 2) {
-      // the last of the tiles of queries that need tile t
-      const auto last_of = [&](int t) { return t < it.count[1] ? 1 : 0; };
-#pragma unroll
-      for (int i = 0; i < C::NQ; ++i) {
-        if (it.count[i] == 0) continue;
-        if (!wait(sh.q_full[i], loads[i]++)) return false;
-        if (!score(i, unit, i, i == last_of(0))) return false;
-        if (it.count[i] == 1) arrive(sh.q_free[i]);
-      }
-      for (int t = 0; t < it.tiles; ++t, unit += 2) {
-        const bool check = partly_seen<kKeys, C::NQ>(a, it, tpt, t);
-#pragma unroll
+      // after a tile's sums the next one's scores, which take the place of its weights
+#pragma unroll 1
+      for (int t = -1; t < it.tiles; ++t) {
+        const bool check = t >= 0 && partly_seen<kKeys, C::NQ>(a, it, tpt, t);
+#pragma unroll 1
         for (int i = 0; i < C::NQ; ++i) {
-          if (t >= it.count[i]) continue;
-          if (t == 0 && done[i] > 0 && !wait(sh.o_free[i], done[i] - 1)) return false;
-          if (!weigh(i, unit + 1, i, weighed[i]++, t == 0, check, i == last_of(t))) return false;
-          if (t + 1 >= it.count[i]) continue;
-          if (!score(i, unit + 2, i, i == last_of(t + 1))) return false;
-          if (t + 2 == it.count[i]) arrive(sh.q_free[i]);
+          const int count = i ? it.count[1] : it.count[0];
+          // (the last of the tiles of queries that need a tile of keys lets it go)
+          if (t >= 0 && t < count) {
+            if (!weigh(i, t, unit + 2 * t + 1, i, i ? weighed[1] : weighed[0], check, i == 1 || t >= it.count[1])) return false;
+            ++(i ? weighed[1] : weighed[0]);
+          }
+          if (t + 1 < count && !score(i, t + 1, unit + 2 * t + 2, i, i == 1 || t + 1 >= it.count[1])) return false;
         }
       }
-#pragma unroll
-      for (int i = 0; i < C::NQ; ++i) done[i] += it.count[i] > 0;
+      unit += 2 * it.tiles;
+      done[0] += it.count[0] > 0;
+      done[1] += it.count[1] > 0;
     } else {
-      if (!wait(sh.q_full[0], loads[0]++)) return false;
-      if (!score(0, unit, tile & 1, true)) return false;
-      unit += C::kHalves;
-      if (it.tiles == 1) arrive(sh.q_free[0]);
-      for (int t = 0; t < it.tiles; ++t, ++tile) {
+#pragma unroll 1
+      for (int t = -1; t < it.tiles; ++t) {
         if (t + 1 < it.tiles) {
-          if (!score(0, unit, tile + 1 & 1, true)) return false;
+          if (!score(0, t + 1, unit, tile + t + 1 & 1, true)) return false;
           unit += C::kHalves;
-          if (t + 2 == it.tiles) arrive(sh.q_free[0]);
         }
-        if (t == 0 && done[0] > 0 && !wait(sh.o_free[0], done[0] - 1)) return false;
-        if (!weigh(0, unit, tile & 1, tile >> 1, t == 0, partly_seen<kKeys, C::NQ>(a, it, tpt, t), true)) return false;
+        if (t < 0) continue;
+        if (!weigh(0, t, unit, tile + t & 1, tile + t >> 1, partly_seen<kKeys, C::NQ>(a, it, tpt, t), true)) return false;
         unit += C::kHalves;
       }
+      tile += it.tiles;
       ++done[0];
     }
   }
@@ -570,25 +598,9 @@ __global__ void __launch_bounds__(Config<DP>::kThreads, 1)
   } else {
     if constexpr (C::NQ == 2) tc::registers_down<C::kOtherRegisters>();
     if (warp == C::kSoftmaxWarps) {
-      Finder finder{0, 0};
+      Finder finder{};
       Loads under{};
-      if (!load_role<DP>(a, maps, tpt, sh, q_at, kv_at, finder, under)) {
-        // What is under way ends before its memory is given up: the last copies to each place, which no other role may have
-        // waited for, and the answer.  Items that no other role knows of are spoilt here.
-        int unused = 0;
-        for (int u = max(0, under.units - C::kStages); u < under.units; ++u)
-          tc::barrier_wait(tc::smem_address(&sh.kv_full[u % C::kStages]), u / C::kStages & 1, &unused, tc::kEndCycles);
-        for (int i = 0; i < C::NQ; ++i)
-          if (under.queries[i] > 0) tc::barrier_wait(tc::smem_address(&sh.q_full[i]), under.queries[i] - 1 & 1, &unused, tc::kEndCycles);
-        Item it;
-        for (; finder.find<kKeys, C::NQ>(a, sh.sequences, tpt, under.next, it); under.next += gridDim.x) spoil<uint16_t>(a, it, tpt, C::NQ, tid & 31, 32);
-        if (under.asked) {
-          const bool answered = tc::barrier_wait(tc::smem_address(&sh.answer), under.answers & 1, &unused, tc::kEndCycles);
-          const int x = __all_sync(0xffffffffu, answered) ? tc::taken_block(tc::smem_address(&sh.block)) : -1;
-          if (x >= 0)
-            for (long long index = x; finder.find<kKeys, C::NQ>(a, sh.sequences, tpt, index, it); index += gridDim.x) spoil<uint16_t>(a, it, tpt, C::NQ, tid & 31, 32);
-        }
-      }
+      if (!load_role<DP>(a, maps, tpt, sh, q_at, kv_at, finder, under)) end_loads<DP>(a, tpt, sh, finder, under);
     } else if (warp == C::kSoftmaxWarps + 1) {
       if (tc::elected()) {
         product_role<DP>(a, tpt, sh, q_at, kv_at, tmem);
