@@ -3,6 +3,8 @@
 // stack's count, page ids), by the slots and positions written for prompts.
 #include "sv_kv.cuh"
 
+#include <algorithm>
+
 namespace sv {
 
 namespace {
@@ -60,18 +62,125 @@ __device__ __forceinline__ long long block_inclusive(long long v, long long* scr
   return v + (warp > 0 ? scratch[warp - 1] : 0);
 }
 
-// The first of the block's sequences whose inclusive sum is above i.
+// The first of the block's sequences whose inclusive sum is above i (which the last one's is).  Without branches, so that several
+// searches run at a time.
 __device__ __forceinline__ int owner(const long long* sums, long long i) {
-  int lo = 0, hi = kThreads - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (sums[mid] > i)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return lo;
+  int k = 0;
+#pragma unroll
+  for (int step = kThreads / 2; step > 0; step >>= 1) k += sums[k + step - 1] <= i ? step : 0;
+  return k;
 }
+
+// Depth of node i of a tree; what is wrong with its own parent is flagged.
+__device__ __forceinline__ int depth_of(const AssignView& a, int b, const int32_t* parents, int i) {
+  int depth = 0;
+  for (int u = i; u >= 0;) {
+    const int p = __ldg(parents + u);
+    if (u == i && (u == 0 ? p != -1 : (p < 0 || p >= u))) kv_flag(a.w, b, SV_ROW_BAD_PARENT);
+    u = p >= 0 && p < u ? p : -1;
+    depth += u >= 0;
+  }
+  return depth;
+}
+
+// The slot of token j on a page (flagged, and -1, outside the pool).
+__device__ __forceinline__ int64_t slot_on(const AssignView& a, int b, int page, int j) {
+  if (page >= 0 && page < a.w.num_pages) return (static_cast<int64_t>(page) << a.w.page_shift) + (j & ((1 << a.w.page_shift) - 1));
+  kv_flag(a.w, b, SV_ROW_BAD_PAGE);
+  return -1;
+}
+
+// ---- up to 1024 sequences ----
+
+// Every block scans what all sequences give, lack and bring, a thread a
+// sequence, and then moves its share of the pages and places its share of the
+// tokens, one to a thread: the i-th page taken is the i-th given, or what lies
+// that deep on the stack, and a new token's page is known before it is in the
+// table, so that no block waits for another.  Lengths, the stack's count and
+// the flags change in one block alone, when all others are done: with kAll in
+// the same launch, which then is of one block, else in one of its own.
+enum { kAll, kMove, kUpdate };
+
+template <int WHAT>
+__global__ void __launch_bounds__(kThreads) kv_assign_few_kernel(AssignView a) {
+  __shared__ long long scratch[33], gives[kThreads], lacks[kThreads], brings[kThreads];
+  __shared__ int ctxs[kThreads], rows[kThreads], helds[kThreads], wants[kThreads];  // wants: -1 where the sequence is left out
+  const int tid = threadIdx.x, batch = a.w.batch, size = a.w.num_pages, shift = a.w.page_shift;
+  if (WHAT != kAll) wait_for_stream();
+  const int count = min(max(*a.free_count, 0), size);
+  Need n{0, 0, false};
+  KvSpan s{0, 0, 0, false};
+  if (tid < batch) {
+    s = kv_span(a.w, tid);
+    n = need_of(a, tid);
+  }
+  const int gave = max(n.held - n.want, 0), lack = max(n.want - n.held, 0);
+  const long long given_upto = block_inclusive(gave, scratch), given = scratch[32];
+  const long long lacked = block_inclusive(lack, scratch);
+  const long long there = min(count + given, static_cast<long long>(size));
+  const bool refused = lack > 0 && lacked > there;
+  const long long taken = min(block_inclusive(refused ? 0 : lack, scratch), there), all_taken = scratch[32];
+  const int flag = tid >= batch || (n.ok && !refused) ? 0 : n.ok ? SV_ROW_NO_PAGE : SV_ROW_BAD_LENGTH;
+  if (WHAT == kAll && tid < batch && a.w.status) a.w.status[tid] = flag;
+  if (WHAT != kUpdate) {
+    gives[tid] = given_upto;
+    lacks[tid] = taken;
+    const bool tokens = a.slots || a.positions;
+    brings[tid] = block_inclusive(tokens && s.n > 0 ? s.n : 0, scratch);
+    const long long brought = scratch[32];
+    ctxs[tid] = s.ctx;
+    rows[tid] = s.row0;
+    helds[tid] = n.held;
+    wants[tid] = !n.ok ? -1 : refused ? n.held : n.want;
+    __syncthreads();
+    const long long first = static_cast<long long>(blockIdx.x) * kThreads + tid, step = static_cast<long long>(gridDim.x) * kThreads;
+    // the i-th page given
+    const auto given_page = [&](long long i) {
+      const int k = owner(gives, i), col = wants[k] + static_cast<int>(i - (k > 0 ? gives[k - 1] : 0));
+      return sv_in(col, a.w.max_pages) ? a.table[k * a.w.table_stride + col] : -1;
+    };
+    // and the i-th page taken (there are no more given than the stack has room for, or the first ones given are lost)
+    const auto taken_page = [&](long long i) {
+      const long long at = there - 1 - i;
+      return at >= count ? given_page(count + given - 1 - at) : sv_in(at, size) ? a.free_pages[at] : -1;
+    };
+#pragma unroll 4
+    for (long long i = first; i < given; i += step) {
+      const long long at = count + given - 1 - i;
+      if (at < size && sv_in(at, size)) a.free_pages[at] = given_page(i);
+    }
+#pragma unroll 4
+    for (long long i = first; i < all_taken; i += step) {
+      const int k = owner(lacks, i), col = helds[k] + static_cast<int>(i - (k > 0 ? lacks[k - 1] : 0));
+      if (sv_in(col, a.w.max_pages)) a.table[k * a.w.table_stride + col] = taken_page(i);
+    }
+#pragma unroll 4
+    for (long long i = first; i < brought; i += step) {
+      const int k = owner(brings, i), t = static_cast<int>(i - (k > 0 ? brings[k - 1] : 0));
+      const int64_t row = rows[k] + static_cast<int64_t>(t);
+      if (!kv_row_in(a.w, row)) continue;
+      int64_t slot = -1;
+      int position = 0;
+      if (wants[k] >= 0) {
+        const int j = ctxs[k] + t, col = j >> shift;
+        position = a.parents ? ctxs[k] + depth_of(a, k, a.parents + rows[k], t) : j;
+        // (a sequence that got no pages has fewer than its tokens need)
+        const int tokens_of = static_cast<int>(brings[k] - (k > 0 ? brings[k - 1] : 0));
+        if (a.slots && static_cast<int64_t>(wants[k]) << shift >= static_cast<int64_t>(ctxs[k]) + tokens_of && sv_in(col, a.w.max_pages))
+          slot = slot_on(a, k, col < helds[k] ? a.table[k * a.w.table_stride + col] : taken_page((k > 0 ? lacks[k - 1] : 0) + col - helds[k]), j);
+      }
+      if (a.slots) a.slots[row] = slot;
+      if (a.positions) a.positions[row] = position;
+    }
+  }
+  if (WHAT != kMove) {
+    if (tid < batch && n.ok && !refused) a.held[tid] = n.want;
+    if (WHAT == kUpdate && flag) kv_flag(a.w, tid, flag);
+    if (tid == 0) *a.free_count = static_cast<int>(there - all_taken);
+  }
+}
+
+// ---- any number of sequences ----
 
 // One block: pages move in the order that the sequences have, whatever the
 // launch, so it scans what they give and lack, 1024 at a time, and moves the
@@ -160,30 +269,15 @@ __global__ void __launch_bounds__(kPlaceThreads) kv_assign_places_kernel(AssignV
     if (a.positions) a.positions[row] = 0;
     return;
   }
-  int depth = static_cast<int>(i);
-  if (a.parents) {
-    const int32_t* parents = a.parents + s.row0;
-    depth = 0;
-    for (int u = static_cast<int>(i); u >= 0;) {
-      const int p = __ldg(parents + u);
-      if (u == i && (u == 0 ? p != -1 : (p < 0 || p >= u))) kv_flag(a.w, b, SV_ROW_BAD_PARENT);
-      u = p >= 0 && p < u ? p : -1;
-      depth += u >= 0;
-    }
-  }
-  if (a.positions) a.positions[row] = s.ctx + depth;
+  if (a.positions) a.positions[row] = s.ctx + (a.parents ? depth_of(a, b, a.parents + s.row0, static_cast<int>(i)) : static_cast<int>(i));
   if (!a.slots) return;
   const int j = s.ctx + static_cast<int>(i), col = j >> a.w.page_shift;
-  int64_t slot = -1;
-  if (static_cast<int64_t>(held) << a.w.page_shift >= static_cast<int64_t>(s.ctx) + s.n && sv_in(col, a.w.max_pages)) {
-    const int page = a.table[b * a.w.table_stride + col];
-    if (page >= 0 && page < a.w.num_pages)
-      slot = (static_cast<int64_t>(page) << a.w.page_shift) + (j & ((1 << a.w.page_shift) - 1));
-    else
-      kv_flag(a.w, b, SV_ROW_BAD_PAGE);
-  }
-  a.slots[row] = slot;
+  const bool served = static_cast<int64_t>(held) << a.w.page_shift >= static_cast<int64_t>(s.ctx) + s.n && sv_in(col, a.w.max_pages);
+  a.slots[row] = served ? slot_on(a, b, a.table[b * a.w.table_stride + col], j) : -1;
 }
+
+// From this many pages that sequences could hold, or new tokens, on, several blocks move and place them.
+constexpr int64_t kManyPages = 16384, kManyTokens = 8192;
 
 }  // namespace
 
@@ -201,6 +295,24 @@ sv_status kv_assign(const sv_kv_assign_desc& d, int32_t* free_pages, int32_t* fr
   c.page_table = page_table;
   const AssignView a{kv_view(k, c, ctx_lens, new_start, d.max_new, d.total_new, row_status),
                      free_pages, free_count, page_table, held, parents, slots, positions};
+  if (d.batch <= kThreads) {
+    const int64_t tokens = slots || positions ? d.total_new : 0;
+    const int64_t pages = static_cast<int64_t>(d.batch) * d.max_pages;
+    if (pages <= kManyPages && tokens <= kManyTokens) {
+      kv_assign_few_kernel<kAll><<<1, kThreads, 0, stream>>>(a);
+      if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+      note_launch(stream);
+      return SV_OK;
+    }
+    if (row_status && cudaMemsetAsync(row_status, 0, static_cast<size_t>(d.batch) * sizeof(int32_t), stream) != cudaSuccess) return SV_ERR_CUDA;
+    const int64_t share = std::max(pages, tokens) / (2 * kThreads) + 1;
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(share, 152));
+    if (launch_early(kv_assign_few_kernel<kMove>, dim3(blocks), dim3(kThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
+    note_launch(stream);
+    if (launch_early(kv_assign_few_kernel<kUpdate>, dim3(1), dim3(kThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
+    note_launch(stream);
+    return SV_OK;
+  }
   kv_assign_pages_kernel<<<1, kThreads, 0, stream>>>(a);
   if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);

@@ -27,7 +27,7 @@ struct RopeView {
 // of a far position loses nothing to its size.  A float is m 2^e, so this is
 // m times the bits of 1 / (2 pi), moved by e: off by 2^-64 turns, 2^-33 after
 // 2^31 positions.  (Doubles would do, but eight of them for each thread took
-// longer than the rest of 12,000 tokens of 32 heads: 72 us, now XX.)
+// longer than the rest of 12,000 tokens of 32 heads: 72 us, now 39.)
 __device__ __forceinline__ unsigned long long turns(float inv_freq) {
   constexpr unsigned long long kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f47d4d3770ull;  // 2^128 / (2 pi)
   const uint32_t u = __float_as_uint(inv_freq), raised = u >> 23 & 0xffu;
@@ -216,9 +216,14 @@ void launch(const RopeView& w, cudaStream_t stream) {
     rope_pairs_kernel<E><<<w.rows, kPairThreads, 0, stream>>>(w);
     return;
   }
-  const int split = w.rows >= 152 * 16 ? 1 : w.rows >= 152 * 4 ? 2 : 8;
+  // A warp a token, as many blocks as run at a time: 24,000 tokens of 40 heads take 166 us (more blocks: 170 and up, two warps a
+  // token: 172).  Few tokens are shared by more warps, as long as these have heads: 64 of 40 heads take 6.4 us with one, 4.4 with 8.
+  constexpr int kBlocks = 2 * 152;
+  const int per = 32 / (w.dim >> 4), all = w.heads[0] + w.heads[1];
+  int split = 1;
+  while (split < kWarps && static_cast<int64_t>(w.rows) * split < kBlocks * kWarps && split * per < all) split *= 2;
   const int64_t blocks = (static_cast<int64_t>(w.rows) * split + kWarps - 1) / kWarps;
-  const unsigned grid = static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8);
+  const unsigned grid = static_cast<unsigned>(blocks < kBlocks ? blocks : kBlocks);
   if (w.adjacent)
     rope_units_kernel<E, true><<<grid, kThreads, 0, stream>>>(w, split);
   else

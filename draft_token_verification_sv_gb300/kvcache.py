@@ -244,7 +244,8 @@ def _attention_plan(q, kc, vc, ks, vs, table, lens, start, max_new, parents, sca
 
 
 @functools.lru_cache(maxsize=_KEPT)
-def _assign_plan(free, count, table, held, lens, page, start, max_new, parents, slots, positions, status):
+def _assign_plan(free, count, table, held, lens, page, start, max_new, total, parents, slots, positions, status):
+    """slots None: the call makes its results itself, or has none."""
     free, count, table = _see(free, "pool['free']"), _see(count, "pool['count']"), _see(table, "page_table")
     if free.dtype != torch.int32 or len(free.shape) != 1 or not _contiguous(free):
         raise ValueError("pool['free'] must be a contiguous int32 [num_pages] tensor")
@@ -255,16 +256,28 @@ def _assign_plan(free, count, table, held, lens, page, start, max_new, parents, 
     _int32(status, "row_status", B, _PER_SEQUENCE)
     if start is not None:
         _int32(start, "new_start", B + 1, "one entry more than page_table has rows")
-    s, p = _see(slots, "slots"), _see(positions, "positions")
-    total = _numel(s.shape)
-    if s.dtype != torch.int64 or not _contiguous(s) or p.dtype != torch.int32 or not _contiguous(p) or p.shape != s.shape:
-        raise ValueError("slots must be a contiguous int64 tensor and positions a contiguous int32 tensor of its shape")
-    if start is None and total != B * max_new:
-        raise ValueError("slots and positions must have one entry for each new token")
+    if slots is not None:
+        s, p = _see(slots, "slots"), _see(positions, "positions")
+        if s.dtype != torch.int64 or not _contiguous(s) or p.dtype != torch.int32 or not _contiguous(p) or p.shape != s.shape:
+            raise ValueError("slots must be a contiguous int64 tensor and positions a contiguous int32 tensor of its shape")
+        if total is None:
+            total = _numel(s.shape)
+        elif total != _numel(s.shape):
+            raise ValueError("total differs from the results given")
+    if start is None:
+        if total not in (None, B * max_new):
+            raise ValueError("slots and positions must have one entry for each new token")
+        total = B * max_new
+    elif total is None:
+        raise ValueError("new_start needs total, the number of rows")
+    _count(max_new, "the largest number of new tokens")
+    _count(total, "the number of new tokens")
+    if max_new < 0 or total < 0:
+        raise ValueError("there cannot be fewer than no new tokens")
     _int32(parents, "parents", total, "one entry for each new token")
-    d = N.KvAssignDesc(B, _count(page, "page_size"), _count(free.shape[0], "the number of pages"), columns,
-                       _count(max_new, "the largest number of new tokens"), _count(total, "the number of new tokens"), stride)
-    return ctypes.byref(d), _one_device(free, count, table, held, lens, start, parents, slots, positions, status)
+    d = N.KvAssignDesc(B, _count(page, "page_size"), _count(free.shape[0], "the number of pages"), columns, max_new, total, stride)
+    return ctypes.byref(d), (total,) if start is not None else (B, max_new), _one_device(free, count, table, held, lens, start, parents, slots,
+                                                                                       positions, status)
 
 
 def _at(t):
@@ -286,7 +299,8 @@ def _call(device: int, entry: str, *args) -> None:
     else:
         with torch.cuda.device(device):
             st = getattr(N.lib(), entry)(*args)
-    N.check(st, entry)
+    if st:
+        N.check(st, entry)
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -314,23 +328,19 @@ def kv_assign(pool: dict, page_table: torch.Tensor, held: torch.Tensor, ctx_lens
     beyond ctx_lens go back.
 
     Updates pool, page_table and held, and returns dict(slots=int64,
-    positions=int32), each [B, max_new] or [total] (or ``out``, the two)."""
+    positions=int32), each [B, max_new] or [total] (or ``out``, the two); both
+    are None where ``max_new`` is 0."""
     max_new = int(max_new)
-    if out is None:
-        if new_start is None:
-            shape = (page_table.shape[0], max_new)
-        elif total is None:
-            raise ValueError("new_start needs total, the number of rows")
-        else:
-            shape = (int(total),)
-        out = tuple(_empty(shape, t, page_table.device, stream) for t in (torch.int64, torch.int32))
-    slots, positions = out
+    slots, positions = (None, None) if out is None else out
     free, count = pool["free"], pool["count"]
-    d, gpu = _assign_plan(_meta(free), _meta(count), _meta(page_table), _meta(held), _meta(ctx_lens), int(page_size),
-                          _meta(new_start), max_new, _meta(parents), _meta(slots), _meta(positions), _meta(row_status))
+    d, shape, gpu = _assign_plan(_meta(free), _meta(count), _meta(page_table), _meta(held), _meta(ctx_lens), int(page_size),
+                                 _meta(new_start), max_new, None if total is None else int(total), _meta(parents), _meta(slots),
+                                 _meta(positions), _meta(row_status))
+    if out is None and max_new > 0:
+        device = ctx_lens.device
+        slots, positions = _empty(shape, torch.int64, device, stream), _empty(shape, torch.int32, device, stream)
     _call(gpu, "sv_kv_assign", d, free.data_ptr(), count.data_ptr(), page_table.data_ptr(), held.data_ptr(), ctx_lens.data_ptr(),
-          _at(new_start), _at(parents), slots.data_ptr() or None, positions.data_ptr() or None, _at(row_status),
-          _stream_of(stream, gpu))
+          _at(new_start), _at(parents), _at(slots) or None, _at(positions) or None, _at(row_status), _stream_of(stream, gpu))
     return dict(slots=slots, positions=positions)
 
 

@@ -19,6 +19,11 @@ from .kvcache import (_KEPT, _PER_SEQUENCE, _at, _call, _contiguous, _count, _em
 from .verify import _code
 
 
+def _empty_like(x, stream):
+    """A contiguous result of x's shape and type (see _empty)."""
+    return _empty(x.shape, x.dtype, x.device, stream)
+
+
 def _token_rows(m, name):
     """_rows of [B, n, heads, dim] or [total, heads, dim], whichever it is."""
     if len(m.shape) not in (3, 4):
@@ -28,6 +33,7 @@ def _token_rows(m, name):
 
 @functools.lru_cache(maxsize=_KEPT)
 def _rope_plan(q, k, positions, inv_freq, sections, adjacent, q_out, k_out):
+    """q_out None: the call makes its results itself."""
     q, k, p, f = _see(q, "q"), _see(k, "k"), _see(positions, "positions"), _see(inv_freq, "inv_freq")
     q_out, k_out = _see(q_out, "out[0]"), _see(k_out, "out[1]")
     lead = q.shape[:-2]
@@ -43,17 +49,20 @@ def _rope_plan(q, k, positions, inv_freq, sections, adjacent, q_out, k_out):
     sections = (half,) if sections is None and axes == 1 else sections
     if sections is None or len(sections) != axes or min(sections) < 0 or sum(sections) != half:
         raise ValueError("sections must have one entry for each axis of positions, and inv_freq's length as their sum")
-    if q_out.shape != q.shape or q_out.dtype != q.dtype:
-        raise ValueError("out[0] must match q in shape and dtype")
-    _, _, _, *q_out_strides = _token_rows(q_out, "out[0]")
-    k_heads, k_strides, k_out_strides = 0, (dim, dim), (dim, dim)
+    q_out_strides, k_heads, k_strides, k_out_strides = (heads * dim, dim), 0, (dim, dim), (dim, dim)
+    if q_out is not None:
+        if q_out.shape != q.shape or q_out.dtype != q.dtype:
+            raise ValueError("out[0] must match q in shape and dtype")
+        _, _, _, *q_out_strides = _token_rows(q_out, "out[0]")
     if k is not None:
         k_rows, k_heads, k_dim, *k_strides = _token_rows(k, "k")
         if k.shape[:-2] != lead or k_dim != dim or k.dtype != q.dtype:
             raise ValueError("k must match q in tokens, dim and dtype")
-        if k_out is None or k_out.shape != k.shape or k_out.dtype != k.dtype:
-            raise ValueError("out[1] must match k in shape and dtype")
-        _, _, _, *k_out_strides = _token_rows(k_out, "out[1]")
+        k_out_strides = (k_heads * dim, dim)
+        if q_out is not None:
+            if k_out is None or k_out.shape != k.shape or k_out.dtype != k.dtype:
+                raise ValueError("out[1] must match k in shape and dtype")
+            _, _, _, *k_out_strides = _token_rows(k_out, "out[1]")
     d = N.RopeDesc(rows, heads, k_heads, dim, 2 * half, axes, int(adjacent), _code(q), rows, *q_strides, *k_strides,
                    *q_out_strides, *k_out_strides)
     d.axis[:half] = [a for a, n in enumerate(sections) for _ in range(n)]
@@ -70,11 +79,11 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
     radians a position of every pair; dims beyond 2 * len(inv_freq) stay.
     Pairs are (i, i + len(inv_freq)), with ``adjacent`` (2i, 2i + 1).  Returns
     (q, k) in new memory, or in ``out``, which may be (q, k) themselves."""
-    if out is None:
-        out = (_empty(q.shape, q.dtype, q.device, stream), None if k is None else _empty(k.shape, k.dtype, k.device, stream))
-    q_out, k_out = out
+    q_out, k_out = (None, None) if out is None else out
     d, gpu = _rope_plan(_meta(q), _meta(k), _meta(positions), _meta(inv_freq),
                         None if sections is None else tuple(int(n) for n in sections), bool(adjacent), _meta(q_out), _meta(k_out))
+    if out is None:
+        q_out, k_out = _empty_like(q, stream), None if k is None else _empty_like(k, stream)
     _call(gpu, "sv_rope", d, q.data_ptr(), _at(k), positions.data_ptr(), inv_freq.data_ptr(), q_out.data_ptr(),
           None if k is None else k_out.data_ptr(), _stream_of(stream, gpu))
     return q_out, None if k is None else k_out
@@ -82,6 +91,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
 
 @functools.lru_cache(maxsize=_KEPT)
 def _prompt_plan(q, k, v, start, max_new, scale, window, sinks, out, status):
+    """out None: the call makes its result itself."""
     q, k, v, out = _see(q, "q"), _see(k, "k"), _see(v, "v"), _see(out, "out")
     ragged = start is not None
     if not ragged and len(q.shape) != 4:
@@ -94,9 +104,11 @@ def _prompt_plan(q, k, v, start, max_new, scale, window, sinks, out, status):
     nv, hv, dv, *v_strides = _rows(v, "v", B, ragged)
     if (nk, dk) != (n, dim) or (nv, hv, dv) != (nk, kv_heads, dk) or k.shape != v.shape or not q.dtype == k.dtype == v.dtype:
         raise ValueError("q, k and v must match in tokens, dim and dtype, and k and v in heads")
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must match q in shape and dtype")
-    _, _, _, *out_strides = _rows(out, "out", B, ragged)
+    out_strides = (heads * dim, dim)
+    if out is not None:
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must match q in shape and dtype")
+        _, _, _, *out_strides = _rows(out, "out", B, ragged)
     _int32(status, "row_status", B, _PER_SEQUENCE)
     a = N.PromptAttentionDesc(B, heads, kv_heads, dim, _new(start, max_new, q, B), n, _code(q), dim ** -0.5 if scale is None else scale,
                               _count(window, "window"), _count(sinks, "sinks"), *q_strides, *k_strides, *v_strides, *out_strides)
@@ -113,10 +125,10 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, new_s
     ``new_start`` [B + 1] and ``max_new``, the most tokens of a sequence),
     float32 or bfloat16; ``scale`` defaults to 1 / sqrt(dim).  Returns out like
     q, and with ``lse`` the log-sum-exp [..., heads] float32 as well."""
-    if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
     a, gpu = _prompt_plan(_meta(q), _meta(k), _meta(v), _meta(new_start), None if max_new is None else int(max_new),
                           None if scale is None else float(scale), int(window), int(sinks), _meta(out), _meta(row_status))
+    if out is None:
+        out = _empty_like(q, stream)
     sums = _empty(q.shape[:-1], torch.float32, q.device, stream) if lse else None
     _call(gpu, "sv_prompt_attention", a, q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(new_start), out.data_ptr(), _at(sums),
           _at(row_status), _stream_of(stream, gpu))

@@ -50,6 +50,10 @@ class Both:
             kw.update(new_start=_gpu(starts), total=total, out=out)
         got = self.sv.kv_assign(self.pool, self.dev_table, self.dev_held, _gpu(ctx), self.page, **kw)
         self.same()
+        assert st.tolist() == flags
+        if max_new == 0 and not ragged:
+            assert got == dict(slots=None, positions=None)
+            return flags
         want = [np.array([d.get(r, -77) for r in range(total)]) for d in (slots, positions)]
         assert got["slots"].dtype == torch.int64 and got["positions"].dtype == torch.int32
         claims = np.zeros(total, int)  # (a row that two sequences claim is one's or the other's)
@@ -57,7 +61,6 @@ class Both:
             claims[max(first, 0):max(first + n, 0)] += 0 <= n <= max_new and 0 <= first <= total - n
         for have, expect in zip((got["slots"], got["positions"]), want):
             np.testing.assert_array_equal(have.flatten().cpu().numpy()[claims < 2], expect[claims < 2])
-        assert st.tolist() == flags
         assert given is not None or ragged or tuple(got["slots"].shape) == (self.batch, max_new)
         return flags
 
@@ -209,3 +212,17 @@ def test_captured_on_another_stream_and_replayed(sv):
         b.count, slots, positions, _ = PO.assign(b.free, b.count, b.table, b.held, lens, 16, [5, 4], [0, 5], 9, 5)
         b.same()
         assert got["slots"].tolist() == [slots[r] for r in range(9)] and got["positions"].tolist() == [positions[r] for r in range(9)]
+
+
+@pytest.mark.parametrize("batch,columns,most", [(3, 6000, 90_000), (1000, 17, 200), (1024, 40, 33)])
+def test_calls_that_several_blocks_share(sv, batch, columns, most):
+    """Many pages or tokens: gives, takes and places of more than one block."""
+    g = np.random.default_rng(batch)
+    b = Both(sv, int(0.8 * batch * columns), batch, columns, 16, g)
+    for step in range(4):
+        ctx = [int(x) for x in g.integers(0, 16 * columns - most, batch)]
+        new = [int(x) for x in g.integers(0, most + 1, batch)]
+        parents = [p for m in new for p in [-1][:m] + [int(x) for x in (g.integers(0, 9, max(0, m - 1)) % np.arange(1, max(1, m)))]] + 3 * [-1] if step == 2 else None
+        b.call(ctx, new, parents, rows_behind=3)
+    b.call([0] * batch, [0] * batch, ragged=False)
+    assert b.count == b.size

@@ -103,7 +103,7 @@ def _assign_py(**kw):
     dict(page_table=_ints(4, 5, strides=(10, 2))), dict(page_table=_ints(20)), dict(out=(_ints(4, 3), _ints(4, 3))),
     dict(out=(Stand((4, 3), torch.int64), _ints(12))), dict(max_new=4), dict(max_new=-1), dict(max_new=2 ** 31, new_start=_ints(5)),
     dict(new_start=_ints(4)), dict(parents=_ints(11)), dict(row_status=_ints(5)), dict(held=_ints(4, device="cuda:1")),
-    dict(held=_ints(4, device="cpu")), dict(page_size=2 ** 31), dict(new_start=_ints(5), out=None),
+    dict(held=_ints(4, device="cpu")), dict(page_size=2 ** 31), dict(new_start=_ints(5), out=None), dict(new_start=_ints(5), total=11), dict(total=11),
 ], ids=lambda d: "-".join(d))
 def test_assign_refuses_tensors(N, bad):
     with pytest.raises(ValueError):
