@@ -15,6 +15,11 @@ namespace sv {
 
 constexpr int kRows = 128;  // of a tile of queries
 
+// A block's tile of keys or values that is never loaded, in builds that test what happens when waits run out.
+#ifndef SV_PROMPT_LOST_TILE
+#define SV_PROMPT_LOST_TILE -1
+#endif
+
 struct Item {
   int row0, n, h;        // the sequence's rows, the kv head
   int tok0;              // first token
@@ -37,7 +42,7 @@ __device__ __forceinline__ void sort_sequences(const PromptView& a, Sequences& s
   __syncthreads();
   int rank = -1, before = 0;
   PromptSpan s{};
-  for (int b = threadIdx.x; b < a.batch; b += threads) {  // (a thread has one at most: no block is smaller than kSorted)
+  for (int b = threadIdx.x; b < a.batch; b += threads) {  // (one for a thread at most: no block is smaller than kSorted)
     s = prompt_span(a, b);
     rank = 0;
     for (int o = 0; o < a.batch; ++o) {

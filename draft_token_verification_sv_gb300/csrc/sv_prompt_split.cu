@@ -243,7 +243,7 @@ __device__ __forceinline__ bool load_rows(const E* from, Place place, int d0, in
 template <int DP, typename E>
 __device__ bool load_role(const PromptView& a, int tpt, Shared& sh, uint8_t* q_at, uint8_t* stages, bool vec) {
   using C = Config<DP, E>;
-  int unit = 0;
+  int unit = 0, loaded = 0;
   for (int items = 0;; ++items) {
     if (!warp_wait(sh, sh.item_full[items % kItems], items / kItems)) return false;
     Item& it = sh.item[items % kItems];
@@ -267,6 +267,7 @@ __device__ bool load_role(const PromptView& a, int tpt, Shared& sh, uint8_t* q_a
       ++unit;
     };
     const auto keys = [&](int t) {
+      if (loaded++ == SV_PROMPT_LOST_TILE) return false;
       const int kb = key_of<kKeys>(it, t);
       for (int u = 0; u < C::kScoreUnits; ++u) {
         if (!begin()) return false;
@@ -286,6 +287,7 @@ __device__ bool load_role(const PromptView& a, int tpt, Shared& sh, uint8_t* q_a
     if (!keys(0)) return false;
     for (int t = 0; t < tiles; ++t) {
       if (t + 1 < tiles && !keys(t + 1)) return false;
+      if (loaded++ == SV_PROMPT_LOST_TILE) return false;
       const int kb = key_of<kKeys>(it, t);
       for (int u = 0; u < C::kValueUnits; ++u) {
         if (!begin()) return false;

@@ -29,6 +29,8 @@ namespace {
 
 constexpr int kKeys = 128;   // of a tile of keys
 constexpr int kItems = 4;    // items that may be known ahead
+constexpr int kSoftmaxRegisters = 208, kOtherRegisters = 88;  // of 168 at launch, where there are three groups of four warps
+static_assert(8 * kSoftmaxRegisters + 4 * kOtherRegisters <= 12 * 168, "registers of a block");
 constexpr float kLargeSum = 8192.0f, kLargeLog = 13.0f;
 
 template <int DP> struct Config {
@@ -44,7 +46,6 @@ template <int DP> struct Config {
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
   // tensor memory, in columns: two places for scores, then O
   static constexpr int kS = 0, kO = 2 * kKeys;
-  static constexpr int kSoftmaxRegisters = 208, kOtherRegisters = 88;  // (of 168 at launch, where there are three groups of four warps)
 };
 
 struct Shared {
@@ -69,11 +70,6 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar) {
 }
 
 // ---- loading ----
-
-// A block's tile that is never copied, in builds that test what happens when waits run out.
-#ifndef SV_PROMPT_LOST_TILE
-#define SV_PROMPT_LOST_TILE -1
-#endif
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -593,10 +589,10 @@ __global__ void __launch_bounds__(Config<DP>::kThreads, 1)
   tc::fence_after();
   const uint32_t tmem = sh.tmem;
   if (warp < C::kSoftmaxWarps) {
-    if constexpr (C::NQ == 2) tc::registers_up<C::kSoftmaxRegisters>();
+    if constexpr (C::NQ == 2) tc::registers_up<kSoftmaxRegisters>();
     softmax_role<DP>(a, tpt, f, sh, tmem, out_vec32);
   } else {
-    if constexpr (C::NQ == 2) tc::registers_down<C::kOtherRegisters>();
+    if constexpr (C::NQ == 2) tc::registers_down<kOtherRegisters>();
     if (warp == C::kSoftmaxWarps) {
       Finder finder{};
       Loads under{};
