@@ -58,6 +58,7 @@ struct Shared {
   Sequences sequences;
   uint32_t tmem;
   int gave_up;
+  int look[10];          // are there rows that do not see all of the values in a stage?
   int claimed, finished[8];  // items known, and done with by each warp that writes results
 };
 
@@ -145,12 +146,14 @@ __device__ bool load_role(const PromptView& a, const Maps& maps, int tpt, Shared
         const Turn turn = turn_of<C::NQ>(u, it.tiles);
         const int kb = key_of<kKeys>(it, turn.t);
         const CUtensorMap* map = turn.keys ? &maps.k : &maps.v;
+        const bool look = !turn.keys && partly_seen<kKeys, C::NQ>(a, it, tpt, turn.t);
 #pragma unroll 1
         for (int half = 0; half < C::kHalves; ++half) {
           const int unit = under.units, stage = unit % C::kStages;
           if (unit >= C::kStages && !warp_wait(sh, sh.kv_free[stage], unit / C::kStages - 1)) return false;
           const uint32_t bar = tc::smem_address(&sh.kv_full[stage]);
           if (lane == 0) {
+            sh.look[stage] = look;
             tc::barrier_expect(bar, C::kUnitBytes);
 #pragma unroll
             for (int d = 0; d < C::kUnitDims; d += 64)
@@ -201,7 +204,7 @@ __device__ __forceinline__ uint32_t finite_of(uint32_t w) { return w & ~__vcmpge
 
 // It takes part in every copy's way, so that it is never a round of the stages behind.
 template <int DP>
-__device__ bool check_role(const PromptView& a, int tpt, Shared& sh, uint8_t* kv) {
+__device__ bool check_role(Shared& sh, uint8_t* kv) {
   using C = Config<DP>;
   const int tid = threadIdx.x - 32 * (C::kSoftmaxWarps + 2);
   int unit = 0;
@@ -211,32 +214,27 @@ __device__ bool check_role(const PromptView& a, int tpt, Shared& sh, uint8_t* kv
     const int tiles = it.tiles;
     if (tiles < 0) return true;
 #pragma unroll 1
-    for (int u = 0; u < 2 * tiles; ++u) {
-      const Turn turn = turn_of<C::NQ>(u, tiles);
-      const bool look = !turn.keys && partly_seen<kKeys, C::NQ>(a, it, tpt, turn.t);
-#pragma unroll 1
-      for (int half = 0; half < C::kHalves; ++half, ++unit) {
-        const int stage = unit % C::kStages;
-        if (!warp_wait(sh, sh.kv_full[stage], unit / C::kStages)) return false;
-        if (look) {
-          uint4* at = reinterpret_cast<uint4*>(kv + stage * C::kUnitBytes);
-          bool found = false;
+    for (int u = 0; u < 2 * C::kHalves * tiles; ++u, ++unit) {
+      const int stage = unit % C::kStages;
+      if (!warp_wait(sh, sh.kv_full[stage], unit / C::kStages)) return false;
+      if (sh.look[stage]) {
+        uint4* at = reinterpret_cast<uint4*>(kv + stage * C::kUnitBytes);
+        bool found = false;
 #pragma unroll 4
-          for (int c = tid; c < C::kUnitBytes / 16; c += 32 * C::kCheckWarps) {
-            uint4 v = at[c];
-            // the largest magnitude of each half word: 0x7f80 and more is not finite
-            const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-            if (__vcmpgeu2(m, 0x7f807f80u)) {
-              found = true;
-              at[c] = make_uint4(finite_of(v.x), finite_of(v.y), finite_of(v.z), finite_of(v.w));
-            }
+        for (int c = tid; c < C::kUnitBytes / 16; c += 32 * C::kCheckWarps) {
+          uint4 v = at[c];
+          // the largest magnitude of each half word: 0x7f80 and more is not finite
+          const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+          if (__vcmpgeu2(m, 0x7f807f80u)) {
+            found = true;
+            at[c] = make_uint4(finite_of(v.x), finite_of(v.y), finite_of(v.z), finite_of(v.w));
           }
-          if (found) it.dirty = 1;
-          tc::publish_shared();
-          warp_arrive(sh.checked[stage]);
         }
-        warp_arrive(sh.kv_free[stage]);
+        if (found) it.dirty = 1;
+        tc::publish_shared();
+        warp_arrive(sh.checked[stage]);
       }
+      warp_arrive(sh.kv_free[stage]);
     }
     warp_arrive(sh.item_free[items % kItems]);
   }
@@ -244,98 +242,137 @@ __device__ bool check_role(const PromptView& a, int tpt, Shared& sh, uint8_t* kv
 
 // ---- products ----
 
+// A place in the ring of stages, and the parity of its barriers' phase.
+template <int STAGES>
+struct Ring {
+  int stage;
+  uint32_t parity;
+  __device__ __forceinline__ Ring next() const {
+    return stage + 1 == STAGES ? Ring{0, parity ^ 1u} : Ring{stage + 1, parity};
+  }
+};
+
+// One thread.  Eight products or so may wait for the tensor core, 65 cycles each: what the thread does between two batches is kept
+// shorter than that (parities in bits, each tile of keys and values waited for once).
 template <int DP>
-__device__ bool product_role(const PromptView& a, int tpt, Shared& sh, uint32_t q_at, uint32_t kv_at, uint32_t tmem) {
+__device__ bool product_role(const PromptView& a, Shared& sh, uint32_t q_at, uint32_t kv_at, uint32_t tmem) {
   using C = Config<DP>;
   constexpr uint32_t kScores = tc::product_kind_bf16(kKeys, false), kValues = tc::product_kind_bf16(C::kUnitDims, true);
-  const auto wait = [&](uint64_t& bar, int n) {
-    const bool ok = tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up);
-    tc::fence_after();
-    return ok;
-  };
+  const auto wait = [&](uint64_t& bar, uint32_t parity) { return tc::barrier_wait(tc::smem_address(&bar), parity & 1u, &sh.gave_up); };
   const auto arrive = [&](uint64_t& bar) { tc::products_arrive(tc::smem_address(&bar)); };
-  uint32_t checks = 0;  // parity of `checked` for each stage
-  int unit = 0, done[2] = {0, 0}, weighed[2] = {0, 0}, tile = 0;
+  const uint64_t k0 = tc::tile_descriptor(kv_at, 16, 1024), q0 = tc::tile_descriptor(q_at, 16, 1024);
+  const uint64_t v0 = tc::tile_descriptor(kv_at, C::kBlockBytes, 1024);
+  // S in place s (+)= tile i of queries, from `half` on, with the keys of a stage
+  const auto score = [&](int i, int half, int s, int stage) {
+    const uint64_t q = q0 + (i * C::kQueryBytes + half * (kRows * 256) >> 4), k = k0 + (stage * C::kUnitBytes >> 4);
+#pragma unroll
+    for (int d = 0; d < C::kUnitDims / 16; ++d) {
+      const int off = (d >> 2) * (kRows * 128) + (d & 3) * 32 >> 4;  // (tiles of queries and keys are of one height)
+      tc::product_f16(tmem + C::kS + s * kKeys, q + off, k + off, kScores, d > 0 || half > 0);
+    }
+  };
+  // O of tile i, from `half` on, (+)= P in place s times the values of a stage
+  const auto weigh = [&](int i, int half, int s, int stage, bool add) {
+    const uint64_t v = v0 + (stage * C::kUnitBytes >> 4);
+#pragma unroll
+    for (int k = 0; k < kKeys / 16; ++k)
+      tc::product_f16(tmem + C::kO + i * DP + half * C::kUnitDims, tmem + C::kS + s * kKeys + k * 8, v + (k * 2048 >> 4), kValues, k > 0 || add);
+  };
+  uint32_t checks = 0;                    // parity of `checked` for each stage
+  uint32_t q_par = 0, p_par = 0, o_par = 3;  // of q_full, p_ready and o_free for each tile (a barrier's phase before its first is over)
+  const auto values_ready = [&](const Ring<C::kStages>& v) {
+    if (!wait(sh.kv_full[v.stage], v.parity)) return false;
+    if (sh.look[v.stage]) {
+      if (!wait(sh.checked[v.stage], checks >> v.stage)) return false;
+      checks ^= 1u << v.stage;
+    }
+    return true;
+  };
+  Ring<C::kStages> at{0, 0};
+  int tile = 0;
   for (int items = 0;; ++items) {
     if (!wait(sh.item_full[items % kItems], items / kItems)) return false;
-    const Item it = sh.item[items % kItems];
+    const int tiles = sh.item[items % kItems].tiles, count0 = sh.item[items % kItems].count[0], count1 = sh.item[items % kItems].count[1];
     tc::barrier_arrive(tc::smem_address(&sh.item_free[items % kItems]));
-    if (it.tiles < 0) return true;
-    // S of tile i of queries with the keys of unit u, to place s
-    const auto score = [&](int i, int t, int u, int s, bool last_use) {
-      if (t == 0 && !wait(sh.q_full[i], i ? done[1] : done[0])) return false;
-#pragma unroll 1
-      for (int half = 0; half < C::kHalves; ++half) {
-        const int stage = (u + half) % C::kStages;
-        if (!wait(sh.kv_full[stage], (u + half) / C::kStages)) return false;
-        const uint64_t k = tc::tile_descriptor(kv_at + stage * C::kUnitBytes, 16, 1024);
-        const uint64_t q = tc::tile_descriptor(q_at + i * C::kQueryBytes + half * (kRows * 256), 16, 1024);
-#pragma unroll
-        for (int d = 0; d < C::kUnitDims / 16; ++d) {
-          constexpr int kStep = 32 >> 4;
-          const int off = (d >> 2) * (kRows * 128 >> 4) + (d & 3) * kStep;  // (tiles of queries and keys are of one height)
-          tc::product_f16(tmem + C::kS + s * kKeys, q + off, k + off, kScores, d > 0 || half > 0);
-        }
-        if (last_use) arrive(sh.kv_free[stage]);
-      }
-      arrive(sh.s_full[s]);
-      if (t + 1 == (i ? it.count[1] : it.count[0])) arrive(sh.q_free[i]);
-      return true;
-    };
-    // O of tile i (+)= P in place s times the values of unit u
-    const auto weigh = [&](int i, int t, int u, int s, int uses, bool check, bool last_use) {
-      const int before = i ? done[1] : done[0];
-      if (t == 0 && before > 0 && !wait(sh.o_free[i], before - 1)) return false;
-      if (!wait(sh.p_ready[s], uses)) return false;
-#pragma unroll 1
-      for (int half = 0; half < C::kHalves; ++half) {
-        const int stage = (u + half) % C::kStages;
-        if (!wait(sh.kv_full[stage], (u + half) / C::kStages)) return false;
-        if (check && !wait(sh.checked[stage], checks >> stage)) return false;
-        const uint64_t v = tc::tile_descriptor(kv_at + stage * C::kUnitBytes, C::kBlockBytes, 1024);
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          tc::product_f16(tmem + C::kO + i * DP + half * C::kUnitDims, tmem + C::kS + s * kKeys + k * 8, v + k * (2048 >> 4), kValues, k > 0 || t > 0);
-        if (last_use) {
-          if (check) checks ^= 1u << stage;
-          arrive(sh.kv_free[stage]);
-        }
-      }
-      arrive(sh.pv_done[i]);
-      return true;
-    };
+    if (tiles < 0) return true;
     if (C::NQ == 2) {
       // after a tile's sums the next one's scores, which take the place of its weights
+      Ring<C::kStages> k = at, v = at;
 #pragma unroll 1
-      for (int t = -1; t < it.tiles; ++t) {
-        const bool check = t >= 0 && partly_seen<kKeys, C::NQ>(a, it, tpt, t);
+      for (int t = -1;; ++t) {
+        bool k_ready = false, v_ready = false;
 #pragma unroll 1
-        for (int i = 0; i < C::NQ; ++i) {
-          const int count = i ? it.count[1] : it.count[0];
+        for (int i = 0; i < 2; ++i) {
+          const int count = i ? count1 : count0;
           // (the last of the tiles of queries that need a tile of keys lets it go)
           if (t >= 0 && t < count) {
-            if (!weigh(i, t, unit + 2 * t + 1, i, i ? weighed[1] : weighed[0], check, i == 1 || t >= it.count[1])) return false;
-            ++(i ? weighed[1] : weighed[0]);
+            if (t == 0) {
+              if (!wait(sh.o_free[i], o_par >> i)) return false;
+              o_par ^= 1u << i;
+            }
+            if (!v_ready && !values_ready(v)) return false;
+            v_ready = true;
+            if (!wait(sh.p_ready[i], p_par >> i)) return false;
+            p_par ^= 1u << i;
+            tc::fence_after();
+            weigh(i, 0, i, v.stage, t > 0);
+            if (i == 1 || t >= count1) arrive(sh.kv_free[v.stage]);
+            arrive(sh.pv_done[i]);
           }
-          if (t + 1 < count && !score(i, t + 1, unit + 2 * t + 2, i, i == 1 || t + 1 >= it.count[1])) return false;
+          if (t + 1 < count) {
+            if (t < 0) {
+              if (!wait(sh.q_full[i], q_par >> i)) return false;
+              q_par ^= 1u << i;
+            }
+            if (!k_ready && !wait(sh.kv_full[k.stage], k.parity)) return false;
+            k_ready = true;
+            tc::fence_after();
+            score(i, 0, i, k.stage);
+            if (i == 1 || t + 1 >= count1) arrive(sh.kv_free[k.stage]);
+            arrive(sh.s_full[i]);
+            if (t + 2 == count) arrive(sh.q_free[i]);
+          }
         }
+        if (t + 1 == tiles) break;
+        v = k.next();
+        k = v.next();
       }
-      unit += 2 * it.tiles;
-      done[0] += it.count[0] > 0;
-      done[1] += it.count[1] > 0;
+      at = k;
     } else {
+      // each tile's scores before the sums of the one before it
 #pragma unroll 1
-      for (int t = -1; t < it.tiles; ++t) {
-        if (t + 1 < it.tiles) {
-          if (!score(0, t + 1, unit, tile + t + 1 & 1, true)) return false;
-          unit += C::kHalves;
+      for (int t = -1; t < tiles; ++t) {
+        if (t + 1 < tiles) {
+          if (t < 0) {
+            if (!wait(sh.q_full[0], q_par)) return false;
+            q_par ^= 1u;
+          }
+#pragma unroll 1
+          for (int half = 0; half < C::kHalves; ++half, at = at.next()) {
+            if (!wait(sh.kv_full[at.stage], at.parity)) return false;
+            tc::fence_after();
+            score(0, half, tile + t + 1 & 1, at.stage);
+            arrive(sh.kv_free[at.stage]);
+          }
+          arrive(sh.s_full[tile + t + 1 & 1]);
+          if (t + 2 == tiles) arrive(sh.q_free[0]);
         }
         if (t < 0) continue;
-        if (!weigh(0, t, unit, tile + t & 1, tile + t >> 1, partly_seen<kKeys, C::NQ>(a, it, tpt, t), true)) return false;
-        unit += C::kHalves;
+        if (t == 0) {
+          if (!wait(sh.o_free[0], o_par)) return false;
+          o_par ^= 1u;
+        }
+        if (!wait(sh.p_ready[tile + t & 1], static_cast<uint32_t>(tile + t >> 1))) return false;
+#pragma unroll 1
+        for (int half = 0; half < C::kHalves; ++half, at = at.next()) {
+          if (!values_ready(at)) return false;
+          tc::fence_after();
+          weigh(0, half, tile + t & 1, at.stage, t > 0);
+          arrive(sh.kv_free[at.stage]);
+        }
+        arrive(sh.pv_done[0]);
       }
-      tile += it.tiles;
-      ++done[0];
+      tile += tiles;
     }
   }
 }
@@ -599,14 +636,14 @@ __global__ void __launch_bounds__(Config<DP>::kThreads, 1)
       if (!load_role<DP>(a, maps, tpt, sh, q_at, kv_at, finder, under)) end_loads<DP>(a, tpt, sh, finder, under);
     } else if (warp == C::kSoftmaxWarps + 1) {
       if (tc::elected()) {
-        product_role<DP>(a, tpt, sh, q_at, kv_at, tmem);
+        product_role<DP>(a, sh, q_at, kv_at, tmem);
         int unused = 0;
         tc::products_arrive(tc::smem_address(&sh.last));
         tc::barrier_wait(tc::smem_address(&sh.last), 0, &unused, tc::kEndCycles);
       }
       __syncwarp();
     } else {
-      check_role<DP>(a, tpt, sh, tiles + C::NQ * C::kQueryBytes);
+      check_role<DP>(sh, tiles + C::NQ * C::kQueryBytes);
     }
   }
   tc::fence_before();
