@@ -692,7 +692,8 @@ sv_status launch(const PromptView& a, cudaStream_t stream) {
 bool prompt_takes_tiles(const PromptView& a, sv_dtype dtype) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
   const int64_t strides = a.q_row | a.q_head | a.k_row | a.k_head | a.v_row | a.v_head;
-  return dtype == SV_BF16 && at % 16 == 0 && strides % 8 == 0 && a.total_new > 0;
+  // (a tensor map holds strides of less than 2^40 bytes)
+  return dtype == SV_BF16 && at % 16 == 0 && strides % 8 == 0 && strides < int64_t{1} << 39 && a.total_new > 0;
 }
 
 sv_status prompt_tiles(const PromptView& a, cudaStream_t stream) {

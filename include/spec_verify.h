@@ -624,7 +624,8 @@ typedef struct sv_kv_assign_desc {
  *   ctx_lens [B], new_start [B + 1] or NULL, parents [total_new] or NULL.
  *   slots      optional [total_new] int64;  positions optional [total_new] int32.
  *   row_status optional [B] int32 (SV_ROW_*).
- * No two of these may share memory (refused where one of them is written).
+ * No two of these may share memory (refused where one of them is written),
+ * and calls that use one pool, table or held run one after the other.
  */
 sv_status sv_kv_assign(const sv_kv_assign_desc* desc, int32_t* free_pages, int32_t* free_count, int32_t* page_table,
                        int32_t* held, const int32_t* ctx_lens, const int32_t* new_start, const int32_t* parents,

@@ -192,26 +192,33 @@ def test_slots_beyond_32_bits(sv):
     assert want.max() > 2 ** 31
 
 
-def test_captured_on_another_stream_and_replayed(sv):
+@pytest.mark.parametrize("batch,columns", [(2, 20), (40, 500), (1100, 20)])
+def test_captured_on_another_stream_and_replayed(sv, batch, columns):
+    """One launch of a block, of many, and of more sequences than that takes."""
     import torch
     g = np.random.default_rng(4)
-    b = Both(sv, 40, 2, 20, 16, g)
-    ctx, start = _gpu([0, 0]), _gpu([0, 5, 9])
+    b = Both(sv, 20 * batch, batch, columns, 16, g)
+    new = [int(x) for x in g.integers(0, 6, batch)]
+    starts = np.concatenate([[0], np.cumsum(new)]).tolist()
+    total = starts[-1]
+    ctx, start = _gpu([0] * batch), _gpu(starts)
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
-        got = sv.kv_assign(b.pool, b.dev_table, b.dev_held, ctx, 16, new_start=start, max_new=5, total=9)
+        kw = dict(new_start=start, max_new=5, total=total)
+        got = sv.kv_assign(b.pool, b.dev_table, b.dev_held, ctx, 16, **kw)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
-            sv.kv_assign(b.pool, b.dev_table, b.dev_held, ctx, 16, new_start=start, max_new=5, total=9, out=(got["slots"], got["positions"]))
-    b.count, slots, positions, _ = PO.assign(b.free, b.count, b.table, b.held, [0, 0], 16, [5, 4], [0, 5], 9, 5)
-    for lens in ([30, 100], [16, 3], [0, 290]):
+            sv.kv_assign(b.pool, b.dev_table, b.dev_held, ctx, 16, out=(got["slots"], got["positions"]), **kw)
+    b.count, slots, positions, _ = PO.assign(b.free, b.count, b.table, b.held, [0] * batch, 16, new, starts[:-1], total, 5)
+    for step in range(3):
+        lens = [int(x) for x in g.integers(0, 16 * 20 - 5, batch)]
         ctx.copy_(_gpu(lens))
         graph.replay()
         torch.cuda.synchronize()
-        b.count, slots, positions, _ = PO.assign(b.free, b.count, b.table, b.held, lens, 16, [5, 4], [0, 5], 9, 5)
+        b.count, slots, positions, _ = PO.assign(b.free, b.count, b.table, b.held, lens, 16, new, starts[:-1], total, 5)
         b.same()
-        assert got["slots"].tolist() == [slots[r] for r in range(9)] and got["positions"].tolist() == [positions[r] for r in range(9)]
+        assert got["slots"].tolist() == [slots[r] for r in range(total)] and got["positions"].tolist() == [positions[r] for r in range(total)]
 
 
 @pytest.mark.parametrize("batch,columns,most", [(3, 6000, 90_000), (1000, 17, 200), (1024, 40, 33)])

@@ -159,6 +159,20 @@ def test_strides_and_alignments(sv, dtype, place, dim):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("which", range(3))
+@pytest.mark.parametrize("stride", [2 ** 38, 2 ** 39, 2 ** 40 - 8])
+def test_strides_beyond_those_of_a_tensor_map(sv, dtype, which, stride):
+    """(Of a single row, which are never stepped over.)"""
+    import torch
+    g = np.random.default_rng(0)
+    x = [to_gpu(x, dtype) for x in _inputs(g, dtype, 1, 4, 2, 64)]
+    kw = dict(new_start=to_gpu(np.array([0, 1], np.int32)), max_new=1)
+    want = sv.prompt_attention(*x, **kw)
+    x[which] = x[which].as_strided(x[which].shape, (stride, 64, 1))
+    assert torch.equal(sv.prompt_attention(*x, **kw), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shift", [1, 2, 4, 8, 16])
 def test_results_with_strides_of_their_own(sv, dtype, shift):
     import torch
