@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) kv_assign_few_kernel(AssignView a) {
   __shared__ long long scratch[33], gives[kThreads], lacks[kThreads], brings[kThreads];
   __shared__ int ctxs[kThreads], rows[kThreads], helds[kThreads], wants[kThreads];  // wants: -1 where the sequence is left out
   const int tid = threadIdx.x, batch = a.w.batch, size = a.w.num_pages, shift = a.w.page_shift;
-  if (WHAT != kAll) wait_for_stream();
+  wait_for_stream();
   const int count = min(max(*a.free_count, 0), size);
   Need n{0, 0, false};
   KvSpan s{0, 0, 0, false};
@@ -299,8 +299,7 @@ sv_status kv_assign(const sv_kv_assign_desc& d, int32_t* free_pages, int32_t* fr
     const int64_t tokens = slots || positions ? d.total_new : 0;
     const int64_t pages = static_cast<int64_t>(d.batch) * d.max_pages;
     if (pages <= kManyPages && tokens <= kManyTokens) {
-      kv_assign_few_kernel<kAll><<<1, kThreads, 0, stream>>>(a);
-      if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+      if (launch_early(kv_assign_few_kernel<kAll>, dim3(1), dim3(kThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
       note_launch(stream);
       return SV_OK;
     }

@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_split_kernel(const __grid_
     tc::publish_shared();
   }
   if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), 512);
+  wait_for_stream();
   sort_sequences(a, sh.sequences, tpt, kThreads);
   if (blockIdx.x == 0) flag_lengths(a, kThreads);
   tc::fence_before();
@@ -646,8 +647,9 @@ sv_status launch(const PromptView& a, cudaStream_t stream) {
   const bool vec = at % 16 == 0 && strides % 4 == 0;
   const bool out_vec32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && (a.out_row | a.out_head) * sizeof(E) % 32 == 0;
   const int tpt = kRows / a.group;
-  kernel<<<prompt_blocks(a, tpt), kThreads, C::kShared, stream>>>(a, tpt, a.scale * 1.44269504088896340736f, vec, out_vec32);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_early(kernel, dim3(prompt_blocks(a, tpt)), dim3(kThreads), C::kShared, stream, a, tpt, a.scale * 1.44269504088896340736f, static_cast<int>(vec),
+                   static_cast<int>(out_vec32)) != cudaSuccess)
+    return SV_ERR_CUDA;
   note_launch(stream);
   return SV_OK;
 }

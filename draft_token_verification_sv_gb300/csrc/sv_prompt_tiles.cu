@@ -619,6 +619,7 @@ __global__ void __launch_bounds__(Config<DP>::kThreads, 1)
     tc::publish_shared();
   }
   if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), 512);
+  wait_for_stream();
   sort_sequences(a, sh.sequences, C::NQ * tpt, C::kThreads);
   if (blockIdx.x == 0) flag_lengths(a, C::kThreads);
   tc::fence_before();
@@ -681,8 +682,9 @@ sv_status launch(const PromptView& a, cudaStream_t stream) {
       !rows_map(&maps.v, a.v, a.dim, a.kv_heads, a.total_new, a.v_head, a.v_row, 1, kKeys))
     return SV_ERR_UNSUPPORTED;
   const bool vec32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_row % 16 == 0 && a.out_head % 16 == 0;
-  kernel<<<prompt_blocks(a, C::NQ * tpt), C::kThreads, C::kShared, stream>>>(a, maps, tpt, a.scale * 1.44269504088896340736f, vec32);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_early(kernel, dim3(prompt_blocks(a, C::NQ * tpt)), dim3(C::kThreads), C::kShared, stream, a, maps, tpt, a.scale * 1.44269504088896340736f,
+                   static_cast<int>(vec32)) != cudaSuccess)
+    return SV_ERR_CUDA;
   note_launch(stream);
   return SV_OK;
 }

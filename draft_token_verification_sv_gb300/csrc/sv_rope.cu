@@ -73,6 +73,7 @@ constexpr int kPairThreads = 128;
 template <typename E>
 __global__ void __launch_bounds__(kPairThreads) rope_pairs_kernel(const __grid_constant__ RopeView w) {
   const int row = blockIdx.x;
+  wait_for_stream();
   if (!sv_in(row, w.rows)) return;
   for (int u = threadIdx.x; u < w.dim - w.half; u += kPairThreads) {
     const bool pair = u < w.half;
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(kThreads) rope_units_kernel(const __grid_const
   const int lane = threadIdx.x & 31, unit = lane % units, sub = lane / units;
   const int warp = threadIdx.x >> 5, part = warp % split, first = warp / split;
   const bool turned = unit < w.half >> 3, busy = sub < per;
+  wait_for_stream();
   unsigned long long by[8];
   uint32_t axes = 0;
 #pragma unroll
@@ -211,11 +213,8 @@ bool whole_vectors(const RopeView& w) {
 }
 
 template <typename E>
-void launch(const RopeView& w, cudaStream_t stream) {
-  if (!whole_vectors<E>(w)) {
-    rope_pairs_kernel<E><<<w.rows, kPairThreads, 0, stream>>>(w);
-    return;
-  }
+cudaError_t launch(const RopeView& w, cudaStream_t stream) {
+  if (!whole_vectors<E>(w)) return launch_early(rope_pairs_kernel<E>, dim3(w.rows), dim3(kPairThreads), 0, stream, w);
   // A warp a token, as many blocks as run at a time: 24,000 tokens of 40 heads take 166 us (more blocks: 170 and up, two warps a
   // token: 172).  Few tokens are shared by more warps, as long as these have heads: 64 of 40 heads take 6.4 us with one, 4.4 with 8.
   constexpr int kBlocks = 2 * 152;
@@ -224,10 +223,7 @@ void launch(const RopeView& w, cudaStream_t stream) {
   while (split < kWarps && static_cast<int64_t>(w.rows) * split < kBlocks * kWarps && split * per < all) split *= 2;
   const int64_t blocks = (static_cast<int64_t>(w.rows) * split + kWarps - 1) / kWarps;
   const unsigned grid = static_cast<unsigned>(blocks < kBlocks ? blocks : kBlocks);
-  if (w.adjacent)
-    rope_units_kernel<E, true><<<grid, kThreads, 0, stream>>>(w, split);
-  else
-    rope_units_kernel<E, false><<<grid, kThreads, 0, stream>>>(w, split);
+  return launch_early(w.adjacent ? rope_units_kernel<E, true> : rope_units_kernel<E, false>, dim3(grid), dim3(kThreads), 0, stream, w, split);
 }
 
 }  // namespace
@@ -249,11 +245,7 @@ sv_status rope(const sv_rope_desc& d, const void* q, const void* k, const int32_
   w.positions = positions;
   w.inv_freq = inv_freq;
   for (int i = 0; i < w.half; ++i) w.axis[i] = d.axis[i];
-  if (d.dtype == SV_BF16)
-    launch<uint16_t>(w, stream);
-  else
-    launch<float>(w, stream);
-  if (cudaGetLastError() != cudaSuccess) return SV_ERR_CUDA;
+  if ((d.dtype == SV_BF16 ? launch<uint16_t>(w, stream) : launch<float>(w, stream)) != cudaSuccess) return SV_ERR_CUDA;
   note_launch(stream);
   return SV_OK;
 }
