@@ -90,10 +90,11 @@ __device__ __forceinline__ bool partly_seen(const PromptView& a, const Item& it,
   return !all;
 }
 
-// Bits c of [from, to) for the 32 from `base` on.
-__device__ __forceinline__ uint32_t bits32(int base, int from, int to) {
-  const int lo = min(max(from - base, 0), 32), hi = min(max(to - base, 0), 32);
-  return static_cast<uint32_t>(((1ull << hi) - 1ull) & ~((1ull << lo) - 1ull));
+// The lowest n bits, none for less, all for more.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  uint32_t r;
+  asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(~0u), "r"(32 - min(max(n, 0), 32)));  // (which moves by 32, too)
+  return r;
 }
 
 // Finds items by their numbers: sequences in order (longest first where they are few), in each the last tokens first, kv heads

@@ -468,8 +468,8 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
       tc::tmem_load32(scores + 32, x[1]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        seen[c] = bits32(kb + 32 * c, a.window ? max(0, token - a.window + 1) : 0, token + 1);
-        if (a.window) seen[c] |= bits32(kb + 32 * c, 0, min(a.sinks, token + 1));
+        seen[c] = bits_below(token + 1 - kb - 32 * c);
+        if (a.window) seen[c] = (seen[c] & ~bits_below(max(0, token - a.window + 1) - kb - 32 * c)) | bits_below(min(a.sinks, token + 1) - kb - 32 * c);
       }
       tc::wait_loads(x[0]);
       tc::wait_loads(x[1]);

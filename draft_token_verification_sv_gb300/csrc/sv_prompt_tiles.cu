@@ -485,13 +485,18 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
         }
         if (slow) {
           uint32_t x[32], w[16];
-          const auto seen = [&](int c) { return bits32(kb + 32 * c, from, token + 1) | bits32(kb + 32 * c, 0, sinks); };
+          // a row sees keys [lo, hi) of the tile and, under a window, those before `low`; no row of the warp sees any from `end` on
+          const int lo = from - kb, hi = held ? token + 1 - kb : 0, low = held ? sinks - kb : 0;
+          const auto seen = [&](int c) {
+            const uint32_t past = bits_below(hi - 32 * c);
+            return a.window ? (past & ~bits_below(lo - 32 * c)) | bits_below(low - 32 * c) : past;
+          };
+          const int end = (__reduce_max_sync(0xffffffffu, max(min(hi, kKeys), 0)) + 31) >> 5;
           float top = m;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t mask = seen(c);
-            if (!__any_sync(0xffffffffu, mask != 0)) continue;
+          for (int c = 0; c < end; ++c) {
             tc::tmem_load32(scores + 32 * c, x);
+            const uint32_t mask = seen(c);
             tc::wait_loads(x);
             top = fmaxf(top, largest32<true>(x, mask, f));
           }
@@ -516,18 +521,17 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
           const float base = m == -CUDART_INF_F ? 0.0f : m;
           float sum = 0.0f;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < end; ++c) {
+            tc::tmem_load32(scores + 32 * c, x);
             const uint32_t mask = seen(c);
-            if (__any_sync(0xffffffffu, mask != 0)) {
-              tc::tmem_load32(scores + 32 * c, x);
-              tc::wait_loads(x);
-              sum += weights32<true>(x, mask, f, -base, w);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) w[k] = 0;
-            }
+            tc::wait_loads(x);
+            sum += weights32<true>(x, mask, f, -base, w);
             tc::tmem_store(scores + 16 * c, w);
           }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = 0;
+#pragma unroll 1
+          for (int c = end; c < 4; ++c) tc::tmem_store(scores + 16 * c, w);
           l += sum;
         }
         tc::wait_stores();

@@ -1,10 +1,13 @@
 """Greedy decoding with draft trees over the paged 8-bit cache.
 
-A small random-weight transformer is the target model.  Every step drafts a
-tree of tokens, runs all of its nodes through the target in one pass
-(kv_append, then kv_attention with the tree's parents), verifies the logits
-(verify_tree) and keeps the accepted path in the cache (kv_commit).  The same
-tokens are then decoded one at a time, without drafts, and compared.
+A small random-weight transformer is the target model.  A prompt gets pages and
+positions (kv_assign), its attention runs over its own keys (prompt_attention)
+and the cache takes these in (kv_append).  Every step then drafts a tree of
+tokens, runs all of its nodes through the target in one pass (kv_append, then
+kv_attention with the tree's parents), verifies the logits (verify_tree) and
+keeps the accepted path in the cache (kv_commit); pages of nodes that were
+rejected go back.  The same tokens are then decoded one at a time, without
+drafts, and compared.
 
     python examples/tree_decoding.py [--tokens N] [--batch B] [--seed S]
 """
@@ -31,14 +34,6 @@ def norm(x):
     return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)
 
 
-def rotate(x, position):
-    """Rotary position embedding of [B, n, heads, DIM]."""
-    freq = 10000.0 ** (-torch.arange(0, DIM, 2, device=x.device) / DIM)
-    angle = position[..., None, None] * freq
-    a, b = x[..., ::2], x[..., 1::2]
-    return torch.stack((a * angle.cos() - b * angle.sin(), a * angle.sin() + b * angle.cos()), -1).flatten(-2)
-
-
 class Target:
     """The target model and its caches of `batch` sequences of up to `most` tokens."""
 
@@ -51,20 +46,29 @@ class Target:
                        for _ in range(LAYERS)]
         pages = -(-most // PAGE)
         self.caches = [sv.kv_cache(batch * pages, KV_HEADS, DIM, PAGE, device) for _ in range(LAYERS)]
-        self.table = torch.randperm(batch * pages, generator=g).to(device, torch.int32).view(batch, pages)
+        self.pool = sv.kv_pool(batch * pages, device)
+        self.table = torch.zeros(batch, pages, dtype=torch.int32, device=device)
+        self.held = torch.zeros(batch, dtype=torch.int32, device=device)
         self.lens = torch.zeros(batch, dtype=torch.int32, device=device)
+        self.inv_freq = 10000.0 ** (-torch.arange(0, DIM, 2, device=device) / DIM)
 
-    def score(self, tokens, depth, parents=None):
-        """Logits of new tokens [B, n] at `depth` behind the cached ones, whose keys and values they join."""
+    def score(self, tokens, parents=None, prompt=False):
+        """Logits of new tokens [B, n] behind the cached ones, whose keys and values they join."""
         B, n = tokens.shape
         x = self.embed[tokens]
-        position = (self.lens[:, None] + depth).float()
+        position = sv.kv_assign(self.pool, self.table, self.held, self.lens, PAGE, max_new=n, parents=parents)["positions"]
         for w, cache in zip(self.layers, self.caches):
             q, k, v = (norm(x) @ w["qkv"]).view(B, n, -1, DIM).split((HEADS, KV_HEADS, KV_HEADS), 2)
-            sv.kv_append(cache, rotate(k, position), v, self.table, self.lens)
-            seen = sv.kv_attention(rotate(q, position), cache, self.table, self.lens, parents=parents)
+            q, k = sv.rope(q, k, position, self.inv_freq, adjacent=True)
+            sv.kv_append(cache, k, v, self.table, self.lens)
+            seen = sv.prompt_attention(q, k, v) if prompt else sv.kv_attention(q, cache, self.table, self.lens, parents=parents)
             x = x + seen.flatten(2) @ w["out"]
         return norm(x) @ self.unembed
+
+    def keep(self, lens):
+        """The sequences' lengths from now on; pages that they no longer need go back."""
+        self.lens = lens
+        sv.kv_assign(self.pool, self.table, self.held, lens, PAGE)
 
     def draft(self, tokens):
         """The drafter: the target without its layers."""
@@ -79,11 +83,10 @@ def plain(batch, tokens, seed, device="cuda"):
     """Greedy decoding, one token a pass: [B, tokens]."""
     prompt = prompt_of(batch, seed, device)
     model = Target(batch, prompt.shape[1] + tokens + 1, seed, device)
-    at = torch.arange(prompt.shape[1], device=device)
-    out = [model.score(prompt, at)[:, -1].argmax(-1)]
+    out = [model.score(prompt, prompt=True)[:, -1].argmax(-1)]
     model.lens += prompt.shape[1]
     while len(out) < tokens:
-        out.append(model.score(out[-1][:, None], at[:1])[:, -1].argmax(-1))
+        out.append(model.score(out[-1][:, None])[:, -1].argmax(-1))
         model.lens += 1
     return torch.stack(out, 1)
 
@@ -92,11 +95,10 @@ def with_trees(batch, tokens, seed, device="cuda"):
     """The same with draft trees: [B, tokens] and the passes it took."""
     prompt = prompt_of(batch, seed, device)
     model = Target(batch, prompt.shape[1] + tokens + 2 * len(PARENTS), seed, device)
-    root = model.score(prompt, torch.arange(prompt.shape[1], device=device))[:, -1].argmax(-1)
+    root = model.score(prompt, prompt=True)[:, -1].argmax(-1)
     model.lens += prompt.shape[1]
     out = [[t] for t in root.tolist()]
     parents = torch.tensor(PARENTS, dtype=torch.int32, device=device).expand(batch, -1).contiguous()
-    depth = torch.tensor(DEPTH, device=device)
     passes = 0
     while min(map(len, out)) < tokens:
         nodes = torch.zeros_like(parents)
@@ -106,12 +108,12 @@ def with_trees(batch, tokens, seed, device="cuda"):
                 best = model.draft(nodes[:, i])
                 for child in (c for c, p in enumerate(PARENTS) if p == i):
                     nodes[:, child] = best[:, CHOICE[child]]
-        got = sv.verify_tree(model.score(nodes, depth, parents), parents, nodes, max(DEPTH))
+        got = sv.verify_tree(model.score(nodes, parents), parents, nodes, max(DEPTH))
         for cache in model.caches:
             new_lens = sv.kv_commit(cache, model.table, model.lens, got["path"], got["accept_len"], len(PARENTS))
         # a sequence that has its tokens stays where it is
         done = torch.tensor([len(o) >= tokens for o in out], device=device)
-        model.lens = torch.where(done, model.lens, new_lens)
+        model.keep(torch.where(done, model.lens, new_lens))
         kept, length = got["out_tokens"], got["accept_len"].long()
         root = torch.where(done, root, kept.gather(1, length[:, None])[:, 0].long())
         for o, row, n in zip(out, kept.tolist(), length.tolist()):

@@ -82,7 +82,8 @@ def test_padded_batch(sv, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 3), (64, 0), (63, 4), (65, 130), (100, 1), (128, 128), (200, 300), (1000, 5)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 3), (64, 0), (63, 4), (65, 130), (100, 1), (128, 128), (200, 300), (1000, 5),
+                                          (2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (7, 2 ** 31 - 1)])
 def test_windows_and_sinks(sv, dtype, window, sinks):
     _check(sv, dtype, [520, 129, 7], heads=2, kv_heads=1, dim=64, window=window, sinks=sinks)
 
