@@ -3,18 +3,24 @@
 //
 // A float32 value is the sum of three bf16 values (8 significant bits each,
 // with signs, and float's range), so a product of two is the sum of the six
-// products of their parts that are not below 2^-24 of it, taken from the small
-// ones to the large.  Queries, keys and values are read with ordinary loads,
-// split, and written to shared memory as the products want them; weights are
-// split where they are made.  One tile of 128 query rows (sv_prompt_items.cuh)
-// against tiles of 64 keys, two of which are under way.  Roles of a block's
-// warps:
+// products of their parts that are not below 2^-24 of it.  Tensor memory cuts
+// sums off, it does not round them, so the sum of the five small products is
+// formed beside that of the large one, and the sums over values are formed anew
+// for each tile of keys and added to the results where they are rounded.
+// (Scores of 256 dims lost 8.7 * 2^-23 of their size in the mean with all six in
+// one sum, 0.8 with two.)
+//
+// Queries, keys and values are read with ordinary loads, split, and written to
+// shared memory as the products want them; weights are split where they are
+// made.  One tile of 128 query rows (sv_prompt_items.cuh) against tiles of 64
+// keys, two of which are under way.  Roles of a block's warps:
 //   four turn scores into weights, a row a thread (sv_prompt_tiles.cu says how);
 //   eight load and split, and leave out values that are not finite, which rows
 //   that see them get where results are written;
 //   one issues the products; one finds the items.
 // Above 128 float32 dims a block's queries do not fit shared memory: they come
-// again with each tile of keys, 64 dims at a time.
+// again with each tile of keys, 64 dims at a time, and tensor memory has room for
+// the scores of one tile only.
 #include "sv_prompt_items.cuh"
 
 #include <algorithm>
@@ -48,9 +54,10 @@ template <int DP, typename E> struct Config {
   static constexpr int kBytes = kQueryBytes + kStages * kStageBytes;
   // more than half of an SM's shared memory keeps it to one block
   static constexpr int kShared = (kBytes > 118 * 1024 ? kBytes : 118 * 1024) + 1024;
-  // tensor memory, in columns: two places for scores and the weights they become, O, and the sums of a unit of values
-  static constexpr int kPlace = kParts == 1 ? 64 : DP == 256 ? 96 : 128, kO = 2 * kPlace, kSums = kO + DP;
-  static_assert(kPlace >= kParts * (kKeys / 2) && kPlace >= kKeys && kSums + kValueDims <= 512, "tensor memory");
+  // tensor memory, in columns: places for scores (large and small products' sums) and the weights they become, O, and the sums of a
+  // unit of values
+  static constexpr int kPlaces = kStream ? 1 : 2, kPlace = kParts == 1 ? kKeys : 2 * kKeys, kO = kPlaces * kPlace, kSums = kO + DP;
+  static_assert(kPlace >= kParts * (kKeys / 2) && kSums + kValueDims <= 512, "tensor memory");
 };
 
 struct Shared {
@@ -286,7 +293,7 @@ __device__ bool load_role(const PromptView& a, int tpt, Shared& sh, uint8_t* q_a
     }
     if (!keys(0)) return false;
     for (int t = 0; t < tiles; ++t) {
-      if (t + 1 < tiles && !keys(t + 1)) return false;
+      if (C::kPlaces == 2 && t + 1 < tiles && !keys(t + 1)) return false;
       if (loaded++ == SV_PROMPT_LOST_TILE) return false;
       const int kb = key_of<kKeys>(it, t);
       for (int u = 0; u < C::kValueUnits; ++u) {
@@ -295,6 +302,7 @@ __device__ bool load_role(const PromptView& a, int tpt, Shared& sh, uint8_t* q_a
           it.dirty = 1;
         end();
       }
+      if (C::kPlaces == 1 && t + 1 < tiles && !keys(t + 1)) return false;
     }
     warp_arrive(sh.item_free[items % kItems]);
   }
@@ -339,24 +347,27 @@ __device__ bool product_role(Shared& sh, uint32_t q_at, uint32_t stages, uint32_
         for (int n = 0; n < kProducts; ++n)
 #pragma unroll
           for (int d = 0; d < C::kScoreDims / 16; ++d)
-            tc::product_f16(tmem + s * C::kPlace,
+            tc::product_f16(tmem + s * C::kPlace + (n + 1 < kProducts ? kKeys : 0),
                             tc::tile_descriptor(q + left_part<C::kParts>(n) * C::kQueryPart + (d >> 2) * (kRows * 128) + (d & 3) * 32, 16, 1024),
                             tc::tile_descriptor(k + right_part<C::kParts>(n) * C::kKeyPart + (d >> 2) * (kKeys * 128) + (d & 3) * 32, 16, 1024), kScores,
-                            u > 0 || n > 0 || d > 0);
+                            u > 0 || (n > 0 && n + 1 < kProducts) || d > 0);
         arrive(sh.free[stage]);
       }
       arrive(sh.s_full[s]);
       return true;
     };
     if (!C::kStream && !wait(sh.q_full, items)) return false;
-    if (!score(tile & 1)) return false;
-    if (!C::kStream && tiles == 1) arrive(sh.q_free);
+    // the next tile's scores are formed before a tile's sums, where they have a place of their own
+    const auto next = [&](int t) {
+      if (t >= tiles) return true;
+      if (!score((tile + (C::kPlaces == 2 && t > 0)) % C::kPlaces)) return false;
+      if (!C::kStream && t + 1 == tiles) arrive(sh.q_free);
+      return true;
+    };
+    if (!next(0)) return false;
     for (int t = 0; t < tiles; ++t, ++tile) {
-      if (t + 1 < tiles) {
-        if (!score(tile + 1 & 1)) return false;
-        if (!C::kStream && t + 2 == tiles) arrive(sh.q_free);
-      }
-      if (!wait(sh.p_ready[tile & 1], tile >> 1)) return false;
+      if (C::kPlaces == 2 && !next(t + 1)) return false;
+      if (!wait(sh.p_ready[tile % C::kPlaces], tile / C::kPlaces)) return false;
       for (int u = 0; u < C::kValueUnits; ++u, ++unit, ++sums) {
         const int stage = unit % C::kStages;
         if (!wait(sh.full[stage], unit / C::kStages)) return false;
@@ -366,12 +377,13 @@ __device__ bool product_role(Shared& sh, uint32_t q_at, uint32_t stages, uint32_
         for (int n = 0; n < kProducts; ++n)
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            tc::product_f16(tmem + C::kSums, tmem + (tile & 1) * C::kPlace + left_part<C::kParts>(n) * (kKeys / 2) + k * 8,
+            tc::product_f16(tmem + C::kSums, tmem + tile % C::kPlaces * C::kPlace + left_part<C::kParts>(n) * (kKeys / 2) + k * 8,
                             tc::tile_descriptor(v + right_part<C::kParts>(n) * C::kValuePart + k * 2048, kKeys * 128, 1024), kValues,
                             n > 0 || k > 0);
         arrive(sh.free[stage]);
         arrive(sh.sums_full);
       }
+      if (C::kPlaces == 1 && !next(t + 1)) return false;
     }
   }
 }
@@ -460,9 +472,9 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
     const bool held = at.row >= 0;
     float m = held ? -CUDART_INF_F : 0.0f, l = 0.0f, fix = 1.0f, fix_before = 1.0f;  // fix: of what was summed before this tile
     for (int t = 0; t < tiles; ++t, ++tile) {
-      const int s = tile & 1, kb = key_of<kKeys>(it, t);
+      const int s = tile % C::kPlaces, kb = key_of<kKeys>(it, t);
       const uint32_t scores = mine + s * C::kPlace;
-      if (!wait(sh.s_full[s], tile >> 1)) return false;
+      if (!wait(sh.s_full[s], tile / C::kPlaces)) return false;
       uint32_t x[2][32], w[C::kParts][16], seen[2];
       tc::tmem_load32(scores, x[0]);
       tc::tmem_load32(scores + 32, x[1]);
@@ -473,6 +485,16 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
       }
       tc::wait_loads(x[0]);
       tc::wait_loads(x[1]);
+      if constexpr (C::kParts == 3) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t y[32];
+          tc::tmem_load32(scores + kKeys + 32 * c, y);
+          tc::wait_loads(y);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[c][k] = __float_as_uint(__uint_as_float(x[c][k]) + __uint_as_float(y[k]));
+        }
+      }
       bool raise = held && m == -CUDART_INF_F;
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
@@ -506,11 +528,12 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
       tc::wait_stores();
       tc::fence_before();
       warp_arrive(sh.p_ready[s]);
-      if (t > 0 && !gather(t == 1, fix_before)) return false;
+      // (with two places the last tile's sums are formed while this one's weights are made)
+      if (C::kPlaces == 2 ? t > 0 && !gather(t == 1, fix_before) : !gather(t == 0, fix)) return false;
       fix_before = fix;
       fix = 1.0f;
     }
-    if (!gather(tiles == 1, fix_before)) return false;
+    if (C::kPlaces == 2 && !gather(tiles == 1, fix_before)) return false;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     E* out = static_cast<E*>(a.out) + at.row * a.out_row + at.head * a.out_head;
     const bool dirty = *const_cast<const volatile int*>(&it.dirty) != 0;

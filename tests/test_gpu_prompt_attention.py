@@ -57,6 +57,21 @@ def test_head_dims(sv, dtype, dim):
     _check(sv, dtype, [150, 1, 37], dim=dim)
 
 
+@pytest.mark.parametrize("dim", [16, 64, 128, 144, 192, 208, 256])
+def test_what_float32_scores_lose(sv, dim):
+    """Alone in its sequence a token's lse is its score.  Of positive terms the
+    sum grows evenly, so that what is cut off with each 16 of them (less than
+    the last place, 2^-23 of the sum so far; half of that in the mean) comes to
+    (dim / 16 + 1) / 4 of 2^-23 of the score; scaling, to base 2 and back, and
+    the products that are left out take less than 2 of 2^-23."""
+    g = np.random.default_rng(dim)
+    q, k, v = (round_to(g.uniform(0.5, 2, (300, 2, dim)), "f32") for _ in range(3))
+    starts = np.arange(301, dtype=np.int32)
+    _, lse = sv.prompt_attention(*(to_gpu(x, "f32") for x in (q, k, v)), new_start=to_gpu(starts), max_new=1, lse=True)
+    want = (q.astype(np.float64) * k).sum(-1) * float(np.float32(dim ** -0.5))
+    assert abs((lse.double().cpu().numpy() / want - 1).mean()) <= ((dim / 16 + 1) / 4 + 2) * 2.0 ** -23
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("heads,kv_heads", [(1, 1), (3, 3), (8, 2), (6, 2), (5, 1), (7, 1), (14, 2), (16, 1), (40, 1), (100, 1), (128, 1)])
 def test_shared_heads(sv, dtype, heads, kv_heads):
