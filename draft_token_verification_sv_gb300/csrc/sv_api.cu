@@ -195,6 +195,7 @@ bool prompt_desc_ok(const sv_prompt_attention_desc* d, bool ragged) {
   if (d->max_new < 0 || d->total_new < 0) return false;
   if (!ragged && static_cast<int64_t>(d->batch) * d->max_new != d->total_new) return false;
   if (static_cast<int64_t>(d->max_new) * (d->heads / d->kv_heads) > INT32_MAX - 256) return false;
+  if (static_cast<int64_t>(d->total_new) * d->heads > INT32_MAX) return false;
   if (!valid_dtype(d->dtype) || !std::isfinite(d->scale) || d->window < 0 || d->sinks < 0) return false;
   const int64_t strides[8] = {d->q_row_stride, d->q_head_stride, d->k_row_stride, d->k_head_stride,
                               d->v_row_stride, d->v_head_stride, d->out_row_stride, d->out_head_stride};
@@ -508,6 +509,15 @@ sv_status sv_rope(const sv_rope_desc* desc, const void* q, const void* k, const 
     return SV_ERR_INVALID_ARGUMENT;
   if (desc->kv_heads > 0 && (!k || !k_out || !aligned_elem(k, desc->dtype) || !aligned_elem(k_out, desc->dtype)))
     return SV_ERR_INVALID_ARGUMENT;
+  // a result takes its own input's place or none (seen where they begin at one address)
+  const bool rows = desc->rows > 1;
+  if (q_out == q && ((rows && desc->q_out_row_stride != desc->q_row_stride) || (desc->heads > 1 && desc->q_out_head_stride != desc->q_head_stride)))
+    return SV_ERR_INVALID_ARGUMENT;
+  if (desc->kv_heads > 0) {
+    if (q_out == k || q_out == k_out || k_out == q) return SV_ERR_INVALID_ARGUMENT;
+    if (k_out == k && ((rows && desc->k_out_row_stride != desc->k_row_stride) || (desc->kv_heads > 1 && desc->k_out_head_stride != desc->k_head_stride)))
+      return SV_ERR_INVALID_ARGUMENT;
+  }
   return rope(*desc, q, k, positions, inv_freq, q_out, k_out, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -521,6 +531,7 @@ sv_status sv_prompt_attention(const sv_prompt_attention_desc* desc, const void* 
     const void* rows[4] = {q, k, v, out};
     for (const void* p : rows)
       if (!p || !aligned_elem(p, desc->dtype)) return SV_ERR_INVALID_ARGUMENT;
+    if (out == q || out == k || out == v) return SV_ERR_INVALID_ARGUMENT;
   }
   return prompt_attention(*desc, q, k, v, new_start, out, lse, row_status, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -80,6 +80,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
     Pairs are (i, i + len(inv_freq)), with ``adjacent`` (2i, 2i + 1).  Returns
     (q, k) in new memory, or in ``out``, which may be (q, k) themselves."""
     q_out, k_out = (None, None) if out is None else out
+    if out is not None and q_out is None:
+        raise ValueError("out must be (q's result, k's)")
     d, gpu = _rope_plan(_meta(q), _meta(k), _meta(positions), _meta(inv_freq),
                         None if sections is None else tuple(int(n) for n in sections), bool(adjacent), _meta(q_out), _meta(k_out))
     if out is None:

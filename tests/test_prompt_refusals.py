@@ -23,6 +23,7 @@ def N():
     return _native
 
 
+ELSE = ctypes.c_void_p(0x20000000)
 A, ODD, OFF4 = ctypes.c_void_p(0x10000000), ctypes.c_void_p(0x10000001), ctypes.c_void_p(0x10000004)
 
 
@@ -126,7 +127,7 @@ def _rope(N, ptr=None, axis=None, **kw):
         setattr(d, k, v)
     if axis:
         d.axis[axis[0]] = axis[1]
-    at = dict(q=A, k=A, positions=A, freq=A, q_out=A, k_out=A)
+    at = dict(q=A, k=OFF4, positions=A, freq=A, q_out=A, k_out=OFF4)
     at.update(ptr or {})
     return N.lib().sv_rope(ctypes.byref(d), at["q"], at["k"], at["positions"], at["freq"], at["q_out"], at["k_out"], None)
 
@@ -152,6 +153,14 @@ def test_rope_refuses_pointers(N, name):
     assert _rope(N, {name: ODD}) == N.SV_ERR_INVALID_ARGUMENT
 
 
+@pytest.mark.parametrize("ptr,kw", [
+    (dict(q_out=OFF4), {}), (dict(k_out=A), {}), (dict(q_out=ELSE, k_out=ELSE), {}), ({}, dict(q_out_row_stride=264)), ({}, dict(q_out_head_stride=72)),
+    ({}, dict(k_out_row_stride=136)), ({}, dict(k_out_head_stride=72)), (dict(k_out=A), dict(kv_heads=1, rows=1)),
+])
+def test_rope_refuses_results_in_another_input_s_place(N, ptr, kw):
+    assert _rope(N, ptr, **kw) == N.SV_ERR_INVALID_ARGUMENT
+
+
 def _rope_py(**kw):
     args = dict(q=Stand((7, 4, 64)), k=Stand((7, 2, 64)), positions=_ints(7), inv_freq=Stand((32,)), out=(Stand((7, 4, 64)), Stand((7, 2, 64))))
     args.update(kw)
@@ -167,7 +176,7 @@ def _rope_py(**kw):
     (dict(inv_freq=Stand((32,), strides=(2,))), ValueError), (dict(q=Stand((7, 64))), ValueError), (dict(q=Stand((7, 4, 64), torch.float16)), TypeError),
     (dict(k=Stand((6, 2, 64))), ValueError), (dict(k=Stand((7, 2, 32))), ValueError), (dict(k=Stand((7, 2, 64), torch.bfloat16)), ValueError),
     (dict(out=(Stand((7, 4, 32)), Stand((7, 2, 64)))), ValueError), (dict(out=(Stand((7, 4, 64)), None)), ValueError),
-    (dict(out=(Stand((7, 4, 64)), Stand((7, 3, 64)))), ValueError), (dict(q=Stand((7, 4, 64), strides=(256, 1, 4))), ValueError),
+    (dict(out=(None, Stand((7, 2, 64)))), ValueError), (dict(out=(Stand((7, 4, 64)), Stand((7, 3, 64)))), ValueError), (dict(q=Stand((7, 4, 64), strides=(256, 1, 4))), ValueError),
     (dict(positions=_ints(7, device="cuda:1")), ValueError), (dict(positions=_ints(7, device="cpu")), ValueError),
 ], ids=lambda d: "-".join(d) if isinstance(d, dict) else "")
 def test_rope_refuses_tensors(N, bad, error):
@@ -190,7 +199,7 @@ def _prompt_desc(N, **kw):
 
 
 def _prompt(N, ptr=None, **kw):
-    at = dict(q=A, k=A, v=A, start=None, out=A, lse=None, status=None)
+    at = dict(q=A, k=A, v=A, start=None, out=OFF4, lse=None, status=None)
     at.update(ptr or {})
     return N.lib().sv_prompt_attention(ctypes.byref(_prompt_desc(N, **kw)), *(at[n] for n in at), None)
 
@@ -219,6 +228,15 @@ def test_prompt_attention_without_sequences_and_with_too_many_rows(N):
     assert _prompt(N, batch=0, total_new=0) == N.SV_OK
     # rows times heads of a kv head pass 32 bits
     assert _prompt(N, {"start": A}, max_new=1 << 30, total_new=12) == N.SV_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_prompt_attention_refuses_results_in_an_input_s_place(N, name):
+    assert _prompt(N, {name: OFF4}) == N.SV_ERR_INVALID_ARGUMENT
+
+
+def test_prompt_attention_refuses_more_rows_than_items_are_counted_for(N):
+    assert _prompt(N, {"start": A}, total_new=1 << 28) == N.SV_ERR_INVALID_ARGUMENT
 
 
 def _prompt_py(**kw):
