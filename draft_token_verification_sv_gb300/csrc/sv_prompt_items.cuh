@@ -26,7 +26,7 @@ struct Item {
   int tiles;             // of keys, -1: no more items
   int count[2];          // of them for each tile of queries
   int first, window;     // tiles of the first tokens (sinks), then from this tile on
-  int dirty;             // values that are not finite were taken out
+  int dirty;             // not 0: values that are not finite were taken out
 };
 
 // Sequences where they are few: the longest first, their rows, and the items up to and with each.
@@ -197,6 +197,33 @@ __device__ __forceinline__ float value_of(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float value_of(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16); }
 __device__ __forceinline__ void put_value(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put_value(uint16_t* p, float v) { *p = static_cast<uint16_t>(floats_to_bf16x2(v, 0.0f)); }
+
+__device__ __forceinline__ float held_at(const float* p) { return *p; }
+__device__ __forceinline__ float held_at(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
+
+// Adds to a row's results what it sees of values that are not finite and were taken out: those of tiles that every row sees, which
+// were added up (NULL: none were taken out), and, token by token, those of the few others.
+template <int KEYS, typename E>
+__device__ __noinline__ void add_rest(const PromptView& a, const Item& it, int tpt, int token, E* out, const volatile float* whole_tiles) {
+  if (whole_tiles)
+    for (int d = 0; d < a.dim; ++d) {
+      const float y = whole_tiles[d];
+      if (y != 0.0f) put_value(out + d, held_at(out + d) + y);
+    }
+  const E* v = static_cast<const E*>(a.v) + static_cast<int64_t>(it.row0) * a.v_row + it.h * a.v_head;
+  for (int t = 0; t < it.tiles; ++t) {
+    if (!partly_seen<KEYS, 2>(a, it, tpt, t)) continue;
+    const int kb = key_of<KEYS>(it, t);
+    for (int j = kb; j < kb + KEYS && j <= token; ++j) {
+      if (a.window != 0 && token - j >= a.window && j >= a.sinks) continue;
+      if (!sv_in(it.row0 + static_cast<int64_t>(j), a.total_new)) break;
+      for (int d = 0; d < a.dim; ++d) {
+        const float y = value_of(v + j * a.v_row + d);
+        if (!(fabsf(y) < CUDART_INF_F)) put_value(out + d, held_at(out + d) + y);
+      }
+    }
+  }
+}
 
 // A wait ran out: results of the item are not valid.
 template <typename E>

@@ -67,6 +67,7 @@ struct Shared {
   uint4 block;
   Item item[kItems];
   Sequences sequences;
+  float rest[kSoftmaxWarps][SV_MAX_HEAD_DIM];  // see sum_rest
   uint32_t tmem;
   int gave_up;
   int claimed, finished[kSoftmaxWarps];
@@ -299,7 +300,7 @@ __device__ bool load_role(const PromptView& a, int tpt, Shared& sh, uint8_t* q_a
       for (int u = 0; u < C::kValueUnits; ++u) {
         if (!begin()) return false;
         if (load_rows<E, kKeys, C::kValueDims>(v, token(kb, a.v_row), u * C::kValueDims, a.dim, vec, true, stages + unit % C::kStages * C::kStageBytes))
-          it.dirty = 1;
+          atomicOr(&it.dirty, 1 << (t & 31));
         end();
       }
       if (C::kPlaces == 1 && t + 1 < tiles && !keys(t + 1)) return false;
@@ -409,17 +410,24 @@ __device__ __forceinline__ float weights32(const uint32_t (&x)[32], uint32_t see
   return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
-// What the row sees of values that are not finite and were left out.
+// Sums of the values that were left out of tiles that every row sees, by a warp; `dirty`: where there may be some.
 template <typename E>
-__device__ __noinline__ float rest_of(const PromptView& a, const Item& it, int token, int d) {
+__device__ __noinline__ void sum_rest(const PromptView& a, const Item& it, int tpt, int dirty, float* sums) {
   const E* v = static_cast<const E*>(a.v) + static_cast<int64_t>(it.row0) * a.v_row + it.h * a.v_head;
-  float sum = 0.0f;
-  for (int j = 0; j <= token && sv_in(it.row0 + static_cast<int64_t>(j), a.total_new); ++j) {
-    if (a.window != 0 && token - j >= a.window && j >= a.sinks) continue;
-    const float y = value_of(v + j * a.v_row + d);
-    if (!(fabsf(y) < CUDART_INF_F)) sum += y;
+  for (int d = threadIdx.x & 31; d < a.dim; d += 32) {
+    float sum = 0.0f;
+    for (int t = 0; t < it.tiles; ++t) {
+      if (!(dirty >> (t & 31) & 1) || partly_seen<kKeys, 1>(a, it, tpt, t)) continue;
+      const int kb = key_of<kKeys>(it, t);
+#pragma unroll 8
+      for (int j = kb; j < kb + kKeys; ++j) {
+        const float y = sv_in(it.row0 + static_cast<int64_t>(j), a.total_new) ? value_of(v + j * a.v_row + d) : 0.0f;
+        sum += fabsf(y) < CUDART_INF_F ? 0.0f : y;
+      }
+    }
+    sums[d] = sum;
   }
-  return sum;
+  __syncwarp();
 }
 
 template <int DP, typename E>
@@ -536,7 +544,6 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
     if (C::kPlaces == 2 && !gather(tiles == 1, fix_before)) return false;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     E* out = static_cast<E*>(a.out) + at.row * a.out_row + at.head * a.out_head;
-    const bool dirty = *const_cast<const volatile int*>(&it.dirty) != 0;
 #pragma unroll 1
     for (int d = 0; d < DP; d += 16) {
       uint32_t o[16];
@@ -546,9 +553,6 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
         float x[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]) * inv;
-        if (__builtin_expect(dirty, 0))
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] += rest_of<E>(a, it, token, d + k);
         if (out_vec32) {
 #pragma unroll
           for (int h = 0; h < static_cast<int>(sizeof(E)) / 2; ++h) {
@@ -563,6 +567,11 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
         }
       }
       __syncwarp();
+    }
+    const int dirty = *const_cast<const volatile int*>(&it.dirty);
+    if (dirty != 0) {
+      sum_rest<E>(a, it, tpt, dirty, sh.rest[quarter]);
+      if (held) add_rest<kKeys, E>(a, it, tpt, token, out, sh.rest[quarter]);
     }
     if (held && a.lse) a.lse[at.row * a.heads + at.head] = (m + log2f(l)) * 0.69314718055994530942f;
     __syncwarp();
@@ -606,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_split_kernel(const __grid_
     tc::barrier_init(tc::smem_address(&sh.answer), 1);
     tc::publish_shared();
   }
+  wait_for_stream();  // (before tensor memory is taken, which the launch before may still need)
   if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), 512);
-  wait_for_stream();
   sort_sequences(a, sh.sequences, tpt, kThreads);
   if (blockIdx.x == 0) flag_lengths(a, kThreads);
   tc::fence_before();

@@ -408,25 +408,6 @@ __device__ __forceinline__ float largest32(const uint32_t (&x)[32], uint32_t see
   return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
 }
 
-// Adds to a row's results what it sees of values that are not finite and were left out.
-__device__ __noinline__ void add_rest(const PromptView& a, const Item& it, int tpt, int token, uint16_t* out) {
-  const uint16_t* v = static_cast<const uint16_t*>(a.v) + static_cast<int64_t>(it.row0) * a.v_row + it.h * a.v_head;
-  for (int d = 0; d < a.dim; ++d) {
-    float sum = 0.0f;
-    for (int t = 0; t < it.tiles; ++t) {
-      const int kb = key_of<kKeys>(it, t);
-      if (!partly_seen<kKeys, 2>(a, it, tpt, t)) continue;
-      for (int j = kb; j < kb + kKeys && j <= token; ++j) {
-        if (a.window != 0 && token - j >= a.window && j >= a.sinks) continue;
-        if (!sv_in(it.row0 + static_cast<int64_t>(j), a.total_new)) break;
-        const float y = value_of(v + j * a.v_row + d);
-        if (!(fabsf(y) < CUDART_INF_F)) sum += y;
-      }
-    }
-    if (sum != 0.0f) put_value(out + d, __uint_as_float(static_cast<uint32_t>(out[d]) << 16) + sum);
-  }
-}
-
 // (What runs once an item, or for a few of its tiles, is kept short: its instructions are fetched anew each time.)
 template <int DP>
 __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, uint32_t tmem, bool out_vec32) {
@@ -574,7 +555,7 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
         }
         __syncwarp();
       }
-      if (*const_cast<const volatile int*>(&it.dirty) != 0 && held) add_rest(a, it, tpt, token, out);
+      if (*const_cast<const volatile int*>(&it.dirty) != 0 && held) add_rest<kKeys, uint16_t>(a, it, tpt, token, out, nullptr);
     }
     __syncwarp();
     if ((threadIdx.x & 31) == 0) sh.finished[threadIdx.x >> 5] = items + 1;
@@ -622,8 +603,8 @@ __global__ void __launch_bounds__(Config<DP>::kThreads, 1)
     tc::barrier_init(tc::smem_address(&sh.answer), 1);
     tc::publish_shared();
   }
+  wait_for_stream();  // (before tensor memory is taken, which the launch before may still need)
   if (warp == 0) tc::tmem_alloc(tc::smem_address(&sh.tmem), 512);
-  wait_for_stream();
   sort_sequences(a, sh.sequences, C::NQ * tpt, C::kThreads);
   if (blockIdx.x == 0) flag_lengths(a, C::kThreads);
   tc::fence_before();

@@ -68,3 +68,41 @@ def test_waits_that_run_out_are_reported():
     r = subprocess.run([sys.executable, "-c", child], cwd=ROOT, env=dict(os.environ, SPEC_VERIFY_LIBRARY=library),
                        capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "child ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
+
+
+LONG_CHILD = r"""
+import sys
+import torch
+sys.path[:0] = [{root!r}]
+import draft_token_verification_sv_gb300 as sv
+
+n, heads, dim = 20000, 4, 64
+for dtype, shift in ((torch.float32, 0), (torch.bfloat16, 0), (torch.bfloat16, 1)):
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q, k, v = (torch.randn(1, n, heads, dim + 8, generator=g, device="cuda").to(dtype)[..., shift:dim + shift] for _ in range(3))
+    st = torch.full((1,), -7, dtype=torch.int32, device="cuda")
+    clean = sv.prompt_attention(q, k, v)
+    assert torch.isfinite(clean).all()
+    v[0, 0, :, 5] = float("inf")
+    v[0, 3, 1, 7] = float("nan")
+    v[0, 9999, 2, 9] = float("-inf")
+    out = sv.prompt_attention(q, k, v, row_status=st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [0], (dtype, shift, st)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0, :, :, 5] = True
+    hit[0, 3:, 1, 7] = True
+    hit[0, 9999:, 2, 9] = True
+    assert torch.equal(torch.isfinite(out), ~hit), (dtype, shift)
+    assert torch.equal(out.masked_fill(hit, 0), clean.masked_fill(hit, 0)), (dtype, shift)
+print("child ok")
+"""
+
+
+def test_a_value_that_is_not_finite_does_not_hold_a_long_prompt_up():
+    """Waits of 17 ms are far more than any role takes for its share, with such values or without."""
+    from draft_token_verification_sv_gb300 import build as b
+    library = b.build(variant="short_prompt_waits", defines=("SV_WAIT_CYCLES=(1ll<<25)",))
+    r = subprocess.run([sys.executable, "-c", LONG_CHILD.format(root=ROOT)], cwd=ROOT, env=dict(os.environ, SPEC_VERIFY_LIBRARY=library),
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "child ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
