@@ -16,10 +16,12 @@
  *     reported per batch row in `row_status` (bits SV_ROW_*); such rows emit
  *     num_accepted = 0 / accept_len = 0 and token -1.
  *   - No kernel waits on one that may run beside it, and no wait is endless.
- *     The attention over the cache begins while the launch before it in the
- *     stream ends, waits for that end and then works; inside its many-row
- *     kernel the warps of a block wait for one another, two seconds at most
- *     (then the call ends with SV_ROW_TIMEOUT).
+ *     The attention over the cache, and what prepares a request for it
+ *     (sv_kv_assign, sv_rope, sv_prompt_attention), begin while the launch
+ *     before them in the stream ends, wait for that end and then work; inside
+ *     the attention kernels that use the tensor cores the warps of a block
+ *     wait for one another, two seconds at most (then the call ends with
+ *     SV_ROW_TIMEOUT, and NaN where results are missing).
  *
  * Layouts: logits are row-major; a "row" is one position's logits over the
  * vocabulary.  Row strides are in ELEMENTS and at least the row length; any
@@ -658,9 +660,11 @@ typedef struct sv_rope_desc {
  * are within 2^-23 of their values, and the result is rounded once.
  *
  *   q [rows, heads, D], k [rows, kv_heads, D];  positions [axes, rows] int32
- *   (any value);  inv_freq [R / 2] float, finite: radians a position.
+ *   (any value);  inv_freq [R / 2] float, below 2^60 in magnitude:
+ *   radians a position.
  *   q_out, k_out: like q and k.  Either may be its input (the same pointer
- *   and strides); otherwise they share no memory with q or k.
+ *   and strides); otherwise they share no memory with q, k or one another
+ *   (refused where they begin at one address).
  */
 sv_status sv_rope(const sv_rope_desc* desc, const void* q, const void* k, const int32_t* positions,
                   const float* inv_freq, void* q_out, void* k_out, sv_stream_t stream);
@@ -692,15 +696,24 @@ typedef struct sv_prompt_attention_desc {
  *   lse = ln(sum_j exp(s_j)).
  * What a query does not see has no influence on its result, whatever it
  * holds (infinities and NaN too).  Rows that belong to no sequence are not
- * touched.  A sequence with a negative length, more than max_new tokens or
- * rows outside [0, total_new) is left out and flagged SV_ROW_BAD_LENGTH.
+ * touched, those of several are any one's.  A sequence with a negative
+ * length, more than max_new tokens or rows outside [0, total_new) is left
+ * out and flagged SV_ROW_BAD_LENGTH.
  *
  *   q [total_new, heads, D];  k, v [total_new, kv_heads, D];
- *   out [total_new, heads, D], shares no memory with q, k or v;
+ *   out [total_new, heads, D], shares no memory with q, k or v (refused
+ *   where it begins at one of them);
  *   lse optional [total_new, heads] float, contiguous;
  *   new_start [B + 1] int32 or NULL;  row_status optional [B] int32.
  *
- * Scores and sums are held in fp32.
+ * Scores and sums are held in fp32.  bf16 calls round each weight to bf16
+ * (2^-8 of itself) and nothing else but the result.  float32 calls multiply
+ * sums of three bf16 values that make up each query, key, value and weight
+ * and leave products below 2^-24 of the whole out; values below 2^-100 keep
+ * fewer bits.  Weights are not taken from a row's largest score but from one
+ * within 2^13 a tile of it, so sums over values overflow where their
+ * magnitudes pass 2^100.  A query or key that is not finite makes NaN of the
+ * results that it enters.
  */
 sv_status sv_prompt_attention(const sv_prompt_attention_desc* desc, const void* q, const void* k, const void* v,
                               const int32_t* new_start, void* out, float* lse, int32_t* row_status,

@@ -123,6 +123,15 @@ def test_more_sequences_than_a_block_scans_at_once(sv):
     assert b.count == 4000
 
 
+def test_a_largest_number_of_tokens_far_above_what_comes(sv):
+    g = np.random.default_rng(3)
+    batch = 1100
+    both = Both(sv, 9000, batch, 700, 16, g)
+    new = g.integers(0, 30, batch)
+    new[[5, 900]] = 11_000, 5_003
+    both.call(np.zeros(batch, int), new, max_new=2 ** 31 - 1)
+
+
 @pytest.mark.parametrize("short", [0, 1, 7])
 def test_what_a_call_gives_back_a_later_sequence_takes(sv, short):
     g = np.random.default_rng(1)
