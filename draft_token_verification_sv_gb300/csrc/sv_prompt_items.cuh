@@ -90,6 +90,20 @@ __device__ __forceinline__ bool partly_seen(const PromptView& a, const Item& it,
   return !all;
 }
 
+// The u-th of an item's tiles of keys and values in the order in which they are loaded and used: each tile's keys and then its
+// values or, AHEAD, the next tile's keys, whose scores are formed meanwhile, before the values.
+struct Turn {
+  bool keys;
+  int t;
+};
+template <bool AHEAD>
+__device__ __forceinline__ Turn turn_of(int u, int tiles) {
+  if (!AHEAD) return Turn{(u & 1) == 0, u >> 1};
+  const bool last = u == 2 * tiles - 1;
+  const bool keys = !last && (u == 0 || (u & 1));
+  return Turn{keys, keys ? (u + 1) >> 1 : last ? tiles - 1 : (u >> 1) - 1};
+}
+
 // The lowest n bits, none for less, all for more.
 __device__ __forceinline__ uint32_t bits_below(int n) {
   uint32_t r;

@@ -18,6 +18,11 @@
 //   eight load and split, and leave out values that are not finite, which rows
 //   that see them get where results are written;
 //   one issues the products; one finds the items.
+// Three prompts of up to 4001 tokens under windows of 2048 (16 heads of 64
+// float32 dims) take 435 us, 127 TFLOP/s, six times that in products: the
+// tensor core is busy for 0.6 of a tile's 3300 cycles.  The chain of a row's
+// thread (scores, 64 weights in three parts each, sums) bounds it, and the
+// issue slots and instruction fetches that it shares with the loaders.
 // Above 128 float32 dims a block's queries do not fit shared memory: they come
 // again with each tile of keys, 64 dims at a time, and tensor memory has room for
 // the scores of one tile only.
@@ -42,12 +47,11 @@ static_assert(kSoftmaxWarps * kSoftmaxRegisters + kLoadWarps * kLoadRegisters + 
 template <int DP, typename E> struct Config {
   static constexpr int kParts = sizeof(E) == 4 ? 3 : 1;           // bf16 values that make a value
   static constexpr bool kStream = DP == 256 && kParts == 3;       // queries come with each tile of keys
-  static constexpr int kScoreDims = kStream ? 64 : DP < 128 ? DP : 128, kScoreUnits = DP / kScoreDims;  // dims of a unit of a tile of keys
-  static constexpr int kValueDims = kStream || DP < 128 ? 64 : 128, kValueUnits = DP / kValueDims;      // and of values
-  static constexpr int kQueryPart = kRows * (kStream ? kScoreDims : DP) * 2;  // bytes of one part of a tile of queries (of a unit's)
-  static constexpr int kKeyPart = kKeys * kScoreDims * 2, kValuePart = kKeys * kValueDims * 2;
+  static constexpr int kUnitDims = kStream || DP < 128 ? 64 : 128, kUnits = DP / kUnitDims;  // of a tile of keys or values
+  static constexpr int kQueryPart = kRows * (kStream ? kUnitDims : DP) * 2;  // bytes of one part of a tile of queries (of a unit's)
+  static constexpr int kPart = kKeys * kUnitDims * 2;  // and of keys or values
   static constexpr int kKeyAt = kStream ? kParts * kQueryPart : 0;  // of the keys in a stage
-  static constexpr int kStageBytes = std::max(kKeyAt + kParts * kKeyPart, kParts * kValuePart);
+  static constexpr int kStageBytes = kKeyAt + kParts * kPart;
   static constexpr int kQueryBytes = kStream ? 0 : kParts * kQueryPart;
   static constexpr int kRoom = 224 * 1024 - kQueryBytes;
   static constexpr int kStages = kRoom / kStageBytes < 6 ? kRoom / kStageBytes : 6;
@@ -57,7 +61,7 @@ template <int DP, typename E> struct Config {
   // tensor memory, in columns: places for scores (large and small products' sums) and the weights they become, O, and the sums of a
   // unit of values
   static constexpr int kPlaces = kStream ? 1 : 2, kPlace = kParts == 1 ? kKeys : 2 * kKeys, kO = kPlaces * kPlace, kSums = kO + DP;
-  static_assert(kPlace >= kParts * (kKeys / 2) && kSums + kValueDims <= 512, "tensor memory");
+  static_assert(kPlace >= kParts * (kKeys / 2) && kSums + kUnitDims <= 512, "tensor memory");
 };
 
 struct Shared {
@@ -223,10 +227,10 @@ __device__ __forceinline__ bool store8(const uint32_t (&raw)[2 * sizeof(E)], boo
 }
 
 // ROWS rows of DIMS dims from d0 on to shared memory, in their parts, in blocks of 64 dims of swizzled rows.  place(r): the row's
-// offset, or -1.
-template <typename E, int ROWS, int DIMS, typename Place>
+// offset, or -1.  MOST: eights of a thread under way.
+template <typename E, int ROWS, int DIMS, int MOST, typename Place>
 __device__ __forceinline__ bool load_rows(const E* from, Place place, int d0, int dim, bool vec, bool leave_out, uint8_t* to) {
-  constexpr int kParts = sizeof(E) == 4 ? 3 : 1, kChunks = DIMS / 8, kAll = ROWS * kChunks / kLoadThreads, kOnce = kAll < 4 ? kAll : 4;
+  constexpr int kParts = sizeof(E) == 4 ? 3 : 1, kChunks = DIMS / 8, kAll = ROWS * kChunks / kLoadThreads, kOnce = kAll < MOST ? kAll : MOST;
   static_assert(ROWS * kChunks % kLoadThreads == 0 && kAll % kOnce == 0, "chunks of a thread");
   const int tid = threadIdx.x - 32 * kSoftmaxWarps;
   bool left = false;
@@ -274,36 +278,31 @@ __device__ bool load_role(const PromptView& a, int tpt, Shared& sh, uint8_t* q_a
       warp_arrive(sh.full[unit % C::kStages]);
       ++unit;
     };
-    const auto keys = [&](int t) {
-      if (loaded++ == SV_PROMPT_LOST_TILE) return false;
-      const int kb = key_of<kKeys>(it, t);
-      for (int u = 0; u < C::kScoreUnits; ++u) {
-        if (!begin()) return false;
-        uint8_t* at = stages + unit % C::kStages * C::kStageBytes;
-        if constexpr (C::kStream) load_rows<E, kRows, C::kScoreDims>(q, query, u * C::kScoreDims, a.dim, vec, false, at);
-        load_rows<E, kKeys, C::kScoreDims>(k, token(kb, a.k_row), u * C::kScoreDims, a.dim, vec, false, at + C::kKeyAt);
-        end();
-      }
-      return true;
-    };
     if constexpr (!C::kStream) {
       if (items > 0 && !warp_wait(sh, sh.q_free, items - 1)) return false;
-      load_rows<E, kRows, DP>(q, query, 0, a.dim, vec, false, q_at);
+      load_rows<E, kRows, DP, 2>(q, query, 0, a.dim, vec, false, q_at);
       tc::publish_shared();
       warp_arrive(sh.q_full);
     }
-    if (!keys(0)) return false;
-    for (int t = 0; t < tiles; ++t) {
-      if (C::kPlaces == 2 && t + 1 < tiles && !keys(t + 1)) return false;
+    // (keys and values by the same instructions, queries by few: they are fetched anew each time, and a copy for each took 446 us
+    // for what now takes 435)
+#pragma unroll 1
+    for (int n = 0; n < 2 * tiles; ++n) {
       if (loaded++ == SV_PROMPT_LOST_TILE) return false;
-      const int kb = key_of<kKeys>(it, t);
-      for (int u = 0; u < C::kValueUnits; ++u) {
-        if (!begin()) return false;
-        if (load_rows<E, kKeys, C::kValueDims>(v, token(kb, a.v_row), u * C::kValueDims, a.dim, vec, true, stages + unit % C::kStages * C::kStageBytes))
-          atomicOr(&it.dirty, 1 << (t & 31));
-        end();
+      const Turn turn = turn_of<C::kPlaces == 2>(n, tiles);
+      const int kb = key_of<kKeys>(it, turn.t);
+#pragma unroll 1
+      for (int u = 0; u < C::kUnits; ++u) {
+        if (unit >= C::kStages && !warp_wait(sh, sh.free[unit % C::kStages], unit / C::kStages - 1)) return false;
+        uint8_t* at = stages + unit % C::kStages * C::kStageBytes;
+        if (C::kStream && turn.keys) load_rows<E, kRows, C::kUnitDims, 4>(q, query, u * C::kUnitDims, a.dim, vec, false, at);
+        if (load_rows<E, kKeys, C::kUnitDims, 4>(turn.keys ? k : v, token(kb, turn.keys ? a.k_row : a.v_row), u * C::kUnitDims, a.dim, vec, !turn.keys,
+                                              at + (turn.keys ? C::kKeyAt : 0)))
+          atomicOr(&it.dirty, 1 << (turn.t & 31));
+        tc::publish_shared();
+        warp_arrive(sh.full[unit % C::kStages]);
+        ++unit;
       }
-      if (C::kPlaces == 1 && t + 1 < tiles && !keys(t + 1)) return false;
     }
     warp_arrive(sh.item_free[items % kItems]);
   }
@@ -325,7 +324,7 @@ template <int DP, typename E>
 __device__ bool product_role(Shared& sh, uint32_t q_at, uint32_t stages, uint32_t tmem) {
   using C = Config<DP, E>;
   constexpr int kProducts = C::kParts == 1 ? 1 : 6;
-  constexpr uint32_t kScores = tc::product_kind_bf16(kKeys, false), kValues = tc::product_kind_bf16(C::kValueDims, true);
+  constexpr uint32_t kScores = tc::product_kind_bf16(kKeys, false), kValues = tc::product_kind_bf16(C::kUnitDims, true);
   const auto wait = [&](uint64_t& bar, int n) {
     const bool ok = tc::barrier_wait(tc::smem_address(&bar), static_cast<uint32_t>(n & 1), &sh.gave_up);
     tc::fence_after();
@@ -339,18 +338,18 @@ __device__ bool product_role(Shared& sh, uint32_t q_at, uint32_t stages, uint32_
     tc::barrier_arrive(tc::smem_address(&sh.item_free[items % kItems]));
     if (tiles < 0) return true;
     const auto score = [&](int s) {
-      for (int u = 0; u < C::kScoreUnits; ++u, ++unit) {
+      for (int u = 0; u < C::kUnits; ++u, ++unit) {
         const int stage = unit % C::kStages;
         if (!wait(sh.full[stage], unit / C::kStages)) return false;
         const uint32_t at = stages + stage * C::kStageBytes, k = at + C::kKeyAt;
-        const uint32_t q = C::kStream ? at : q_at + u * (C::kScoreDims / 64) * (kRows * 128);
+        const uint32_t q = C::kStream ? at : q_at + u * (C::kUnitDims / 64) * (kRows * 128);
 #pragma unroll
         for (int n = 0; n < kProducts; ++n)
 #pragma unroll
-          for (int d = 0; d < C::kScoreDims / 16; ++d)
+          for (int d = 0; d < C::kUnitDims / 16; ++d)
             tc::product_f16(tmem + s * C::kPlace + (n + 1 < kProducts ? kKeys : 0),
                             tc::tile_descriptor(q + left_part<C::kParts>(n) * C::kQueryPart + (d >> 2) * (kRows * 128) + (d & 3) * 32, 16, 1024),
-                            tc::tile_descriptor(k + right_part<C::kParts>(n) * C::kKeyPart + (d >> 2) * (kKeys * 128) + (d & 3) * 32, 16, 1024), kScores,
+                            tc::tile_descriptor(k + right_part<C::kParts>(n) * C::kPart + (d >> 2) * (kKeys * 128) + (d & 3) * 32, 16, 1024), kScores,
                             u > 0 || (n > 0 && n + 1 < kProducts) || d > 0);
         arrive(sh.free[stage]);
       }
@@ -369,7 +368,7 @@ __device__ bool product_role(Shared& sh, uint32_t q_at, uint32_t stages, uint32_
     for (int t = 0; t < tiles; ++t, ++tile) {
       if (C::kPlaces == 2 && !next(t + 1)) return false;
       if (!wait(sh.p_ready[tile % C::kPlaces], tile / C::kPlaces)) return false;
-      for (int u = 0; u < C::kValueUnits; ++u, ++unit, ++sums) {
+      for (int u = 0; u < C::kUnits; ++u, ++unit, ++sums) {
         const int stage = unit % C::kStages;
         if (!wait(sh.full[stage], unit / C::kStages)) return false;
         if (sums > 0 && !wait(sh.sums_free, sums - 1)) return false;
@@ -379,7 +378,7 @@ __device__ bool product_role(Shared& sh, uint32_t q_at, uint32_t stages, uint32_
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
             tc::product_f16(tmem + C::kSums, tmem + tile % C::kPlaces * C::kPlace + left_part<C::kParts>(n) * (kKeys / 2) + k * 8,
-                            tc::tile_descriptor(v + right_part<C::kParts>(n) * C::kValuePart + k * 2048, kKeys * 128, 1024), kValues,
+                            tc::tile_descriptor(v + right_part<C::kParts>(n) * C::kPart + k * 2048, kKeys * 128, 1024), kValues,
                             n > 0 || k > 0);
         arrive(sh.free[stage]);
         arrive(sh.sums_full);
@@ -445,15 +444,15 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
   // O = O fix + the sums of the next tile: these are formed by themselves, since what the products add to is cut off, not rounded,
   // each time (over 2048 tokens that came to 6e-6 of the result; here it is 2e-7).
   const auto gather = [&](bool first, float fix) {
-    for (int u = 0; u < C::kValueUnits; ++u, ++sums) {
+    for (int u = 0; u < C::kUnits; ++u, ++sums) {
       if (!wait(sh.sums_full, sums)) return false;
 #pragma unroll 1
-      for (int d = 0; d < C::kValueDims; d += 32) {
+      for (int d = 0; d < C::kUnitDims; d += 32) {
         uint32_t y[32], o[2][16];
         tc::tmem_load32(mine + C::kSums + d, y);
         if (!first) {
-          tc::tmem_load16(own_o + u * C::kValueDims + d, o[0]);
-          tc::tmem_load16(own_o + u * C::kValueDims + d + 16, o[1]);
+          tc::tmem_load16(own_o + u * C::kUnitDims + d, o[0]);
+          tc::tmem_load16(own_o + u * C::kUnitDims + d + 16, o[1]);
           tc::wait_loads(o[0]);
           tc::wait_loads(o[1]);
         }
@@ -461,8 +460,8 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
 #pragma unroll
         for (int k = 0; k < 32; ++k)
           o[k >> 4][k & 15] = first ? y[k] : __float_as_uint(fmaf(__uint_as_float(o[k >> 4][k & 15]), fix, __uint_as_float(y[k])));
-        tc::tmem_store(own_o + u * C::kValueDims + d, o[0]);
-        tc::tmem_store(own_o + u * C::kValueDims + d + 16, o[1]);
+        tc::tmem_store(own_o + u * C::kUnitDims + d, o[0]);
+        tc::tmem_store(own_o + u * C::kUnitDims + d + 16, o[1]);
       }
       tc::wait_stores();
       tc::fence_before();
