@@ -27,8 +27,8 @@
 // 836 tokens (80 us) are bound by each item's chain: its first and its masked
 // tiles, its results, and the instructions of these, which are fetched anew for
 // each item.  256 dims leave room for one tile of queries: each tile of keys and
-// values, 128 KB, is read for that alone, and shared memory bounds it (71 us for
-// three prompts of up to 2011 tokens with 14 heads, 895 TFLOP/s).
+// values, 128 KB, is read for that alone, and shared memory bounds it (68 us for
+// three prompts of up to 2011 tokens with 14 heads, 930 TFLOP/s).
 #include "sv_prompt_items.cuh"
 
 #include <type_traits>
@@ -68,7 +68,7 @@ struct Shared {
   Sequences sequences;
   uint32_t tmem;
   int gave_up;
-  int look[10];          // are there rows that do not see all of the values in a stage?
+  int look[10];          // of the values in a stage the last ones that some rows do not see
   int claimed, finished[8];  // items known, and done with by each warp that writes results
 };
 
@@ -142,7 +142,8 @@ __device__ bool load_role(const PromptView& a, const Maps& maps, int tpt, Shared
         const Turn turn = turn_of<C::NQ == 1>(u, it.tiles);
         const int kb = key_of<kKeys>(it, turn.t);
         const CUtensorMap* map = turn.keys ? &maps.k : &maps.v;
-        const bool look = !turn.keys && partly_seen<kKeys, C::NQ>(a, it, tpt, turn.t);
+        // (without a window every row sees those up to the first token)
+        const int look = turn.keys || !partly_seen<kKeys, C::NQ>(a, it, tpt, turn.t) ? 0 : a.window ? kKeys : kKeys - max(0, it.tok0 + 1 - kb);
 #pragma unroll 1
         for (int half = 0; half < C::kHalves; ++half) {
           const int unit = under.units, stage = unit % C::kStages;
@@ -198,7 +199,11 @@ __device__ __noinline__ void end_loads(const PromptView& a, int tpt, Shared& sh,
 // Both values of a word, 0 where they are not finite.
 __device__ __forceinline__ uint32_t finite_of(uint32_t w) { return w & ~__vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u); }
 
-// It takes part in every copy's way, so that it is never a round of the stages behind.
+// The top bit of each half is set where its value is not finite: an exponent of ones carries into it.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
+
+// It takes part in every copy's way, so that it is never a round of the stages behind.  (The last tile's sums wait for it: with all
+// of its values looked at, 256 dims took 72 us.)
 template <int DP>
 __device__ bool check_role(Shared& sh, uint8_t* kv) {
   using C = Config<DP>;
@@ -213,17 +218,18 @@ __device__ bool check_role(Shared& sh, uint8_t* kv) {
     for (int u = 0; u < 2 * C::kHalves * tiles; ++u, ++unit) {
       const int stage = unit % C::kStages;
       if (!warp_wait(sh, sh.kv_full[stage], unit / C::kStages)) return false;
-      if (sh.look[stage]) {
-        uint4* at = reinterpret_cast<uint4*>(kv + stage * C::kUnitBytes);
+      if (const int look = sh.look[stage]) {
         bool found = false;
-#pragma unroll 4
-        for (int c = tid; c < C::kUnitBytes / 16; c += 32 * C::kCheckWarps) {
-          uint4 v = at[c];
-          // the largest magnitude of each half word: 0x7f80 and more is not finite
-          const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-          if (__vcmpgeu2(m, 0x7f807f80u)) {
-            found = true;
-            at[c] = make_uint4(finite_of(v.x), finite_of(v.y), finite_of(v.z), finite_of(v.w));
+#pragma unroll 1
+        for (int block = 0; block < C::kUnitBytes; block += C::kBlockBytes) {
+          uint4* at = reinterpret_cast<uint4*>(kv + stage * C::kUnitBytes + block) + (kKeys - look) * 8;
+#pragma unroll 2
+          for (int c = tid; c < look * 8; c += 32 * C::kCheckWarps) {
+            const uint4 v = at[c];
+            if ((not_finite(v.x) | not_finite(v.y) | not_finite(v.z) | not_finite(v.w)) & 0x80008000u) {
+              found = true;
+              at[c] = make_uint4(finite_of(v.x), finite_of(v.y), finite_of(v.z), finite_of(v.w));
+            }
           }
         }
         if (found) it.dirty = 1;
