@@ -348,3 +348,17 @@ def test_captured_and_replayed_beside_another_stream(sv, dtype):
         other = sv.prompt_attention(q, k, v, new_start=start, max_new=500, stream=side)
     side.synchronize()
     assert torch.equal(other, want)
+
+
+@pytest.mark.parametrize("dtype,shift", [("bf16", 0), ("bf16", 1), ("f32", 0)])
+def test_offsets_beyond_32_bits(sv, dtype, shift):
+    import torch
+    g = np.random.default_rng(5)
+    n, step = 40, 1 << 26
+    dev = [to_gpu(x, dtype) for x in _inputs(g, dtype, n, 4, 2, 64)]
+    memory = torch.empty(n * step, dtype=dev[0].dtype, device="cuda")
+    far = [memory.as_strided((n, h, 64), (step, 64, 1), 1024 * i + shift) for i, h in enumerate((4, 2, 2, 4))]
+    for x, y in zip(far, dev):
+        x.copy_(y)
+    out = sv.prompt_attention(*far[:3], out=far[3], new_start=to_gpu(np.array([0, n], np.int32)), max_new=n)
+    near(out.double().cpu().numpy(), None, *(x.double().cpu().numpy() for x in dev), [0, n], 64 ** -0.5, 0, 0, dtype)

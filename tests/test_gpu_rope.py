@@ -155,3 +155,18 @@ def test_captured_and_replayed(sv):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[0], sv.rope(x, None, positions, freq)[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_offsets_beyond_32_bits(sv, dtype, shift):
+    import torch
+    g = np.random.default_rng(5)
+    n, step = 40, 1 << 26
+    rows, positions, freq = [round_to(g.normal(0, 1, (n, h, 64)), dtype) for h in (4, 2)], np.arange(n, dtype=np.int32), _freq(32)
+    memory = torch.empty(n * step, dtype=to_gpu(rows[0], dtype).dtype, device="cuda")
+    far = [memory.as_strided((n, h, 64), (step, 64, 1), 1024 * i + shift) for i, h in enumerate((4, 2))]
+    for x, y in zip(far, rows):
+        x.copy_(to_gpu(y, dtype))
+    for x, y in zip(sv.rope(*far, to_gpu(positions), to_gpu(freq), out=tuple(far)), rows):
+        _near(x, y, positions[None], freq, np.zeros(32, int), False, dtype)
