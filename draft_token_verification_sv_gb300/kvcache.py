@@ -245,7 +245,7 @@ def _attention_plan(q, kc, vc, ks, vs, table, lens, start, max_new, parents, sca
 
 @functools.lru_cache(maxsize=_KEPT)
 def _assign_plan(free, count, table, held, lens, page, start, max_new, total, parents, slots, positions, status):
-    """slots None: the call makes its results itself, or has none."""
+    """slots and positions None: the call makes its results itself, or has none."""
     free, count, table = _see(free, "pool['free']"), _see(count, "pool['count']"), _see(table, "page_table")
     if free.dtype != torch.int32 or len(free.shape) != 1 or not _contiguous(free):
         raise ValueError("pool['free'] must be a contiguous int32 [num_pages] tensor")
@@ -332,6 +332,8 @@ def kv_assign(pool: dict, page_table: torch.Tensor, held: torch.Tensor, ctx_lens
     are None where ``max_new`` is 0."""
     max_new = int(max_new)
     slots, positions = (None, None) if out is None else out
+    if out is not None and (slots is None or positions is None):
+        raise ValueError("out must be (slots, positions), both of them")
     free, count = pool["free"], pool["count"]
     d, shape, gpu = _assign_plan(_meta(free), _meta(count), _meta(page_table), _meta(held), _meta(ctx_lens), int(page_size),
                                  _meta(new_start), max_new, None if total is None else int(total), _meta(parents), _meta(slots),
