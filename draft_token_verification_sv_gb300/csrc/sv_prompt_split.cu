@@ -541,7 +541,7 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
       fix = 1.0f;
     }
     if (C::kPlaces == 2 && !gather(tiles == 1, fix_before)) return false;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = 1.0f / l;  // (see sv_prompt_tiles.cu)
     E* out = static_cast<E*>(a.out) + at.row * a.out_row + at.head * a.out_head;
 #pragma unroll 1
     for (int d = 0; d < DP; d += 16) {

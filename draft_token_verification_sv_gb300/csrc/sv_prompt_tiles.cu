@@ -523,7 +523,7 @@ __device__ bool softmax_role(const PromptView& a, int tpt, float f, Shared& sh, 
         tc::fence_before();
         warp_arrive(sh.p_ready[s]);
       }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = 1.0f / l;  // (a row sees its own token: l is 0 where all of its scores are -inf, and its results NaN)
       const int64_t row = it.row0 + static_cast<int64_t>(token);
       const int head = it.h * a.group + row_head;
       uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.out_row + head * a.out_head;

@@ -712,8 +712,11 @@ typedef struct sv_prompt_attention_desc {
  * and leave products below 2^-24 of the whole out; values below 2^-100 keep
  * fewer bits.  Weights are not taken from a row's largest score but from one
  * within 2^13 a tile of it, so sums over values overflow where their
- * magnitudes pass 2^100.  A query or key that is not finite makes NaN of the
- * results that it enters.
+ * magnitudes pass 2^100.  Of bf16 queries and keys that are not finite scores
+ * are as the formula says: -inf has weight 0, a query that sees no other
+ * score gets NaN and an lse of -inf, one that sees a NaN or inf gets NaN for
+ * both.  A float32 query or key that is not finite makes NaN of the results
+ * that it enters.
  */
 sv_status sv_prompt_attention(const sv_prompt_attention_desc* desc, const void* q, const void* k, const void* v,
                               const int32_t* new_start, void* out, float* lse, int32_t* row_status,
