@@ -146,8 +146,9 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&w)[PARTS]) {
 }
 
 // The same of values whose first part may not be finite: it is taken towards
-// zero where it would pass bf16's range, and infinities and NaN are their own
-// first part (or left out, which the answer says).
+// zero where it would pass bf16's range, and infinities and NaN become NaN (or
+// are left out, which the answer says): products of an infinity with the other
+// side's parts would have their signs, which differ.
 __device__ __noinline__ bool split_any(const float (&x)[8], bool leave_out, uint32_t (&w)[3][4]) {
   bool left = false;
   for (int p = 0; p < 3; ++p)
@@ -161,7 +162,7 @@ __device__ __noinline__ bool split_any(const float (&x)[8], bool leave_out, uint
     }
     const bool large = (__float_as_uint(v) & 0x7fffffffu) >= 0x7f7f8000u;
     for (int p = 0; p < (finite ? 3 : 1); ++p) {
-      const uint32_t top = v != v ? 0x7fffu : large ? __float_as_uint(v) >> 16 : floats_to_bf16x2(v, 0.0f) & 0xffffu;
+      const uint32_t top = !finite ? 0x7fffu : large ? __float_as_uint(v) >> 16 : floats_to_bf16x2(v, 0.0f) & 0xffffu;
       w[p][k >> 1] |= top << (16 * (k & 1));
       v -= __uint_as_float(top << 16);
     }

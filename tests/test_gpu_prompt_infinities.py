@@ -2,7 +2,8 @@
 
 bf16 calls take the formula as it stands: a score of -inf has weight 0, a row
 that sees no other is NaN with a log-sum-exp of -inf, and a score that is NaN or
-inf makes NaN of both."""
+inf makes NaN of both.  float32 calls, which multiply parts of the values, make
+NaN of all that such a query or key enters."""
 import numpy as np
 import pytest
 
@@ -79,7 +80,30 @@ def test_bf16_follows_the_formula(sv, dim, shift, what, window, sinks):
         assert (np.abs(out[known] - want[known]) <= tol[known]).all() and (np.abs(lse[known] - wlse[known]) <= ltol[known]).all()
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 3)])
+def test_float32_results_that_a_key_enters_are_nan(sv, dim, what, window, sinks):
+    g = np.random.default_rng(dim)
+    q, k, v = (round_to(g.normal(0, s, (N, h, dim)), "f32") for h, s in ((HEADS, 1.5), (KV_HEADS, 1), (KV_HEADS, 1)))
+    # values whose second and third parts have their sign, or are 0: such infinities gave scores of their own
+    q[::2, :, 5] = np.float32(1 + 2 ** -10 + 2 ** -18)
+    q[1::4, :, 5] = 2
+    i = np.arange(N)
+    for bad in (0, 140, 257, 299):
+        spoilt = k.copy()
+        spoilt[bad, 1, 5] = what
+        sees = (i >= bad) & ((window == 0) | (i - bad < window) | (bad < sinks))
+        out, lse = _call(sv, (q, spoilt, v), "f32", 0, window, sinks)
+        hit = np.zeros((N, HEADS), bool)
+        hit[sees, HEADS // 2:] = True
+        assert np.isnan(out[hit]).all() and np.isnan(lse[hit]).all(), (bad, np.argwhere(hit & ~np.isnan(lse))[:4].tolist())
+        out[hit], lse[hit] = 0, 0
+        clean = _call(sv, (q, k, v), "f32", 0, window, sinks)
+        assert (out[~hit] == clean[0][~hit]).all() and (lse[~hit] == clean[1][~hit]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
 def test_a_query_s_row_is_nan(sv, dtype, dim, what):
