@@ -53,11 +53,15 @@ __device__ __forceinline__ unsigned long long turns(float inv_freq) {
 
 // Cosine and sine of an angle in units of 2^-64 turns: the nearest quarter
 // turn, and Taylor's polynomials on the rest, which is at most pi / 4 (the
-// first term left out is 2^-29 of a sine, 2^-32 of a cosine).
+// first term left out is 2^-29 of a sine, 2^-32 of a cosine).  The rest is
+// taken in two halves of 32 bits with signs, so that a small one keeps float's
+// bits, and with it the sine of a small angle: 2^-21 of its value.
 __device__ __forceinline__ float2 cos_sin(unsigned long long angle) {
-  const uint32_t a = static_cast<uint32_t>(angle >> 32);
-  const uint32_t quarter = (a + 0x20000000u) >> 30;
-  const float x = static_cast<float>(static_cast<int32_t>(a - (quarter << 30))) * 1.46291807926715968105e-9f;  // 2 pi / 2^32
+  constexpr float kUnit = 1.46291807926715968105e-9f;  // 2 pi / 2^32
+  const uint32_t quarter = static_cast<uint32_t>((angle + (1ull << 61)) >> 62);
+  const unsigned long long rest = angle - (static_cast<unsigned long long>(quarter) << 62);
+  const int32_t low = static_cast<int32_t>(static_cast<uint32_t>(rest)), high = static_cast<int32_t>(static_cast<uint32_t>(rest + 0x80000000ull >> 32));
+  const float x = fmaf(static_cast<float>(high), kUnit, static_cast<float>(low) * (kUnit * 0x1p-32f));
   const float z = x * x;
   const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 2.755731922e-6f, -1.984126984e-4f), 8.333333333e-3f), -1.666666667e-1f), x);
   const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.755731922e-7f, 2.480158730e-5f), -1.388888889e-3f), 4.166666667e-2f), -0.5f), 1.0f);

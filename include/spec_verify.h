@@ -656,8 +656,9 @@ typedef struct sv_rope_desc {
  *   (a cos t - b sin t, a sin t + b cos t),  t = positions[axis[i], r] * inv_freq[i].
  * Text has one axis; images and video have one for the time, the height and
  * the width each, which share the pairs.  t is taken modulo a whole turn in
- * 64 bits, so that far positions are as exact as near ones; sine and cosine
- * are within 2^-23 of their values, and the result is rounded once.
+ * 64 bits (2^-64 of a turn is lost for each position at most), so that far
+ * positions are as exact as near ones; sine and cosine are off by 2^-23 at
+ * most and, next to 0, by 2^-21 of themselves; the result is rounded once.
  *
  *   q [rows, heads, D], k [rows, kv_heads, D];  positions [axes, rows] int32
  *   (any value);  inv_freq [R / 2] float, below 2^60 in magnitude:
