@@ -51,6 +51,9 @@ __device__ __forceinline__ unsigned long long turns(float inv_freq) {
   return u >> 31 ? 0ull - t : t;
 }
 
+// Is it one that turns() takes?
+__device__ __forceinline__ bool is_frequency(float inv_freq) { return fabsf(inv_freq) < 0x1p60f; }
+
 // Cosine and sine of an angle in units of 2^-64 turns: the nearest quarter
 // turn, and Taylor's polynomials on the rest, which is at most pi / 4 (the
 // first term left out is 2^-29 of a sine, 2^-32 of a cosine).  The rest is
@@ -91,7 +94,10 @@ __global__ void __launch_bounds__(kPairThreads) rope_pairs_kernel(const __grid_c
     const bool pair = u < w.half;
     const int i = !pair ? u + w.half : w.adjacent ? 2 * u : u, j = w.adjacent ? 2 * u + 1 : u + w.half;
     float2 t = make_float2(1.0f, 0.0f);
-    if (pair) t = cos_sin(static_cast<unsigned long long>(angle_position(w, u, row)) * turns(__ldg(w.inv_freq + u)));
+    if (pair) {
+      const float f = __ldg(w.inv_freq + u);
+      t = is_frequency(f) ? cos_sin(static_cast<unsigned long long>(angle_position(w, u, row)) * turns(f)) : make_float2(CUDART_NAN_F, CUDART_NAN_F);
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const E* x = static_cast<const E*>(w.side[s].x) + row * w.side[s].x_row;
@@ -139,12 +145,14 @@ __global__ void __launch_bounds__(kThreads) rope_units_kernel(const __grid_const
   const bool turned = unit < w.half >> 3, busy = sub < per;
   wait_for_stream();
   unsigned long long by[8];
-  uint32_t axes = 0;
+  uint32_t axes = 0, none = 0;  // two bits a pair: its axis; a bit: it has no frequency
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     by[i] = 0;
     if (turned) {
-      by[i] = turns(__ldg(w.inv_freq + 8 * unit + i));
+      const float f = __ldg(w.inv_freq + 8 * unit + i);
+      by[i] = turns(f);
+      none |= is_frequency(f) ? 0u : 1u << i;
       axes |= static_cast<uint32_t>(w.axis[8 * unit + i]) << (2 * i);
     }
   }
@@ -172,6 +180,11 @@ __global__ void __launch_bounds__(kThreads) rope_units_kernel(const __grid_const
         const long long mine = n & 2 ? (n & 1 ? position[3] : position[2]) : (n & 1 ? position[1] : position[0]);
         t[i] = cos_sin(static_cast<unsigned long long>(mine) * by[i]);
       }
+    }
+    if (none != 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (none >> i & 1u) t[i] = make_float2(CUDART_NAN_F, CUDART_NAN_F);
     }
     if (!busy) continue;
     for (int h0 = part * per + sub; h0 < all; h0 += kHeads * step) {

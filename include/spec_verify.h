@@ -661,8 +661,8 @@ typedef struct sv_rope_desc {
  * most and, next to 0, by 2^-21 of themselves; the result is rounded once.
  *
  *   q [rows, heads, D], k [rows, kv_heads, D];  positions [axes, rows] int32
- *   (any value);  inv_freq [R / 2] float, below 2^60 in magnitude:
- *   radians a position.
+ *   (any value);  inv_freq [R / 2] float, radians a position: a pair whose
+ *   one is not below 2^60 in magnitude (NaN) becomes NaN.
  *   q_out, k_out: like q and k.  Either may be its input (the same pointer
  *   and strides); otherwise they share no memory with q, k or one another
  *   (refused where they begin at one address).

@@ -1,4 +1,5 @@
-"""Rotary positions at angles next to a multiple of a quarter turn.
+"""Rotary positions at angles next to a multiple of a quarter turn, and at
+frequencies that are none.
 
 An angle is a number of 2^-64 turns, at most one of them too small for each
 position; the rest behind the nearest quarter turn becomes a float by two
@@ -71,3 +72,30 @@ def test_small_angles_keep_their_bits(sv, half, adjacent, position):
         off, tol = np.abs(have - want), (2.0 ** -21 + 2.0 ** -24) * np.abs(want) + lost
         assert (off <= tol).all(), (freq[off > tol].tolist(), (off / np.maximum(np.abs(want), 1e-300))[off > tol].tolist())
 
+
+NONE = [np.nan, np.inf, -np.inf, 2.0 ** 60, -2.0 ** 60, 2.0 ** 63, 2.0 ** 64, 1e30, float(np.finfo(np.float32).max)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,half", [(64, 32), (64, 31), (128, 16)])
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("axes", [1, 3])
+def test_pairs_of_a_frequency_that_is_none_are_nan(sv, dtype, dim, half, adjacent, axes):
+    import torch
+    g = np.random.default_rng(0)
+    freq = (10000.0 ** (-np.arange(half) / half)).astype(np.float32)
+    bad = g.permutation(half)[:len(NONE)]
+    freq[np.setdiff1d(np.arange(half), bad)[0]] = np.nextafter(np.float32(2.0 ** 60), np.float32(0))
+    x = to_gpu(g.normal(size=(5, 6, dim)).astype(np.float32), dtype)
+    positions = to_gpu(g.integers(0, 1000, (axes, 5)).astype(np.int32))
+    kw = dict(adjacent=adjacent, sections=None if axes == 1 else (half - 2, 1, 1))
+    positions = positions[0].contiguous() if axes == 1 else positions
+    clean = sv.rope(x[:, :4], x[:, 4:], positions, to_gpu(freq), **kw)
+    assert all(y.isfinite().all() for y in clean)
+    freq[bad] = NONE
+    for y, want in zip(sv.rope(x[:, :4], x[:, 4:], positions, to_gpu(freq), **kw), clean):
+        hit = torch.zeros(dim, dtype=torch.bool, device="cuda")
+        for i in bad.tolist():
+            hit[[2 * i, 2 * i + 1] if adjacent else [i, i + half]] = True
+        assert y[..., hit].isnan().all()
+        assert torch.equal(y[..., ~hit], want[..., ~hit])
