@@ -289,10 +289,12 @@ __global__ void __launch_bounds__(kPlaceThreads) kv_assign_places_kernel(AssignV
     place_token(a, b, s, held, static_cast<int>(i));
 }
 
-// From this many pages that sequences could hold, or new tokens, on, several blocks move and place them.  Of 64 sequences with a
-// token each a call takes 4.3 us in one block, 6.2 in two launches; with 2048 tokens 5.6 and 6.6, with 4000 7.1 and 6.5, with 8000
-// 10.5 and 6.5.  Pages cost one block 0.5 us for 1000 that move (16,000: 12.6 and 7.3 us), but a step moves few of those that a
-// sequence could hold.
+// From this many new tokens to place, or pages that may move, on, several blocks do that, in two launches behind a memset of the
+// flags.  64 sequences with a token each take 4.3 us in one block and 10.3 in several (6.7 without flags); without flags 2048 tokens
+// take 5.6 in one and 6.6 in several, 4000 7.1 and 6.5, 8000 10.5 and 6.5; pages cost one block 0.5 us for 1000 that move.  A call
+// of new tokens takes about the pages that these fill, whatever the table has room for (64 sequences with room for 2048 pages each:
+// 4.6 us, 10.3 where the room decided), and a call without any may give back all that the pool has.  (Should a call of few tokens
+// move 120,000 pages, they take 62 us more than in several blocks.)
 constexpr int64_t kManyPages = 16384, kManyTokens = 4000;
 
 }  // namespace
@@ -313,14 +315,15 @@ sv_status kv_assign(const sv_kv_assign_desc& d, int32_t* free_pages, int32_t* fr
                      free_pages, free_count, page_table, held, parents, slots, positions};
   if (d.batch <= kThreads) {
     const int64_t tokens = slots || positions ? d.total_new : 0;
-    const int64_t pages = static_cast<int64_t>(d.batch) * d.max_pages;
+    const int64_t room = std::min<int64_t>(static_cast<int64_t>(d.batch) * d.max_pages, d.num_pages);
+    const int64_t pages = std::min<int64_t>(room, d.total_new > 0 ? d.total_new / d.page_size + d.batch : room);
     if (pages <= kManyPages && tokens <= kManyTokens) {
       if (launch_early(kv_assign_few_kernel<kAll>, dim3(1), dim3(kThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
       note_launch(stream);
       return SV_OK;
     }
     if (row_status && cudaMemsetAsync(row_status, 0, static_cast<size_t>(d.batch) * sizeof(int32_t), stream) != cudaSuccess) return SV_ERR_CUDA;
-    const int64_t share = std::max(pages, tokens) / (2 * kThreads) + 1;
+    const int64_t share = std::max(room, tokens) / (2 * kThreads) + 1;
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(share, 152));
     if (launch_early(kv_assign_few_kernel<kMove>, dim3(blocks), dim3(kThreads), 0, stream, a) != cudaSuccess) return SV_ERR_CUDA;
     note_launch(stream);
