@@ -112,7 +112,9 @@ def _prompt_plan(q, k, v, start, max_new, scale, window, sinks, out, status):
             raise ValueError("out must match q in shape and dtype")
         _, _, _, *out_strides = _rows(out, "out", B, ragged)
     _int32(status, "row_status", B, _PER_SEQUENCE)
-    a = N.PromptAttentionDesc(B, heads, kv_heads, dim, _new(start, max_new, q, B), n, _code(q), dim ** -0.5 if scale is None else scale,
+    most = _new(start, max_new, q, B)
+    # (of packed rows no sequence has more than there are; the library refuses bounds whose rows of heads pass 32 bits)
+    a = N.PromptAttentionDesc(B, heads, kv_heads, dim, min(most, n) if ragged else most, n, _code(q), dim ** -0.5 if scale is None else scale,
                               _count(window, "window"), _count(sinks, "sinks"), *q_strides, *k_strides, *v_strides, *out_strides)
     return ctypes.byref(a), _one_device(q, k, v, start, out, status)
 

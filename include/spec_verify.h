@@ -675,7 +675,7 @@ typedef struct sv_prompt_attention_desc {
   int32_t heads;         /* query heads: a multiple of kv_heads, heads / kv_heads <= 128 */
   int32_t kv_heads;      /* in [1, 1024] */
   int32_t head_dim;      /* D: a multiple of 16 in [16, SV_MAX_HEAD_DIM] */
-  int32_t max_new;       /* >= 0: the most tokens of a sequence */
+  int32_t max_new;       /* >= 0: the most tokens of a sequence; max_new * (heads / kv_heads) < 2^31 - 256 */
   int32_t total_new;     /* rows of q, k, v and out; batch * max_new when new_start is NULL; total_new * heads < 2^31 */
   sv_dtype dtype;        /* of q, k, v and out */
   float scale;           /* of the scores, finite (normally 1 / sqrt(D)) */
