@@ -23,6 +23,16 @@ def test_many_sequences_of_many_heads(sv, dtype):  # noqa: F811
     _check(sv, dtype, [1] * 300, heads=512, kv_heads=512, dim=16)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_bound_far_above_what_comes(sv, dtype):  # noqa: F811
+    import torch
+    g = np.random.default_rng(0)
+    x = [to_gpu(x, dtype) for x in _inputs(g, dtype, 200, 4, 2, 64)]
+    start = to_gpu(np.array([0, 70, 70, 200], np.int32))
+    want = sv.prompt_attention(*x, new_start=start, max_new=130)
+    assert torch.equal(sv.prompt_attention(*x, new_start=start, max_new=2 ** 31 - 1), want)
+
+
 @pytest.mark.parametrize("dtype,dim,n", [("bf16", 64, 50_001), ("bf16", 128, 20_001), ("bf16", 256, 9_001), ("f32", 64, 9_001)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (5000, 7)])
 def test_rows_of_a_long_prompt(sv, dtype, dim, n, window, sinks):  # noqa: F811
