@@ -329,7 +329,9 @@ def kv_assign(pool: dict, page_table: torch.Tensor, held: torch.Tensor, ctx_lens
 
     Updates pool, page_table and held, and returns dict(slots=int64,
     positions=int32), each [B, max_new] or [total] (or ``out``, the two); both
-    are None where ``max_new`` is 0."""
+    are None where ``max_new`` is 0.  Rows of no sequence, and of those whose
+    starts are no rows of the call, are not written: in results that the call
+    makes itself they hold anything."""
     max_new = int(max_new)
     slots, positions = (None, None) if out is None else out
     if out is not None and (slots is None or positions is None):

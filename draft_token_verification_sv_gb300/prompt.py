@@ -128,7 +128,11 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, new_s
     q [B, n, heads, dim], k and v [B, n, kv_heads, dim] (or [total, ...] with
     ``new_start`` [B + 1] and ``max_new``, the most tokens of a sequence),
     float32 or bfloat16; ``scale`` defaults to 1 / sqrt(dim).  Returns out like
-    q, and with ``lse`` the log-sum-exp [..., heads] float32 as well."""
+    q, and with ``lse`` the log-sum-exp [..., heads] float32 as well.
+
+    Rows of no sequence, and of sequences that are left out (``row_status``
+    says which), are not written: in ``out`` they keep what they had, in results
+    that the call makes itself they hold anything."""
     a, gpu = _prompt_plan(_meta(q), _meta(k), _meta(v), _meta(new_start), None if max_new is None else int(max_new),
                           None if scale is None else float(scale), int(window), int(sinks), _meta(out), _meta(row_status))
     if out is None:

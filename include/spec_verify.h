@@ -696,10 +696,10 @@ typedef struct sv_prompt_attention_desc {
  *   s_j = scale * <q_i, k_j>,  out = sum_j softmax(s)_j v_j,
  *   lse = ln(sum_j exp(s_j)).
  * What a query does not see has no influence on its result, whatever it
- * holds (infinities and NaN too).  Rows that belong to no sequence are not
- * touched, those of several are any one's.  A sequence with a negative
- * length, more than max_new tokens or rows outside [0, total_new) is left
- * out and flagged SV_ROW_BAD_LENGTH.
+ * holds (infinities and NaN too).  A sequence with a negative length, more
+ * than max_new tokens or rows outside [0, total_new) is left out and flagged
+ * SV_ROW_BAD_LENGTH.  Rows of out and lse that belong to no sequence, or to
+ * one that is left out, are not touched, those of several are any one's.
  *
  *   q [total_new, heads, D];  k, v [total_new, kv_heads, D];
  *   out [total_new, heads, D], shares no memory with q, k or v (refused
