@@ -273,12 +273,6 @@ __device__ bool load_role(const PromptView& a, int tpt, Shared& sh, uint8_t* q_a
     const auto token = [&](int kb, int64_t stride) {
       return [=, &a](int r) { return kb + r < n && sv_in(static_cast<int64_t>(it.row0) + kb + r, a.total_new) ? (kb + r) * stride : int64_t{-1}; };
     };
-    const auto begin = [&]() { return unit < C::kStages || warp_wait(sh, sh.free[unit % C::kStages], unit / C::kStages - 1); };
-    const auto end = [&]() {
-      tc::publish_shared();
-      warp_arrive(sh.full[unit % C::kStages]);
-      ++unit;
-    };
     if constexpr (!C::kStream) {
       if (items > 0 && !warp_wait(sh, sh.q_free, items - 1)) return false;
       load_rows<E, kRows, DP, 2>(q, query, 0, a.dim, vec, false, q_at);
