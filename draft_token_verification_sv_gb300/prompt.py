@@ -32,7 +32,7 @@ def _token_rows(m, name):
 
 
 @functools.lru_cache(maxsize=_KEPT)
-def _rope_plan(q, k, positions, inv_freq, sections, adjacent, q_out, k_out):
+def _rope_plan(q, k, positions, inv_freq, sections, axis, adjacent, q_out, k_out):
     """q_out None: the call makes its results itself."""
     q, k, p, f = _see(q, "q"), _see(k, "k"), _see(positions, "positions"), _see(inv_freq, "inv_freq")
     q_out, k_out = _see(q_out, "out[0]"), _see(k_out, "out[1]")
@@ -46,9 +46,13 @@ def _rope_plan(q, k, positions, inv_freq, sections, adjacent, q_out, k_out):
         raise ValueError("positions must be a contiguous int32 tensor with one entry for each token, or [axes, ...] of such")
     if not 1 <= axes <= N.SV_MAX_ROPE_AXES:
         raise ValueError(f"positions may have 1 to {N.SV_MAX_ROPE_AXES} axes")
-    sections = (half,) if sections is None and axes == 1 else sections
-    if sections is None or len(sections) != axes or min(sections) < 0 or sum(sections) != half:
-        raise ValueError("sections must have one entry for each axis of positions, and inv_freq's length as their sum")
+    if axis is None:
+        sections = (half,) if sections is None and axes == 1 else sections
+        if sections is None or len(sections) != axes or min(sections) < 0 or sum(sections) != half:
+            raise ValueError("sections must have one entry for each axis of positions, and inv_freq's length as their sum")
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    elif sections is not None or len(axis) != half or min(axis) < 0 or max(axis) >= axes:
+        raise ValueError("axis must have one entry for each of inv_freq, which is an axis of positions, and takes the place of sections")
     q_out_strides, k_heads, k_strides, k_out_strides = (heads * dim, dim), 0, (dim, dim), (dim, dim)
     if q_out is not None:
         if q_out.shape != q.shape or q_out.dtype != q.dtype:
@@ -65,25 +69,27 @@ def _rope_plan(q, k, positions, inv_freq, sections, adjacent, q_out, k_out):
             _, _, _, *k_out_strides = _token_rows(k_out, "out[1]")
     d = N.RopeDesc(rows, heads, k_heads, dim, 2 * half, axes, int(adjacent), _code(q), rows, *q_strides, *k_strides,
                    *q_out_strides, *k_out_strides)
-    d.axis[:half] = [a for a, n in enumerate(sections) for _ in range(n)]
+    d.axis[:half] = axis
     return ctypes.byref(d), _one_device(q, k, p, f, q_out, k_out)
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor, *,
-         sections: tuple | None = None, adjacent: bool = False, out: tuple | None = None, stream=None):
+         sections: tuple | None = None, axis: tuple | None = None, adjacent: bool = False, out: tuple | None = None, stream=None):
     """Rotary position embedding of queries and keys; see sv_rope.
 
     q [..., heads, dim], k [..., kv_heads, dim] or None, float32 or bfloat16;
     ``positions`` int32 [...], or [axes, ...] with ``sections``: how many pairs,
-    one after the other, turn with each axis.  ``inv_freq`` float32 holds the
-    radians a position of every pair; dims beyond 2 * len(inv_freq) stay.
+    one after the other, turn with each axis, or with ``axis``: the axis of each
+    pair.  ``inv_freq`` float32 holds the radians a position of every pair; dims
+    beyond 2 * len(inv_freq) stay.
     Pairs are (i, i + len(inv_freq)), with ``adjacent`` (2i, 2i + 1).  Returns
     (q, k) in new memory, or in ``out``, which may be (q, k) themselves."""
     q_out, k_out = (None, None) if out is None else out
     if out is not None and q_out is None:
         raise ValueError("out must be (q's result, k's)")
     d, gpu = _rope_plan(_meta(q), _meta(k), _meta(positions), _meta(inv_freq),
-                        None if sections is None else tuple(int(n) for n in sections), bool(adjacent), _meta(q_out), _meta(k_out))
+                        None if sections is None else tuple(int(n) for n in sections), None if axis is None else tuple(int(a) for a in axis),
+                        bool(adjacent), _meta(q_out), _meta(k_out))
     if out is None:
         q_out, k_out = _empty_like(q, stream), None if k is None else _empty_like(k, stream)
     _call(gpu, "sv_rope", d, q.data_ptr(), _at(k), positions.data_ptr(), inv_freq.data_ptr(), q_out.data_ptr(),
