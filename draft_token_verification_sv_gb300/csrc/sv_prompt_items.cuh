@@ -29,15 +29,56 @@ struct Item {
   int dirty;             // not 0: values that are not finite were taken out
 };
 
-// Sequences where they are few: the longest first, their rows, and the items up to and with each.
+// Sequences where they are few: the longest first, their rows, and the items up to and with each.  Where they are more, packed ones:
+// the items up to and with each of at most kSorted runs of them (padded ones need none: all have as many).
 constexpr int kSorted = 96;
 struct Sequences {
-  int n[kSorted], row0[kSorted], items[kSorted];
+  union {
+    struct {
+      int n[kSorted], row0[kSorted];
+    } few;
+    long long upto[kSorted];
+  };
+  int items[kSorted];
 };
+
+// Of how many sequences a run is, where they are more than kSorted.
+__device__ __forceinline__ int run_of(const PromptView& a) { return (a.batch + kSorted - 1) / kSorted; }
+
+// Items of the runs, a warp a run, and their sums: without them a search went through all sequences (16,000 padded ones of 8 tokens
+// took 112 ms).
+__device__ __forceinline__ void sum_runs(const PromptView& a, Sequences& sq, int per, int threads) {
+  const int run = run_of(a), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int r = warp; r < kSorted; r += threads >> 5) {
+    const int end = min((r + 1) * run, a.batch);
+    long long own = 0;
+    for (int b = r * run + lane; b < end; b += 32) own += static_cast<long long>((prompt_span(a, b).n + per - 1) / per) * a.kv_heads;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) own += __shfl_down_sync(0xffffffffu, own, o);
+    if (lane == 0) sq.upto[r] = own;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long before = 0;
+    for (int r = lane; r < kSorted; r += 32) {
+      long long upto = sq.upto[r];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+      }
+      sq.upto[r] = before + upto;
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+}
 
 // By all threads of the block, of `per` tokens to an item; complete behind its next barrier.
 __device__ __forceinline__ void sort_sequences(const PromptView& a, Sequences& sq, int per, int threads) {
-  if (a.batch > kSorted) return;
+  if (a.batch > kSorted) {
+    if (a.new_start) sum_runs(a, sq, per, threads);
+    return;
+  }
   for (int b = threadIdx.x; b < a.batch; b += threads) sq.items[b] = prompt_span(a, b).n;
   __syncthreads();
   int rank = -1, before = 0;
@@ -55,8 +96,8 @@ __device__ __forceinline__ void sort_sequences(const PromptView& a, Sequences& s
   }
   __syncthreads();
   if (rank >= 0) {
-    sq.n[rank] = s.n;
-    sq.row0[rank] = s.row0;
+    sq.few.n[rank] = s.n;
+    sq.few.row0[rank] = s.row0;
     sq.items[rank] = before;
   }
 }
@@ -112,7 +153,7 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 }
 
 // Finds items by their numbers: sequences in order (longest first where they are few), in each the last tokens first, kv heads
-// innermost.  One warp.
+// innermost.  One warp.  (32 sequences of a run are looked at at a time, 683 at most.)
 struct Finder {
   int at;            // sequences passed
   long long before;  // items of those
@@ -123,7 +164,7 @@ struct Finder {
     int local;  // the item's number among its sequence's
     if (a.batch <= kSorted) {
       if (!find_sorted(a, sq, index, it, local)) return false;
-    } else if (!find_any(a, per, index, it, local)) {
+    } else if (a.new_start ? !find_packed(a, sq, per, index, it, local) : !find_padded(a, per, index, it, local)) {
       return false;
     }
     const int group = local / a.kv_heads;
@@ -149,17 +190,40 @@ struct Finder {
       const unsigned past = __ballot_sync(0xffffffffu, o < a.batch && sq.items[o] > index);
       if (past == 0) continue;
       const int who = base + __ffs(past) - 1;
-      it.n = sq.n[who];
-      it.row0 = sq.row0[who];
+      it.n = sq.few.n[who];
+      it.row0 = sq.few.row0[who];
       local = static_cast<int>(index) - (who > 0 ? sq.items[who - 1] : 0);
       return true;
     }
     return false;
   }
 
-  __device__ __forceinline__ bool find_any(const PromptView& a, int per, long long index, Item& it, int& local) {
-    const int lane = threadIdx.x & 31;
-    if (index < before) at = 0, before = 0;
+  // (There are fewer than 2^31 items, and an index is less than 2^30 beyond.)
+  __device__ __forceinline__ bool find_padded(const PromptView& a, int per, long long index, Item& it, int& local) {
+    const unsigned own = static_cast<unsigned>((a.max_new + per - 1) / per) * static_cast<unsigned>(a.kv_heads), i = static_cast<unsigned>(index);
+    const unsigned who = own > 0 ? i / own : static_cast<unsigned>(a.batch);
+    if (who >= static_cast<unsigned>(a.batch)) return false;
+    it.n = a.max_new;
+    it.row0 = static_cast<int>(who) * a.max_new;
+    local = static_cast<int>(i - who * own);
+    return true;
+  }
+
+  __device__ __forceinline__ bool find_packed(const PromptView& a, const Sequences& sq, int per, long long index, Item& it, int& local) {
+    const int lane = threadIdx.x & 31, run = run_of(a);
+    // the run that holds it, from its first sequence on or from where the last search ended
+    int r = 0;
+    for (; r < kSorted; r += 32) {
+      const unsigned past = __ballot_sync(0xffffffffu, sq.upto[r + lane] > index);
+      if (past == 0) continue;
+      r += __ffs(past) - 1;
+      break;
+    }
+    if (r >= kSorted) return false;
+    if (at < r * run || at >= (r + 1) * run || before > index) {
+      at = r * run;
+      before = r > 0 ? sq.upto[r - 1] : 0;
+    }
     for (; at < a.batch;) {
       const PromptSpan s = at + lane < a.batch ? prompt_span(a, at + lane) : PromptSpan{0, 0, false};
       const long long own = static_cast<long long>((s.n + per - 1) / per) * a.kv_heads;
