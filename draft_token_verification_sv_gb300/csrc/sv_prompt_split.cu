@@ -19,10 +19,13 @@
 //   that see them get where results are written;
 //   one issues the products; one finds the items.
 // Three prompts of up to 4001 tokens under windows of 2048 (16 heads of 64
-// float32 dims) take 435 us, 127 TFLOP/s, six times that in products: the
-// tensor core is busy for 0.6 of a tile's 3300 cycles.  The chain of a row's
-// thread (scores, 64 weights in three parts each, sums) bounds it, and the
-// issue slots and instruction fetches that it shares with the loaders.
+// float32 dims) take 435 us, 127 TFLOP/s, six times that in products.  A tile's
+// 48 products, 50 cycles each one after the other, fill 0.7 of its 3300 cycles
+// (their arithmetic, 32 cycles each, 0.5; ncu has the tensor core active for
+// 0.38 of the kernel's time); the chain of a row's thread (scores, 64 weights in
+// three parts each, sums) is about as long, with issue slots and instruction
+// fetches that it shares with the loaders.  Which of these bounds it is not
+// settled: less of one alone gained nothing.
 // Above 128 float32 dims a block's queries do not fit shared memory: they come
 // again with each tile of keys, 64 dims at a time, and tensor memory has room for
 // the scores of one tile only.

@@ -20,15 +20,18 @@
 // before their product, and rows that do see them get them where results are
 // written.
 //
-// Two prompts of up to 8192 tokens (32 heads of 128 dims) take 575 us, 1680
-// TFLOP/s, 85% of the measured rate of a matrix product: the tensor core bounds
-// it, two tiles of queries against 128 keys at a time, one of which has its
-// scores turned into weights while the other's products run.  Prompts of up to
+// Two prompts of up to 8192 tokens (32 heads of 128 dims) take 575 to 631 us, by
+// what power allows: 1680 to 1530 TFLOP/s, 85 to 77% of the measured rate of a
+// matrix product.  The tensor core bounds it, two tiles of queries against 128
+// keys at a time, one of which has its scores turned into weights while the
+// other's products run.  Prompts of up to
 // 836 tokens (80 us) are bound by each item's chain: its first and its masked
 // tiles, its results, and the instructions of these, which are fetched anew for
-// each item.  256 dims leave room for one tile of queries: each tile of keys and
-// values, 128 KB, is read for that alone, and shared memory bounds it (68 us for
-// three prompts of up to 2011 tokens with 14 heads, 930 TFLOP/s).
+// each item.  256 dims leave room for one tile of queries, so each tile of keys and
+// values, 128 KB, is read for that alone, and nothing but the next tile's scores
+// runs beside a tile's weights (68 us for three prompts of up to 2011 tokens with
+// 14 heads, 930 TFLOP/s; the tensor core is active for half of it, the banks of
+// shared memory for 17% in reads and 12% in writes, as far as these count).
 #include "sv_prompt_items.cuh"
 
 #include <type_traits>
